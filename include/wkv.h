@@ -2,7 +2,7 @@
  * wkv.h - C ABI of the RWKV-4 WKV time-mixing operator for AMD MI355X (gfx950),
  * with the receptance gate and the token-shift mix around it, and the
  * matrix-state WKV of RWKV-5 and RWKV-6 (per-token decay), forward and
- * backward.
+ * backward, and the gated delta rule on the same kind of state.
  *
  * The operator, per channel c of each batch row b, tokens t = 1..T
  * ("RWKV（Receptance Weighted Key Value）概念", section 3.2; and
@@ -491,6 +491,92 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
                            const void* go, const float* s_in, const float* ds_out, float* dr, float* dk,
                            float* dv, float* dw, float* du, float* ds_in, const void* ckpt, void* workspace,
                            size_t workspace_bytes, void* hip_stream);
+
+/*
+ * wkv_delta_forward - the gated delta rule: a matrix state per head whose update
+ * first takes back what the state already says of the key.
+ *
+ * Defines, per batch row and value head, from the state S_0 [N, N] (key-major):
+ *     D_t = e^{-w_t} S_{t-1},   e_t = v_t - k_t D_t,
+ *     S_t = D_t + beta_t k_t^T e_t,   o_t = r_t S_t
+ * (unlike wkv5 / wkv6, o_t reads the state after the token, there is no bonus,
+ * and the decay is one rate per token and head).  The pages name the matrix
+ * state and its decay ("RWKV模型深度研究报告（截至2026年初）", section 1.3.2);
+ * the delta write is this library's own extension of it.
+ *
+ * Up to 16 tokens without a ckpt are computed token by token with the state in
+ * registers (decoding); more, or with a ckpt, by 16-token blocks on the matrix
+ * cores.  All arithmetic is float32 whatever the inputs' dtype; outputs are
+ * rounded once.
+ *
+ * B, T      batch rows, tokens (>= 0).
+ * H, HK     value heads and key heads: H a multiple of HK, value head h reads
+ *           r, k of key head h / (H / HK).
+ * N         head size of keys and values: 64 or 128.
+ * in_dtype  WKV_F32 or WKV_BF16: dtype of r, k, v and o.
+ * lengths   [B] int32 or NULL: tokens of each row (clamped to 0 .. T).  Tokens
+ *           behind it are not read, leave the state as it is, and their rows
+ *           of o are zeros.
+ * w         [B, T, H] float32 rates, >= 0; +inf clears the state.
+ * beta      [B, T, H] float32 write strengths.  With |k_t| <= 1 and beta in
+ *           [0, 1] no step enlarges the state it corrects.
+ * r, k      [B, T, HK N], v [B, T, H N] (in_dtype).
+ * o         [B, T, H N] in_dtype, fully overwritten; must not alias inputs.
+ * s_in      [B, H, N, N] float32 state before token 1, or NULL (zero).
+ * s_out     [B, H, N, N] float32 state after each row's last token, or NULL; may
+ *           be s_in.  With T == 0 it receives s_in (or zeros).
+ * ckpt      NULL, or wkv_delta_ckpt_bytes() bytes for wkv_delta_backward on the
+ *           same inputs: the errors e_t and the state before every 64 tokens,
+ *           float32 (opaque).
+ * workspace NULL (no time split), or wkv_delta_forward_workspace_bytes() bytes,
+ *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
+ * r, k, v, o, s_in, s_out, ckpt are 16-byte aligned (WKV_EALIGN otherwise).
+ * WKV_EINVAL also for another N or an H that HK does not divide.
+ * A non-finite input reaches every output of its 64-token block and all after.
+ */
+wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
+                               const int32_t* lengths, const float* w, const float* beta,
+                               const void* r, const void* k, const void* v, void* o,
+                               const float* s_in, float* s_out, void* ckpt, void* workspace,
+                               size_t workspace_bytes, void* hip_stream);
+
+/* Bytes of wkv_delta_forward's ckpt (0 for invalid arguments or no tokens), of
+ * its optional scratch (0 when no time split would be made), and of
+ * wkv_delta_backward's scratch (flags: WKV_WS_HAVE_CKPT when a ckpt will be
+ * passed; else room to recompute it is included). */
+size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N);
+size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N);
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags);
+
+/*
+ * wkv_delta_backward - gradients of wkv_delta_forward for the loss
+ * L = sum <go_t, o_t> + <ds_out, S_T>.  With G_t the gradient of S_t before
+ * token t + 1 acts on it (G_T = ds_out, or 0 when NULL) and G'_t = G_t + r_t^T go_t:
+ *     dr_t = S_t go_t^T,   lambda_t = beta_t k_t G'_t,   dv_t = lambda_t,
+ *     dk_t = beta_t G'_t e_t^T - D_t lambda_t^T,   dbeta_t = e_t . k_t G'_t,
+ *     H_t = G'_t - k_t^T lambda_t,   dw_t = -<H_t, D_t>,   G_{t-1} = e^{-w_t} H_t
+ * and ds_in = G_0.  dr and dk of a key head are summed over its value heads in
+ * a fixed order; all results are bitwise reproducible.
+ *
+ * go        [B, T, H N] in_dtype: the gradient of o.  Rows behind a row's length
+ *           are not read.
+ * dr, dk    [B, T, HK N], dv [B, T, H N] in_dtype; dw, dbeta [B, T, H] float32:
+ *           fully overwritten, zeros behind a row's length.
+ * ds_out, ds_in  [B, H, N, N] float32 or NULL; ds_in may be ds_out.  With T == 0
+ *           ds_in receives ds_out (or zeros).
+ * ckpt      what wkv_delta_forward wrote for these inputs, lengths and s_in, or
+ *           NULL (recomputed, from s_in).
+ * workspace wkv_delta_backward_workspace_bytes(..., flags) bytes, 256-byte
+ *           aligned; clobbered.
+ * Other arguments and errors as wkv_delta_forward; go, dr, dk, dv, ds_out and
+ * ds_in are 16-byte aligned too.
+ */
+wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
+                                const int32_t* lengths, const float* w, const float* beta,
+                                const void* r, const void* k, const void* v, const void* go,
+                                const float* s_in, const float* ds_out, void* dr, void* dk, void* dv,
+                                float* dw, float* dbeta, float* ds_in, const void* ckpt, void* workspace,
+                                size_t workspace_bytes, void* hip_stream);
 
 /*
  * wkv_token_shift / wkv_token_shift_backward - the token-shift mix that

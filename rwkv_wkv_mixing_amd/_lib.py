@@ -39,6 +39,11 @@ EXPORTS = (
     "wkv6_ckpt_bytes",
     "wkv6_backward_workspace_bytes",
     "wkv6_backward",
+    "wkv_delta_forward",
+    "wkv_delta_ckpt_bytes",
+    "wkv_delta_forward_workspace_bytes",
+    "wkv_delta_backward_workspace_bytes",
+    "wkv_delta_backward",
     "wkv_token_shift_workspace_bytes",
     "wkv_token_shift",
     "wkv_token_shift_backward",
@@ -121,6 +126,16 @@ def declare(L):
     L.wkv6_backward.restype = i32
     L.wkv6_backward.argtypes = [i64, i64, i64, i64, i32, fp, fp, vp, vp, vp, vp, fp, fp, fp, fp, fp, fp, fp, fp, vp, vp,
                                 sz, vp]
+    L.wkv_delta_forward.restype = i32
+    L.wkv_delta_forward.argtypes = [i64] * 5 + [i32] + [vp] * 11 + [sz, vp]
+    L.wkv_delta_ckpt_bytes.restype = sz
+    L.wkv_delta_ckpt_bytes.argtypes = [i64] * 4
+    L.wkv_delta_forward_workspace_bytes.restype = sz
+    L.wkv_delta_forward_workspace_bytes.argtypes = [i64] * 5
+    L.wkv_delta_backward_workspace_bytes.restype = sz
+    L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 5 + [i32]
+    L.wkv_delta_backward.restype = i32
+    L.wkv_delta_backward.argtypes = [i64] * 5 + [i32] + [vp] * 17 + [sz, vp]
     L.wkv_token_shift_workspace_bytes.restype = sz
     L.wkv_token_shift_workspace_bytes.argtypes = [i64, i64, i64, i64]
     L.wkv_token_shift.restype = i32

@@ -674,6 +674,113 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
     return hip_status(run_bwd<wkv::Wkv6BwdArgs, wkv::launch_wkv6_bwd>(ba, l, true, workspace, stream));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Shared argument checks of the delta-rule calls and the layout of their scratch.
+struct DeltaPlan {
+    wkv_status_t st;
+    int64_t ns;                          // elements of a state array [B, H, N, N]
+    size_t rows_bytes, states_bytes;     // float32 [B, T, H, N] and [B, H, ceil(T / 64), N, N], rounded up to 256
+};
+
+DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype) {
+    const auto bad = [](wkv_status_t st) { return DeltaPlan{st, 0, 0, 0}; };
+    if (B < 0 || T < 0 || H < 0 || HK < 0 || (N != 64 && N != 128)) return bad(WKV_EINVAL);
+    if (HK == 0 ? H != 0 : H % HK != 0) return bad(WKV_EINVAL);
+    if (!dtype_ok(in_dtype)) return bad(WKV_EDTYPE);
+    DeltaPlan p{WKV_OK, 0, 0, 0};
+    constexpr int64_t kMost = int64_t{1} << 60;
+    int64_t bh, hn, n, st;
+    if (!mul3(B, H, 1, &bh) || !mul3(bh, N, N, &p.ns) || p.ns > kMost / 4) return bad(WKV_ESIZE);
+    if (!mul3(H, N, 4, &hn) || !mul3(B, T, hn, &n) || n > kMost) return bad(WKV_ESIZE);
+    if (!mul3(p.ns, (T + 63) / 64, 4, &st) || st > kMost) return bad(WKV_ESIZE);
+    // grids: a workgroup per (64 columns, pair) and per (64 tokens, row, key head), below 2^31
+    int64_t tiles;
+    if (bh >= (int64_t{1} << 30) || !mul3(B, HK, (T + 63) / 64, &tiles) || tiles >= (int64_t{1} << 31)) return bad(WKV_ESIZE);
+    p.rows_bytes = (static_cast<size_t>(n) + 255) / 256 * 256;
+    p.states_bytes = (static_cast<size_t>(st) + 255) / 256 * 256;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
+    const DeltaPlan p = delta_plan(B, T, H, H, N, WKV_F32);
+    return p.st == WKV_OK ? p.rows_bytes + p.states_bytes : 0;
+}
+
+size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N) {
+    (void)delta_plan(B, T, H, HK, N, WKV_F32);
+    return 0;
+}
+
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags) {
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
+    if (p.st != WKV_OK) return 0;
+    const size_t one = p.rows_bytes + p.states_bytes;
+    return (flags & WKV_WS_HAVE_CKPT) != 0 ? one : 2 * one;
+}
+
+wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
+                               const int32_t* lengths, const float* w, const float* beta, const void* r, const void* k,
+                               const void* v, void* o, const float* s_in, float* s_out, void* ckpt, void* workspace,
+                               size_t workspace_bytes, void* hip_stream) {
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype);
+    if (p.st != WKV_OK) return p.st;
+    (void)workspace;
+    (void)workspace_bytes;
+    if (p.ns == 0) return WKV_OK;
+    if ((s_in && !aligned(s_in, 16)) || (s_out && !aligned(s_out, 16))) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (T == 0) return hip_status(wkv::launch_wkv5_state_copy(s_in, s_out, p.ns, stream));
+    if (!w || !beta || !r || !k || !v || !o) return WKV_EINVAL;
+    if (!aligned(w, 4) || !aligned(beta, 4) || !aligned(r, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+        (lengths && !aligned(lengths, 4)) || (ckpt && !aligned(ckpt, 16)))
+        return WKV_EALIGN;
+    float* errs = static_cast<float*>(ckpt);
+    float* states = ckpt ? reinterpret_cast<float*>(static_cast<char*>(ckpt) + p.rows_bytes) : nullptr;
+    const wkv::DeltaArgs a{B, T, H, HK, N, in_dtype == WKV_BF16, lengths, w, beta, r, k, v, o, s_in, s_out, errs, states};
+    return hip_status(wkv::launch_delta_fwd(a, stream));
+}
+
+wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
+                                const int32_t* lengths, const float* w, const float* beta, const void* r, const void* k,
+                                const void* v, const void* go, const float* s_in, const float* ds_out, void* dr, void* dk,
+                                void* dv, float* dw, float* dbeta, float* ds_in, const void* ckpt, void* workspace,
+                                size_t workspace_bytes, void* hip_stream) {
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype);
+    if (p.st != WKV_OK) return p.st;
+    if (p.ns == 0) return WKV_OK;
+    if ((ds_in && !aligned(ds_in, 16)) || (ds_out && !aligned(ds_out, 16))) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (T == 0) return hip_status(wkv::launch_wkv5_state_copy(ds_out, ds_in, p.ns, stream));  // dS0 = dS_T
+    if (!w || !beta || !r || !k || !v || !go || !dr || !dk || !dv || !dw || !dbeta) return WKV_EINVAL;
+    if (!aligned(w, 4) || !aligned(beta, 4) || !aligned(r, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(go, 16) ||
+        !aligned(dr, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dw, 4) || !aligned(dbeta, 4) ||
+        (s_in && !aligned(s_in, 16)) || (lengths && !aligned(lengths, 4)) || (ckpt && !aligned(ckpt, 16)))
+        return WKV_EALIGN;
+    const size_t one = p.rows_bytes + p.states_bytes;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (ckpt ? one : 2 * one)) return WKV_EWORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    const bool bf = in_dtype == WKV_BF16;
+    const char* saved = static_cast<const char*>(ckpt);
+    if (ckpt == nullptr) {  // the errors and states, by a forward pass without outputs
+        saved = ws + one;
+        const wkv::DeltaArgs fa{B, T, H, HK, N, bf, lengths, w, beta, r, k, v, nullptr, s_in, nullptr,
+                                reinterpret_cast<float*>(ws + one), reinterpret_cast<float*>(ws + one + p.rows_bytes)};
+        const hipError_t e = wkv::launch_delta_fwd(fa, stream);
+        if (e != hipSuccess) return hip_status(e);
+    }
+    const wkv::DeltaBwdArgs a{B, T, H, HK, N, bf, lengths, w, beta, r, k, go, reinterpret_cast<const float*>(saved),
+                              reinterpret_cast<const float*>(saved + p.rows_bytes), ds_out, reinterpret_cast<float*>(ws),
+                              reinterpret_cast<float*>(ws + p.rows_bytes), dr, dk, dv, dw, dbeta, ds_in};
+    return hip_status(wkv::launch_delta_bwd(a, stream));
+}
+
 size_t wkv_token_shift_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t M) {
     const ShiftPlan p = shift_plan(B, T, C, M, WKV_F32);
     return p.st == WKV_OK ? p.ws_bytes : 0;

@@ -1,0 +1,857 @@
+// The gated delta rule: a matrix state per head that is decayed, corrected and read.
+//
+// Per (batch row, value head), with a state S [N, N] (key x value), N = 64 or 128:
+//     D_t = e^{-w_t} S_{t-1}                    (decay, one rate per token and head)
+//     e_t = v_t - k_t D_t                       (what the state gets wrong about this key)
+//     S_t = D_t + beta_t k_t^T e_t,   o_t = r_t S_t
+// H value heads share HK key heads (H a multiple of HK): head h reads r, k of key head h / (H / HK).
+//
+// Over a block of tokens i = 0.. from the state S0, with the decay products
+//     since_i = prod_{l <= i} e^{-w_l},  ratio_ij = prod_{j < l <= i} e^{-w_l},  until_j = prod_{l > j} e^{-w_l}
+// the recurrence unrolls to a triangular system for the errors and two products:
+//     (I + M diag(beta)) e = V - diag(since) K S0,     M_ij = ratio_ij k_i . k_j   (j < i)
+//     o   = diag(since) R S0 + A e,                    A_ij = ratio_ij r_i . k_j beta_j   (j <= i)
+//     S1  = since_last S0 + K^T diag(until beta) e
+// The block here is 16 tokens: the system's inverse X = (I + M diag(beta))^{-1} is a 16 x 16 unit
+// lower triangle found by forward substitution (no cancellation, whatever the keys), and the state
+// stays in the accumulators of its products.  Every ratio is exp of a sum of the rates between its
+// two tokens, never a quotient or a difference of running sums, so a rate of any size (+inf included:
+// the state is cleared) gives factors in [0, 1].
+//
+// Lane layout.  A wave owns 16 value columns of the state: N / 16 accumulators of the 16 x 16 products,
+// where lane (l16, g) holds rows 4 g .. 4 g + 3 of column l16.  As the right operand of the next product
+// the same registers are already in place when the contracted index runs in that order: register r of
+// group g is row 4 g + r.  The left operand is then read from its rows in the same order.  So neither
+// the state nor e, nor anything between the products, ever crosses lanes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "wkv_launch.h"
+
+namespace wkv {
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 64;   // tokens staged at a time, and between saved states
+constexpr int kSub = 16;    // tokens of one triangular system
+constexpr int kWaves = 4;   // per workgroup: one per sub-block of a tile, 16 value columns each
+constexpr int kCols = 16 * kWaves;
+constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+
+// four consecutive elements as float32
+__device__ __forceinline__ f4 load4(const uint16_t* p) {
+    const u16x4 x = *reinterpret_cast<const u16x4*>(p);
+    return f4{widen(x[0]), widen(x[1]), widen(x[2]), widen(x[3])};
+}
+__device__ __forceinline__ f4 load4(const float* p) { return *reinterpret_cast<const f4*>(p); }
+
+__device__ __forceinline__ uint32_t pk2(float a, float b) {
+    const f2 p = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
+}
+__device__ __forceinline__ uint16_t narrow(float x) { return static_cast<uint16_t>(pk2(x, x) & 0xffffu); }
+
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = narrow(x); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store4(uint16_t* p, f4 x) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pk2(x[0], x[1]), pk2(x[2], x[3])};
+}
+__device__ __forceinline__ void store4(float* p, f4 x) { *reinterpret_cast<f4*>(p) = x; }
+
+// float32 product: lane (l16, g) gives row l16 of A and column l16 of B at contracted index g
+__device__ __forceinline__ f4 mfma4(float a, float b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// acc += A B over 16 contracted indices 4 g + r
+__device__ __forceinline__ f4 mma16(f4 a, f4 b, f4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = mfma4(a[r], b[r], c);
+    return c;
+}
+
+// Elements a row of a staged [kTile, N] array: padded by 16 bytes, so that 16 lanes reading 16
+// consecutive rows start in different banks.
+template <typename T, int N>
+constexpr int kRow = N + 16 / static_cast<int>(sizeof(T));
+
+// Rows t0 .. t0 + 63 of a [rows, stride] array, W columns from its base, on their way to LDS: held in
+// registers between fetch and put, so that the next tile's loads overlap this tile's arithmetic.
+// Rows at or past `end` are zeros and are not read.
+template <typename T, int W>
+struct Staged {
+    static constexpr int kPer = 16 / static_cast<int>(sizeof(T));  // elements a 16-byte vector
+    static constexpr int kRowVecs = W / kPer;
+    static constexpr int kVecs = kTile * kRowVecs / (64 * kWaves);
+    u32x4 x[kVecs];
+
+    __device__ __forceinline__ void fetch(const T* base, int64_t stride, int64_t t0, int64_t end) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+            const int64_t t = t0 + q / kRowVecs;
+            x[i] = t < end ? *reinterpret_cast<const u32x4*>(base + t * stride + q % kRowVecs * kPer) : u32x4{0, 0, 0, 0};
+        }
+    }
+    template <int ROW>
+    __device__ __forceinline__ void put(T (*dst)[ROW]) const {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+            *reinterpret_cast<u32x4*>(&dst[q / kRowVecs][q % kRowVecs * kPer]) = x[i];
+        }
+    }
+};
+
+__device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t T) {
+    if (lengths == nullptr) return T;
+    const int64_t n = lengths[b];
+    return n < 0 ? 0 : n < T ? n : T;
+}
+
+// What the four 16-token blocks of a tile need besides their rows.
+struct Blocks {
+    float w[kTile], beta[kTile];         // rates in log2 units; zero behind the row's length
+    float since[kTile], until[kTile];    // decay from the block's start through the token, and after it to its end
+    float inv[kWaves][kSub][kPadM];      // X
+    float att[kWaves][kSub][kPadM];      // A
+    float m[kWaves][kSub][kPadM];        // M diag(beta), while X is found
+};
+
+// Wave s prepares block s of the staged tile: decays, X and A.  The 16 x 16 products take their rows of
+// k and r as they are staged; register r of group g holds element (i = 4 g + r, j = l16).
+template <typename T, int N>
+__device__ __forceinline__ void prepare_block(int s, int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>],
+                                              Blocks& B) {
+    f4 kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+        const f4 a = load4(&K[kSub * s + l16][16 * c + 4 * g]);
+        kk = mma16(a, a, kk);
+        rk = mma16(load4(&R[kSub * s + l16][16 * c + 4 * g]), a, rk);
+    }
+    float gap[4] = {0.f, 0.f, 0.f, 0.f};  // sum of w over j < l <= i
+    float run = 0.f, pre = 0.f, suf = 0.f;
+#pragma unroll
+    for (int l = 0; l < kSub; ++l) {
+        const float wl = B.w[kSub * s + l];
+        run += l > l16 ? wl : 0.f;
+        pre += l <= l16 ? wl : 0.f;
+        suf += l > l16 ? wl : 0.f;
+        if (l / 4 == g) gap[l % 4] = run;
+    }
+    if (g == 0) {
+        B.since[kSub * s + l16] = ex2(-pre);
+        B.until[kSub * s + l16] = ex2(-suf);
+    }
+    const float bj = B.beta[kSub * s + l16];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = 4 * g + r;
+        const float f = ex2(-gap[r]) * bj;
+        B.m[s][i][l16] = l16 < i ? f * kk[r] : 0.f;
+        B.att[s][i][l16] = l16 <= i ? f * rk[r] : 0.f;
+    }
+    __builtin_amdgcn_wave_barrier();  // the table is read back by the wave that wrote it
+    // column l16 of X, row by row: x_i = [i == l16] - sum_{j < i} (M diag(beta))_ij x_j
+    float x[kSub];
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+        float acc = i == l16 ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) acc = fmaf(-B.m[s][i][j], x[j], acc);
+        x[i] = acc;
+    }
+    if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) B.inv[s][i][l16] = x[i];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_rates(Blocks& B, const float* w, const float* beta, int64_t H, int64_t t0, int64_t end) {
+    if (threadIdx.x < kTile) {
+        const int64_t t = t0 + threadIdx.x;
+        B.w[threadIdx.x] = t < end ? w[t * H] * kLog2e : 0.f;
+        B.beta[threadIdx.x] = t < end ? beta[t * H] : 0.f;
+    }
+}
+
+template <typename T, int N>
+struct FwdShared {
+    T k[kTile][kRow<T, N>];
+    T r[kTile][kRow<T, N>];
+    T v[kTile][kRow<T, kCols>];
+    Blocks blk;
+};
+
+// Chunked forward.  One workgroup per (64 value columns, batch row, head) walks the tiles in order: stage
+// the tile, each wave prepares one of its four blocks, then each wave takes its 16 columns through the
+// blocks one after the other with no barrier between them.
+template <typename T, int N>
+__global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) {
+    __shared__ FwdShared<T, N> sm;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int64_t BH = P.B * P.H;
+    const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
+    const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
+    const int64_t len = row_length(P.lengths, b, P.T);
+    const int64_t ks = P.HK * N, vs = P.H * N;  // row strides
+    const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
+    const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
+    const int64_t vo = b * P.T * vs + h * N + cb * kCols;
+    const T* v = static_cast<const T*>(P.v) + vo;
+    T* o = P.o != nullptr ? static_cast<T*>(P.o) + vo : nullptr;
+    const float* w = P.w + b * P.T * P.H + h;
+    const float* beta = P.beta + b * P.T * P.H + h;
+    const int col = 16 * wv + l16;           // of the workgroup's 64
+    const int64_t scol = cb * kCols + col;   // of the state
+    const int64_t ntile = (P.T + kTile - 1) / kTile;
+
+    f4 S[N / 16];
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            S[c][q] = P.s_in != nullptr ? P.s_in[(bh * N + 16 * c + 4 * g + q) * N + scol] : 0.f;
+
+    Staged<T, N> fk, fr;
+    Staged<T, kCols> fv;
+    fk.fetch(k, ks, 0, len);
+    fr.fetch(r, ks, 0, len);
+    fv.fetch(v, vs, 0, len);
+    int64_t t0 = 0;
+    for (; t0 < len; t0 += kTile) {
+        __syncthreads();  // the last tile's readers are done
+        fk.put(sm.k);
+        fr.put(sm.r);
+        fv.put(sm.v);
+        load_rates<T>(sm.blk, w, beta, P.H, t0, len);
+        __syncthreads();
+        if (t0 + kTile < len) {
+            fk.fetch(k, ks, t0 + kTile, len);
+            fr.fetch(r, ks, t0 + kTile, len);
+            fv.fetch(v, vs, t0 + kTile, len);
+        }
+        prepare_block<T, N>(wv, l16, g, sm.k, sm.r, sm.blk);
+        if (P.states != nullptr) {
+            float* st = P.states + (bh * ntile + t0 / kTile) * N * N + scol;
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) st[(16 * c + 4 * g + q) * N] = S[c][q];
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int s = 0; s < kTile / kSub; ++s) {
+            const int tb = kSub * s;
+            if (t0 + tb >= P.T) break;
+            f4 kS = {0.f, 0.f, 0.f, 0.f}, rS = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) {
+                kS = mma16(load4(&sm.k[tb + l16][16 * c + 4 * g]), S[c], kS);
+                rS = mma16(load4(&sm.r[tb + l16][16 * c + 4 * g]), S[c], rS);
+            }
+            const f4 since = load4(&sm.blk.since[tb + 4 * g]);
+            const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
+            f4 e0, out;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                e0[q] = widen(sm.v[tb + 4 * g + q][col]) - since[q] * kS[q];
+                out[q] = since[q] * rS[q];
+            }
+            const f4 e = mma16(load4(&sm.blk.inv[s][l16][4 * g]), e0, f4{0.f, 0.f, 0.f, 0.f});
+            out = mma16(load4(&sm.blk.att[s][l16][4 * g]), e, out);
+            const f4 u = put * e;
+            const float total = sm.blk.since[tb + kSub - 1];
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) {
+                f4 a;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) a[q] = widen(sm.k[tb + 4 * g + q][16 * c + l16]);
+                S[c] = mma16(a, u, S[c] * total);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t t = t0 + tb + 4 * g + q;
+                if (t >= P.T) continue;
+                if (o != nullptr) store1(&o[t * vs + col], out[q]);
+                if (P.errs != nullptr) P.errs[vo + t * vs + col] = e[q];
+            }
+        }
+    }
+    if (o != nullptr) {  // whole tiles behind the row's length: zeros
+        for (int64_t t = t0 + threadIdx.x / 16; t < P.T; t += 16) store4(&o[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
+    }
+    if (P.s_out != nullptr) {
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) P.s_out[(bh * N + 16 * c + 4 * g + q) * N + scol] = S[c][q];
+    }
+}
+
+// A few tokens (decoding): the state makes one trip through memory, updated token by token in
+// registers.  One wave per (batch row, head, 64 value columns): lane (q, g) owns columns 4 q .. 4 q + 3
+// of rows g N/4 .. (g + 1) N/4 - 1.  k S and r S are both taken from the state before the token, so one
+// round of shuffles serves both:  o = e^{-w} r S + (r . k) beta e.
+template <typename T, int N>
+__global__ void __launch_bounds__(256) delta_step_kernel(DeltaArgs P) {
+    constexpr int M = N / 4;  // rows a lane
+    __shared__ __attribute__((aligned(16))) float tab[kWaves][2][N];
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kWaves + wv;
+    if (id >= P.B * P.H * (N / 64)) return;  // a whole wave; the kernel has no barrier
+    const int64_t bh = id / (N / 64), cb = id % (N / 64);
+    const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
+    const int64_t len = row_length(P.lengths, b, P.T);
+    const int q = lane & 15, g = lane >> 4;
+    const int64_t c0 = cb * 64 + 4 * q;
+    const int64_t e0 = (bh * N + g * M) * N + c0;
+    f4 x[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        x[m] = P.s_in != nullptr ? __builtin_nontemporal_load(reinterpret_cast<const f4*>(P.s_in + e0 + m * N))
+                                 : f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int64_t t = 0; t < len; ++t) {
+        const int64_t row = b * P.T + t;
+        float rk = 0.f;
+#pragma unroll
+        for (int c = 0; c < N; c += 64) {
+            const float rl = widen(static_cast<const T*>(P.r)[(row * P.HK + hk) * N + c + lane]);
+            const float kl = widen(static_cast<const T*>(P.k)[(row * P.HK + hk) * N + c + lane]);
+            tab[wv][0][c + lane] = rl;
+            tab[wv][1][c + lane] = kl;
+            rk = fmaf(rl, kl, rk);
+        }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) rk += __shfl_xor(rk, m, 64);
+        const f4 v = load4(static_cast<const T*>(P.v) + (row * P.H + h) * N + c0);
+        const float a = ex2(-P.w[row * P.H + h] * kLog2e), beta = P.beta[row * P.H + h];
+        __builtin_amdgcn_wave_barrier();
+        f4 kS = {0.f, 0.f, 0.f, 0.f}, rS = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < M; m += 4) {
+            const f4 r4 = load4(&tab[wv][0][g * M + m]), k4 = load4(&tab[wv][1][g * M + m]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                rS += r4[i] * x[m + i];
+                kS += k4[i] * x[m + i];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            kS[c] += __shfl_xor(kS[c], 16, 64);
+            rS[c] += __shfl_xor(rS[c], 16, 64);
+            kS[c] += __shfl_xor(kS[c], 32, 64);
+            rS[c] += __shfl_xor(rS[c], 32, 64);
+        }
+        const f4 u = beta * (v - a * kS);
+#pragma unroll
+        for (int m = 0; m < M; m += 4) {
+            const f4 k4 = load4(&tab[wv][1][g * M + m]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[m + i] = a * x[m + i] + k4[i] * u;
+        }
+        if (g == 0) store4(static_cast<T*>(P.o) + (row * P.H + h) * N + c0, a * rS + rk * u);
+        __builtin_amdgcn_wave_barrier();  // tab is read before the next token overwrites it
+    }
+    for (int64_t t = len; t < P.T; ++t)
+        if (g == 0) store4(static_cast<T*>(P.o) + ((b * P.T + t) * P.H + h) * N + c0, f4{0.f, 0.f, 0.f, 0.f});
+    if (P.s_out != nullptr) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) __builtin_nontemporal_store(x[m], reinterpret_cast<f4*>(P.s_out + e0 + m * N));
+    }
+}
+
+// ---- backward -----------------------------------------------------------------------------------
+// For L = <go, o> + <ds_out, S_T>, over a block with G the gradient of the state after it:
+//     y      = A^T go + diag(beta until) K G
+//     lambda = X^T y                               (the gradient of v, and of V - diag(since) K S0)
+//     G0     = since_last G + R^T diag(since) go - K^T diag(since) lambda
+// which needs neither the states nor the errors of the forward: the adjoint walk below takes the tiles
+// last to first with the forward's layout, writes lambda and the gradient of the state after every tile,
+// and leaves the rest, which is independent from tile to tile, to delta_grad_kernel.
+template <typename T, int N>
+struct AdjShared {
+    T k[kTile][kRow<T, N>];
+    T r[kTile][kRow<T, N>];
+    T go[kTile][kRow<T, kCols>];
+    Blocks blk;
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdArgs P) {
+    __shared__ AdjShared<T, N> sm;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int64_t BH = P.B * P.H;
+    const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
+    const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
+    const int64_t len = row_length(P.lengths, b, P.T);
+    const int64_t ks = P.HK * N, vs = P.H * N;
+    const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
+    const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
+    const int64_t vo = b * P.T * vs + h * N + cb * kCols;
+    const T* go = static_cast<const T*>(P.go) + vo;
+    T* dv = static_cast<T*>(P.dv) + vo;
+    const float* w = P.w + b * P.T * P.H + h;
+    const float* beta = P.beta + b * P.T * P.H + h;
+    const int col = 16 * wv + l16;
+    const int64_t scol = cb * kCols + col;
+    const int64_t ntile = (P.T + kTile - 1) / kTile;
+
+    f4 G[N / 16];
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            G[c][q] = P.ds_out != nullptr ? P.ds_out[(bh * N + 16 * c + 4 * g + q) * N + scol] : 0.f;
+
+    const int64_t live = (len + kTile - 1) / kTile;  // tiles with a token of this row
+    for (int64_t t = live * kTile + threadIdx.x / 16; t < P.T; t += 16)
+        store4(&dv[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
+    Staged<T, N> fk, fr;
+    Staged<T, kCols> fg;
+    if (live > 0) {
+        fk.fetch(k, ks, (live - 1) * kTile, len);
+        fr.fetch(r, ks, (live - 1) * kTile, len);
+        fg.fetch(go, vs, (live - 1) * kTile, len);
+    }
+    for (int64_t tile = live - 1; tile >= 0; --tile) {
+        const int64_t t0 = tile * kTile;
+        __syncthreads();
+        fk.put(sm.k);
+        fr.put(sm.r);
+        fg.put(sm.go);
+        load_rates<T>(sm.blk, w, beta, P.H, t0, len);
+        __syncthreads();
+        if (tile > 0) {
+            fk.fetch(k, ks, t0 - kTile, len);
+            fr.fetch(r, ks, t0 - kTile, len);
+            fg.fetch(go, vs, t0 - kTile, len);
+        }
+        prepare_block<T, N>(wv, l16, g, sm.k, sm.r, sm.blk);
+        float* gt = P.gstates + (bh * ntile + tile) * N * N + scol;
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) gt[(16 * c + 4 * g + q) * N] = G[c][q];
+        __syncthreads();
+#pragma unroll 1
+        for (int s = kTile / kSub - 1; s >= 0; --s) {
+            const int tb = kSub * s;
+            f4 kG = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) kG = mma16(load4(&sm.k[tb + l16][16 * c + 4 * g]), G[c], kG);
+            const f4 since = load4(&sm.blk.since[tb + 4 * g]);
+            const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
+            f4 d, att, inv;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                d[q] = widen(sm.go[tb + 4 * g + q][col]);
+                att[q] = sm.blk.att[s][4 * g + q][l16];
+                inv[q] = sm.blk.inv[s][4 * g + q][l16];
+            }
+            const f4 y = mma16(att, d, put * kG);
+            const f4 lam = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
+            const f4 gr = since * d, gk = -since * lam;
+            const float total = sm.blk.since[tb + kSub - 1];
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) {
+                f4 a, a2;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q] = widen(sm.r[tb + 4 * g + q][16 * c + l16]);
+                    a2[q] = widen(sm.k[tb + 4 * g + q][16 * c + l16]);
+                }
+                G[c] = mma16(a2, gk, mma16(a, gr, G[c] * total));
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t t = t0 + tb + 4 * g + q;
+                if (t >= P.T) continue;
+                store1(&dv[t * vs + col], lam[q]);
+                P.lambda[vo + t * vs + col] = lam[q];
+            }
+        }
+    }
+    if (P.ds_in != nullptr) {
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) P.ds_in[(bh * N + 16 * c + 4 * g + q) * N + scol] = G[c][q];
+    }
+}
+
+// The gradients that are sums over the value columns, tile by tile.  Over a tile of 64 tokens from the
+// state S0 with G the gradient of the state after it, all decays now counted inside the tile:
+//     dA_ij = ratio_ij beta_j go_i . e_j  (j <= i),   dM_ij = -ratio_ij beta_j lambda_i . e_j  (j < i)
+//     dr_i = since_i S0 go_i + sum_j dA_ij k_j
+//     dk_i = -since_i S0 lambda_i + until_i beta_i G e_i
+//            + sum_{j < i} dM_ij k_j + sum_{l >= i} dA_li r_l + sum_{l > i} dM_li k_l
+//     dbeta_j = until_j k_j . G e_j + sum_i P_ij,   P_ij = ratio_ij (r_i . k_j go_i - k_i . k_j lambda_i) . e_j
+// and the rate of token t takes every term whose path crosses from before t to t or later:
+//     -dw_t = sum_{j < t <= i} beta_j P_ij + sum_{i >= t} since_i (r_i . S0 go_i - k_i . S0 lambda_i)
+//             + sum_{j < t} until_j beta_j k_j . G e_j + since_last <G, S0>
+// sums of the terms themselves, so no running sum is subtracted from another.
+//
+// One workgroup per (tile, batch row, key head); it takes the value heads of its key head one after the
+// other and keeps dr, dk in registers (a fixed order of summation).  Wave x owns tokens 16 x .. 16 x + 15:
+// as i it meets the blocks J <= x, as j the blocks I >= x (5 blocks for every wave).  Both times the
+// 16 x 16 block is formed with the wave's own tokens as its columns, so it is already the right operand
+// of the products that follow; dr and dk come out transposed, four consecutive channels a lane.
+template <typename T, int N>
+struct GradShared {
+    static constexpr bool kGoInLds = sizeof(T) * N <= 256;  // float32 at N = 128 reads go from memory: 160 KB of LDS
+    T k[kTile][kRow<T, N>];
+    T r[kTile][kRow<T, N>];
+    T go[kGoInLds ? kTile : 1][kRow<T, N>];
+    float e[kTile][N + 4];
+    float lam[kTile][N + 4];
+    float w[kTile], beta[kTile];
+    float pre[kTile], suf[kTile];        // sums of w in the token's block: through it, and after it
+    float total[kWaves];                 // of w in each block
+    float diag[kWaves][kSub][kPadM];     // beta_j P_ij of the blocks I == J
+    float cross[kWaves][kWaves];         // [I][J]: sum of beta_j P_ij
+    float rows[kWaves], cols[kWaves];    // block sums of the terms that pair with S0, and with G
+    float rowv[kWaves][kSub], colv[kWaves][kSub];
+};
+
+__device__ __forceinline__ float sum_groups(float x) {
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs P) {
+    __shared__ GradShared<T, N> sm;
+    constexpr int NC = N / 16;
+    const int lane = threadIdx.x & 63;
+    const int x = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int64_t ntile = (P.T + kTile - 1) / kTile;
+    const int64_t bhk = blockIdx.x % (P.B * P.HK), tile = blockIdx.x / (P.B * P.HK);
+    const int64_t b = bhk / P.HK, hk = bhk % P.HK, per = P.H / P.HK;
+    const int64_t len = row_length(P.lengths, b, P.T);
+    const int64_t ks = P.HK * N, vs = P.H * N, t0 = tile * kTile;
+    const int64_t ko = b * P.T * ks + hk * N;
+    T* dr = static_cast<T*>(P.dr) + ko;
+    T* dk = static_cast<T*>(P.dk) + ko;
+    const int64_t rows = P.T - t0 < kTile ? P.T - t0 : kTile;
+    if (t0 >= len) {  // nothing of this row here
+        for (int64_t t = threadIdx.x / 16; t < rows; t += 16) {
+            for (int c = threadIdx.x % 16 * 4; c < N; c += 64) {
+                store4(&dr[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
+                store4(&dk[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
+            }
+        }
+        for (int64_t i = threadIdx.x; i < rows * per; i += 64 * kWaves) {
+            const int64_t at = (b * P.T + t0 + i / per) * P.H + hk * per + i % per;
+            P.dw[at] = 0.f;
+            P.dbeta[at] = 0.f;
+        }
+        return;
+    }
+    {
+        Staged<T, N> s;
+        s.fetch(static_cast<const T*>(P.k) + ko, ks, t0, len);
+        s.put(sm.k);
+        s.fetch(static_cast<const T*>(P.r) + ko, ks, t0, len);
+        s.put(sm.r);
+    }
+    f4 drT[NC], dkT[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) drT[c] = dkT[c] = f4{0.f, 0.f, 0.f, 0.f};
+    const int mine = kSub * x + l16;  // this lane's token of the tile
+
+#pragma unroll 1
+    for (int64_t h = hk * per; h < (hk + 1) * per; ++h) {
+        const int64_t bh = b * P.H + h, vo = b * P.T * vs + h * N;
+        const T* go = static_cast<const T*>(P.go) + vo;
+        __syncthreads();  // the last head's readers are done
+        if constexpr (GradShared<T, N>::kGoInLds) {
+            Staged<T, N> s;
+            s.fetch(go, vs, t0, len);
+            s.put(sm.go);
+        }
+        {
+            Staged<float, N> s;
+            s.fetch(P.errs + vo, vs, t0, len);
+            s.put(sm.e);
+            s.fetch(P.lambda + vo, vs, t0, len);
+            s.put(sm.lam);
+        }
+        if (threadIdx.x < kTile) {
+            const int64_t t = t0 + threadIdx.x;
+            sm.w[threadIdx.x] = t < len ? P.w[(b * P.T + t) * P.H + h] * kLog2e : 0.f;
+            sm.beta[threadIdx.x] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
+        }
+        __syncthreads();
+        float pre = 0.f, suf = 0.f;  // of this lane's token
+#pragma unroll
+        for (int l = 0; l < kSub; ++l) {
+            const float wl = sm.w[kSub * x + l];
+            pre += l <= l16 ? wl : 0.f;
+            suf += l > l16 ? wl : 0.f;
+        }
+        if (g == 0) {
+            sm.pre[mine] = pre;
+            sm.suf[mine] = suf;
+            if (l16 == 15) sm.total[x] = pre;
+        }
+        __syncthreads();
+        float before = 0.f, after = 0.f;  // rates of the blocks before and after this wave's
+        for (int i = 0; i < kWaves; ++i) {
+            before += i < x ? sm.total[i] : 0.f;
+            after += i > x ? sm.total[i] : 0.f;
+        }
+        const float since = ex2(-(before + pre)), until = ex2(-(suf + after)), beta = sm.beta[mine];
+        const float all = ex2(-(before + sm.total[x] + after));
+
+        // rows of this wave's tokens: go, lambda, e as right operands
+        const auto go4 = [&](int row, int c) -> f4 {
+            if constexpr (GradShared<T, N>::kGoInLds) {
+                return load4(&sm.go[row][16 * c + 4 * g]);
+            } else {
+                return t0 + row < len ? load4(&go[(t0 + row) * vs + 16 * c + 4 * g]) : f4{0.f, 0.f, 0.f, 0.f};
+            }
+        };
+        f4 goX[NC], laX[NC], eX[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            goX[c] = go4(mine, c);
+            laX[c] = load4(&sm.lam[mine][16 * c + 4 * g]);
+            eX[c] = load4(&sm.e[mine][16 * c + 4 * g]);
+        }
+        // products with the states before and after the tile
+        const float* S0 = P.states + (bh * ntile + tile) * N * N;
+        const float* G1 = P.gstates + (bh * ntile + tile) * N * N;
+        float withS = 0.f, withG = 0.f, inner = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < NC; ++c) {
+            f4 sg = {0.f, 0.f, 0.f, 0.f}, sl = {0.f, 0.f, 0.f, 0.f}, ge = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < NC; ++d) {
+                const f4 s4 = load4(&S0[(16 * c + l16) * N + 16 * d + 4 * g]);
+                const f4 g4 = load4(&G1[(16 * c + l16) * N + 16 * d + 4 * g]);
+                sg = mma16(s4, goX[d], sg);
+                sl = mma16(s4, laX[d], sl);
+                ge = mma16(g4, eX[d], ge);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) inner = fmaf(s4[q], g4[q], inner);
+            }
+            const f4 rr = load4(&sm.r[mine][16 * c + 4 * g]), kk = load4(&sm.k[mine][16 * c + 4 * g]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                withS += rr[q] * sg[q] - kk[q] * sl[q];
+                withG += kk[q] * ge[q];
+            }
+            const f4 a = since * sg, d = until * beta * ge - since * sl;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {  // (drT[c] with c known only at run time would spill)
+                if (j == c) {
+                    drT[j] += a;
+                    dkT[j] += d;
+                }
+            }
+        }
+        withS = since * sum_groups(withS);
+        withG = until * sum_groups(withG);
+        inner = sum16(sum_groups(inner));
+        float rowv = withS, colv = beta * withG, dbeta = withG;
+
+        // blocks J <= x with this wave's tokens as i: rows j = 4 g + q, columns i
+#pragma unroll 1
+        for (int J = 0; J <= x; ++J) {
+            f4 ae = {0.f, 0.f, 0.f, 0.f}, le = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const f4 e4 = load4(&sm.e[kSub * J + l16][16 * c + 4 * g]);
+                ae = mma16(e4, goX[c], ae);
+                le = mma16(e4, laX[c], le);
+                const f4 k4 = load4(&sm.k[kSub * J + l16][16 * c + 4 * g]);
+                kk = mma16(k4, load4(&sm.k[mine][16 * c + 4 * g]), kk);
+                rk = mma16(k4, load4(&sm.r[mine][16 * c + 4 * g]), rk);
+            }
+            float mid = pre;
+            for (int i = 0; i < kWaves; ++i) mid += i > J && i < x ? sm.total[i] : 0.f;
+            f4 da, dm;
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = 4 * g + q;
+                float gap = mid + sm.suf[kSub * J + j];
+                if (J == x) {
+                    gap = 0.f;
+#pragma unroll
+                    for (int l = 0; l < kSub; ++l) gap += l > j && l <= l16 ? sm.w[kSub * x + l] : 0.f;
+                }
+                const bool ia = J < x || j <= l16, im = J < x || j < l16;
+                const float f = ex2(-gap) * sm.beta[kSub * J + j];
+                da[q] = ia ? f * ae[q] : 0.f;
+                dm[q] = im ? -f * le[q] : 0.f;
+                sum += da[q] * rk[q] + dm[q] * kk[q];
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                f4 a;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) a[q] = widen(sm.k[kSub * J + 4 * g + q][16 * c + l16]);
+                drT[c] = mma16(a, da, drT[c]);
+                dkT[c] = mma16(a, dm, dkT[c]);
+            }
+            if (J < x) {
+                sum = sum_groups(sum);
+                rowv += sum;
+                sum = sum16(sum);
+                if (lane == 0) sm.cross[x][J] = sum;
+            }
+        }
+        // blocks I >= x with this wave's tokens as j: rows i = 4 g + q, columns j
+#pragma unroll 1
+        for (int I = x; I < kWaves; ++I) {
+            f4 ae = {0.f, 0.f, 0.f, 0.f}, le = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                ae = mma16(go4(kSub * I + l16, c), eX[c], ae);
+                le = mma16(load4(&sm.lam[kSub * I + l16][16 * c + 4 * g]), eX[c], le);
+                const f4 k4 = load4(&sm.k[mine][16 * c + 4 * g]);
+                kk = mma16(load4(&sm.k[kSub * I + l16][16 * c + 4 * g]), k4, kk);
+                rk = mma16(load4(&sm.r[kSub * I + l16][16 * c + 4 * g]), k4, rk);
+            }
+            float mid = suf;
+            for (int i = 0; i < kWaves; ++i) mid += i > x && i < I ? sm.total[i] : 0.f;
+            f4 da, dm;
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 4 * g + q;
+                float gap = mid + sm.pre[kSub * I + i];
+                if (I == x) {
+                    gap = 0.f;
+#pragma unroll
+                    for (int l = 0; l < kSub; ++l) gap += l > l16 && l <= i ? sm.w[kSub * x + l] : 0.f;
+                }
+                const bool ia = I > x || l16 <= i, im = I > x || l16 < i;
+                const float f = ex2(-gap);
+                da[q] = ia ? f * ae[q] : 0.f;
+                dm[q] = im ? -f * le[q] : 0.f;
+                const float p = da[q] * rk[q] + dm[q] * kk[q];
+                if (I == x) sm.diag[x][i][l16] = beta * p;
+                sum += p;
+            }
+            sum = sum_groups(sum);
+            dbeta += sum;
+            if (I > x) colv += beta * sum;
+            da *= beta;
+            dm *= beta;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                f4 a, a2;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q] = widen(sm.r[kSub * I + 4 * g + q][16 * c + l16]);
+                    a2[q] = widen(sm.k[kSub * I + 4 * g + q][16 * c + l16]);
+                }
+                dkT[c] = mma16(a2, dm, mma16(a, da, dkT[c]));
+            }
+        }
+        // the rates
+        const float rowsum = sum16(withS), colsum = sum16(beta * withG);
+        if (lane == 0) {
+            sm.rows[x] = rowsum;
+            sm.cols[x] = colsum;
+        }
+        if (g == 0) {
+            sm.rowv[x][l16] = rowv;
+            sm.colv[x][l16] = colv;
+        }
+        __syncthreads();
+        if (g == 0 && t0 + mine < P.T) {
+            float c = all * inner;
+            for (int I = x + 1; I < kWaves; ++I) {
+                c += sm.rows[I];
+                for (int J = 0; J < x; ++J) c += sm.cross[I][J];
+            }
+            for (int J = 0; J < x; ++J) c += sm.cols[J];
+            for (int i = 0; i < kSub; ++i) {
+                c += i >= l16 ? sm.rowv[x][i] : sm.colv[x][i];
+                for (int j = 0; j < kSub; ++j) c += j < l16 && i >= l16 ? sm.diag[x][i][j] : 0.f;
+            }
+            const int64_t at = (b * P.T + t0 + mine) * P.H + h;
+            P.dw[at] = t0 + mine < len ? -c : 0.f;
+            P.dbeta[at] = dbeta;
+        }
+    }
+    if (t0 + mine < P.T) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            store4(&dr[(t0 + mine) * ks + 16 * c + 4 * g], drT[c]);
+            store4(&dk[(t0 + mine) * ks + 16 * c + 4 * g], dkT[c]);
+        }
+    }
+}
+
+template <typename T, int N>
+hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
+    if (a.states == nullptr && a.o != nullptr && a.T <= kDeltaStepMaxT) {
+        const int64_t waves = a.B * a.H * (N / 64);
+        hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)),
+                           dim3(64 * kWaves), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((delta_fwd_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.H * (N / kCols))),
+                           dim3(64 * kWaves), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((delta_adjoint_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.H * (N / kCols))),
+                       dim3(64 * kWaves), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t ntile = (a.T + kTile - 1) / kTile;
+    hipLaunchKernelGGL((delta_grad_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.HK * ntile)), dim3(64 * kWaves), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream) {
+    if (a.bf16) return a.N == 64 ? launch_fwd<uint16_t, 64>(a, stream) : launch_fwd<uint16_t, 128>(a, stream);
+    return a.N == 64 ? launch_fwd<float, 64>(a, stream) : launch_fwd<float, 128>(a, stream);
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
+    if (a.bf16) return a.N == 64 ? launch_bwd<uint16_t, 64>(a, stream) : launch_bwd<uint16_t, 128>(a, stream);
+    return a.N == 64 ? launch_bwd<float, 64>(a, stream) : launch_bwd<float, 128>(a, stream);
+}
+
+}  // namespace wkv

@@ -239,6 +239,51 @@ hipError_t launch_wkv6_bwd(const Wkv6BwdArgs& a, hipStream_t stream);
 hipError_t launch_wkv5_state_copy(const float* s_in, float* s_out, int64_t n, hipStream_t stream);
 hipError_t launch_wkv5_bwd(const Wkv5BwdArgs& a, hipStream_t stream);
 
+// Up to this many tokens without saved states the delta rule runs token by token (delta_step_kernel).
+constexpr int64_t kDeltaStepMaxT = 16;
+
+struct DeltaArgs {
+    int64_t B, T, H, HK, N;   // H value heads of N channels share HK key heads
+    bool bf16;
+    const int32_t* lengths;   // [B] tokens of each row, or NULL (T)
+    const float* w;           // [B, T, H] decay rates
+    const float* beta;        // [B, T, H] write strengths
+    const void* r;            // [B, T, HK N]
+    const void* k;
+    const void* v;            // [B, T, H N]
+    void* o;                  // [B, T, H N] or NULL (a pass for the saved states only)
+    const float* s_in;        // [B, H, N, N] or NULL (zero state)
+    float* s_out;             // [B, H, N, N] or NULL
+    float* errs;              // [B, T, H, N] the errors e_t, or NULL
+    float* states;            // [B, H, ceil(T / 64), N, N] the state before every 64 tokens, or NULL
+};
+
+struct DeltaBwdArgs {
+    int64_t B, T, H, HK, N;
+    bool bf16;
+    const int32_t* lengths;
+    const float* w;
+    const float* beta;
+    const void* r;
+    const void* k;
+    const void* go;           // [B, T, H N] gradient of o
+    const float* errs;        // as DeltaArgs
+    const float* states;
+    const float* ds_out;      // [B, H, N, N] or NULL (zero)
+    float* lambda;            // scratch [B, T, H, N]
+    float* gstates;           // scratch [B, H, ceil(T / 64), N, N]
+    void* dr;                 // [B, T, HK N]
+    void* dk;
+    void* dv;                 // [B, T, H N]
+    float* dw;                // [B, T, H]
+    float* dbeta;
+    float* ds_in;             // [B, H, N, N] or NULL
+};
+
+// gated delta rule (wkv_delta.hip)
+hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream);
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream);
+
 // decode step (wkv_step.hip)
 hipError_t launch_step(const StepArgs& s, hipStream_t stream);
 

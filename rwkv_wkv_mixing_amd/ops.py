@@ -672,3 +672,158 @@ class Wkv6Function(torch.autograd.Function):
                                                need_state_grad=state_in is not None and ctx.needs_input_grad[5],
                                                ckpt=ckpt)
         return dw, du, dr.to(r.dtype), dk.to(k.dtype), dv.to(v.dtype), ds
+
+
+def _delta_shape(w, r, v):
+    """(B, T, H, HK, N) of a delta-rule call from w [B, T, H], r [B, T, HK N], v [B, T, H N]."""
+    if w.dim() != 3 or r.dim() != 3 or v.dim() != 3:
+        raise ValueError("w, r and v must have three dimensions [B, T, .]")
+    B, T, H = w.shape
+    N = v.shape[2] // H if H else 64
+    if N not in (64, 128) or v.shape[2] != H * N:
+        raise ValueError(f"v has {v.shape[2]} channels for {H} heads: heads of 64 or 128 are needed")
+    HK = r.shape[2] // N
+    if r.shape[2] != HK * N or (H % HK if HK else H):
+        raise ValueError(f"r has {r.shape[2]} channels: a multiple of {N} whose heads divide {H} is needed")
+    return B, T, H, HK, N
+
+
+def _delta_inputs(w, beta, r, k, v, lengths):
+    _need(r, "r", (torch.float32, torch.bfloat16))
+    dev, dt = r.device, r.dtype
+    B, T, H, HK, N = shape = _delta_shape(w, r, v)
+    _need(r, "r", dt, (B, T, HK * N), dev)
+    _need(k, "k", dt, (B, T, HK * N), dev)
+    _need(v, "v", dt, (B, T, H * N), dev)
+    _need(w, "w", torch.float32, (B, T, H), dev)
+    _need(beta, "beta", torch.float32, (B, T, H), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    return shape
+
+
+def _bytes_of(t):
+    return t.numel() * t.element_size()
+
+
+def _scratch(workspace, nbytes, dev):
+    """A workspace of at least nbytes: the caller's, checked, or a new one."""
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", None, None, dev)
+    if _bytes_of(workspace) < nbytes:
+        raise ValueError(f"workspace has {_bytes_of(workspace)} bytes, needs {nbytes}")
+    return workspace
+
+
+def _launch_on(dev, bind, name, fn, args, result, scope):
+    """_launch with dev the current device, which the library's calls run on."""
+    if dev.index == torch.cuda.current_device():
+        return _launch(bind, name, fn, args, result, scope)
+    if bind:
+        raise ValueError(f"bind needs the tensors' device {dev} to be the current one")
+    with torch.cuda.device(dev):
+        return _launch(bind, name, fn, args, result, scope)
+
+
+def delta_ckpt_bytes(B: int, T: int, H: int, N: int) -> int:
+    return int(L.lib().wkv_delta_ckpt_bytes(B, T, H, N))
+
+
+def new_delta_ckpt(B: int, T: int, H: int, N: int, device) -> torch.Tensor:
+    """Buffer for what delta_forward saves for delta_backward (opaque bytes)."""
+    return torch.empty(max(delta_ckpt_bytes(B, T, H, N), 1), dtype=torch.uint8, device=device)
+
+
+def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=None, return_state=False, out=None,
+                  ckpt=None, workspace=None, split=True, bind=False):
+    """The gated delta rule: o [B, T, H N] from w, beta [B, T, H] float32, r, k [B, T, HK N] and
+    v [B, T, H N] (float32 or bfloat16, o too); N is 64 or 128 and value head h reads key head
+    h // (H // HK).  Per token D = e^{-w} S, e = v - k D, S = D + beta k^T e, o = r S.
+
+    lengths: None or [B] int32, the tokens of each row (the rest are not read, leave the state and
+    give zeros).  state_in: [B, H, N, N] float32 or None (zero).  state_out: tensor to receive the
+    state after each row's last token (may be state_in); with return_state and no state_out one is
+    allocated and the call returns (o, state).  ckpt: None or a new_delta_ckpt() buffer for
+    delta_backward.  With few (row, head) pairs and many tokens the call splits the sequences in
+    time, in a workspace it allocates (or is given); split=False keeps them whole."""
+    B, T, H, HK, N = _delta_inputs(w, beta, r, k, v, lengths)
+    dev = r.device
+    if out is None:
+        out = torch.empty((B, T, H * N), dtype=r.dtype, device=dev)
+    else:
+        _need(out, "out", r.dtype, (B, T, H * N), dev)
+    if state_in is not None:
+        _need(state_in, "state_in", torch.float32, (B, H, N, N), dev)
+    if state_out is None and return_state:
+        state_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
+    elif state_out is not None:
+        _need(state_out, "state_out", torch.float32, (B, H, N, N), dev)
+    lib = L.lib()
+    if ckpt is not None:
+        _need(ckpt, "ckpt", torch.uint8, None, dev)
+        if ckpt.numel() < delta_ckpt_bytes(B, T, H, N):
+            raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {delta_ckpt_bytes(B, T, H, N)}")
+    nws = int(lib.wkv_delta_forward_workspace_bytes(B, T, H, HK, N)) if split else 0
+    workspace = _scratch(workspace, nws, dev) if nws else None
+    args = (B, T, H, HK, N, _DT[r.dtype], _p(lengths), _p(w), _p(beta), _p(r), _p(k), _p(v), _p(out), _p(state_in),
+            _p(state_out), _p(ckpt), _p(workspace), _bytes_of(workspace) if nws else 0, _stream(dev))
+    return _launch_on(dev, bind, "wkv_delta_forward", lib.wkv_delta_forward, args,
+                      (out, state_out) if return_state else out, locals())
+
+
+def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_state_out=None, need_state_grad=False,
+                   ckpt=None, workspace=None, bind=False):
+    """Gradients of sum <go, o> + <grad_state_out, S_T> for (o, S_T) = delta_forward(w, beta, r, k, v,
+    lengths=lengths, state_in=state_in, return_state=True): (dr, dk, dv, dw, dbeta, ds_in), dr, dk, dv
+    in r's dtype (those of a key head summed over its value heads), dw, dbeta [B, T, H] float32, ds_in
+    [B, H, N, N] float32 or None.  go: [B, T, H N] in r's dtype.  ckpt: None or what the forward wrote."""
+    B, T, H, HK, N = _delta_inputs(w, beta, r, k, v, lengths)
+    dev = r.device
+    _need(go, "go", r.dtype, (B, T, H * N), dev)
+    if state_in is not None:
+        _need(state_in, "state_in", torch.float32, (B, H, N, N), dev)
+    if grad_state_out is not None:
+        _need(grad_state_out, "grad_state_out", torch.float32, (B, H, N, N), dev)
+    dr, dk, dv = torch.empty_like(r), torch.empty_like(k), torch.empty_like(v)
+    dw, dbeta = torch.empty_like(w), torch.empty_like(beta)
+    ds = torch.empty((B, H, N, N), dtype=torch.float32, device=dev) if need_state_grad else None
+    lib = L.lib()
+    if ckpt is not None:
+        _need(ckpt, "ckpt", torch.uint8, None, dev)
+        if ckpt.numel() < delta_ckpt_bytes(B, T, H, N):
+            raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {delta_ckpt_bytes(B, T, H, N)}")
+    nbytes = int(lib.wkv_delta_backward_workspace_bytes(B, T, H, HK, N, 1 if ckpt is not None else 0))
+    workspace = _scratch(workspace, nbytes, dev)
+    args = (B, T, H, HK, N, _DT[r.dtype], _p(lengths), _p(w), _p(beta), _p(r), _p(k), _p(v), _p(go), _p(state_in),
+            _p(grad_state_out), _p(dr), _p(dk), _p(dv), _p(dw), _p(dbeta), _p(ds), _p(ckpt), _p(workspace),
+            _bytes_of(workspace), _stream(dev))
+    return _launch_on(dev, bind, "wkv_delta_backward", lib.wkv_delta_backward, args, (dr, dk, dv, dw, dbeta, ds), locals())
+
+
+class DeltaFunction(torch.autograd.Function):
+    """Autograd wrapper: (o, state) = delta_forward(...); backward through delta_backward."""
+
+    @staticmethod
+    def forward(ctx, w, beta, r, k, v, state_in, lengths):
+        B, T, H, HK, N = _delta_shape(w, r, v)
+        ckpt = new_delta_ckpt(B, T, H, N, r.device)
+        o, state = delta_forward(w, beta, r, k, v, lengths=lengths, state_in=state_in, return_state=True, ckpt=ckpt)
+        ctx.save_for_backward(w, beta, r, k, v, state_in, lengths, ckpt)
+        ctx.set_materialize_grads(False)
+        return o, state
+
+    @staticmethod
+    def backward(ctx, go, gstate):
+        w, beta, r, k, v, state_in, lengths, ckpt = ctx.saved_tensors
+        go = torch.zeros_like(v) if go is None else go.contiguous()
+        dr, dk, dv, dw, dbeta, ds = delta_backward(
+            w, beta, r, k, v, go, lengths=lengths, state_in=state_in,
+            grad_state_out=None if gstate is None else gstate.contiguous(),
+            need_state_grad=state_in is not None and ctx.needs_input_grad[5], ckpt=ckpt)
+        return dw, dbeta, dr, dk, dv, ds, None
+
+
+def delta_rule(w, beta, r, k, v, state_in=None, lengths=None):
+    """Differentiable gated delta rule: (o, state after each row's last token) (see delta_forward)."""
+    return DeltaFunction.apply(w, beta, r, k, v, state_in, lengths)
