@@ -2,7 +2,8 @@
  * wkv.h - C ABI of the RWKV-4 WKV time-mixing operator for AMD MI355X (gfx950),
  * with the receptance gate and the token-shift mix around it, and the
  * matrix-state WKV of RWKV-5 and RWKV-6 (per-token decay), forward and
- * backward, and the gated delta rule on the same kind of state.
+ * backward, the gated delta rule on the same kind of state, and the norms
+ * around the mixing.
  *
  * The operator, per channel c of each batch row b, tokens t = 1..T
  * ("RWKV（Receptance Weighted Key Value）概念", section 3.2; and
@@ -577,6 +578,84 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
                                 const float* s_in, const float* ds_out, void* dr, void* dk, void* dv,
                                 float* dw, float* dbeta, float* ds_in, const void* ckpt, void* workspace,
                                 size_t workspace_bytes, void* hip_stream);
+
+/* The norms' flags and the activation of their gate. */
+#define WKV_NORM_CENTER 1 /* take the mean off (layer norm); without it, root mean square */
+#define WKV_NORM_SHARED 2 /* head norm: weight and bias [G], one for all heads */
+enum { WKV_ACT_NONE = 0, WKV_ACT_SIGMOID = 1, WKV_ACT_SILU = 2 };
+
+/*
+ * wkv_head_norm / wkv_head_norm_backward - the norm over each head's channels
+ * with its gate: behind the matrix-state mixing, before the output projection
+ * ("RWKV模型深度研究报告（截至2026年初）", section 1.3.2: the multi-head state;
+ * the norm over each head and its gate are this library's extension); without a
+ * gate and with weight 1 / sqrt(G) it makes unit keys.
+ *
+ * Defines, per row and head of G channels, with norm(y) = (y - m) /
+ * sqrt(mean((y - m)^2) + eps), m the mean (WKV_NORM_CENTER) or 0:
+ *     out = act(gate) * (norm(y) * weight + bias)
+ * act(g) is g, sigmoid(g) or g sigmoid(g); without a gate the factor is 1.
+ * Float32 arithmetic; outputs rounded once.
+ *
+ * rows, H, G  rows (>= 0), heads (>= 0), channels a head (1 .. 1024).
+ * y_dtype   dtype of y and dy; dtype: of gate, gout, out and dgate.  WKV_BF16 y
+ *           needs WKV_BF16 for both (WKV_EDTYPE otherwise).
+ * y, gate, out, gout, dy, dgate  [rows, H G]; out must not alias an input.
+ * weight    [H G] float32, or [G] with WKV_NORM_SHARED; bias alike, or NULL.
+ * gate      or NULL.
+ * dweight, dbias  like weight, overwritten with sums over the rows (and heads,
+ *           when shared) in a fixed order; dbias is needed with bias, dgate with
+ *           gate, and they are not written without.
+ * workspace wkv_head_norm_backward_workspace_bytes() bytes, 256-byte aligned;
+ *           clobbered.  Not needed without elements.
+ */
+wkv_status_t wkv_head_norm(int64_t rows, int64_t H, int64_t G, int y_dtype, int dtype, int flags, int act, float eps,
+                           const void* y, const float* weight, const float* bias, const void* gate, void* out,
+                           void* hip_stream);
+size_t wkv_head_norm_backward_workspace_bytes(int64_t rows, int64_t H, int64_t G);
+wkv_status_t wkv_head_norm_backward(int64_t rows, int64_t H, int64_t G, int y_dtype, int dtype, int flags, int act,
+                                    float eps, const void* y, const float* weight, const float* bias, const void* gate,
+                                    const void* gout, void* dy, float* dweight, float* dbias, void* dgate,
+                                    void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * wkv_block_norm / wkv_block_norm_backward - what stands between two blocks:
+ * the norm after a block with its gate and residual scale, the residual sum,
+ * and the norm before the next block, in one pass.
+ *
+ * Defines, per row of C channels (norm and act as wkv_head_norm):
+ *     z = act(gate) * (norm(y) * post_w + post_b)     (post_w NULL: act(gate) * y)
+ *     x_out = x + scale * z,   h = norm(x_out) * pre_w + pre_b
+ * ("RWKV（Receptance Weighted Key Value）概念", section 3.3: the channel mixing's
+ * output is gated by sigmoid(r) and added to the residual stream.)  h is taken
+ * from x_out before its rounding.
+ *
+ * The backward takes x_out as the forward returned it, gh the gradient of h
+ * and gx that of x_out from later in the residual stream (or NULL), and gives
+ *     dx = gx + (gradient through h)      (the gradient of x, and of the sum)
+ * and, of the same sum, dy, dgate, dscale, dpost_w, dpost_b; and dpre_w, dpre_b.
+ *
+ * rows, C   rows (>= 0), channels (0 .. 8192).
+ * x_dtype   dtype of x, x_out, gx, dx; dtype: of y, gate, h, gh, dy, dgate.
+ *           WKV_BF16 x needs WKV_BF16 for both.
+ * post_w, post_b, scale, pre_w, pre_b  [C] float32; all but pre_w may be NULL, and
+ *           post_b needs post_w.  Each given one needs its gradient's buffer
+ *           (overwritten, summed over the rows in a fixed order); gate needs dgate.
+ * x_out may be x, and dx may be gx (the same dtype, the same place).
+ * workspace wkv_block_norm_backward_workspace_bytes() bytes, 256-byte aligned;
+ *           clobbered.  Not needed without rows.
+ */
+wkv_status_t wkv_block_norm(int64_t rows, int64_t C, int x_dtype, int dtype, int flags, int act, float eps,
+                            const void* x, const void* y, const void* gate, const float* post_w, const float* post_b,
+                            const float* scale, const float* pre_w, const float* pre_b, void* x_out, void* h,
+                            void* hip_stream);
+size_t wkv_block_norm_backward_workspace_bytes(int64_t rows, int64_t C);
+wkv_status_t wkv_block_norm_backward(int64_t rows, int64_t C, int x_dtype, int dtype, int flags, int act, float eps,
+                                     const void* x_out, const void* y, const void* gate, const float* post_w,
+                                     const float* post_b, const float* scale, const float* pre_w, const float* pre_b,
+                                     const void* gx, const void* gh, void* dx, void* dy, void* dgate, float* dpost_w,
+                                     float* dpost_b, float* dscale, float* dpre_w, float* dpre_b, void* workspace,
+                                     size_t workspace_bytes, void* hip_stream);
 
 /*
  * wkv_token_shift / wkv_token_shift_backward - the token-shift mix that

@@ -16,6 +16,8 @@ WKV_STATIC_SCRATCH_BYTES = 32 << 20
 WKV_F32, WKV_BF16 = 0, 1
 WKV_OP_FORWARD, WKV_OP_BACKWARD = 0, 1
 WKV_CKPT_LEN = 16
+WKV_NORM_CENTER, WKV_NORM_SHARED = 1, 2
+WKV_ACT_NONE, WKV_ACT_SIGMOID, WKV_ACT_SILU = 0, 1, 2
 
 # every symbol include/wkv.h declares
 EXPORTS = (
@@ -44,6 +46,12 @@ EXPORTS = (
     "wkv_delta_forward_workspace_bytes",
     "wkv_delta_backward_workspace_bytes",
     "wkv_delta_backward",
+    "wkv_head_norm",
+    "wkv_head_norm_backward_workspace_bytes",
+    "wkv_head_norm_backward",
+    "wkv_block_norm",
+    "wkv_block_norm_backward_workspace_bytes",
+    "wkv_block_norm_backward",
     "wkv_token_shift_workspace_bytes",
     "wkv_token_shift",
     "wkv_token_shift_backward",
@@ -136,6 +144,19 @@ def declare(L):
     L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 5 + [i32]
     L.wkv_delta_backward.restype = i32
     L.wkv_delta_backward.argtypes = [i64] * 5 + [i32] + [vp] * 17 + [sz, vp]
+    f32 = ctypes.c_float
+    L.wkv_head_norm.restype = i32
+    L.wkv_head_norm.argtypes = [i64] * 3 + [i32] * 4 + [f32] + [vp] * 6
+    L.wkv_head_norm_backward_workspace_bytes.restype = sz
+    L.wkv_head_norm_backward_workspace_bytes.argtypes = [i64] * 3
+    L.wkv_head_norm_backward.restype = i32
+    L.wkv_head_norm_backward.argtypes = [i64] * 3 + [i32] * 4 + [f32] + [vp] * 10 + [sz, vp]
+    L.wkv_block_norm.restype = i32
+    L.wkv_block_norm.argtypes = [i64] * 2 + [i32] * 4 + [f32] + [vp] * 11
+    L.wkv_block_norm_backward_workspace_bytes.restype = sz
+    L.wkv_block_norm_backward_workspace_bytes.argtypes = [i64] * 2
+    L.wkv_block_norm_backward.restype = i32
+    L.wkv_block_norm_backward.argtypes = [i64] * 2 + [i32] * 4 + [f32] + [vp] * 19 + [sz, vp]
     L.wkv_token_shift_workspace_bytes.restype = sz
     L.wkv_token_shift_workspace_bytes.argtypes = [i64, i64, i64, i64]
     L.wkv_token_shift.restype = i32

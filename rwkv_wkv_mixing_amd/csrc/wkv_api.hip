@@ -781,6 +781,175 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
     return hip_status(wkv::launch_delta_bwd(a, stream));
 }
 
+}  // extern "C"
+
+namespace {
+
+bool act_ok(int act) { return act == WKV_ACT_NONE || act == WKV_ACT_SIGMOID || act == WKV_ACT_SILU; }
+
+// Checks the norms share: a wide dtype (of the statistics' input) and a narrow one no wider than it,
+// flags, activation, and eps a finite number >= 0.
+wkv_status_t norm_check(int wide, int narrow, int flags, int known, int act, float eps) {
+    if (!dtype_ok(wide) || !dtype_ok(narrow) || (wide == WKV_BF16 && narrow == WKV_F32)) return WKV_EDTYPE;
+    if ((flags & ~known) != 0 || !act_ok(act) || !(eps >= 0.f) || eps > 1e30f) return WKV_EINVAL;
+    return WKV_OK;
+}
+
+constexpr int64_t kMaxHeadNorm = 1024;   // channels a wave holds
+constexpr int64_t kMaxBlockNorm = 8192;  // channels a workgroup holds
+
+wkv_status_t head_norm_check(int64_t rows, int64_t H, int64_t G, int64_t* n) {
+    if (rows < 0 || H < 0 || G < 1 || G > kMaxHeadNorm) return WKV_EINVAL;
+    if (!mul3(rows, H, G, n) || *n > (int64_t{1} << 58)) return WKV_ESIZE;
+    if (rows * H >= (int64_t{1} << 31) || H * G >= (int64_t{1} << 31)) return WKV_ESIZE;
+    return WKV_OK;
+}
+
+wkv_status_t block_norm_check(int64_t rows, int64_t C, int64_t* n) {
+    if (rows < 0 || C < 0 || C > kMaxBlockNorm) return WKV_EINVAL;
+    if (!mul3(rows, C, 1, n) || rows >= (int64_t{1} << 31)) return WKV_ESIZE;
+    return WKV_OK;
+}
+
+// all of the pointers (NULL counts) aligned to `a`
+template <class... P>
+bool all_aligned(size_t a, P... p) {
+    return (aligned(p, a) && ...);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wkv_head_norm_backward_workspace_bytes(int64_t rows, int64_t H, int64_t G) {
+    int64_t n;
+    if (head_norm_check(rows, H, G, &n) != WKV_OK) return 0;
+    return static_cast<size_t>(wkv::head_norm_chunks(rows)) * static_cast<size_t>(H * G) * 2 * sizeof(float);
+}
+
+wkv_status_t wkv_head_norm(int64_t rows, int64_t H, int64_t G, int y_dtype, int dtype, int flags, int act, float eps,
+                           const void* y, const float* weight, const float* bias, const void* gate, void* out,
+                           void* hip_stream) {
+    int64_t n;
+    wkv_status_t st = head_norm_check(rows, H, G, &n);
+    if (st == WKV_OK) st = norm_check(y_dtype, dtype, flags, WKV_NORM_CENTER | WKV_NORM_SHARED, act, eps);
+    if (st != WKV_OK) return st;
+    if (n == 0) return WKV_OK;
+    if (!y || !weight || !out) return WKV_EINVAL;
+    if (!aligned(y, in_size(y_dtype)) || !all_aligned(4, weight, bias) || !all_aligned(in_size(dtype), gate, out))
+        return WKV_EALIGN;
+    wkv::HeadNormArgs a{rows, H, G, y_dtype == WKV_BF16, dtype == WKV_BF16, (flags & WKV_NORM_CENTER) != 0,
+                        (flags & WKV_NORM_SHARED) != 0, false, act, eps, y, weight, bias, gate};
+    a.out = out;
+    a.vec = G % 8 == 0 && all_aligned(16, y, weight, bias, gate, out);
+    return hip_status(wkv::launch_head_norm(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+wkv_status_t wkv_head_norm_backward(int64_t rows, int64_t H, int64_t G, int y_dtype, int dtype, int flags, int act,
+                                    float eps, const void* y, const float* weight, const float* bias, const void* gate,
+                                    const void* gout, void* dy, float* dweight, float* dbias, void* dgate,
+                                    void* workspace, size_t workspace_bytes, void* hip_stream) {
+    int64_t n;
+    wkv_status_t st = head_norm_check(rows, H, G, &n);
+    if (st == WKV_OK) st = norm_check(y_dtype, dtype, flags, WKV_NORM_CENTER | WKV_NORM_SHARED, act, eps);
+    if (st != WKV_OK) return st;
+    if (!dweight || (bias && !dbias)) return WKV_EINVAL;
+    if (!all_aligned(4, weight, bias, dweight, dbias)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const bool shared = (flags & WKV_NORM_SHARED) != 0;
+    if (n == 0) {  // empty sums
+        const int64_t nw = shared ? G : H * G;
+        hipError_t e = wkv::launch_norm_zero(dweight, nw, stream);
+        if (e == hipSuccess && bias) e = wkv::launch_norm_zero(dbias, nw, stream);
+        return hip_status(e);
+    }
+    if (!y || !weight || !gout || !dy || (gate && !dgate)) return WKV_EINVAL;
+    if (!all_aligned(in_size(y_dtype), y, dy) || !all_aligned(in_size(dtype), gate, gout, dgate)) return WKV_EALIGN;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < wkv_head_norm_backward_workspace_bytes(rows, H, G))
+        return WKV_EWORKSPACE;
+    wkv::HeadNormArgs a{rows, H, G, y_dtype == WKV_BF16, dtype == WKV_BF16, (flags & WKV_NORM_CENTER) != 0, shared,
+                        false, act, eps, y, weight, bias, gate};
+    a.gout = gout;
+    a.dy = dy;
+    a.dgate = dgate;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.ws = static_cast<float*>(workspace);
+    a.vec = G % 8 == 0 && all_aligned(16, y, weight, bias, gate, gout, dy, dgate);
+    return hip_status(wkv::launch_head_norm_bwd(a, stream));
+}
+
+size_t wkv_block_norm_backward_workspace_bytes(int64_t rows, int64_t C) {
+    int64_t n;
+    if (block_norm_check(rows, C, &n) != WKV_OK) return 0;
+    return static_cast<size_t>(wkv::block_norm_slots(rows, C)) * static_cast<size_t>(C) * 5 * sizeof(float);
+}
+
+wkv_status_t wkv_block_norm(int64_t rows, int64_t C, int x_dtype, int dtype, int flags, int act, float eps,
+                            const void* x, const void* y, const void* gate, const float* post_w, const float* post_b,
+                            const float* scale, const float* pre_w, const float* pre_b, void* x_out, void* h,
+                            void* hip_stream) {
+    int64_t n;
+    wkv_status_t st = block_norm_check(rows, C, &n);
+    if (st == WKV_OK) st = norm_check(x_dtype, dtype, flags, WKV_NORM_CENTER, act, eps);
+    if (st != WKV_OK) return st;
+    if (n == 0) return WKV_OK;
+    if (!x || !y || !pre_w || !x_out || !h || (post_b && !post_w)) return WKV_EINVAL;
+    if (!all_aligned(in_size(x_dtype), x, x_out) || !all_aligned(in_size(dtype), y, gate, h) ||
+        !all_aligned(4, post_w, post_b, scale, pre_w, pre_b))
+        return WKV_EALIGN;
+    wkv::BlockNormArgs a{rows, C, x_dtype == WKV_BF16, dtype == WKV_BF16, (flags & WKV_NORM_CENTER) != 0, false, act, eps,
+                         x, y, gate, post_w, post_b, scale, pre_w, pre_b};
+    a.x_out = x_out;
+    a.h = h;
+    a.vec = C % 8 == 0 && all_aligned(16, x, y, gate, post_w, post_b, scale, pre_w, pre_b, x_out, h);
+    return hip_status(wkv::launch_block_norm(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+wkv_status_t wkv_block_norm_backward(int64_t rows, int64_t C, int x_dtype, int dtype, int flags, int act, float eps,
+                                     const void* x_out, const void* y, const void* gate, const float* post_w,
+                                     const float* post_b, const float* scale, const float* pre_w, const float* pre_b,
+                                     const void* gx, const void* gh, void* dx, void* dy, void* dgate, float* dpost_w,
+                                     float* dpost_b, float* dscale, float* dpre_w, float* dpre_b, void* workspace,
+                                     size_t workspace_bytes, void* hip_stream) {
+    int64_t n;
+    wkv_status_t st = block_norm_check(rows, C, &n);
+    if (st == WKV_OK) st = norm_check(x_dtype, dtype, flags, WKV_NORM_CENTER, act, eps);
+    if (st != WKV_OK) return st;
+    if (C == 0) return WKV_OK;
+    if (!dpre_w || (pre_b && !dpre_b) || (post_w && !dpost_w) || (post_b && (!dpost_b || !post_w)) || (scale && !dscale))
+        return WKV_EINVAL;
+    if (!all_aligned(4, post_w, post_b, scale, pre_w, pre_b, dpost_w, dpost_b, dscale, dpre_w, dpre_b)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (rows == 0) {  // empty sums
+        float* const out[5] = {dpre_w, pre_b ? dpre_b : nullptr, post_w ? dpost_w : nullptr, post_b ? dpost_b : nullptr,
+                               scale ? dscale : nullptr};
+        hipError_t e = hipSuccess;
+        for (int k = 0; k < 5 && e == hipSuccess; ++k) e = wkv::launch_norm_zero(out[k], C, stream);
+        return hip_status(e);
+    }
+    if (!x_out || !y || !pre_w || !gh || !dx || !dy || (gate && !dgate)) return WKV_EINVAL;
+    if (!all_aligned(in_size(x_dtype), x_out, gx, dx) || !all_aligned(in_size(dtype), y, gate, gh, dy, dgate))
+        return WKV_EALIGN;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < wkv_block_norm_backward_workspace_bytes(rows, C))
+        return WKV_EWORKSPACE;
+    wkv::BlockNormArgs a{rows, C, x_dtype == WKV_BF16, dtype == WKV_BF16, (flags & WKV_NORM_CENTER) != 0, false, act, eps,
+                         x_out, y, gate, post_w, post_b, scale, pre_w, pre_b};
+    a.gx = gx;
+    a.gh = gh;
+    a.dx = dx;
+    a.dy = dy;
+    a.dgate = dgate;
+    a.dpost_w = dpost_w;
+    a.dpost_b = dpost_b;
+    a.dscale = dscale;
+    a.dpre_w = dpre_w;
+    a.dpre_b = dpre_b;
+    a.ws = static_cast<float*>(workspace);
+    a.vec = C % 8 == 0 && all_aligned(16, x_out, y, gate, post_w, post_b, scale, pre_w, pre_b, gx, gh, dx, dy, dgate);
+    return hip_status(wkv::launch_block_norm_bwd(a, stream));
+}
+
 size_t wkv_token_shift_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t M) {
     const ShiftPlan p = shift_plan(B, T, C, M, WKV_F32);
     return p.st == WKV_OK ? p.ws_bytes : 0;

@@ -284,6 +284,72 @@ struct DeltaBwdArgs {
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream);
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, hipStream_t stream);
 
+enum { kActNone = 0, kActSigmoid = 1, kActSilu = 2 };  // = WKV_ACT_* in include/wkv.h
+
+struct HeadNormArgs {
+    int64_t rows, H, G;
+    bool y_bf16, bf16;        // dtype of y, dy; of gate, gout, out, dgate
+    bool center, shared;      // mean taken off; weight and bias [G] for all heads
+    bool vec;                 // 16-byte vectors: G a multiple of 8, pointers 16-byte aligned
+    int act;
+    float eps;
+    const void* y;            // [rows, H G]
+    const float* weight;      // [H G] or [G]
+    const float* bias;        // or NULL
+    const void* gate;         // [rows, H G] or NULL
+    void* out = nullptr;
+    // backward
+    const void* gout = nullptr;
+    void* dy = nullptr;
+    void* dgate = nullptr;
+    float* dweight = nullptr;
+    float* dbias = nullptr;
+    float* ws = nullptr;      // 2 head_norm_chunks(rows) H G floats
+    int lanes = 0, hpb = 0;   // lanes a head, heads a workgroup (set by the launch)
+    int64_t chunks = 0;
+};
+
+struct BlockNormArgs {
+    int64_t rows, C;
+    bool x_bf16, bf16;        // dtype of x, x_out, gx, dx; of y, gate, h and their gradients
+    bool center, vec;
+    int act;
+    float eps;
+    const void* x;            // [rows, C]; backward: the forward's x_out
+    const void* y;
+    const void* gate;         // or NULL
+    const float* post_w;      // [C] or NULL (y as it is)
+    const float* post_b;      // or NULL
+    const float* scale;       // or NULL (1)
+    const float* pre_w;
+    const float* pre_b;       // or NULL
+    void* x_out = nullptr;
+    void* h = nullptr;
+    // backward
+    const void* gx = nullptr; // or NULL (zero)
+    const void* gh = nullptr;
+    void* dx = nullptr;
+    void* dy = nullptr;
+    void* dgate = nullptr;
+    float* dpre_w = nullptr;
+    float* dpre_b = nullptr;
+    float* dpost_w = nullptr;
+    float* dpost_b = nullptr;
+    float* dscale = nullptr;
+    float* ws = nullptr;      // 5 block_norm_slots(rows, C) C floats
+    int threads = 0;          // that hold a row (set by the launch)
+    int64_t slots = 0;
+};
+
+// norms (wkv_norm.hip)
+hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream);
+hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream);
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t stream);
+hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream);
+int64_t head_norm_chunks(int64_t rows);
+int64_t block_norm_slots(int64_t rows, int64_t C);
+
 // decode step (wkv_step.hip)
 hipError_t launch_step(const StepArgs& s, hipStream_t stream);
 

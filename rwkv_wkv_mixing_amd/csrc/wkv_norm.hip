@@ -1,0 +1,691 @@
+// The norms around the mixing.
+//
+// Head norm (behind the matrix-state mixing, and on keys before it): per row and head of G channels
+//     out = act(gate) * (norm(y) * weight + bias)
+// Block norm (between two blocks): per row of C channels
+//     z = act(gate) * (norm(y) * post_w + post_b),   x_out = x + scale * z,   h = norm(x_out) * pre_w + pre_b
+// with norm(y) = (y - m) / sqrt(mean((y - m)^2) + eps), m the mean, or 0 (root mean square).
+//
+// Streaming work: every element is read once and stays in registers between the statistics and the
+// outputs.  The mean is taken first and the squares of what is left of it second, so a mean far above
+// the deviation costs no digits.  A head is held by 4 .. 64 lanes of a wave (8 elements each, 16 with
+// more than 512 channels) and its sums meet by shuffles; a row of a block norm by 64 .. 1024 threads.
+//
+// Backward, with g the gradient of norm(y) (that of z times act(gate) weight):
+//     dy = (g - yhat mean(g yhat) - [mean(g)]) / sqrt(mean((y - m)^2) + eps)
+// from statistics computed again.  The gradients of weights are sums over the rows: every workgroup
+// keeps its channels' sums in registers over the rows it takes, writes them as one row of partial
+// sums, and norm_reduce_kernel adds those in order (bitwise reproducible).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "wkv_launch.h"
+
+namespace wkv {
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ uint32_t pk2(float a, float b) {
+    const f2 p = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
+}
+
+// V consecutive elements as float32: 8 in 16-byte accesses, or 1.
+template <int V>
+__device__ __forceinline__ void load(const uint16_t* p, float (&f)[V]) {
+    if constexpr (V == 8) {
+        const u4 x = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(x[i] << 16);
+            f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+        }
+    } else {
+        f[0] = widen(*p);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load(const float* p, float (&f)[V]) {
+    if constexpr (V == 8) {
+        const f4 a = *reinterpret_cast<const f4*>(p), b = *reinterpret_cast<const f4*>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    } else {
+        f[0] = *p;
+    }
+}
+template <int V>
+__device__ __forceinline__ void store(uint16_t* p, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<u4*>(p) = u4{pk2(f[0], f[1]), pk2(f[2], f[3]), pk2(f[4], f[5]), pk2(f[6], f[7])};
+    } else {
+        *p = static_cast<uint16_t>(pk2(f[0], f[0]) & 0xffffu);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store(float* p, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<f4*>(p) = f4{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f4*>(p + 4) = f4{f[4], f[5], f[6], f[7]};
+    } else {
+        *p = f[0];
+    }
+}
+
+// act(g) and its derivative.  exp overflows to inf for g below -88, where both sigmoids are 0.
+__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
+    if (act == kActNone) {
+        a = g;
+        da = 1.f;
+        return;
+    }
+    const float s = 1.f / (1.f + __expf(-g));
+    if (act == kActSigmoid) {
+        a = s;
+        da = s * (1.f - s);
+    } else {
+        a = g * s;
+        da = s * (1.f + g * (1.f - s));
+    }
+}
+
+__device__ __forceinline__ float sum_lanes(float x, int lanes) {
+    for (int m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+constexpr int kBlock = 256;
+constexpr int kScalarVecs = 16;  // elements a lane of the element-by-element path: G up to 1024
+
+// What a lane holds of its head: NV vectors of V channels, vector i at channel (i lanes + lane) V.
+template <typename TY, typename TG, int V, int NV>
+__global__ void __launch_bounds__(kBlock) head_norm_kernel(HeadNormArgs P) {
+    const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1);
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
+    const bool live = id < P.rows * P.H;
+    const int64_t h = id % P.H, base = id * P.G, wb = P.shared ? 0 : h * P.G;
+    const int G = static_cast<int>(P.G);
+    const float inv_g = 1.f / static_cast<float>(G);
+    float y[NV][V];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+        if (live && c < G) {
+            load<V>(static_cast<const TY*>(P.y) + base + c, y[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[i][j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += y[i][j];
+    }
+    const float mean = P.center ? sum_lanes(sum, lanes) * inv_g : 0.f;
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if ((i * lanes + lane) * V < G) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                y[i][j] -= mean;
+                sq = fmaf(y[i][j], y[i][j], sq);
+            }
+        }
+    }
+    const float inv = 1.f / sqrtf(sum_lanes(sq, lanes) * inv_g + P.eps);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+        if (c >= G) continue;
+        float w[V], b[V], g[V];
+        load<V>(P.weight + wb + c, w);
+        if (P.bias != nullptr) load<V>(P.bias + wb + c, b);
+        if (P.gate != nullptr) load<V>(static_cast<const TG*>(P.gate) + base + c, g);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float z = y[i][j] * inv * w[j];
+            if (P.bias != nullptr) z += b[j];
+            if (P.gate != nullptr) {
+                float a, da;
+                activate(P.act, g[j], a, da);
+                z *= a;
+            }
+            y[i][j] = z;
+        }
+        store<V>(static_cast<TG*>(P.out) + base + c, y[i]);
+    }
+}
+
+// A workgroup takes hpb consecutive heads of rows r0, r0 + step, .., `rpb` rows at a time, and adds its
+// rows' sums in LDS at the end.
+template <typename TY, typename TG, int V, int NV>
+__global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
+    extern __shared__ float part[];  // [rpb][hpb G]
+    const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes;
+    const int hpb = P.hpb, rpb = kBlock / lanes / hpb;
+    const int64_t hblocks = (P.H + hpb - 1) / hpb;
+    const int64_t hb = blockIdx.x % hblocks, chunk = blockIdx.x / hblocks;
+    const int hs = slot % hpb, rs = slot / hpb;
+    const int64_t h = hb * hpb + hs;
+    const int G = static_cast<int>(P.G);
+    const int64_t C = P.H * P.G, wb = P.shared ? 0 : h * P.G;
+    const float inv_g = 1.f / static_cast<float>(G);
+    float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * lanes + lane) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[i][j] = b[i][j] = dw[i][j] = db[i][j] = 0.f;
+        if (h < P.H && c < G) {
+            load<V>(P.weight + wb + c, w[i]);
+            if (P.bias != nullptr) load<V>(P.bias + wb + c, b[i]);
+        }
+    }
+    for (int64_t r0 = chunk * rpb; r0 < P.rows; r0 += P.chunks * rpb) {
+        const int64_t row = r0 + rs;
+        const bool live = h < P.H && row < P.rows;
+        const int64_t base = row * C + h * P.G;
+        float y[NV][V], go[NV][V], g[NV][V];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * lanes + lane) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[i][j] = go[i][j] = g[i][j] = 0.f;
+            if (live && c < G) {
+                load<V>(static_cast<const TY*>(P.y) + base + c, y[i]);
+                load<V>(static_cast<const TG*>(P.gout) + base + c, go[i]);
+                if (P.gate != nullptr) load<V>(static_cast<const TG*>(P.gate) + base + c, g[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += y[i][j];
+        }
+        const float mean = P.center ? sum_lanes(sum, lanes) * inv_g : 0.f;
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((i * lanes + lane) * V < G) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    y[i][j] -= mean;
+                    sq = fmaf(y[i][j], y[i][j], sq);
+                }
+            }
+        }
+        const float inv = 1.f / sqrtf(sum_lanes(sq, lanes) * inv_g + P.eps);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float yh = y[i][j] * inv;
+                float dz = go[i][j];
+                if (P.gate != nullptr) {
+                    float a, da;
+                    activate(P.act, g[i][j], a, da);
+                    g[i][j] = dz * (yh * w[i][j] + b[i][j]) * da;
+                    dz *= a;
+                }
+                dw[i][j] = fmaf(dz, yh, dw[i][j]);
+                db[i][j] += dz;
+                const float d = dz * w[i][j];
+                s1 += d;
+                s2 = fmaf(d, yh, s2);
+                y[i][j] = yh;
+                go[i][j] = d;
+            }
+        }
+        s1 = P.center ? sum_lanes(s1, lanes) * inv_g : 0.f;
+        s2 = sum_lanes(s2, lanes) * inv_g;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * lanes + lane) * V;
+            if (c >= G) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[i][j] = inv * (go[i][j] - s1 - y[i][j] * s2);
+            store<V>(static_cast<TY*>(P.dy) + base + c, y[i]);
+            if (P.gate != nullptr) store<V>(static_cast<TG*>(P.dgate) + base + c, g[i]);
+        }
+    }
+    // the workgroup's rows in order, first dweight, then dbias
+    for (int what = 0; what < (P.bias != nullptr ? 2 : 1); ++what) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * lanes + lane) * V;
+            if (c >= G) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) part[(rs * hpb + hs) * G + c + j] = what ? db[i][j] : dw[i][j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < hpb * G; i += kBlock) {
+            if (hb * hpb * G + i >= C) continue;
+            float s = 0.f;
+            for (int q = 0; q < rpb; ++q) s += part[q * hpb * G + i];
+            P.ws[(what * P.chunks + chunk) * C + hb * hpb * G + i] = s;
+        }
+    }
+}
+
+// Partial sums [rows][cols] at part[k] to out[k][cols], k = blockIdx.y: 16 columns and 64 runs of rows a
+// workgroup, each run and then the runs in order.
+struct ReduceArgs {
+    int64_t rows, cols;
+    int count = 0;
+    const float* part[5];
+    float* out[5];
+    void add(const float* from, float* to) {
+        part[count] = from;
+        out[count++] = to;
+    }
+};
+
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(ReduceArgs P) {
+    __shared__ float s[64][17];
+    const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 + c;
+    const float* part = P.part[blockIdx.y];
+    float a = 0.f;
+    if (col < P.cols)
+        for (int64_t r = run; r < P.rows; r += 64) a += part[r * P.cols + col];
+    s[run][c] = a;
+    __syncthreads();
+    if (run == 0 && col < P.cols) {
+        float t = 0.f;
+        for (int i = 0; i < 64; ++i) t += s[i][c];
+        P.out[blockIdx.y][col] = t;
+    }
+}
+
+hipError_t launch_reduce(const ReduceArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.cols + 15) / 16), a.count), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+}
+
+// ---- block norm -----------------------------------------------------------------------------------
+
+// Sums of K values over the `threads` threads that hold a row (64: one wave; else the whole workgroup),
+// to all of them.  Every call of a row uses another half of the table, so one barrier a call is enough.
+template <int K>
+__device__ __forceinline__ void row_sums(float (&x)[K], int threads, float (*tab)[16][K], int& turn) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = sum_lanes(x[k], 64);
+    if (threads == 64) return;
+    const int waves = threads / 64, wv = threadIdx.x / 64;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) tab[turn][wv][k] = x[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float s = 0.f;
+        for (int i = 0; i < waves; ++i) s += tab[turn][i][k];
+        x[k] = s;
+    }
+}
+
+// `threads` threads hold a row, vector i of a thread at channel (i threads + thread) V.  With 64 the
+// workgroup's other waves hold other rows.
+template <typename TX, typename TY, int V, int NV>
+__global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
+    __shared__ float tab[2][16][1];
+    int turn = 0;
+    const int n = P.threads, th = threadIdx.x % n;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
+    if (row >= P.rows) return;  // a whole wave of a 64-thread row; a whole workgroup otherwise
+    const int C = static_cast<int>(P.C);
+    const float inv_c = 1.f / static_cast<float>(C);
+    const int64_t base = row * P.C;
+    float z[NV][V];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * n + th) * V;
+        if (c < C) {
+            load<V>(static_cast<const TY*>(P.y) + base + c, z[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) z[i][j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[0] += z[i][j];
+    }
+    if (P.post_w != nullptr) {
+        float mean = 0.f;
+        if (P.center) {
+            row_sums<1>(s, n, tab, turn);
+            mean = s[0] * inv_c;
+        }
+        s[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((i * n + th) * V >= C) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                z[i][j] -= mean;
+                s[0] = fmaf(z[i][j], z[i][j], s[0]);
+            }
+        }
+        row_sums<1>(s, n, tab, turn);
+        const float inv = 1.f / sqrtf(s[0] * inv_c + P.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c >= C) continue;
+            float w[V], b[V];
+            load<V>(P.post_w + c, w);
+            if (P.post_b != nullptr) load<V>(P.post_b + c, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) z[i][j] = z[i][j] * inv * w[j] + (P.post_b != nullptr ? b[j] : 0.f);
+        }
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * n + th) * V;
+        if (c >= C) continue;
+        float x[V], g[V], sc[V];
+        load<V>(static_cast<const TX*>(P.x) + base + c, x);
+        if (P.gate != nullptr) load<V>(static_cast<const TY*>(P.gate) + base + c, g);
+        if (P.scale != nullptr) load<V>(P.scale + c, sc);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a = 1.f, da;
+            if (P.gate != nullptr) activate(P.act, g[j], a, da);
+            if (P.scale != nullptr) a *= sc[j];
+            z[i][j] = fmaf(z[i][j], a, x[j]);
+            s[0] += z[i][j];
+        }
+        store<V>(static_cast<TX*>(P.x_out) + base + c, z[i]);
+    }
+    float mean = 0.f;
+    if (P.center) {
+        row_sums<1>(s, n, tab, turn);
+        mean = s[0] * inv_c;
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if ((i * n + th) * V >= C) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            z[i][j] -= mean;
+            s[0] = fmaf(z[i][j], z[i][j], s[0]);
+        }
+    }
+    row_sums<1>(s, n, tab, turn);
+    const float inv = 1.f / sqrtf(s[0] * inv_c + P.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * n + th) * V;
+        if (c >= C) continue;
+        float w[V], b[V];
+        load<V>(P.pre_w + c, w);
+        if (P.pre_b != nullptr) load<V>(P.pre_b + c, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[i][j] = z[i][j] * inv * w[j] + (P.pre_b != nullptr ? b[j] : 0.f);
+        store<V>(static_cast<TY*>(P.h) + base + c, z[i]);
+    }
+}
+
+// The rows of slot q (of `slots`): q, q + slots, ..  Partial sums [5][slots][C]: dpre_w, dpre_b, dpost_w,
+// dpost_b, dscale.
+template <typename TX, typename TY, int V, int NV>
+__global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs P) {
+    __shared__ float tab[2][16][2];
+    int turn = 0;
+    const int n = P.threads, th = threadIdx.x % n;
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
+    const int C = static_cast<int>(P.C);
+    const float inv_c = 1.f / static_cast<float>(C);
+    const bool post = P.post_w != nullptr, gated = P.gate != nullptr;
+    float acc[5][NV][V];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[k][i][j] = 0.f;
+    for (int64_t row = slot; row < P.rows; row += P.slots) {  // the same trip count for a row's threads
+        const int64_t base = row * P.C;
+        float x[NV][V], y[NV][V], d[NV][V];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c < C) {
+                load<V>(static_cast<const TX*>(P.x) + base + c, x[i]);
+                load<V>(static_cast<const TY*>(P.y) + base + c, y[i]);
+                load<V>(static_cast<const TY*>(P.gh) + base + c, d[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[i][j] = y[i][j] = d[i][j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[0] += x[i][j];
+                s[1] += y[i][j];
+            }
+        }
+        float mx = 0.f, my = 0.f;
+        if (P.center) {
+            row_sums<2>(s, n, tab, turn);
+            mx = s[0] * inv_c;
+            my = post ? s[1] * inv_c : 0.f;
+        }
+        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((i * n + th) * V >= C) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[i][j] -= mx;
+                s[0] = fmaf(x[i][j], x[i][j], s[0]);
+                y[i][j] -= my;
+                s[1] = fmaf(y[i][j], y[i][j], s[1]);
+            }
+        }
+        row_sums<2>(s, n, tab, turn);
+        const float ix = 1.f / sqrtf(s[0] * inv_c + P.eps);
+        const float iy = post ? 1.f / sqrtf(s[1] * inv_c + P.eps) : 1.f;
+        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c >= C) continue;
+            float w[V];
+            load<V>(P.pre_w + c, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                x[i][j] *= ix;
+                y[i][j] *= iy;
+                acc[0][i][j] = fmaf(d[i][j], x[i][j], acc[0][i][j]);
+                acc[1][i][j] += d[i][j];
+                d[i][j] *= w[j];
+                s[0] += d[i][j];
+                s[1] = fmaf(d[i][j], x[i][j], s[1]);
+            }
+        }
+        row_sums<2>(s, n, tab, turn);
+        const float m1 = P.center ? s[0] * inv_c : 0.f, m2 = s[1] * inv_c;
+        s[0] = s[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c >= C) continue;
+            float t[V], g[V], sc[V], w[V], b[V];
+            if (P.gx != nullptr) load<V>(static_cast<const TX*>(P.gx) + base + c, t);
+            if (gated) load<V>(static_cast<const TY*>(P.gate) + base + c, g);
+            if (P.scale != nullptr) load<V>(P.scale + c, sc);
+            if (post) load<V>(P.post_w + c, w);
+            if (P.post_b != nullptr) load<V>(P.post_b + c, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float dx = ix * (d[i][j] - m1 - x[i][j] * m2) + (P.gx != nullptr ? t[j] : 0.f);
+                x[i][j] = dx;
+                float z = y[i][j];
+                if (post) z = z * w[j] + (P.post_b != nullptr ? b[j] : 0.f);
+                float a = 1.f, da = 0.f;
+                if (gated) activate(P.act, g[j], a, da);
+                acc[4][i][j] = fmaf(dx, z * a, acc[4][i][j]);
+                const float ds = P.scale != nullptr ? dx * sc[j] : dx;
+                g[j] = ds * z * da;
+                const float dz = ds * a;
+                acc[2][i][j] = fmaf(dz, y[i][j], acc[2][i][j]);
+                acc[3][i][j] += dz;
+                d[i][j] = post ? dz * w[j] : dz;
+                s[0] += d[i][j];
+                s[1] = fmaf(d[i][j], y[i][j], s[1]);
+            }
+            store<V>(static_cast<TX*>(P.dx) + base + c, x[i]);
+            if (gated) store<V>(static_cast<TY*>(P.dgate) + base + c, g);
+        }
+        float p1 = 0.f, p2 = 0.f;
+        if (post) {
+            row_sums<2>(s, n, tab, turn);
+            p1 = P.center ? s[0] * inv_c : 0.f;
+            p2 = s[1] * inv_c;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c >= C) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[i][j] = iy * (d[i][j] - p1 - y[i][j] * p2);
+            store<V>(static_cast<TY*>(P.dy) + base + c, d[i]);
+        }
+    }
+    if (slot >= P.slots) return;
+    const bool want[5] = {true, P.pre_b != nullptr, post, P.post_b != nullptr, P.scale != nullptr};
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        if (!want[k]) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * n + th) * V;
+            if (c < C) store<V>(P.ws + (k * P.slots + slot) * P.C + c, acc[k][i]);
+        }
+    }
+}
+
+__global__ void norm_zero_kernel(float* p, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+    if (i < n) p[i] = 0.f;
+}
+
+int64_t pow2_at_least(int64_t x) {
+    int64_t p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+template <typename TY, typename TG, int V, int NV>
+hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
+    if (!bwd) {
+        const int64_t per = kBlock / a.lanes;
+        hipLaunchKernelGGL((head_norm_kernel<TY, TG, V, NV>), dim3(static_cast<unsigned>((a.rows * a.H + per - 1) / per)),
+                           dim3(kBlock), 0, stream, a);
+        return hipGetLastError();
+    }
+    const int64_t C = a.H * a.G;
+    const size_t lds = static_cast<size_t>(kBlock / a.lanes) * a.G * sizeof(float);
+    hipLaunchKernelGGL((head_norm_bwd_kernel<TY, TG, V, NV>), dim3(static_cast<unsigned>((a.H + a.hpb - 1) / a.hpb * a.chunks)),
+                       dim3(kBlock), lds, stream, a);
+    hipError_t e = hipGetLastError();
+    // one weight for all heads: the heads' sums are rows too
+    ReduceArgs r{a.shared ? a.chunks * a.H : a.chunks, a.shared ? a.G : C};
+    r.add(a.ws, a.dweight);
+    if (a.bias != nullptr) r.add(a.ws + a.chunks * C, a.dbias);
+    return e == hipSuccess ? launch_reduce(r, stream) : e;
+}
+
+template <typename TY, typename TG>
+hipError_t launch_head_v(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
+    if (!a.vec) return launch_head<TY, TG, 1, kScalarVecs>(a, bwd, stream);
+    return a.G <= 512 ? launch_head<TY, TG, 8, 1>(a, bwd, stream) : launch_head<TY, TG, 8, 2>(a, bwd, stream);
+}
+
+hipError_t launch_head_t(HeadNormArgs a, bool bwd, hipStream_t stream) {
+    a.lanes = a.vec ? static_cast<int>(pow2_at_least(a.G / 8 < 64 ? a.G / 8 : 64)) : 64;
+    const int slots = kBlock / a.lanes;
+    // heads side by side for at least 512 bytes a row of bf16, the workgroup's other slots over rows
+    a.hpb = 1;
+    while (a.hpb < slots && a.hpb < a.H && a.hpb * a.G < 256) a.hpb *= 2;
+    a.chunks = head_norm_chunks(a.rows);
+    if (a.y_bf16) return launch_head_v<uint16_t, uint16_t>(a, bwd, stream);
+    return a.bf16 ? launch_head_v<float, uint16_t>(a, bwd, stream) : launch_head_v<float, float>(a, bwd, stream);
+}
+
+template <typename TX, typename TY, int V, int NV>
+hipError_t launch_block(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
+    const int64_t block = a.threads == 64 ? 256 : a.threads, per = block / a.threads;
+    if (!bwd) {
+        hipLaunchKernelGGL((block_norm_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                           dim3(static_cast<unsigned>(block)), 0, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((block_norm_bwd_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.slots + per - 1) / per)),
+                       dim3(static_cast<unsigned>(block)), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    float* const out[5] = {a.dpre_w, a.pre_b ? a.dpre_b : nullptr, a.post_w ? a.dpost_w : nullptr,
+                           a.post_b ? a.dpost_b : nullptr, a.scale ? a.dscale : nullptr};
+    ReduceArgs r{a.slots, a.C};
+    for (int k = 0; k < 5; ++k)
+        if (out[k] != nullptr) r.add(a.ws + k * a.slots * a.C, out[k]);
+    return e == hipSuccess ? launch_reduce(r, stream) : e;
+}
+
+template <typename TX, typename TY>
+hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
+    a.slots = block_norm_slots(a.rows, a.C);
+    if (!a.vec) {
+        a.threads = 1024;
+        return launch_block<TX, TY, 1, 8>(a, bwd, stream);
+    }
+    a.threads = a.C <= 512 ? 64 : static_cast<int>(pow2_at_least(a.C / 8));
+    return launch_block<TX, TY, 8, 1>(a, bwd, stream);
+}
+
+hipError_t launch_block_t(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
+    if (a.x_bf16) return launch_block_v<uint16_t, uint16_t>(a, bwd, stream);
+    return a.bf16 ? launch_block_v<float, uint16_t>(a, bwd, stream) : launch_block_v<float, float>(a, bwd, stream);
+}
+
+}  // namespace
+
+int64_t head_norm_chunks(int64_t rows) {
+    const int64_t n = (rows + 63) / 64;
+    return n < 128 ? n : 128;
+}
+
+int64_t block_norm_slots(int64_t rows, int64_t C) {
+    // as many rows of partial sums as fill the card with two workgroups a compute unit
+    const int64_t most = C <= 512 ? 1024 : 512;
+    return rows < most ? rows : most;
+}
+
+hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream) {
+    if (p == nullptr || n <= 0) return hipSuccess;
+    hipLaunchKernelGGL(norm_zero_kernel, dim3(static_cast<unsigned>((n + kBlock - 1) / kBlock)), dim3(kBlock), 0, stream, p, n);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream) { return launch_head_t(a, false, stream); }
+hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream) { return launch_head_t(a, true, stream); }
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream) { return launch_block_t(a, false, stream); }
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t stream) { return launch_block_t(a, true, stream); }
+
+}  // namespace wkv

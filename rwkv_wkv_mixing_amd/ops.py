@@ -827,3 +827,180 @@ class DeltaFunction(torch.autograd.Function):
 def delta_rule(w, beta, r, k, v, state_in=None, lengths=None):
     """Differentiable gated delta rule: (o, state after each row's last token) (see delta_forward)."""
     return DeltaFunction.apply(w, beta, r, k, v, state_in, lengths)
+
+
+_ACT = {"none": L.WKV_ACT_NONE, "sigmoid": L.WKV_ACT_SIGMOID, "silu": L.WKV_ACT_SILU}
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _act(act):
+    if act not in _ACT:
+        raise ValueError(f"act is {act!r}, expected one of {', '.join(_ACT)}")
+    return _ACT[act]
+
+
+def _narrow(name, t, wide_name, wide):
+    """t's dtype: float32 or bfloat16, and no wider than the tensor it goes with."""
+    if wide == torch.bfloat16 and t.dtype == torch.float32:
+        raise TypeError(f"{name} is float32 and {wide_name} is bfloat16: {wide_name} may be the wider one only")
+    return t.dtype
+
+
+def _head_norm_inputs(y, weight, bias, gate, heads):
+    _need(y, "y", _FLOATS)
+    dev = y.device
+    C = y.shape[-1] if y.dim() else 0
+    if heads < 1 or C % heads or not 1 <= C // heads <= 1024:
+        raise ValueError(f"y has {C} channels for {heads} heads: heads of 1 to 1024 channels are needed")
+    G = C // heads
+    _need(weight, "weight", torch.float32, None, dev)
+    if tuple(weight.shape) not in ((C,), (G,)):
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({C},) or ({G},)")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, weight.shape, dev)
+    dt = y.dtype
+    if gate is not None:
+        _need(gate, "gate", _FLOATS, y.shape, dev)
+        dt = _narrow("gate", gate, "y", y.dtype)
+    return dev, y.numel() // C, G, dt, weight.shape[0] == G and heads > 1
+
+
+def head_norm(y, weight, bias=None, gate=None, *, heads, act="silu", center=False, eps=1e-5, out=None, bind=False):
+    """out = act(gate) * (norm(y) * weight + bias), the norm over each of the last axis's heads: root
+    mean square, or with center the mean taken off first.  y [..., C] float32 or bfloat16; gate like
+    y or narrower, or None (no factor); act "none", "sigmoid" or "silu"; weight, bias [C] or, one for
+    all heads, [C / heads], float32.  out has gate's dtype (y's without a gate)."""
+    dev, rows, G, dt, shared = _head_norm_inputs(y, weight, bias, gate, heads)
+    if out is None:
+        out = torch.empty(y.shape, dtype=dt, device=dev)
+    else:
+        _need(out, "out", dt if gate is not None else _FLOATS, y.shape, dev)
+        dt = _narrow("out", out, "y", y.dtype)
+    flags = (L.WKV_NORM_CENTER if center else 0) | (L.WKV_NORM_SHARED if shared else 0)
+    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _p(y), _p(weight), _p(bias), _p(gate),
+            _p(out), _stream(dev))
+    return _launch_on(dev, bind, "wkv_head_norm", L.lib().wkv_head_norm, args, out, locals())
+
+
+def head_norm_backward(y, gout, weight, bias=None, gate=None, *, heads, act="silu", center=False, eps=1e-5,
+                       workspace=None, bind=False):
+    """Gradients of sum <gout, head_norm(y, weight, bias, gate, ...)>: (dy, dweight, dbias, dgate), each in
+    its input's dtype, None for one that is None.  gout has the forward output's dtype."""
+    dev, rows, G, dt, shared = _head_norm_inputs(y, weight, bias, gate, heads)
+    _need(gout, "gout", dt if gate is not None else _FLOATS, y.shape, dev)
+    dt = _narrow("gout", gout, "y", y.dtype)
+    dy, dweight = torch.empty_like(y), torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dgate = None if gate is None else torch.empty_like(gate)
+    lib = L.lib()
+    workspace = _scratch(workspace, int(lib.wkv_head_norm_backward_workspace_bytes(rows, heads, G)), dev)
+    flags = (L.WKV_NORM_CENTER if center else 0) | (L.WKV_NORM_SHARED if shared else 0)
+    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _p(y), _p(weight), _p(bias), _p(gate),
+            _p(gout), _p(dy), _p(dweight), _p(dbias), _p(dgate), _p(workspace), _bytes_of(workspace), _stream(dev))
+    return _launch_on(dev, bind, "wkv_head_norm_backward", lib.wkv_head_norm_backward, args,
+                      (dy, dweight, dbias, dgate), locals())
+
+
+class HeadNormFunction(torch.autograd.Function):
+    """Autograd wrapper of head_norm: saves its inputs; the statistics are computed again."""
+
+    @staticmethod
+    def forward(ctx, y, weight, bias, gate, heads, act, center, eps):
+        ctx.save_for_backward(y, weight, bias, gate)
+        ctx.kw = dict(heads=heads, act=act, center=center, eps=eps)
+        return head_norm(y, weight, bias, gate, **ctx.kw)
+
+    @staticmethod
+    def backward(ctx, gout):
+        y, weight, bias, gate = ctx.saved_tensors
+        return *head_norm_backward(y, gout.contiguous(), weight, bias, gate, **ctx.kw), None, None, None, None
+
+
+def head_norm_gated(y, weight, bias=None, gate=None, *, heads, act="silu", center=False, eps=1e-5):
+    """Differentiable head_norm (see HeadNormFunction)."""
+    return HeadNormFunction.apply(y, weight, bias, gate, heads, act, center, eps)
+
+
+def _block_norm_inputs(x, xname, y, pre_w, pre_b, gate, post_w, post_b, scale):
+    _need(x, xname, _FLOATS)
+    dev = x.device
+    C = x.shape[-1] if x.dim() else 0
+    if not 1 <= C <= 8192:
+        raise ValueError(f"{xname} has {C} channels: 1 to 8192 are needed")
+    _need(y, "y", _FLOATS, x.shape, dev)
+    _narrow("y", y, xname, x.dtype)
+    if gate is not None:
+        _need(gate, "gate", y.dtype, x.shape, dev)
+    _need(pre_w, "pre_w", torch.float32, (C,), dev)
+    for t, n in ((pre_b, "pre_b"), (post_w, "post_w"), (post_b, "post_b"), (scale, "scale")):
+        if t is not None:
+            _need(t, n, torch.float32, (C,), dev)
+    if post_b is not None and post_w is None:
+        raise ValueError("post_b needs post_w")
+    return dev, x.numel() // C, C
+
+
+def block_norm(x, y, pre_w, pre_b=None, *, gate=None, act="sigmoid", post_w=None, post_b=None, scale=None, center=True,
+               eps=1e-5, x_out=None, h=None, bind=False):
+    """(x_out, h) between two blocks: z = act(gate) * (norm(y) * post_w + post_b), x_out = x + scale * z,
+    h = norm(x_out) * pre_w + pre_b, over the last axis (up to 8192 channels).  x the residual stream
+    (float32 or bfloat16, x_out too; x_out may be x); y, gate, h in y's dtype, no wider than x's;
+    post_w None: no norm of y; gate None: no factor; the weights [C] float32.  Both norms take the
+    mean off (center) or are root mean square.  act "none", "sigmoid" or "silu"."""
+    dev, rows, C = _block_norm_inputs(x, "x", y, pre_w, pre_b, gate, post_w, post_b, scale)
+    x_out = torch.empty_like(x) if x_out is None else x_out
+    h = torch.empty_like(y) if h is None else h
+    _need(x_out, "x_out", x.dtype, x.shape, dev)
+    _need(h, "h", y.dtype, x.shape, dev)
+    args = (rows, C, _DT[x.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _p(x), _p(y),
+            _p(gate), _p(post_w), _p(post_b), _p(scale), _p(pre_w), _p(pre_b), _p(x_out), _p(h), _stream(dev))
+    return _launch_on(dev, bind, "wkv_block_norm", L.lib().wkv_block_norm, args, (x_out, h), locals())
+
+
+def block_norm_backward(x_out, y, gh, pre_w, pre_b=None, *, gx=None, gate=None, act="sigmoid", post_w=None, post_b=None,
+                        scale=None, center=True, eps=1e-5, workspace=None, bind=False):
+    """Gradients of sum <gx, x_out> + <gh, h> for (x_out, h) = block_norm(x, y, ...), from x_out as it
+    returned it: a dict of dx, dy, dgate, dpre_w, dpre_b, dpost_w, dpost_b, dscale, each in its input's
+    dtype, None for one that is None.  gx None: no gradient from later in the residual stream."""
+    dev, rows, C = _block_norm_inputs(x_out, "x_out", y, pre_w, pre_b, gate, post_w, post_b, scale)
+    _need(gh, "gh", y.dtype, y.shape, dev)
+    if gx is not None:
+        _need(gx, "gx", x_out.dtype, y.shape, dev)
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    g = dict(dx=like(x_out), dy=like(y), dgate=like(gate), dpre_w=like(pre_w), dpre_b=like(pre_b), dpost_w=like(post_w),
+             dpost_b=like(post_b), dscale=like(scale))
+    lib = L.lib()
+    workspace = _scratch(workspace, int(lib.wkv_block_norm_backward_workspace_bytes(rows, C)), dev)
+    args = (rows, C, _DT[x_out.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _p(x_out), _p(y),
+            _p(gate), _p(post_w), _p(post_b), _p(scale), _p(pre_w), _p(pre_b), _p(gx), _p(gh), _p(g["dx"]), _p(g["dy"]),
+            _p(g["dgate"]), _p(g["dpost_w"]), _p(g["dpost_b"]), _p(g["dscale"]), _p(g["dpre_w"]), _p(g["dpre_b"]),
+            _p(workspace), _bytes_of(workspace), _stream(dev))
+    keep = (x_out, y, gh, pre_w, pre_b, gx, gate, post_w, post_b, scale, workspace, tuple(g.values()))
+    return _launch_on(dev, bind, "wkv_block_norm_backward", lib.wkv_block_norm_backward, args, g, dict(keep=keep))
+
+
+class BlockNormFunction(torch.autograd.Function):
+    """Autograd wrapper of block_norm: saves x_out, y, gate and the weights."""
+
+    @staticmethod
+    def forward(ctx, x, y, pre_w, pre_b, gate, post_w, post_b, scale, act, center, eps):
+        ctx.kw = dict(act=act, center=center, eps=eps)
+        x_out, h = block_norm(x, y, pre_w, pre_b, gate=gate, post_w=post_w, post_b=post_b, scale=scale, **ctx.kw)
+        ctx.save_for_backward(x_out, y, pre_w, pre_b, gate, post_w, post_b, scale)
+        ctx.set_materialize_grads(False)
+        return x_out, h
+
+    @staticmethod
+    def backward(ctx, gx, gh):
+        x_out, y, pre_w, pre_b, gate, post_w, post_b, scale = ctx.saved_tensors
+        g = block_norm_backward(x_out, y, torch.zeros_like(y) if gh is None else gh.contiguous(), pre_w, pre_b,
+                                gx=None if gx is None else gx.contiguous(), gate=gate, post_w=post_w, post_b=post_b,
+                                scale=scale, **ctx.kw)
+        return (g["dx"], g["dy"], g["dpre_w"], g["dpre_b"], g["dgate"], g["dpost_w"], g["dpost_b"], g["dscale"],
+                None, None, None)
+
+
+def block_join(x, y, pre_w, pre_b=None, *, gate=None, act="sigmoid", post_w=None, post_b=None, scale=None, center=True,
+               eps=1e-5):
+    """Differentiable block_norm (see BlockNormFunction): (x_out, h)."""
+    return BlockNormFunction.apply(x, y, pre_w, pre_b, gate, post_w, post_b, scale, act, center, eps)
