@@ -39,12 +39,16 @@ typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 64;   // tokens staged at a time, and between saved states
 constexpr int kSub = 16;    // tokens of one triangular system
 constexpr int kWaves = 4;   // per workgroup: one per sub-block of a tile, 16 value columns each
 constexpr int kCols = 16 * kWaves;
 constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
+template <typename T, int N>
+constexpr int kOcc = sizeof(T) * N > 256 ? 1 : 2;  // workgroups a compute unit has the LDS for
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -88,6 +92,136 @@ __device__ __forceinline__ f4 mma16(f4 a, f4 b, f4 c) {
 // consecutive rows start in different banks.
 template <typename T, int N>
 constexpr int kRow = N + 16 / static_cast<int>(sizeof(T));
+
+// ---- products with bf16 inputs -------------------------------------------------------------------
+// A bf16 input is exact as an operand of the bf16 products, which run 16 times as fast as the float32
+// ones.  A float32 factor x is given as three bf16 terms, x = hi + mid + lo, each the upper half of
+// what the ones before leave: 24 bits in all, so the split is exact and the products summed in float32
+// are those of float32 operands.  Where a result is rounded to bf16 and goes nowhere else, hi + mid
+// (16 bits, off by at most 2^-16) is enough: rounding moves it by up to 2^-8.
+struct Terms {
+    u32x2 hi, mid, lo;
+};
+
+__device__ __forceinline__ uint32_t uppers(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+__device__ __forceinline__ Terms split(f4 x) {
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = __float_as_uint(x[i]);
+        const float rest = x[i] - __uint_as_float(h[i] & 0xffff0000u);
+        m[i] = __float_as_uint(rest);
+        l[i] = __float_as_uint(rest - __uint_as_float(m[i] & 0xffff0000u));
+    }
+    return Terms{{uppers(h[0], h[1]), uppers(h[2], h[3])},
+                 {uppers(m[0], m[1]), uppers(m[2], m[3])},
+                 {uppers(l[0], l[1]), uppers(l[2], l[3])}};
+}
+
+__device__ __forceinline__ bf8 pair(u32x2 a, u32x2 b) { return __builtin_bit_cast(bf8, u32x4{a[0], a[1], b[0], b[1]}); }
+__device__ __forceinline__ bf8 raw8(const uint16_t* p) { return __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4*>(p)); }
+
+// 32 contracted indices, eight a lane; which of them a lane holds is the same for A and B.  Sums of 16
+// indices take it too, one half filled twice or with zeros: a 16-index product that adds to what a
+// 32-index one has just written (or the other way round) has been measured to lose part of it.
+__device__ __forceinline__ f4 mfma32(bf8 a, bf8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+// Row of the state that register r of group g holds in accumulator c: a lane's registers of the
+// accumulators 2 m and 2 m + 1 are eight consecutive rows, so that one 16-byte read of a token's k gives
+// the matching left operand.
+__device__ __forceinline__ constexpr int state_row(int c, int g, int r) { return 32 * (c >> 1) + 8 * g + 4 * (c & 1) + r; }
+
+// acc[i][j] = sum over the N channels of a row i of A and a row j of B (rows l16 of each), both staged
+template <int N>
+__device__ __forceinline__ f4 rows_product(const uint16_t* a, const uint16_t* b, int g) {
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < N / 32; ++m) acc = mfma32(raw8(a + 32 * m + 8 * g), raw8(b + 32 * m + 8 * g), acc);
+    return acc;
+}
+template <int N>
+__device__ __forceinline__ f4 rows_product(const float* a, const float* b, int g) {
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) acc = mma16(load4(a + 16 * c + 4 * g), load4(b + 16 * c + 4 * g), acc);
+    return acc;
+}
+
+// The state's 16 columns as a right operand, for one block.
+template <typename T, int N>
+struct StateOperand;
+
+template <int N>
+struct StateOperand<float, N> {
+    f4 s[N / 16];
+    __device__ __forceinline__ explicit StateOperand(const f4 (&S)[N / 16]) {
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) s[c] = S[c];
+    }
+    // rows (row l16 at `row`) times the state
+    template <bool kRounded>
+    __device__ __forceinline__ f4 times(const float* row, int g) const {
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) acc = mma16(load4(row + state_row(c, g, 0)), s[c], acc);
+        return acc;
+    }
+};
+
+template <int N>
+struct StateOperand<uint16_t, N> {
+    bf8 hi[N / 32], mid[N / 32], lo[N / 32];
+    __device__ __forceinline__ explicit StateOperand(const f4 (&S)[N / 16]) {
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) {
+            const Terms a = split(S[2 * m]), b = split(S[2 * m + 1]);
+            hi[m] = pair(a.hi, b.hi);
+            mid[m] = pair(a.mid, b.mid);
+            lo[m] = pair(a.lo, b.lo);
+        }
+    }
+    // kRounded: the result is rounded to bf16 and used for nothing else
+    template <bool kRounded>
+    __device__ __forceinline__ f4 times(const uint16_t* row, int g) const {
+        f4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent products
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) {
+            const bf8 a = raw8(row + 32 * m + 8 * g);
+            acc2 = mfma32(a, mid[m], acc2);
+            if constexpr (!kRounded) acc2 = mfma32(a, lo[m], acc2);
+            acc = mfma32(a, hi[m], acc);
+        }
+        return acc + acc2;
+    }
+};
+
+// S += X^T u over a block's 16 tokens: X rows tb .. tb + 15 of a staged array, u four tokens a lane.
+template <int N>
+__device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const float (*X)[kRow<float, N>], int tb, f4 u, int l16, int g) {
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+        f4 a;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[q] = X[tb + 4 * g + q][state_row(c, l16 >> 2, l16 & 3)];
+        S[c] = mma16(a, u, S[c]);
+    }
+}
+// bf16: one transposing LDS read gives a lane its four tokens of one channel (in each group of 16 lanes,
+// lane 4 e + p reads four channels of token e, and lane j receives element j % 4 of lane 4 e + j / 4's
+// read for e = 0 .. 3); hi and mid of u share one 32-index product over the same tokens twice.
+template <int N>
+__device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const uint16_t (*X)[kRow<uint16_t, N>], int tb, f4 u, int l16, int g) {
+    const Terms t = split(u);
+    const bf8 b = pair(t.hi, t.mid), b2 = pair(t.lo, u32x2{0, 0});
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+        const uint16_t* at = &X[tb + 4 * g + (l16 >> 2)][state_row(c, l16 & 3, 0)];
+        const s4 raw = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at);
+        const u32x2 a = __builtin_bit_cast(u32x2, raw);
+        S[c] = mfma32(pair(a, a), b2, S[c]);
+        S[c] = mfma32(pair(a, a), b, S[c]);
+    }
+}
 
 // Rows t0 .. t0 + 63 of a [rows, stride] array, W columns from its base, on their way to LDS: held in
 // registers between fetch and put, so that the next tile's loads overlap this tile's arithmetic.
@@ -137,13 +271,9 @@ struct Blocks {
 template <typename T, int N>
 __device__ __forceinline__ void prepare_block(int s, int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>],
                                               Blocks& B) {
-    f4 kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < N / 16; ++c) {
-        const f4 a = load4(&K[kSub * s + l16][16 * c + 4 * g]);
-        kk = mma16(a, a, kk);
-        rk = mma16(load4(&R[kSub * s + l16][16 * c + 4 * g]), a, rk);
-    }
+    asm volatile("" : "+v"(l16), "+v"(g));  // else the comparisons below are kept in registers from tile to tile
+    const f4 kk = rows_product<N>(K[kSub * s + l16], K[kSub * s + l16], g);
+    const f4 rk = rows_product<N>(R[kSub * s + l16], K[kSub * s + l16], g);
     float gap[4] = {0.f, 0.f, 0.f, 0.f};  // sum of w over j < l <= i
     float run = 0.f, pre = 0.f, suf = 0.f;
 #pragma unroll
@@ -203,7 +333,7 @@ struct FwdShared {
 // the tile, each wave prepares one of its four blocks, then each wave takes its 16 columns through the
 // blocks one after the other with no barrier between them.
 template <typename T, int N>
-__global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) {
+__global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(DeltaArgs P) {
     __shared__ FwdShared<T, N> sm;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -229,7 +359,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) 
     for (int c = 0; c < N / 16; ++c)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            S[c][q] = P.s_in != nullptr ? P.s_in[(bh * N + 16 * c + 4 * g + q) * N + scol] : 0.f;
+            S[c][q] = P.s_in != nullptr ? P.s_in[(bh * N + state_row(c, g, q)) * N + scol] : 0.f;
 
     Staged<T, N> fk, fr;
     Staged<T, kCols> fv;
@@ -255,19 +385,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) 
 #pragma unroll
             for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) st[(16 * c + 4 * g + q) * N] = S[c][q];
+                for (int q = 0; q < 4; ++q) st[state_row(c, g, q) * N] = S[c][q];
         }
         __syncthreads();
 #pragma unroll 1
         for (int s = 0; s < kTile / kSub; ++s) {
             const int tb = kSub * s;
             if (t0 + tb >= P.T) break;
-            f4 kS = {0.f, 0.f, 0.f, 0.f}, rS = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c) {
-                kS = mma16(load4(&sm.k[tb + l16][16 * c + 4 * g]), S[c], kS);
-                rS = mma16(load4(&sm.r[tb + l16][16 * c + 4 * g]), S[c], rS);
-            }
+            const StateOperand<T, N> op(S);
+            const f4 kS = op.template times<false>(sm.k[tb + l16], g);
+            const f4 rS = op.template times<true>(sm.r[tb + l16], g);
             const f4 since = load4(&sm.blk.since[tb + 4 * g]);
             const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
             f4 e0, out;
@@ -281,12 +408,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) 
             const f4 u = put * e;
             const float total = sm.blk.since[tb + kSub - 1];
 #pragma unroll
-            for (int c = 0; c < N / 16; ++c) {
-                f4 a;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) a[q] = widen(sm.k[tb + 4 * g + q][16 * c + l16]);
-                S[c] = mma16(a, u, S[c] * total);
-            }
+            for (int c = 0; c < N / 16; ++c) S[c] *= total;
+            add_outer<N>(S, sm.k, tb, u, l16, g);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t t = t0 + tb + 4 * g + q;
@@ -303,7 +426,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_fwd_kernel(DeltaArgs P) 
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) P.s_out[(bh * N + 16 * c + 4 * g + q) * N + scol] = S[c][q];
+            for (int q = 0; q < 4; ++q) P.s_out[(bh * N + state_row(c, g, q)) * N + scol] = S[c][q];
     }
 }
 
@@ -399,7 +522,7 @@ struct AdjShared {
 };
 
 template <typename T, int N>
-__global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdArgs P) {
+__global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kernel(DeltaBwdArgs P) {
     __shared__ AdjShared<T, N> sm;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -425,7 +548,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdA
     for (int c = 0; c < N / 16; ++c)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            G[c][q] = P.ds_out != nullptr ? P.ds_out[(bh * N + 16 * c + 4 * g + q) * N + scol] : 0.f;
+            G[c][q] = P.ds_out != nullptr ? P.ds_out[(bh * N + state_row(c, g, q)) * N + scol] : 0.f;
 
     const int64_t live = (len + kTile - 1) / kTile;  // tiles with a token of this row
     for (int64_t t = live * kTile + threadIdx.x / 16; t < P.T; t += 16)
@@ -455,14 +578,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdA
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) gt[(16 * c + 4 * g + q) * N] = G[c][q];
+            for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N] = G[c][q];
         __syncthreads();
 #pragma unroll 1
         for (int s = kTile / kSub - 1; s >= 0; --s) {
             const int tb = kSub * s;
-            f4 kG = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c) kG = mma16(load4(&sm.k[tb + l16][16 * c + 4 * g]), G[c], kG);
+            const f4 kG = StateOperand<T, N>(G).template times<false>(sm.k[tb + l16], g);
             const f4 since = load4(&sm.blk.since[tb + 4 * g]);
             const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
             f4 d, att, inv;
@@ -477,15 +598,9 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdA
             const f4 gr = since * d, gk = -since * lam;
             const float total = sm.blk.since[tb + kSub - 1];
 #pragma unroll
-            for (int c = 0; c < N / 16; ++c) {
-                f4 a, a2;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    a[q] = widen(sm.r[tb + 4 * g + q][16 * c + l16]);
-                    a2[q] = widen(sm.k[tb + 4 * g + q][16 * c + l16]);
-                }
-                G[c] = mma16(a2, gk, mma16(a, gr, G[c] * total));
-            }
+            for (int c = 0; c < N / 16; ++c) G[c] *= total;
+            add_outer<N>(G, sm.r, tb, gr, l16, g);
+            add_outer<N>(G, sm.k, tb, gk, l16, g);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t t = t0 + tb + 4 * g + q;
@@ -499,7 +614,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) delta_adjoint_kernel(DeltaBwdA
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) P.ds_in[(bh * N + 16 * c + 4 * g + q) * N + scol] = G[c][q];
+            for (int q = 0; q < 4; ++q) P.ds_in[(bh * N + state_row(c, g, q)) * N + scol] = G[c][q];
     }
 }
 
