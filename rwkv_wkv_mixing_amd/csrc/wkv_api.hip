@@ -824,7 +824,9 @@ extern "C" {
 size_t wkv_head_norm_backward_workspace_bytes(int64_t rows, int64_t H, int64_t G) {
     int64_t n;
     if (head_norm_check(rows, H, G, &n) != WKV_OK) return 0;
-    return static_cast<size_t>(wkv::head_norm_chunks(rows)) * static_cast<size_t>(H * G) * 2 * sizeof(float);
+    if (n == 0) return 0;
+    const int64_t own = wkv::head_norm_chunks(rows, H * G) * H * G, shared = wkv::head_norm_chunks(rows * H, G) * G;
+    return static_cast<size_t>(own > shared ? own : shared) * 2 * sizeof(float);
 }
 
 wkv_status_t wkv_head_norm(int64_t rows, int64_t H, int64_t G, int y_dtype, int dtype, int flags, int act, float eps,
@@ -881,7 +883,7 @@ wkv_status_t wkv_head_norm_backward(int64_t rows, int64_t H, int64_t G, int y_dt
 
 size_t wkv_block_norm_backward_workspace_bytes(int64_t rows, int64_t C) {
     int64_t n;
-    if (block_norm_check(rows, C, &n) != WKV_OK) return 0;
+    if (block_norm_check(rows, C, &n) != WKV_OK || n == 0) return 0;
     return static_cast<size_t>(wkv::block_norm_slots(rows, C)) * static_cast<size_t>(C) * 5 * sizeof(float);
 }
 

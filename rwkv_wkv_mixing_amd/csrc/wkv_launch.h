@@ -304,7 +304,7 @@ struct HeadNormArgs {
     void* dgate = nullptr;
     float* dweight = nullptr;
     float* dbias = nullptr;
-    float* ws = nullptr;      // 2 head_norm_chunks(rows) H G floats
+    float* ws = nullptr;      // 2 head_norm_chunks(rows, H G) H G floats (rows H and G when shared)
     int lanes = 0, hpb = 0;   // lanes a head, heads a workgroup (set by the launch)
     int64_t chunks = 0;
 };
@@ -347,7 +347,7 @@ hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream);
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t stream);
 hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream);
-int64_t head_norm_chunks(int64_t rows);
+int64_t head_norm_chunks(int64_t rows, int64_t C);
 int64_t block_norm_slots(int64_t rows, int64_t C);
 
 // decode step (wkv_step.hip)

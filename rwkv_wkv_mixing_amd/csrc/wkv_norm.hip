@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "wkv_lanes.h"
 #include "wkv_launch.h"
 
 namespace wkv {
@@ -81,6 +82,36 @@ __device__ __forceinline__ void store(float* p, const float (&f)[V]) {
     }
 }
 
+// V consecutive elements as they are in memory: loads issued long before their use.
+template <typename T, int V>
+struct Raw {
+    static constexpr int kWords = V == 8 ? V * static_cast<int>(sizeof(T)) / 16 : 1;
+    u4 w[V == 8 ? kWords : 1];
+    T one;
+    __device__ __forceinline__ void fetch(const T* p) {
+        if constexpr (V == 8) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const u4*>(p)[i];
+        } else {
+            one = *p;
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+        if constexpr (V == 1) {
+            f[0] = widen(one);
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[0][i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[0][i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i / 4][i % 4]);
+        }
+    }
+};
+
 // act(g) and its derivative.  exp overflows to inf for g below -88, where both sigmoids are 0.
 __device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
     if (act == kActNone) {
@@ -88,7 +119,7 @@ __device__ __forceinline__ void activate(int act, float g, float& a, float& da) 
         da = 1.f;
         return;
     }
-    const float s = 1.f / (1.f + __expf(-g));
+    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-g));  // within 1 ulp of the quotient
     if (act == kActSigmoid) {
         a = s;
         da = s * (1.f - s);
@@ -98,11 +129,9 @@ __device__ __forceinline__ void activate(int act, float g, float& a, float& da) 
     }
 }
 
-__device__ __forceinline__ float sum_lanes(float x, int lanes) {
-    for (int m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m, 64);
-    return x;
-}
-
+#ifndef WKV_BN_NV2
+#define WKV_BN_NV2 1024
+#endif
 constexpr int kBlock = 256;
 constexpr int kScalarVecs = 16;  // elements a lane of the element-by-element path: G up to 1024
 
@@ -112,7 +141,7 @@ __global__ void __launch_bounds__(kBlock) head_norm_kernel(HeadNormArgs P) {
     const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1);
     const int64_t id = static_cast<int64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
     const bool live = id < P.rows * P.H;
-    const int64_t h = id % P.H, base = id * P.G, wb = P.shared ? 0 : h * P.G;
+    const int64_t h = id % P.H, base = id * P.G, wb = h * P.G;
     const int G = static_cast<int>(P.G);
     const float inv_g = 1.f / static_cast<float>(G);
     float y[NV][V];
@@ -178,7 +207,7 @@ __global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
     const int hs = slot % hpb, rs = slot / hpb;
     const int64_t h = hb * hpb + hs;
     const int G = static_cast<int>(P.G);
-    const int64_t C = P.H * P.G, wb = P.shared ? 0 : h * P.G;
+    const int64_t C = P.H * P.G, wb = h * P.G;
     const float inv_g = 1.f / static_cast<float>(G);
     float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
@@ -349,17 +378,24 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
     const int C = static_cast<int>(P.C);
     const float inv_c = 1.f / static_cast<float>(C);
     const int64_t base = row * P.C;
+    // every input is on its way before the first sum waits for its own
+    Raw<TY, V> ry[NV], rg[NV];
+    Raw<TX, V> rx[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * n + th) * V;
+        if (c >= C) continue;
+        ry[i].fetch(static_cast<const TY*>(P.y) + base + c);
+        rx[i].fetch(static_cast<const TX*>(P.x) + base + c);
+        if (P.gate != nullptr) rg[i].fetch(static_cast<const TY*>(P.gate) + base + c);
+    }
     float z[NV][V];
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * n + th) * V;
-        if (c < C) {
-            load<V>(static_cast<const TY*>(P.y) + base + c, z[i]);
-        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) z[i][j] = 0.f;
-        }
+        for (int j = 0; j < V; ++j) z[i][j] = 0.f;
+        if ((i * n + th) * V < C) ry[i].get(z[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) s[0] += z[i][j];
     }
@@ -398,8 +434,8 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
         const int c = (i * n + th) * V;
         if (c >= C) continue;
         float x[V], g[V], sc[V];
-        load<V>(static_cast<const TX*>(P.x) + base + c, x);
-        if (P.gate != nullptr) load<V>(static_cast<const TY*>(P.gate) + base + c, g);
+        rx[i].get(x);
+        if (P.gate != nullptr) rg[i].get(g);
         if (P.scale != nullptr) load<V>(P.scale + c, sc);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -443,9 +479,13 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
 
 // The rows of slot q (of `slots`): q, q + slots, ..  Partial sums [5][slots][C]: dpre_w, dpre_b, dpost_w,
 // dpost_b, dscale.
-template <typename TX, typename TY, int V, int NV>
-__global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs P) {
+//
+// A row's inputs are fetched while the row before it is worked on (NV == 1; the channels' five sums and
+// four weights leave room for that in 256 registers, not in 128: a workgroup has at most 512 threads).
+template <typename TX, typename TY, int V, int NV, int Threads>
+__global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P) {
     __shared__ float tab[2][16][2];
+    constexpr bool kAhead = NV == 1;
     int turn = 0;
     const int n = P.threads, th = threadIdx.x % n;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
@@ -459,26 +499,70 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs P) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[k][i][j] = 0.f;
-    for (int64_t row = slot; row < P.rows; row += P.slots) {  // the same trip count for a row's threads
-        const int64_t base = row * P.C;
-        float x[NV][V], y[NV][V], d[NV][V];
-        float s[2] = {0.f, 0.f};
+    struct Weights {
+        float pre[V], post[V], bias[V], scale[V];
+    };
+    const auto weights = [&](int c, Weights& w) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w.post[j] = w.scale[j] = 1.f;
+            w.bias[j] = 0.f;
+        }
+        load<V>(P.pre_w + c, w.pre);
+        if (post) load<V>(P.post_w + c, w.post);
+        if (P.post_b != nullptr) load<V>(P.post_b + c, w.bias);
+        if (P.scale != nullptr) load<V>(P.scale + c, w.scale);
+    };
+    Raw<TX, V> rx[NV], rt[kAhead ? NV : 1];
+    Raw<TY, V> ry[NV], rd[NV], rg[kAhead ? NV : 1];
+    const auto fetch_late = [&](int64_t at, int i) {  // needed after the statistics only
+        if (gated) rg[i].fetch(static_cast<const TY*>(P.gate) + at);
+        if (P.gx != nullptr) rt[i].fetch(static_cast<const TX*>(P.gx) + at);
+    };
+    const auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * n + th) * V;
-            if (c < C) {
-                load<V>(static_cast<const TX*>(P.x) + base + c, x[i]);
-                load<V>(static_cast<const TY*>(P.y) + base + c, y[i]);
-                load<V>(static_cast<const TY*>(P.gh) + base + c, d[i]);
-            } else {
+            if (c >= C) continue;
+            const int64_t at = row * P.C + c;
+            rx[i].fetch(static_cast<const TX*>(P.x) + at);
+            ry[i].fetch(static_cast<const TY*>(P.y) + at);
+            rd[i].fetch(static_cast<const TY*>(P.gh) + at);
+            if constexpr (kAhead) fetch_late(at, i);
+        }
+    };
+    Weights kept;
+    if (kAhead && th * V < C) weights(th * V, kept);
+    if (kAhead && slot < P.rows) fetch(slot);
+    for (int64_t row = slot; row < P.rows; row += P.slots) {  // the same trip count for a row's threads
+        const int64_t base = row * P.C;
+        if constexpr (!kAhead) fetch(row);
+        float x[NV][V], y[NV][V], d[NV][V], g[V], t[V];
+        const auto late = [&](int i) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) x[i][j] = y[i][j] = d[i][j] = 0.f;
+            for (int j = 0; j < V; ++j) g[j] = t[j] = 0.f;
+            if (gated) rg[i].get(g);
+            if (P.gx != nullptr) rt[i].get(t);
+        };
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[i][j] = y[i][j] = d[i][j] = 0.f;
+            if ((i * n + th) * V < C) {
+                rx[i].get(x[i]);
+                ry[i].get(y[i]);
+                rd[i].get(d[i]);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 s[0] += x[i][j];
                 s[1] += y[i][j];
             }
+        }
+        if constexpr (kAhead) {
+            late(0);
+            if (row + P.slots < P.rows) fetch(row + P.slots);
         }
         float mx = 0.f, my = 0.f;
         if (P.center) {
@@ -507,14 +591,14 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs P) {
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             float w[V];
-            load<V>(P.pre_w + c, w);
+            if constexpr (!kAhead) load<V>(P.pre_w + c, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 x[i][j] *= ix;
                 y[i][j] *= iy;
                 acc[0][i][j] = fmaf(d[i][j], x[i][j], acc[0][i][j]);
                 acc[1][i][j] += d[i][j];
-                d[i][j] *= w[j];
+                d[i][j] *= kAhead ? kept.pre[j] : w[j];
                 s[0] += d[i][j];
                 s[1] = fmaf(d[i][j], x[i][j], s[1]);
             }
@@ -526,27 +610,27 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormArgs P) {
         for (int i = 0; i < NV; ++i) {
             const int c = (i * n + th) * V;
             if (c >= C) continue;
-            float t[V], g[V], sc[V], w[V], b[V];
-            if (P.gx != nullptr) load<V>(static_cast<const TX*>(P.gx) + base + c, t);
-            if (gated) load<V>(static_cast<const TY*>(P.gate) + base + c, g);
-            if (P.scale != nullptr) load<V>(P.scale + c, sc);
-            if (post) load<V>(P.post_w + c, w);
-            if (P.post_b != nullptr) load<V>(P.post_b + c, b);
+            Weights here;
+            if constexpr (!kAhead) {
+                fetch_late(base + c, 0);
+                weights(c, here);
+                late(0);
+            }
+            const Weights& w = kAhead ? kept : here;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float dx = ix * (d[i][j] - m1 - x[i][j] * m2) + (P.gx != nullptr ? t[j] : 0.f);
+                const float dx = ix * (d[i][j] - m1 - x[i][j] * m2) + t[j];
                 x[i][j] = dx;
-                float z = y[i][j];
-                if (post) z = z * w[j] + (P.post_b != nullptr ? b[j] : 0.f);
+                const float z = y[i][j] * w.post[j] + w.bias[j];
                 float a = 1.f, da = 0.f;
                 if (gated) activate(P.act, g[j], a, da);
                 acc[4][i][j] = fmaf(dx, z * a, acc[4][i][j]);
-                const float ds = P.scale != nullptr ? dx * sc[j] : dx;
+                const float ds = dx * w.scale[j];
                 g[j] = ds * z * da;
                 const float dz = ds * a;
                 acc[2][i][j] = fmaf(dz, y[i][j], acc[2][i][j]);
                 acc[3][i][j] += dz;
-                d[i][j] = post ? dz * w[j] : dz;
+                d[i][j] = dz * w.post[j];
                 s[0] += d[i][j];
                 s[1] = fmaf(d[i][j], y[i][j], s[1]);
             }
@@ -605,8 +689,7 @@ hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
     hipLaunchKernelGGL((head_norm_bwd_kernel<TY, TG, V, NV>), dim3(static_cast<unsigned>((a.H + a.hpb - 1) / a.hpb * a.chunks)),
                        dim3(kBlock), lds, stream, a);
     hipError_t e = hipGetLastError();
-    // one weight for all heads: the heads' sums are rows too
-    ReduceArgs r{a.shared ? a.chunks * a.H : a.chunks, a.shared ? a.G : C};
+    ReduceArgs r{a.chunks, C};
     r.add(a.ws, a.dweight);
     if (a.bias != nullptr) r.add(a.ws + a.chunks * C, a.dbias);
     return e == hipSuccess ? launch_reduce(r, stream) : e;
@@ -619,25 +702,32 @@ hipError_t launch_head_v(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
 }
 
 hipError_t launch_head_t(HeadNormArgs a, bool bwd, hipStream_t stream) {
+    if (a.shared) {  // one weight for all heads: rows H rows of one head
+        a.rows *= a.H;
+        a.H = 1;
+    }
     a.lanes = a.vec ? static_cast<int>(pow2_at_least(a.G / 8 < 64 ? a.G / 8 : 64)) : 64;
     const int slots = kBlock / a.lanes;
     // heads side by side for at least 512 bytes a row of bf16, the workgroup's other slots over rows
     a.hpb = 1;
     while (a.hpb < slots && a.hpb < a.H && a.hpb * a.G < 256) a.hpb *= 2;
-    a.chunks = head_norm_chunks(a.rows);
+    a.chunks = head_norm_chunks(a.rows, a.H * a.G);
     if (a.y_bf16) return launch_head_v<uint16_t, uint16_t>(a, bwd, stream);
     return a.bf16 ? launch_head_v<float, uint16_t>(a, bwd, stream) : launch_head_v<float, float>(a, bwd, stream);
 }
 
 template <typename TX, typename TY, int V, int NV>
-hipError_t launch_block(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
+hipError_t launch_block_fwd(const BlockNormArgs& a, hipStream_t stream) {
     const int64_t block = a.threads == 64 ? 256 : a.threads, per = block / a.threads;
-    if (!bwd) {
-        hipLaunchKernelGGL((block_norm_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
-                           dim3(static_cast<unsigned>(block)), 0, stream, a);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((block_norm_bwd_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.slots + per - 1) / per)),
+    hipLaunchKernelGGL((block_norm_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                       dim3(static_cast<unsigned>(block)), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename TX, typename TY, int V, int NV, int Threads>
+hipError_t launch_block_bwd(const BlockNormArgs& a, hipStream_t stream) {
+    const int64_t block = a.threads == 64 ? 256 : a.threads, per = block / a.threads;
+    hipLaunchKernelGGL((block_norm_bwd_kernel<TX, TY, V, NV, Threads>), dim3(static_cast<unsigned>((a.slots + per - 1) / per)),
                        dim3(static_cast<unsigned>(block)), 0, stream, a);
     hipError_t e = hipGetLastError();
     float* const out[5] = {a.dpre_w, a.pre_b ? a.dpre_b : nullptr, a.post_w ? a.dpost_w : nullptr,
@@ -648,15 +738,23 @@ hipError_t launch_block(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
     return e == hipSuccess ? launch_reduce(r, stream) : e;
 }
 
+// Threads that hold a row: 8 channels each from the smallest count that does (the backward 16 beyond
+// 4096 channels, in at most 512 threads), or, off the 16-byte grid, 1024 threads of single elements.
 template <typename TX, typename TY>
 hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     a.slots = block_norm_slots(a.rows, a.C);
-    if (!a.vec) {
-        a.threads = 1024;
-        return launch_block<TX, TY, 1, 8>(a, bwd, stream);
+    a.threads = !a.vec ? 1024 : a.C <= 512 ? 64 : static_cast<int>(pow2_at_least(a.C / 8));
+    if (!bwd) {
+        if (!a.vec) return launch_block_fwd<TX, TY, 1, 8>(a, stream);
+        if (a.C < WKV_BN_NV2) return launch_block_fwd<TX, TY, 8, 1>(a, stream);
+        a.threads /= 2;
+        return launch_block_fwd<TX, TY, 8, 2>(a, stream);
     }
-    a.threads = a.C <= 512 ? 64 : static_cast<int>(pow2_at_least(a.C / 8));
-    return launch_block<TX, TY, 8, 1>(a, bwd, stream);
+    if (!a.vec)
+        return a.C <= 4096 ? launch_block_bwd<TX, TY, 1, 4, 1024>(a, stream) : launch_block_bwd<TX, TY, 1, 8, 1024>(a, stream);
+    if (a.C <= 4096) return launch_block_bwd<TX, TY, 8, 1, 512>(a, stream);
+    a.threads = 512;
+    return launch_block_bwd<TX, TY, 8, 2, 512>(a, stream);
 }
 
 hipError_t launch_block_t(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
@@ -666,15 +764,19 @@ hipError_t launch_block_t(const BlockNormArgs& a, bool bwd, hipStream_t stream) 
 
 }  // namespace
 
-int64_t head_norm_chunks(int64_t rows) {
-    const int64_t n = (rows + 63) / 64;
-    return n < 128 ? n : 128;
+// Rows of partial sums of a head norm's backward: enough workgroups to fill the card (256 channels each),
+// and no fewer than 32 rows behind each.
+int64_t head_norm_chunks(int64_t rows, int64_t C) {
+    const int64_t most = (int64_t{1} << 19) / C, n = (rows + 31) / 32;
+    const int64_t cap = most < 32 ? 32 : most > 2048 ? 2048 : most;
+    return n < cap ? n : cap;
 }
 
+// Rows of partial sums of a block norm's backward: 8 waves a compute unit, 4 rows or more behind each.
 int64_t block_norm_slots(int64_t rows, int64_t C) {
-    // as many rows of partial sums as fill the card with two workgroups a compute unit
-    const int64_t most = C <= 512 ? 1024 : 512;
-    return rows < most ? rows : most;
+    const int64_t threads = C <= 512 ? 64 : pow2_at_least((C + 7) / 8 < 512 ? (C + 7) / 8 : 512);
+    const int64_t most = 256 * 512 / threads, n = (rows + 3) / 4;
+    return n < most ? n : most;
 }
 
 hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream) {
