@@ -28,6 +28,7 @@
 
 #include <type_traits>
 
+#include "wkv_lanes.h"
 #include "wkv_launch.h"
 
 namespace wkv {
@@ -635,12 +636,12 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
 // as i it meets the blocks J <= x, as j the blocks I >= x (5 blocks for every wave).  Both times the
 // 16 x 16 block is formed with the wave's own tokens as its columns, so it is already the right operand
 // of the products that follow; dr and dk come out transposed, four consecutive channels a lane.
-template <typename T, int N>
+template <int N>
 struct GradShared {
-    static constexpr bool kGoInLds = sizeof(T) * N <= 256;  // float32 at N = 128 reads go from memory: 160 KB of LDS
-    T k[kTile][kRow<T, N>];
-    T r[kTile][kRow<T, N>];
-    T go[kGoInLds ? kTile : 1][kRow<T, N>];
+    static constexpr bool kGoInLds = N == 64;  // N = 128 reads go from memory: 160 KB of LDS
+    float k[kTile][kRow<float, N>];
+    float r[kTile][kRow<float, N>];
+    float go[kGoInLds ? kTile : 1][kRow<float, N>];
     float e[kTile][N + 4];
     float lam[kTile][N + 4];
     float w[kTile], beta[kTile];
@@ -652,19 +653,29 @@ struct GradShared {
     float rowv[kWaves][kSub], colv[kWaves][kSub];
 };
 
-__device__ __forceinline__ float sum_groups(float x) {
-    x += __shfl_xor(x, 16, 64);
-    return x + __shfl_xor(x, 32, 64);
-}
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) x += __shfl_xor(x, m, 64);
-    return x;
+// The gradients of a tile behind its row's length: zeros.
+template <typename T, int N>
+__device__ void zero_tile(const DeltaBwdArgs& P, T* dr, T* dk, int64_t b, int64_t hk, int64_t t0) {
+    const int64_t rows = P.T - t0 < kTile ? P.T - t0 : kTile, per = P.H / P.HK, ks = P.HK * N;
+    for (int64_t t = threadIdx.x / 16; t < rows; t += 16) {
+        for (int c = threadIdx.x % 16 * 4; c < N; c += 64) {
+            store4(&dr[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
+            store4(&dk[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
+        }
+    }
+    for (int64_t i = threadIdx.x; i < rows * per; i += 64 * kWaves) {
+        const int64_t at = (b * P.T + t0 + i / per) * P.H + hk * per + i % per;
+        P.dw[at] = 0.f;
+        P.dbeta[at] = 0.f;
+    }
 }
 
-template <typename T, int N>
+__device__ __forceinline__ float sum16(float x) { return sum_lanes(x, 16); }
+
+template <int N>
 __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs P) {
-    __shared__ GradShared<T, N> sm;
+    using T = float;
+    __shared__ GradShared<N> sm;
     constexpr int NC = N / 16;
     const int lane = threadIdx.x & 63;
     const int x = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -677,19 +688,8 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
     const int64_t ko = b * P.T * ks + hk * N;
     T* dr = static_cast<T*>(P.dr) + ko;
     T* dk = static_cast<T*>(P.dk) + ko;
-    const int64_t rows = P.T - t0 < kTile ? P.T - t0 : kTile;
     if (t0 >= len) {  // nothing of this row here
-        for (int64_t t = threadIdx.x / 16; t < rows; t += 16) {
-            for (int c = threadIdx.x % 16 * 4; c < N; c += 64) {
-                store4(&dr[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
-                store4(&dk[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
-            }
-        }
-        for (int64_t i = threadIdx.x; i < rows * per; i += 64 * kWaves) {
-            const int64_t at = (b * P.T + t0 + i / per) * P.H + hk * per + i % per;
-            P.dw[at] = 0.f;
-            P.dbeta[at] = 0.f;
-        }
+        zero_tile<T, N>(P, dr, dk, b, hk, t0);
         return;
     }
     {
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
         const int64_t bh = b * P.H + h, vo = b * P.T * vs + h * N;
         const T* go = static_cast<const T*>(P.go) + vo;
         __syncthreads();  // the last head's readers are done
-        if constexpr (GradShared<T, N>::kGoInLds) {
+        if constexpr (GradShared<N>::kGoInLds) {
             Staged<T, N> s;
             s.fetch(go, vs, t0, len);
             s.put(sm.go);
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 
         // rows of this wave's tokens: go, lambda, e as right operands
         const auto go4 = [&](int row, int c) -> f4 {
-            if constexpr (GradShared<T, N>::kGoInLds) {
+            if constexpr (GradShared<N>::kGoInLds) {
                 return load4(&sm.go[row][16 * c + 4 * g]);
             } else {
                 return t0 + row < len ? load4(&go[(t0 + row) * vs + 16 * c + 4 * g]) : f4{0.f, 0.f, 0.f, 0.f};
@@ -795,9 +795,9 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
                 }
             }
         }
-        withS = since * sum_groups(withS);
-        withG = until * sum_groups(withG);
-        inner = sum16(sum_groups(inner));
+        withS = since * sum_rows(withS);
+        withG = until * sum_rows(withG);
+        inner = sum16(sum_rows(inner));
         float rowv = withS, colv = beta * withG, dbeta = withG;
 
         // blocks J <= x with this wave's tokens as i: rows j = 4 g + q, columns i
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
                 dkT[c] = mma16(a, dm, dkT[c]);
             }
             if (J < x) {
-                sum = sum_groups(sum);
+                sum = sum_rows(sum);
                 rowv += sum;
                 sum = sum16(sum);
                 if (lane == 0) sm.cross[x][J] = sum;
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
                 if (I == x) sm.diag[x][i][l16] = beta * p;
                 sum += p;
             }
-            sum = sum_groups(sum);
+            sum = sum_rows(sum);
             dbeta += sum;
             if (I > x) colv += beta * sum;
             da *= beta;
@@ -932,6 +932,407 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
     }
 }
 
+// The same from bf16 inputs.  Here a wave owns 16 channels of r and k (N / 64 times) instead of 16 tokens:
+// it reads its rows of S0 and G once, splits them in registers, and takes the tile's 64 tokens of go,
+// lambda and e, split when they are staged, past them.  Phases between barriers:
+//   1. stage k, r, go, and the three terms of e and lambda
+//   2. the 16 x 16 blocks (I, J), J <= I, of dA, dM and P: ten blocks dealt to the four waves;
+//      the products with S0 and G
+//   3. dA, dM and their transposes, as hi + mid (dr and dk are rounded to bf16), to LDS over e and
+//      lambda, each lane's eight values where the lane that needs them reads them
+//   4. every wave: its channels of the products of k and r with all ten blocks; and the rates
+// LDS rows are not padded (two workgroups a compute unit at N = 64): the 16-byte piece q of row t lies at
+// q ^ swizzle(t), so that 16 rows' pieces q meet 16 different bank groups.
+template <int N>
+struct GradShared16 {
+    uint16_t k[kTile][N], r[kTile][N], go[kTile][N];
+    union {
+        struct {
+            uint16_t e[3][kTile][N], lam[3][kTile][N];
+        };
+        uint16_t da[10][4][64][8];  // [block][dA, dM, dA^T, dM^T][lane][hi 4, mid 4]
+    };
+    float w[kTile], beta[kTile];
+    float pre[kTile], suf[kTile], since[kTile], until[kTile];
+    float total[kWaves];
+    float rowsum[10][kSub], colsum[10][kSub];  // of beta_j P_ij over j, of P_ij over i
+    float withS[kWaves][kTile], withG[kWaves][kTile], inner[kWaves];
+    float diag[kTile];                         // the crossing pairs inside the token's own block
+    float rowv[kTile], colv[kTile];
+};
+
+template <int N>
+__device__ __forceinline__ int swizzled(int t, int c) {
+    const int s = N == 64 ? (t >> 1) & 7 : t & 15;
+    return (((c >> 3) ^ s) << 3) | (c & 7);
+}
+template <int N>
+__device__ __forceinline__ bf8 row8(const uint16_t (*X)[N], int t, int c) { return raw8(&X[t][swizzled<N>(t, c)]); }
+
+// tokens tb + 4 g .. + 3 of channel c0 + l16, twice
+template <int N>
+__device__ __forceinline__ bf8 col_twice(const uint16_t (*X)[N], int tb, int c0, int l16, int g) {
+    const int t = tb + 4 * g + (l16 >> 2);
+    const s4 raw = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s4*)&X[t][swizzled<N>(t, c0 + 4 * (l16 & 3))]);
+    const u32x2 a = __builtin_bit_cast(u32x2, raw);
+    return pair(a, a);
+}
+
+template <int N>
+__device__ __forceinline__ void stage_rows(uint16_t (*dst)[N], const uint16_t* base, int64_t stride, int64_t t0, int64_t end) {
+    constexpr int kRowVecs = N / 8;
+#pragma unroll
+    for (int i = 0; i < kTile * kRowVecs / (64 * kWaves); ++i) {
+        const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+        const int t = q / kRowVecs, c = q % kRowVecs * 8;
+        const u32x4 x = t0 + t < end ? *reinterpret_cast<const u32x4*>(base + (t0 + t) * stride + c) : u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(&dst[t][swizzled<N>(t, c)]) = x;
+    }
+}
+
+__device__ __forceinline__ void split8(f4 a, f4 b, bf8 (&out)[3]) {
+    const Terms x = split(a), y = split(b);
+    out[0] = pair(x.hi, y.hi);
+    out[1] = pair(x.mid, y.mid);
+    out[2] = pair(x.lo, y.lo);
+}
+
+template <int N>
+__device__ __forceinline__ void stage_terms(uint16_t (*dst)[kTile][N], const float* base, int64_t stride, int64_t t0, int64_t end) {
+    constexpr int kRowVecs = N / 8;
+#pragma unroll
+    for (int i = 0; i < kTile * kRowVecs / (64 * kWaves); ++i) {
+        const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+        const int t = q / kRowVecs, c = q % kRowVecs * 8;
+        f4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+        if (t0 + t < end) {
+            a = load4(base + (t0 + t) * stride + c);
+            b = load4(base + (t0 + t) * stride + c + 4);
+        }
+        bf8 x[3];
+        split8(a, b, x);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8*>(&dst[p][t][swizzled<N>(t, c)]) = x[p];
+    }
+}
+
+// a b of two factors in three terms each: all but the products below 2^-24 of the whole
+__device__ __forceinline__ f4 mma_terms(const bf8 (&a)[3], const bf8 (&b)[3], f4 c) {
+    c = mfma32(a[2], b[0], c);
+    c = mfma32(a[0], b[2], c);
+    c = mfma32(a[1], b[1], c);
+    c = mfma32(a[1], b[0], c);
+    c = mfma32(a[0], b[1], c);
+    return mfma32(a[0], b[0], c);
+}
+__device__ __forceinline__ f4 mma_terms(const bf8 (&a)[3], bf8 b, f4 c) {
+    c = mfma32(a[2], b, c);
+    c = mfma32(a[1], b, c);
+    return mfma32(a[0], b, c);
+}
+
+template <int N>
+__global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_kernel(DeltaBwdArgs P) {
+    __shared__ GradShared16<N> sm;
+    constexpr int NK = N / kCols;  // 16-channel slices a wave owns
+    constexpr int NM = N / 32;
+    int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int l16 = lane & 15, g = lane >> 4;
+    const int64_t ntile = (P.T + kTile - 1) / kTile;
+    const int64_t bhk = blockIdx.x % (P.B * P.HK), tile = blockIdx.x / (P.B * P.HK);
+    const int64_t b = bhk / P.HK, hk = bhk % P.HK, per = P.H / P.HK;
+    const int64_t len = row_length(P.lengths, b, P.T);
+    const int64_t ks = P.HK * N, vs = P.H * N, t0 = tile * kTile;
+    const int64_t ko = b * P.T * ks + hk * N;
+    uint16_t* dr = static_cast<uint16_t*>(P.dr) + ko;
+    uint16_t* dk = static_cast<uint16_t*>(P.dk) + ko;
+    if (t0 >= len) {  // nothing of this row here
+        zero_tile<uint16_t, N>(P, dr, dk, b, hk, t0);
+        return;
+    }
+    stage_rows<N>(sm.k, static_cast<const uint16_t*>(P.k) + ko, ks, t0, len);
+    stage_rows<N>(sm.r, static_cast<const uint16_t*>(P.r) + ko, ks, t0, len);
+    f4 drT[NK][4], dkT[NK][4];  // [slice][token block]: channels 4 g .. 4 g + 3 of token l16
+#pragma unroll
+    for (int c = 0; c < NK; ++c)
+#pragma unroll
+        for (int X = 0; X < 4; ++X) drT[c][X] = dkT[c][X] = f4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll 1
+    for (int64_t h = hk * per; h < (hk + 1) * per; ++h) {
+        const int64_t bh = b * P.H + h, vo = b * P.T * vs + h * N;
+        // else every address and comparison below is worked out before the loop and kept in registers
+        asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
+        __syncthreads();  // the last head's readers are done
+        stage_rows<N>(sm.go, static_cast<const uint16_t*>(P.go) + vo, vs, t0, len);
+        stage_terms<N>(sm.e, P.errs + vo, vs, t0, len);
+        stage_terms<N>(sm.lam, P.lambda + vo, vs, t0, len);
+        if (threadIdx.x < kTile) {  // one wave: the decays of its 64 tokens
+            const int64_t t = t0 + threadIdx.x;
+            sm.w[lane] = t < len ? P.w[(b * P.T + t) * P.H + h] * kLog2e : 0.f;
+            sm.beta[lane] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
+            float pre = 0.f, suf = 0.f, total[kWaves], before = 0.f, after = 0.f;
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) {
+                const float wi = sm.w[i];
+                if (i % kSub == 0) total[i / kSub] = 0.f;
+                total[i / kSub] += wi;
+                if (i / kSub == g) {
+                    pre += i % kSub <= l16 ? wi : 0.f;
+                    suf += i % kSub > l16 ? wi : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                before += i < g ? total[i] : 0.f;
+                after += i > g ? total[i] : 0.f;
+            }
+            sm.pre[lane] = pre;
+            sm.suf[lane] = suf;
+            sm.since[lane] = ex2(-(before + pre));
+            sm.until[lane] = ex2(-(suf + after));
+            if (l16 == 0) sm.total[g] = g == 0 ? total[0] : g == 1 ? total[1] : g == 2 ? total[2] : total[3];
+        }
+        __syncthreads();
+
+        // ---- the 16 x 16 blocks: rows i = 4 g + q of block I, column j = l16 of block J
+        f4 da[3], dm[3];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const int id = wv + 4 * n;
+            if (id >= 10) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            const int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0, J = id - I * (I + 1) / 2;
+            const int ti = kSub * I + l16, tj = kSub * J + l16;
+            f4 ae = {0.f, 0.f, 0.f, 0.f}, le = ae, kk = ae, rk = ae;
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const int c = 32 * m + 8 * g;
+                const bf8 e[3] = {row8<N>(sm.e[0], tj, c), row8<N>(sm.e[1], tj, c), row8<N>(sm.e[2], tj, c)};
+                const bf8 la[3] = {row8<N>(sm.lam[0], ti, c), row8<N>(sm.lam[1], ti, c), row8<N>(sm.lam[2], ti, c)};
+                const bf8 go = row8<N>(sm.go, ti, c), kj = row8<N>(sm.k, tj, c);
+                ae = mfma32(go, e[2], ae);
+                rk = mfma32(row8<N>(sm.r, ti, c), kj, rk);
+                ae = mfma32(go, e[1], ae);
+                kk = mfma32(row8<N>(sm.k, ti, c), kj, kk);
+                ae = mfma32(go, e[0], ae);
+                le = mma_terms(la, e, le);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            float mid = sm.suf[tj];
+            for (int i = J + 1; i < I; ++i) mid += sm.total[i];
+            float gap[4];
+            if (I == J) {
+                float run = 0.f;
+                int lj = l16;
+                asm volatile("" : "+v"(lj));  // else the comparisons are kept in registers for the whole kernel
+#pragma unroll
+                for (int l = 0; l < kSub; ++l) {
+                    run += l > lj ? sm.w[kSub * I + l] : 0.f;
+                    if (l / 4 == g) gap[l % 4] = run;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) gap[q] = mid + sm.pre[kSub * I + 4 * g + q];
+            }
+            const float beta = sm.beta[tj];
+            f4 p;
+            float col = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = 4 * g + q;
+                const float f = ex2(-gap[q]);
+                da[n][q] = I > J || l16 <= i ? f * ae[q] : 0.f;
+                dm[n][q] = I > J || l16 < i ? -f * le[q] : 0.f;
+                p[q] = da[n][q] * rk[q] + dm[n][q] * kk[q];
+                col += p[q];
+            }
+            const float all = sum_rows(col);
+            if (g == 0) sm.colsum[id][l16] = all;
+            da[n] *= beta;
+            dm[n] *= beta;
+            p *= beta;
+            if (I > J) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float s = sum16(p[q]);
+                    if (l16 == 0) sm.rowsum[id][4 * g + q] = s;
+                }
+            } else {  // pairs j < t <= i: sums over i >= t down the columns, then over j < t along the row
+                const float down = beta * col;  // of this lane's four rows
+                float below = 0.f;
+#pragma unroll
+                for (int o = 1; o < 4; ++o) {
+                    const float x = __shfl(down, (lane + 16 * o) & 63, 64);
+                    below += g + o < 4 ? x : 0.f;
+                }
+#pragma unroll
+                for (int q = 3; q >= 0; --q) {
+                    below += p[q];
+                    const float s = sum16(l16 < 4 * g + q ? below : 0.f);
+                    if (l16 == 0) sm.diag[kSub * I + 4 * g + q] = s;
+                }
+            }
+        }
+
+        // ---- products with the states before and after the tile, for this wave's channels
+        float withS[4] = {0.f, 0.f, 0.f, 0.f}, withG[4] = {0.f, 0.f, 0.f, 0.f}, inner = 0.f;
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int c0 = 16 * (wv + kWaves * c);
+            const float* S0 = P.states + ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
+            const float* G1 = P.gstates + ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
+            f4 sg[4], sl[4], ge[4];
+#pragma unroll
+            for (int X = 0; X < 4; ++X) sg[X] = sl[X] = ge[X] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const f4 sa = load4(S0 + 32 * m), sb = load4(S0 + 32 * m + 4);
+                const f4 ga = load4(G1 + 32 * m), gb = load4(G1 + 32 * m + 4);
+                bf8 s3[3], g3[3];
+                split8(sa, sb, s3);
+                split8(ga, gb, g3);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) inner = fmaf(sa[q], ga[q], fmaf(sb[q], gb[q], inner));
+#pragma unroll
+                for (int X = 0; X < 4; ++X) {
+                    const int t = kSub * X + l16, v = 32 * m + 8 * g;
+                    const bf8 e[3] = {row8<N>(sm.e[0], t, v), row8<N>(sm.e[1], t, v), row8<N>(sm.e[2], t, v)};
+                    const bf8 la[3] = {row8<N>(sm.lam[0], t, v), row8<N>(sm.lam[1], t, v), row8<N>(sm.lam[2], t, v)};
+                    sg[X] = mma_terms(s3, row8<N>(sm.go, t, v), sg[X]);
+                    sl[X] = mma_terms(s3, la, sl[X]);
+                    ge[X] = mma_terms(g3, e, ge[X]);
+                    __builtin_amdgcn_sched_barrier(0);  // the reads of all four blocks at once would spill
+                }
+            }
+#pragma unroll
+            for (int X = 0; X < 4; ++X) {
+                const int t = kSub * X + l16, at = swizzled<N>(t, c0 + 4 * g);
+                const f4 rr = load4(&sm.r[t][at]), kk = load4(&sm.k[t][at]);
+                const float since = sm.since[t], until = sm.until[t], put = until * sm.beta[t];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    withS[X] += since * (rr[q] * sg[X][q] - kk[q] * sl[X][q]);
+                    withG[X] += until * kk[q] * ge[X][q];
+                }
+                drT[c][X] += since * sg[X];
+                dkT[c][X] += put * ge[X] - since * sl[X];
+            }
+        }
+#pragma unroll
+        for (int X = 0; X < 4; ++X) {
+            const float a = sum_rows(withS[X]), d = sum_rows(withG[X]);
+            if (g == 0) {
+                sm.withS[wv][kSub * X + l16] = a;
+                sm.withG[wv][kSub * X + l16] = d;
+            }
+        }
+        inner = sum_lanes(inner, 64);
+        if (lane == 0) sm.inner[wv] = inner;
+        __syncthreads();  // e and lambda are read; the sums are in place
+
+        // ---- dA, dM and their transposes as right operands
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const int id = wv + 4 * n;
+            if (id >= 10) continue;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const Terms x = split(w ? dm[n] : da[n]);
+                *reinterpret_cast<bf8*>(sm.da[id][w][lane]) = pair(x.hi, x.mid);
+                // the lane of row i, columns 4 (l16 / 4) ..: this lane's value is its number l16 % 4
+                uint16_t* to = &sm.da[id][2 + w][16 * (l16 >> 2) + 4 * g][l16 & 3];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    to[8 * q] = static_cast<uint16_t>(x.hi[q / 2] >> (16 * (q & 1)));
+                    to[8 * q + 4] = static_cast<uint16_t>(x.mid[q / 2] >> (16 * (q & 1)));
+                }
+            }
+        }
+        float rowv = 0.f, colv = 0.f, sS = 0.f, sG = 0.f;
+        if (threadIdx.x < kTile) {  // token `lane`, of block g
+            float dbeta = 0.f;
+            for (int i = 0; i < kWaves; ++i) {
+                sS += sm.withS[i][lane];
+                sG += sm.withG[i][lane];
+            }
+            rowv = sS;
+            for (int J = 0; J < g; ++J) rowv += sm.rowsum[g * (g + 1) / 2 + J][l16];
+            for (int I = g; I < kWaves; ++I) {
+                const float x = sm.colsum[I * (I + 1) / 2 + g][l16];
+                dbeta += x;
+                colv += I > g ? x : 0.f;
+            }
+            colv = sm.beta[lane] * (colv + sG);
+            sm.rowv[lane] = rowv;
+            sm.colv[lane] = colv;
+            if (t0 + lane < P.T) P.dbeta[(b * P.T + t0 + lane) * P.H + h] = sG + dbeta;
+        }
+        __syncthreads();
+        if (threadIdx.x < kTile) {
+            // blocks' totals: rows that pair with S0, columns that pair with G, and whole blocks (I, J)
+            float c = sm.inner[0] + sm.inner[1] + sm.inner[2] + sm.inner[3];
+            c *= sm.since[kTile - 1];
+            const float rowS = sum16(sS), colG = sum16(sm.beta[lane] * sG);
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                const float x = __shfl(rowS, 16 * i, 64), y = __shfl(colG, 16 * i, 64);
+                c += (i > g ? x : 0.f) + (i < g ? y : 0.f);
+            }
+#pragma unroll
+            for (int I = 1; I < kWaves; ++I) {
+#pragma unroll
+                for (int J = 0; J < I; ++J) {
+                    const float x = sum16(sm.rowsum[I * (I + 1) / 2 + J][l16]);
+                    c += I > g && J < g ? x : 0.f;
+                }
+            }
+            for (int i = 0; i < kSub; ++i) c += i >= l16 ? sm.rowv[kSub * g + i] : sm.colv[kSub * g + i];
+            c += sm.diag[lane];
+            if (t0 + lane < P.T) P.dw[(b * P.T + t0 + lane) * P.H + h] = t0 + lane < len ? -c : 0.f;
+        }
+
+        // ---- k and r times the blocks, for this wave's channels
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int c0 = 16 * (wv + kWaves * c);
+            bf8 kT[4], rT[4];
+#pragma unroll
+            for (int X = 0; X < 4; ++X) {
+                kT[X] = col_twice<N>(sm.k, kSub * X, c0, l16, g);
+                rT[X] = col_twice<N>(sm.r, kSub * X, c0, l16, g);
+            }
+#pragma unroll
+            for (int I = 0; I < 4; ++I) {
+#pragma unroll
+                for (int J = 0; J <= I; ++J) {
+                    const int id = I * (I + 1) / 2 + J;
+                    const auto at = [&](int w) { return raw8(sm.da[id][w][lane]); };
+                    dkT[c][J] = mfma32(rT[I], at(0), dkT[c][J]);
+                    drT[c][I] = mfma32(kT[J], at(2), drT[c][I]);
+                    dkT[c][J] = mfma32(kT[I], at(1), dkT[c][J]);
+                    dkT[c][I] = mfma32(kT[J], at(3), dkT[c][I]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int X = 0; X < 4; ++X) {
+        const int64_t t = t0 + kSub * X + l16;
+        if (t >= P.T) continue;
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+            const int64_t at = t * ks + 16 * (wv + kWaves * c) + 4 * g;
+            store4(&dr[at], drT[c][X]);
+            store4(&dk[at], dkT[c][X]);
+        }
+    }
+}
+
 template <typename T, int N>
 hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
     if (a.states == nullptr && a.o != nullptr && a.T <= kDeltaStepMaxT) {
@@ -952,8 +1353,12 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ntile = (a.T + kTile - 1) / kTile;
-    hipLaunchKernelGGL((delta_grad_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.HK * ntile)), dim3(64 * kWaves), 0,
-                       stream, a);
+    const dim3 grid(static_cast<unsigned>(a.B * a.HK * ntile));
+    if constexpr (std::is_same_v<T, uint16_t>) {
+        hipLaunchKernelGGL((delta_grad16_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((delta_grad_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
+    }
     return hipGetLastError();
 }
 
