@@ -696,6 +696,7 @@ DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int
     if (!mul3(B, H, 1, &bh) || !mul3(bh, N, N, &p.ns) || p.ns > kMost / 4) return bad(WKV_ESIZE);
     if (!mul3(H, N, 4, &hn) || !mul3(B, T, hn, &n) || n > kMost) return bad(WKV_ESIZE);
     if (!mul3(p.ns, (T + 63) / 64, 4, &st) || st > kMost) return bad(WKV_ESIZE);
+    if (H * N >= (int64_t{1} << 22)) return bad(WKV_ESIZE);  // 64 rows of float32 values below 2^31 bytes
     // grids: a workgroup per (64 columns, pair) and per (64 tokens, row, key head), below 2^31
     int64_t tiles;
     if (bh >= (int64_t{1} << 30) || !mul3(B, HK, (T + 63) / 64, &tiles) || tiles >= (int64_t{1} << 31)) return bad(WKV_ESIZE);

@@ -148,6 +148,25 @@ __device__ __forceinline__ f4 rows_product(const float* a, const float* b, int g
     return acc;
 }
 
+// A block's 16 rows of a staged array as a left operand (row l16 a lane): bf16 rows are held in registers,
+// so that they are read while the state is still being split; float32 rows are read as they are used.
+template <typename T, int N>
+struct LeftRows;
+
+template <int N>
+struct LeftRows<float, N> {
+    const float* row;
+    __device__ __forceinline__ LeftRows(const float* p, int) : row(p) {}
+};
+template <int N>
+struct LeftRows<uint16_t, N> {
+    bf8 a[N / 32];
+    __device__ __forceinline__ LeftRows(const uint16_t* p, int g) {
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) a[m] = raw8(p + 32 * m + 8 * g);
+    }
+};
+
 // The state's 16 columns as a right operand, for one block.
 template <typename T, int N>
 struct StateOperand;
@@ -159,12 +178,11 @@ struct StateOperand<float, N> {
 #pragma unroll
         for (int c = 0; c < N / 16; ++c) s[c] = S[c];
     }
-    // rows (row l16 at `row`) times the state
     template <bool kRounded>
-    __device__ __forceinline__ f4 times(const float* row, int g) const {
+    __device__ __forceinline__ f4 times(const LeftRows<float, N>& x, int g) const {
         f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) acc = mma16(load4(row + state_row(c, g, 0)), s[c], acc);
+        for (int c = 0; c < N / 16; ++c) acc = mma16(load4(x.row + state_row(c, g, 0)), s[c], acc);
         return acc;
     }
 };
@@ -183,45 +201,79 @@ struct StateOperand<uint16_t, N> {
     }
     // kRounded: the result is rounded to bf16 and used for nothing else
     template <bool kRounded>
-    __device__ __forceinline__ f4 times(const uint16_t* row, int g) const {
+    __device__ __forceinline__ f4 times(const LeftRows<uint16_t, N>& x, int) const {
         f4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent products
 #pragma unroll
         for (int m = 0; m < N / 32; ++m) {
-            const bf8 a = raw8(row + 32 * m + 8 * g);
-            acc2 = mfma32(a, mid[m], acc2);
-            if constexpr (!kRounded) acc2 = mfma32(a, lo[m], acc2);
-            acc = mfma32(a, hi[m], acc);
+            acc2 = mfma32(x.a[m], mid[m], acc2);
+            acc = mfma32(x.a[m], hi[m], acc);
+            if constexpr (!kRounded) {
+                if (m & 1) acc = mfma32(x.a[m], lo[m], acc);
+                else acc2 = mfma32(x.a[m], lo[m], acc2);
+            }
         }
         return acc + acc2;
     }
 };
 
-// S += X^T u over a block's 16 tokens: X rows tb .. tb + 15 of a staged array, u four tokens a lane.
-template <int N>
-__device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const float (*X)[kRow<float, N>], int tb, f4 u, int l16, int g) {
-#pragma unroll
-    for (int c = 0; c < N / 16; ++c) {
-        f4 a;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) a[q] = X[tb + 4 * g + q][state_row(c, l16 >> 2, l16 & 3)];
-        S[c] = mma16(a, u, S[c]);
-    }
+// A block's 16 rows of a staged array as the left operand of S += X^T u: four tokens of one channel a lane,
+// in the state's row order.  bf16: one transposing LDS read gives a lane its four tokens of one channel (in
+// each group of 16 lanes, lane 4 e + p reads four channels of token e, and lane j receives element j % 4 of
+// lane 4 e + j / 4's read for e = 0 .. 3).
+__device__ __forceinline__ u32x2 read_tr(const uint16_t* at) {
+    const s4 raw = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at);
+    return __builtin_bit_cast(u32x2, raw);
 }
-// bf16: one transposing LDS read gives a lane its four tokens of one channel (in each group of 16 lanes,
-// lane 4 e + p reads four channels of token e, and lane j receives element j % 4 of lane 4 e + j / 4's
-// read for e = 0 .. 3); hi and mid of u share one 32-index product over the same tokens twice.
+
+template <typename T, int N>
+struct LeftCols;
+
 template <int N>
-__device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const uint16_t (*X)[kRow<uint16_t, N>], int tb, f4 u, int l16, int g) {
-    const Terms t = split(u);
-    const bf8 b = pair(t.hi, t.mid), b2 = pair(t.lo, u32x2{0, 0});
+struct LeftCols<float, N> {
+    const float (*x)[kRow<float, N>];
+    int l16;
+    __device__ __forceinline__ LeftCols(const float (*X)[kRow<float, N>], int tb, int l16_, int g) : x(X + tb + 4 * g), l16(l16_) {}
+    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], f4 u) const {
 #pragma unroll
-    for (int c = 0; c < N / 16; ++c) {
-        const uint16_t* at = &X[tb + 4 * g + (l16 >> 2)][state_row(c, l16 & 3, 0)];
-        const s4 raw = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at);
-        const u32x2 a = __builtin_bit_cast(u32x2, raw);
-        S[c] = mfma32(pair(a, a), b2, S[c]);
-        S[c] = mfma32(pair(a, a), b, S[c]);
+        for (int c = 0; c < N / 16; ++c) {
+            f4 a;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) a[q] = x[q][state_row(c, l16 >> 2, l16 & 3)];
+            S[c] = mma16(a, u, S[c]);
+        }
     }
+};
+template <int N>
+struct LeftCols<uint16_t, N> {
+    u32x2 a[N / 16];
+    __device__ __forceinline__ LeftCols(const uint16_t (*X)[kRow<uint16_t, N>], int tb, int l16, int g) {
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) a[c] = read_tr(&X[tb + 4 * g + (l16 >> 2)][state_row(c, l16 & 3, 0)]);
+    }
+    // hi and mid of u share one 32-index product over the same tokens twice
+    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], f4 u) const {
+        const Terms t = split(u);
+        const bf8 b = pair(t.hi, t.mid), b2 = pair(t.lo, u32x2{0, 0});
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) S[c] = mfma32(pair(a[c], a[c]), b2, S[c]);
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) S[c] = mfma32(pair(a[c], a[c]), b, S[c]);
+    }
+};
+
+// Four tokens tb + 4 g .. of column c0 + l16 of a staged array of value columns.
+template <int ROW>
+__device__ __forceinline__ f4 value_column(const float (*X)[ROW], int tb, int c0, int l16, int g) {
+    f4 x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = X[tb + 4 * g + q][c0 + l16];
+    return x;
+}
+template <int ROW>
+__device__ __forceinline__ f4 value_column(const uint16_t (*X)[ROW], int tb, int c0, int l16, int g) {
+    const u32x2 x = read_tr(&X[tb + 4 * g + (l16 >> 2)][c0 + 4 * (l16 & 3)]);
+    return f4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+              __uint_as_float(x[1] & 0xffff0000u)};
 }
 
 // Rows t0 .. t0 + 63 of a [rows, stride] array, W columns from its base, on their way to LDS: held in
@@ -250,6 +302,18 @@ struct Staged {
             *reinterpret_cast<u32x4*>(&dst[q / kRowVecs][q % kRowVecs * kPer]) = x[i];
         }
     }
+    // the other way: this thread's pieces of a staged array to rows t0 .. of `base`, below `end`
+    template <int ROW>
+    static __device__ __forceinline__ void flush(const T (*src)[ROW], T* base, int64_t stride, int64_t t0, int64_t end) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+            const int64_t t = t0 + q / kRowVecs;
+            if (t < end)
+                *reinterpret_cast<u32x4*>(base + t * stride + q % kRowVecs * kPer) =
+                    *reinterpret_cast<const u32x4*>(&src[q / kRowVecs][q % kRowVecs * kPer]);
+        }
+    }
 };
 
 __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t T) {
@@ -261,64 +325,101 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b,
 // What the four 16-token blocks of a tile need besides their rows.
 struct Blocks {
     float w[kTile], beta[kTile];         // rates in log2 units; zero behind the row's length
-    float since[kTile], until[kTile];    // decay from the block's start through the token, and after it to its end
-    float inv[kWaves][kSub][kPadM];      // X
-    float att[kWaves][kSub][kPadM];      // A
+    float since[kTile];                  // decay from the block's start through the token
+    float put[kTile];                    // beta until: the write strength, decayed to the block's end
+    float inv[kWaves][kSub][kPadM];      // X, or its transpose
+    float att[kWaves][kSub][kPadM];      // A, or its transpose
     float m[kWaves][kSub][kPadM];        // M diag(beta), while X is found
 };
 
-// Wave s prepares block s of the staged tile: decays, X and A.  The 16 x 16 products take their rows of
-// k and r as they are staged; register r of group g holds element (i = 4 g + r, j = l16).
-template <typename T, int N>
+// A thread's token of the next tile's rates.
+struct Rates {
+    float w, beta;
+    __device__ __forceinline__ void fetch(const float* pw, const float* pb, int64_t H, int64_t t0, int64_t end) {
+        const int64_t t = t0 + threadIdx.x;
+        w = beta = 0.f;
+        if (threadIdx.x < kTile && t < end) {
+            w = pw[t * H];
+            beta = pb[t * H];
+        }
+    }
+    __device__ __forceinline__ void put(Blocks& B) const {
+        if (threadIdx.x < kTile) {
+            B.w[threadIdx.x] = w * kLog2e;
+            B.beta[threadIdx.x] = beta;
+        }
+    }
+};
+
+// Wave s prepares block s of the staged tile: decays, X and (kAtt) A, or (kAdj) their transposes.
+// Register r of group g holds element (i = 4 g + r, j = l16) of the 16 x 16 products.
+template <typename T, int N, bool kAtt, bool kAdj>
 __device__ __forceinline__ void prepare_block(int s, int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>],
                                               Blocks& B) {
     asm volatile("" : "+v"(l16), "+v"(g));  // else the comparisons below are kept in registers from tile to tile
     const f4 kk = rows_product<N>(K[kSub * s + l16], K[kSub * s + l16], g);
-    const f4 rk = rows_product<N>(R[kSub * s + l16], K[kSub * s + l16], g);
+    f4 rk = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kAtt) rk = rows_product<N>(R[kSub * s + l16], K[kSub * s + l16], g);
+    f4 wv[kSub / 4];
+#pragma unroll
+    for (int l = 0; l < kSub / 4; ++l) wv[l] = load4(&B.w[kSub * s + 4 * l]);
+    const float bj = B.beta[kSub * s + l16];
     float gap[4] = {0.f, 0.f, 0.f, 0.f};  // sum of w over j < l <= i
-    float run = 0.f, pre = 0.f, suf = 0.f;
+    float run = 0.f, pre = 0.f;
 #pragma unroll
     for (int l = 0; l < kSub; ++l) {
-        const float wl = B.w[kSub * s + l];
-        run += l > l16 ? wl : 0.f;
-        pre += l <= l16 ? wl : 0.f;
-        suf += l > l16 ? wl : 0.f;
+        const float wl = wv[l / 4][l % 4];
+        const bool behind = l > l16;
+        run += behind ? wl : 0.f;
+        pre += behind ? 0.f : wl;
         if (l / 4 == g) gap[l % 4] = run;
     }
     if (g == 0) {
         B.since[kSub * s + l16] = ex2(-pre);
-        B.until[kSub * s + l16] = ex2(-suf);
+        B.put[kSub * s + l16] = ex2(-run) * bj;
     }
-    const float bj = B.beta[kSub * s + l16];
+    f4 m, att;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = 4 * g + r;
         const float f = ex2(-gap[r]) * bj;
-        B.m[s][i][l16] = l16 < i ? f * kk[r] : 0.f;
-        B.att[s][i][l16] = l16 <= i ? f * rk[r] : 0.f;
+        m[r] = l16 < i ? f * kk[r] : 0.f;
+        att[r] = l16 <= i ? f * rk[r] : 0.f;
+    }
+    // Forward: row l16 of X, its elements from the last, x_j = [j == l16] - sum_{i > j} x_i m_ij, the table
+    // holding the transpose of m.  Adjoint: column l16, x_i = [i == l16] - sum_{j < i} m_ij x_j.  Either way
+    // the lane ends with a row of what the products take.
+    if constexpr (kAdj) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) B.m[s][4 * g + r][l16] = m[r];
+        *reinterpret_cast<f4*>(&B.att[s][l16][4 * g]) = att;
+    } else {
+        *reinterpret_cast<f4*>(&B.m[s][l16][4 * g]) = m;
+        if constexpr (kAtt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) B.att[s][4 * g + r][l16] = att[r];
+        }
     }
     __builtin_amdgcn_wave_barrier();  // the table is read back by the wave that wrote it
-    // column l16 of X, row by row: x_i = [i == l16] - sum_{j < i} (M diag(beta))_ij x_j
     float x[kSub];
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-        float acc = i == l16 ? 1.f : 0.f;
+    for (int n = 0; n < kSub; ++n) {
+        const int at = kAdj ? n : kSub - 1 - n;
+        f4 row[kSub / 4];
 #pragma unroll
-        for (int j = 0; j < i; ++j) acc = fmaf(-B.m[s][i][j], x[j], acc);
-        x[i] = acc;
+        for (int l = 0; l < kSub / 4; ++l) row[l] = load4(&B.m[s][at][4 * l]);
+        float acc = at == l16 ? 1.f : 0.f;
+#pragma unroll
+        for (int l = 0; l < n; ++l) {
+            const int j = kAdj ? l : kSub - 1 - l;
+            acc = fmaf(-row[j / 4][j % 4], x[j], acc);
+        }
+        x[at] = acc;
     }
     if (g == 0) {
 #pragma unroll
-        for (int i = 0; i < kSub; ++i) B.inv[s][i][l16] = x[i];
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void load_rates(Blocks& B, const float* w, const float* beta, int64_t H, int64_t t0, int64_t end) {
-    if (threadIdx.x < kTile) {
-        const int64_t t = t0 + threadIdx.x;
-        B.w[threadIdx.x] = t < end ? w[t * H] * kLog2e : 0.f;
-        B.beta[threadIdx.x] = t < end ? beta[t * H] : 0.f;
+        for (int l = 0; l < kSub / 4; ++l)
+            *reinterpret_cast<f4*>(&B.inv[s][l16][4 * l]) = f4{x[4 * l], x[4 * l + 1], x[4 * l + 2], x[4 * l + 3]};
     }
 }
 
@@ -326,19 +427,27 @@ template <typename T, int N>
 struct FwdShared {
     T k[kTile][kRow<T, N>];
     T r[kTile][kRow<T, N>];
-    T v[kTile][kRow<T, kCols>];
+    T v[kTile][kRow<T, kCols>];  // and, block by block, o in its place
     Blocks blk;
 };
 
+// Four rows 4 g + q of a wave's columns to a float32 array of value rows, those below `rows`.
+__device__ __forceinline__ void store_rows(float* base, int stride, int at, f4 x, int g, int rows) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (4 * g + q < rows) base[(4 * g + q) * stride + at] = x[q];
+}
+
 // Chunked forward.  One workgroup per (64 value columns, batch row, head) walks the tiles in order: stage
 // the tile, each wave prepares one of its four blocks, then each wave takes its 16 columns through the
-// blocks one after the other with no barrier between them.
-template <typename T, int N>
+// blocks one after the other with no barrier between them.  kOut false: a pass for the saved errors and
+// states, or the final state, only.
+template <typename T, int N, bool kOut>
 __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(DeltaArgs P) {
     __shared__ FwdShared<T, N> sm;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
+    int l16 = lane & 15, g = lane >> 4;
     const int64_t BH = P.B * P.H;
     const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
     const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
@@ -348,11 +457,10 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
     const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
     const int64_t vo = b * P.T * vs + h * N + cb * kCols;
     const T* v = static_cast<const T*>(P.v) + vo;
-    T* o = P.o != nullptr ? static_cast<T*>(P.o) + vo : nullptr;
+    T* o = static_cast<T*>(P.o) + vo;
     const float* w = P.w + b * P.T * P.H + h;
     const float* beta = P.beta + b * P.T * P.H + h;
-    const int col = 16 * wv + l16;           // of the workgroup's 64
-    const int64_t scol = cb * kCols + col;   // of the state
+    const int64_t scol = cb * kCols + 16 * wv + l16;  // of the state
     const int64_t ntile = (P.T + kTile - 1) / kTile;
 
     f4 S[N / 16];
@@ -364,63 +472,74 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
 
     Staged<T, N> fk, fr;
     Staged<T, kCols> fv;
-    fk.fetch(k, ks, 0, len);
-    fr.fetch(r, ks, 0, len);
-    fv.fetch(v, vs, 0, len);
+    Rates fw;
+    const auto fetch = [&](int64_t t) {
+        fk.fetch(k, ks, t, len);
+        if constexpr (kOut) fr.fetch(r, ks, t, len);
+        fv.fetch(v, vs, t, len);
+        fw.fetch(w, beta, P.H, t, len);
+    };
+    fetch(0);
     int64_t t0 = 0;
+#pragma unroll 1
     for (; t0 < len; t0 += kTile) {
-        __syncthreads();  // the last tile's readers are done
+        // else every address and comparison below is worked out before the loop and kept in registers
+        asm volatile("" : "+v"(l16), "+v"(g));
+        __syncthreads();  // the last tile's readers are done, and its outputs in place
+        if (kOut && t0 > 0) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
         fk.put(sm.k);
-        fr.put(sm.r);
+        if constexpr (kOut) fr.put(sm.r);
         fv.put(sm.v);
-        load_rates<T>(sm.blk, w, beta, P.H, t0, len);
+        fw.put(sm.blk);
         __syncthreads();
-        if (t0 + kTile < len) {
-            fk.fetch(k, ks, t0 + kTile, len);
-            fr.fetch(r, ks, t0 + kTile, len);
-            fv.fetch(v, vs, t0 + kTile, len);
-        }
-        prepare_block<T, N>(wv, l16, g, sm.k, sm.r, sm.blk);
+        if (t0 + kTile < len) fetch(t0 + kTile);
+        prepare_block<T, N, kOut, false>(wv, l16, g, sm.k, sm.r, sm.blk);
         if (P.states != nullptr) {
-            float* st = P.states + (bh * ntile + t0 / kTile) * N * N + scol;
+            float* st = P.states + (bh * ntile + t0 / kTile) * N * N + cb * kCols + 16 * wv;
 #pragma unroll
             for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) st[state_row(c, g, q) * N] = S[c][q];
+                for (int q = 0; q < 4; ++q) st[state_row(c, g, q) * N + l16] = S[c][q];
         }
         __syncthreads();
 #pragma unroll 1
         for (int s = 0; s < kTile / kSub; ++s) {
             const int tb = kSub * s;
-            if (t0 + tb >= P.T) break;
-            const StateOperand<T, N> op(S);
-            const f4 kS = op.template times<false>(sm.k[tb + l16], g);
-            const f4 rS = op.template times<true>(sm.r[tb + l16], g);
-            const f4 since = load4(&sm.blk.since[tb + 4 * g]);
-            const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
-            f4 e0, out;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                e0[q] = widen(sm.v[tb + 4 * g + q][col]) - since[q] * kS[q];
-                out[q] = since[q] * rS[q];
-            }
-            const f4 e = mma16(load4(&sm.blk.inv[s][l16][4 * g]), e0, f4{0.f, 0.f, 0.f, 0.f});
-            out = mma16(load4(&sm.blk.att[s][l16][4 * g]), e, out);
-            const f4 u = put * e;
+            // everything the block reads is on its way while the state is split
+            const LeftRows<T, N> kr(sm.k[tb + l16], g);
+            const f4 e_in = value_column(sm.v, tb, 16 * wv, l16, g);
+            const f4 since = load4(&sm.blk.since[tb + 4 * g]), put = load4(&sm.blk.put[tb + 4 * g]);
+            const f4 inv = load4(&sm.blk.inv[s][l16][4 * g]);
             const float total = sm.blk.since[tb + kSub - 1];
+            const LeftCols<T, N> kc(sm.k, tb, l16, g);
+            const LeftRows<T, N> rr(sm.r[tb + l16], g);
+            const f4 att = load4(&sm.blk.att[s][l16][4 * g]);
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+            const StateOperand<T, N> op(S);
+            const f4 kS = op.template times<false>(kr, g);
+            f4 out = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (kOut) out = since * op.template times<true>(rr, g);
 #pragma unroll
             for (int c = 0; c < N / 16; ++c) S[c] *= total;
-            add_outer<N>(S, sm.k, tb, u, l16, g);
+            const f4 e = mma16(inv, e_in - since * kS, f4{0.f, 0.f, 0.f, 0.f});
+            kc.add_outer(S, put * e);
+            if constexpr (kOut) {
+                out = mma16(att, e, out);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t t = t0 + tb + 4 * g + q;
-                if (t >= P.T) continue;
-                if (o != nullptr) store1(&o[t * vs + col], out[q]);
-                if (P.errs != nullptr) P.errs[vo + t * vs + col] = e[q];
+                for (int q = 0; q < 4; ++q) store1(&sm.v[tb + 4 * g + q][16 * wv + l16], out[q]);
+            }
+            if (P.errs != nullptr) {
+                const int64_t left = P.T - t0 - tb;
+                if (left > 0)
+                    store_rows(P.errs + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, e, g,
+                               left < kSub ? static_cast<int>(left) : kSub);
             }
         }
     }
-    if (o != nullptr) {  // whole tiles behind the row's length: zeros
+    if constexpr (kOut) {
+        __syncthreads();
+        if (t0 > 0) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
+        // whole tiles behind the row's length: zeros
         for (int64_t t = t0 + threadIdx.x / 16; t < P.T; t += 16) store4(&o[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
     }
     if (P.s_out != nullptr) {
@@ -518,7 +637,7 @@ template <typename T, int N>
 struct AdjShared {
     T k[kTile][kRow<T, N>];
     T r[kTile][kRow<T, N>];
-    T go[kTile][kRow<T, kCols>];
+    T go[kTile][kRow<T, kCols>];  // and, block by block, dv in its place
     Blocks blk;
 };
 
@@ -527,7 +646,7 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
     __shared__ AdjShared<T, N> sm;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
+    int l16 = lane & 15, g = lane >> 4;
     const int64_t BH = P.B * P.H;
     const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
     const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
@@ -540,8 +659,7 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
     T* dv = static_cast<T*>(P.dv) + vo;
     const float* w = P.w + b * P.T * P.H + h;
     const float* beta = P.beta + b * P.T * P.H + h;
-    const int col = 16 * wv + l16;
-    const int64_t scol = cb * kCols + col;
+    const int64_t scol = cb * kCols + 16 * wv + l16;
     const int64_t ntile = (P.T + kTile - 1) / kTile;
 
     f4 G[N / 16];
@@ -556,61 +674,61 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
         store4(&dv[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
     Staged<T, N> fk, fr;
     Staged<T, kCols> fg;
-    if (live > 0) {
-        fk.fetch(k, ks, (live - 1) * kTile, len);
-        fr.fetch(r, ks, (live - 1) * kTile, len);
-        fg.fetch(go, vs, (live - 1) * kTile, len);
-    }
+    Rates fw;
+    const auto fetch = [&](int64_t t) {
+        fk.fetch(k, ks, t, len);
+        fr.fetch(r, ks, t, len);
+        fg.fetch(go, vs, t, len);
+        fw.fetch(w, beta, P.H, t, len);
+    };
+    if (live > 0) fetch((live - 1) * kTile);
+#pragma unroll 1
     for (int64_t tile = live - 1; tile >= 0; --tile) {
+        asm volatile("" : "+v"(l16), "+v"(g));  // as in the forward
         const int64_t t0 = tile * kTile;
         __syncthreads();
+        if (tile + 1 < live) Staged<T, kCols>::flush(sm.go, dv, vs, t0 + kTile, P.T);
         fk.put(sm.k);
         fr.put(sm.r);
         fg.put(sm.go);
-        load_rates<T>(sm.blk, w, beta, P.H, t0, len);
+        fw.put(sm.blk);
         __syncthreads();
-        if (tile > 0) {
-            fk.fetch(k, ks, t0 - kTile, len);
-            fr.fetch(r, ks, t0 - kTile, len);
-            fg.fetch(go, vs, t0 - kTile, len);
-        }
-        prepare_block<T, N>(wv, l16, g, sm.k, sm.r, sm.blk);
-        float* gt = P.gstates + (bh * ntile + tile) * N * N + scol;
+        if (tile > 0) fetch(t0 - kTile);
+        prepare_block<T, N, true, true>(wv, l16, g, sm.k, sm.r, sm.blk);
+        float* gt = P.gstates + (bh * ntile + tile) * N * N + cb * kCols + 16 * wv;
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N] = G[c][q];
+            for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N + l16] = G[c][q];
         __syncthreads();
 #pragma unroll 1
         for (int s = kTile / kSub - 1; s >= 0; --s) {
             const int tb = kSub * s;
-            const f4 kG = StateOperand<T, N>(G).template times<false>(sm.k[tb + l16], g);
-            const f4 since = load4(&sm.blk.since[tb + 4 * g]);
-            const f4 put = load4(&sm.blk.until[tb + 4 * g]) * load4(&sm.blk.beta[tb + 4 * g]);
-            f4 d, att, inv;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                d[q] = widen(sm.go[tb + 4 * g + q][col]);
-                att[q] = sm.blk.att[s][4 * g + q][l16];
-                inv[q] = sm.blk.inv[s][4 * g + q][l16];
-            }
-            const f4 y = mma16(att, d, put * kG);
-            const f4 lam = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
-            const f4 gr = since * d, gk = -since * lam;
+            const LeftRows<T, N> kr(sm.k[tb + l16], g);
+            const f4 d = value_column(sm.go, tb, 16 * wv, l16, g);
+            const f4 since = load4(&sm.blk.since[tb + 4 * g]), put = load4(&sm.blk.put[tb + 4 * g]);
+            const f4 att = load4(&sm.blk.att[s][l16][4 * g]), inv = load4(&sm.blk.inv[s][l16][4 * g]);
             const float total = sm.blk.since[tb + kSub - 1];
+            const LeftCols<T, N> rc(sm.r, tb, l16, g);
+            const LeftCols<T, N> kc(sm.k, tb, l16, g);
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+            const f4 kG = StateOperand<T, N>(G).template times<false>(kr, g);
 #pragma unroll
             for (int c = 0; c < N / 16; ++c) G[c] *= total;
-            add_outer<N>(G, sm.r, tb, gr, l16, g);
-            add_outer<N>(G, sm.k, tb, gk, l16, g);
+            rc.add_outer(G, since * d);
+            const f4 y = mma16(att, d, put * kG);
+            const f4 lam = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
+            kc.add_outer(G, -since * lam);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t t = t0 + tb + 4 * g + q;
-                if (t >= P.T) continue;
-                store1(&dv[t * vs + col], lam[q]);
-                P.lambda[vo + t * vs + col] = lam[q];
-            }
+            for (int q = 0; q < 4; ++q) store1(&sm.go[tb + 4 * g + q][16 * wv + l16], lam[q]);
+            const int64_t left = P.T - t0 - tb;
+            if (left > 0)
+                store_rows(P.lambda + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, lam, g,
+                           left < kSub ? static_cast<int>(left) : kSub);
         }
     }
+    __syncthreads();
+    if (live > 0) Staged<T, kCols>::flush(sm.go, dv, vs, 0, P.T);
     if (P.ds_in != nullptr) {
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
@@ -1340,8 +1458,12 @@ hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)),
                            dim3(64 * kWaves), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((delta_fwd_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.H * (N / kCols))),
-                           dim3(64 * kWaves), 0, stream, a);
+        const dim3 grid(static_cast<unsigned>(a.B * a.H * (N / kCols)));
+        if (a.o != nullptr) {
+            hipLaunchKernelGGL((delta_fwd_kernel<T, N, true>), grid, dim3(64 * kWaves), 0, stream, a);
+        } else {
+            hipLaunchKernelGGL((delta_fwd_kernel<T, N, false>), grid, dim3(64 * kWaves), 0, stream, a);
+        }
     }
     return hipGetLastError();
 }
