@@ -714,16 +714,71 @@ size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
     return p.st == WKV_OK ? p.rows_bytes + p.states_bytes : 0;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The scratch of a time split: what the segments do, [B H, nseg, 2, N, N], and their start states,
+// [B H, nseg, N, N], float32.  0 when there is none to make.
+size_t delta_split_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int64_t* nseg, int64_t* per) {
+    *nseg = wkv::delta_segments(B * H, T, N, per);
+    return *nseg > 1 ? static_cast<size_t>(B * H * *nseg) * 3 * N * N * sizeof(float) : 0;
+}
+
+// A forward in whole sequences, or (scratch not NULL) in nseg segments at once.
+hipError_t run_delta_fwd(wkv::DeltaArgs a, int64_t nseg, int64_t per, void* scratch, hipStream_t stream) {
+    a.per = (a.T + 63) / 64;
+    if (scratch == nullptr || nseg <= 1) return wkv::launch_delta_fwd(a, stream);
+    float* local = static_cast<float*>(scratch);
+    float* starts = local + a.B * a.H * nseg * 2 * a.N * a.N;
+    a.nseg = nseg;
+    a.per = per;
+    wkv::DeltaArgs p1 = a;
+    p1.o = nullptr;
+    p1.s_out = p1.errs = p1.states = nullptr;
+    p1.local = local;
+    hipError_t e = wkv::launch_delta_fwd(p1, stream);
+    if (e != hipSuccess) return e;
+    e = wkv::launch_delta_chain(wkv::DeltaChainArgs{a.B * a.H, a.N, nseg, false, a.s_in, local, starts}, stream);
+    if (e != hipSuccess) return e;
+    a.starts = starts;
+    return wkv::launch_delta_fwd(a, stream);
+}
+
+hipError_t run_delta_bwd(wkv::DeltaBwdArgs a, int64_t nseg, int64_t per, void* scratch, hipStream_t stream) {
+    a.per = (a.T + 63) / 64;
+    if (scratch == nullptr || nseg <= 1) return wkv::launch_delta_bwd(a, stream);
+    float* local = static_cast<float*>(scratch);
+    float* starts = local + a.B * a.H * nseg * 2 * a.N * a.N;
+    a.nseg = nseg;
+    a.per = per;
+    wkv::DeltaBwdArgs p1 = a;
+    p1.local = local;
+    hipError_t e = wkv::launch_delta_bwd(p1, stream);
+    if (e != hipSuccess) return e;
+    e = wkv::launch_delta_chain(wkv::DeltaChainArgs{a.B * a.H, a.N, nseg, true, a.ds_out, local, starts}, stream);
+    if (e != hipSuccess) return e;
+    a.starts = starts;
+    return wkv::launch_delta_bwd(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N) {
-    (void)delta_plan(B, T, H, HK, N, WKV_F32);
-    return 0;
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
+    int64_t nseg, per;
+    return p.st == WKV_OK && p.ns > 0 ? delta_split_bytes(B, T, H, N, &nseg, &per) : 0;
 }
 
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags) {
     const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
-    if (p.st != WKV_OK) return 0;
+    if (p.st != WKV_OK || p.ns == 0 || T == 0) return 0;
+    int64_t nseg, per;
     const size_t one = p.rows_bytes + p.states_bytes;
-    return (flags & WKV_WS_HAVE_CKPT) != 0 ? one : 2 * one;
+    const size_t split = (flags & WKV_WS_NO_SPLIT) != 0 ? 0 : delta_split_bytes(B, T, H, N, &nseg, &per);
+    return ((flags & WKV_WS_HAVE_CKPT) != 0 ? one : 2 * one) + split;
 }
 
 wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
@@ -732,8 +787,6 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
                                size_t workspace_bytes, void* hip_stream) {
     const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype);
     if (p.st != WKV_OK) return p.st;
-    (void)workspace;
-    (void)workspace_bytes;
     if (p.ns == 0) return WKV_OK;
     if ((s_in && !aligned(s_in, 16)) || (s_out && !aligned(s_out, 16))) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
@@ -742,10 +795,13 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
     if (!aligned(w, 4) || !aligned(beta, 4) || !aligned(r, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
         (lengths && !aligned(lengths, 4)) || (ckpt && !aligned(ckpt, 16)))
         return WKV_EALIGN;
+    int64_t nseg = 1, per = 0;
+    const size_t need = delta_split_bytes(B, T, H, N, &nseg, &per);
+    if (workspace && (workspace_bytes < need || !aligned(workspace, 256))) return WKV_EWORKSPACE;
     float* errs = static_cast<float*>(ckpt);
     float* states = ckpt ? reinterpret_cast<float*>(static_cast<char*>(ckpt) + p.rows_bytes) : nullptr;
     const wkv::DeltaArgs a{B, T, H, HK, N, in_dtype == WKV_BF16, lengths, w, beta, r, k, v, o, s_in, s_out, errs, states};
-    return hip_status(wkv::launch_delta_fwd(a, stream));
+    return hip_status(run_delta_fwd(a, nseg, per, workspace, stream));
 }
 
 wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
@@ -764,22 +820,26 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
         !aligned(dr, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dw, 4) || !aligned(dbeta, 4) ||
         (s_in && !aligned(s_in, 16)) || (lengths && !aligned(lengths, 4)) || (ckpt && !aligned(ckpt, 16)))
         return WKV_EALIGN;
-    const size_t one = p.rows_bytes + p.states_bytes;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < (ckpt ? one : 2 * one)) return WKV_EWORKSPACE;
+    // lambda and the states' gradients; the recomputed errors and states; the scratch of a time split
+    const size_t one = p.rows_bytes + p.states_bytes, unsplit = ckpt ? one : 2 * one;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < unsplit) return WKV_EWORKSPACE;
+    int64_t nseg = 1, per = 0;
+    const size_t need = delta_split_bytes(B, T, H, N, &nseg, &per);
     char* ws = static_cast<char*>(workspace);
+    void* scratch = need > 0 && workspace_bytes >= unsplit + need ? ws + unsplit : nullptr;
     const bool bf = in_dtype == WKV_BF16;
     const char* saved = static_cast<const char*>(ckpt);
     if (ckpt == nullptr) {  // the errors and states, by a forward pass without outputs
         saved = ws + one;
         const wkv::DeltaArgs fa{B, T, H, HK, N, bf, lengths, w, beta, r, k, v, nullptr, s_in, nullptr,
                                 reinterpret_cast<float*>(ws + one), reinterpret_cast<float*>(ws + one + p.rows_bytes)};
-        const hipError_t e = wkv::launch_delta_fwd(fa, stream);
+        const hipError_t e = run_delta_fwd(fa, nseg, per, scratch, stream);
         if (e != hipSuccess) return hip_status(e);
     }
     const wkv::DeltaBwdArgs a{B, T, H, HK, N, bf, lengths, w, beta, r, k, go, reinterpret_cast<const float*>(saved),
                               reinterpret_cast<const float*>(saved + p.rows_bytes), ds_out, reinterpret_cast<float*>(ws),
                               reinterpret_cast<float*>(ws + p.rows_bytes), dr, dk, dv, dw, dbeta, ds_in};
-    return hip_status(wkv::launch_delta_bwd(a, stream));
+    return hip_status(run_delta_bwd(a, nseg, per, scratch, stream));
 }
 
 }  // extern "C"

@@ -50,6 +50,20 @@ constexpr int kCols = 16 * kWaves;
 constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
 template <typename T, int N>
 constexpr int kOcc = sizeof(T) * N > 256 ? 1 : 2;  // workgroups a compute unit has the LDS for
+// A sequence is split in time when there are at most kSplitMost workgroups' worth of pairs, into segments
+// of kSplitTiles tiles or more and about kSplitGroups workgroups in all.  8192 tokens in bf16, whole and split:
+// 8 groups 647 and 78 us, 32 671 and 156, 64 609 and 273, 128 604 and 443 (N = 128: 851 and 699); a training
+// call with 256 groups took 530 us whole and 570 split.  256 groups in all were slower (32: 175), 1024 no faster.
+#ifndef WKV_DELTA_SPLIT_MOST
+#define WKV_DELTA_SPLIT_MOST 128
+#endif
+#ifndef WKV_DELTA_SPLIT_TILES
+#define WKV_DELTA_SPLIT_TILES 4
+#endif
+#ifndef WKV_DELTA_SPLIT_GROUPS
+#define WKV_DELTA_SPLIT_GROUPS 512
+#endif
+constexpr int64_t kSplitMost = WKV_DELTA_SPLIT_MOST, kSplitTiles = WKV_DELTA_SPLIT_TILES, kSplitGroups = WKV_DELTA_SPLIT_GROUPS;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -423,6 +437,18 @@ __device__ __forceinline__ void prepare_block(int s, int l16, int g, const T (*K
     }
 }
 
+// A workgroup's place: (batch row, head) fastest, so that what shares rows of r, k and v runs together.
+struct Segment {
+    int64_t bh, cb, seg, begin, end;  // tokens [begin, end) of the sequence
+    __device__ __forceinline__ Segment(int64_t id, int64_t BH, int64_t blocks, int64_t nseg, int64_t per, int64_t T) {
+        bh = id % BH;
+        cb = id / BH % blocks;
+        seg = id / BH / blocks;
+        begin = seg * per * kTile;
+        end = seg == nseg - 1 ? T : (seg + 1) * per * kTile;
+    }
+};
+
 template <typename T, int N>
 struct FwdShared {
     T k[kTile][kRow<T, N>];
@@ -449,10 +475,16 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int l16 = lane & 15, g = lane >> 4;
     const int64_t BH = P.B * P.H;
-    const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
+    constexpr int64_t kBlocks = N / kCols;  // column blocks
+    const Segment at(blockIdx.x, BH, kOut || P.local == nullptr ? kBlocks : 2 * kBlocks, P.nseg, P.per, P.T);
+    const int64_t bh = at.bh, seg = at.seg;
+    const bool unit = at.cb >= kBlocks;  // columns of the identity: no values
+    if (unit && seg == 0) return;        // the first segment starts from the given state
+    const int64_t cb = unit ? at.cb - kBlocks : at.cb;
     const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
     const int64_t len = row_length(P.lengths, b, P.T);
-    const int64_t ks = P.HK * N, vs = P.H * N;  // row strides
+    const int64_t end = len < at.end ? len : at.end;  // of this segment's tokens
+    const int64_t ks = P.HK * N, vs = P.H * N;        // row strides
     const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
     const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
     const int64_t vo = b * P.T * vs + h * N + cb * kCols;
@@ -463,12 +495,16 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
     const int64_t scol = cb * kCols + 16 * wv + l16;  // of the state
     const int64_t ntile = (P.T + kTile - 1) / kTile;
 
+    const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
+                         : P.s_in != nullptr && seg == 0 ? P.s_in + bh * N * N : nullptr;
     f4 S[N / 16];
 #pragma unroll
     for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            S[c][q] = P.s_in != nullptr ? P.s_in[(bh * N + state_row(c, g, q)) * N + scol] : 0.f;
+        for (int q = 0; q < 4; ++q) {
+            const int row = state_row(c, g, q);
+            S[c][q] = unit ? (row == scol ? 1.f : 0.f) : first != nullptr ? first[row * N + scol] : 0.f;
+        }
 
     Staged<T, N> fk, fr;
     Staged<T, kCols> fv;
@@ -476,23 +512,23 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
     const auto fetch = [&](int64_t t) {
         fk.fetch(k, ks, t, len);
         if constexpr (kOut) fr.fetch(r, ks, t, len);
-        fv.fetch(v, vs, t, len);
+        fv.fetch(v, vs, t, unit ? 0 : len);
         fw.fetch(w, beta, P.H, t, len);
     };
-    fetch(0);
-    int64_t t0 = 0;
+    fetch(at.begin);
+    int64_t t0 = at.begin;
 #pragma unroll 1
-    for (; t0 < len; t0 += kTile) {
+    for (; t0 < end; t0 += kTile) {
         // else every address and comparison below is worked out before the loop and kept in registers
         asm volatile("" : "+v"(l16), "+v"(g));
         __syncthreads();  // the last tile's readers are done, and its outputs in place
-        if (kOut && t0 > 0) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
+        if (kOut && t0 > at.begin) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
         fk.put(sm.k);
         if constexpr (kOut) fr.put(sm.r);
         fv.put(sm.v);
         fw.put(sm.blk);
         __syncthreads();
-        if (t0 + kTile < len) fetch(t0 + kTile);
+        if (t0 + kTile < end) fetch(t0 + kTile);
         prepare_block<T, N, kOut, false>(wv, l16, g, sm.k, sm.r, sm.blk);
         if (P.states != nullptr) {
             float* st = P.states + (bh * ntile + t0 / kTile) * N * N + cb * kCols + 16 * wv;
@@ -538,15 +574,17 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(De
     }
     if constexpr (kOut) {
         __syncthreads();
-        if (t0 > 0) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
+        if (t0 > at.begin) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
         // whole tiles behind the row's length: zeros
-        for (int64_t t = t0 + threadIdx.x / 16; t < P.T; t += 16) store4(&o[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
+        for (int64_t t = t0 + threadIdx.x / 16; t < at.end; t += 16) store4(&o[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
     }
-    if (P.s_out != nullptr) {
+    float* last = !kOut && P.local != nullptr ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
+                  : P.s_out != nullptr && seg == P.nseg - 1 ? P.s_out + bh * N * N : nullptr;
+    if (last != nullptr) {
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) P.s_out[(bh * N + state_row(c, g, q)) * N + scol] = S[c][q];
+            for (int q = 0; q < 4; ++q) last[state_row(c, g, q) * N + scol] = S[c][q];
     }
 }
 
@@ -641,16 +679,24 @@ struct AdjShared {
     Blocks blk;
 };
 
-template <typename T, int N>
+// kOut false: a pass for what a segment does to the gradient of the state after it (DeltaBwdArgs::local).
+template <typename T, int N, bool kOut>
 __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kernel(DeltaBwdArgs P) {
     __shared__ AdjShared<T, N> sm;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int l16 = lane & 15, g = lane >> 4;
     const int64_t BH = P.B * P.H;
-    const int64_t bh = blockIdx.x % BH, cb = blockIdx.x / BH;
+    constexpr int64_t kBlocks = N / kCols;
+    // the pass over segments leaves out the first, which nothing comes before
+    const Segment at(blockIdx.x + (kOut ? 0 : BH * 2 * kBlocks), BH, kOut ? kBlocks : 2 * kBlocks, P.nseg, P.per, P.T);
+    const int64_t bh = at.bh, seg = at.seg;
+    const bool unit = at.cb >= kBlocks;
+    if (unit && seg == P.nseg - 1) return;  // the last segment starts from the given gradient
+    const int64_t cb = unit ? at.cb - kBlocks : at.cb;
     const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
     const int64_t len = row_length(P.lengths, b, P.T);
+    const int64_t end = len < at.end ? len : at.end;
     const int64_t ks = P.HK * N, vs = P.H * N;
     const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
     const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
@@ -662,44 +708,53 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
     const int64_t scol = cb * kCols + 16 * wv + l16;
     const int64_t ntile = (P.T + kTile - 1) / kTile;
 
+    const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
+                         : P.ds_out != nullptr && seg == P.nseg - 1 ? P.ds_out + bh * N * N : nullptr;
     f4 G[N / 16];
 #pragma unroll
     for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            G[c][q] = P.ds_out != nullptr ? P.ds_out[(bh * N + state_row(c, g, q)) * N + scol] : 0.f;
+        for (int q = 0; q < 4; ++q) {
+            const int row = state_row(c, g, q);
+            G[c][q] = unit ? (row == scol ? 1.f : 0.f) : first != nullptr ? first[row * N + scol] : 0.f;
+        }
 
-    const int64_t live = (len + kTile - 1) / kTile;  // tiles with a token of this row
-    for (int64_t t = live * kTile + threadIdx.x / 16; t < P.T; t += 16)
-        store4(&dv[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
+    const int64_t begin = at.begin / kTile;  // tiles of the segment with a token of this row: [begin, live)
+    const int64_t live = end > at.begin ? (end + kTile - 1) / kTile : begin;
+    if constexpr (kOut) {
+        for (int64_t t = live * kTile + threadIdx.x / 16; t < at.end; t += 16)
+            store4(&dv[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
+    }
     Staged<T, N> fk, fr;
     Staged<T, kCols> fg;
     Rates fw;
     const auto fetch = [&](int64_t t) {
         fk.fetch(k, ks, t, len);
         fr.fetch(r, ks, t, len);
-        fg.fetch(go, vs, t, len);
+        fg.fetch(go, vs, t, unit ? 0 : len);
         fw.fetch(w, beta, P.H, t, len);
     };
-    if (live > 0) fetch((live - 1) * kTile);
+    if (live > begin) fetch((live - 1) * kTile);
 #pragma unroll 1
-    for (int64_t tile = live - 1; tile >= 0; --tile) {
+    for (int64_t tile = live - 1; tile >= begin; --tile) {
         asm volatile("" : "+v"(l16), "+v"(g));  // as in the forward
         const int64_t t0 = tile * kTile;
         __syncthreads();
-        if (tile + 1 < live) Staged<T, kCols>::flush(sm.go, dv, vs, t0 + kTile, P.T);
+        if (kOut && tile + 1 < live) Staged<T, kCols>::flush(sm.go, dv, vs, t0 + kTile, P.T);
         fk.put(sm.k);
         fr.put(sm.r);
         fg.put(sm.go);
         fw.put(sm.blk);
         __syncthreads();
-        if (tile > 0) fetch(t0 - kTile);
+        if (tile > begin) fetch(t0 - kTile);
         prepare_block<T, N, true, true>(wv, l16, g, sm.k, sm.r, sm.blk);
-        float* gt = P.gstates + (bh * ntile + tile) * N * N + cb * kCols + 16 * wv;
+        if constexpr (kOut) {
+            float* gt = P.gstates + (bh * ntile + tile) * N * N + cb * kCols + 16 * wv;
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c)
+            for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N + l16] = G[c][q];
+                for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N + l16] = G[c][q];
+        }
         __syncthreads();
 #pragma unroll 1
         for (int s = kTile / kSub - 1; s >= 0; --s) {
@@ -719,6 +774,7 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
             const f4 y = mma16(att, d, put * kG);
             const f4 lam = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
             kc.add_outer(G, -since * lam);
+            if constexpr (!kOut) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) store1(&sm.go[tb + 4 * g + q][16 * wv + l16], lam[q]);
             const int64_t left = P.T - t0 - tb;
@@ -727,13 +783,17 @@ __global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kerne
                            left < kSub ? static_cast<int>(left) : kSub);
         }
     }
-    __syncthreads();
-    if (live > 0) Staged<T, kCols>::flush(sm.go, dv, vs, 0, P.T);
-    if (P.ds_in != nullptr) {
+    if constexpr (kOut) {
+        __syncthreads();
+        if (live > begin) Staged<T, kCols>::flush(sm.go, dv, vs, begin * kTile, P.T);
+    }
+    float* last = !kOut ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
+                  : P.ds_in != nullptr && seg == 0 ? P.ds_in + bh * N * N : nullptr;
+    if (last != nullptr) {
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) P.ds_in[(bh * N + state_row(c, g, q)) * N + scol] = G[c][q];
+            for (int q = 0; q < 4; ++q) last[state_row(c, g, q) * N + scol] = G[c][q];
     }
 }
 
@@ -775,13 +835,13 @@ struct GradShared {
 template <typename T, int N>
 __device__ void zero_tile(const DeltaBwdArgs& P, T* dr, T* dk, int64_t b, int64_t hk, int64_t t0) {
     const int64_t rows = P.T - t0 < kTile ? P.T - t0 : kTile, per = P.H / P.HK, ks = P.HK * N;
-    for (int64_t t = threadIdx.x / 16; t < rows; t += 16) {
+    for (int64_t t = threadIdx.x / 16; t < rows; t += blockDim.x / 16) {
         for (int c = threadIdx.x % 16 * 4; c < N; c += 64) {
             store4(&dr[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
             store4(&dk[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
         }
     }
-    for (int64_t i = threadIdx.x; i < rows * per; i += 64 * kWaves) {
+    for (int64_t i = threadIdx.x; i < rows * per; i += blockDim.x) {
         const int64_t at = (b * P.T + t0 + i / per) * P.H + hk * per + i % per;
         P.dw[at] = 0.f;
         P.dbeta[at] = 0.f;
@@ -1050,17 +1110,23 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
     }
 }
 
-// The same from bf16 inputs.  Here a wave owns 16 channels of r and k (N / 64 times) instead of 16 tokens:
-// it reads its rows of S0 and G once, splits them in registers, and takes the tile's 64 tokens of go,
-// lambda and e, split when they are staged, past them.  Phases between barriers:
+// The same from bf16 inputs.  Here a wave owns 16 channels of r and k instead of 16 tokens: it reads its
+// rows of S0 and G once, splits them in registers, and takes the tile's tokens of go, lambda and e, split
+// when they are staged, past them (eight waves; at N = 64 two of them share a slice, 32 tokens each).
+// Phases between barriers:
 //   1. stage k, r, go, and the three terms of e and lambda
-//   2. the 16 x 16 blocks (I, J), J <= I, of dA, dM and P: ten blocks dealt to the four waves;
-//      the products with S0 and G
+//   2. the products with S0 and G; the 16 x 16 blocks (I, J), J <= I, of dA, dM and P: ten blocks dealt
+//      to the waves
 //   3. dA, dM and their transposes, as hi + mid (dr and dk are rounded to bf16), to LDS over e and
 //      lambda, each lane's eight values where the lane that needs them reads them
 //   4. every wave: its channels of the products of k and r with all ten blocks; and the rates
+// The wave waits for its LDS reads more than for anything else, so the registers are kept to what four
+// waves a SIMD have (N = 64: 128) and chains of dependent products are taken in turn.
 // LDS rows are not padded (two workgroups a compute unit at N = 64): the 16-byte piece q of row t lies at
 // q ^ swizzle(t), so that 16 rows' pieces q meet 16 different bank groups.
+constexpr int kGradWaves = 8;
+constexpr int kGradThreads = 64 * kGradWaves;
+
 template <int N>
 struct GradShared16 {
     uint16_t k[kTile][N], r[kTile][N], go[kTile][N];
@@ -1074,7 +1140,7 @@ struct GradShared16 {
     float pre[kTile], suf[kTile], since[kTile], until[kTile];
     float total[kWaves];
     float rowsum[10][kSub], colsum[10][kSub];  // of beta_j P_ij over j, of P_ij over i
-    float withS[kWaves][kTile], withG[kWaves][kTile], inner[kWaves];
+    float withS[N / 16][kTile], withG[N / 16][kTile], inner[N / 16];
     float diag[kTile];                         // the crossing pairs inside the token's own block
     float rowv[kTile], colv[kTile];
 };
@@ -1101,8 +1167,8 @@ template <int N>
 __device__ __forceinline__ void stage_rows(uint16_t (*dst)[N], const uint16_t* base, int64_t stride, int64_t t0, int64_t end) {
     constexpr int kRowVecs = N / 8;
 #pragma unroll
-    for (int i = 0; i < kTile * kRowVecs / (64 * kWaves); ++i) {
-        const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+    for (int i = 0; i < kTile * kRowVecs / kGradThreads; ++i) {
+        const int q = static_cast<int>(threadIdx.x) + i * kGradThreads;
         const int t = q / kRowVecs, c = q % kRowVecs * 8;
         const u32x4 x = t0 + t < end ? *reinterpret_cast<const u32x4*>(base + (t0 + t) * stride + c) : u32x4{0, 0, 0, 0};
         *reinterpret_cast<u32x4*>(&dst[t][swizzled<N>(t, c)]) = x;
@@ -1120,8 +1186,8 @@ template <int N>
 __device__ __forceinline__ void stage_terms(uint16_t (*dst)[kTile][N], const float* base, int64_t stride, int64_t t0, int64_t end) {
     constexpr int kRowVecs = N / 8;
 #pragma unroll
-    for (int i = 0; i < kTile * kRowVecs / (64 * kWaves); ++i) {
-        const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
+    for (int i = 0; i < kTile * kRowVecs / kGradThreads; ++i) {
+        const int q = static_cast<int>(threadIdx.x) + i * kGradThreads;
         const int t = q / kRowVecs, c = q % kRowVecs * 8;
         f4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
         if (t0 + t < end) {
@@ -1135,25 +1201,18 @@ __device__ __forceinline__ void stage_terms(uint16_t (*dst)[kTile][N], const flo
     }
 }
 
-// a b of two factors in three terms each: all but the products below 2^-24 of the whole
-__device__ __forceinline__ f4 mma_terms(const bf8 (&a)[3], const bf8 (&b)[3], f4 c) {
-    c = mfma32(a[2], b[0], c);
-    c = mfma32(a[0], b[2], c);
-    c = mfma32(a[1], b[1], c);
-    c = mfma32(a[1], b[0], c);
-    c = mfma32(a[0], b[1], c);
-    return mfma32(a[0], b[0], c);
-}
-__device__ __forceinline__ f4 mma_terms(const bf8 (&a)[3], bf8 b, f4 c) {
-    c = mfma32(a[2], b, c);
-    c = mfma32(a[1], b, c);
-    return mfma32(a[0], b, c);
+// Step i of a b for two factors in three terms each: all but the products below 2^-24 of the whole, the
+// smallest first.
+__device__ __forceinline__ f4 mma_step(int i, const bf8 (&a)[3], const bf8 (&b)[3], f4 c) {
+    constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+    return mfma32(a[kA[i]], b[kB[i]], c);
 }
 
 template <int N>
-__global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_kernel(DeltaBwdArgs P) {
+__global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_kernel(DeltaBwdArgs P) {
     __shared__ GradShared16<N> sm;
-    constexpr int NK = N / kCols;  // 16-channel slices a wave owns
+    constexpr int NS = N / 16;               // slices of 16 channels
+    constexpr int NX = 4 * NS / kGradWaves;  // token blocks a wave takes of its slice
     constexpr int NM = N / 32;
     int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1172,11 +1231,10 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
     }
     stage_rows<N>(sm.k, static_cast<const uint16_t*>(P.k) + ko, ks, t0, len);
     stage_rows<N>(sm.r, static_cast<const uint16_t*>(P.r) + ko, ks, t0, len);
-    f4 drT[NK][4], dkT[NK][4];  // [slice][token block]: channels 4 g .. 4 g + 3 of token l16
+    const int slice = wv % NS, c0 = 16 * slice, X0 = wv / NS * NX;
+    f4 drT[NX], dkT[NX];  // of token block X0 + x: channels c0 + 4 g .. + 3 of token l16
 #pragma unroll
-    for (int c = 0; c < NK; ++c)
-#pragma unroll
-        for (int X = 0; X < 4; ++X) drT[c][X] = dkT[c][X] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < NX; ++x) drT[x] = dkT[x] = f4{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll 1
     for (int64_t h = hk * per; h < (hk + 1) * per; ++h) {
@@ -1189,37 +1247,110 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
         stage_terms<N>(sm.lam, P.lambda + vo, vs, t0, len);
         if (threadIdx.x < kTile) {  // one wave: the decays of its 64 tokens
             const int64_t t = t0 + threadIdx.x;
-            sm.w[lane] = t < len ? P.w[(b * P.T + t) * P.H + h] * kLog2e : 0.f;
-            sm.beta[lane] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
-            float pre = 0.f, suf = 0.f, total[kWaves], before = 0.f, after = 0.f;
-#pragma unroll
-            for (int i = 0; i < kTile; ++i) {
-                const float wi = sm.w[i];
-                if (i % kSub == 0) total[i / kSub] = 0.f;
-                total[i / kSub] += wi;
-                if (i / kSub == g) {
-                    pre += i % kSub <= l16 ? wi : 0.f;
-                    suf += i % kSub > l16 ? wi : 0.f;
-                }
-            }
+            const float wt = t < len ? P.w[(b * P.T + t) * P.H + h] * kLog2e : 0.f;
+            // sums in the token's block, through it and after it, by shifts along the rows of 16 lanes
+            float pre = wt, suf = dpp<0x101>(wt);
+            pre += dpp<0x111>(pre);
+            suf += dpp<0x101>(suf);
+            pre += dpp<0x112>(pre);
+            suf += dpp<0x102>(suf);
+            pre += dpp<0x114>(pre);
+            suf += dpp<0x104>(suf);
+            pre += dpp<0x118>(pre);
+            suf += dpp<0x108>(suf);
+            float before = 0.f, after = 0.f;
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) {
-                before += i < g ? total[i] : 0.f;
-                after += i > g ? total[i] : 0.f;
+                const float total = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pre), kSub * i + kSub - 1));
+                before += i < g ? total : 0.f;
+                after += i > g ? total : 0.f;
             }
+            sm.w[lane] = wt;
+            sm.beta[lane] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
             sm.pre[lane] = pre;
             sm.suf[lane] = suf;
             sm.since[lane] = ex2(-(before + pre));
             sm.until[lane] = ex2(-(suf + after));
-            if (l16 == 0) sm.total[g] = g == 0 ? total[0] : g == 1 ? total[1] : g == 2 ? total[2] : total[3];
+            if (l16 == kSub - 1) sm.total[g] = pre;
         }
         __syncthreads();
 
-        // ---- the 16 x 16 blocks: rows i = 4 g + q of block I, column j = l16 of block J
-        f4 da[3], dm[3];
+        // ---- products with the states before and after the tile, for this wave's channels and tokens
+        {
+            const int64_t at0 = ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
+            const float* S0 = P.states + at0;
+            const float* G1 = P.gstates + at0;
+            float inner = 0.f;
+            f4 sg[NX], sl[NX], ge[NX];
 #pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            const int id = wv + 4 * n;
+            for (int x = 0; x < NX; ++x) sg[x] = sl[x] = ge[x] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const f4 sa = load4(S0 + 32 * m), sb = load4(S0 + 32 * m + 4);
+                const f4 ga = load4(G1 + 32 * m), gb = load4(G1 + 32 * m + 4);
+                const int v = 32 * m + 8 * g;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) inner = fmaf(sa[q], ga[q], fmaf(sb[q], gb[q], inner));
+                bf8 s3[3];
+                split8(sa, sb, s3);
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int t = kSub * (X0 + x) + l16;
+                    const bf8 la[3] = {row8<N>(sm.lam[0], t, v), row8<N>(sm.lam[1], t, v), row8<N>(sm.lam[2], t, v)};
+                    const bf8 go = row8<N>(sm.go, t, v);
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        sl[x] = mma_step(i, s3, la, sl[x]);
+                        if (i % 2) sg[x] = mfma32(s3[2 - i / 2], go, sg[x]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // more of the reads at once would spill
+                }
+                bf8 g3[3];
+                split8(ga, gb, g3);
+#pragma unroll
+                for (int x = 0; x < NX; x += 2) {
+                    const int t = kSub * (X0 + x) + l16;
+                    const bf8 e[3] = {row8<N>(sm.e[0], t, v), row8<N>(sm.e[1], t, v), row8<N>(sm.e[2], t, v)};
+                    const bf8 e2[3] = {row8<N>(sm.e[0], t + kSub, v), row8<N>(sm.e[1], t + kSub, v),
+                                       row8<N>(sm.e[2], t + kSub, v)};
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        ge[x] = mma_step(i, g3, e, ge[x]);
+                        ge[x + 1] = mma_step(i, g3, e2, ge[x + 1]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                const int t = kSub * (X0 + x) + l16, at = swizzled<N>(t, c0 + 4 * g);
+                const f4 rr = load4(&sm.r[t][at]), kk = load4(&sm.k[t][at]);
+                const float since = sm.since[t], until = sm.until[t], put = until * sm.beta[t];
+                float withS = 0.f, withG = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    withS += rr[q] * sg[x][q] - kk[q] * sl[x][q];
+                    withG += kk[q] * ge[x][q];
+                }
+                drT[x] += since * sg[x];
+                dkT[x] += put * ge[x] - since * sl[x];
+                withS = sum_rows(since * withS);
+                withG = sum_rows(until * withG);
+                if (g == 0) {
+                    sm.withS[slice][t] = withS;
+                    sm.withG[slice][t] = withG;
+                }
+            }
+            inner = sum_lanes(inner, 64);
+            if (lane == 0) sm.inner[slice] = inner;
+        }
+        asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- the 16 x 16 blocks: rows i = 4 g + q of block I, column j = l16 of block J
+        f4 da[2], dm[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int id = wv + kGradWaves * n;
             if (id >= 10) continue;
             __builtin_amdgcn_sched_barrier(0);
             const int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0, J = id - I * (I + 1) / 2;
@@ -1231,12 +1362,18 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
                 const bf8 e[3] = {row8<N>(sm.e[0], tj, c), row8<N>(sm.e[1], tj, c), row8<N>(sm.e[2], tj, c)};
                 const bf8 la[3] = {row8<N>(sm.lam[0], ti, c), row8<N>(sm.lam[1], ti, c), row8<N>(sm.lam[2], ti, c)};
                 const bf8 go = row8<N>(sm.go, ti, c), kj = row8<N>(sm.k, tj, c);
+                const bf8 ri = row8<N>(sm.r, ti, c), ki = row8<N>(sm.k, ti, c);
+                le = mma_step(0, la, e, le);
                 ae = mfma32(go, e[2], ae);
-                rk = mfma32(row8<N>(sm.r, ti, c), kj, rk);
+                le = mma_step(1, la, e, le);
                 ae = mfma32(go, e[1], ae);
-                kk = mfma32(row8<N>(sm.k, ti, c), kj, kk);
+                le = mma_step(2, la, e, le);
                 ae = mfma32(go, e[0], ae);
-                le = mma_terms(la, e, le);
+                le = mma_step(3, la, e, le);
+                rk = mfma32(ri, kj, rk);
+                le = mma_step(4, la, e, le);
+                kk = mfma32(ki, kj, kk);
+                le = mma_step(5, la, e, le);
                 __builtin_amdgcn_sched_barrier(0);
             }
             float mid = sm.suf[tj];
@@ -1295,67 +1432,14 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
             }
         }
 
-        // ---- products with the states before and after the tile, for this wave's channels
-        float withS[4] = {0.f, 0.f, 0.f, 0.f}, withG[4] = {0.f, 0.f, 0.f, 0.f}, inner = 0.f;
-#pragma unroll
-        for (int c = 0; c < NK; ++c) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int c0 = 16 * (wv + kWaves * c);
-            const float* S0 = P.states + ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
-            const float* G1 = P.gstates + ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
-            f4 sg[4], sl[4], ge[4];
-#pragma unroll
-            for (int X = 0; X < 4; ++X) sg[X] = sl[X] = ge[X] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const f4 sa = load4(S0 + 32 * m), sb = load4(S0 + 32 * m + 4);
-                const f4 ga = load4(G1 + 32 * m), gb = load4(G1 + 32 * m + 4);
-                bf8 s3[3], g3[3];
-                split8(sa, sb, s3);
-                split8(ga, gb, g3);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) inner = fmaf(sa[q], ga[q], fmaf(sb[q], gb[q], inner));
-#pragma unroll
-                for (int X = 0; X < 4; ++X) {
-                    const int t = kSub * X + l16, v = 32 * m + 8 * g;
-                    const bf8 e[3] = {row8<N>(sm.e[0], t, v), row8<N>(sm.e[1], t, v), row8<N>(sm.e[2], t, v)};
-                    const bf8 la[3] = {row8<N>(sm.lam[0], t, v), row8<N>(sm.lam[1], t, v), row8<N>(sm.lam[2], t, v)};
-                    sg[X] = mma_terms(s3, row8<N>(sm.go, t, v), sg[X]);
-                    sl[X] = mma_terms(s3, la, sl[X]);
-                    ge[X] = mma_terms(g3, e, ge[X]);
-                    __builtin_amdgcn_sched_barrier(0);  // the reads of all four blocks at once would spill
-                }
-            }
-#pragma unroll
-            for (int X = 0; X < 4; ++X) {
-                const int t = kSub * X + l16, at = swizzled<N>(t, c0 + 4 * g);
-                const f4 rr = load4(&sm.r[t][at]), kk = load4(&sm.k[t][at]);
-                const float since = sm.since[t], until = sm.until[t], put = until * sm.beta[t];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    withS[X] += since * (rr[q] * sg[X][q] - kk[q] * sl[X][q]);
-                    withG[X] += until * kk[q] * ge[X][q];
-                }
-                drT[c][X] += since * sg[X];
-                dkT[c][X] += put * ge[X] - since * sl[X];
-            }
-        }
-#pragma unroll
-        for (int X = 0; X < 4; ++X) {
-            const float a = sum_rows(withS[X]), d = sum_rows(withG[X]);
-            if (g == 0) {
-                sm.withS[wv][kSub * X + l16] = a;
-                sm.withG[wv][kSub * X + l16] = d;
-            }
-        }
-        inner = sum_lanes(inner, 64);
-        if (lane == 0) sm.inner[wv] = inner;
         __syncthreads();  // e and lambda are read; the sums are in place
 
+        asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
+        __builtin_amdgcn_sched_barrier(0);
         // ---- dA, dM and their transposes as right operands
 #pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            const int id = wv + 4 * n;
+        for (int n = 0; n < 2; ++n) {
+            const int id = wv + kGradWaves * n;
             if (id >= 10) continue;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -1373,7 +1457,7 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
         float rowv = 0.f, colv = 0.f, sS = 0.f, sG = 0.f;
         if (threadIdx.x < kTile) {  // token `lane`, of block g
             float dbeta = 0.f;
-            for (int i = 0; i < kWaves; ++i) {
+            for (int i = 0; i < NS; ++i) {
                 sS += sm.withS[i][lane];
                 sG += sm.withG[i][lane];
             }
@@ -1392,7 +1476,8 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
         __syncthreads();
         if (threadIdx.x < kTile) {
             // blocks' totals: rows that pair with S0, columns that pair with G, and whole blocks (I, J)
-            float c = sm.inner[0] + sm.inner[1] + sm.inner[2] + sm.inner[3];
+            float c = 0.f;
+            for (int i = 0; i < NS; ++i) c += sm.inner[i];
             c *= sm.since[kTile - 1];
             const float rowS = sum16(sS), colG = sum16(sm.beta[lane] * sG);
 #pragma unroll
@@ -1413,41 +1498,82 @@ __global__ void __launch_bounds__(64 * kWaves, (N == 64 ? 2 : 1)) delta_grad16_k
             if (t0 + lane < P.T) P.dw[(b * P.T + t0 + lane) * P.H + h] = t0 + lane < len ? -c : 0.f;
         }
 
-        // ---- k and r times the blocks, for this wave's channels
+        asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- k and r times the blocks, for this wave's channels and tokens
 #pragma unroll
-        for (int c = 0; c < NK; ++c) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int c0 = 16 * (wv + kWaves * c);
-            bf8 kT[4], rT[4];
+        for (int X = 0; X < 4; ++X) {
+            const bf8 kT = col_twice<N>(sm.k, kSub * X, c0, l16, g), rT = col_twice<N>(sm.r, kSub * X, c0, l16, g);
+            const auto at = [&](int I, int J, int w) { return raw8(sm.da[I * (I + 1) / 2 + J][w][lane]); };
 #pragma unroll
-            for (int X = 0; X < 4; ++X) {
-                kT[X] = col_twice<N>(sm.k, kSub * X, c0, l16, g);
-                rT[X] = col_twice<N>(sm.r, kSub * X, c0, l16, g);
-            }
-#pragma unroll
-            for (int I = 0; I < 4; ++I) {
-#pragma unroll
-                for (int J = 0; J <= I; ++J) {
-                    const int id = I * (I + 1) / 2 + J;
-                    const auto at = [&](int w) { return raw8(sm.da[id][w][lane]); };
-                    dkT[c][J] = mfma32(rT[I], at(0), dkT[c][J]);
-                    drT[c][I] = mfma32(kT[J], at(2), drT[c][I]);
-                    dkT[c][J] = mfma32(kT[I], at(1), dkT[c][J]);
-                    dkT[c][I] = mfma32(kT[J], at(3), dkT[c][I]);
+            for (int x = 0; x < NX; ++x) {
+                const int Y = X0 + x;
+                if (X <= Y) {  // as j, for the rows of block Y
+                    drT[x] = mfma32(kT, at(Y, X, 2), drT[x]);
+                    dkT[x] = mfma32(kT, at(Y, X, 3), dkT[x]);
+                }
+                if (X >= Y) {  // as i, for the columns of block Y
+                    dkT[x] = mfma32(rT, at(X, Y, 0), dkT[x]);
+                    dkT[x] = mfma32(kT, at(X, Y, 1), dkT[x]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
-    for (int X = 0; X < 4; ++X) {
-        const int64_t t = t0 + kSub * X + l16;
+    for (int x = 0; x < NX; ++x) {
+        const int64_t t = t0 + kSub * (X0 + x) + l16;
         if (t >= P.T) continue;
+        store4(&dr[t * ks + c0 + 4 * g], drT[x]);
+        store4(&dk[t * ks + c0 + 4 * g], dkT[x]);
+    }
+}
+
+// ---- time split ---------------------------------------------------------------------------------
+// A segment maps the state before it linearly: S -> M S + L.  Both are found by walking the segment
+// without outputs, L from a zero state and M from the identity without values (its columns are 2 N
+// independent ones, N / 8 waves).  Then the segments' start states follow one from the other, and all
+// segments are walked at once.  The adjoint walk does the same from the other end.
+//
+// One workgroup per (pair, 16 columns); wave w owns rows 16 w .. of the product and the columns meet
+// in LDS.  M_p and L_p are read before the state they act on is known.
+template <int N>
+__global__ void __launch_bounds__(4 * N) delta_chain_kernel(DeltaChainArgs P) {
+    __shared__ float x[N][kSub + 1];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+    const int64_t bh = blockIdx.x % P.BH, col = blockIdx.x / P.BH * 16 + l16;
+    const int row = 16 * wv + 4 * g;  // this lane's four rows
+    f4 s;
 #pragma unroll
-        for (int c = 0; c < NK; ++c) {
-            const int64_t at = t * ks + 16 * (wv + kWaves * c) + 4 * g;
-            store4(&dr[at], drT[c][X]);
-            store4(&dk[at], dkT[c][X]);
+    for (int q = 0; q < 4; ++q) s[q] = P.first != nullptr ? P.first[(bh * N + row + q) * N + col] : 0.f;
+    for (int64_t n = 0; n < P.nseg; ++n) {
+        const int64_t seg = P.reverse ? P.nseg - 1 - n : n;
+        float* to = P.starts + (bh * P.nseg + seg) * N * N;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) to[(row + q) * N + col] = s[q];
+        if (n == P.nseg - 1) break;
+        const float* L = P.local + (bh * P.nseg + seg) * 2 * N * N;
+        f4 next;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) next[q] = L[(row + q) * N + col];
+        if (n > 0) {  // the first segment's local end is its end
+            const float* M = L + N * N + (16 * wv + l16) * N + 4 * g;
+            f4 m[N / 16];
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) m[c] = load4(M + 16 * c);
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[row + q][l16] = s[q];
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c) {
+                f4 b;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = x[16 * c + 4 * g + q][l16];
+                next = mma16(m[c], b, next);
+            }
         }
+        s = next;
     }
 }
 
@@ -1458,7 +1584,8 @@ hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)),
                            dim3(64 * kWaves), 0, stream, a);
     } else {
-        const dim3 grid(static_cast<unsigned>(a.B * a.H * (N / kCols)));
+        const int64_t blocks = a.B * a.H * (N / kCols);
+        const dim3 grid(static_cast<unsigned>(a.local != nullptr ? 2 * blocks * (a.nseg - 1) : blocks * a.nseg));
         if (a.o != nullptr) {
             hipLaunchKernelGGL((delta_fwd_kernel<T, N, true>), grid, dim3(64 * kWaves), 0, stream, a);
         } else {
@@ -1470,14 +1597,20 @@ hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
 
 template <typename T, int N>
 hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, N>), dim3(static_cast<unsigned>(a.B * a.H * (N / kCols))),
-                       dim3(64 * kWaves), 0, stream, a);
+    const int64_t blocks = a.B * a.H * (N / kCols);
+    if (a.local != nullptr) {  // what the segments do, for the chain
+        hipLaunchKernelGGL((delta_adjoint_kernel<T, N, false>), dim3(static_cast<unsigned>(2 * blocks * (a.nseg - 1))),
+                           dim3(64 * kWaves), 0, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((delta_adjoint_kernel<T, N, true>), dim3(static_cast<unsigned>(blocks * a.nseg)), dim3(64 * kWaves),
+                       0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ntile = (a.T + kTile - 1) / kTile;
     const dim3 grid(static_cast<unsigned>(a.B * a.HK * ntile));
     if constexpr (std::is_same_v<T, uint16_t>) {
-        hipLaunchKernelGGL((delta_grad16_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
+        hipLaunchKernelGGL((delta_grad16_kernel<N>), grid, dim3(kGradThreads), 0, stream, a);
     } else {
         hipLaunchKernelGGL((delta_grad_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
     }
@@ -1485,6 +1618,26 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
+
+int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
+    const int64_t work = BH * (N / kCols), tiles = (T + kTile - 1) / kTile;
+    *per = tiles;
+    if (work < 1 || work > kSplitMost || tiles < 2 * kSplitTiles) return 1;
+    int64_t nseg = kSplitGroups / work;
+    if (nseg > tiles / kSplitTiles) nseg = tiles / kSplitTiles;
+    *per = (tiles + nseg - 1) / nseg;
+    return (tiles + *per - 1) / *per;
+}
+
+hipError_t launch_delta_chain(const DeltaChainArgs& a, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(a.BH * (a.N / 16)));
+    if (a.N == 64) {
+        hipLaunchKernelGGL(delta_chain_kernel<64>, grid, dim3(256), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL(delta_chain_kernel<128>, grid, dim3(512), 0, stream, a);
+    }
+    return hipGetLastError();
+}
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream) {
     if (a.bf16) return a.N == 64 ? launch_fwd<uint16_t, 64>(a, stream) : launch_fwd<uint16_t, 128>(a, stream);

@@ -256,6 +256,12 @@ struct DeltaArgs {
     float* s_out;             // [B, H, N, N] or NULL
     float* errs;              // [B, T, H, N] the errors e_t, or NULL
     float* states;            // [B, H, ceil(T / 64), N, N] the state before every 64 tokens, or NULL
+    // time split: nseg > 1 segments of `per` 64-token tiles a sequence, each by workgroups of its own
+    int64_t nseg = 1, per = 0;
+    const float* starts = nullptr;  // [B H, nseg, N, N] the segments' start states, in place of s_in
+    float* local = nullptr;         // [B H, nseg, 2, N, N]: a pass for what each segment but the last does to a state:
+                                    // its end state from zero (the first segment: from s_in), and the end states
+                                    // from the columns of the identity without its values
 };
 
 struct DeltaBwdArgs {
@@ -278,7 +284,26 @@ struct DeltaBwdArgs {
     float* dw;                // [B, T, H]
     float* dbeta;
     float* ds_in;             // [B, H, N, N] or NULL
+    // time split, as DeltaArgs, from the last segment: starts holds the gradients of the states after the
+    // segments, local those before each segment but the first
+    int64_t nseg = 1, per = 0;
+    const float* starts = nullptr;
+    float* local = nullptr;
 };
+
+// The states at the segments' starts from what the segments do (DeltaArgs::local): x_0 = first,
+// x_1 = its local end, x_{p+1} = M_p x_p + L_p; reverse: the same from the last segment.
+struct DeltaChainArgs {
+    int64_t BH, N, nseg;
+    bool reverse;
+    const float* first;  // [B H, N, N] or NULL (zero)
+    const float* local;
+    float* starts;
+};
+
+hipError_t launch_delta_chain(const DeltaChainArgs& a, hipStream_t stream);
+// segments for a time split of BH pairs over T tokens (1: no split), *per 64-token tiles each
+int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per);
 
 // gated delta rule (wkv_delta.hip)
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream);

@@ -773,11 +773,12 @@ def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=No
 
 
 def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_state_out=None, need_state_grad=False,
-                   ckpt=None, workspace=None, bind=False):
+                   ckpt=None, workspace=None, split=True, bind=False):
     """Gradients of sum <go, o> + <grad_state_out, S_T> for (o, S_T) = delta_forward(w, beta, r, k, v,
     lengths=lengths, state_in=state_in, return_state=True): (dr, dk, dv, dw, dbeta, ds_in), dr, dk, dv
     in r's dtype (those of a key head summed over its value heads), dw, dbeta [B, T, H] float32, ds_in
-    [B, H, N, N] float32 or None.  go: [B, T, H N] in r's dtype.  ckpt: None or what the forward wrote."""
+    [B, H, N, N] float32 or None.  go: [B, T, H N] in r's dtype.  ckpt: None or what the forward wrote.  split as in
+    delta_forward."""
     B, T, H, HK, N = _delta_inputs(w, beta, r, k, v, lengths)
     dev = r.device
     _need(go, "go", r.dtype, (B, T, H * N), dev)
@@ -793,11 +794,13 @@ def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_st
         _need(ckpt, "ckpt", torch.uint8, None, dev)
         if ckpt.numel() < delta_ckpt_bytes(B, T, H, N):
             raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {delta_ckpt_bytes(B, T, H, N)}")
-    nbytes = int(lib.wkv_delta_backward_workspace_bytes(B, T, H, HK, N, 1 if ckpt is not None else 0))
+    flags = (1 if ckpt is not None else 0) | (0 if split else 2)  # WKV_WS_HAVE_CKPT, WKV_WS_NO_SPLIT
+    nbytes = int(lib.wkv_delta_backward_workspace_bytes(B, T, H, HK, N, flags))
     workspace = _scratch(workspace, nbytes, dev)
+    # without split the call is told only the unsplit size, so it never splits
     args = (B, T, H, HK, N, _DT[r.dtype], _p(lengths), _p(w), _p(beta), _p(r), _p(k), _p(v), _p(go), _p(state_in),
             _p(grad_state_out), _p(dr), _p(dk), _p(dv), _p(dw), _p(dbeta), _p(ds), _p(ckpt), _p(workspace),
-            _bytes_of(workspace), _stream(dev))
+            _bytes_of(workspace) if split else nbytes, _stream(dev))
     return _launch_on(dev, bind, "wkv_delta_backward", lib.wkv_delta_backward, args, (dr, dk, dv, dw, dbeta, ds), locals())
 
 

@@ -292,3 +292,43 @@ def test_other_stream():
         o2, S2 = O.delta_forward(*(d[n] for n in ("w", "beta", "r", "k", "v")), state_in=d["S0"], return_state=True)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+SPLIT = [(1, 1000, 2, 1, 64), (1, 700, 1, 1, 128), (2, 515, 2, 2, 64)]  # sequences split in time
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", SPLIT, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("state", [False, True], ids=["zero", "state"])
+def test_time_split(shape, dtype, state):
+    """The split and the whole walk, forward (with and without a ckpt) and backward, within the bounds."""
+    O = ops()
+    B, T, H, HK, N = shape
+    assert O.L.lib().wkv_delta_forward_workspace_bytes(B, T, H, HK, N) > 0
+    p = problem(*shape, dtype, seed=20 + sum(shape), state=state, wmax=0.05)
+    for split in (True, False):
+        check_fwd(p, split=split)
+        ck = O.new_delta_ckpt(B, T, H, N, DEV)
+        check_fwd(p, split=split, ckpt=ck)
+    *ref, mw, mb = ref_bwd(p)
+    for kw in (dict(ckpt=ck), dict(split=False), dict()):
+        for n, g, r, s in zip(("dr", "dk", "dv", "dw", "dbeta", "dS0"), run_bwd(p, **kw), ref, (None, None, None, mw, mb, None)):
+            check(n, g, r, 2 * eps_of(p), s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[1000, 0, 257], [256, 512, 1], [255, 999, 640]])
+def test_time_split_lengths(dtype, lengths):
+    """Rows that end before, at and inside a segment; what lies behind them is NaN."""
+    p = problem(3, 1000, 2, 1, 64, dtype, seed=30, wmax=0.05)
+    for b, n in enumerate(lengths):
+        for name in ("w", "beta", "r", "k", "v", "go"):
+            p[name][b, n:] = float("nan")
+    q = {n: torch.nan_to_num(x) if isinstance(x, torch.Tensor) else x for n, x in p.items()}
+    o, S = run_fwd(p, lengths)
+    ro, rS = ref_fwd(q, lengths)
+    check("o", o, ro, eps_of(p))
+    check("S", S, rS, eps_of(p))
+    *ref, mw, mb = ref_bwd(q, lengths)
+    for n, g, r, s in zip(("dr", "dk", "dv", "dw", "dbeta", "dS0"), run_bwd(p, lengths), ref, (None, None, None, mw, mb, None)):
+        check(n, g, r, 2 * eps_of(p), s)
