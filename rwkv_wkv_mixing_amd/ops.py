@@ -19,11 +19,22 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (0.1 us against 2)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(dev):
+    if _raw_stream is not None and dev.index is not None:
+        return ctypes.c_void_p(_raw_stream(dev.index))
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _need(t, name, dtype=None, shape=None, device=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (device is None or t.device == device)
+            and (dtype is None or (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype))
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -674,6 +685,11 @@ class Wkv6Function(torch.autograd.Function):
         return dw, du, dr.to(r.dtype), dk.to(k.dtype), dv.to(v.dtype), ds
 
 
+def _at(t):
+    """A tensor's address as a plain number, which the calls take as they take _p's."""
+    return None if t is None else t.data_ptr()
+
+
 def _delta_shape(w, r, v):
     """(B, T, H, HK, N) of a delta-rule call from w [B, T, H], r [B, T, HK N], v [B, T, H N]."""
     if w.dim() != 3 or r.dim() != 3 or v.dim() != 3:
@@ -703,7 +719,7 @@ def _delta_inputs(w, beta, r, k, v, lengths):
 
 
 def _bytes_of(t):
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _scratch(workspace, nbytes, dev):
@@ -717,13 +733,18 @@ def _scratch(workspace, nbytes, dev):
 
 
 def _launch_on(dev, bind, name, fn, args, result, scope):
-    """_launch with dev the current device, which the library's calls run on."""
-    if dev.index == torch.cuda.current_device():
+    """_launch with dev the current device, which the library's calls run on.  scope: what a BoundCall
+    keeps alive (bind only)."""
+    if dev.index == _current_device():
+        if not bind:
+            L.check(name, fn(*args))
+            return result
         return _launch(bind, name, fn, args, result, scope)
     if bind:
         raise ValueError(f"bind needs the tensors' device {dev} to be the current one")
     with torch.cuda.device(dev):
-        return _launch(bind, name, fn, args, result, scope)
+        L.check(name, fn(*args))
+    return result
 
 
 def delta_ckpt_bytes(B: int, T: int, H: int, N: int) -> int:
@@ -750,7 +771,7 @@ def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=No
     B, T, H, HK, N = _delta_inputs(w, beta, r, k, v, lengths)
     dev = r.device
     if out is None:
-        out = torch.empty((B, T, H * N), dtype=r.dtype, device=dev)
+        out = torch.empty_like(v)
     else:
         _need(out, "out", r.dtype, (B, T, H * N), dev)
     if state_in is not None:
@@ -766,10 +787,10 @@ def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=No
             raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {delta_ckpt_bytes(B, T, H, N)}")
     nws = int(lib.wkv_delta_forward_workspace_bytes(B, T, H, HK, N)) if split else 0
     workspace = _scratch(workspace, nws, dev) if nws else None
-    args = (B, T, H, HK, N, _DT[r.dtype], _p(lengths), _p(w), _p(beta), _p(r), _p(k), _p(v), _p(out), _p(state_in),
-            _p(state_out), _p(ckpt), _p(workspace), _bytes_of(workspace) if nws else 0, _stream(dev))
+    args = (B, T, H, HK, N, _DT[r.dtype], _at(lengths), _at(w), _at(beta), _at(r), _at(k), _at(v), _at(out), _at(state_in),
+            _at(state_out), _at(ckpt), _at(workspace), _bytes_of(workspace) if nws else 0, _stream(dev))
     return _launch_on(dev, bind, "wkv_delta_forward", lib.wkv_delta_forward, args,
-                      (out, state_out) if return_state else out, locals())
+                      (out, state_out) if return_state else out, locals() if bind else None)
 
 
 def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_state_out=None, need_state_grad=False,
@@ -798,10 +819,10 @@ def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_st
     nbytes = int(lib.wkv_delta_backward_workspace_bytes(B, T, H, HK, N, flags))
     workspace = _scratch(workspace, nbytes, dev)
     # without split the call is told only the unsplit size, so it never splits
-    args = (B, T, H, HK, N, _DT[r.dtype], _p(lengths), _p(w), _p(beta), _p(r), _p(k), _p(v), _p(go), _p(state_in),
-            _p(grad_state_out), _p(dr), _p(dk), _p(dv), _p(dw), _p(dbeta), _p(ds), _p(ckpt), _p(workspace),
+    args = (B, T, H, HK, N, _DT[r.dtype], _at(lengths), _at(w), _at(beta), _at(r), _at(k), _at(v), _at(go), _at(state_in),
+            _at(grad_state_out), _at(dr), _at(dk), _at(dv), _at(dw), _at(dbeta), _at(ds), _at(ckpt), _at(workspace),
             _bytes_of(workspace) if split else nbytes, _stream(dev))
-    return _launch_on(dev, bind, "wkv_delta_backward", lib.wkv_delta_backward, args, (dr, dk, dv, dw, dbeta, ds), locals())
+    return _launch_on(dev, bind, "wkv_delta_backward", lib.wkv_delta_backward, args, (dr, dk, dv, dw, dbeta, ds), locals() if bind else None)
 
 
 class DeltaFunction(torch.autograd.Function):
@@ -875,14 +896,14 @@ def head_norm(y, weight, bias=None, gate=None, *, heads, act="silu", center=Fals
     all heads, [C / heads], float32.  out has gate's dtype (y's without a gate)."""
     dev, rows, G, dt, shared = _head_norm_inputs(y, weight, bias, gate, heads)
     if out is None:
-        out = torch.empty(y.shape, dtype=dt, device=dev)
+        out = torch.empty_like(y if gate is None else gate)
     else:
         _need(out, "out", dt if gate is not None else _FLOATS, y.shape, dev)
         dt = _narrow("out", out, "y", y.dtype)
     flags = (L.WKV_NORM_CENTER if center else 0) | (L.WKV_NORM_SHARED if shared else 0)
-    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _p(y), _p(weight), _p(bias), _p(gate),
-            _p(out), _stream(dev))
-    return _launch_on(dev, bind, "wkv_head_norm", L.lib().wkv_head_norm, args, out, locals())
+    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _at(y), _at(weight), _at(bias), _at(gate),
+            _at(out), _stream(dev))
+    return _launch_on(dev, bind, "wkv_head_norm", L.lib().wkv_head_norm, args, out, locals() if bind else None)
 
 
 def head_norm_backward(y, gout, weight, bias=None, gate=None, *, heads, act="silu", center=False, eps=1e-5,
@@ -898,10 +919,10 @@ def head_norm_backward(y, gout, weight, bias=None, gate=None, *, heads, act="sil
     lib = L.lib()
     workspace = _scratch(workspace, int(lib.wkv_head_norm_backward_workspace_bytes(rows, heads, G)), dev)
     flags = (L.WKV_NORM_CENTER if center else 0) | (L.WKV_NORM_SHARED if shared else 0)
-    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _p(y), _p(weight), _p(bias), _p(gate),
-            _p(gout), _p(dy), _p(dweight), _p(dbias), _p(dgate), _p(workspace), _bytes_of(workspace), _stream(dev))
+    args = (rows, heads, G, _DT[y.dtype], _DT[dt], flags, _act(act), eps, _at(y), _at(weight), _at(bias), _at(gate),
+            _at(gout), _at(dy), _at(dweight), _at(dbias), _at(dgate), _at(workspace), _bytes_of(workspace), _stream(dev))
     return _launch_on(dev, bind, "wkv_head_norm_backward", lib.wkv_head_norm_backward, args,
-                      (dy, dweight, dbias, dgate), locals())
+                      (dy, dweight, dbias, dgate), locals() if bind else None)
 
 
 class HeadNormFunction(torch.autograd.Function):
@@ -955,9 +976,9 @@ def block_norm(x, y, pre_w, pre_b=None, *, gate=None, act="sigmoid", post_w=None
     h = torch.empty_like(y) if h is None else h
     _need(x_out, "x_out", x.dtype, x.shape, dev)
     _need(h, "h", y.dtype, x.shape, dev)
-    args = (rows, C, _DT[x.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _p(x), _p(y),
-            _p(gate), _p(post_w), _p(post_b), _p(scale), _p(pre_w), _p(pre_b), _p(x_out), _p(h), _stream(dev))
-    return _launch_on(dev, bind, "wkv_block_norm", L.lib().wkv_block_norm, args, (x_out, h), locals())
+    args = (rows, C, _DT[x.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _at(x), _at(y),
+            _at(gate), _at(post_w), _at(post_b), _at(scale), _at(pre_w), _at(pre_b), _at(x_out), _at(h), _stream(dev))
+    return _launch_on(dev, bind, "wkv_block_norm", L.lib().wkv_block_norm, args, (x_out, h), locals() if bind else None)
 
 
 def block_norm_backward(x_out, y, gh, pre_w, pre_b=None, *, gx=None, gate=None, act="sigmoid", post_w=None, post_b=None,
@@ -974,10 +995,10 @@ def block_norm_backward(x_out, y, gh, pre_w, pre_b=None, *, gx=None, gate=None, 
              dpost_b=like(post_b), dscale=like(scale))
     lib = L.lib()
     workspace = _scratch(workspace, int(lib.wkv_block_norm_backward_workspace_bytes(rows, C)), dev)
-    args = (rows, C, _DT[x_out.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _p(x_out), _p(y),
-            _p(gate), _p(post_w), _p(post_b), _p(scale), _p(pre_w), _p(pre_b), _p(gx), _p(gh), _p(g["dx"]), _p(g["dy"]),
-            _p(g["dgate"]), _p(g["dpost_w"]), _p(g["dpost_b"]), _p(g["dscale"]), _p(g["dpre_w"]), _p(g["dpre_b"]),
-            _p(workspace), _bytes_of(workspace), _stream(dev))
+    args = (rows, C, _DT[x_out.dtype], _DT[y.dtype], L.WKV_NORM_CENTER if center else 0, _act(act), eps, _at(x_out), _at(y),
+            _at(gate), _at(post_w), _at(post_b), _at(scale), _at(pre_w), _at(pre_b), _at(gx), _at(gh), _at(g["dx"]), _at(g["dy"]),
+            _at(g["dgate"]), _at(g["dpost_w"]), _at(g["dpost_b"]), _at(g["dscale"]), _at(g["dpre_w"]), _at(g["dpre_b"]),
+            _at(workspace), _bytes_of(workspace), _stream(dev))
     keep = (x_out, y, gh, pre_w, pre_b, gx, gate, post_w, post_b, scale, workspace, tuple(g.values()))
     return _launch_on(dev, bind, "wkv_block_norm_backward", lib.wkv_block_norm_backward, args, g, dict(keep=keep))
 
