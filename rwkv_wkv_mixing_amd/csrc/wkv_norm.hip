@@ -112,22 +112,49 @@ struct Raw {
     }
 };
 
-// act(g) and its derivative.  exp overflows to inf for g below -88, where both sigmoids are 0.
-__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
-    if (act == kActNone) {
-        a = g;
-        da = 1.f;
+// act(g) and (kGrad) its derivative of a thread's V elements; without a gate 1 and 0.  exp overflows to
+// inf for g below -88, where both sigmoids are 0.  The choice is made once for the V elements: made for
+// each it took as many instructions as the arithmetic.
+template <int V, bool kGrad>
+__device__ __forceinline__ void activate(int act, bool gated, const float (&g)[V], float (&a)[V], float (&da)[V]) {
+    if (!gated || act == kActNone) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            a[j] = gated ? g[j] : 1.f;
+            da[j] = gated ? 1.f : 0.f;
+        }
         return;
     }
-    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-g));  // within 1 ulp of the quotient
+#pragma unroll
+    for (int j = 0; j < V; ++j) a[j] = __builtin_amdgcn_rcpf(1.f + __expf(-g[j]));  // within 1 ulp of the quotient
     if (act == kActSigmoid) {
-        a = s;
-        da = s * (1.f - s);
-    } else {
-        a = g * s;
-        da = s * (1.f + g * (1.f - s));
+        if constexpr (kGrad) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) da[j] = a[j] * (1.f - a[j]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float s = a[j];
+        a[j] = g[j] * s;
+        if constexpr (kGrad) da[j] = s * fmaf(g[j], 1.f - s, 1.f);
     }
 }
+
+// V elements of an optional [C] parameter
+template <int V>
+__device__ __forceinline__ void load_or(const float* p, int64_t c, float otherwise, float (&f)[V]) {
+    if (p != nullptr) {
+        load<V>(p + c, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = otherwise;
+    }
+}
+
+// 1 / sqrt, within 1 ulp
+__device__ __forceinline__ float rsqrt1(float x) { return __builtin_amdgcn_rsqf(x); }
 
 #ifndef WKV_BN_NV2
 #define WKV_BN_NV2 1024
@@ -170,27 +197,19 @@ __global__ void __launch_bounds__(kBlock) head_norm_kernel(HeadNormArgs P) {
             }
         }
     }
-    const float inv = 1.f / sqrtf(sum_lanes(sq, lanes) * inv_g + P.eps);
+    const float inv = rsqrt1(sum_lanes(sq, lanes) * inv_g + P.eps);
     if (!live) return;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * lanes + lane) * V;
         if (c >= G) continue;
-        float w[V], b[V], g[V];
+        float w[V], b[V], g[V], a[V], da[V];
         load<V>(P.weight + wb + c, w);
-        if (P.bias != nullptr) load<V>(P.bias + wb + c, b);
+        load_or<V>(P.bias, wb + c, 0.f, b);
         if (P.gate != nullptr) load<V>(static_cast<const TG*>(P.gate) + base + c, g);
+        activate<V, false>(P.act, P.gate != nullptr, g, a, da);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float z = y[i][j] * inv * w[j];
-            if (P.bias != nullptr) z += b[j];
-            if (P.gate != nullptr) {
-                float a, da;
-                activate(P.act, g[j], a, da);
-                z *= a;
-            }
-            y[i][j] = z;
-        }
+        for (int j = 0; j < V; ++j) y[i][j] = fmaf(y[i][j] * inv, w[j], b[j]) * a[j];
         store<V>(static_cast<TG*>(P.out) + base + c, y[i]);
     }
 }
@@ -251,20 +270,16 @@ __global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
                 }
             }
         }
-        const float inv = 1.f / sqrtf(sum_lanes(sq, lanes) * inv_g + P.eps);
+        const float inv = rsqrt1(sum_lanes(sq, lanes) * inv_g + P.eps);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            float a[V], da[V];
+            activate<V, true>(P.act, P.gate != nullptr, g[i], a, da);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float yh = y[i][j] * inv;
-                float dz = go[i][j];
-                if (P.gate != nullptr) {
-                    float a, da;
-                    activate(P.act, g[i][j], a, da);
-                    g[i][j] = dz * (yh * w[i][j] + b[i][j]) * da;
-                    dz *= a;
-                }
+                const float yh = y[i][j] * inv, dz = go[i][j] * a[j];
+                g[i][j] = go[i][j] * fmaf(yh, w[i][j], b[i][j]) * da[j];
                 dw[i][j] = fmaf(dz, yh, dw[i][j]);
                 db[i][j] += dz;
                 const float d = dz * w[i][j];
@@ -282,7 +297,7 @@ __global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
             const int c = (i * lanes + lane) * V;
             if (c >= G) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[i][j] = inv * (go[i][j] - s1 - y[i][j] * s2);
+            for (int j = 0; j < V; ++j) y[i][j] = inv * fmaf(-y[i][j], s2, go[i][j] - s1);
             store<V>(static_cast<TY*>(P.dy) + base + c, y[i]);
             if (P.gate != nullptr) store<V>(static_cast<TG*>(P.dgate) + base + c, g[i]);
         }
@@ -358,12 +373,9 @@ __device__ __forceinline__ void row_sums(float (&x)[K], int threads, float (*tab
         for (int k = 0; k < K; ++k) tab[turn][wv][k] = x[k];
     }
     __syncthreads();
+    const int i = threadIdx.x & (waves - 1);  // a power of two
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float s = 0.f;
-        for (int i = 0; i < waves; ++i) s += tab[turn][i][k];
-        x[k] = s;
-    }
+    for (int k = 0; k < K; ++k) x[k] = sum_lanes(tab[turn][i][k], waves);
 }
 
 // `threads` threads hold a row, vector i of a thread at channel (i threads + thread) V.  With 64 the
@@ -416,16 +428,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
             }
         }
         row_sums<1>(s, n, tab, turn);
-        const float inv = 1.f / sqrtf(s[0] * inv_c + P.eps);
+        const float inv = rsqrt1(s[0] * inv_c + P.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             float w[V], b[V];
             load<V>(P.post_w + c, w);
-            if (P.post_b != nullptr) load<V>(P.post_b + c, b);
+            load_or<V>(P.post_b, c, 0.f, b);
 #pragma unroll
-            for (int j = 0; j < V; ++j) z[i][j] = z[i][j] * inv * w[j] + (P.post_b != nullptr ? b[j] : 0.f);
+            for (int j = 0; j < V; ++j) z[i][j] = fmaf(z[i][j] * inv, w[j], b[j]);
         }
     }
     s[0] = 0.f;
@@ -433,16 +445,14 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
     for (int i = 0; i < NV; ++i) {
         const int c = (i * n + th) * V;
         if (c >= C) continue;
-        float x[V], g[V], sc[V];
+        float x[V], g[V], sc[V], a[V], da[V];
         rx[i].get(x);
         if (P.gate != nullptr) rg[i].get(g);
-        if (P.scale != nullptr) load<V>(P.scale + c, sc);
+        load_or<V>(P.scale, c, 1.f, sc);
+        activate<V, false>(P.act, P.gate != nullptr, g, a, da);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float a = 1.f, da;
-            if (P.gate != nullptr) activate(P.act, g[j], a, da);
-            if (P.scale != nullptr) a *= sc[j];
-            z[i][j] = fmaf(z[i][j], a, x[j]);
+            z[i][j] = fmaf(z[i][j], a[j] * sc[j], x[j]);
             s[0] += z[i][j];
         }
         store<V>(static_cast<TX*>(P.x_out) + base + c, z[i]);
@@ -463,16 +473,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
         }
     }
     row_sums<1>(s, n, tab, turn);
-    const float inv = 1.f / sqrtf(s[0] * inv_c + P.eps);
+    const float inv = rsqrt1(s[0] * inv_c + P.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * n + th) * V;
         if (c >= C) continue;
         float w[V], b[V];
         load<V>(P.pre_w + c, w);
-        if (P.pre_b != nullptr) load<V>(P.pre_b + c, b);
+        load_or<V>(P.pre_b, c, 0.f, b);
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[i][j] = z[i][j] * inv * w[j] + (P.pre_b != nullptr ? b[j] : 0.f);
+        for (int j = 0; j < V; ++j) z[i][j] = fmaf(z[i][j] * inv, w[j], b[j]);
         store<V>(static_cast<TY*>(P.h) + base + c, z[i]);
     }
 }
@@ -480,12 +490,13 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
 // The rows of slot q (of `slots`): q, q + slots, ..  Partial sums [5][slots][C]: dpre_w, dpre_b, dpost_w,
 // dpost_b, dscale.
 //
-// A row's inputs are fetched while the row before it is worked on (NV == 1; the channels' five sums and
-// four weights leave room for that in 256 registers, not in 128: a workgroup has at most 512 threads).
+// A row's inputs are fetched while the row before it is worked on (NV == 1), and the channels' four weights
+// are kept in registers where there are 256 of them (at most 512 threads) beside the five sums.
 template <typename TX, typename TY, int V, int NV, int Threads>
 __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P) {
     __shared__ float tab[2][16][2];
     constexpr bool kAhead = NV == 1;
+    constexpr bool kKeep = kAhead && Threads <= 512;  // the weights in registers
     int turn = 0;
     const int n = P.threads, th = threadIdx.x % n;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
@@ -503,15 +514,10 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
         float pre[V], post[V], bias[V], scale[V];
     };
     const auto weights = [&](int c, Weights& w) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w.post[j] = w.scale[j] = 1.f;
-            w.bias[j] = 0.f;
-        }
         load<V>(P.pre_w + c, w.pre);
-        if (post) load<V>(P.post_w + c, w.post);
-        if (P.post_b != nullptr) load<V>(P.post_b + c, w.bias);
-        if (P.scale != nullptr) load<V>(P.scale + c, w.scale);
+        load_or<V>(P.post_w, c, 1.f, w.post);
+        load_or<V>(P.post_b, c, 0.f, w.bias);
+        load_or<V>(P.scale, c, 1.f, w.scale);
     };
     Raw<TX, V> rx[NV], rt[kAhead ? NV : 1];
     Raw<TY, V> ry[NV], rd[NV], rg[kAhead ? NV : 1];
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
         }
     };
     Weights kept;
-    if (kAhead && th * V < C) weights(th * V, kept);
+    if (kKeep && th * V < C) weights(th * V, kept);
     if (kAhead && slot < P.rows) fetch(slot);
     for (int64_t row = slot; row < P.rows; row += P.slots) {  // the same trip count for a row's threads
         const int64_t base = row * P.C;
@@ -583,22 +589,22 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             }
         }
         row_sums<2>(s, n, tab, turn);
-        const float ix = 1.f / sqrtf(s[0] * inv_c + P.eps);
-        const float iy = post ? 1.f / sqrtf(s[1] * inv_c + P.eps) : 1.f;
+        const float ix = rsqrt1(s[0] * inv_c + P.eps);
+        const float iy = post ? rsqrt1(s[1] * inv_c + P.eps) : 1.f;
         s[0] = s[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             float w[V];
-            if constexpr (!kAhead) load<V>(P.pre_w + c, w);
+            if constexpr (!kKeep) load<V>(P.pre_w + c, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 x[i][j] *= ix;
                 y[i][j] *= iy;
                 acc[0][i][j] = fmaf(d[i][j], x[i][j], acc[0][i][j]);
                 acc[1][i][j] += d[i][j];
-                d[i][j] *= kAhead ? kept.pre[j] : w[j];
+                d[i][j] *= kKeep ? kept.pre[j] : w[j];
                 s[0] += d[i][j];
                 s[1] = fmaf(d[i][j], x[i][j], s[1]);
             }
@@ -611,23 +617,23 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             Weights here;
+            if constexpr (!kKeep) weights(c, here);
             if constexpr (!kAhead) {
                 fetch_late(base + c, 0);
-                weights(c, here);
                 late(0);
             }
-            const Weights& w = kAhead ? kept : here;
+            const Weights& w = kKeep ? kept : here;
+            float a[V], da[V];
+            activate<V, true>(P.act, gated, g, a, da);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float dx = ix * (d[i][j] - m1 - x[i][j] * m2) + t[j];
+                const float dx = fmaf(ix, fmaf(-x[i][j], m2, d[i][j] - m1), t[j]);
                 x[i][j] = dx;
-                const float z = y[i][j] * w.post[j] + w.bias[j];
-                float a = 1.f, da = 0.f;
-                if (gated) activate(P.act, g[j], a, da);
-                acc[4][i][j] = fmaf(dx, z * a, acc[4][i][j]);
+                const float z = fmaf(y[i][j], w.post[j], w.bias[j]);
+                acc[4][i][j] = fmaf(dx, z * a[j], acc[4][i][j]);
                 const float ds = dx * w.scale[j];
-                g[j] = ds * z * da;
-                const float dz = ds * a;
+                g[j] = ds * z * da[j];
+                const float dz = ds * a[j];
                 acc[2][i][j] = fmaf(dz, y[i][j], acc[2][i][j]);
                 acc[3][i][j] += dz;
                 d[i][j] = dz * w.post[j];
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             const int c = (i * n + th) * V;
             if (c >= C) continue;
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[i][j] = iy * (d[i][j] - p1 - y[i][j] * p2);
+            for (int j = 0; j < V; ++j) d[i][j] = iy * fmaf(-y[i][j], p2, d[i][j] - p1);
             store<V>(static_cast<TY*>(P.dy) + base + c, d[i]);
         }
     }
@@ -738,8 +744,8 @@ hipError_t launch_block_bwd(const BlockNormArgs& a, hipStream_t stream) {
     return e == hipSuccess ? launch_reduce(r, stream) : e;
 }
 
-// Threads that hold a row: 8 channels each from the smallest count that does (the backward 16 beyond
-// 4096 channels, in at most 512 threads), or, off the 16-byte grid, 1024 threads of single elements.
+// Threads that hold a row: 8 channels each from the smallest count that does (the forward 16 from
+// WKV_BN_NV2 channels), or, off the 16-byte grid, 1024 threads of single elements.
 template <typename TX, typename TY>
 hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     a.slots = block_norm_slots(a.rows, a.C);
@@ -752,9 +758,7 @@ hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     }
     if (!a.vec)
         return a.C <= 4096 ? launch_block_bwd<TX, TY, 1, 4, 1024>(a, stream) : launch_block_bwd<TX, TY, 1, 8, 1024>(a, stream);
-    if (a.C <= 4096) return launch_block_bwd<TX, TY, 8, 1, 512>(a, stream);
-    a.threads = 512;
-    return launch_block_bwd<TX, TY, 8, 2, 512>(a, stream);
+    return a.C <= 4096 ? launch_block_bwd<TX, TY, 8, 1, 512>(a, stream) : launch_block_bwd<TX, TY, 8, 1, 1024>(a, stream);
 }
 
 hipError_t launch_block_t(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
@@ -774,7 +778,7 @@ int64_t head_norm_chunks(int64_t rows, int64_t C) {
 
 // Rows of partial sums of a block norm's backward: 8 waves a compute unit, 4 rows or more behind each.
 int64_t block_norm_slots(int64_t rows, int64_t C) {
-    const int64_t threads = C <= 512 ? 64 : pow2_at_least((C + 7) / 8 < 512 ? (C + 7) / 8 : 512);
+    const int64_t threads = C <= 512 ? 64 : pow2_at_least((C + 7) / 8);
     const int64_t most = 256 * 512 / threads, n = (rows + 3) / 4;
     return n < most ? n : most;
 }
