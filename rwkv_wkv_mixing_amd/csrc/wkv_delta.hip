@@ -46,10 +46,7 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 constexpr int kTile = 64;   // tokens staged at a time, and between saved states
 constexpr int kSub = 16;    // tokens of one triangular system
 constexpr int kWaves = 4;   // per workgroup: one per sub-block of a tile, 16 value columns each
-constexpr int kCols = 16 * kWaves;
 constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
-template <typename T, int N>
-constexpr int kOcc = sizeof(T) * N > 256 ? 1 : 2;  // workgroups a compute unit has the LDS for
 // A sequence is split in time when there are at most kSplitMost workgroups' worth of pairs, into segments
 // of kSplitTiles tiles or more and about kSplitGroups workgroups in all.  8192 tokens in bf16, whole and split:
 // 8 groups 647 and 78 us, 32 671 and 156, 64 609 and 273, 128 604 and 443 (N = 128: 851 and 699); a training
@@ -316,18 +313,6 @@ struct Staged {
             *reinterpret_cast<u32x4*>(&dst[q / kRowVecs][q % kRowVecs * kPer]) = x[i];
         }
     }
-    // the other way: this thread's pieces of a staged array to rows t0 .. of `base`, below `end`
-    template <int ROW>
-    static __device__ __forceinline__ void flush(const T (*src)[ROW], T* base, int64_t stride, int64_t t0, int64_t end) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int q = static_cast<int>(threadIdx.x) + i * 64 * kWaves;
-            const int64_t t = t0 + q / kRowVecs;
-            if (t < end)
-                *reinterpret_cast<u32x4*>(base + t * stride + q % kRowVecs * kPer) =
-                    *reinterpret_cast<const u32x4*>(&src[q / kRowVecs][q % kRowVecs * kPer]);
-        }
-    }
 };
 
 __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b, int64_t T) {
@@ -336,255 +321,369 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b,
     return n < 0 ? 0 : n < T ? n : T;
 }
 
-// What the four 16-token blocks of a tile need besides their rows.
-struct Blocks {
-    float w[kTile], beta[kTile];         // rates in log2 units; zero behind the row's length
-    float since[kTile];                  // decay from the block's start through the token
-    float put[kTile];                    // beta until: the write strength, decayed to the block's end
-    float inv[kWaves][kSub][kPadM];      // X, or its transpose
-    float att[kWaves][kSub][kPadM];      // A, or its transpose
-    float m[kWaves][kSub][kPadM];        // M diag(beta), while X is found
+// ---- the walk -----------------------------------------------------------------------------------
+// Forward and adjoint walk a sequence tile by tile (64 tokens; 32 where LDS has no room for two tiles of
+// float32 rows) with the state in registers.  A workgroup has two kinds of waves:
+//   N / 16 state waves, 16 value columns each, take the tile's blocks one after the other;
+//   one preparing wave per block of a tile, which meanwhile writes out its 16 rows of the last tile's
+//   results, stages its 16 rows of the next tile, and finds that block's decays, X and A from them (no
+//   other wave's rows are needed), its loads for the tile after that already on their way.
+// All buffers are double, and one barrier a tile is all that is left of waiting for each other.  Before,
+// four waves did both in turn with three barriers a tile: 5.2 us a tile and workgroup alone on its compute
+// unit at N = 64 (12 400 cycles, of which the blocks' own chain of products is about two thirds).
+//
+// Adjoint, for L = <go, o> + <ds_out, S_T>, over a block with G the gradient of the state after it:
+//     y      = A^T go + diag(beta until) K G
+//     lambda = X^T y                               (the gradient of v, and of V - diag(since) K S0)
+//     G0     = since_last G + R^T diag(since) go - K^T diag(since) lambda
+// which needs neither the states nor the errors of the forward: it writes lambda and the gradient of the
+// state after every 64 tokens and leaves the rest, which is independent from tile to tile, to the
+// gradient kernels below.
+template <typename T, int N>
+constexpr int kWalkTile = sizeof(T) * N > 256 ? 32 : 64;
+
+struct WalkArgs {
+    int64_t B, T, H, HK, nseg, per;
+    const int32_t* lengths;
+    const float* w;
+    const float* beta;
+    const void* r;
+    const void* k;
+    const void* x;        // v; adjoint: go
+    void* y;              // o; adjoint: dv
+    const float* first;   // the state before the walk, or NULL (zero)
+    const float* starts;  // the same for every segment, or NULL
+    float* last;          // the state after it, or NULL
+    float* local;         // [B H, nseg, 2, N, N]: a pass for what the segments do
+    float* rows;          // the errors, or NULL; adjoint: lambda
+    float* states;        // the states before every 64 tokens, or NULL; adjoint: their gradients after
 };
 
-// A thread's token of the next tile's rates.
-struct Rates {
-    float w, beta;
-    __device__ __forceinline__ void fetch(const float* pw, const float* pb, int64_t H, int64_t t0, int64_t end) {
-        const int64_t t = t0 + threadIdx.x;
-        w = beta = 0.f;
-        if (threadIdx.x < kTile && t < end) {
-            w = pw[t * H];
-            beta = pb[t * H];
-        }
-    }
-    __device__ __forceinline__ void put(Blocks& B) const {
-        if (threadIdx.x < kTile) {
-            B.w[threadIdx.x] = w * kLog2e;
-            B.beta[threadIdx.x] = beta;
-        }
-    }
+template <typename T, int N>
+struct WalkShared {
+    static constexpr int kTok = kWalkTile<T, N>;
+    T k[2][kTok][kRow<T, N>], r[2][kTok][kRow<T, N>];
+    T v[2][kTok][kRow<T, N>];                     // x and, block by block, y in its place
+    float since[2][kTok];                         // decay from the block's start through the token
+    float put[2][kTok];                           // beta until: the write strength, decayed to the block's end
+    float inv[2][kTok / kSub][kSub][kPadM];       // X or its transpose; before that M diag(beta)
+    float att[2][kTok / kSub][kSub][kPadM];       // A or its transpose
 };
 
-// Wave s prepares block s of the staged tile: decays, X and (kAtt) A, or (kAdj) their transposes.
-// Register r of group g holds element (i = 4 g + r, j = l16) of the 16 x 16 products.
-template <typename T, int N, bool kAtt, bool kAdj>
-__device__ __forceinline__ void prepare_block(int s, int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>],
-                                              Blocks& B) {
-    asm volatile("" : "+v"(l16), "+v"(g));  // else the comparisons below are kept in registers from tile to tile
-    const f4 kk = rows_product<N>(K[kSub * s + l16], K[kSub * s + l16], g);
-    f4 rk = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (kAtt) rk = rows_product<N>(R[kSub * s + l16], K[kSub * s + l16], g);
-    f4 wv[kSub / 4];
+// A wave's 16 rows of N elements between memory (from `base`, the same for the wave) and LDS.  Rows from
+// `left` on are zeros and not read, or not written.  Offsets from the base are 32 bits (the host's checks
+// keep 64 rows below 2^31 bytes): one register serves every row.
+template <typename T, int N>
+struct BlockRows {
+    static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kRowVecs = N / kPer, kRows = 64 / kRowVecs;  // vectors a row, rows an access
+    static constexpr int kVecs = kSub / kRows;
+    u32x4 x[kVecs];
+
+    __device__ __forceinline__ void fetch(const T* base, int stride, int left, int lane) {
+        const int row = lane / kRowVecs;
+        const uint32_t at = static_cast<uint32_t>(row * stride + lane % kRowVecs * kPer);
 #pragma unroll
-    for (int l = 0; l < kSub / 4; ++l) wv[l] = load4(&B.w[kSub * s + 4 * l]);
-    const float bj = B.beta[kSub * s + l16];
+        for (int i = 0; i < kVecs; ++i) {
+            const T* p = base + static_cast<int64_t>(i * kRows) * stride;
+            x[i] = u32x4{0, 0, 0, 0};
+            if (row + i * kRows < left) x[i] = *reinterpret_cast<const u32x4*>(p + at);
+        }
+    }
+    __device__ __forceinline__ void put(T (*dst)[kRow<T, N>], int lane) const {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            *reinterpret_cast<u32x4*>(&dst[lane / kRowVecs + i * kRows][lane % kRowVecs * kPer]) = x[i];
+    }
+    static __device__ __forceinline__ void flush(const T (*src)[kRow<T, N>], T* base, int stride, int left, int lane) {
+        const int row = lane / kRowVecs;
+        const uint32_t at = static_cast<uint32_t>(row * stride + lane % kRowVecs * kPer);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            T* p = base + static_cast<int64_t>(i * kRows) * stride;
+            if (row + i * kRows < left)
+                *reinterpret_cast<u32x4*>(p + at) =
+                    *reinterpret_cast<const u32x4*>(&src[row + i * kRows][lane % kRowVecs * kPer]);
+        }
+    }
+};
+
+// rows from `at` up to `end` as an int, 0 when there are none, at most a tile
+__device__ __forceinline__ int rows_left(int64_t at, int64_t end) {
+    const int64_t n = end - at;
+    return n < 0 ? 0 : n < kTile ? static_cast<int>(n) : kTile;
+}
+
+// The state's registers (state_row) to and from columns `col` of a row-major [N, N] array.
+template <int N>
+__device__ __forceinline__ void store_state(float* to, const f4 (&S)[N / 16], int col, int g) {
+    const uint32_t at = static_cast<uint32_t>(state_row(0, g, 0) * N + col);
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) (to + state_row(c, 0, q) * N)[at] = S[c][q];
+}
+template <int N>
+__device__ __forceinline__ void load_state(const float* from, f4 (&S)[N / 16], int col, int g) {
+    const uint32_t at = static_cast<uint32_t>(state_row(0, g, 0) * N + col);
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) S[c][q] = (from + state_row(c, 0, q) * N)[at];
+}
+
+// One wave prepares a block whose rows K, R it has staged: decays, X and (kAtt) A, or (kAdj) their
+// transposes.  wt, bt: rate (log2 units) and write strength of token l16.  Register r of group g holds
+// element (i = 4 g + r, j = l16) of the 16 x 16 products.
+template <typename T, int N, bool kAtt, bool kAdj>
+__device__ __forceinline__ void prepare_block(int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>], float wt,
+                                              float bt, float* since, float* put, float (*inv)[kPadM], float (*att)[kPadM]) {
+    asm volatile("" : "+v"(l16), "+v"(g));  // else the comparisons below are kept in registers from tile to tile
+    const f4 kk = rows_product<N>(K[l16], K[l16], g);
+    f4 rk = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kAtt) rk = rows_product<N>(R[l16], K[l16], g);
     float gap[4] = {0.f, 0.f, 0.f, 0.f};  // sum of w over j < l <= i
     float run = 0.f, pre = 0.f;
 #pragma unroll
     for (int l = 0; l < kSub; ++l) {
-        const float wl = wv[l / 4][l % 4];
+        const float wl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), l));
         const bool behind = l > l16;
         run += behind ? wl : 0.f;
         pre += behind ? 0.f : wl;
         if (l / 4 == g) gap[l % 4] = run;
     }
     if (g == 0) {
-        B.since[kSub * s + l16] = ex2(-pre);
-        B.put[kSub * s + l16] = ex2(-run) * bj;
+        since[l16] = ex2(-pre);
+        put[l16] = ex2(-run) * bt;
     }
-    f4 m, att;
+    f4 m, a;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int i = 4 * g + r;
-        const float f = ex2(-gap[r]) * bj;
+        const float f = ex2(-gap[r]) * bt;
         m[r] = l16 < i ? f * kk[r] : 0.f;
-        att[r] = l16 <= i ? f * rk[r] : 0.f;
+        a[r] = l16 <= i ? f * rk[r] : 0.f;
     }
     // Forward: row l16 of X, its elements from the last, x_j = [j == l16] - sum_{i > j} x_i m_ij, the table
     // holding the transpose of m.  Adjoint: column l16, x_i = [i == l16] - sum_{j < i} m_ij x_j.  Either way
     // the lane ends with a row of what the products take.
     if constexpr (kAdj) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) B.m[s][4 * g + r][l16] = m[r];
-        *reinterpret_cast<f4*>(&B.att[s][l16][4 * g]) = att;
+        for (int r = 0; r < 4; ++r) inv[4 * g + r][l16] = m[r];
+        *reinterpret_cast<f4*>(&att[l16][4 * g]) = a;
     } else {
-        *reinterpret_cast<f4*>(&B.m[s][l16][4 * g]) = m;
+        *reinterpret_cast<f4*>(&inv[l16][4 * g]) = m;
         if constexpr (kAtt) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) B.att[s][4 * g + r][l16] = att[r];
+            for (int r = 0; r < 4; ++r) att[4 * g + r][l16] = a[r];
         }
     }
     __builtin_amdgcn_wave_barrier();  // the table is read back by the wave that wrote it
     float x[kSub];
+    f4 row[3][kSub / 4];  // two rows ahead of the one in use; all at once they would spill
+    const auto read_row = [&](int n) {
+#pragma unroll
+        for (int l = 0; l < kSub / 4; ++l)
+            if (kAdj ? 4 * l < n : 4 * l + 3 > kSub - 1 - n) row[n % 3][l] = load4(&inv[kAdj ? n : kSub - 1 - n][4 * l]);
+    };
+    read_row(1);
+    read_row(2);
 #pragma unroll
     for (int n = 0; n < kSub; ++n) {
+        if (n > 0 && n + 2 < kSub) read_row(n + 2);
+        __builtin_amdgcn_sched_barrier(0);
         const int at = kAdj ? n : kSub - 1 - n;
-        f4 row[kSub / 4];
-#pragma unroll
-        for (int l = 0; l < kSub / 4; ++l) row[l] = load4(&B.m[s][at][4 * l]);
         float acc = at == l16 ? 1.f : 0.f;
 #pragma unroll
         for (int l = 0; l < n; ++l) {
             const int j = kAdj ? l : kSub - 1 - l;
-            acc = fmaf(-row[j / 4][j % 4], x[j], acc);
+            acc = fmaf(-row[n % 3][j / 4][j % 4], x[j], acc);
         }
         x[at] = acc;
     }
-    if (g == 0) {
+    __builtin_amdgcn_wave_barrier();  // every row has been read
+    // every group has the whole row and writes a quarter (a write under g == 0 would take the arithmetic
+    // above under that condition too, behind all of its reads)
+    f4 mine;
 #pragma unroll
-        for (int l = 0; l < kSub / 4; ++l)
-            *reinterpret_cast<f4*>(&B.inv[s][l16][4 * l]) = f4{x[4 * l], x[4 * l + 1], x[4 * l + 2], x[4 * l + 3]};
-    }
+    for (int q = 0; q < 4; ++q) mine[q] = g == 0 ? x[q] : g == 1 ? x[4 + q] : g == 2 ? x[8 + q] : x[12 + q];
+    *reinterpret_cast<f4*>(&inv[l16][4 * g]) = mine;
 }
-
-// A workgroup's place: (batch row, head) fastest, so that what shares rows of r, k and v runs together.
-struct Segment {
-    int64_t bh, cb, seg, begin, end;  // tokens [begin, end) of the sequence
-    __device__ __forceinline__ Segment(int64_t id, int64_t BH, int64_t blocks, int64_t nseg, int64_t per, int64_t T) {
-        bh = id % BH;
-        cb = id / BH % blocks;
-        seg = id / BH / blocks;
-        begin = seg * per * kTile;
-        end = seg == nseg - 1 ? T : (seg + 1) * per * kTile;
-    }
-};
-
-template <typename T, int N>
-struct FwdShared {
-    T k[kTile][kRow<T, N>];
-    T r[kTile][kRow<T, N>];
-    T v[kTile][kRow<T, kCols>];  // and, block by block, o in its place
-    Blocks blk;
-};
 
 // Four rows 4 g + q of a wave's columns to a float32 array of value rows, those below `rows`.
 __device__ __forceinline__ void store_rows(float* base, int stride, int at, f4 x, int g, int rows) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        if (4 * g + q < rows) base[(4 * g + q) * stride + at] = x[q];
+        if (4 * g + q < rows) (base + q * stride)[static_cast<uint32_t>(4 * g * stride + at)] = x[q];
 }
 
-// Chunked forward.  One workgroup per (64 value columns, batch row, head) walks the tiles in order: stage
-// the tile, each wave prepares one of its four blocks, then each wave takes its 16 columns through the
-// blocks one after the other with no barrier between them.  kOut false: a pass for the saved errors and
-// states, or the final state, only.
-template <typename T, int N, bool kOut>
-__global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_fwd_kernel(DeltaArgs P) {
-    __shared__ FwdShared<T, N> sm;
+template <typename T, int N>
+constexpr int kWalkThreads = 64 * (N / 16 + kWalkTile<T, N> / kSub);
+// waves a SIMD: two workgroups a compute unit where LDS has room for them (bf16 at N = 64), else one
+template <typename T, int N>
+constexpr int kWalkWaves = sizeof(T) * N <= 128 ? 4 : (kWalkThreads<T, N> / 64 + 3) / 4;
+
+// kOut false: a pass without o (adjoint: dv, lambda and the states' gradients): for the saved errors and
+// states, for the final state, or (local) for what the segments of a time split do.
+template <typename T, int N, bool kAdj, bool kOut>
+__global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delta_walk_kernel(WalkArgs P) {
+    using Shared = WalkShared<T, N>;
+    __shared__ Shared sm;
+    constexpr int kTok = Shared::kTok, kBlocks = kTok / kSub, kStateWaves = N / 16;
+    constexpr bool kNeedR = kAdj || kOut;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int l16 = lane & 15, g = lane >> 4;
-    const int64_t BH = P.B * P.H;
-    constexpr int64_t kBlocks = N / kCols;  // column blocks
-    const Segment at(blockIdx.x, BH, kOut || P.local == nullptr ? kBlocks : 2 * kBlocks, P.nseg, P.per, P.T);
-    const int64_t bh = at.bh, seg = at.seg;
-    const bool unit = at.cb >= kBlocks;  // columns of the identity: no values
-    if (unit && seg == 0) return;        // the first segment starts from the given state
-    const int64_t cb = unit ? at.cb - kBlocks : at.cb;
+    // (batch row, head) fastest, so that what shares rows of r and k runs together; then value columns or
+    // (local) the identity's; then the segment.  A pass over segments leaves out the one nothing follows.
+    const bool pass = !kOut && P.local != nullptr;
+    const int64_t BH = P.B * P.H, bh = blockIdx.x % BH, rest = blockIdx.x / BH;
+    const bool unit = pass && (rest & 1) != 0;
+    const int64_t seg = (pass ? rest >> 1 : rest) + (kAdj && pass ? 1 : 0);
+    const bool given = seg == (kAdj ? P.nseg - 1 : 0);  // starts from the call's own state
+    if (unit && given) return;
+    const int64_t begin = seg * P.per * kTile, stop = seg == P.nseg - 1 ? P.T : (seg + 1) * P.per * kTile;
     const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
     const int64_t len = row_length(P.lengths, b, P.T);
-    const int64_t end = len < at.end ? len : at.end;  // of this segment's tokens
-    const int64_t ks = P.HK * N, vs = P.H * N;        // row strides
-    const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
-    const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
-    const int64_t vo = b * P.T * vs + h * N + cb * kCols;
-    const T* v = static_cast<const T*>(P.v) + vo;
-    T* o = static_cast<T*>(P.o) + vo;
-    const float* w = P.w + b * P.T * P.H + h;
-    const float* beta = P.beta + b * P.T * P.H + h;
-    const int64_t scol = cb * kCols + 16 * wv + l16;  // of the state
-    const int64_t ntile = (P.T + kTile - 1) / kTile;
+    const int64_t end = len < stop ? len : stop;
+    const int64_t count = end > begin ? (end - begin + kTok - 1) / kTok : 0;  // tiles with a token of this row
+    const int64_t vs = P.H * N, vo = b * P.T * vs + h * N;
+    const auto start_of = [&](int64_t n) { return begin + (kAdj ? count - 1 - n : n) * kTok; };
 
-    const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
-                         : P.s_in != nullptr && seg == 0 ? P.s_in + bh * N * N : nullptr;
-    f4 S[N / 16];
-#pragma unroll
-    for (int c = 0; c < N / 16; ++c)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int row = state_row(c, g, q);
-            S[c][q] = unit ? (row == scol ? 1.f : 0.f) : first != nullptr ? first[row * N + scol] : 0.f;
-        }
-
-    Staged<T, N> fk, fr;
-    Staged<T, kCols> fv;
-    Rates fw;
-    const auto fetch = [&](int64_t t) {
-        fk.fetch(k, ks, t, len);
-        if constexpr (kOut) fr.fetch(r, ks, t, len);
-        fv.fetch(v, vs, t, unit ? 0 : len);
-        fw.fetch(w, beta, P.H, t, len);
-    };
-    fetch(at.begin);
-    int64_t t0 = at.begin;
-#pragma unroll 1
-    for (; t0 < end; t0 += kTile) {
-        // else every address and comparison below is worked out before the loop and kept in registers
-        asm volatile("" : "+v"(l16), "+v"(g));
-        __syncthreads();  // the last tile's readers are done, and its outputs in place
-        if (kOut && t0 > at.begin) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
-        fk.put(sm.k);
-        if constexpr (kOut) fr.put(sm.r);
-        fv.put(sm.v);
-        fw.put(sm.blk);
-        __syncthreads();
-        if (t0 + kTile < end) fetch(t0 + kTile);
-        prepare_block<T, N, kOut, false>(wv, l16, g, sm.k, sm.r, sm.blk);
-        if (P.states != nullptr) {
-            float* st = P.states + (bh * ntile + t0 / kTile) * N * N + cb * kCols + 16 * wv;
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) st[state_row(c, g, q) * N + l16] = S[c][q];
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int s = 0; s < kTile / kSub; ++s) {
-            const int tb = kSub * s;
-            // everything the block reads is on its way while the state is split
-            const LeftRows<T, N> kr(sm.k[tb + l16], g);
-            const f4 e_in = value_column(sm.v, tb, 16 * wv, l16, g);
-            const f4 since = load4(&sm.blk.since[tb + 4 * g]), put = load4(&sm.blk.put[tb + 4 * g]);
-            const f4 inv = load4(&sm.blk.inv[s][l16][4 * g]);
-            const float total = sm.blk.since[tb + kSub - 1];
-            const LeftCols<T, N> kc(sm.k, tb, l16, g);
-            const LeftRows<T, N> rr(sm.r[tb + l16], g);
-            const f4 att = load4(&sm.blk.att[s][l16][4 * g]);
-            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
-            const StateOperand<T, N> op(S);
-            const f4 kS = op.template times<false>(kr, g);
-            f4 out = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (kOut) out = since * op.template times<true>(rr, g);
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c) S[c] *= total;
-            const f4 e = mma16(inv, e_in - since * kS, f4{0.f, 0.f, 0.f, 0.f});
-            kc.add_outer(S, put * e);
-            if constexpr (kOut) {
-                out = mma16(att, e, out);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) store1(&sm.v[tb + 4 * g + q][16 * wv + l16], out[q]);
-            }
-            if (P.errs != nullptr) {
-                const int64_t left = P.T - t0 - tb;
-                if (left > 0)
-                    store_rows(P.errs + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, e, g,
-                               left < kSub ? static_cast<int>(left) : kSub);
-            }
-        }
-    }
-    if constexpr (kOut) {
-        __syncthreads();
-        if (t0 > at.begin) Staged<T, kCols>::flush(sm.v, o, vs, t0 - kTile, P.T);
-        // whole tiles behind the row's length: zeros
-        for (int64_t t = t0 + threadIdx.x / 16; t < at.end; t += 16) store4(&o[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
-    }
-    float* last = !kOut && P.local != nullptr ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
-                  : P.s_out != nullptr && seg == P.nseg - 1 ? P.s_out + bh * N * N : nullptr;
-    if (last != nullptr) {
+    if (wv < kStateWaves) {
+        const int col = 16 * wv + l16;
+        const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
+                             : P.first != nullptr && given ? P.first + bh * N * N : nullptr;
+        f4 S[N / 16];
 #pragma unroll
         for (int c = 0; c < N / 16; ++c)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) last[state_row(c, g, q) * N + scol] = S[c][q];
+            for (int q = 0; q < 4; ++q) S[c][q] = unit && state_row(c, g, q) == col ? 1.f : 0.f;
+        if (!unit && first != nullptr) load_state<N>(first, S, col, g);
+        __syncthreads();  // the first tile is prepared
+#pragma unroll 1
+        for (int64_t n = 0; n < count; ++n) {
+            asm volatile("" : "+v"(l16), "+v"(g));  // as in prepare_block
+            const int64_t t0 = start_of(n);
+            const int f = static_cast<int>(n & 1);
+            if (P.states != nullptr && !pass && (kTok == kTile || n == 0 || t0 % kTile == (kAdj ? kTile - kTok : 0))) {
+                store_state<N>(P.states + (bh * ((P.T + kTile - 1) / kTile) + t0 / kTile) * N * N, S, 16 * wv + l16, g);
+            }
+#pragma unroll 1
+            for (int i = 0; i < kBlocks; ++i) {
+                const int s = kAdj ? kBlocks - 1 - i : i, tb = kSub * s;
+                // everything the block reads is on its way while the state is split
+                const LeftRows<T, N> kr(sm.k[f][tb + l16], g);
+                const f4 x = value_column(sm.v[f], tb, 16 * wv, l16, g);
+                const f4 since = load4(&sm.since[f][tb + 4 * g]), put = load4(&sm.put[f][tb + 4 * g]);
+                const f4 inv = load4(&sm.inv[f][s][l16][4 * g]);
+                const float total = sm.since[f][tb + kSub - 1];
+                const LeftCols<T, N> kc(sm.k[f], tb, l16, g);
+                f4 result;  // e; adjoint: lambda
+                if constexpr (kAdj) {
+                    const f4 att = load4(&sm.att[f][s][l16][4 * g]);
+                    const LeftCols<T, N> rc(sm.r[f], tb, l16, g);
+                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+                    const f4 kG = StateOperand<T, N>(S).template times<false>(kr, g);
+#pragma unroll
+                    for (int c = 0; c < N / 16; ++c) S[c] *= total;
+                    rc.add_outer(S, since * x);
+                    const f4 y = mma16(att, x, put * kG);
+                    result = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
+                    kc.add_outer(S, -since * result);
+                    if constexpr (kOut) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) store1(&sm.v[f][tb + 4 * g + q][16 * wv + l16], result[q]);
+                    }
+                } else {
+                    const LeftRows<T, N> rr(sm.r[f][tb + l16], g);
+                    const f4 att = load4(&sm.att[f][s][l16][4 * g]);
+                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+                    const StateOperand<T, N> op(S);
+                    const f4 kS = op.template times<false>(kr, g);
+                    f4 out = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (kOut) out = since * op.template times<true>(rr, g);
+#pragma unroll
+                    for (int c = 0; c < N / 16; ++c) S[c] *= total;
+                    result = mma16(inv, x - since * kS, f4{0.f, 0.f, 0.f, 0.f});
+                    kc.add_outer(S, put * result);
+                    if constexpr (kOut) {
+                        out = mma16(att, result, out);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) store1(&sm.v[f][tb + 4 * g + q][16 * wv + l16], out[q]);
+                    }
+                }
+                if (P.rows != nullptr && !pass) {
+                    const int64_t left = P.T - t0 - tb;
+                    if (left > 0)
+                        store_rows(P.rows + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, result, g,
+                                   left < kSub ? static_cast<int>(left) : kSub);
+                }
+            }
+            __syncthreads();  // the next tile is prepared, this one's results are in place
+        }
+        float* last = pass ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
+                      : P.last != nullptr && seg == (kAdj ? 0 : P.nseg - 1) ? P.last + bh * N * N : nullptr;
+        if (last != nullptr) store_state<N>(last, S, 16 * wv + l16, g);
+    } else {
+        const int s = wv - kStateWaves;  // this wave's block of every tile
+        const int64_t ks = P.HK * N;
+        const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
+        const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
+        const T* x = static_cast<const T*>(P.x) + vo;
+        T* y = static_cast<T*>(P.y) + vo;
+        const float* w = P.w + b * P.T * P.H + h;
+        const float* beta = P.beta + b * P.T * P.H + h;
+        BlockRows<T, N> fk, fr, fx;
+        float wt = 0.f, bt = 0.f;
+        const auto fetch = [&](int64_t n) {
+            const int64_t t0 = start_of(n) + kSub * s;
+            const int left = rows_left(t0, len);
+            fk.fetch(k + t0 * ks, static_cast<int>(ks), left, lane);
+            if constexpr (kNeedR) fr.fetch(r + t0 * ks, static_cast<int>(ks), left, lane);
+            fx.fetch(x + t0 * vs, static_cast<int>(vs), unit ? 0 : left, lane);
+            wt = bt = 0.f;
+            if (l16 < left) {
+                const uint32_t at = static_cast<uint32_t>(l16 * static_cast<int>(P.H));
+                wt = (w + t0 * P.H)[at];
+                bt = (beta + t0 * P.H)[at];
+            }
+        };
+        const auto prepare = [&](int64_t n) {  // what has been fetched, as tile n; then tile n + 1 is fetched
+            const int f = static_cast<int>(n & 1), tb = kSub * s;
+            fk.put(&sm.k[f][tb], lane);
+            if constexpr (kNeedR) fr.put(&sm.r[f][tb], lane);
+            fx.put(&sm.v[f][tb], lane);
+            __builtin_amdgcn_wave_barrier();  // the rows are read back by the wave that wrote them
+            prepare_block<T, N, kNeedR, kAdj>(l16, g, &sm.k[f][tb], &sm.r[f][tb], wt * kLog2e, bt, &sm.since[f][tb],
+                                              &sm.put[f][tb], sm.inv[f][s], sm.att[f][s]);
+            // not before: the registers are needed; the state waves take longer than this one, so there is time
+            __builtin_amdgcn_sched_barrier(0);
+            if (n + 1 < count) fetch(n + 1);
+        };
+        const auto flush = [&](int64_t n) {
+            const int64_t t0 = start_of(n) + kSub * s;
+            BlockRows<T, N>::flush(&sm.v[n & 1][kSub * s], y + t0 * vs, static_cast<int>(vs), rows_left(t0, P.T), lane);
+        };
+        if (count > 0) {
+            fetch(0);
+            prepare(0);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int64_t n = 0; n < count; ++n) {
+            if (kOut && n > 0) flush(n - 1);
+            if (n + 1 < count) prepare(n + 1);
+            __syncthreads();
+        }
+        if constexpr (kOut) {
+            if (count > 0) flush(count - 1);
+            // whole tiles behind the row's length: zeros
+            constexpr int kPer = 64 * kBlocks * 4 / N;  // rows at a time
+            const int at = static_cast<int>(threadIdx.x) - 64 * kStateWaves;
+            for (int64_t t = begin + count * kTok + at / (N / 4); t < stop; t += kPer)
+                store4(&y[t * vs + at % (N / 4) * 4], f4{0.f, 0.f, 0.f, 0.f});
+        }
     }
 }
 
@@ -663,140 +762,7 @@ __global__ void __launch_bounds__(256) delta_step_kernel(DeltaArgs P) {
     }
 }
 
-// ---- backward -----------------------------------------------------------------------------------
-// For L = <go, o> + <ds_out, S_T>, over a block with G the gradient of the state after it:
-//     y      = A^T go + diag(beta until) K G
-//     lambda = X^T y                               (the gradient of v, and of V - diag(since) K S0)
-//     G0     = since_last G + R^T diag(since) go - K^T diag(since) lambda
-// which needs neither the states nor the errors of the forward: the adjoint walk below takes the tiles
-// last to first with the forward's layout, writes lambda and the gradient of the state after every tile,
-// and leaves the rest, which is independent from tile to tile, to delta_grad_kernel.
-template <typename T, int N>
-struct AdjShared {
-    T k[kTile][kRow<T, N>];
-    T r[kTile][kRow<T, N>];
-    T go[kTile][kRow<T, kCols>];  // and, block by block, dv in its place
-    Blocks blk;
-};
-
-// kOut false: a pass for what a segment does to the gradient of the state after it (DeltaBwdArgs::local).
-template <typename T, int N, bool kOut>
-__global__ void __launch_bounds__(64 * kWaves, (kOcc<T, N>)) delta_adjoint_kernel(DeltaBwdArgs P) {
-    __shared__ AdjShared<T, N> sm;
-    const int lane = threadIdx.x & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int l16 = lane & 15, g = lane >> 4;
-    const int64_t BH = P.B * P.H;
-    constexpr int64_t kBlocks = N / kCols;
-    // the pass over segments leaves out the first, which nothing comes before
-    const Segment at(blockIdx.x + (kOut ? 0 : BH * 2 * kBlocks), BH, kOut ? kBlocks : 2 * kBlocks, P.nseg, P.per, P.T);
-    const int64_t bh = at.bh, seg = at.seg;
-    const bool unit = at.cb >= kBlocks;
-    if (unit && seg == P.nseg - 1) return;  // the last segment starts from the given gradient
-    const int64_t cb = unit ? at.cb - kBlocks : at.cb;
-    const int64_t b = bh / P.H, h = bh % P.H, hk = h / (P.H / P.HK);
-    const int64_t len = row_length(P.lengths, b, P.T);
-    const int64_t end = len < at.end ? len : at.end;
-    const int64_t ks = P.HK * N, vs = P.H * N;
-    const T* r = static_cast<const T*>(P.r) + b * P.T * ks + hk * N;
-    const T* k = static_cast<const T*>(P.k) + b * P.T * ks + hk * N;
-    const int64_t vo = b * P.T * vs + h * N + cb * kCols;
-    const T* go = static_cast<const T*>(P.go) + vo;
-    T* dv = static_cast<T*>(P.dv) + vo;
-    const float* w = P.w + b * P.T * P.H + h;
-    const float* beta = P.beta + b * P.T * P.H + h;
-    const int64_t scol = cb * kCols + 16 * wv + l16;
-    const int64_t ntile = (P.T + kTile - 1) / kTile;
-
-    const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
-                         : P.ds_out != nullptr && seg == P.nseg - 1 ? P.ds_out + bh * N * N : nullptr;
-    f4 G[N / 16];
-#pragma unroll
-    for (int c = 0; c < N / 16; ++c)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int row = state_row(c, g, q);
-            G[c][q] = unit ? (row == scol ? 1.f : 0.f) : first != nullptr ? first[row * N + scol] : 0.f;
-        }
-
-    const int64_t begin = at.begin / kTile;  // tiles of the segment with a token of this row: [begin, live)
-    const int64_t live = end > at.begin ? (end + kTile - 1) / kTile : begin;
-    if constexpr (kOut) {
-        for (int64_t t = live * kTile + threadIdx.x / 16; t < at.end; t += 16)
-            store4(&dv[t * vs + threadIdx.x % 16 * 4], f4{0.f, 0.f, 0.f, 0.f});
-    }
-    Staged<T, N> fk, fr;
-    Staged<T, kCols> fg;
-    Rates fw;
-    const auto fetch = [&](int64_t t) {
-        fk.fetch(k, ks, t, len);
-        fr.fetch(r, ks, t, len);
-        fg.fetch(go, vs, t, unit ? 0 : len);
-        fw.fetch(w, beta, P.H, t, len);
-    };
-    if (live > begin) fetch((live - 1) * kTile);
-#pragma unroll 1
-    for (int64_t tile = live - 1; tile >= begin; --tile) {
-        asm volatile("" : "+v"(l16), "+v"(g));  // as in the forward
-        const int64_t t0 = tile * kTile;
-        __syncthreads();
-        if (kOut && tile + 1 < live) Staged<T, kCols>::flush(sm.go, dv, vs, t0 + kTile, P.T);
-        fk.put(sm.k);
-        fr.put(sm.r);
-        fg.put(sm.go);
-        fw.put(sm.blk);
-        __syncthreads();
-        if (tile > begin) fetch(t0 - kTile);
-        prepare_block<T, N, true, true>(wv, l16, g, sm.k, sm.r, sm.blk);
-        if constexpr (kOut) {
-            float* gt = P.gstates + (bh * ntile + tile) * N * N + cb * kCols + 16 * wv;
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) gt[state_row(c, g, q) * N + l16] = G[c][q];
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int s = kTile / kSub - 1; s >= 0; --s) {
-            const int tb = kSub * s;
-            const LeftRows<T, N> kr(sm.k[tb + l16], g);
-            const f4 d = value_column(sm.go, tb, 16 * wv, l16, g);
-            const f4 since = load4(&sm.blk.since[tb + 4 * g]), put = load4(&sm.blk.put[tb + 4 * g]);
-            const f4 att = load4(&sm.blk.att[s][l16][4 * g]), inv = load4(&sm.blk.inv[s][l16][4 * g]);
-            const float total = sm.blk.since[tb + kSub - 1];
-            const LeftCols<T, N> rc(sm.r, tb, l16, g);
-            const LeftCols<T, N> kc(sm.k, tb, l16, g);
-            if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
-            const f4 kG = StateOperand<T, N>(G).template times<false>(kr, g);
-#pragma unroll
-            for (int c = 0; c < N / 16; ++c) G[c] *= total;
-            rc.add_outer(G, since * d);
-            const f4 y = mma16(att, d, put * kG);
-            const f4 lam = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
-            kc.add_outer(G, -since * lam);
-            if constexpr (!kOut) continue;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) store1(&sm.go[tb + 4 * g + q][16 * wv + l16], lam[q]);
-            const int64_t left = P.T - t0 - tb;
-            if (left > 0)
-                store_rows(P.lambda + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, lam, g,
-                           left < kSub ? static_cast<int>(left) : kSub);
-        }
-    }
-    if constexpr (kOut) {
-        __syncthreads();
-        if (live > begin) Staged<T, kCols>::flush(sm.go, dv, vs, begin * kTile, P.T);
-    }
-    float* last = !kOut ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
-                  : P.ds_in != nullptr && seg == 0 ? P.ds_in + bh * N * N : nullptr;
-    if (last != nullptr) {
-#pragma unroll
-        for (int c = 0; c < N / 16; ++c)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) last[state_row(c, g, q) * N + scol] = G[c][q];
-    }
-}
-
+// ---- gradients ----------------------------------------------------------------------------------
 // The gradients that are sums over the value columns, tile by tile.  Over a tile of 64 tokens from the
 // state S0 with G the gradient of the state after it, all decays now counted inside the tile:
 //     dA_ij = ratio_ij beta_j go_i . e_j  (j <= i),   dM_ij = -ratio_ij beta_j lambda_i . e_j  (j < i)
@@ -1577,35 +1543,33 @@ __global__ void __launch_bounds__(4 * N) delta_chain_kernel(DeltaChainArgs P) {
     }
 }
 
+template <typename T, int N, bool kAdj, bool kOut>
+hipError_t launch_walk(const WalkArgs& a, hipStream_t stream) {
+    const int64_t groups = a.B * a.H * (a.local != nullptr ? 2 * (a.nseg - 1) : a.nseg);
+    hipLaunchKernelGGL((delta_walk_kernel<T, N, kAdj, kOut>), dim3(static_cast<unsigned>(groups)), dim3(kWalkThreads<T, N>), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
 template <typename T, int N>
 hipError_t launch_fwd(const DeltaArgs& a, hipStream_t stream) {
     if (a.states == nullptr && a.o != nullptr && a.T <= kDeltaStepMaxT) {
         const int64_t waves = a.B * a.H * (N / 64);
         hipLaunchKernelGGL((delta_step_kernel<T, N>), dim3(static_cast<unsigned>((waves + kWaves - 1) / kWaves)),
                            dim3(64 * kWaves), 0, stream, a);
-    } else {
-        const int64_t blocks = a.B * a.H * (N / kCols);
-        const dim3 grid(static_cast<unsigned>(a.local != nullptr ? 2 * blocks * (a.nseg - 1) : blocks * a.nseg));
-        if (a.o != nullptr) {
-            hipLaunchKernelGGL((delta_fwd_kernel<T, N, true>), grid, dim3(64 * kWaves), 0, stream, a);
-        } else {
-            hipLaunchKernelGGL((delta_fwd_kernel<T, N, false>), grid, dim3(64 * kWaves), 0, stream, a);
-        }
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    const WalkArgs w{a.B, a.T, a.H, a.HK, a.nseg, a.per, a.lengths, a.w, a.beta, a.r, a.k, a.v, a.o, a.s_in, a.starts, a.s_out,
+                     a.local, a.errs, a.states};
+    return a.o != nullptr ? launch_walk<T, N, false, true>(w, stream) : launch_walk<T, N, false, false>(w, stream);
 }
 
 template <typename T, int N>
 hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
-    const int64_t blocks = a.B * a.H * (N / kCols);
-    if (a.local != nullptr) {  // what the segments do, for the chain
-        hipLaunchKernelGGL((delta_adjoint_kernel<T, N, false>), dim3(static_cast<unsigned>(2 * blocks * (a.nseg - 1))),
-                           dim3(64 * kWaves), 0, stream, a);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((delta_adjoint_kernel<T, N, true>), dim3(static_cast<unsigned>(blocks * a.nseg)), dim3(64 * kWaves),
-                       0, stream, a);
-    hipError_t e = hipGetLastError();
+    const WalkArgs w{a.B, a.T, a.H, a.HK, a.nseg, a.per, a.lengths, a.w, a.beta, a.r, a.k, a.go, a.dv, a.ds_out, a.starts,
+                     a.ds_in, a.local, a.lambda, a.gstates};
+    if (a.local != nullptr) return launch_walk<T, N, true, false>(w, stream);  // what the segments do, for the chain
+    hipError_t e = launch_walk<T, N, true, true>(w, stream);
     if (e != hipSuccess) return e;
     const int64_t ntile = (a.T + kTile - 1) / kTile;
     const dim3 grid(static_cast<unsigned>(a.B * a.HK * ntile));
@@ -1620,7 +1584,7 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
-    const int64_t work = BH * (N / kCols), tiles = (T + kTile - 1) / kTile;
+    const int64_t work = BH * (N / 64), tiles = (T + kTile - 1) / kTile;
     *per = tiles;
     if (work < 1 || work > kSplitMost || tiles < 2 * kSplitTiles) return 1;
     int64_t nseg = kSplitGroups / work;
