@@ -1086,11 +1086,13 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 //   3. dA, dM and their transposes, as hi + mid (dr and dk are rounded to bf16), to LDS over e and
 //      lambda, each lane's eight values where the lane that needs them reads them
 //   4. every wave: its channels of the products of k and r with all ten blocks; and the rates
-// The wave waits for its LDS reads more than for anything else, so the registers are kept to what four
-// waves a SIMD have (N = 64: 128) and chains of dependent products are taken in turn.
+// Everything the tile needs of a head is on its way before the first of it is put into LDS, and chains of
+// dependent products are taken in turn.  Held to 128 registers for two workgroups a compute unit at N = 64 it
+// spilled and was no faster (405 to 440 us against 400).
 // LDS rows are not padded (two workgroups a compute unit at N = 64): the 16-byte piece q of row t lies at
 // q ^ swizzle(t), so that 16 rows' pieces q meet 16 different bank groups.
 constexpr int kGradWaves = 8;
+constexpr unsigned kGradGroups = 256;  // compute units
 constexpr int kGradThreads = 64 * kGradWaves;
 
 template <int N>
@@ -1108,7 +1110,6 @@ struct GradShared16 {
     float rowsum[10][kSub], colsum[10][kSub];  // of beta_j P_ij over j, of P_ij over i
     float withS[N / 16][kTile], withG[N / 16][kTile], inner[N / 16];
     float diag[kTile];                         // the crossing pairs inside the token's own block
-    float rowv[kTile], colv[kTile];
 };
 
 template <int N>
@@ -1129,18 +1130,6 @@ __device__ __forceinline__ bf8 col_twice(const uint16_t (*X)[N], int tb, int c0,
     return pair(a, a);
 }
 
-template <int N>
-__device__ __forceinline__ void stage_rows(uint16_t (*dst)[N], const uint16_t* base, int64_t stride, int64_t t0, int64_t end) {
-    constexpr int kRowVecs = N / 8;
-#pragma unroll
-    for (int i = 0; i < kTile * kRowVecs / kGradThreads; ++i) {
-        const int q = static_cast<int>(threadIdx.x) + i * kGradThreads;
-        const int t = q / kRowVecs, c = q % kRowVecs * 8;
-        const u32x4 x = t0 + t < end ? *reinterpret_cast<const u32x4*>(base + (t0 + t) * stride + c) : u32x4{0, 0, 0, 0};
-        *reinterpret_cast<u32x4*>(&dst[t][swizzled<N>(t, c)]) = x;
-    }
-}
-
 __device__ __forceinline__ void split8(f4 a, f4 b, bf8 (&out)[3]) {
     const Terms x = split(a), y = split(b);
     out[0] = pair(x.hi, y.hi);
@@ -1148,24 +1137,58 @@ __device__ __forceinline__ void split8(f4 a, f4 b, bf8 (&out)[3]) {
     out[2] = pair(x.lo, y.lo);
 }
 
+// A workgroup's rows t0 .. t0 + 63 of a [rows, N] array at `base` (the first row), between memory and LDS:
+// all of a tile's loads are issued before the first is waited for.
 template <int N>
-__device__ __forceinline__ void stage_terms(uint16_t (*dst)[kTile][N], const float* base, int64_t stride, int64_t t0, int64_t end) {
-    constexpr int kRowVecs = N / 8;
+struct GradRows {
+    static constexpr int kRowVecs = N / 8, kRows = kGradThreads / kRowVecs, kVecs = kTile / kRows;
+    u32x4 x[kVecs];
+    __device__ __forceinline__ void fetch(const uint16_t* base, int stride, int left) {
+        const int row = static_cast<int>(threadIdx.x) / kRowVecs;
+        const uint32_t at = static_cast<uint32_t>(row * stride + static_cast<int>(threadIdx.x) % kRowVecs * 8);
 #pragma unroll
-    for (int i = 0; i < kTile * kRowVecs / kGradThreads; ++i) {
-        const int q = static_cast<int>(threadIdx.x) + i * kGradThreads;
-        const int t = q / kRowVecs, c = q % kRowVecs * 8;
-        f4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-        if (t0 + t < end) {
-            a = load4(base + (t0 + t) * stride + c);
-            b = load4(base + (t0 + t) * stride + c + 4);
+        for (int i = 0; i < kVecs; ++i) {
+            x[i] = u32x4{0, 0, 0, 0};
+            if (row + i * kRows < left)
+                x[i] = *reinterpret_cast<const u32x4*>(base + static_cast<int64_t>(i * kRows) * stride + at);
         }
-        bf8 x[3];
-        split8(a, b, x);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8*>(&dst[p][t][swizzled<N>(t, c)]) = x[p];
     }
-}
+    __device__ __forceinline__ void put(uint16_t (*dst)[N]) const {
+        const int row = static_cast<int>(threadIdx.x) / kRowVecs, c = static_cast<int>(threadIdx.x) % kRowVecs * 8;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) *reinterpret_cast<u32x4*>(&dst[row + i * kRows][swizzled<N>(row + i * kRows, c)]) = x[i];
+    }
+};
+
+// the same from float32, split into its terms
+template <int N>
+struct GradTerms {
+    static constexpr int kRowVecs = N / 8, kRows = kGradThreads / kRowVecs, kVecs = kTile / kRows;
+    f4 a[kVecs], b[kVecs];
+    __device__ __forceinline__ void fetch(const float* base, int stride, int left) {
+        const int row = static_cast<int>(threadIdx.x) / kRowVecs;
+        const uint32_t at = static_cast<uint32_t>(row * stride + static_cast<int>(threadIdx.x) % kRowVecs * 8);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            a[i] = b[i] = f4{0.f, 0.f, 0.f, 0.f};
+            if (row + i * kRows < left) {
+                const float* p = base + static_cast<int64_t>(i * kRows) * stride + at;
+                a[i] = load4(p);
+                b[i] = load4(p + 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(uint16_t (*dst)[kTile][N]) const {
+        const int row = static_cast<int>(threadIdx.x) / kRowVecs, c = static_cast<int>(threadIdx.x) % kRowVecs * 8;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            bf8 x[3];
+            split8(a[i], b[i], x);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8*>(&dst[p][row + i * kRows][swizzled<N>(row + i * kRows, c)]) = x[p];
+        }
+    }
+};
 
 // Step i of a b for two factors in three terms each: all but the products below 2^-24 of the whole, the
 // smallest first.
@@ -1175,7 +1198,7 @@ __device__ __forceinline__ f4 mma_step(int i, const bf8 (&a)[3], const bf8 (&b)[
 }
 
 template <int N>
-__global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_kernel(DeltaBwdArgs P) {
+__global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdArgs P) {
     __shared__ GradShared16<N> sm;
     constexpr int NS = N / 16;               // slices of 16 channels
     constexpr int NX = 4 * NS / kGradWaves;  // token blocks a wave takes of its slice
@@ -1183,37 +1206,94 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
     int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int l16 = lane & 15, g = lane >> 4;
-    const int64_t ntile = (P.T + kTile - 1) / kTile;
-    const int64_t bhk = blockIdx.x % (P.B * P.HK), tile = blockIdx.x / (P.B * P.HK);
-    const int64_t b = bhk / P.HK, hk = bhk % P.HK, per = P.H / P.HK;
-    const int64_t len = row_length(P.lengths, b, P.T);
-    const int64_t ks = P.HK * N, vs = P.H * N, t0 = tile * kTile;
-    const int64_t ko = b * P.T * ks + hk * N;
-    uint16_t* dr = static_cast<uint16_t*>(P.dr) + ko;
-    uint16_t* dk = static_cast<uint16_t*>(P.dk) + ko;
-    if (t0 >= len) {  // nothing of this row here
-        zero_tile<uint16_t, N>(P, dr, dk, b, hk, t0);
-        return;
-    }
-    stage_rows<N>(sm.k, static_cast<const uint16_t*>(P.k) + ko, ks, t0, len);
-    stage_rows<N>(sm.r, static_cast<const uint16_t*>(P.r) + ko, ks, t0, len);
+    const int64_t ntile = (P.T + kTile - 1) / kTile, pairs = P.B * P.HK, per = P.H / P.HK;
+    const int64_t ks = P.HK * N, vs = P.H * N;
     const int slice = wv % NS, c0 = 16 * slice, X0 = wv / NS * NX;
+
+    // A (tile, batch row, key head), batch row and head fastest, and one of its value heads.
+    struct Place {
+        int64_t item, b, hk, tile, t0, h;
+        int left;
+    };
+    Place at, next;
+    // the workgroup's next item that holds tokens; those that hold none get zeros
+    const auto settle = [&](Place& p) {
+        for (; p.item < pairs * ntile; p.item += gridDim.x) {
+            const int64_t bhk = p.item % pairs;
+            p.b = bhk / P.HK;
+            p.hk = bhk % P.HK;
+            p.tile = p.item / pairs;
+            p.t0 = p.tile * kTile;
+            p.h = p.hk * per;
+            p.left = rows_left(p.t0, row_length(P.lengths, p.b, P.T));
+            if (p.left > 0) return;
+            const int64_t ko = p.b * P.T * ks + p.hk * N;
+            zero_tile<uint16_t, N>(P, static_cast<uint16_t*>(P.dr) + ko, static_cast<uint16_t*>(P.dk) + ko, p.b, p.hk, p.t0);
+        }
+    };
+    GradRows<N> fk, fr, fg;
+    GradTerms<N> fe, fl;
+    float wt, bt;
+    // The next tile's inputs, and this wave's rows of the states before and after it, arrive behind the work
+    // on this one at N = 64; at N = 128 they are twice as much, which there are no registers for.
+    constexpr bool kAhead = N == 64;
+    f4 sa[kAhead ? NM : 1], sb[kAhead ? NM : 1], ga[kAhead ? NM : 1], gb[kAhead ? NM : 1];
+    const auto fetch_states = [&](const Place& p, int m, int to) {
+        const int64_t from = ((p.b * P.H + p.h) * ntile + p.tile) * N * N + 32 * m;
+        const uint32_t mine = static_cast<uint32_t>((c0 + l16) * N + 8 * g);
+        sa[to] = load4(P.states + from + mine);
+        sb[to] = load4(P.states + from + 4 + mine);
+        ga[to] = load4(P.gstates + from + mine);
+        gb[to] = load4(P.gstates + from + 4 + mine);
+    };
+    const auto fetch = [&](const Place& p) {
+        const int64_t ko = (p.b * P.T + p.t0) * ks + p.hk * N, vo = (p.b * P.T + p.t0) * vs + p.h * N;
+        fk.fetch(static_cast<const uint16_t*>(P.k) + ko, static_cast<int>(ks), p.left);
+        fr.fetch(static_cast<const uint16_t*>(P.r) + ko, static_cast<int>(ks), p.left);
+        fg.fetch(static_cast<const uint16_t*>(P.go) + vo, static_cast<int>(vs), p.left);
+        fe.fetch(P.errs + vo, static_cast<int>(vs), p.left);
+        fl.fetch(P.lambda + vo, static_cast<int>(vs), p.left);
+        wt = bt = 0.f;
+        if (static_cast<int>(threadIdx.x) < p.left) {
+            wt = P.w[(p.b * P.T + p.t0 + lane) * P.H + p.h] * kLog2e;
+            bt = P.beta[(p.b * P.T + p.t0 + lane) * P.H + p.h];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto fetch_states_ahead = [&](const Place& p) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) fetch_states(p, m, m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
     f4 drT[NX], dkT[NX];  // of token block X0 + x: channels c0 + 4 g .. + 3 of token l16
 #pragma unroll
     for (int x = 0; x < NX; ++x) drT[x] = dkT[x] = f4{0.f, 0.f, 0.f, 0.f};
 
+    at.item = blockIdx.x;
+    settle(at);
+    if (at.item >= pairs * ntile) return;
+    if constexpr (kAhead) {
+        fetch(at);
+        fetch_states_ahead(at);
+    }
+    bool first = true;
 #pragma unroll 1
-    for (int64_t h = hk * per; h < (hk + 1) * per; ++h) {
-        const int64_t bh = b * P.H + h, vo = b * P.T * vs + h * N;
+    while (at.item < pairs * ntile) {
         // else every address and comparison below is worked out before the loop and kept in registers
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
-        __syncthreads();  // the last head's readers are done
-        stage_rows<N>(sm.go, static_cast<const uint16_t*>(P.go) + vo, vs, t0, len);
-        stage_terms<N>(sm.e, P.errs + vo, vs, t0, len);
-        stage_terms<N>(sm.lam, P.lambda + vo, vs, t0, len);
+        const int64_t b = at.b, h = at.h, t0 = at.t0;
+        const int64_t len = t0 + at.left;
+        if constexpr (!kAhead) fetch(at);
+        if (!first) __syncthreads();  // the last tile's readers are done
+        first = false;
+        fk.put(sm.k);
+        fr.put(sm.r);
+        fg.put(sm.go);
+        fe.put(sm.e);
+        fl.put(sm.lam);
         if (threadIdx.x < kTile) {  // one wave: the decays of its 64 tokens
-            const int64_t t = t0 + threadIdx.x;
-            const float wt = t < len ? P.w[(b * P.T + t) * P.H + h] * kLog2e : 0.f;
             // sums in the token's block, through it and after it, by shifts along the rows of 16 lanes
             float pre = wt, suf = dpp<0x101>(wt);
             pre += dpp<0x111>(pre);
@@ -1232,7 +1312,7 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
                 after += i > g ? total : 0.f;
             }
             sm.w[lane] = wt;
-            sm.beta[lane] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
+            sm.beta[lane] = bt;
             sm.pre[lane] = pre;
             sm.suf[lane] = suf;
             sm.since[lane] = ex2(-(before + pre));
@@ -1241,24 +1321,28 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
         }
         __syncthreads();
 
+        // the next head or tile on its way, behind the work on this one
+        next = at;
+        if (++next.h == (at.hk + 1) * per) {
+            next.item += gridDim.x;
+            settle(next);
+        }
+        if (kAhead && next.item < pairs * ntile) fetch(next);
+
         // ---- products with the states before and after the tile, for this wave's channels and tokens
         {
-            const int64_t at0 = ((bh * ntile + tile) * N + c0 + l16) * N + 8 * g;
-            const float* S0 = P.states + at0;
-            const float* G1 = P.gstates + at0;
             float inner = 0.f;
             f4 sg[NX], sl[NX], ge[NX];
 #pragma unroll
             for (int x = 0; x < NX; ++x) sg[x] = sl[x] = ge[x] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                const f4 sa = load4(S0 + 32 * m), sb = load4(S0 + 32 * m + 4);
-                const f4 ga = load4(G1 + 32 * m), gb = load4(G1 + 32 * m + 4);
-                const int v = 32 * m + 8 * g;
+                const int v = 32 * m + 8 * g, k = kAhead ? m : 0;
+                if constexpr (!kAhead) fetch_states(at, m, 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) inner = fmaf(sa[q], ga[q], fmaf(sb[q], gb[q], inner));
+                for (int q = 0; q < 4; ++q) inner = fmaf(sa[k][q], ga[k][q], fmaf(sb[k][q], gb[k][q], inner));
                 bf8 s3[3];
-                split8(sa, sb, s3);
+                split8(sa[k], sb[k], s3);
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     const int t = kSub * (X0 + x) + l16;
@@ -1272,7 +1356,7 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
                     __builtin_amdgcn_sched_barrier(0);  // more of the reads at once would spill
                 }
                 bf8 g3[3];
-                split8(ga, gb, g3);
+                split8(ga[k], gb[k], g3);
 #pragma unroll
                 for (int x = 0; x < NX; x += 2) {
                     const int t = kSub * (X0 + x) + l16;
@@ -1310,14 +1394,15 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
             inner = sum_lanes(inner, 64);
             if (lane == 0) sm.inner[slice] = inner;
         }
+        if (kAhead && next.item < pairs * ntile) fetch_states_ahead(next);
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
         __builtin_amdgcn_sched_barrier(0);
         // ---- the 16 x 16 blocks: rows i = 4 g + q of block I, column j = l16 of block J
         f4 da[2], dm[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const int id = wv + kGradWaves * n;
-            if (id >= 10) continue;
+            const int id = wv + (kGradWaves - 6) * n;  // waves 6 and 7 take two; wave 0 has the rates
+            if (n > 0 && wv < 6) continue;
             __builtin_amdgcn_sched_barrier(0);
             const int I = id >= 6 ? 3 : id >= 3 ? 2 : id >= 1 ? 1 : 0, J = id - I * (I + 1) / 2;
             const int ti = kSub * I + l16, tj = kSub * J + l16;
@@ -1405,8 +1490,8 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
         // ---- dA, dM and their transposes as right operands
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const int id = wv + kGradWaves * n;
-            if (id >= 10) continue;
+            const int id = wv + (kGradWaves - 6) * n;
+            if (n > 0 && wv < 6) continue;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const Terms x = split(w ? dm[n] : da[n]);
@@ -1420,50 +1505,59 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
                 }
             }
         }
-        float rowv = 0.f, colv = 0.f, sS = 0.f, sG = 0.f;
-        if (threadIdx.x < kTile) {  // token `lane`, of block g
-            float dbeta = 0.f;
+        if (wv == 0) {  // dbeta and dw: token `lane`, of block g
+            float sS = 0.f, sG = 0.f, total = 0.f, dbeta = 0.f, later = 0.f;
+#pragma unroll
             for (int i = 0; i < NS; ++i) {
                 sS += sm.withS[i][lane];
                 sG += sm.withG[i][lane];
+                total += sm.inner[i];
             }
-            rowv = sS;
-            for (int J = 0; J < g; ++J) rowv += sm.rowsum[g * (g + 1) / 2 + J][l16];
-            for (int I = g; I < kWaves; ++I) {
-                const float x = sm.colsum[I * (I + 1) / 2 + g][l16];
-                dbeta += x;
-                colv += I > g ? x : 0.f;
-            }
-            colv = sm.beta[lane] * (colv + sG);
-            sm.rowv[lane] = rowv;
-            sm.colv[lane] = colv;
-            if (t0 + lane < P.T) P.dbeta[(b * P.T + t0 + lane) * P.H + h] = sG + dbeta;
-        }
-        __syncthreads();
-        if (threadIdx.x < kTile) {
-            // blocks' totals: rows that pair with S0, columns that pair with G, and whole blocks (I, J)
-            float c = 0.f;
-            for (int i = 0; i < NS; ++i) c += sm.inner[i];
-            c *= sm.since[kTile - 1];
-            const float rowS = sum16(sS), colG = sum16(sm.beta[lane] * sG);
+            const float beta = sm.beta[lane];
+            // sums over the blocks (I, J): down the token's column, along its row, and of the whole blocks that
+            // cross its own
+            float rowv = sS, whole = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
-                const float x = __shfl(rowS, 16 * i, 64), y = __shfl(colG, 16 * i, 64);
-                c += (i > g ? x : 0.f) + (i < g ? y : 0.f);
-            }
+            for (int I = 0; I < kWaves; ++I) {
 #pragma unroll
-            for (int I = 1; I < kWaves; ++I) {
-#pragma unroll
-                for (int J = 0; J < I; ++J) {
-                    const float x = sum16(sm.rowsum[I * (I + 1) / 2 + J][l16]);
-                    c += I > g && J < g ? x : 0.f;
+                for (int J = 0; J <= I; ++J) {
+                    const int id = I * (I + 1) / 2 + J;
+                    const float c = sm.colsum[id][l16];
+                    dbeta += J == g ? c : 0.f;
+                    if (I == J) continue;
+                    later += J == g ? c : 0.f;
+                    const float r = sm.rowsum[id][l16];
+                    rowv += I == g ? r : 0.f;
+                    const float all = sum16(r);
+                    whole += I > g && J < g ? all : 0.f;
                 }
             }
-            for (int i = 0; i < kSub; ++i) c += i >= l16 ? sm.rowv[kSub * g + i] : sm.colv[kSub * g + i];
-            c += sm.diag[lane];
-            if (t0 + lane < P.T) P.dw[(b * P.T + t0 + lane) * P.H + h] = t0 + lane < len ? -c : 0.f;
+            float colv = beta * (later + sG);
+            const float rowS = sum16(sS), colG = sum16(beta * sG);
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rowS), kSub * i));
+                const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(colG), kSub * i));
+                whole += (i > g ? x : 0.f) + (i < g ? y : 0.f);
+            }
+            // rows of the block from the token on, columns before it, by shifts along the rows of 16 lanes
+            rowv += dpp<0x101>(rowv);
+            colv = dpp<0x111>(colv);
+            rowv += dpp<0x102>(rowv);
+            colv += dpp<0x111>(colv);
+            rowv += dpp<0x104>(rowv);
+            colv += dpp<0x112>(colv);
+            rowv += dpp<0x108>(rowv);
+            colv += dpp<0x114>(colv);
+            colv += dpp<0x118>(colv);
+            const float dw = fmaf(total, sm.since[kTile - 1], whole) + rowv + colv + sm.diag[lane];
+            if (t0 + lane < P.T) {
+                const int64_t to = (b * P.T + t0 + lane) * P.H + h;
+                P.dbeta[to] = sG + dbeta;
+                P.dw[to] = t0 + lane < len ? -dw : 0.f;
+            }
         }
-
+        __syncthreads();
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
         __builtin_amdgcn_sched_barrier(0);
         // ---- k and r times the blocks, for this wave's channels and tokens
@@ -1485,13 +1579,19 @@ __global__ void __launch_bounds__(kGradThreads, (N == 64 ? 4 : 2)) delta_grad16_
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-    }
+        if (next.item != at.item) {
+            const int64_t ko = b * P.T * ks + at.hk * N;
 #pragma unroll
-    for (int x = 0; x < NX; ++x) {
-        const int64_t t = t0 + kSub * (X0 + x) + l16;
-        if (t >= P.T) continue;
-        store4(&dr[t * ks + c0 + 4 * g], drT[x]);
-        store4(&dk[t * ks + c0 + 4 * g], dkT[x]);
+            for (int x = 0; x < NX; ++x) {
+                const int64_t t = t0 + kSub * (X0 + x) + l16;
+                if (t < P.T) {
+                    store4(static_cast<uint16_t*>(P.dr) + ko + t * ks + c0 + 4 * g, drT[x]);
+                    store4(static_cast<uint16_t*>(P.dk) + ko + t * ks + c0 + 4 * g, dkT[x]);
+                }
+                drT[x] = dkT[x] = f4{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+        at = next;
     }
 }
 
@@ -1574,7 +1674,9 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
     const int64_t ntile = (a.T + kTile - 1) / kTile;
     const dim3 grid(static_cast<unsigned>(a.B * a.HK * ntile));
     if constexpr (std::is_same_v<T, uint16_t>) {
-        hipLaunchKernelGGL((delta_grad16_kernel<N>), grid, dim3(kGradThreads), 0, stream, a);
+        // one workgroup a compute unit walks the tiles, the next one's inputs arriving behind the work on this one
+        const dim3 some(grid.x < kGradGroups ? grid.x : kGradGroups);
+        hipLaunchKernelGGL((delta_grad16_kernel<N>), some, dim3(kGradThreads), 0, stream, a);
     } else {
         hipLaunchKernelGGL((delta_grad_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
     }
