@@ -442,19 +442,38 @@ __device__ __forceinline__ void prepare_block(int l16, int g, const T (*K)[kRow<
     const f4 kk = rows_product<N>(K[l16], K[l16], g);
     f4 rk = {0.f, 0.f, 0.f, 0.f};
     if constexpr (kAtt) rk = rows_product<N>(R[l16], K[l16], g);
-    float gap[4] = {0.f, 0.f, 0.f, 0.f};  // sum of w over j < l <= i
-    float run = 0.f, pre = 0.f;
-#pragma unroll
-    for (int l = 0; l < kSub; ++l) {
-        const float wl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), l));
-        const bool behind = l > l16;
-        run += behind ? wl : 0.f;
-        pre += behind ? 0.f : wl;
-        if (l / 4 == g) gap[l % 4] = run;
-    }
+    // sums through the token and after it, by shifts along the rows of 16 lanes
+    float pre = wt, suf = dpp<0x101>(wt);
+    pre += dpp<0x111>(pre);
+    suf += dpp<0x101>(suf);
+    pre += dpp<0x112>(pre);
+    suf += dpp<0x102>(suf);
+    pre += dpp<0x114>(pre);
+    suf += dpp<0x104>(suf);
+    pre += dpp<0x118>(pre);
+    suf += dpp<0x108>(suf);
     if (g == 0) {
         since[l16] = ex2(-pre);
-        put[l16] = ex2(-run) * bt;
+        put[l16] = ex2(-suf) * bt;
+    }
+    // sum of w over j < l <= i, by quads of tokens: after j in its quad, whole quads between, through i in its
+    // own; or what lies between the two when they share one
+    const int jq = l16 >> 2, jr = l16 & 3;
+    const float w1 = dpp<0x55>(wt), w2 = dpp<0xAA>(wt), w3 = dpp<0xFF>(wt);  // the quad's; by every lane
+    const float after = (jr < 1 ? w1 : 0.f) + (jr < 2 ? w2 : 0.f) + (jr < 3 ? w3 : 0.f);
+    float quad = wt + dpp<0xB1>(wt);
+    quad += dpp<0x4E>(quad);
+    const float quad1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(quad), 4));
+    const float quad2 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(quad), 8));
+    float run = jq == g ? 0.f : after;
+    run += jq == 0 && g >= 2 ? quad1 : 0.f;
+    run += jq <= 1 && g == 3 ? quad2 : 0.f;
+    float gap[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float wi = __shfl(wt, 4 * g + r, 64);
+        run += jq == g && r <= jr ? 0.f : wi;
+        gap[r] = run;
     }
     f4 m, a;
 #pragma unroll
