@@ -47,20 +47,6 @@ constexpr int kTile = 64;   // tokens staged at a time, and between saved states
 constexpr int kSub = 16;    // tokens of one triangular system
 constexpr int kWaves = 4;   // per workgroup: one per sub-block of a tile, 16 value columns each
 constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
-// A sequence is split in time when there are at most kSplitMost workgroups' worth of pairs, into segments
-// of kSplitTiles tiles or more and about kSplitGroups workgroups in all.  8192 tokens in bf16, whole and split:
-// 8 groups 647 and 78 us, 32 671 and 156, 64 609 and 273, 128 604 and 443 (N = 128: 851 and 699); a training
-// call with 256 groups took 530 us whole and 570 split.  256 groups in all were slower (32: 175), 1024 no faster.
-#ifndef WKV_DELTA_SPLIT_MOST
-#define WKV_DELTA_SPLIT_MOST 128
-#endif
-#ifndef WKV_DELTA_SPLIT_TILES
-#define WKV_DELTA_SPLIT_TILES 4
-#endif
-#ifndef WKV_DELTA_SPLIT_GROUPS
-#define WKV_DELTA_SPLIT_GROUPS 512
-#endif
-constexpr int64_t kSplitMost = WKV_DELTA_SPLIT_MOST, kSplitTiles = WKV_DELTA_SPLIT_TILES, kSplitGroups = WKV_DELTA_SPLIT_GROUPS;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -1704,14 +1690,35 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Segments of a time split, by what the walks would take, in units of one tile of a workgroup alone on its
+// compute unit (4.3 us at N = 64, 8.6 at N = 128; two at N = 64 share one in 1.55, at N = 128 only one fits).
+// A split walks the segments twice, once without outputs (0.65 of a tile) for the state and for the identity,
+// chains them (0.3 each) and launches two kernels more (1.2).  Measured whole and split, bf16:
+//   8192 tokens, N = 64:  8 pairs 647 and 74 us, 64 pairs 609 and 260, 128 pairs 604 and 431
+//   8192 tokens, N = 128: 64 pairs 851 and 677;  a training call of 128 pairs 530 and 570 (not split)
+//   512 tokens: 4 pairs 38 and 29 us;  256 tokens: 4 pairs 20 and 27 (not split)
 int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
-    const int64_t work = BH * (N / 64), tiles = (T + kTile - 1) / kTile;
+    const int64_t tiles = (T + kTile - 1) / kTile;
+    const auto walk = [&](int64_t groups) {
+        if (N != 64) return static_cast<double>((groups + 255) / 256);
+        const int64_t rest = groups % 512;
+        return 1.55 * static_cast<double>(groups / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.55);
+    };
     *per = tiles;
-    if (work < 1 || work > kSplitMost || tiles < 2 * kSplitTiles) return 1;
-    int64_t nseg = kSplitGroups / work;
-    if (nseg > tiles / kSplitTiles) nseg = tiles / kSplitTiles;
-    *per = (tiles + nseg - 1) / nseg;
-    return (tiles + *per - 1) / *per;
+    int64_t nseg = 1;
+    if (BH < 1 || BH > 512) return nseg;
+    double best = walk(BH) * static_cast<double>(tiles);
+    for (int64_t n = 2; n <= 64 && 2 * n <= tiles; ++n) {
+        const int64_t p = (tiles + n - 1) / n;
+        if ((tiles + p - 1) / p != n) continue;
+        const double t = static_cast<double>(p) * (0.65 * walk(2 * BH * (n - 1)) + walk(BH * n)) + 0.3 * static_cast<double>(n) + 1.2;
+        if (t < best) {
+            best = t;
+            nseg = n;
+            *per = p;
+        }
+    }
+    return nseg;
 }
 
 hipError_t launch_delta_chain(const DeltaChainArgs& a, hipStream_t stream) {
