@@ -532,8 +532,10 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  * workspace NULL (no time split), or wkv_delta_forward_workspace_bytes() bytes,
  *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
  * r, k, v, o, s_in, s_out, ckpt are 16-byte aligned (WKV_EALIGN otherwise).
- * WKV_EINVAL also for another N or an H that HK does not divide.
- * A non-finite input reaches every output of its 64-token block and all after.
+ * WKV_EINVAL also for another N or an H that HK does not divide; WKV_ESIZE
+ * from H N = 2^22.
+ * A non-finite input may reach every output of its head from the 64 tokens it is
+ * among on.
  */
 wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
                                const int32_t* lengths, const float* w, const float* beta,

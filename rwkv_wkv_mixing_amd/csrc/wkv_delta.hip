@@ -19,10 +19,10 @@
 // the state is cleared) gives factors in [0, 1].
 //
 // Lane layout.  A wave owns 16 value columns of the state: N / 16 accumulators of the 16 x 16 products,
-// where lane (l16, g) holds rows 4 g .. 4 g + 3 of column l16.  As the right operand of the next product
-// the same registers are already in place when the contracted index runs in that order: register r of
-// group g is row 4 g + r.  The left operand is then read from its rows in the same order.  So neither
-// the state nor e, nor anything between the products, ever crosses lanes.
+// where lane (l16, g) holds four rows of column l16 of each (which four: state_row).  As the right
+// operand of the next product the same registers are already in place when the contracted index runs in
+// that order; the left operand is then read from its rows in the same order.  So neither the state nor
+// e, nor anything between the products, ever crosses lanes.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -45,7 +45,7 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 64;   // tokens staged at a time, and between saved states
 constexpr int kSub = 16;    // tokens of one triangular system
-constexpr int kWaves = 4;   // per workgroup: one per sub-block of a tile, 16 value columns each
+constexpr int kWaves = 4;   // 16-token blocks of a tile; waves of the step and the float32 gradient kernel
 constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -314,9 +314,11 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b,
 //   one preparing wave per block of a tile, which meanwhile writes out its 16 rows of the last tile's
 //   results, stages its 16 rows of the next tile, and finds that block's decays, X and A from them (no
 //   other wave's rows are needed), its loads for the tile after that already on their way.
-// All buffers are double, and one barrier a tile is all that is left of waiting for each other.  Before,
-// four waves did both in turn with three barriers a tile: 5.2 us a tile and workgroup alone on its compute
-// unit at N = 64 (12 400 cycles, of which the blocks' own chain of products is about two thirds).
+// All buffers are double, and one barrier a tile is all that is left of waiting for each other: at N = 64
+// 4.3 us a tile for a workgroup alone on its compute unit and 1.55 for two side by side.  (Four waves that
+// did both in turn, with three barriers a tile, took 5.2.)
+// What is left is the chain of dependent products of the four blocks one after the other, and the vector
+// instructions that split the state, issued on about 60 % of the cycles of a full card.
 //
 // Adjoint, for L = <go, o> + <ds_out, S_T>, over a block with G the gradient of the state after it:
 //     y      = A^T go + diag(beta until) K G
@@ -1100,8 +1102,9 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 // Everything the tile needs of a head is on its way before the first of it is put into LDS, and chains of
 // dependent products are taken in turn.  Held to 128 registers for two workgroups a compute unit at N = 64 it
 // spilled and was no faster (405 to 440 us against 400).
-// LDS rows are not padded (two workgroups a compute unit at N = 64): the 16-byte piece q of row t lies at
-// q ^ swizzle(t), so that 16 rows' pieces q meet 16 different bank groups.
+// LDS rows are not padded (they would not fit at N = 128): the 16-byte piece q of row t lies at q ^ swizzle(t),
+// so that 16 rows' pieces q meet 16 different bank groups.  8 x 1024 tokens of 64 heads of 64 take 370 us for
+// 870 MB (2.4 TB/s): the phases' products and LDS traffic, which meet at four barriers a tile.
 constexpr int kGradWaves = 8;
 constexpr unsigned kGradGroups = 256;  // compute units
 constexpr int kGradThreads = 64 * kGradWaves;

@@ -8,7 +8,7 @@
 //
 // Streaming work: every element is read once and stays in registers between the statistics and the
 // outputs.  The mean is taken first and the squares of what is left of it second, so a mean far above
-// the deviation costs no digits.  A head is held by 4 .. 64 lanes of a wave (8 elements each, 16 with
+// the deviation costs no digits.  A head is held by 1 .. 64 lanes of a wave (8 elements each, 16 with
 // more than 512 channels) and its sums meet by shuffles; a row of a block norm by 64 .. 1024 threads.
 //
 // Backward, with g the gradient of norm(y) (that of z times act(gate) weight):
@@ -156,10 +156,8 @@ __device__ __forceinline__ void load_or(const float* p, int64_t c, float otherwi
 // 1 / sqrt, within 1 ulp
 __device__ __forceinline__ float rsqrt1(float x) { return __builtin_amdgcn_rsqf(x); }
 
-#ifndef WKV_BN_NV2
-#define WKV_BN_NV2 1024
-#endif
 constexpr int kBlock = 256;
+constexpr int kPairs = 1024;      // channels from which a thread of the block norm holds two vectors
 constexpr int kScalarVecs = 16;  // elements a lane of the element-by-element path: G up to 1024
 
 // What a lane holds of its head: NV vectors of V channels, vector i at channel (i lanes + lane) V.
@@ -270,7 +268,8 @@ __global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
                 }
             }
         }
-        const float inv = rsqrt1(sum_lanes(sq, lanes) * inv_g + P.eps);
+        const float scaled = sum_lanes(sq, lanes) * inv_g + P.eps;
+        const float inv = live ? rsqrt1(scaled) : 0.f;  // (a slot without a row adds 0 to the sums, with eps 0 too)
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -744,15 +743,16 @@ hipError_t launch_block_bwd(const BlockNormArgs& a, hipStream_t stream) {
     return e == hipSuccess ? launch_reduce(r, stream) : e;
 }
 
-// Threads that hold a row: 8 channels each from the smallest count that does (the forward 16 from
-// WKV_BN_NV2 channels), or, off the 16-byte grid, 1024 threads of single elements.
+// Threads that hold a row: 8 channels each from the smallest count that does (the forward 16 from kPairs
+// channels, half the threads to sum over: 8192 rows of 4096 with everything given 75 us against 80); or, off
+// the 16-byte grid, 1024 threads of single elements.
 template <typename TX, typename TY>
 hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     a.slots = block_norm_slots(a.rows, a.C);
     a.threads = !a.vec ? 1024 : a.C <= 512 ? 64 : static_cast<int>(pow2_at_least(a.C / 8));
     if (!bwd) {
         if (!a.vec) return launch_block_fwd<TX, TY, 1, 8>(a, stream);
-        if (a.C < WKV_BN_NV2) return launch_block_fwd<TX, TY, 8, 1>(a, stream);
+        if (a.C < kPairs) return launch_block_fwd<TX, TY, 8, 1>(a, stream);
         a.threads /= 2;
         return launch_block_fwd<TX, TY, 8, 2>(a, stream);
     }

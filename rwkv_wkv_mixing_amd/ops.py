@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -825,6 +826,13 @@ def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_st
     return _launch_on(dev, bind, "wkv_delta_backward", lib.wkv_delta_backward, args, (dr, dk, dv, dw, dbeta, ds), locals() if bind else None)
 
 
+def _on_grid(grad):
+    """A gradient as the calls take it: contiguous, and (a view into another tensor's gradient may start
+    anywhere) on the 16-byte grid."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
 class DeltaFunction(torch.autograd.Function):
     """Autograd wrapper: (o, state) = delta_forward(...); backward through delta_backward."""
 
@@ -838,12 +846,13 @@ class DeltaFunction(torch.autograd.Function):
         return o, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, go, gstate):
         w, beta, r, k, v, state_in, lengths, ckpt = ctx.saved_tensors
-        go = torch.zeros_like(v) if go is None else go.contiguous()
+        go = torch.zeros_like(v) if go is None else _on_grid(go)
         dr, dk, dv, dw, dbeta, ds = delta_backward(
             w, beta, r, k, v, go, lengths=lengths, state_in=state_in,
-            grad_state_out=None if gstate is None else gstate.contiguous(),
+            grad_state_out=None if gstate is None else _on_grid(gstate),
             need_state_grad=state_in is not None and ctx.needs_input_grad[5], ckpt=ckpt)
         return dw, dbeta, dr, dk, dv, ds, None
 
@@ -935,6 +944,7 @@ class HeadNormFunction(torch.autograd.Function):
         return head_norm(y, weight, bias, gate, **ctx.kw)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gout):
         y, weight, bias, gate = ctx.saved_tensors
         return *head_norm_backward(y, gout.contiguous(), weight, bias, gate, **ctx.kw), None, None, None, None
@@ -1015,6 +1025,7 @@ class BlockNormFunction(torch.autograd.Function):
         return x_out, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gx, gh):
         x_out, y, pre_w, pre_b, gate, post_w, post_b, scale = ctx.saved_tensors
         g = block_norm_backward(x_out, y, torch.zeros_like(y) if gh is None else gh.contiguous(), pre_w, pre_b,

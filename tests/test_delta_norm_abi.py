@@ -119,7 +119,8 @@ def test_head_norm_refusals(lib, bwd):
         assert head(lib, bwd, **bad) == L.WKV_EINVAL, bad
     for bad in (dict(yd=L.WKV_BF16, dt=L.WKV_F32), dict(yd=5), dict(dt=-1)):
         assert head(lib, bwd, **bad) == L.WKV_EDTYPE, bad
-    for bad in (dict(rows=1 << 31, H=1), dict(rows=1 << 40, H=1 << 30), dict(H=1 << 26, G=1024)):
+    for bad in (dict(rows=1 << 31, H=1), dict(rows=1 << 40, H=1 << 30), dict(H=1 << 26, G=1024),
+                dict(rows=0, H=1 << 58)):
         assert head(lib, bwd, **bad) == L.WKV_ESIZE, bad
     for bad in (dict(y=X + 2), dict(weight=X + 1), dict(bias=X + 2), dict(gate=X + 1)):
         assert head(lib, bwd, **bad) == L.WKV_EALIGN, bad

@@ -208,3 +208,116 @@ def test_bound_calls_and_refused_shapes():
         O.block_norm(x, v, weight, post_b=weight)
     with pytest.raises(TypeError):
         O.block_norm(x, v.float(), weight)
+
+
+@pytest.mark.parametrize("rows,G,act", [(1, 64, "silu"), (5, 64, "none"), (333, 80, "sigmoid")])
+def test_head_norm_without_eps(rows, G, act):
+    """eps 0 is allowed: slots of a workgroup that hold no row must not add 0 * inf to the weights' sums."""
+    O = ops()
+    g = torch.Generator().manual_seed(rows)
+    y, gout, gate = (torch.randn(rows, 3 * G, generator=g, dtype=torch.float64) for _ in range(3))
+    weight = torch.rand(3 * G, generator=g, dtype=torch.float64) + 0.5
+    leaves = [t.requires_grad_() for t in (y, weight, gate)]
+    a = {"none": gate, "sigmoid": torch.sigmoid(gate), "silu": torch.nn.functional.silu(gate)}[act]
+    (rms(y.view(rows, 3, G), 0.0).reshape(rows, 3 * G) * weight * a * gout).sum().backward()
+    own = [t.detach().float().to(DEV) for t in (y, gout, weight)]
+    dy, dw, _, dg = O.head_norm_backward(*own, None, gate.detach().float().to(DEV), heads=3, act=act, eps=0.0)
+    # a sum of G (dy) or rows (dw) terms, each of some ten roundings
+    for got, leaf, n in zip((dy, dw, dg), leaves, (G, rows, 1)):
+        err = (got.double().cpu() - leaf.grad).norm() / leaf.grad.norm()
+        assert err <= U * (16 + n), (float(err), n)
+
+
+def test_gradients_that_are_views():
+    """A gradient may arrive as a view that starts off the 16-byte grid, or is not contiguous."""
+    O = ops()
+    w, beta, r, k, v, go, S, x = step_case(9, 40, 2, 64, torch.bfloat16)
+    want = O.delta_backward(w, beta, r, k, v, go, state_in=S, grad_state_out=S, need_state_grad=True)
+    for odd in (True, False):
+        leaves = [t.clone().requires_grad_() for t in (w, beta, r, k, v, S)]
+        o, s1 = O.delta_rule(*leaves)
+        pad = torch.zeros(3, device=DEV, requires_grad=True)
+        if odd:
+            out = torch.cat([pad.bfloat16(), o.reshape(-1)]), torch.cat([pad, s1.reshape(-1)])
+            grads = torch.cat([pad.bfloat16(), go.reshape(-1)]), torch.cat([pad, S.reshape(-1)])
+        else:
+            out = o.transpose(0, 1), s1.transpose(2, 3)
+            grads = go.transpose(0, 1).contiguous(), S.transpose(2, 3).contiguous()
+        torch.autograd.backward(out, [g.detach() for g in grads])
+        for leaf, g in zip(leaves, (want[3], want[4], want[0], want[1], want[2], want[5])):
+            assert torch.equal(leaf.grad, g)
+
+
+def test_second_derivatives_are_refused():
+    O = ops()
+    w, beta, r, k, v, go, S, x = step_case(9, 20, 2, 64, torch.float32)
+    v.requires_grad_()
+    ones = torch.ones(128, device=DEV)
+    for out in (O.delta_rule(w, beta, r, k, v)[0], O.head_norm_gated(v, ones, None, x, heads=2), O.block_join(x, v, ones)[1]):
+        (g,) = torch.autograd.grad(out.square().sum(), v, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing: each gives what it gives alone."""
+    O = ops()
+    cases = [step_case(s, 700, 2, 64, torch.bfloat16) for s in (1, 2)]
+    weight = torch.ones(128, device=DEV)
+
+    def step(w, beta, r, k, v, go, S, x):
+        o, s1 = O.delta_forward(w, beta, r, k, v, state_in=S, return_state=True)  # split in time
+        d = O.delta_backward(w, beta, r, k, v, go, state_in=S, grad_state_out=s1)
+        g = O.block_norm_backward(x, o, go, weight, gate=v)
+        h = O.head_norm_backward(o, go, weight[:64], heads=2)
+        return [o, s1, *d[:5], *(t for t in (*g.values(), *h) if t is not None)]
+
+    want = [step(*c) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(step(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            for j, (a, b) in enumerate(zip(run, want[i])):
+                assert torch.equal(a, b), (i, j)
+
+
+def test_large_offsets():
+    """Arrays of more than 2^32 bytes and 2^31 elements: the last batch row, which lies behind that, holds the
+    first one's data and must give the first one's results bit for bit (which other tests check)."""
+    O = ops()
+    B, T, H, N = 3, 300000, 40, 64  # 2.3e9 elements
+    C = H * N
+    g = torch.Generator(device=DEV).manual_seed(0)
+
+    def thrice(*shape, dtype=torch.bfloat16, scale=1.0):
+        x = torch.empty((B, *shape), dtype=dtype, device=DEV)
+        for t0 in range(0, T, 70000):
+            part = (torch.randn((min(70000, T - t0), *shape[1:]), generator=g, device=DEV) * scale).to(dtype)
+            x[0, t0:t0 + 70000], x[1, t0:t0 + 70000], x[2, t0:t0 + 70000] = part, 0, part
+        return x
+
+    r, k, v = thrice(T, C // 2), thrice(T, C // 2, scale=0.1), thrice(T, C)
+    w, beta = thrice(T, H, dtype=torch.float32).abs_(), thrice(T, H, dtype=torch.float32).abs_().clamp_(max=1)
+    lens = torch.tensor([T - 5, 1, T - 5], dtype=torch.int32, device=DEV)
+    o, S = O.delta_forward(w, beta, r, k, v, lengths=lens, return_state=True)
+    assert torch.equal(S[0], S[2]) and bool(torch.isfinite(S).all()) and float(S[0].abs().max()) > 0
+    assert torch.equal(o[0], o[2]) and not bool(o[:, T - 5:].any()) and bool(o[2, T - 6].any())
+    grads = O.delta_backward(w, beta, r, k, v, o, lengths=lens)
+    for t in grads[:5]:
+        assert torch.equal(t[0], t[2]) and not bool(t[:, T - 5:].any()) and bool(t[2, T - 6].any())
+    del grads
+    weight = torch.ones(C, device=DEV)
+    n = O.head_norm(v, weight, None, o, heads=H)
+    assert torch.equal(n[0], n[2]) and bool(n[2, T - 6].any())
+    x1, h = O.block_norm(v, o, weight, gate=n, post_w=weight)
+    assert torch.equal(x1[0], x1[2]) and torch.equal(h[0], h[2]) and bool(h[2, T - 1].any())
+    back = O.block_norm_backward(x1, o, h, weight, gate=n, post_w=weight)
+    assert torch.equal(back["dx"][0], back["dx"][2]) and torch.equal(back["dy"][0], back["dy"][2])
+    back = O.head_norm_backward(v, h, weight, None, o, heads=H)
+    assert torch.equal(back[0][0], back[0][2]) and torch.equal(back[3][0], back[3][2])
