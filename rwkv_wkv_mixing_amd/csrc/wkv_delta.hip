@@ -46,7 +46,7 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 constexpr int kTile = 64;   // tokens staged at a time, and between saved states
 constexpr int kSub = 16;    // tokens of one triangular system
 constexpr int kWaves = 4;   // 16-token blocks of a tile; waves of the step and the float32 gradient kernel
-constexpr int kPadM = kSub + 4;  // floats a row of the 16 x 16 tables
+constexpr int kPadM = kSub + 4;  // floats a row of the float32 gradient kernel's 16 x 16 tables
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -86,35 +86,56 @@ __device__ __forceinline__ f4 mma16(f4 a, f4 b, f4 c) {
     return c;
 }
 
-// Elements a row of a staged [kTile, N] array: padded by 16 bytes, so that 16 lanes reading 16
-// consecutive rows start in different banks.
+// Elements a row of a staged [kTile, N] array, and where element c of row t lies.  Float32 rows are padded by
+// 16 bytes, so that 16 lanes reading 16 consecutive rows start in different banks.  bf16 rows are not (two
+// workgroups a compute unit, or all of a tile's terms, would not fit): the 16-byte piece q of row t lies at
+// q ^ swizzle(t), the same for a row of every 16, so that 16 rows' pieces q meet 16 different bank groups.
 template <typename T, int N>
-constexpr int kRow = N + 16 / static_cast<int>(sizeof(T));
+constexpr int kRow = sizeof(T) == 2 ? N : N + 4;
+
+template <int N>
+__device__ __forceinline__ int swizzled(int t, int c) {
+    const int s = N == 64 ? (t >> 1) & 7 : t & 15;
+    return (((c >> 3) ^ s) << 3) | (c & 7);
+}
+template <typename T, int N>
+__device__ __forceinline__ int place(int t, int c) {
+    return t * kRow<T, N> + (sizeof(T) == 2 ? swizzled<N>(t, c) : c);
+}
 
 // ---- products with bf16 inputs -------------------------------------------------------------------
 // A bf16 input is exact as an operand of the bf16 products, which run 16 times as fast as the float32
-// ones.  A float32 factor x is given as three bf16 terms, x = hi + mid + lo, each the upper half of
-// what the ones before leave: 24 bits in all, so the split is exact and the products summed in float32
-// are those of float32 operands.  Where a result is rounded to bf16 and goes nowhere else, hi + mid
-// (16 bits, off by at most 2^-16) is enough: rounding moves it by up to 2^-8.
+// ones.  A float32 factor x is given as three bf16 terms, x = hi + mid + lo, each what the ones before leave,
+// rounded: 8 bits and a sign a term, so the split is exact and the products summed in float32 are those of
+// float32 operands.  Where a result is rounded to bf16 and goes nowhere else, hi + mid (off by at most 2^-18)
+// is enough: rounding moves it by up to 2^-8.
 struct Terms {
     u32x2 hi, mid, lo;
 };
 
-__device__ __forceinline__ uint32_t uppers(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+// What two rounded values leave of x: one dot product with (-1, 0) or (0, -1) each, exact, instead of a
+// widening and a subtraction (14 instructions for a split of four instead of 22).  The factors are kept from
+// the compiler, which turns (-1, 0) into an inline constant that multiplies the upper value.
+__device__ __forceinline__ f2 left_of(uint32_t rounded, f2 x) {
+    uint32_t first = 0x0000bf80u, second = 0xbf800000u;
+    asm("" : "+s"(first), "+s"(second));
+    const bf2 h = __builtin_bit_cast(bf2, rounded);
+    return f2{__builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf2, first), x[0], false),
+              __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf2, second), x[1], false)};
+}
 
 __device__ __forceinline__ Terms split(f4 x) {
-    uint32_t h[4], m[4], l[4];
+    Terms t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = __float_as_uint(x[i]);
-        const float rest = x[i] - __uint_as_float(h[i] & 0xffff0000u);
-        m[i] = __float_as_uint(rest);
-        l[i] = __float_as_uint(rest - __uint_as_float(m[i] & 0xffff0000u));
+    for (int i = 0; i < 2; ++i) {
+        const f2 a = {x[2 * i], x[2 * i + 1]};
+        t.hi[i] = pk2(a[0], a[1]);
+        const f2 b = left_of(t.hi[i], a);
+        t.mid[i] = pk2(b[0], b[1]);
+        const f2 c = left_of(t.mid[i], b);
+        t.lo[i] = pk2(c[0], c[1]);
     }
-    return Terms{{uppers(h[0], h[1]), uppers(h[2], h[3])},
-                 {uppers(m[0], m[1]), uppers(m[2], m[3])},
-                 {uppers(l[0], l[1]), uppers(l[2], l[3])}};
+    return t;
 }
 
 __device__ __forceinline__ bf8 pair(u32x2 a, u32x2 b) { return __builtin_bit_cast(bf8, u32x4{a[0], a[1], b[0], b[1]}); }
@@ -129,42 +150,50 @@ __device__ __forceinline__ f4 mfma32(bf8 a, bf8 b, f4 c) { return __builtin_amdg
 // the matching left operand.
 __device__ __forceinline__ constexpr int state_row(int c, int g, int r) { return 32 * (c >> 1) + 8 * g + 4 * (c & 1) + r; }
 
+// A block's rows are given by the address of the first of its 16.
+
 // acc[i][j] = sum over the N channels of a row i of A and a row j of B (rows l16 of each), both staged
 template <int N>
-__device__ __forceinline__ f4 rows_product(const uint16_t* a, const uint16_t* b, int g) {
+__device__ __forceinline__ f4 rows_product(const uint16_t* a, const uint16_t* b, int l16, int g) {
     f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < N / 32; ++m) acc = mfma32(raw8(a + 32 * m + 8 * g), raw8(b + 32 * m + 8 * g), acc);
+    for (int m = 0; m < N / 32; ++m) {
+        const int at = place<uint16_t, N>(l16, 32 * m + 8 * g);
+        acc = mfma32(raw8(a + at), raw8(b + at), acc);
+    }
     return acc;
 }
 template <int N>
-__device__ __forceinline__ f4 rows_product(const float* a, const float* b, int g) {
+__device__ __forceinline__ f4 rows_product(const float* a, const float* b, int l16, int g) {
     f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < N / 16; ++c) acc = mma16(load4(a + 16 * c + 4 * g), load4(b + 16 * c + 4 * g), acc);
+    for (int c = 0; c < N / 16; ++c) {
+        const int at = place<float, N>(l16, 16 * c + 4 * g);
+        acc = mma16(load4(a + at), load4(b + at), acc);
+    }
     return acc;
 }
 
-// A block's 16 rows of a staged array as a left operand (row l16 a lane): bf16 rows are held in registers,
-// so that they are read while the state is still being split; float32 rows are read as they are used.
+// A block's rows as a left operand (row l16 a lane): bf16 rows are held in registers, so that they are read
+// while the state is still being split; float32 rows are read as they are used.
 template <typename T, int N>
 struct LeftRows;
 
 template <int N>
 struct LeftRows<float, N> {
     const float* row;
-    __device__ __forceinline__ LeftRows(const float* p, int) : row(p) {}
+    __device__ __forceinline__ LeftRows(const float* x, int l16, int) : row(x + place<float, N>(l16, 0)) {}
 };
 template <int N>
 struct LeftRows<uint16_t, N> {
     bf8 a[N / 32];
-    __device__ __forceinline__ LeftRows(const uint16_t* p, int g) {
+    __device__ __forceinline__ LeftRows(const uint16_t* x, int l16, int g) {
 #pragma unroll
-        for (int m = 0; m < N / 32; ++m) a[m] = raw8(p + 32 * m + 8 * g);
+        for (int m = 0; m < N / 32; ++m) a[m] = raw8(x + place<uint16_t, N>(l16, 32 * m + 8 * g));
     }
 };
 
-// The state's 16 columns as a right operand, for one block.
+// The state's 16 columns as a right operand.
 template <typename T, int N>
 struct StateOperand;
 
@@ -213,10 +242,10 @@ struct StateOperand<uint16_t, N> {
     }
 };
 
-// A block's 16 rows of a staged array as the left operand of S += X^T u: four tokens of one channel a lane,
-// in the state's row order.  bf16: one transposing LDS read gives a lane its four tokens of one channel (in
-// each group of 16 lanes, lane 4 e + p reads four channels of token e, and lane j receives element j % 4 of
-// lane 4 e + j / 4's read for e = 0 .. 3).
+// The rows of kG blocks as the left operand of S += X^T u: four tokens of one channel a lane, in the state's
+// row order.  bf16: one transposing LDS read gives a lane its four tokens of one channel (in each group of 16
+// lanes, lane 4 e + p reads four channels of token e, and lane j receives element j % 4 of lane 4 e + j / 4's
+// read for e = 0 .. 3).
 __device__ __forceinline__ u32x2 read_tr(const uint16_t* at) {
     const s4 raw = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at);
     return __builtin_bit_cast(u32x2, raw);
@@ -227,48 +256,52 @@ struct LeftCols;
 
 template <int N>
 struct LeftCols<float, N> {
-    const float (*x)[kRow<float, N>];
-    int l16;
-    __device__ __forceinline__ LeftCols(const float (*X)[kRow<float, N>], int tb, int l16_, int g) : x(X + tb + 4 * g), l16(l16_) {}
-    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], f4 u) const {
+    const float* x;
+    int l16, g;
+    __device__ __forceinline__ LeftCols(const float* X, int l16_, int g_) : x(X), l16(l16_), g(g_) {}
+    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const f4 (&u)[1]) const {
 #pragma unroll
         for (int c = 0; c < N / 16; ++c) {
             f4 a;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a[q] = x[q][state_row(c, l16 >> 2, l16 & 3)];
-            S[c] = mma16(a, u, S[c]);
+            for (int q = 0; q < 4; ++q) a[q] = x[place<float, N>(4 * g + q, state_row(c, l16 >> 2, l16 & 3))];
+            S[c] = mma16(a, u[0], S[c]);
         }
     }
 };
 template <int N>
 struct LeftCols<uint16_t, N> {
-    u32x2 a[N / 16];
-    __device__ __forceinline__ LeftCols(const uint16_t (*X)[kRow<uint16_t, N>], int tb, int l16, int g) {
+    u32x2 a[2][N / 16];
+    __device__ __forceinline__ LeftCols(const uint16_t* X, int l16, int g) {
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) a[c] = read_tr(&X[tb + 4 * g + (l16 >> 2)][state_row(c, l16 & 3, 0)]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < N / 16; ++c)
+                a[j][c] = read_tr(X + j * kSub * kRow<uint16_t, N> +
+                                  place<uint16_t, N>(4 * g + (l16 >> 2), state_row(c, l16 & 3, 0)));
     }
-    // hi and mid of u share one 32-index product over the same tokens twice
-    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], f4 u) const {
-        const Terms t = split(u);
-        const bf8 b = pair(t.hi, t.mid), b2 = pair(t.lo, u32x2{0, 0});
+    // the two blocks' tokens are the 32 contracted indices
+    __device__ __forceinline__ void add_outer(f4 (&S)[N / 16], const f4 (&u)[2]) const {
+        const Terms t = split(u[0]), t2 = split(u[1]);
+        const bf8 b[3] = {pair(t.lo, t2.lo), pair(t.mid, t2.mid), pair(t.hi, t2.hi)};
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) S[c] = mfma32(pair(a[c], a[c]), b2, S[c]);
+        for (int i = 0; i < 3; ++i)
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) S[c] = mfma32(pair(a[c], a[c]), b, S[c]);
+            for (int c = 0; c < N / 16; ++c) S[c] = mfma32(pair(a[0][c], a[1][c]), b[i], S[c]);
     }
 };
 
-// Four tokens tb + 4 g .. of column c0 + l16 of a staged array of value columns.
-template <int ROW>
-__device__ __forceinline__ f4 value_column(const float (*X)[ROW], int tb, int c0, int l16, int g) {
+// Four tokens 4 g .. of a block, column c0 + l16, of a staged array of value columns.
+template <int N>
+__device__ __forceinline__ f4 value_column(const float* X, int c0, int l16, int g) {
     f4 x;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = X[tb + 4 * g + q][c0 + l16];
+    for (int q = 0; q < 4; ++q) x[q] = X[place<float, N>(4 * g + q, c0 + l16)];
     return x;
 }
-template <int ROW>
-__device__ __forceinline__ f4 value_column(const uint16_t (*X)[ROW], int tb, int c0, int l16, int g) {
-    const u32x2 x = read_tr(&X[tb + 4 * g + (l16 >> 2)][c0 + 4 * (l16 & 3)]);
+template <int N>
+__device__ __forceinline__ f4 value_column(const uint16_t* X, int c0, int l16, int g) {
+    const u32x2 x = read_tr(X + place<uint16_t, N>(4 * g + (l16 >> 2), c0 + 4 * (l16 & 3)));
     return f4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
               __uint_as_float(x[1] & 0xffff0000u)};
 }
@@ -347,16 +380,24 @@ struct WalkArgs {
     float* states;        // the states before every 64 tokens, or NULL; adjoint: their gradients after
 };
 
+// Blocks that the state is split for at once (bf16; see the pairs below).
+template <typename T>
+constexpr int kPair = sizeof(T) == 2 ? 2 : 1;
+
 template <typename T, int N>
 struct WalkShared {
-    static constexpr int kTok = kWalkTile<T, N>;
-    T k[2][kTok][kRow<T, N>], r[2][kTok][kRow<T, N>];
-    T v[2][kTok][kRow<T, N>];                     // x and, block by block, y in its place
+    static constexpr int kTok = kWalkTile<T, N>, kPairs = kTok / (kSub * kPair<T>);
+    T k[2][kTok * kRow<T, N>], r[2][kTok * kRow<T, N>];
+    T v[2][kTok * kRow<T, N>];                    // x and, block by block, y in its place
     float since[2][kTok];                         // decay from the block's start through the token
     float put[2][kTok];                           // beta until: the write strength, decayed to the block's end
-    float inv[2][kTok / kSub][kSub][kPadM];       // X or its transpose; before that M diag(beta)
-    float att[2][kTok / kSub][kSub][kPadM];       // A or its transpose
+    float inv[2][kTok / kSub][kSub * kSub];       // X or its transpose; before that M diag(beta)
+    float att[2][kTok / kSub][kSub * kSub];       // A or its transpose
+    uint16_t off[kPair<T> == 2 ? 2 * kPairs : 1][6][64][4];  // terms of what a pair's blocks do to each other, per lane
 };
+
+// The piece of four elements 4 q .. of row i of a 16 x 16 table: 16 rows' pieces q lie in different banks.
+__device__ __forceinline__ int piece(int i, int q) { return 16 * i + 4 * (q ^ ((i >> 1) & 3)); }
 
 // A wave's 16 rows of N elements between memory (from `base`, the same for the wave) and LDS.  Rows from
 // `left` on are zeros and not read, or not written.  Offsets from the base are 32 bits (the host's checks
@@ -378,12 +419,12 @@ struct BlockRows {
             if (row + i * kRows < left) x[i] = *reinterpret_cast<const u32x4*>(p + at);
         }
     }
-    __device__ __forceinline__ void put(T (*dst)[kRow<T, N>], int lane) const {
+    __device__ __forceinline__ void put(T* dst, int lane) const {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            *reinterpret_cast<u32x4*>(&dst[lane / kRowVecs + i * kRows][lane % kRowVecs * kPer]) = x[i];
+            *reinterpret_cast<u32x4*>(dst + place<T, N>(lane / kRowVecs + i * kRows, lane % kRowVecs * kPer)) = x[i];
     }
-    static __device__ __forceinline__ void flush(const T (*src)[kRow<T, N>], T* base, int stride, int left, int lane) {
+    static __device__ __forceinline__ void flush(const T* src, T* base, int stride, int left, int lane) {
         const int row = lane / kRowVecs;
         const uint32_t at = static_cast<uint32_t>(row * stride + lane % kRowVecs * kPer);
 #pragma unroll
@@ -391,7 +432,7 @@ struct BlockRows {
             T* p = base + static_cast<int64_t>(i * kRows) * stride;
             if (row + i * kRows < left)
                 *reinterpret_cast<u32x4*>(p + at) =
-                    *reinterpret_cast<const u32x4*>(&src[row + i * kRows][lane % kRowVecs * kPer]);
+                    *reinterpret_cast<const u32x4*>(src + place<T, N>(row + i * kRows, lane % kRowVecs * kPer));
         }
     }
 };
@@ -420,16 +461,91 @@ __device__ __forceinline__ void load_state(const float* from, f4 (&S)[N / 16], i
         for (int q = 0; q < 4; ++q) S[c][q] = (from + state_row(c, 0, q) * N)[at];
 }
 
+// Pairs (bf16).  Splitting the state for each block of 16 tokens took as long as the products, so two blocks
+// 0, 1 share one split: K_j S and R_j S are taken from the state before both, and what block 0 does to block 1
+// goes through two more 16 x 16 tables, their decays taken apart at the border of the blocks:
+//     e_1 = X_1 (v_1 - total_0 since_1 K_1 S - since_1 (K_1 K_0^T) put_0 e_0),   o_1 += since_1 (R_1 K_0^T) put_0 e_0
+// Adjoint: block 1 acts on block 0,
+//     y_0 += put_0 ((K_0 R_1^T) since_1 go_1 - (K_0 K_1^T) since_1 lambda_1)
+// The tables are split into terms here, once; the wave that prepares the block they lead to reads the other
+// one's rows itself, in the order of the products, so it waits for no other wave.  The state's update sums
+// over both blocks' tokens at once.
+template <typename T, int N, bool kAdj>
+struct Partner {};
+
+template <int N, bool kAdj>
+struct Partner<uint16_t, N, kAdj> {
+    bf8 k[N / 32], r[kAdj ? N / 32 : 1];
+
+    // rows of the other block from `k0` and `r0`, zeros from `left` on
+    __device__ __forceinline__ void fetch(const uint16_t* k0, const uint16_t* r0, int stride, int left, int l16, int g) {
+        const uint32_t at = static_cast<uint32_t>(l16 * stride + 8 * g);
+        const bf8 none = __builtin_bit_cast(bf8, u32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) {
+            k[m] = none;
+            if constexpr (kAdj) r[m] = none;
+        }
+        if (l16 < left) {
+#pragma unroll
+            for (int m = 0; m < N / 32; ++m) {
+                k[m] = raw8(k0 + 32 * m + at);
+                if constexpr (kAdj) r[m] = raw8(r0 + 32 * m + at);
+            }
+        }
+    }
+    // x, a row l16 of a table at columns 4 g .., as its terms
+    template <int kCount>
+    static __device__ __forceinline__ void put(f4 x, uint16_t (*to)[64][4], int lane) {
+        const Terms t = split(x);
+        *reinterpret_cast<u32x2*>(to[0][lane]) = t.hi;
+        *reinterpret_cast<u32x2*>(to[1][lane]) = t.mid;
+        if constexpr (kCount == 3) *reinterpret_cast<u32x2*>(to[2][lane]) = t.lo;
+    }
+    // scale: of row l16
+    template <bool kAtt>
+    __device__ __forceinline__ void connect(const uint16_t* K, const uint16_t* R, float scale, uint16_t (*off)[64][4], int l16,
+                                            int g) const {
+        f4 kk = {0.f, 0.f, 0.f, 0.f}, rk = kk;
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) {
+            const int at = place<uint16_t, N>(l16, 32 * m + 8 * g);
+            kk = mfma32(k[m], raw8(K + at), kk);
+            if constexpr (kAdj) rk = mfma32(r[m], raw8(K + at), rk);
+            else if constexpr (kAtt) rk = mfma32(k[m], raw8(R + at), rk);
+        }
+        put<3>((kAdj ? -scale : scale) * kk, off, l16 + 16 * g);
+        if constexpr (kAdj) put<3>(scale * rk, off + 3, l16 + 16 * g);
+        else if constexpr (kAtt) put<2>(-scale * rk, off + 3, l16 + 16 * g);
+    }
+};
+
+// A table's product with t: all three terms, or (kTerms 2) for a result that is rounded to bf16.
+template <int kTerms>
+__device__ __forceinline__ f4 times_table(const uint16_t (*off)[64][4], const Terms& t, int lane) {
+    const u32x2 hi = *reinterpret_cast<const u32x2*>(off[0][lane]), mid = *reinterpret_cast<const u32x2*>(off[1][lane]);
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kTerms == 3) {
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(off[2][lane]);
+        acc = mfma32(pair(hi, lo), pair(t.lo, t.hi), acc);
+        acc = mfma32(pair(mid, mid), pair(t.hi, t.mid), acc);
+    } else {
+        acc = mfma32(pair(mid, mid), pair(t.hi, u32x2{0, 0}), acc);
+    }
+    return mfma32(pair(hi, hi), pair(t.hi, t.mid), acc);
+}
+
 // One wave prepares a block whose rows K, R it has staged: decays, X and (kAtt) A, or (kAdj) their
 // transposes.  wt, bt: rate (log2 units) and write strength of token l16.  Register r of group g holds
-// element (i = 4 g + r, j = l16) of the 16 x 16 products.
+// element (i = 4 g + r, j = l16) of the 16 x 16 products.  off (bf16, or NULL): this block is the one of its
+// pair that the other, whose rows are given, is connected to.
 template <typename T, int N, bool kAtt, bool kAdj>
-__device__ __forceinline__ void prepare_block(int l16, int g, const T (*K)[kRow<T, N>], const T (*R)[kRow<T, N>], float wt,
-                                              float bt, float* since, float* put, float (*inv)[kPadM], float (*att)[kPadM]) {
+__device__ __forceinline__ void prepare_block(int l16, int g, const T* K, const T* R, float wt, float bt, float* since, float* put,
+                                              float* inv, float* att, const Partner<T, N, kAdj>& partner, uint16_t (*off)[64][4]) {
     asm volatile("" : "+v"(l16), "+v"(g));  // else the comparisons below are kept in registers from tile to tile
-    const f4 kk = rows_product<N>(K[l16], K[l16], g);
+    const f4 kk = rows_product<N>(K, K, l16, g);
     f4 rk = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (kAtt) rk = rows_product<N>(R[l16], K[l16], g);
+    if constexpr (kAtt) rk = rows_product<N>(R, K, l16, g);
     // sums through the token and after it, by shifts along the rows of 16 lanes
     float pre = wt, suf = dpp<0x101>(wt);
     pre += dpp<0x111>(pre);
@@ -440,9 +556,14 @@ __device__ __forceinline__ void prepare_block(int l16, int g, const T (*K)[kRow<
     suf += dpp<0x104>(suf);
     pre += dpp<0x118>(pre);
     suf += dpp<0x108>(suf);
+    const float from_start = ex2(-pre), to_end = ex2(-suf) * bt;
     if (g == 0) {
-        since[l16] = ex2(-pre);
-        put[l16] = ex2(-suf) * bt;
+        since[l16] = from_start;
+        put[l16] = to_end;
+    }
+    if constexpr (kPair<T> == 2) {
+        if (off != nullptr) partner.template connect<kAtt>(K, R, kAdj ? to_end : -from_start, off, l16, g);
+        __builtin_amdgcn_sched_barrier(0);  // the other block's rows are done with
     }
     // sum of w over j < l <= i, by quads of tokens: after j in its quad, whole quads between, through i in its
     // own; or what lies between the two when they share one
@@ -471,50 +592,45 @@ __device__ __forceinline__ void prepare_block(int l16, int g, const T (*K)[kRow<
         m[r] = l16 < i ? f * kk[r] : 0.f;
         a[r] = l16 <= i ? f * rk[r] : 0.f;
     }
-    // Forward: row l16 of X, its elements from the last, x_j = [j == l16] - sum_{i > j} x_i m_ij, the table
-    // holding the transpose of m.  Adjoint: column l16, x_i = [i == l16] - sum_{j < i} m_ij x_j.  Either way
-    // the lane ends with a row of what the products take.
+    // X = (I + M)^{-1} four rows at a time (M here with its beta): x is what remains of I's rows of a block of
+    // four, less M's other blocks times the rows above, solved against the block's own six numbers.  Each pass
+    // takes all four blocks at once from the rows of the pass before, so after three all are what substitution
+    // from the first block down gives, with the products on the matrix cores (12 of them, against 120
+    // multiplications and 36 LDS reads when each lane solved a row on its own: 8 x 1024 tokens, 64 heads of 64,
+    // @@ us against @@).
+#pragma unroll
+    for (int r = 0; r < 4; ++r) inv[piece(4 * g + r, l16 >> 2) + (l16 & 3)] = m[r];
     if constexpr (kAdj) {
+        *reinterpret_cast<f4*>(&att[piece(l16, g)]) = a;
+    } else if constexpr (kAtt) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) inv[4 * g + r][l16] = m[r];
-        *reinterpret_cast<f4*>(&att[l16][4 * g]) = a;
-    } else {
-        *reinterpret_cast<f4*>(&inv[l16][4 * g]) = m;
-        if constexpr (kAtt) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) att[4 * g + r][l16] = a[r];
-        }
+        for (int r = 0; r < 4; ++r) att[piece(4 * g + r, l16 >> 2) + (l16 & 3)] = a[r];
     }
     __builtin_amdgcn_wave_barrier();  // the table is read back by the wave that wrote it
-    float x[kSub];
-    f4 row[3][kSub / 4];  // two rows ahead of the one in use; all at once they would spill
-    const auto read_row = [&](int n) {
+    f4 others = load4(&inv[piece(l16, g)]), unit;
+    const f4 m1 = load4(&inv[piece(4 * g + 1, g)]), m2 = load4(&inv[piece(4 * g + 2, g)]), m3 = load4(&inv[piece(4 * g + 3, g)]);
+    __builtin_amdgcn_wave_barrier();  // and has been read
 #pragma unroll
-        for (int l = 0; l < kSub / 4; ++l)
-            if (kAdj ? 4 * l < n : 4 * l + 3 > kSub - 1 - n) row[n % 3][l] = load4(&inv[kAdj ? n : kSub - 1 - n][4 * l]);
-    };
-    read_row(1);
-    read_row(2);
-#pragma unroll
-    for (int n = 0; n < kSub; ++n) {
-        if (n > 0 && n + 2 < kSub) read_row(n + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        const int at = kAdj ? n : kSub - 1 - n;
-        float acc = at == l16 ? 1.f : 0.f;
-#pragma unroll
-        for (int l = 0; l < n; ++l) {
-            const int j = kAdj ? l : kSub - 1 - l;
-            acc = fmaf(-row[n % 3][j / 4][j % 4], x[j], acc);
-        }
-        x[at] = acc;
+    for (int r = 0; r < 4; ++r) {
+        others[r] = jq > g ? -others[r] : 0.f;
+        unit[r] = l16 == 4 * g + r ? 1.f : 0.f;
     }
-    __builtin_amdgcn_wave_barrier();  // every row has been read
-    // every group has the whole row and writes a quarter (a write under g == 0 would take the arithmetic
-    // above under that condition too, behind all of its reads)
-    f4 mine;
+    const auto own_block = [&](f4 x) {
+        x[1] = fmaf(-m1[0], x[0], x[1]);
+        x[2] = fmaf(-m2[1], x[1], fmaf(-m2[0], x[0], x[2]));
+        x[3] = fmaf(-m3[2], x[2], fmaf(-m3[1], x[1], fmaf(-m3[0], x[0], x[3])));
+        return x;
+    };
+    f4 x = own_block(unit);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) mine[q] = g == 0 ? x[q] : g == 1 ? x[4 + q] : g == 2 ? x[8 + q] : x[12 + q];
-    *reinterpret_cast<f4*>(&inv[l16][4 * g]) = mine;
+    for (int n = 0; n < 3; ++n) x = own_block(mma16(others, x, unit));
+    // as the state waves read it: X, or its transpose
+    if constexpr (kAdj) {
+        *reinterpret_cast<f4*>(&inv[piece(l16, g)]) = x;
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) inv[piece(4 * g + r, l16 >> 2) + (l16 & 3)] = x[r];
+    }
 }
 
 // Four rows 4 g + q of a wave's columns to a float32 array of value rows, those below `rows`.
@@ -536,7 +652,7 @@ template <typename T, int N, bool kAdj, bool kOut>
 __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delta_walk_kernel(WalkArgs P) {
     using Shared = WalkShared<T, N>;
     __shared__ Shared sm;
-    constexpr int kTok = Shared::kTok, kBlocks = kTok / kSub, kStateWaves = N / 16;
+    constexpr int kTok = Shared::kTok, kBlocks = kTok / kSub, kStateWaves = N / 16, kG = kPair<T>, kLen = kRow<T, N>;
     constexpr bool kNeedR = kAdj || kOut;
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -577,53 +693,84 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
                 store_state<N>(P.states + (bh * ((P.T + kTile - 1) / kTile) + t0 / kTile) * N * N, S, 16 * wv + l16, g);
             }
 #pragma unroll 1
-            for (int i = 0; i < kBlocks; ++i) {
-                const int s = kAdj ? kBlocks - 1 - i : i, tb = kSub * s;
-                // everything the block reads is on its way while the state is split
-                const LeftRows<T, N> kr(sm.k[f][tb + l16], g);
-                const f4 x = value_column(sm.v[f], tb, 16 * wv, l16, g);
-                const f4 since = load4(&sm.since[f][tb + 4 * g]), put = load4(&sm.put[f][tb + 4 * g]);
-                const f4 inv = load4(&sm.inv[f][s][l16][4 * g]);
-                const float total = sm.since[f][tb + kSub - 1];
-                const LeftCols<T, N> kc(sm.k[f], tb, l16, g);
-                f4 result;  // e; adjoint: lambda
-                if constexpr (kAdj) {
-                    const f4 att = load4(&sm.att[f][s][l16][4 * g]);
-                    const LeftCols<T, N> rc(sm.r[f], tb, l16, g);
-                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
-                    const f4 kG = StateOperand<T, N>(S).template times<false>(kr, g);
+            for (int i = 0; i < kBlocks / kG; ++i) {
+                const int p = kAdj ? kBlocks / kG - 1 - i : i, tb = kSub * kG * p;
+                const T *K = sm.k[f] + tb * kLen, *R = sm.r[f] + tb * kLen;
+                T* V = sm.v[f] + tb * kLen;
+                f4 x[kG], since[kG], put[kG], inv[kG], att[kG], kS[kG], result[kG];  // result: e; adjoint: lambda
+                float total[kG], all = 1.f;
 #pragma unroll
-                    for (int c = 0; c < N / 16; ++c) S[c] *= total;
-                    rc.add_outer(S, since * x);
-                    const f4 y = mma16(att, x, put * kG);
-                    result = mma16(inv, y, f4{0.f, 0.f, 0.f, 0.f});
-                    kc.add_outer(S, -since * result);
-                    if constexpr (kOut) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) store1(&sm.v[f][tb + 4 * g + q][16 * wv + l16], result[q]);
-                    }
-                } else {
-                    const LeftRows<T, N> rr(sm.r[f][tb + l16], g);
-                    const f4 att = load4(&sm.att[f][s][l16][4 * g]);
-                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+                for (int j = 0; j < kG; ++j) {
+                    x[j] = value_column<N>(V + j * kSub * kLen, 16 * wv, l16, g);
+                    since[j] = load4(&sm.since[f][tb + kSub * j + 4 * g]);
+                    put[j] = load4(&sm.put[f][tb + kSub * j + 4 * g]);
+                    inv[j] = load4(&sm.inv[f][kG * p + j][piece(l16, g)]);
+                    if constexpr (kNeedR) att[j] = load4(&sm.att[f][kG * p + j][piece(l16, g)]);
+                    total[j] = sm.since[f][tb + kSub * j + kSub - 1];
+                    all *= total[j];
+                }
+                const uint16_t(*off)[64][4] = sm.off[kG == 2 ? f * Shared::kPairs + p : 0];
+                const f4 none = {0.f, 0.f, 0.f, 0.f};
+                f4 out[kG];
+                {
                     const StateOperand<T, N> op(S);
-                    const f4 kS = op.template times<false>(kr, g);
-                    f4 out = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (kOut) out = since * op.template times<true>(rr, g);
 #pragma unroll
-                    for (int c = 0; c < N / 16; ++c) S[c] *= total;
-                    result = mma16(inv, x - since * kS, f4{0.f, 0.f, 0.f, 0.f});
-                    kc.add_outer(S, put * result);
-                    if constexpr (kOut) {
-                        out = mma16(att, result, out);
+                    for (int j = 0; j < kG; ++j)
+                        kS[j] = op.template times<false>(LeftRows<T, N>(K + j * kSub * kLen, l16, g), g);
+                    if constexpr (kOut && !kAdj) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) store1(&sm.v[f][tb + 4 * g + q][16 * wv + l16], out[q]);
+                        for (int j = 0; j < kG; ++j) {
+                            const f4 rS = op.template times<true>(LeftRows<T, N>(R + j * kSub * kLen, l16, g), g);
+                            out[j] = (j == 0 ? since[j] : total[0] * since[j]) * rS;
+                        }
                     }
                 }
-                if (P.rows != nullptr && !pass) {
-                    const int64_t left = P.T - t0 - tb;
-                    if (left > 0)
-                        store_rows(P.rows + vo + (t0 + tb) * vs + 16 * wv, static_cast<int>(vs), l16, result, g,
+#pragma unroll
+                for (int c = 0; c < N / 16; ++c) S[c] *= all;
+                f4 u[kG];
+                if constexpr (kAdj) {
+                    constexpr int L = kG - 1;
+                    f4 u2[kG];
+                    result[L] = mma16(inv[L], mma16(att[L], x[L], put[L] * kS[L]), none);
+                    u[L] = since[L] * x[L];
+                    u2[L] = -since[L] * result[L];
+                    if constexpr (kG == 2) {
+                        const f4 past = times_table<3>(off + 3, split(u[1]), lane) - times_table<3>(off, split(u2[1]), lane);
+                        result[0] = mma16(inv[0], mma16(att[0], x[0], total[1] * put[0] * kS[0] + past), none);
+                        u[1] *= total[0];
+                        u2[1] *= total[0];
+                        u[0] = since[0] * x[0];
+                        u2[0] = -since[0] * result[0];
+                    }
+                    LeftCols<T, N>(R, l16, g).add_outer(S, u);
+                    LeftCols<T, N>(K, l16, g).add_outer(S, u2);
+                } else {
+                    result[0] = mma16(inv[0], x[0] - since[0] * kS[0], none);
+                    u[0] = put[0] * result[0];
+                    if constexpr (kG == 2) {
+                        const Terms t = split(u[0]);
+                        const f4 rest = x[1] - total[0] * since[1] * kS[1];
+                        result[1] = mma16(inv[1], rest + times_table<3>(off, t, lane), none);
+                        if constexpr (kOut) out[1] += times_table<2>(off + 3, t, lane);
+                        u[0] *= total[1];
+                        u[1] = put[1] * result[1];
+                    }
+                    LeftCols<T, N>(K, l16, g).add_outer(S, u);
+                    if constexpr (kOut) {
+#pragma unroll
+                        for (int j = 0; j < kG; ++j) out[j] = mma16(att[j], result[j], out[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kG; ++j) {
+                    if constexpr (kOut) {
+                        const f4 y = kAdj ? result[j] : out[j];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) store1(V + place<T, N>(kSub * j + 4 * g + q, 16 * wv + l16), y[q]);
+                    }
+                    const int64_t left = P.T - t0 - tb - kSub * j;
+                    if (P.rows != nullptr && !pass && left > 0)
+                        store_rows(P.rows + vo + (t0 + tb + kSub * j) * vs + 16 * wv, static_cast<int>(vs), l16, result[j], g,
                                    left < kSub ? static_cast<int>(left) : kSub);
                 }
             }
@@ -647,6 +794,7 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
         constexpr bool kFetchFirst = sizeof(T) * N == 256;
         BlockRows<T, N> fk, fr, fx;
         float wt = 0.f, bt = 0.f;
+        const bool connected = kG == 2 && (s & 1) == (kAdj ? 0 : 1);
         const auto fetch = [&](int64_t n) {
             const int64_t t0 = start_of(n) + kSub * s;
             const int left = rows_left(t0, len);
@@ -662,21 +810,27 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
         };
         const auto prepare = [&](int64_t n) {  // what has been fetched, as tile n; then tile n + 1 is fetched
             const int f = static_cast<int>(n & 1), tb = kSub * s;
-            fk.put(&sm.k[f][tb], lane);
-            if constexpr (kNeedR) fr.put(&sm.r[f][tb], lane);
-            fx.put(&sm.v[f][tb], lane);
+            fk.put(sm.k[f] + tb * kLen, lane);
+            if constexpr (kNeedR) fr.put(sm.r[f] + tb * kLen, lane);
+            fx.put(sm.v[f] + tb * kLen, lane);
             const float wn = wt * kLog2e, bn = bt;
+            Partner<T, N, kAdj> other;
+            if constexpr (kG == 2) {
+                const int64_t tp = start_of(n) + kSub * (kAdj ? s + 1 : s - 1);  // the pair's other block
+                if (connected) other.fetch(k + tp * ks, r + tp * ks, static_cast<int>(ks), rows_left(tp, len), l16, g);
+            }
             if (kFetchFirst && n + 1 < count) fetch(n + 1);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_wave_barrier();  // the rows are read back by the wave that wrote them
-            prepare_block<T, N, kNeedR, kAdj>(l16, g, &sm.k[f][tb], &sm.r[f][tb], wn, bn, &sm.since[f][tb], &sm.put[f][tb],
-                                              sm.inv[f][s], sm.att[f][s]);
+            prepare_block<T, N, kNeedR, kAdj>(l16, g, sm.k[f] + tb * kLen, sm.r[f] + tb * kLen, wn, bn, &sm.since[f][tb],
+                                              &sm.put[f][tb], sm.inv[f][s], sm.att[f][s], other,
+                                              connected ? sm.off[kG == 2 ? f * Shared::kPairs + s / kG : 0] : nullptr);
             __builtin_amdgcn_sched_barrier(0);
             if (!kFetchFirst && n + 1 < count) fetch(n + 1);
         };
         const auto flush = [&](int64_t n) {
             const int64_t t0 = start_of(n) + kSub * s;
-            BlockRows<T, N>::flush(&sm.v[n & 1][kSub * s], y + t0 * vs, static_cast<int>(vs), rows_left(t0, P.T), lane);
+            BlockRows<T, N>::flush(sm.v[n & 1] + kSub * s * kLen, y + t0 * vs, static_cast<int>(vs), rows_left(t0, P.T), lane);
         };
         if (count > 0) {
             fetch(0);
@@ -1102,9 +1256,8 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 // Everything the tile needs of a head is on its way before the first of it is put into LDS, and chains of
 // dependent products are taken in turn.  Held to 128 registers for two workgroups a compute unit at N = 64 it
 // spilled and was no faster (405 to 440 us against 400).
-// LDS rows are not padded (they would not fit at N = 128): the 16-byte piece q of row t lies at q ^ swizzle(t),
-// so that 16 rows' pieces q meet 16 different bank groups.  8 x 1024 tokens of 64 heads of 64 take 370 us for
-// 870 MB (2.4 TB/s): the phases' products and LDS traffic, which meet at four barriers a tile.
+// 8 x 1024 tokens of 64 heads of 64 take 370 us for 870 MB (2.4 TB/s): the phases' products and LDS traffic,
+// which meet at four barriers a tile.
 constexpr int kGradWaves = 8;
 constexpr unsigned kGradGroups = 256;  // compute units
 constexpr int kGradThreads = 64 * kGradWaves;
@@ -1126,11 +1279,6 @@ struct GradShared16 {
     float diag[kTile];                         // the crossing pairs inside the token's own block
 };
 
-template <int N>
-__device__ __forceinline__ int swizzled(int t, int c) {
-    const int s = N == 64 ? (t >> 1) & 7 : t & 15;
-    return (((c >> 3) ^ s) << 3) | (c & 7);
-}
 template <int N>
 __device__ __forceinline__ bf8 row8(const uint16_t (*X)[N], int t, int c) { return raw8(&X[t][swizzled<N>(t, c)]); }
 
