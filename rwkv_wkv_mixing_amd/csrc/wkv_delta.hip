@@ -644,7 +644,7 @@ template <typename T, int N>
 constexpr int kWalkThreads = 64 * (N / 16 + kWalkTile<T, N> / kSub);
 // waves a SIMD: two workgroups a compute unit where LDS has room for them (bf16 at N = 64), else one
 template <typename T, int N>
-constexpr int kWalkWaves = sizeof(T) * N <= 128 ? 4 : (kWalkThreads<T, N> / 64 + 3) / 4;
+constexpr int kWalkWaves = ((sizeof(T) * N <= 128 ? 2 : 1) * kWalkThreads<T, N> / 64 + 3) / 4;
 
 // kOut false: a pass without o (adjoint: dv, lambda and the states' gradients): for the saved errors and
 // states, for the final state, or (local) for what the segments of a time split do.
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
     const auto start_of = [&](int64_t n) { return begin + (kAdj ? count - 1 - n : n) * kTok; };
 
     if (wv < kStateWaves) {
-        const int col = 16 * wv + l16;
+        const int c0 = 16 * wv, col = c0 + l16;  // this wave's columns, and this lane's
         const float* first = P.starts != nullptr ? P.starts + (bh * P.nseg + seg) * N * N
                              : P.first != nullptr && given ? P.first + bh * N * N : nullptr;
         f4 S[N / 16];
@@ -690,33 +690,28 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
             const int64_t t0 = start_of(n);
             const int f = static_cast<int>(n & 1);
             if (P.states != nullptr && !pass && (kTok == kTile || n == 0 || t0 % kTile == (kAdj ? kTile - kTok : 0))) {
-                store_state<N>(P.states + (bh * ((P.T + kTile - 1) / kTile) + t0 / kTile) * N * N, S, 16 * wv + l16, g);
+                store_state<N>(P.states + (bh * ((P.T + kTile - 1) / kTile) + t0 / kTile) * N * N, S, col, g);
             }
 #pragma unroll 1
             for (int i = 0; i < kBlocks / kG; ++i) {
                 const int p = kAdj ? kBlocks / kG - 1 - i : i, tb = kSub * kG * p;
                 const T *K = sm.k[f] + tb * kLen, *R = sm.r[f] + tb * kLen;
                 T* V = sm.v[f] + tb * kLen;
-                f4 x[kG], since[kG], put[kG], inv[kG], att[kG], kS[kG], result[kG];  // result: e; adjoint: lambda
+                f4 since[kG], put[kG], inv[kG], att[kG];
+                f4 x[kG], kS[kG], out[kG], result[kG];  // result: e; adjoint: lambda
                 float total[kG], all = 1.f;
 #pragma unroll
                 for (int j = 0; j < kG; ++j) {
-                    x[j] = value_column<N>(V + j * kSub * kLen, 16 * wv, l16, g);
                     since[j] = load4(&sm.since[f][tb + kSub * j + 4 * g]);
-                    put[j] = load4(&sm.put[f][tb + kSub * j + 4 * g]);
-                    inv[j] = load4(&sm.inv[f][kG * p + j][piece(l16, g)]);
-                    if constexpr (kNeedR) att[j] = load4(&sm.att[f][kG * p + j][piece(l16, g)]);
                     total[j] = sm.since[f][tb + kSub * j + kSub - 1];
                     all *= total[j];
                 }
                 const uint16_t(*off)[64][4] = sm.off[kG == 2 ? f * Shared::kPairs + p : 0];
                 const f4 none = {0.f, 0.f, 0.f, 0.f};
-                f4 out[kG];
                 {
                     const StateOperand<T, N> op(S);
 #pragma unroll
-                    for (int j = 0; j < kG; ++j)
-                        kS[j] = op.template times<false>(LeftRows<T, N>(K + j * kSub * kLen, l16, g), g);
+                    for (int j = 0; j < kG; ++j) kS[j] = op.template times<false>(LeftRows<T, N>(K + j * kSub * kLen, l16, g), g);
                     if constexpr (kOut && !kAdj) {
 #pragma unroll
                         for (int j = 0; j < kG; ++j) {
@@ -726,11 +721,17 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
                     }
                 }
 #pragma unroll
+                for (int j = 0; j < kG; ++j) {
+                    x[j] = value_column<N>(V + j * kSub * kLen, c0, l16, g);
+                    put[j] = load4(&sm.put[f][tb + kSub * j + 4 * g]);
+                    inv[j] = load4(&sm.inv[f][kG * p + j][piece(l16, g)]);
+                    if constexpr (kNeedR) att[j] = load4(&sm.att[f][kG * p + j][piece(l16, g)]);
+                }
+                f4 u[kG], u2[kG];
+#pragma unroll
                 for (int c = 0; c < N / 16; ++c) S[c] *= all;
-                f4 u[kG];
                 if constexpr (kAdj) {
                     constexpr int L = kG - 1;
-                    f4 u2[kG];
                     result[L] = mma16(inv[L], mma16(att[L], x[L], put[L] * kS[L]), none);
                     u[L] = since[L] * x[L];
                     u2[L] = -since[L] * result[L];
@@ -742,8 +743,6 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
                         u[0] = since[0] * x[0];
                         u2[0] = -since[0] * result[0];
                     }
-                    LeftCols<T, N>(R, l16, g).add_outer(S, u);
-                    LeftCols<T, N>(K, l16, g).add_outer(S, u2);
                 } else {
                     result[0] = mma16(inv[0], x[0] - since[0] * kS[0], none);
                     u[0] = put[0] * result[0];
@@ -755,22 +754,19 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
                         u[0] *= total[1];
                         u[1] = put[1] * result[1];
                     }
-                    LeftCols<T, N>(K, l16, g).add_outer(S, u);
-                    if constexpr (kOut) {
-#pragma unroll
-                        for (int j = 0; j < kG; ++j) out[j] = mma16(att[j], result[j], out[j]);
-                    }
                 }
+                if constexpr (kAdj) LeftCols<T, N>(R, l16, g).add_outer(S, u);
+                LeftCols<T, N>(K, l16, g).add_outer(S, kAdj ? u2 : u);
 #pragma unroll
                 for (int j = 0; j < kG; ++j) {
                     if constexpr (kOut) {
-                        const f4 y = kAdj ? result[j] : out[j];
+                        const f4 y = kAdj ? result[j] : mma16(att[j], result[j], out[j]);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) store1(V + place<T, N>(kSub * j + 4 * g + q, 16 * wv + l16), y[q]);
+                        for (int q = 0; q < 4; ++q) store1(V + place<T, N>(kSub * j + 4 * g + q, col), y[q]);
                     }
                     const int64_t left = P.T - t0 - tb - kSub * j;
                     if (P.rows != nullptr && !pass && left > 0)
-                        store_rows(P.rows + vo + (t0 + tb + kSub * j) * vs + 16 * wv, static_cast<int>(vs), l16, result[j], g,
+                        store_rows(P.rows + vo + (t0 + tb + kSub * j) * vs + c0, static_cast<int>(vs), l16, result[j], g,
                                    left < kSub ? static_cast<int>(left) : kSub);
                 }
             }
@@ -778,7 +774,7 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
         }
         float* last = pass ? P.local + ((bh * P.nseg + seg) * 2 + unit) * N * N
                       : P.last != nullptr && seg == (kAdj ? 0 : P.nseg - 1) ? P.last + bh * N * N : nullptr;
-        if (last != nullptr) store_state<N>(last, S, 16 * wv + l16, g);
+        if (last != nullptr) store_state<N>(last, S, col, g);
     } else {
         const int s = wv - kStateWaves;  // this wave's block of every tile
         const int64_t ks = P.HK * N;
@@ -788,10 +784,6 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
         T* y = static_cast<T*>(P.y) + vo;
         const float* w = P.w + b * P.T * P.H + h;
         const float* beta = P.beta + b * P.T * P.H + h;
-        // The next rows' loads before the block is prepared (a tile's time to arrive) where there are registers
-        // for both, or after it: ragged prompts at N = 128 201 us against 214; 8 x 1024 tokens, 64 heads of 64,
-        // 110 (some spilled) against 106.
-        constexpr bool kFetchFirst = sizeof(T) * N == 256;
         BlockRows<T, N> fk, fr, fx;
         float wt = 0.f, bt = 0.f;
         const bool connected = kG == 2 && (s & 1) == (kAdj ? 0 : 1);
@@ -819,14 +811,13 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
                 const int64_t tp = start_of(n) + kSub * (kAdj ? s + 1 : s - 1);  // the pair's other block
                 if (connected) other.fetch(k + tp * ks, r + tp * ks, static_cast<int>(ks), rows_left(tp, len), l16, g);
             }
-            if (kFetchFirst && n + 1 < count) fetch(n + 1);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_wave_barrier();  // the rows are read back by the wave that wrote them
             prepare_block<T, N, kNeedR, kAdj>(l16, g, sm.k[f] + tb * kLen, sm.r[f] + tb * kLen, wn, bn, &sm.since[f][tb],
                                               &sm.put[f][tb], sm.inv[f][s], sm.att[f][s], other,
                                               connected ? sm.off[kG == 2 ? f * Shared::kPairs + s / kG : 0] : nullptr);
             __builtin_amdgcn_sched_barrier(0);
-            if (!kFetchFirst && n + 1 < count) fetch(n + 1);
+            if (n + 1 < count) fetch(n + 1);
         };
         const auto flush = [&](int64_t n) {
             const int64_t t0 = start_of(n) + kSub * s;
