@@ -347,11 +347,12 @@ __device__ __forceinline__ int64_t row_length(const int32_t* lengths, int64_t b,
 //   one preparing wave per block of a tile, which meanwhile writes out its 16 rows of the last tile's
 //   results, stages its 16 rows of the next tile, and finds that block's decays, X and A from them (no
 //   other wave's rows are needed), its loads for the tile after that already on their way.
-// All buffers are double, and one barrier a tile is all that is left of waiting for each other: at N = 64
-// 4.3 us a tile for a workgroup alone on its compute unit and 1.55 for two side by side.  (Four waves that
-// did both in turn, with three barriers a tile, took 5.2.)
-// What is left is the chain of dependent products of the four blocks one after the other, and the vector
-// instructions that split the state, issued on about 60 % of the cycles of a full card.
+// All buffers are double, and one barrier a tile is all that is left of waiting for each other: 3.1 us a tile
+// at N = 64 for a workgroup alone on its compute unit and 5.9 for two side by side, 6.3 at N = 128.  (Four waves
+// that did both in turn, with three barriers a tile, took 5.2 at N = 64.)  What bounds it: the state waves wait
+// for nobody, and their chain of products with the splits between takes the time; a full SIMD issues vector
+// instructions on about 55 % of its cycles and has products under way on 32 %, and the float32 ones (measured)
+// keep it from vector instructions.  Fewer vector instructions or LDS accesses alone no longer moved it.
 //
 // Adjoint, for L = <go, o> + <ds_out, S_T>, over a block with G the gradient of the state after it:
 //     y      = A^T go + diag(beta until) K G
@@ -596,8 +597,8 @@ __device__ __forceinline__ void prepare_block(int l16, int g, const T* K, const 
     // four, less M's other blocks times the rows above, solved against the block's own six numbers.  Each pass
     // takes all four blocks at once from the rows of the pass before, so after three all are what substitution
     // from the first block down gives, with the products on the matrix cores (12 of them, against 120
-    // multiplications and 36 LDS reads when each lane solved a row on its own: 8 x 1024 tokens, 64 heads of 64,
-    // @@ us against @@).
+    // multiplications and 36 LDS reads a lane when each solved a row on its own, whose registers were what the
+    // walks spilled).
 #pragma unroll
     for (int r = 0; r < 4; ++r) inv[piece(4 * g + r, l16 >> 2) + (l16 & 3)] = m[r];
     if constexpr (kAdj) {
@@ -1839,18 +1840,20 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Segments of a time split, by what the walks would take, in units of one tile of a workgroup alone on its
-// compute unit (4.3 us at N = 64, 8.6 at N = 128; two at N = 64 share one in 1.55, at N = 128 only one fits).
+// compute unit (3.1 us at N = 64, 6.3 at N = 128; two at N = 64 share one in 1.9, at N = 128 only one fits).
 // A split walks the segments twice, once without outputs (0.65 of a tile) for the state and for the identity,
-// chains them (0.3 each) and launches two kernels more (1.2).  Measured whole and split, bf16:
-//   8192 tokens, N = 64:  8 pairs 647 and 74 us, 64 pairs 609 and 260, 128 pairs 604 and 431
-//   8192 tokens, N = 128: 64 pairs 851 and 677;  a training call of 128 pairs 530 and 570 (not split)
-//   512 tokens: 4 pairs 38 and 29 us;  256 tokens: 4 pairs 20 and 27 (not split)
+// chains them (0.3 each) and launches two kernels more (2.5).  Measured whole and split, bf16:
+//   8192 tokens, N = 64:  8 pairs 387 and 71 us, 64 pairs 391 and 245, 128 pairs 403 and 367
+//   8192 tokens, N = 128: 64 pairs 805 and 522, 128 pairs 808 and 746
+//   1024 tokens, N = 64:  64 pairs 54 and 48, 128 pairs 56 and 59 (not split);  training 213 and 218 (not split)
+//   1024 tokens, N = 128, training: 128 pairs 462 and 497 (not split)
+//   512 tokens, N = 64:   4 pairs 30 and 25
 int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
     const int64_t tiles = (T + kTile - 1) / kTile;
     const auto walk = [&](int64_t groups) {
         if (N != 64) return static_cast<double>((groups + 255) / 256);
         const int64_t rest = groups % 512;
-        return 1.55 * static_cast<double>(groups / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.55);
+        return 1.9 * static_cast<double>(groups / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.9);
     };
     *per = tiles;
     int64_t nseg = 1;
@@ -1859,7 +1862,7 @@ int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
     for (int64_t n = 2; n <= 64 && 2 * n <= tiles; ++n) {
         const int64_t p = (tiles + n - 1) / n;
         if ((tiles + p - 1) / p != n) continue;
-        const double t = static_cast<double>(p) * (0.65 * walk(2 * BH * (n - 1)) + walk(BH * n)) + 0.3 * static_cast<double>(n) + 1.2;
+        const double t = static_cast<double>(p) * (0.65 * walk(2 * BH * (n - 1)) + walk(BH * n)) + 0.3 * static_cast<double>(n) + 2.5;
         if (t < best) {
             best = t;
             nseg = n;
