@@ -1246,12 +1246,14 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 //      lambda, each lane's eight values where the lane that needs them reads them
 //   4. every wave: its channels of the products of k and r with all ten blocks; and the rates
 // Everything the tile needs of a head is on its way before the first of it is put into LDS, and chains of
-// dependent products are taken in turn.  Held to 128 registers for two workgroups a compute unit at N = 64 it
-// spilled and was no faster (405 to 440 us against 400).
-// 8 x 1024 tokens of 64 heads of 64 take 370 us for 870 MB (2.4 TB/s): the phases' products and LDS traffic,
-// which meet at four barriers a tile.
+// dependent products are taken in turn.  At N = 64 two workgroups share a compute unit (128 registers, some
+// spilled), each one's loads behind the other's work; one with twice the registers that fetched its next tile
+// ahead took as long (8 x 1024 tokens of 64 heads, forward and backward, 601 us against 607).  The 870 MB of
+// that case take about 360 us (2.4 TB/s): the phases' products and LDS traffic, which meet at four barriers a
+// tile.
 constexpr int kGradWaves = 8;
-constexpr unsigned kGradGroups = 256;  // compute units
+template <int N>
+constexpr int kGradShare = N == 64 ? 2 : 1;  // workgroups a compute unit
 constexpr int kGradThreads = 64 * kGradWaves;
 
 template <int N>
@@ -1352,7 +1354,7 @@ __device__ __forceinline__ f4 mma_step(int i, const bf8 (&a)[3], const bf8 (&b)[
 }
 
 template <int N>
-__global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdArgs P) {
+__global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_kernel(DeltaBwdArgs P) {
     __shared__ GradShared16<N> sm;
     constexpr int NS = N / 16;               // slices of 16 channels
     constexpr int NX = 4 * NS / kGradWaves;  // token blocks a wave takes of its slice
@@ -1388,18 +1390,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
     GradRows<N> fk, fr, fg;
     GradTerms<N> fe, fl;
     float wt, bt;
-    // The next tile's inputs, and this wave's rows of the states before and after it, arrive behind the work
-    // on this one at N = 64; at N = 128 they are twice as much, which there are no registers for.
-    constexpr bool kAhead = N == 64;
-    f4 sa[kAhead ? NM : 1], sb[kAhead ? NM : 1], ga[kAhead ? NM : 1], gb[kAhead ? NM : 1];
-    const auto fetch_states = [&](const Place& p, int m, int to) {
-        const int64_t from = ((p.b * P.H + p.h) * ntile + p.tile) * N * N + 32 * m;
-        const uint32_t mine = static_cast<uint32_t>((c0 + l16) * N + 8 * g);
-        sa[to] = load4(P.states + from + mine);
-        sb[to] = load4(P.states + from + 4 + mine);
-        ga[to] = load4(P.gstates + from + mine);
-        gb[to] = load4(P.gstates + from + 4 + mine);
-    };
     const auto fetch = [&](const Place& p) {
         const int64_t ko = (p.b * P.T + p.t0) * ks + p.hk * N, vo = (p.b * P.T + p.t0) * vs + p.h * N;
         fk.fetch(static_cast<const uint16_t*>(P.k) + ko, static_cast<int>(ks), p.left);
@@ -1414,13 +1404,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    const auto fetch_states_ahead = [&](const Place& p) {
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int m = 0; m < NM; ++m) fetch_states(p, m, m);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
     f4 drT[NX], dkT[NX];  // of token block X0 + x: channels c0 + 4 g .. + 3 of token l16
 #pragma unroll
     for (int x = 0; x < NX; ++x) drT[x] = dkT[x] = f4{0.f, 0.f, 0.f, 0.f};
@@ -1428,10 +1411,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
     at.item = blockIdx.x;
     settle(at);
     if (at.item >= pairs * ntile) return;
-    if constexpr (kAhead) {
-        fetch(at);
-        fetch_states_ahead(at);
-    }
     bool first = true;
 #pragma unroll 1
     while (at.item < pairs * ntile) {
@@ -1439,7 +1418,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
         const int64_t b = at.b, h = at.h, t0 = at.t0;
         const int64_t len = t0 + at.left;
-        if constexpr (!kAhead) fetch(at);
+        fetch(at);
         if (!first) __syncthreads();  // the last tile's readers are done
         first = false;
         fk.put(sm.k);
@@ -1475,13 +1454,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
         }
         __syncthreads();
 
-        // the next head or tile on its way, behind the work on this one
         next = at;
         if (++next.h == (at.hk + 1) * per) {
             next.item += gridDim.x;
             settle(next);
         }
-        if (kAhead && next.item < pairs * ntile) fetch(next);
 
         // ---- products with the states before and after the tile, for this wave's channels and tokens
         {
@@ -1491,12 +1468,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
             for (int x = 0; x < NX; ++x) sg[x] = sl[x] = ge[x] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                const int v = 32 * m + 8 * g, k = kAhead ? m : 0;
-                if constexpr (!kAhead) fetch_states(at, m, 0);
+                const int v = 32 * m + 8 * g;
+                const int64_t from = ((b * P.H + h) * ntile + at.tile) * N * N + 32 * m;
+                const uint32_t mine = static_cast<uint32_t>((c0 + l16) * N + 8 * g);
+                const f4 sa = load4(P.states + from + mine), sb = load4(P.states + from + 4 + mine);
+                const f4 ga = load4(P.gstates + from + mine), gb = load4(P.gstates + from + 4 + mine);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) inner = fmaf(sa[k][q], ga[k][q], fmaf(sb[k][q], gb[k][q], inner));
+                for (int q = 0; q < 4; ++q) inner = fmaf(sa[q], ga[q], fmaf(sb[q], gb[q], inner));
                 bf8 s3[3];
-                split8(sa[k], sb[k], s3);
+                split8(sa, sb, s3);
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     const int t = kSub * (X0 + x) + l16;
@@ -1510,7 +1490,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
                     __builtin_amdgcn_sched_barrier(0);  // more of the reads at once would spill
                 }
                 bf8 g3[3];
-                split8(ga[k], gb[k], g3);
+                split8(ga, gb, g3);
 #pragma unroll
                 for (int x = 0; x < NX; x += 2) {
                     const int t = kSub * (X0 + x) + l16;
@@ -1548,7 +1528,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad16_kernel(DeltaBwdA
             inner = sum_lanes(inner, 64);
             if (lane == 0) sm.inner[slice] = inner;
         }
-        if (kAhead && next.item < pairs * ntile) fetch_states_ahead(next);
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
         __builtin_amdgcn_sched_barrier(0);
         // ---- the 16 x 16 blocks: rows i = 4 g + q of block I, column j = l16 of block J
@@ -1828,8 +1807,9 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
     const int64_t ntile = (a.T + kTile - 1) / kTile;
     const dim3 grid(static_cast<unsigned>(a.B * a.HK * ntile));
     if constexpr (std::is_same_v<T, uint16_t>) {
-        // one workgroup a compute unit walks the tiles, the next one's inputs arriving behind the work on this one
-        const dim3 some(grid.x < kGradGroups ? grid.x : kGradGroups);
+        // as many workgroups as the card holds at once walk the tiles
+        const unsigned most = 256 * kGradShare<N>;
+        const dim3 some(grid.x < most ? grid.x : most);
         hipLaunchKernelGGL((delta_grad16_kernel<N>), some, dim3(kGradThreads), 0, stream, a);
     } else {
         hipLaunchKernelGGL((delta_grad_kernel<N>), grid, dim3(64 * kWaves), 0, stream, a);
