@@ -1362,36 +1362,46 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
     int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int l16 = lane & 15, g = lane >> 4;
-    const int64_t ntile = (P.T + kTile - 1) / kTile, pairs = P.B * P.HK, per = P.H / P.HK;
+    // counted in 32 bits (the host's checks keep the tiles of all pairs below 2^31), stepped without a division
+    const uint32_t ntile = static_cast<uint32_t>((P.T + kTile - 1) / kTile), HK = static_cast<uint32_t>(P.HK);
+    const uint32_t pairs = static_cast<uint32_t>(P.B) * HK, per = static_cast<uint32_t>(P.H) / HK;
+    const uint32_t tiles_on = gridDim.x / pairs, pairs_on = gridDim.x % pairs;
     const int64_t ks = P.HK * N, vs = P.H * N;
     const int slice = wv % NS, c0 = 16 * slice, X0 = wv / NS * NX;
 
     // A (tile, batch row, key head), batch row and head fastest, and one of its value heads.
     struct Place {
-        int64_t item, b, hk, tile, t0, h;
+        uint32_t pair, tile, b, hk, h;
         int left;
     };
     Place at, next;
-    // the workgroup's next item that holds tokens; those that hold none get zeros
+    const auto advance = [&](Place& p) {
+        p.tile += tiles_on;
+        p.pair += pairs_on;
+        if (p.pair >= pairs) {
+            p.pair -= pairs;
+            ++p.tile;
+        }
+    };
+    // from a place on, the workgroup's first that holds tokens; those that hold none get zeros
     const auto settle = [&](Place& p) {
-        for (; p.item < pairs * ntile; p.item += gridDim.x) {
-            const int64_t bhk = p.item % pairs;
-            p.b = bhk / P.HK;
-            p.hk = bhk % P.HK;
-            p.tile = p.item / pairs;
-            p.t0 = p.tile * kTile;
+        for (; p.tile < ntile; advance(p)) {
+            p.b = p.pair / HK;
+            p.hk = p.pair % HK;
             p.h = p.hk * per;
-            p.left = rows_left(p.t0, row_length(P.lengths, p.b, P.T));
+            const int64_t t0 = static_cast<int64_t>(p.tile) * kTile;
+            p.left = rows_left(t0, row_length(P.lengths, p.b, P.T));
             if (p.left > 0) return;
             const int64_t ko = p.b * P.T * ks + p.hk * N;
-            zero_tile<uint16_t, N>(P, static_cast<uint16_t*>(P.dr) + ko, static_cast<uint16_t*>(P.dk) + ko, p.b, p.hk, p.t0);
+            zero_tile<uint16_t, N>(P, static_cast<uint16_t*>(P.dr) + ko, static_cast<uint16_t*>(P.dk) + ko, p.b, p.hk, t0);
         }
     };
     GradRows<N> fk, fr, fg;
     GradTerms<N> fe, fl;
     float wt, bt;
     const auto fetch = [&](const Place& p) {
-        const int64_t ko = (p.b * P.T + p.t0) * ks + p.hk * N, vo = (p.b * P.T + p.t0) * vs + p.h * N;
+        const int64_t row = p.b * P.T + static_cast<int64_t>(p.tile) * kTile;
+        const int64_t ko = row * ks + p.hk * N, vo = row * vs + p.h * N;
         fk.fetch(static_cast<const uint16_t*>(P.k) + ko, static_cast<int>(ks), p.left);
         fr.fetch(static_cast<const uint16_t*>(P.r) + ko, static_cast<int>(ks), p.left);
         fg.fetch(static_cast<const uint16_t*>(P.go) + vo, static_cast<int>(vs), p.left);
@@ -1399,8 +1409,8 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
         fl.fetch(P.lambda + vo, static_cast<int>(vs), p.left);
         wt = bt = 0.f;
         if (static_cast<int>(threadIdx.x) < p.left) {
-            wt = P.w[(p.b * P.T + p.t0 + lane) * P.H + p.h] * kLog2e;
-            bt = P.beta[(p.b * P.T + p.t0 + lane) * P.H + p.h];
+            wt = P.w[(row + lane) * P.H + p.h] * kLog2e;
+            bt = P.beta[(row + lane) * P.H + p.h];
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -1408,15 +1418,16 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
 #pragma unroll
     for (int x = 0; x < NX; ++x) drT[x] = dkT[x] = f4{0.f, 0.f, 0.f, 0.f};
 
-    at.item = blockIdx.x;
+    at.pair = blockIdx.x % pairs;
+    at.tile = blockIdx.x / pairs;
     settle(at);
-    if (at.item >= pairs * ntile) return;
+    if (at.tile >= ntile) return;
     bool first = true;
 #pragma unroll 1
-    while (at.item < pairs * ntile) {
+    while (at.tile < ntile) {
         // else every address and comparison below is worked out before the loop and kept in registers
         asm volatile("" : "+v"(lane), "+v"(l16), "+v"(g));
-        const int64_t b = at.b, h = at.h, t0 = at.t0;
+        const int64_t b = at.b, h = at.h, t0 = static_cast<int64_t>(at.tile) * kTile;
         const int64_t len = t0 + at.left;
         fetch(at);
         if (!first) __syncthreads();  // the last tile's readers are done
@@ -1456,7 +1467,7 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
 
         next = at;
         if (++next.h == (at.hk + 1) * per) {
-            next.item += gridDim.x;
+            advance(next);
             settle(next);
         }
 
@@ -1712,7 +1723,7 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (next.item != at.item) {
+        if (next.pair != at.pair || next.tile != at.tile) {
             const int64_t ko = b * P.T * ks + at.hk * N;
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
