@@ -14,6 +14,7 @@ from torch.autograd.function import once_differentiable
 from . import _lib as L
 
 _DT = {torch.float32: L.WKV_F32, torch.bfloat16: L.WKV_BF16}
+_FLOATS = tuple(_DT)
 
 
 def _p(t):
@@ -33,7 +34,7 @@ def _stream(dev):
 
 def _need(t, name, dtype=None, shape=None, device=None):
     if (isinstance(t, torch.Tensor) and t.is_cuda and (device is None or t.device == device)
-            and (dtype is None or (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype))
+            and (dtype is None or t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype))
             and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor):
@@ -706,10 +707,11 @@ def _delta_shape(w, r, v):
 
 
 def _delta_inputs(w, beta, r, k, v, lengths):
-    _need(r, "r", (torch.float32, torch.bfloat16))
+    _need(r, "r", _FLOATS)  # its shape is what B, T, HK and N are taken from
     dev, dt = r.device, r.dtype
     B, T, H, HK, N = shape = _delta_shape(w, r, v)
-    _need(r, "r", dt, (B, T, HK * N), dev)
+    if r.shape[0] != B or r.shape[1] != T:
+        _need(r, "r", dt, (B, T, HK * N), dev)
     _need(k, "k", dt, (B, T, HK * N), dev)
     _need(v, "v", dt, (B, T, H * N), dev)
     _need(w, "w", torch.float32, (B, T, H), dev)
@@ -786,7 +788,8 @@ def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=No
         _need(ckpt, "ckpt", torch.uint8, None, dev)
         if ckpt.numel() < delta_ckpt_bytes(B, T, H, N):
             raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {delta_ckpt_bytes(B, T, H, N)}")
-    nws = int(lib.wkv_delta_forward_workspace_bytes(B, T, H, HK, N)) if split else 0
+    # (a call of one 64-token tile has nothing to split)
+    nws = int(lib.wkv_delta_forward_workspace_bytes(B, T, H, HK, N)) if split and T > 64 else 0
     workspace = _scratch(workspace, nws, dev) if nws else None
     args = (B, T, H, HK, N, _DT[r.dtype], _at(lengths), _at(w), _at(beta), _at(r), _at(k), _at(v), _at(out), _at(state_in),
             _at(state_out), _at(ckpt), _at(workspace), _bytes_of(workspace) if nws else 0, _stream(dev))
@@ -863,7 +866,6 @@ def delta_rule(w, beta, r, k, v, state_in=None, lengths=None):
 
 
 _ACT = {"none": L.WKV_ACT_NONE, "sigmoid": L.WKV_ACT_SIGMOID, "silu": L.WKV_ACT_SILU}
-_FLOATS = (torch.float32, torch.bfloat16)
 
 
 def _act(act):
