@@ -719,10 +719,12 @@ size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
 namespace {
 
 // The scratch of a time split: what the segments do, [B H, nseg, 2, N, N], and their start states,
-// [B H, nseg, N, N], float32.  0 when there is none to make.
-size_t delta_split_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int64_t* nseg, int64_t* per) {
-    *nseg = wkv::delta_segments(B * H, T, N, per);
-    return *nseg > 1 ? static_cast<size_t>(B * H * *nseg) * 3 * N * N * sizeof(float) : 0;
+// [B H, nseg, N, N], float32, for the dtype that takes more segments.  0 when there is none to make.
+size_t delta_split_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
+    int64_t per;
+    const int64_t a = wkv::delta_segments(B * H, T, N, true, &per), b = wkv::delta_segments(B * H, T, N, false, &per);
+    const int64_t nseg = a > b ? a : b;
+    return nseg > 1 ? static_cast<size_t>(B * H * nseg) * 3 * N * N * sizeof(float) : 0;
 }
 
 // A forward in whole sequences, or (scratch not NULL) in nseg segments at once.
@@ -768,16 +770,14 @@ extern "C" {
 
 size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N) {
     const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
-    int64_t nseg, per;
-    return p.st == WKV_OK && p.ns > 0 ? delta_split_bytes(B, T, H, N, &nseg, &per) : 0;
+    return p.st == WKV_OK && p.ns > 0 ? delta_split_bytes(B, T, H, N) : 0;
 }
 
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags) {
     const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
     if (p.st != WKV_OK || p.ns == 0 || T == 0) return 0;
-    int64_t nseg, per;
     const size_t one = p.rows_bytes + p.states_bytes;
-    const size_t split = (flags & WKV_WS_NO_SPLIT) != 0 ? 0 : delta_split_bytes(B, T, H, N, &nseg, &per);
+    const size_t split = (flags & WKV_WS_NO_SPLIT) != 0 ? 0 : delta_split_bytes(B, T, H, N);
     return ((flags & WKV_WS_HAVE_CKPT) != 0 ? one : 2 * one) + split;
 }
 
@@ -795,8 +795,9 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
     if (!aligned(w, 4) || !aligned(beta, 4) || !aligned(r, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
         (lengths && !aligned(lengths, 4)) || (ckpt && !aligned(ckpt, 16)))
         return WKV_EALIGN;
-    int64_t nseg = 1, per = 0;
-    const size_t need = delta_split_bytes(B, T, H, N, &nseg, &per);
+    int64_t per = 0;
+    const int64_t nseg = wkv::delta_segments(B * H, T, N, in_dtype == WKV_BF16, &per);
+    const size_t need = delta_split_bytes(B, T, H, N);
     if (workspace && (workspace_bytes < need || !aligned(workspace, 256))) return WKV_EWORKSPACE;
     float* errs = static_cast<float*>(ckpt);
     float* states = ckpt ? reinterpret_cast<float*>(static_cast<char*>(ckpt) + p.rows_bytes) : nullptr;
@@ -823,8 +824,9 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
     // lambda and the states' gradients; the recomputed errors and states; the scratch of a time split
     const size_t one = p.rows_bytes + p.states_bytes, unsplit = ckpt ? one : 2 * one;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < unsplit) return WKV_EWORKSPACE;
-    int64_t nseg = 1, per = 0;
-    const size_t need = delta_split_bytes(B, T, H, N, &nseg, &per);
+    int64_t per = 0;
+    const int64_t nseg = wkv::delta_segments(B * H, T, N, in_dtype == WKV_BF16, &per);
+    const size_t need = delta_split_bytes(B, T, H, N);
     char* ws = static_cast<char*>(workspace);
     void* scratch = need > 0 && workspace_bytes >= unsplit + need ? ws + unsplit : nullptr;
     const bool bf = in_dtype == WKV_BF16;

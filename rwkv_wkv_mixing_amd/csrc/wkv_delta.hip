@@ -1833,13 +1833,16 @@ hipError_t launch_bwd(const DeltaBwdArgs& a, hipStream_t stream) {
 // Segments of a time split, by what the walks would take, in units of one tile of a workgroup alone on its
 // compute unit (3.1 us at N = 64, 6.3 at N = 128; two at N = 64 share one in 1.9, at N = 128 only one fits).
 // A split walks the segments twice, once without outputs (0.65 of a tile) for the state and for the identity,
-// chains them (0.3 each) and launches two kernels more (2.5).  Measured whole and split, bf16:
+// chains them (0.3 each) and launches two kernels more (2.5; 1.3 of float32's tiles, which take twice as long).
+// Measured whole and split, bf16:
 //   8192 tokens, N = 64:  8 pairs 387 and 71 us, 64 pairs 391 and 245, 128 pairs 403 and 367
 //   8192 tokens, N = 128: 64 pairs 805 and 522, 128 pairs 808 and 746
 //   1024 tokens, N = 64:  64 pairs 54 and 48, 128 pairs 56 and 59 (not split);  training 213 and 218 (not split)
 //   1024 tokens, N = 128, training: 128 pairs 462 and 497 (not split)
 //   512 tokens, N = 64:   4 pairs 30 and 25
-int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
+// float32: 512 tokens, N = 64, 4 pairs 48 and 32, 64 pairs 50 and 47;  N = 128, 16 pairs 150 and 80;  333 tokens,
+// N = 64, 16 pairs, training 111 and 100
+int64_t delta_segments(int64_t BH, int64_t T, int64_t N, bool bf16, int64_t* per) {
     const int64_t tiles = (T + kTile - 1) / kTile;
     const auto walk = [&](int64_t groups) {
         if (N != 64) return static_cast<double>((groups + 255) / 256);
@@ -1849,11 +1852,12 @@ int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per) {
     *per = tiles;
     int64_t nseg = 1;
     if (BH < 1 || BH > 512) return nseg;
+    const double more = bf16 ? 2.5 : 1.3;
     double best = walk(BH) * static_cast<double>(tiles);
     for (int64_t n = 2; n <= 64 && 2 * n <= tiles; ++n) {
         const int64_t p = (tiles + n - 1) / n;
         if ((tiles + p - 1) / p != n) continue;
-        const double t = static_cast<double>(p) * (0.65 * walk(2 * BH * (n - 1)) + walk(BH * n)) + 0.3 * static_cast<double>(n) + 2.5;
+        const double t = static_cast<double>(p) * (0.65 * walk(2 * BH * (n - 1)) + walk(BH * n)) + 0.3 * static_cast<double>(n) + more;
         if (t < best) {
             best = t;
             nseg = n;

@@ -303,7 +303,7 @@ struct DeltaChainArgs {
 
 hipError_t launch_delta_chain(const DeltaChainArgs& a, hipStream_t stream);
 // segments for a time split of BH pairs over T tokens (1: no split), *per 64-token tiles each
-int64_t delta_segments(int64_t BH, int64_t T, int64_t N, int64_t* per);
+int64_t delta_segments(int64_t BH, int64_t T, int64_t N, bool bf16, int64_t* per);
 
 // gated delta rule (wkv_delta.hip)
 hipError_t launch_delta_fwd(const DeltaArgs& a, hipStream_t stream);
