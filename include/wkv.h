@@ -533,7 +533,7 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
  * r, k, v, o, s_in, s_out, ckpt are 16-byte aligned (WKV_EALIGN otherwise).
  * WKV_EINVAL also for another N or an H that HK does not divide; WKV_ESIZE
- * from H N = 2^22.
+ * from H N = 2^22, and from B H = 2^22 (2^25 for up to 16 tokens without a ckpt).
  * A non-finite input may reach every output of its head from the 64 tokens it is
  * among on.
  */
@@ -599,7 +599,8 @@ enum { WKV_ACT_NONE = 0, WKV_ACT_SIGMOID = 1, WKV_ACT_SILU = 2 };
  * act(g) is g, sigmoid(g) or g sigmoid(g); without a gate the factor is 1.
  * Float32 arithmetic; outputs rounded once.
  *
- * rows, H, G  rows (>= 0), heads (>= 0), channels a head (1 .. 1024).
+ * rows, H, G  rows (>= 0), heads (>= 0), channels a head (1 .. 1024); H G below
+ *           2^24 and rows H below 2^31 (WKV_ESIZE otherwise).
  * y_dtype   dtype of y and dy; dtype: of gate, gout, out and dgate.  WKV_BF16 y
  *           needs WKV_BF16 for both (WKV_EDTYPE otherwise).
  * y, gate, out, gout, dy, dgate  [rows, H G]; out must not alias an input.
@@ -637,7 +638,7 @@ wkv_status_t wkv_head_norm_backward(int64_t rows, int64_t H, int64_t G, int y_dt
  *     dx = gx + (gradient through h)      (the gradient of x, and of the sum)
  * and, of the same sum, dy, dgate, dscale, dpost_w, dpost_b; and dpre_w, dpre_b.
  *
- * rows, C   rows (>= 0), channels (0 .. 8192).
+ * rows, C   rows (0 .. 2^31 - 1), channels (0 .. 8192).
  * x_dtype   dtype of x, x_out, gx, dx; dtype: of y, gate, h, gh, dy, dgate.
  *           WKV_BF16 x needs WKV_BF16 for both.
  * post_w, post_b, scale, pre_w, pre_b  [C] float32; all but pre_w may be NULL, and

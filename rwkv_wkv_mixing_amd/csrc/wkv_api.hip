@@ -685,7 +685,8 @@ struct DeltaPlan {
     size_t rows_bytes, states_bytes;     // float32 [B, T, H, N] and [B, H, ceil(T / 64), N, N], rounded up to 256
 };
 
-DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype) {
+// walks: the call has a ckpt or is the backward.
+DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype, bool walks) {
     const auto bad = [](wkv_status_t st) { return DeltaPlan{st, 0, 0, 0}; };
     if (B < 0 || T < 0 || H < 0 || HK < 0 || (N != 64 && N != 128)) return bad(WKV_EINVAL);
     if (HK == 0 ? H != 0 : H % HK != 0) return bad(WKV_EINVAL);
@@ -697,9 +698,10 @@ DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int
     if (!mul3(H, N, 4, &hn) || !mul3(B, T, hn, &n) || n > kMost) return bad(WKV_ESIZE);
     if (!mul3(p.ns, (T + 63) / 64, 4, &st) || st > kMost) return bad(WKV_ESIZE);
     if (H * N >= (int64_t{1} << 22)) return bad(WKV_ESIZE);  // 64 rows of float32 values below 2^31 bytes
-    // grids: a workgroup per (64 columns, pair) and per (64 tokens, row, key head), below 2^31
+    // grids of fewer than 2^32 threads: up to 768 a pair, or 128 for a few tokens; 256 per (64 tokens, row, key head)
     int64_t tiles;
-    if (bh >= (int64_t{1} << 30) || !mul3(B, HK, (T + 63) / 64, &tiles) || tiles >= (int64_t{1} << 31)) return bad(WKV_ESIZE);
+    if (bh >= (int64_t{1} << 22) && (walks || T > wkv::kDeltaStepMaxT || bh >= (int64_t{1} << 25))) return bad(WKV_ESIZE);
+    if (!mul3(B, HK, (T + 63) / 64, &tiles) || tiles >= (int64_t{1} << (walks ? 24 : 31))) return bad(WKV_ESIZE);
     p.rows_bytes = (static_cast<size_t>(n) + 255) / 256 * 256;
     p.states_bytes = (static_cast<size_t>(st) + 255) / 256 * 256;
     return p;
@@ -710,7 +712,7 @@ DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int
 extern "C" {
 
 size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
-    const DeltaPlan p = delta_plan(B, T, H, H, N, WKV_F32);
+    const DeltaPlan p = delta_plan(B, T, H, H, N, WKV_F32, true);
     return p.st == WKV_OK ? p.rows_bytes + p.states_bytes : 0;
 }
 
@@ -769,12 +771,12 @@ hipError_t run_delta_bwd(wkv::DeltaBwdArgs a, int64_t nseg, int64_t per, void* s
 extern "C" {
 
 size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N) {
-    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32, false);
     return p.st == WKV_OK && p.ns > 0 ? delta_split_bytes(B, T, H, N) : 0;
 }
 
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags) {
-    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32);
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, WKV_F32, true);
     if (p.st != WKV_OK || p.ns == 0 || T == 0) return 0;
     const size_t one = p.rows_bytes + p.states_bytes;
     const size_t split = (flags & WKV_WS_NO_SPLIT) != 0 ? 0 : delta_split_bytes(B, T, H, N);
@@ -785,7 +787,7 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
                                const int32_t* lengths, const float* w, const float* beta, const void* r, const void* k,
                                const void* v, void* o, const float* s_in, float* s_out, void* ckpt, void* workspace,
                                size_t workspace_bytes, void* hip_stream) {
-    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype);
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype, ckpt != nullptr);
     if (p.st != WKV_OK) return p.st;
     if (p.ns == 0) return WKV_OK;
     if ((s_in && !aligned(s_in, 16)) || (s_out && !aligned(s_out, 16))) return WKV_EALIGN;
@@ -810,7 +812,7 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
                                 const void* v, const void* go, const float* s_in, const float* ds_out, void* dr, void* dk,
                                 void* dv, float* dw, float* dbeta, float* ds_in, const void* ckpt, void* workspace,
                                 size_t workspace_bytes, void* hip_stream) {
-    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype);
+    const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype, true);
     if (p.st != WKV_OK) return p.st;
     if (p.ns == 0) return WKV_OK;
     if ((ds_in && !aligned(ds_in, 16)) || (ds_out && !aligned(ds_out, 16))) return WKV_EALIGN;
@@ -864,7 +866,7 @@ constexpr int64_t kMaxBlockNorm = 8192;  // channels a workgroup holds
 wkv_status_t head_norm_check(int64_t rows, int64_t H, int64_t G, int64_t* n) {
     if (rows < 0 || H < 0 || G < 1 || G > kMaxHeadNorm) return WKV_EINVAL;
     if (!mul3(rows, H, G, n) || *n > (int64_t{1} << 58)) return WKV_ESIZE;
-    if (H > ((int64_t{1} << 31) - 1) / G || rows * H >= (int64_t{1} << 31)) return WKV_ESIZE;
+    if (H >= (int64_t{1} << 24) / G || rows * H >= (int64_t{1} << 31)) return WKV_ESIZE;
     return WKV_OK;
 }
 

@@ -157,6 +157,15 @@ __device__ __forceinline__ void load_or(const float* p, int64_t c, float otherwi
 __device__ __forceinline__ float rsqrt1(float x) { return __builtin_amdgcn_rsqf(x); }
 
 constexpr int kBlock = 256;
+
+// Workgroups counted over two dimensions of the grid: one holds fewer than 2^32 threads.
+dim3 grid_of(int64_t blocks) {
+    constexpr int64_t kMost = int64_t{1} << 20;
+    if (blocks <= kMost) return dim3(static_cast<unsigned>(blocks));
+    return dim3(static_cast<unsigned>(kMost), static_cast<unsigned>((blocks + kMost - 1) / kMost));
+}
+__device__ __forceinline__ int64_t block_id() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 constexpr int kPairs = 1024;      // channels from which a thread of the block norm holds two vectors
 constexpr int kScalarVecs = 16;  // elements a lane of the element-by-element path: G up to 1024
 
@@ -164,7 +173,7 @@ constexpr int kScalarVecs = 16;  // elements a lane of the element-by-element pa
 template <typename TY, typename TG, int V, int NV>
 __global__ void __launch_bounds__(kBlock) head_norm_kernel(HeadNormArgs P) {
     const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1);
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
+    const int64_t id = block_id() * (kBlock / lanes) + threadIdx.x / lanes;
     const bool live = id < P.rows * P.H;
     const int64_t h = id % P.H, base = id * P.G, wb = h * P.G;
     const int G = static_cast<int>(P.G);
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
     __shared__ float tab[2][16][1];
     int turn = 0;
     const int n = P.threads, th = threadIdx.x % n;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
+    const int64_t row = block_id() * (blockDim.x / n) + threadIdx.x / n;
     if (row >= P.rows) return;  // a whole wave of a 64-thread row; a whole workgroup otherwise
     const int C = static_cast<int>(P.C);
     const float inv_c = 1.f / static_cast<float>(C);
@@ -687,8 +696,7 @@ template <typename TY, typename TG, int V, int NV>
 hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
     if (!bwd) {
         const int64_t per = kBlock / a.lanes;
-        hipLaunchKernelGGL((head_norm_kernel<TY, TG, V, NV>), dim3(static_cast<unsigned>((a.rows * a.H + per - 1) / per)),
-                           dim3(kBlock), 0, stream, a);
+        hipLaunchKernelGGL((head_norm_kernel<TY, TG, V, NV>), grid_of((a.rows * a.H + per - 1) / per), dim3(kBlock), 0, stream, a);
         return hipGetLastError();
     }
     const int64_t C = a.H * a.G;
@@ -726,8 +734,8 @@ hipError_t launch_head_t(HeadNormArgs a, bool bwd, hipStream_t stream) {
 template <typename TX, typename TY, int V, int NV>
 hipError_t launch_block_fwd(const BlockNormArgs& a, hipStream_t stream) {
     const int64_t block = a.threads == 64 ? 256 : a.threads, per = block / a.threads;
-    hipLaunchKernelGGL((block_norm_kernel<TX, TY, V, NV>), dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
-                       dim3(static_cast<unsigned>(block)), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<TX, TY, V, NV>), grid_of((a.rows + per - 1) / per), dim3(static_cast<unsigned>(block)),
+                       0, stream, a);
     return hipGetLastError();
 }
 

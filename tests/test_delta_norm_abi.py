@@ -49,7 +49,7 @@ def test_delta_refusals(lib, call):
         assert call(lib, **bad) == L.WKV_EINVAL, bad
     assert call(lib, dt=2) == L.WKV_EDTYPE
     for bad in (dict(B=1 << 31), dict(T=1 << 50), dict(H=1 << 40, HK=1 << 40), dict(H=1 << 16, HK=1 << 16),
-                dict(B=1 << 20, H=1 << 12, HK=1)):
+                dict(B=1 << 20, H=1 << 12, HK=1), dict(B=1 << 22, H=1, HK=1), dict(B=1 << 25, H=1, HK=1, T=1)):
         assert call(lib, **bad) == L.WKV_ESIZE, bad
     for name in ("w", "beta", "r", "k", "v"):
         assert call(lib, **{name: None}) == L.WKV_EINVAL, name
@@ -60,6 +60,8 @@ def test_delta_refusals(lib, call):
 
 
 def test_delta_forward_refusals(lib):
+    assert delta_fwd(lib, B=1 << 22, H=1, HK=1, T=16, ck=X) == L.WKV_ESIZE  # with a ckpt it walks
+    assert delta_fwd(lib, B=1 << 22, H=1, HK=1, T=16, o=None) == L.WKV_EINVAL  # without, it may
     assert delta_fwd(lib, o=None) == L.WKV_EINVAL
     for name in ("o", "s_out", "ck"):
         assert delta_fwd(lib, **{name: X + 4}) == L.WKV_EALIGN, name

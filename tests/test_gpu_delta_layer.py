@@ -321,3 +321,26 @@ def test_large_offsets():
     assert torch.equal(back["dx"][0], back["dx"][2]) and torch.equal(back["dy"][0], back["dy"][2])
     back = O.head_norm_backward(v, h, weight, None, o, heads=H)
     assert torch.equal(back[0][0], back[0][2]) and torch.equal(back[3][0], back[3][2])
+
+
+def test_many_narrow_rows():
+    """More rows than one dimension of a grid holds threads for: the last row (and the one where the second
+    dimension begins) must be the first one's, whose values are checked."""
+    O = ops()
+    for rows, H, G in ((70_000_000, 1, 3), (5_000_000, 1, 33)):
+        x = torch.zeros(rows, H * G, dtype=torch.bfloat16, device=DEV)
+        first = torch.randn(H * G, device=DEV).bfloat16()
+        # 2^20 workgroups of four heads, or of one row
+        marks = [0, 4 << 20, (4 << 20) - 1, (1 << 20) - 1, 1 << 20, rows - 1]
+        x[marks] = first
+        weight = torch.rand(H * G, device=DEV) + 0.5
+        want = (rms(first.double()) * weight.double()).cpu()
+        n = O.head_norm(x, weight, heads=H)
+        _, h = O.block_norm(x, x, weight, center=False) if G == 33 else (None, None)
+        for m in marks:
+            assert ((n[m].double().cpu() - want).abs() <= want.abs() * 2.0 ** -8 + 1e-6).all(), m
+            if h is not None:  # x + x, eps off by a factor of 4 in the mean square
+                assert ((h[m].double().cpu() - rms(2 * first.double()).cpu() * weight.double().cpu()).abs()
+                        <= want.abs() * 2.0 ** -7 + 1e-6).all(), m
+        assert int((n != 0).any(-1).sum()) == len(marks)
+        del x, n, h
