@@ -861,7 +861,10 @@ class DeltaFunction(torch.autograd.Function):
 
 
 def delta_rule(w, beta, r, k, v, state_in=None, lengths=None):
-    """Differentiable gated delta rule: (o, state after each row's last token) (see delta_forward)."""
+    """Differentiable gated delta rule: (o, state after each row's last token) (see delta_forward).
+    Without a gradient to take nothing is saved for one, and a few tokens are a decoding step."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (w, beta, r, k, v, state_in))):
+        return delta_forward(w, beta, r, k, v, lengths=lengths, state_in=state_in, return_state=True)
     return DeltaFunction.apply(w, beta, r, k, v, state_in, lengths)
 
 

@@ -344,3 +344,14 @@ def test_many_narrow_rows():
                         <= want.abs() * 2.0 ** -7 + 1e-6).all(), m
         assert int((n != 0).any(-1).sum()) == len(marks)
         del x, n, h
+
+
+def test_delta_rule_without_gradients():
+    O = ops()
+    w, beta, r, k, v, go, S, x = step_case(4, 5, 2, 64, torch.bfloat16)
+    want = O.delta_forward(w, beta, r, k, v, state_in=S, return_state=True)
+    with torch.no_grad():
+        off = O.delta_rule(w, beta, r, k, v.clone().requires_grad_(), S)
+    for got in (O.delta_rule(w, beta, r, k, v, S), off):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and not got[0].requires_grad
+    assert O.delta_rule(w, beta, r, k, v, S.clone().requires_grad_())[0].requires_grad
