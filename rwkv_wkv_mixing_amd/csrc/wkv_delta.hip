@@ -982,7 +982,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
     constexpr int NC = N / 16;
     const int lane = threadIdx.x & 63;
     const int x = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
+    int l16 = lane & 15, g = lane >> 4;
     const int64_t ntile = (P.T + kTile - 1) / kTile;
     const int64_t bhk = blockIdx.x % (P.B * P.HK), tile = blockIdx.x / (P.B * P.HK);
     const int64_t b = bhk / P.HK, hk = bhk % P.HK, per = P.H / P.HK;
@@ -1030,6 +1030,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             sm.beta[threadIdx.x] = t < len ? P.beta[(b * P.T + t) * P.H + h] : 0.f;
         }
         __syncthreads();
+        asm volatile("" : "+v"(l16), "+v"(g));
         float pre = 0.f, suf = 0.f;  // of this lane's token
 #pragma unroll
         for (int l = 0; l < kSub; ++l) {
@@ -1106,6 +1107,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
         // blocks J <= x with this wave's tokens as i: rows j = 4 g + q, columns i
 #pragma unroll 1
         for (int J = 0; J <= x; ++J) {
+            asm volatile("" : "+v"(l16), "+v"(g));  // else comparisons are worked out ahead and kept (spilled)
             f4 ae = {0.f, 0.f, 0.f, 0.f}, le = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -1153,6 +1155,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
         // blocks I >= x with this wave's tokens as j: rows i = 4 g + q, columns j
 #pragma unroll 1
         for (int I = x; I < kWaves; ++I) {
+            asm volatile("" : "+v"(l16), "+v"(g));
             f4 ae = {0.f, 0.f, 0.f, 0.f}, le = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f}, rk = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -1210,17 +1213,23 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             sm.colv[x][l16] = colv;
         }
         __syncthreads();
+        asm volatile("" : "+v"(l16), "+v"(g));
+        float c = 0.f;  // this group's four rows of the token's block
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = 4 * g + q;
+            c += i >= l16 ? sm.rowv[x][i] : sm.colv[x][i];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) c += j < l16 && i >= l16 ? sm.diag[x][i][j] : 0.f;
+        }
+        c = sum_rows(c);
         if (g == 0 && t0 + mine < P.T) {
-            float c = all * inner;
+            c = fmaf(all, inner, c);
             for (int I = x + 1; I < kWaves; ++I) {
                 c += sm.rows[I];
                 for (int J = 0; J < x; ++J) c += sm.cross[I][J];
             }
             for (int J = 0; J < x; ++J) c += sm.cols[J];
-            for (int i = 0; i < kSub; ++i) {
-                c += i >= l16 ? sm.rowv[x][i] : sm.colv[x][i];
-                for (int j = 0; j < kSub; ++j) c += j < l16 && i >= l16 ? sm.diag[x][i][j] : 0.f;
-            }
             const int64_t at = (b * P.T + t0 + mine) * P.H + h;
             P.dw[at] = t0 + mine < len ? -c : 0.f;
             P.dbeta[at] = dbeta;
