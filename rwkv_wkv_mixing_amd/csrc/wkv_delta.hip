@@ -1120,19 +1120,25 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             }
             float mid = pre;
             for (int i = 0; i < kWaves; ++i) mid += i > J && i < x ? sm.total[i] : 0.f;
+            float gap[4];
+            if (J == x) {
+                float run = 0.f;
+#pragma unroll
+                for (int l = kSub - 1; l >= 0; --l) {  // rates after token l, through l16
+                    if (l / 4 == g) gap[l % 4] = run;
+                    run += l <= l16 ? sm.w[kSub * x + l] : 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) gap[q] = mid + sm.suf[kSub * J + 4 * g + q];
+            }
             f4 da, dm;
             float sum = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int j = 4 * g + q;
-                float gap = mid + sm.suf[kSub * J + j];
-                if (J == x) {
-                    gap = 0.f;
-#pragma unroll
-                    for (int l = 0; l < kSub; ++l) gap += l > j && l <= l16 ? sm.w[kSub * x + l] : 0.f;
-                }
                 const bool ia = J < x || j <= l16, im = J < x || j < l16;
-                const float f = ex2(-gap) * sm.beta[kSub * J + j];
+                const float f = ex2(-gap[q]) * sm.beta[kSub * J + j];
                 da[q] = ia ? f * ae[q] : 0.f;
                 dm[q] = im ? -f * le[q] : 0.f;
                 sum += da[q] * rk[q] + dm[q] * kk[q];
@@ -1167,19 +1173,25 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             }
             float mid = suf;
             for (int i = 0; i < kWaves; ++i) mid += i > x && i < I ? sm.total[i] : 0.f;
+            float gap[4];
+            if (I == x) {
+                float run = 0.f;
+#pragma unroll
+                for (int l = 0; l < kSub; ++l) {  // rates after l16, through token l
+                    run += l > l16 ? sm.w[kSub * x + l] : 0.f;
+                    if (l / 4 == g) gap[l % 4] = run;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) gap[q] = mid + sm.pre[kSub * I + 4 * g + q];
+            }
             f4 da, dm;
             float sum = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int i = 4 * g + q;
-                float gap = mid + sm.pre[kSub * I + i];
-                if (I == x) {
-                    gap = 0.f;
-#pragma unroll
-                    for (int l = 0; l < kSub; ++l) gap += l > l16 && l <= i ? sm.w[kSub * x + l] : 0.f;
-                }
                 const bool ia = I > x || l16 <= i, im = I > x || l16 < i;
-                const float f = ex2(-gap);
+                const float f = ex2(-gap[q]);
                 da[q] = ia ? f * ae[q] : 0.f;
                 dm[q] = im ? -f * le[q] : 0.f;
                 const float p = da[q] * rk[q] + dm[q] * kk[q];
