@@ -16,6 +16,10 @@
 // from statistics computed again.  The gradients of weights are sums over the rows: every workgroup
 // keeps its channels' sums in registers over the rows it takes, writes them as one row of partial
 // sums, and norm_reduce_kernel adds those in order (bitwise reproducible).
+//
+// Measured, whole calls: head norm of 8192 x 64 heads of 64, float32 to bf16 with a gate, 46 us (5.8 TB/s);
+// its gradients at 8192 x 32 heads of 128, bf16, 70 us (4.8 TB/s); block norm of 8192 x 4096, bf16, 77 us
+// (4.4 TB/s, four sums over a row with a barrier each), its gradients 125 us (4.3 TB/s and 42 MB of partial sums).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
