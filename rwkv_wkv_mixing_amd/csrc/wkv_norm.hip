@@ -505,12 +505,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNormArgs P) {
 // dpost_b, dscale.
 //
 // A row's inputs are fetched while the row before it is worked on (NV == 1), and the channels' four weights
-// are kept in registers where there are 256 of them (at most 512 threads) beside the five sums.
+// are kept in registers beside the five sums; with NV > 1 there is room for neither.
 template <typename TX, typename TY, int V, int NV, int Threads>
 __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P) {
     __shared__ float tab[2][16][2];
     constexpr bool kAhead = NV == 1;
-    constexpr bool kKeep = kAhead && Threads <= 512;  // the weights in registers
     int turn = 0;
     const int n = P.threads, th = threadIdx.x % n;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
         }
     };
     Weights kept;
-    if (kKeep && th * V < C) weights(th * V, kept);
+    if (kAhead && th * V < C) weights(th * V, kept);
     if (kAhead && slot < P.rows) fetch(slot);
     for (int64_t row = slot; row < P.rows; row += P.slots) {  // the same trip count for a row's threads
         const int64_t base = row * P.C;
@@ -611,14 +610,14 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             float w[V];
-            if constexpr (!kKeep) load<V>(P.pre_w + c, w);
+            if constexpr (!kAhead) load<V>(P.pre_w + c, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 x[i][j] *= ix;
                 y[i][j] *= iy;
                 acc[0][i][j] = fmaf(d[i][j], x[i][j], acc[0][i][j]);
                 acc[1][i][j] += d[i][j];
-                d[i][j] *= kKeep ? kept.pre[j] : w[j];
+                d[i][j] *= kAhead ? kept.pre[j] : w[j];
                 s[0] += d[i][j];
                 s[1] = fmaf(d[i][j], x[i][j], s[1]);
             }
@@ -631,12 +630,12 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             const int c = (i * n + th) * V;
             if (c >= C) continue;
             Weights here;
-            if constexpr (!kKeep) weights(c, here);
+            if constexpr (!kAhead) weights(c, here);
             if constexpr (!kAhead) {
                 fetch_late(base + c, 0);
                 late(0);
             }
-            const Weights& w = kKeep ? kept : here;
+            const Weights& w = kAhead ? kept : here;
             float a[V], da[V];
             activate<V, true>(P.act, gated, g, a, da);
 #pragma unroll
@@ -716,7 +715,11 @@ hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
 
 template <typename TY, typename TG>
 hipError_t launch_head_v(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
-    if (!a.vec) return launch_head<TY, TG, 1, kScalarVecs>(a, bwd, stream);
+    if (!a.vec) {  // as many elements a lane as the head needs (16 always: heads of 100 took ten times those of 128)
+        if (a.G <= 128) return launch_head<TY, TG, 1, 2>(a, bwd, stream);
+        if (a.G <= 256) return launch_head<TY, TG, 1, 4>(a, bwd, stream);
+        return launch_head<TY, TG, 1, kScalarVecs>(a, bwd, stream);
+    }
     return a.G <= 512 ? launch_head<TY, TG, 8, 1>(a, bwd, stream) : launch_head<TY, TG, 8, 2>(a, bwd, stream);
 }
 
@@ -757,22 +760,25 @@ hipError_t launch_block_bwd(const BlockNormArgs& a, hipStream_t stream) {
     return e == hipSuccess ? launch_reduce(r, stream) : e;
 }
 
-// Threads that hold a row: 8 channels each from the smallest count that does (the forward 16 from kPairs
-// channels, half the threads to sum over: 8192 rows of 4096 with everything given 75 us against 80); or, off
-// the 16-byte grid, 1024 threads of single elements.
+// Threads that hold a row: a wave up to 512 channels, else 8 channels each from the smallest count that does (the
+// forward 16 from kPairs channels, half the threads to sum over: 8192 rows of 4096 with everything given 75 us
+// against 80; the backward 16 above 4096, for which 1024 threads have not the registers: 4096 rows of 8192 259 us
+// against 656).  Off the 16-byte grid, single elements: 512 threads in the forward up to 4096 (4096 rows of 1001
+// 24 us; 1024 threads 37), else 1024 (of 8191 140 us; 512 threads 214), and 1024 in the backward (of 4001 241 us;
+// 512 threads, which spill, 319).
 template <typename TX, typename TY>
 hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     a.slots = block_norm_slots(a.rows, a.C);
-    a.threads = !a.vec ? 1024 : a.C <= 512 ? 64 : static_cast<int>(pow2_at_least(a.C / 8));
+    const int wide = static_cast<int>(pow2_at_least((a.C + 7) / 8));
     if (!bwd) {
+        a.threads = a.C <= 512 ? 64 : !a.vec ? (a.C <= 4096 ? 512 : 1024) : a.C < kPairs ? wide : wide / 2;
         if (!a.vec) return launch_block_fwd<TX, TY, 1, 8>(a, stream);
-        if (a.C < kPairs) return launch_block_fwd<TX, TY, 8, 1>(a, stream);
-        a.threads /= 2;
-        return launch_block_fwd<TX, TY, 8, 2>(a, stream);
+        return a.C < kPairs ? launch_block_fwd<TX, TY, 8, 1>(a, stream) : launch_block_fwd<TX, TY, 8, 2>(a, stream);
     }
-    if (!a.vec)
-        return a.C <= 4096 ? launch_block_bwd<TX, TY, 1, 4, 1024>(a, stream) : launch_block_bwd<TX, TY, 1, 8, 1024>(a, stream);
-    return a.C <= 4096 ? launch_block_bwd<TX, TY, 8, 1, 512>(a, stream) : launch_block_bwd<TX, TY, 8, 1, 1024>(a, stream);
+    a.threads = a.C <= 512 ? 64 : !a.vec ? 1024 : a.C <= 4096 ? wide : 512;
+    if (a.vec) return a.C <= 4096 ? launch_block_bwd<TX, TY, 8, 1, 512>(a, stream) : launch_block_bwd<TX, TY, 8, 2, 512>(a, stream);
+    if (a.C <= 512) return launch_block_bwd<TX, TY, 1, 8, 512>(a, stream);
+    return a.C <= 4096 ? launch_block_bwd<TX, TY, 1, 4, 1024>(a, stream) : launch_block_bwd<TX, TY, 1, 8, 1024>(a, stream);
 }
 
 hipError_t launch_block_t(const BlockNormArgs& a, bool bwd, hipStream_t stream) {
@@ -792,7 +798,7 @@ int64_t head_norm_chunks(int64_t rows, int64_t C) {
 
 // Rows of partial sums of a block norm's backward: 8 waves a compute unit, 4 rows or more behind each.
 int64_t block_norm_slots(int64_t rows, int64_t C) {
-    const int64_t threads = C <= 512 ? 64 : pow2_at_least((C + 7) / 8);
+    const int64_t threads = C <= 512 ? 64 : C > 4096 ? 512 : pow2_at_least((C + 7) / 8);
     const int64_t most = 256 * 512 / threads, n = (rows + 3) / 4;
     return n < most ? n : most;
 }

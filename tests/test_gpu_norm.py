@@ -81,6 +81,14 @@ def test_head_norm(shape, types, center):
     run_head(head_case(*shape, *types), shape[1], "silu", center, types[1])
 
 
+@pytest.mark.parametrize("shape", [(33, 3, 100), (20, 2, 129), (21, 2, 201), (6, 2, 257), (50, 64, 100)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("shared", [False, True], ids=["own", "shared"])
+def test_head_norm_off_the_grid(shape, shared):
+    """Heads that are no multiple of 8: two, four or sixteen elements a lane."""
+    run_head(head_case(*shape, F32, BF, shared, True, True), shape[1], "sigmoid", True, BF)
+
+
 @pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
 @pytest.mark.parametrize("shared,bias,gated", [(True, True, True), (True, False, False), (False, False, True)])
 def test_head_norm_options(act, shared, bias, gated):
@@ -139,6 +147,12 @@ def run_block(c, act, center, eps=1e-5):
 @pytest.mark.parametrize("center", [False, True], ids=["rms", "layer"])
 def test_block_norm(shape, types, center):
     run_block(block_case(*shape, *types), "sigmoid", center)
+
+
+@pytest.mark.parametrize("shape", [(1100, 4104), (40, 5000), (30, 4101), (1030, 513), (300, 511)], ids=lambda s: "x".join(map(str, s)))
+def test_block_norm_many_rows(shape):
+    """Wide and odd rows, several to a workgroup of the backward."""
+    run_block(block_case(*shape, F32, BF), "silu", True)
 
 
 @pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
