@@ -513,6 +513,9 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
     int turn = 0;
     const int n = P.threads, th = threadIdx.x % n;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
+    // A spare wave of the last workgroup (with 64 threads a row only, where nothing waits at a barrier).  Its rows
+    // are other slots' rows, whose gx may already hold their dx.
+    if (slot >= P.slots) return;
     const int C = static_cast<int>(P.C);
     const float inv_c = 1.f / static_cast<float>(C);
     const bool post = P.post_w != nullptr, gated = P.gate != nullptr;
@@ -671,7 +674,6 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
             store<V>(static_cast<TY*>(P.dy) + base + c, d[i]);
         }
     }
-    if (slot >= P.slots) return;
     const bool want[5] = {true, P.pre_b != nullptr, post, P.post_b != nullptr, P.scale != nullptr};
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
