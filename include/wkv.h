@@ -543,7 +543,8 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
                                const float* s_in, float* s_out, void* ckpt, void* workspace,
                                size_t workspace_bytes, void* hip_stream);
 
-/* Bytes of wkv_delta_forward's ckpt (0 for invalid arguments or no tokens), of
+/* Bytes of wkv_delta_forward's ckpt (0 for no tokens, and for arguments that it
+ * refuses whatever HK is), of
  * its optional scratch (0 when no time split would be made), and of
  * wkv_delta_backward's scratch (flags: WKV_WS_HAVE_CKPT when a ckpt will be
  * passed; else room to recompute it is included). */

@@ -751,7 +751,10 @@ def _launch_on(dev, bind, name, fn, args, result, scope):
 
 
 def delta_ckpt_bytes(B: int, T: int, H: int, N: int) -> int:
-    return int(L.lib().wkv_delta_ckpt_bytes(B, T, H, N))
+    nbytes = int(L.lib().wkv_delta_ckpt_bytes(B, T, H, N))
+    if nbytes == 0 and B * T * H != 0:
+        raise ValueError(f"no ckpt for B={B}, T={T}, H={H}, N={N}: these are not sizes of a delta-rule call")
+    return nbytes
 
 
 def new_delta_ckpt(B: int, T: int, H: int, N: int, device) -> torch.Tensor:

@@ -1,0 +1,32 @@
+"""CPU-side checks that what the delta-rule and norm calls say of their sizes is what they take: a call whose sizes
+pass is told by the error of the missing output that is looked at next, so nothing is launched."""
+import pytest
+
+from rwkv_wkv_mixing_amd import _lib as L
+from rwkv_wkv_mixing_amd import ops as O
+
+from test_delta_norm_abi import X, delta_bwd, delta_fwd, lib  # noqa: F401  (lib is a fixture)
+
+STATE, ROW = 64 * 64 * 4, 64 * 4
+
+
+@pytest.mark.parametrize("B,T,H,HK", [(53, 257, 64000, 1000), (1, 1 << 24, 64, 1), (4, 17, 64, 1), (3, 64, 5, 5)])
+def test_ckpt_bytes_of_calls_that_are_taken(lib, B, T, H, HK):  # noqa: F811
+    """The errors and the states before every 64 tokens, also where many value heads share few key heads."""
+    assert delta_fwd(lib, B=B, T=T, H=H, HK=HK, ck=X, o=None) == L.WKV_EINVAL  # the sizes pass, the output is missing
+    assert delta_bwd(lib, B=B, T=T, H=H, HK=HK, dr=None) == L.WKV_EINVAL
+    want = B * T * H * ROW + B * H * -(-T // 64) * STATE
+    assert lib.wkv_delta_ckpt_bytes(B, T, H, 64) == want == O.delta_ckpt_bytes(B, T, H, 64)
+    assert lib.wkv_delta_backward_workspace_bytes(B, T, H, HK, 64, 1 | 2) == want
+
+
+@pytest.mark.parametrize("B,T,H,N", [(1, 64, 1, 96), (1 << 22, 64, 1, 64), (1, 1 << 31, 1, 64), (-1, 64, 1, 64)])
+def test_ckpt_of_no_call_is_refused(lib, B, T, H, N):  # noqa: F811
+    assert lib.wkv_delta_ckpt_bytes(B, T, H, N) == 0
+    with pytest.raises(ValueError, match="no ckpt"):
+        O.new_delta_ckpt(B, T, H, N, "cpu")
+
+
+def test_ckpt_of_no_tokens():
+    for B, T, H in ((0, 64, 2), (2, 0, 2), (2, 64, 0)):
+        assert O.delta_ckpt_bytes(B, T, H, 64) == 0 and O.new_delta_ckpt(B, T, H, 64, "cpu").numel() == 1
