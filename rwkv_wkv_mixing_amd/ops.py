@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
@@ -863,10 +864,20 @@ class DeltaFunction(torch.autograd.Function):
         return dw, dbeta, dr, dk, dv, ds, None
 
 
+def _has_tangent(tensors):
+    """Whether one of the tensors carries a forward-mode derivative (which requires_grad says nothing of, and
+    which is carried with gradients switched off too); outside a dual level this is one comparison."""
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def delta_rule(w, beta, r, k, v, state_in=None, lengths=None):
     """Differentiable gated delta rule: (o, state after each row's last token) (see delta_forward).
-    Without a gradient to take nothing is saved for one, and a few tokens are a decoding step."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (w, beta, r, k, v, state_in))):
+    Without a gradient to take nothing is saved for one, and a few tokens are a decoding step.
+    Forward-mode derivatives are refused."""
+    inputs = (w, beta, r, k, v, state_in)
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)) and not _has_tangent(inputs):
         return delta_forward(w, beta, r, k, v, lengths=lengths, state_in=state_in, return_state=True)
     return DeltaFunction.apply(w, beta, r, k, v, state_in, lengths)
 
