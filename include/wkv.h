@@ -533,7 +533,8 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
  * r, k, v, o, s_in, s_out, ckpt are 16-byte aligned (WKV_EALIGN otherwise).
  * WKV_EINVAL also for another N or an H that HK does not divide; WKV_ESIZE
- * from H N = 2^22, and from B H = 2^22 (2^25 for up to 16 tokens without a ckpt).
+ * from H N = 2^22, and from B H = 2^22 (for up to 16 tokens without a ckpt from
+ * B H = 2^25, and 2^25 - 1 with N = 128).
  * A non-finite input may reach every output of its head from the 64 tokens it is
  * among on.
  */

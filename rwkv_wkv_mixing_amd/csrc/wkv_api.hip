@@ -698,9 +698,11 @@ DeltaPlan delta_plan(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int
     if (!mul3(H, N, 4, &hn) || !mul3(B, T, hn, &n) || n > kMost) return bad(WKV_ESIZE);
     if (!mul3(p.ns, (T + 63) / 64, 4, &st) || st > kMost) return bad(WKV_ESIZE);
     if (H * N >= (int64_t{1} << 22)) return bad(WKV_ESIZE);  // 64 rows of float32 values below 2^31 bytes
-    // grids of fewer than 2^32 threads: up to 768 a pair, or 128 for a few tokens; 256 per (64 tokens, row, key head)
+    // grids of fewer than 2^32 threads: up to 768 a pair; 256 per (64 tokens, row, key head); for a few tokens a wave
+    // per 64 columns of a pair, four waves a workgroup
     int64_t tiles;
-    if (bh >= (int64_t{1} << 22) && (walks || T > wkv::kDeltaStepMaxT || bh >= (int64_t{1} << 25))) return bad(WKV_ESIZE);
+    const bool walk = walks || T > wkv::kDeltaStepMaxT;
+    if (bh >= (int64_t{1} << (walk ? 22 : 25)) || (bh * (N / 64) + 3) / 4 >= (int64_t{1} << 24)) return bad(WKV_ESIZE);
     if (!mul3(B, HK, (T + 63) / 64, &tiles) || tiles >= (int64_t{1} << (walks ? 24 : 31))) return bad(WKV_ESIZE);
     p.rows_bytes = (static_cast<size_t>(n) + 255) / 256 * 256;
     p.states_bytes = (static_cast<size_t>(st) + 255) / 256 * 256;

@@ -30,3 +30,12 @@ def test_ckpt_of_no_call_is_refused(lib, B, T, H, N):  # noqa: F811
 def test_ckpt_of_no_tokens():
     for B, T, H in ((0, 64, 2), (2, 0, 2), (2, 64, 0)):
         assert O.delta_ckpt_bytes(B, T, H, 64) == 0 and O.new_delta_ckpt(B, T, H, 64, "cpu").numel() == 1
+
+
+@pytest.mark.parametrize("N,most", [(64, (1 << 25) - 1), (128, (1 << 25) - 2)])
+def test_most_pairs_of_a_few_tokens(lib, N, most):  # noqa: F811
+    """A wave per 64 columns of a pair, four waves a workgroup: one pair more would be a grid of 2^32 threads."""
+    for T in (1, 16):
+        assert delta_fwd(lib, B=most, H=1, HK=1, T=T, N=N, o=None) == L.WKV_EINVAL  # the sizes pass
+        assert delta_fwd(lib, B=most + 1, H=1, HK=1, T=T, N=N, o=None) == L.WKV_ESIZE
+    assert (most * N // 64 + 3) // 4 * 256 < 1 << 32
