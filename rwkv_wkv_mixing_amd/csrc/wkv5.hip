@@ -1663,7 +1663,8 @@ __global__ void wkv5_reduce_kernel(const float* part, int64_t B, int64_t H, floa
 
 // T == 0: the state after the sequence is the state before it (or zero).
 __global__ void wkv5_state_copy_kernel(const float* s_in, float* s_out, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t i = block * blockDim.x + threadIdx.x;
     if (i < n) s_out[i] = s_in != nullptr ? s_in[i] : 0.f;
 }
 
@@ -1671,8 +1672,10 @@ __global__ void wkv5_state_copy_kernel(const float* s_in, float* s_out, int64_t 
 
 hipError_t launch_wkv5_state_copy(const float* s_in, float* s_out, int64_t n, hipStream_t stream) {
     if (n <= 0 || s_out == nullptr || s_in == s_out) return hipSuccess;
-    hipLaunchKernelGGL(wkv5_state_copy_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
-                       s_in, s_out, n);
+    // workgroups counted over two dimensions: one holds fewer than 2^32 threads, a state may hold more elements
+    const int64_t blocks = (n + 255) / 256, most = int64_t{1} << 20;
+    const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>((blocks + most - 1) / most));
+    hipLaunchKernelGGL(wkv5_state_copy_kernel, grid, dim3(256), 0, stream, s_in, s_out, n);
     return hipGetLastError();
 }
 
