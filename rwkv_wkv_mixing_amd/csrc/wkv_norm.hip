@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kBlock) head_norm_bwd_kernel(HeadNormArgs P) {
     const int lanes = P.lanes, lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes;
     const int hpb = P.hpb, rpb = kBlock / lanes / hpb;
     const int64_t hblocks = (P.H + hpb - 1) / hpb;
-    const int64_t hb = blockIdx.x % hblocks, chunk = blockIdx.x / hblocks;
+    const int64_t hb = block_id() % hblocks, chunk = block_id() / hblocks;
+    if (chunk >= P.chunks) return;  // (a whole workgroup, behind the last one of a grid of two dimensions)
     const int hs = slot % hpb, rs = slot / hpb;
     const int64_t h = hb * hpb + hs;
     const int G = static_cast<int>(P.G);
@@ -706,8 +707,8 @@ hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
     }
     const int64_t C = a.H * a.G;
     const size_t lds = static_cast<size_t>(kBlock / a.lanes) * a.G * sizeof(float);
-    hipLaunchKernelGGL((head_norm_bwd_kernel<TY, TG, V, NV>), dim3(static_cast<unsigned>((a.H + a.hpb - 1) / a.hpb * a.chunks)),
-                       dim3(kBlock), lds, stream, a);
+    hipLaunchKernelGGL((head_norm_bwd_kernel<TY, TG, V, NV>), grid_of((a.H + a.hpb - 1) / a.hpb * a.chunks), dim3(kBlock), lds,
+                       stream, a);
     hipError_t e = hipGetLastError();
     ReduceArgs r{a.chunks, C};
     r.add(a.ws, a.dweight);
