@@ -817,7 +817,16 @@ wkv_status_t wkv_delta_backward(int64_t B, int64_t T, int64_t H, int64_t HK, int
                                 size_t workspace_bytes, void* hip_stream) {
     const DeltaPlan p = delta_plan(B, T, H, HK, N, in_dtype, true);
     if (p.st != WKV_OK) return p.st;
-    if (p.ns == 0) return WKV_OK;
+    if (p.ns == 0) {  // dr and dk of key heads that no value head reads: empty sums
+        const int64_t n = B * T * HK * N;
+        if (n == 0) return WKV_OK;
+        if (!dr || !dk) return WKV_EINVAL;
+        if (!aligned(dr, 16) || !aligned(dk, 16)) return WKV_EALIGN;
+        const int64_t words = n / 4 * static_cast<int64_t>(in_size(in_dtype));
+        hipError_t e = wkv::launch_zero(static_cast<float*>(dr), words, static_cast<hipStream_t>(hip_stream));
+        if (e == hipSuccess) e = wkv::launch_zero(static_cast<float*>(dk), words, static_cast<hipStream_t>(hip_stream));
+        return hip_status(e);
+    }
     if ((ds_in && !aligned(ds_in, 16)) || (ds_out && !aligned(ds_out, 16))) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (T == 0) return hip_status(wkv::launch_wkv5_state_copy(ds_out, ds_in, p.ns, stream));  // dS0 = dS_T
@@ -929,8 +938,8 @@ wkv_status_t wkv_head_norm_backward(int64_t rows, int64_t H, int64_t G, int y_dt
     const bool shared = (flags & WKV_NORM_SHARED) != 0;
     if (n == 0) {  // empty sums
         const int64_t nw = shared ? G : H * G;
-        hipError_t e = wkv::launch_norm_zero(dweight, nw, stream);
-        if (e == hipSuccess && bias) e = wkv::launch_norm_zero(dbias, nw, stream);
+        hipError_t e = wkv::launch_zero(dweight, nw, stream);
+        if (e == hipSuccess && bias) e = wkv::launch_zero(dbias, nw, stream);
         return hip_status(e);
     }
     if (!y || !weight || !gout || !dy || (gate && !dgate)) return WKV_EINVAL;
@@ -995,7 +1004,7 @@ wkv_status_t wkv_block_norm_backward(int64_t rows, int64_t C, int x_dtype, int d
         float* const out[5] = {dpre_w, pre_b ? dpre_b : nullptr, post_w ? dpost_w : nullptr, post_b ? dpost_b : nullptr,
                                scale ? dscale : nullptr};
         hipError_t e = hipSuccess;
-        for (int k = 0; k < 5 && e == hipSuccess; ++k) e = wkv::launch_norm_zero(out[k], C, stream);
+        for (int k = 0; k < 5 && e == hipSuccess; ++k) e = wkv::launch_zero(out[k], C, stream);
         return hip_status(e);
     }
     if (!x_out || !y || !pre_w || !gh || !dx || !dy || (gate && !dgate)) return WKV_EINVAL;

@@ -371,7 +371,7 @@ hipError_t launch_head_norm(const HeadNormArgs& a, hipStream_t stream);
 hipError_t launch_head_norm_bwd(const HeadNormArgs& a, hipStream_t stream);
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, hipStream_t stream);
-hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream);
+hipError_t launch_zero(float* p, int64_t n, hipStream_t stream);  // p may be NULL
 int64_t head_norm_chunks(int64_t rows, int64_t C);
 int64_t block_norm_slots(int64_t rows, int64_t C);
 

@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(Threads) block_norm_bwd_kernel(BlockNormArgs P
     }
 }
 
-__global__ void norm_zero_kernel(float* p, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+__global__ void zero_kernel(float* p, int64_t n) {
+    const int64_t i = block_id() * kBlock + threadIdx.x;
     if (i < n) p[i] = 0.f;
 }
 
@@ -806,9 +806,9 @@ int64_t block_norm_slots(int64_t rows, int64_t C) {
     return n < most ? n : most;
 }
 
-hipError_t launch_norm_zero(float* p, int64_t n, hipStream_t stream) {
+hipError_t launch_zero(float* p, int64_t n, hipStream_t stream) {
     if (p == nullptr || n <= 0) return hipSuccess;
-    hipLaunchKernelGGL(norm_zero_kernel, dim3(static_cast<unsigned>((n + kBlock - 1) / kBlock)), dim3(kBlock), 0, stream, p, n);
+    hipLaunchKernelGGL(zero_kernel, grid_of((n + kBlock - 1) / kBlock), dim3(kBlock), 0, stream, p, n);
     return hipGetLastError();
 }
 

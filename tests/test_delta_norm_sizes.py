@@ -39,3 +39,12 @@ def test_most_pairs_of_a_few_tokens(lib, N, most):  # noqa: F811
         assert delta_fwd(lib, B=most, H=1, HK=1, T=T, N=N, o=None) == L.WKV_EINVAL  # the sizes pass
         assert delta_fwd(lib, B=most + 1, H=1, HK=1, T=T, N=N, o=None) == L.WKV_ESIZE
     assert (most * N // 64 + 3) // 4 * 256 < 1 << 32
+
+
+def test_gradients_of_key_heads_without_value_heads(lib):  # noqa: F811
+    """dr and dk are outputs of a call without value heads too."""
+    for name in ("dr", "dk"):
+        assert delta_bwd(lib, H=0, HK=2, **{name: None}) == L.WKV_EINVAL, name
+        assert delta_bwd(lib, H=0, HK=2, **{name: X + 8}) == L.WKV_EALIGN, name
+    assert delta_bwd(lib, H=0, HK=0, dr=None, dk=None) == L.WKV_OK
+    assert delta_bwd(lib, H=0, HK=2, T=0, dr=None, dk=None) == L.WKV_OK
