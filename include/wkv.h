@@ -507,8 +507,12 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  *
  * Up to 16 tokens without a ckpt are computed token by token with the state in
  * registers (decoding); more, or with a ckpt, by 16-token blocks on the matrix
- * cores.  All arithmetic is float32 whatever the inputs' dtype; outputs are
- * rounded once.
+ * cores.  States, errors and sums are float32 whatever the inputs' dtype, and
+ * outputs are rounded once.  By blocks with bf16 inputs, o alone is made of
+ * factors held to 16 bits: it reads the state to within 2^-18 of each term, and
+ * what the 16 tokens before a block's own add to 3 2^-18 (float32 keeps 2^-24; the
+ * state, the ckpt and the float32 call have nothing of it).  o's own rounding is
+ * 2^-8 of it, so this shows where its terms cancel by 2^9 or more.
  *
  * B, T      batch rows, tokens (>= 0).
  * H, HK     value heads and key heads: H a multiple of HK, value head h reads
@@ -545,10 +549,9 @@ wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int6
                                size_t workspace_bytes, void* hip_stream);
 
 /* Bytes of wkv_delta_forward's ckpt (0 for no tokens, and for arguments that it
- * refuses whatever HK is), of
- * its optional scratch (0 when no time split would be made), and of
- * wkv_delta_backward's scratch (flags: WKV_WS_HAVE_CKPT when a ckpt will be
- * passed; else room to recompute it is included). */
+ * refuses whatever HK is), of its optional scratch (0 when no time split would be
+ * made), and of wkv_delta_backward's scratch (flags: WKV_WS_HAVE_CKPT when a ckpt
+ * will be passed; else room to recompute it is included). */
 size_t wkv_delta_ckpt_bytes(int64_t B, int64_t T, int64_t H, int64_t N);
 size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N);
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int flags);
@@ -561,7 +564,9 @@ size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64
  *     dk_t = beta_t G'_t e_t^T - D_t lambda_t^T,   dbeta_t = e_t . k_t G'_t,
  *     H_t = G'_t - k_t^T lambda_t,   dw_t = -<H_t, D_t>,   G_{t-1} = e^{-w_t} H_t
  * and ds_in = G_0.  dr and dk of a key head are summed over its value heads in
- * a fixed order; all results are bitwise reproducible.
+ * a fixed order; all results are bitwise reproducible.  Sums are float32; with
+ * bf16 inputs dr and dk alone take the pairs of tokens of one tile of 64 from
+ * factors held to 16 bits, within 2^-18 of each term (as o in the forward).
  *
  * go        [B, T, H N] in_dtype: the gradient of o.  Rows behind a row's length
  *           are not read.

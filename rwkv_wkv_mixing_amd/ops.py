@@ -767,7 +767,8 @@ def delta_forward(w, beta, r, k, v, *, lengths=None, state_in=None, state_out=No
                   ckpt=None, workspace=None, split=True, bind=False):
     """The gated delta rule: o [B, T, H N] from w, beta [B, T, H] float32, r, k [B, T, HK N] and
     v [B, T, H N] (float32 or bfloat16, o too); N is 64 or 128 and value head h reads key head
-    h // (H // HK).  Per token D = e^{-w} S, e = v - k D, S = D + beta k^T e, o = r S.
+    h // (H // HK).  Per token D = e^{-w} S, e = v - k D, S = D + beta k^T e, o = r S.  The state is
+    float32; bfloat16 calls of more than 16 tokens, or with a ckpt, sum o from terms good to 2^-18.
 
     lengths: None or [B] int32, the tokens of each row (the rest are not read, leave the state and
     give zeros).  state_in: [B, H, N, N] float32 or None (zero).  state_out: tensor to receive the
@@ -807,7 +808,7 @@ def delta_backward(w, beta, r, k, v, go, *, lengths=None, state_in=None, grad_st
     lengths=lengths, state_in=state_in, return_state=True): (dr, dk, dv, dw, dbeta, ds_in), dr, dk, dv
     in r's dtype (those of a key head summed over its value heads), dw, dbeta [B, T, H] float32, ds_in
     [B, H, N, N] float32 or None.  go: [B, T, H N] in r's dtype.  ckpt: None or what the forward wrote.  split as in
-    delta_forward."""
+    delta_forward.  Sums are float32; bfloat16 dr and dk take a tile's pairs of tokens from terms good to 2^-18."""
     B, T, H, HK, N = _delta_inputs(w, beta, r, k, v, lengths)
     dev = r.device
     _need(go, "go", r.dtype, (B, T, H * N), dev)

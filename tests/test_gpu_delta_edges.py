@@ -29,3 +29,92 @@ def test_key_heads_without_value_heads(dtype):
     leaves = [t.requires_grad_() for t in (w, r.clone())]
     O.delta_rule(leaves[0], w.detach(), leaves[1], r, e(2, 37, 0))[0].sum().backward()
     assert not bool(leaves[1].grad.any())
+
+
+U, TWO_TERMS = 2.0 ** -24, 2.0 ** -18
+
+
+def signs(g, *shape):
+    """+-1/8 in 64 channels, as many of each: of length 1 and orthogonal to all ones, both exactly."""
+    x = torch.rand(*shape, 64, generator=g).argsort(-1)
+    return ((x % 2) * 2 - 1) / 8.0
+
+
+def held(name, got, ref, mag, c):
+    import numpy as np
+
+    g = got.double().cpu().numpy()
+    ratio = np.abs(g - ref) / (2.0 ** -8 * np.abs(ref) + c * mag)
+    print(f"  {name}: worst err / bound {ratio.max():.3f}, terms cancel by {np.median(mag / (np.abs(ref) + 1e-30)):.0e}", flush=True)
+    assert ratio.max() <= 1.0, name
+
+
+def test_bf16_output_where_its_terms_cancel():
+    """o reads a state whose rows are alike through r that is orthogonal to them: the terms cancel by 2^12, and the
+    bf16 rounding of what is left hides nothing.  Bound, of the sum of the terms' magnitudes, those of the state
+    before the token's pair of blocks and of the pair's own tokens: 2^-18 for each term of the state and 3 2^-18 for
+    each of the other block, held to two bf16 terms; and the float32 sums, of N + 32 terms at each of T tokens with
+    independent roundings, u sqrt((N + 32) T), eight times that for the largest of all elements."""
+    import numpy as np
+    from oracle import delta_forward_ref
+
+    T, N = 100, 64
+    g = torch.Generator().manual_seed(0)
+    r, k, v = signs(g, 1, T), signs(g, 1, T), torch.randn(1, T, N, generator=g).bfloat16().float()
+    w, beta = torch.full((1, T, 1), 1e-3), torch.rand(1, T, 1, generator=g)
+    S0 = 1000.0 + torch.randn(1, 1, N, N, generator=g)
+    host = [t.double().numpy() for t in (w, beta, r, k, v)]
+    ref, Sref = delta_forward_ref(*host, 1, S0.double().numpy())
+    a, mag, S = np.exp(-host[0][0, :, 0]), np.zeros((T, N)), S0[0, 0].double().numpy()
+    for t0 in range(0, T, 32):  # the terms of a pair of blocks
+        e, D = [], S
+        for t in range(t0, min(t0 + 32, T)):
+            D = a[t] * D
+            e.append(host[4][0, t] - host[3][0, t] @ D)
+            D = D + host[1][0, t, 0] * np.outer(host[3][0, t], e[-1])
+            mag[t] = np.abs(host[2][0, t]) @ np.abs(S) + sum(
+                abs(host[2][0, t] @ host[3][0, t0 + s]) * host[1][0, t0 + s, 0] * np.abs(e[s]) for s in range(len(e)))
+        S = D
+    assert np.allclose(S, Sref[0, 0])
+    d = [t.to(DEV) for t in (w, beta)] + [t.bfloat16().to(DEV) for t in (r, k, v)]
+    o, S1 = ops().delta_forward(*d, state_in=S0.to(DEV), return_state=True)
+    eps = U * np.sqrt((N + 32) * T)
+    held("o", o[0], ref[0], mag, 3 * TWO_TERMS + 8 * eps)
+    assert np.linalg.norm(S1.double().cpu().numpy() - Sref) <= eps * np.linalg.norm(Sref)  # float32 throughout
+
+
+def test_bf16_gradients_where_their_terms_cancel():
+    """Keys and receptances that come with their opposites: dr and dk sum a tile's pairs of tokens that cancel.
+    Bound: 2^-18 of each pair's magnitude (two bf16 terms), and the float32 sums of both walks, 2 u sqrt((N + 32) T),
+    eight times that for the largest of all elements."""
+    import numpy as np
+    from oracle import delta_backward_ref
+
+    T, N = 64, 64
+    g = torch.Generator().manual_seed(1)
+    pairs = lambda x: torch.stack((x, -x), 2).reshape(1, T, N)  # noqa: E731
+    r, k = pairs(signs(g, 1, T // 2)), pairs(signs(g, 1, T // 2))
+    c = torch.randn(1, 1, N, generator=g).bfloat16().float()
+    v, go = 8 * c.expand(1, T, N).contiguous(), c.expand(1, T, N).contiguous()
+    w, beta = torch.zeros(1, T, 1), torch.full((1, T, 1), 2.0 ** -12)
+    host = [t.double().numpy() for t in (w, beta, r, k, v, go)]
+    dr, dk, dv, *_ = delta_backward_ref(*host, 1)
+    S, e = np.zeros((N, N)), []
+    for t in range(T):
+        e.append(host[4][0, t] - host[3][0, t] @ S)
+        S = S + 2.0 ** -12 * np.outer(host[3][0, t], e[-1])
+    size = lambda x: np.linalg.norm(x, axis=-1)  # noqa: E731
+    e, gn, ln, b = size(np.array(e)), size(host[5][0]), size(dv[0]), 2.0 ** -12
+    ra, ka = np.abs(host[2][0]), np.abs(host[3][0])
+    mr, mk = np.zeros((T, N)), np.zeros((T, N))
+    for t in range(T):
+        mr[t] = b * gn[t] * (e[:t + 1, None] * ka[:t + 1]).sum(0)
+        mk[t] = b * (e[t] * (gn[t:, None] * ra[t:]).sum(0) + e[t] * (ln[t + 1:, None] * ka[t + 1:]).sum(0)
+                     + ln[t] * (e[:t, None] * ka[:t]).sum(0))
+    d = [t.to(DEV) for t in (w, beta)] + [t.bfloat16().to(DEV) for t in (r, k, v, go)]
+    got = ops().delta_backward(*d)
+    eps = U * np.sqrt((N + 32) * T)
+    held("dr", got[0][0, 1::2], dr[0, 1::2], mr[1::2], TWO_TERMS + 16 * eps)  # behind a whole pair
+    held("dk", got[1][0, 1::2], dk[0, 1::2], mk[1::2], TWO_TERMS + 16 * eps)
+    held("dr", got[0][0], dr[0], mr, TWO_TERMS + 16 * eps)
+    held("dk", got[1][0], dk[0], mk, TWO_TERMS + 16 * eps)
