@@ -118,3 +118,43 @@ def test_bf16_gradients_where_their_terms_cancel():
     held("dk", got[1][0, 1::2], dk[0, 1::2], mk[1::2], TWO_TERMS + 16 * eps)
     held("dr", got[0][0], dr[0], mr, TWO_TERMS + 16 * eps)
     held("dk", got[1][0], dk[0], mk, TWO_TERMS + 16 * eps)
+
+
+@pytest.mark.parametrize("B,T,HK,H,N", [(16, 130, 16, 32, 64), (11, 130, 10, 20, 128)])
+def test_gradient_workgroups_that_walk_many_tiles(B, T, HK, H, N):
+    """More (64 tokens, row, key head) places than workgroups of the bf16 gradient kernel (512 at N = 64, 256 at
+    N = 128), rows of every length and some of none among them: each row's gradients are bit for bit those of a call
+    of that row alone, in which no workgroup takes a second place, and two rows' are the oracle's."""
+    import numpy as np
+    from oracle import delta_backward_ref
+
+    O = ops()
+    assert -(-T // 64) * B * HK > (512 if N == 64 else 256) >= -(-T // 64) * HK
+    g = torch.Generator().manual_seed(N)
+    rn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    w, beta = torch.rand(B, T, H, generator=g) * 0.3, torch.rand(B, T, H, generator=g)
+    k = rn(B, T, HK, N)
+    k = (k / k.norm(dim=-1, keepdim=True)).reshape(B, T, HK * N)
+    p = [w, beta] + [t.bfloat16() for t in (rn(B, T, HK * N) / N ** 0.5, k, rn(B, T, H * N), rn(B, T, H * N))]
+    S0, dS = rn(B, H, N, N), rn(B, H, N, N)
+    lens = [T, 0, 64, 1, 65, 129, 128, 0, 63, 17, T, 90, 0, 0, 100, T][:B]
+    d = [t.to(DEV) for t in p]
+    call = lambda *a, ln, S, G: O.delta_backward(*a, lengths=ln, state_in=S, grad_state_out=G, need_state_grad=True,  # noqa: E731
+                                                 split=False)
+    ln, S, G = torch.tensor(lens, dtype=torch.int32, device=DEV), S0.to(DEV), dS.to(DEV)
+    got = call(*d, ln=ln, S=S, G=G)
+    names = ("dr", "dk", "dv", "dw", "dbeta", "dS0")
+    for b in range(B):
+        want = call(*(t[b:b + 1].contiguous() for t in d), ln=ln[b:b + 1].contiguous(), S=S[b:b + 1], G=G[b:b + 1])
+        for n, x, y in zip(names, got, want):
+            assert torch.equal(x[b:b + 1], y), (n, b)
+    eps = 2 * U * np.sqrt((N + 32) * T)  # of two walks with independent roundings, as the parity tests derive it
+    for b in (4, 10):
+        *ref, mw, mb = delta_backward_ref(*(t[b:b + 1].double().numpy() for t in p), HK, S0[b:b + 1].double().numpy(),
+                                          dS[b:b + 1].double().numpy(), [lens[b]], magnitude=True)
+        for n, x, y, size in zip(names, got, ref, (None, None, None, mw, mb, None)):
+            half = 2.0 ** -8 if x.dtype == torch.bfloat16 else U
+            err = np.abs(x[b:b + 1].double().cpu().numpy() - y)
+            size = np.abs(y) if size is None else size
+            assert np.linalg.norm(err) <= (eps + half) * np.linalg.norm(size), (n, b)
+            assert (err - half * np.abs(y)).max() <= 8 * eps * size.max(), (n, b)
