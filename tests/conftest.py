@@ -13,6 +13,14 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long CPU test")
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    """What a test draws from torch's own generator is the same whatever ran before it."""
+    import torch
+
+    torch.manual_seed(0)
+
+
 @pytest.fixture(scope="session")
 def ctwin():
     from oracle.ctwin import LIB, build_ctwin, load_ctwin
