@@ -540,7 +540,7 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  * from H N = 2^22, and from B H = 2^22 (for up to 16 tokens without a ckpt from
  * B H = 2^25, and 2^25 - 1 with N = 128).
  * A non-finite input may reach every output of its head from the 64 tokens it is
- * among on.
+ * among on, none behind its row's length.
  */
 wkv_status_t wkv_delta_forward(int64_t B, int64_t T, int64_t H, int64_t HK, int64_t N, int in_dtype,
                                const int32_t* lengths, const float* w, const float* beta,

@@ -429,16 +429,21 @@ struct BlockRows {
         for (int i = 0; i < kVecs; ++i)
             *reinterpret_cast<u32x4*>(dst + place<T, N>(lane / kRowVecs + i * kRows, lane % kRowVecs * kPer)) = x[i];
     }
-    static __device__ __forceinline__ void flush(const T* src, T* base, int stride, int left, int lane) {
+    // rows below `live`, and zeros from there to `left`
+    static __device__ __forceinline__ void flush(const T* src, T* base, int stride, int live, int left, int lane) {
         const int row = lane / kRowVecs;
         const uint32_t at = static_cast<uint32_t>(row * stride + lane % kRowVecs * kPer);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             T* p = base + static_cast<int64_t>(i * kRows) * stride;
-            if (row + i * kRows < left)
+            if (row + i * kRows < live)
                 *reinterpret_cast<u32x4*>(p + at) =
                     *reinterpret_cast<const u32x4*>(src + place<T, N>(row + i * kRows, lane % kRowVecs * kPer));
         }
+        if (live >= left || live >= kSub) return;
+#pragma unroll 1
+        for (int t = live + row; t < left && t < kSub; t += kRows)
+            *reinterpret_cast<u32x4*>(base + static_cast<int64_t>(t) * stride + lane % kRowVecs * kPer) = u32x4{0, 0, 0, 0};
     }
 };
 
@@ -826,7 +831,9 @@ __global__ void __launch_bounds__((kWalkThreads<T, N>), (kWalkWaves<T, N>)) delt
         };
         const auto flush = [&](int64_t n) {
             const int64_t t0 = start_of(n) + kSub * s;
-            BlockRows<T, N>::flush(sm.v[n & 1] + kSub * s * kLen, y + t0 * vs, static_cast<int>(vs), rows_left(t0, P.T), lane);
+            // (behind the row's length zero keys met the state, which may not be finite)
+            BlockRows<T, N>::flush(sm.v[n & 1] + kSub * s * kLen, y + t0 * vs, static_cast<int>(vs), rows_left(t0, len),
+                                   rows_left(t0, P.T), lane);
         };
         if (count > 0) {
             fetch(0);
@@ -962,17 +969,18 @@ struct GradShared {
     float rowv[kWaves][kSub], colv[kWaves][kSub];
 };
 
-// The gradients of a tile behind its row's length: zeros.
+// The gradients of a tile from its row `from` on, which lies behind the row's length: zeros.  (What the products
+// would give there is 0 times the states, which need not be finite.)
 template <typename T, int N>
-__device__ void zero_tile(const DeltaBwdArgs& P, T* dr, T* dk, int64_t b, int64_t hk, int64_t t0) {
+__device__ void zero_tile(const DeltaBwdArgs& P, T* dr, T* dk, int64_t b, int64_t hk, int64_t t0, int from) {
     const int64_t rows = P.T - t0 < kTile ? P.T - t0 : kTile, per = P.H / P.HK, ks = P.HK * N;
-    for (int64_t t = threadIdx.x / 16; t < rows; t += blockDim.x / 16) {
+    for (int64_t t = from + threadIdx.x / 16; t < rows; t += blockDim.x / 16) {
         for (int c = threadIdx.x % 16 * 4; c < N; c += 64) {
             store4(&dr[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
             store4(&dk[(t0 + t) * ks + c], f4{0.f, 0.f, 0.f, 0.f});
         }
     }
-    for (int64_t i = threadIdx.x; i < rows * per; i += blockDim.x) {
+    for (int64_t i = from * per + threadIdx.x; i < rows * per; i += blockDim.x) {
         const int64_t at = (b * P.T + t0 + i / per) * P.H + hk * per + i % per;
         P.dw[at] = 0.f;
         P.dbeta[at] = 0.f;
@@ -997,10 +1005,9 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
     const int64_t ko = b * P.T * ks + hk * N;
     T* dr = static_cast<T*>(P.dr) + ko;
     T* dk = static_cast<T*>(P.dk) + ko;
-    if (t0 >= len) {  // nothing of this row here
-        zero_tile<T, N>(P, dr, dk, b, hk, t0);
-        return;
-    }
+    const int left = rows_left(t0, len);
+    if (left < kTile) zero_tile<T, N>(P, dr, dk, b, hk, t0, left);
+    if (left == 0) return;  // nothing of this row here
     {
         Staged<T, N> s;
         s.fetch(static_cast<const T*>(P.k) + ko, ks, t0, len);
@@ -1241,7 +1248,7 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             for (int j = 0; j < kSub; ++j) c += j < l16 && i >= l16 ? sm.diag[x][i][j] : 0.f;
         }
         c = sum_rows(c);
-        if (g == 0 && t0 + mine < P.T) {
+        if (g == 0 && t0 + mine < len) {
             c = fmaf(all, inner, c);
             for (int I = x + 1; I < kWaves; ++I) {
                 c += sm.rows[I];
@@ -1249,11 +1256,11 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
             }
             for (int J = 0; J < x; ++J) c += sm.cols[J];
             const int64_t at = (b * P.T + t0 + mine) * P.H + h;
-            P.dw[at] = t0 + mine < len ? -c : 0.f;
+            P.dw[at] = -c;
             P.dbeta[at] = dbeta;
         }
     }
-    if (t0 + mine < P.T) {
+    if (t0 + mine < len) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             store4(&dr[(t0 + mine) * ks + 16 * c + 4 * g], drT[c]);
@@ -1410,7 +1417,7 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
             ++p.tile;
         }
     };
-    // from a place on, the workgroup's first that holds tokens; those that hold none get zeros
+    // from a place on, the workgroup's first that holds tokens; what lies behind the rows' lengths gets zeros
     const auto settle = [&](Place& p) {
         for (; p.tile < ntile; advance(p)) {
             p.b = p.pair / HK;
@@ -1418,9 +1425,13 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
             p.h = p.hk * per;
             const int64_t t0 = static_cast<int64_t>(p.tile) * kTile;
             p.left = rows_left(t0, row_length(P.lengths, p.b, P.T));
-            if (p.left > 0) return;
-            const int64_t ko = p.b * P.T * ks + p.hk * N;
-            zero_tile<uint16_t, N>(P, static_cast<uint16_t*>(P.dr) + ko, static_cast<uint16_t*>(P.dk) + ko, p.b, p.hk, t0);
+            if (p.left < kTile) {
+                const int64_t ko = p.b * P.T * ks + p.hk * N;
+                zero_tile<uint16_t, N>(P, static_cast<uint16_t*>(P.dr) + ko, static_cast<uint16_t*>(P.dk) + ko, p.b, p.hk, t0,
+                                       p.left);
+                if (p.left == 0) continue;
+            }
+            return;
         }
     };
     GradRows<N> fk, fr, fg;
@@ -1722,10 +1733,10 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
             colv += dpp<0x114>(colv);
             colv += dpp<0x118>(colv);
             const float dw = fmaf(total, sm.since[kTile - 1], whole) + rowv + colv + sm.diag[lane];
-            if (t0 + lane < P.T) {
+            if (t0 + lane < len) {
                 const int64_t to = (b * P.T + t0 + lane) * P.H + h;
                 P.dbeta[to] = sG + dbeta;
-                P.dw[to] = t0 + lane < len ? -dw : 0.f;
+                P.dw[to] = -dw;
             }
         }
         __syncthreads();
@@ -1755,7 +1766,7 @@ __global__ void __launch_bounds__(kGradThreads, 2 * kGradShare<N>) delta_grad16_
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 const int64_t t = t0 + kSub * (X0 + x) + l16;
-                if (t < P.T) {
+                if (t < len) {
                     store4(static_cast<uint16_t*>(P.dr) + ko + t * ks + c0 + 4 * g, drT[x]);
                     store4(static_cast<uint16_t*>(P.dk) + ko + t * ks + c0 + 4 * g, dkT[x]);
                 }

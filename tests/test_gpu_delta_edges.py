@@ -158,3 +158,31 @@ def test_gradient_workgroups_that_walk_many_tiles(B, T, HK, H, N):
             size = np.abs(y) if size is None else size
             assert np.linalg.norm(err) <= (eps + half) * np.linalg.norm(size), (n, b)
             assert (err - half * np.abs(y)).max() <= 8 * eps * size.max(), (n, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("T", [9, 150, 700])  # token by token, whole, split in time
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_rows_behind_a_length_are_zeros_whatever_the_state(dtype, N, T, bad):
+    """A state or a gradient that is not finite spoils its own row's tokens and nothing behind the row's length."""
+    O = ops()
+    B, H, HK = 3, 2, 1
+    g = torch.Generator().manual_seed(T + N)
+    rn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    lens = [T - 4, T // 2, 1]
+    p = [torch.rand(B, T, H, generator=g) * 0.1, torch.rand(B, T, H, generator=g), rn(B, T, HK * N).to(dtype),
+         (rn(B, T, HK * N) / (2 * N ** 0.5)).to(dtype), rn(B, T, H * N).to(dtype), rn(B, T, H * N).to(dtype)]
+    S, G = rn(B, H, N, N), rn(B, H, N, N)
+    S[:2, :, 3, 5] = bad
+    G[:2, :, 7, 1] = bad
+    d, ln = [t.to(DEV) for t in p], torch.tensor(lens, dtype=torch.int32, device=DEV)
+    kw = dict(lengths=ln, state_in=S.to(DEV))
+    ck = O.new_delta_ckpt(B, T, H, N, DEV)
+    outs = [O.delta_forward(*d[:5], **kw), O.delta_forward(*d[:5], ckpt=ck, **kw)]
+    for ckpt in (ck, None):
+        outs += O.delta_backward(*d, grad_state_out=G.to(DEV), ckpt=ckpt, **kw)[:5]
+    for i, x in enumerate(outs):
+        for b, n in enumerate(lens):
+            assert bool((x[b, n:] == 0).all()), (i, b)
+        assert bool(torch.isfinite(x[2]).all()) and not bool(torch.isfinite(x[0, :lens[0]]).all()), i
