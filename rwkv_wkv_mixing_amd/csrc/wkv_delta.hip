@@ -34,9 +34,6 @@
 namespace wkv {
 namespace {
 
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -51,9 +48,6 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-__device__ __forceinline__ float widen(float x) { return x; }
-
 // four consecutive elements as float32
 __device__ __forceinline__ f4 load4(const uint16_t* p) {
     const u16x4 x = *reinterpret_cast<const u16x4*>(p);
@@ -61,10 +55,6 @@ __device__ __forceinline__ f4 load4(const uint16_t* p) {
 }
 __device__ __forceinline__ f4 load4(const float* p) { return *reinterpret_cast<const f4*>(p); }
 
-__device__ __forceinline__ uint32_t pk2(float a, float b) {
-    const f2 p = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
-}
 __device__ __forceinline__ uint16_t narrow(float x) { return static_cast<uint16_t>(pk2(x, x) & 0xffffu); }
 
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = narrow(x); }

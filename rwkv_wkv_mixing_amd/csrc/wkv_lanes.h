@@ -1,10 +1,23 @@
-// Sums over the lanes of a wave without a trip through LDS.
+// What the delta-rule and norm kernels share: float32 and bf16 values, and sums over the lanes of a wave without a
+// trip through LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace wkv {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+// a and b rounded to bf16, a in the lower half
+__device__ __forceinline__ uint32_t pk2(float a, float b) {
+    const f2 p = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
+}
 
 template <int Ctrl>
 __device__ __forceinline__ float dpp(float x) {

@@ -29,17 +29,7 @@
 namespace wkv {
 namespace {
 
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ uint32_t pk2(float a, float b) {
-    const f2 p = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
-}
 
 // V consecutive elements as float32: 8 in 16-byte accesses, or 1.
 template <int V>
