@@ -538,7 +538,8 @@ wkv_status_t wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t N, int in_dt
  * r, k, v, o, s_in, s_out, ckpt are 16-byte aligned (WKV_EALIGN otherwise).
  * WKV_EINVAL also for another N or an H that HK does not divide; WKV_ESIZE
  * from H N = 2^22, and from B H = 2^22 (for up to 16 tokens without a ckpt from
- * B H = 2^25, and 2^25 - 1 with N = 128).
+ * B H = 2^25, and 2^25 - 1 with N = 128); with a ckpt, and in the backward, also
+ * from B HK ceil(T / 64) = 2^24.
  * A non-finite input may reach every output of its head from the 64 tokens it is
  * among on, none behind its row's length.
  */
@@ -608,6 +609,7 @@ enum { WKV_ACT_NONE = 0, WKV_ACT_SIGMOID = 1, WKV_ACT_SILU = 2 };
  *
  * rows, H, G  rows (>= 0), heads (>= 0), channels a head (1 .. 1024); H G below
  *           2^24 and rows H below 2^31 (WKV_ESIZE otherwise).
+ * eps       0 .. 1e30 (WKV_EINVAL otherwise); with 0 a row of zeros gives NaN.
  * y_dtype   dtype of y and dy; dtype: of gate, gout, out and dgate.  WKV_BF16 y
  *           needs WKV_BF16 for both (WKV_EDTYPE otherwise).
  * y, gate, out, gout, dy, dgate  [rows, H G]; out must not alias an input.

@@ -48,3 +48,11 @@ def test_gradients_of_key_heads_without_value_heads(lib):  # noqa: F811
         assert delta_bwd(lib, H=0, HK=2, **{name: X + 8}) == L.WKV_EALIGN, name
     assert delta_bwd(lib, H=0, HK=0, dr=None, dk=None) == L.WKV_OK
     assert delta_bwd(lib, H=0, HK=2, T=0, dr=None, dk=None) == L.WKV_OK
+
+
+def test_most_tiles_of_a_walk(lib):  # noqa: F811
+    """With a ckpt, and backward: fewer than 2^24 (64 tokens, row, key head) places; without one, more."""
+    most = ((1 << 24) - 1) * 64
+    assert delta_fwd(lib, T=most, H=1, HK=1, ck=X, o=None) == delta_bwd(lib, T=most, H=1, HK=1, dr=None) == L.WKV_EINVAL
+    assert delta_fwd(lib, T=most + 1, H=1, HK=1, ck=X, o=None) == delta_bwd(lib, T=most + 1, H=1, HK=1, dr=None) == L.WKV_ESIZE
+    assert delta_fwd(lib, T=most + 1, H=1, HK=1, o=None) == L.WKV_EINVAL
