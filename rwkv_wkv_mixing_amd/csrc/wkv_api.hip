@@ -878,7 +878,7 @@ constexpr int64_t kMaxBlockNorm = 8192;  // channels a workgroup holds
 wkv_status_t head_norm_check(int64_t rows, int64_t H, int64_t G, int64_t* n) {
     if (rows < 0 || H < 0 || G < 1 || G > kMaxHeadNorm) return WKV_EINVAL;
     if (!mul3(rows, H, G, n) || *n > (int64_t{1} << 58)) return WKV_ESIZE;
-    if (H >= (int64_t{1} << 24) / G || rows * H >= (int64_t{1} << 31)) return WKV_ESIZE;
+    if (H > ((int64_t{1} << 24) - 1) / G || rows * H >= (int64_t{1} << 31)) return WKV_ESIZE;
     return WKV_OK;
 }
 

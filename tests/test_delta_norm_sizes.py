@@ -5,7 +5,7 @@ import pytest
 from rwkv_wkv_mixing_amd import _lib as L
 from rwkv_wkv_mixing_amd import ops as O
 
-from test_delta_norm_abi import X, delta_bwd, delta_fwd, lib  # noqa: F401  (lib is a fixture)
+from test_delta_norm_abi import X, delta_bwd, delta_fwd, head, lib  # noqa: F401  (lib is a fixture)
 
 STATE, ROW = 64 * 64 * 4, 64 * 4
 
@@ -56,3 +56,12 @@ def test_most_tiles_of_a_walk(lib):  # noqa: F811
     assert delta_fwd(lib, T=most, H=1, HK=1, ck=X, o=None) == delta_bwd(lib, T=most, H=1, HK=1, dr=None) == L.WKV_EINVAL
     assert delta_fwd(lib, T=most + 1, H=1, HK=1, ck=X, o=None) == delta_bwd(lib, T=most + 1, H=1, HK=1, dr=None) == L.WKV_ESIZE
     assert delta_fwd(lib, T=most + 1, H=1, HK=1, o=None) == L.WKV_EINVAL
+
+
+@pytest.mark.parametrize("G", [1, 3, 5, 64, 1000, 1024])
+def test_most_channels_of_a_head_norm(lib, G):  # noqa: F811
+    """H G below 2^24: the largest H that the header allows passes, the next does not."""
+    most = ((1 << 24) - 1) // G
+    for bwd in (False, True):
+        assert head(lib, bwd, rows=1, H=most, G=G, y=None) == L.WKV_EINVAL  # the sizes pass
+        assert head(lib, bwd, rows=1, H=most + 1, G=G, y=None) == L.WKV_ESIZE
