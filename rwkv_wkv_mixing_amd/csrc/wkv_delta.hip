@@ -1273,8 +1273,8 @@ __global__ void __launch_bounds__(64 * kWaves, 1) delta_grad_kernel(DeltaBwdArgs
 // dependent products are taken in turn.  At N = 64 two workgroups share a compute unit (128 registers, some
 // spilled), each one's loads behind the other's work; one with twice the registers that fetched its next tile
 // ahead took as long (8 x 1024 tokens of 64 heads, forward and backward, 601 us against 607).  The 870 MB of
-// that case take 343 us (2.5 TB/s): the phases' products and LDS traffic, which meet at four barriers a
-// tile.
+// that case take 325 to 347 us (2.5 to 2.7 TB/s): the phases' products and LDS traffic, which meet at four barriers
+// a tile.
 constexpr int kGradWaves = 8;
 template <int N>
 constexpr int kGradShare = N == 64 ? 2 : 1;  // workgroups a compute unit

@@ -708,7 +708,8 @@ hipError_t launch_head(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
 
 template <typename TY, typename TG>
 hipError_t launch_head_v(const HeadNormArgs& a, bool bwd, hipStream_t stream) {
-    if (!a.vec) {  // as many elements a lane as the head needs (16 always: heads of 100 took ten times those of 128)
+    if (!a.vec) {  // as many elements a lane as the head needs (16 always: gradients of 64 heads of 100 took nine
+                   // times as long as those of as many elements in heads of 128, float32; now 1.2 times)
         if (a.G <= 128) return launch_head<TY, TG, 1, 2>(a, bwd, stream);
         if (a.G <= 256) return launch_head<TY, TG, 1, 4>(a, bwd, stream);
         return launch_head<TY, TG, 1, kScalarVecs>(a, bwd, stream);
@@ -758,7 +759,7 @@ hipError_t launch_block_bwd(const BlockNormArgs& a, hipStream_t stream) {
 // against 80; the backward 16 above 4096, for which 1024 threads have not the registers: 4096 rows of 8192 259 us
 // against 656).  Off the 16-byte grid, single elements: 512 threads in the forward up to 4096 (4096 rows of 1001
 // 24 us; 1024 threads 37), else 1024 (of 8191 140 us; 512 threads 214), and 1024 in the backward (of 4001 241 us;
-// 512 threads, which spill, 319).
+// 512 threads, which spill, 319).  All of these in bf16.
 template <typename TX, typename TY>
 hipError_t launch_block_v(BlockNormArgs a, bool bwd, hipStream_t stream) {
     a.slots = block_norm_slots(a.rows, a.C);
