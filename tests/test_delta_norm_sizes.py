@@ -27,7 +27,7 @@ def test_ckpt_of_no_call_is_refused(lib, B, T, H, N):  # noqa: F811
         O.new_delta_ckpt(B, T, H, N, "cpu")
 
 
-def test_ckpt_of_no_tokens():
+def test_ckpt_of_no_tokens(lib):  # noqa: F811
     for B, T, H in ((0, 64, 2), (2, 0, 2), (2, 64, 0)):
         assert O.delta_ckpt_bytes(B, T, H, 64) == 0 and O.new_delta_ckpt(B, T, H, 64, "cpu").numel() == 1
 

@@ -186,3 +186,37 @@ def test_rows_behind_a_length_are_zeros_whatever_the_state(dtype, N, T, bad):
         for b, n in enumerate(lens):
             assert bool((x[b, n:] == 0).all()), (i, b)
         assert bool(torch.isfinite(x[2]).all()) and not bool(torch.isfinite(x[0, :lens[0]]).all()), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [64, 128])
+def test_rates_that_clear_the_state_of_a_split_sequence(dtype, N):
+    """Infinite and large rates at the borders of tiles and segments, and a stretch of rates of 0, in a sequence that
+    is split in time.  Bounds as the parity tests derive them: u sqrt((N + 32) T), twice that for gradients."""
+    import numpy as np
+    from oracle import delta_backward_ref, delta_forward_ref
+
+    O, T, H = ops(), 900, 2
+    g = torch.Generator().manual_seed(N)
+    rn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    k = rn(1, T, H, N)
+    k = (k / k.norm(dim=-1, keepdim=True)).reshape(1, T, H * N)
+    w = torch.rand(1, T, H, generator=g) * 0.1
+    w[:, [0, 63, 64, 127, 128, 191, 192, 255, 256, 511, 512, 640, 899]] = float("inf")
+    w[:, [100, 320, 448, 700]] = 60.0
+    w[:, 400:440] = 0.0
+    p = [w, torch.rand(1, T, H, generator=g), (rn(1, T, H * N) / N ** 0.5).to(dtype), k.to(dtype), rn(1, T, H * N).to(dtype),
+         rn(1, T, H * N).to(dtype)]
+    S, G = rn(1, H, N, N), rn(1, H, N, N)
+    assert O.L.lib().wkv_delta_forward_workspace_bytes(1, T, H, H, N) > 0
+    host, d = [t.double().numpy() for t in p], [t.to(DEV) for t in p]
+    ref = list(delta_forward_ref(*host[:5], H, S.double().numpy()))
+    *grads, mw, mb = delta_backward_ref(*host, H, S.double().numpy(), G.double().numpy(), magnitude=True)
+    got = [*O.delta_forward(*d[:5], state_in=S.to(DEV), return_state=True),
+           *O.delta_backward(*d, state_in=S.to(DEV), grad_state_out=G.to(DEV), need_state_grad=True)]
+    eps = U * np.sqrt((N + 32) * T)
+    for i, (x, y) in enumerate(zip(got, ref + grads)):
+        half, c = 2.0 ** -8 if x.dtype == torch.bfloat16 else U, eps if i < 2 else 2 * eps
+        err, size = np.abs(x.double().cpu().numpy() - y), np.abs(y) if i not in (5, 6) else (mw, mb)[i - 5]
+        assert np.linalg.norm(err) <= (c + half) * np.linalg.norm(size), i
+        assert (err - half * np.abs(y)).max() <= 8 * c * size.max(), i
