@@ -2,8 +2,9 @@
  * wkv.h - C ABI of the RWKV-4 WKV time-mixing operator for AMD MI355X (gfx950),
  * with the receptance gate and the token-shift mix around it, and the
  * matrix-state WKV of RWKV-5 and RWKV-6 (per-token decay), forward and
- * backward, the gated delta rule on the same kind of state, and the norms
- * around the mixing.
+ * backward, the gated delta rule on the same kind of state, the norms
+ * around the mixing, the selective scan with its short causal convolution, and
+ * the norm and clipping of gradients.
  *
  * The operator, per channel c of each batch row b, tokens t = 1..T
  * ("RWKV（Receptance Weighted Key Value）概念", section 3.2; and
@@ -719,6 +720,159 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
                                       const float* mu, const void* x, const void* x_prev,
                                       const void* gout, float* dx, float* dmu, float* dx_prev,
                                       void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * wkv_conv_forward / wkv_conv_backward - a short causal convolution over time,
+ * a filter of K taps for every channel, with its activation: before the
+ * selective scan, what the token shift is before the other mixes (this library's
+ * extension of it, "RWKV - 把 RNN 重新带回 Transformer 时代的线性大模型", section
+ * "关键设计 1").
+ *
+ * Defines, per batch row of n tokens, with X the K - 1 carried inputs followed by
+ * the row's tokens (X[K - 1 + t] is token t = 0 .. n - 1):
+ *     out_t = act(bias + sum_{j < K} weight[j] X[t + j])
+ * and s_out = X[n .. n + K - 2], the s_in of the next segment or decoding step.
+ * Float32 arithmetic; outputs rounded once.
+ *
+ * B, T, C   batch rows, tokens, channels (>= 0).  K  taps, 2 .. 4 (WKV_EINVAL
+ *           otherwise).  act  WKV_ACT_*.
+ * in_dtype  dtype of x, s_in, s_out, out and, backward, of gout, ds_out, dx, ds_in.
+ * lengths   [B] int32 or NULL: tokens of each row (clamped to 0 .. T).  Rows
+ *           behind it are not read; those of out and dx are zeros.
+ * x, out    [B, T, C]; out must not overlap an input.
+ * weight    [K, C] float32, the last tap on the token itself; bias [C] or NULL.
+ * s_in      [B, K - 1, C] or NULL (zeros).  s_out  alike, or NULL; may be s_in.
+ *           With T == 0 it receives s_in (or zeros).
+ *
+ * Backward, of sum <gout, out> + <ds_out, s_out>: dx, dweight, dbias (needed with
+ * bias), ds_in (or NULL; may be ds_out).  dweight and dbias are sums over rows and
+ * tokens in a fixed order; all outputs are overwritten.
+ * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
+ *           clobbered.  Not needed without tokens.
+ * WKV_ESIZE from T = 2^31, B = 2^31 or C = 2^26.
+ */
+size_t wkv_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K);
+wkv_status_t wkv_conv_forward(int64_t B, int64_t T, int64_t C, int64_t K, int in_dtype, int act, const int32_t* lengths,
+                              const void* x, const float* weight, const float* bias, const void* s_in, void* out,
+                              void* s_out, void* hip_stream);
+wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int in_dtype, int act, const int32_t* lengths,
+                               const void* x, const float* weight, const float* bias, const void* s_in,
+                               const void* gout, const void* ds_out, void* dx, float* dweight, float* dbias, void* ds_in,
+                               void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Flag of the selective scan: delta = log(1 + e^{dt + dt_bias}); without it, dt + dt_bias. */
+#define WKV_SELECT_SOFTPLUS 1
+
+/*
+ * wkv_select_forward - the selective state space scan: a diagonal state of N
+ * numbers a channel whose decay and writes the tokens choose.
+ *
+ * Defines, per batch row and channel, with b and c of the channel's group:
+ *     h_t[n] = e^{-delta_t w[n]} h_{t-1}[n] + delta_t x_t b_t[n]
+ *     y_t = sum_n c_t[n] h_t[n] + d x_t,   out_t = y_t z_t sigmoid(z_t)
+ * delta as WKV_SELECT_SOFTPLUS says.  The state keeps a decay rate for every
+ * channel and number as wkv_forward does for every channel ("RWKV（Receptance
+ * Weighted Key Value）概念", section 3.2), without its normaliser; steps, writes
+ * and reads that the tokens choose are this library's extension.
+ * States and sums are float32 whatever the inputs' dtype; outputs are rounded once.
+ *
+ * B, T, C   batch rows, tokens, channels (>= 0).  G  groups of channels that share
+ *           b and c: a divisor of C (1 with C = 0).  N  8, 16, 32 or 64.
+ * in_dtype  dtype of x, dt, b, c, z and out.
+ * lengths   [B] int32 or NULL: tokens of each row (clamped to 0 .. T).  Tokens
+ *           behind it are not read, leave the state as it is, and their rows of
+ *           out are zeros.
+ * x, dt     [B, T, C].  w  [C, N] float32 rates, >= 0; +inf keeps nothing.
+ * b, c      [B, T, G N].  d  [C] float32 or NULL (0).  z  [B, T, C] or NULL (out = y).
+ * dt_bias   [C] float32 or NULL (0).
+ * out       [B, T, C], fully overwritten; must not overlap an input.
+ * s_in      [B, C, N] float32 state before token 1, or NULL (zero).
+ * s_out     [B, C, N] float32 state after each row's last token, or NULL; may be
+ *           s_in.  With T == 0 it receives s_in (or zeros).
+ * ckpt      NULL, or wkv_select_ckpt_bytes() bytes for wkv_select_backward on the
+ *           same inputs: the state before every 16 tokens (opaque).
+ * workspace NULL (no time split), or wkv_select_forward_workspace_bytes() bytes,
+ *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
+ * w, b, c, s_in, s_out, ckpt are 16-byte aligned, the other tensors to their
+ * elements (WKV_EALIGN otherwise).
+ * WKV_ESIZE from T = 2^31, B = 2^31, C N = 2^30, B G ceil(C / G / 64) = 2^22, and
+ * for up to 8 tokens without a ckpt from B C N = 2^33; in the backward also from
+ * B T G N = 2^30.
+ */
+wkv_status_t wkv_select_forward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int in_dtype, int flags,
+                                const int32_t* lengths, const void* x, const void* dt, const float* w, const void* b,
+                                const void* c, const float* d, const void* z, const float* dt_bias, void* out,
+                                const float* s_in, float* s_out, void* ckpt, void* workspace, size_t workspace_bytes,
+                                void* hip_stream);
+
+/* Bytes of wkv_select_forward's ckpt, of its optional scratch (0 when no time split would be made), and of
+ * wkv_select_backward's scratch (ws_flags: WKV_WS_HAVE_CKPT when a ckpt will be passed, else room to recompute it is
+ * included; WKV_WS_NO_SPLIT for an unsplit call).  0 for sizes of no call. */
+size_t wkv_select_ckpt_bytes(int64_t B, int64_t T, int64_t C, int64_t N);
+size_t wkv_select_forward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N);
+size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int ws_flags);
+
+/*
+ * wkv_select_backward - gradients of wkv_select_forward for the loss
+ * L = sum <go_t, out_t> + <ds_out, h_T>.  With gy_t = go_t z_t sigmoid(z_t), a_t =
+ * e^{-delta_t w}, and g_t the gradient of h_t (g_T = ds_out + c_T gy_T):
+ *     g_t = c_t gy_t + a_{t+1} g_{t+1},   q_t = a_t g_t h_{t-1},   du_t = sum_n g_t b_t
+ *     dx_t = delta_t du_t + d gy_t,   ddelta_t = x_t du_t - sum_n w q_t,
+ *     ddt_t = ddelta_t sigmoid(dt_t + dt_bias)  (ddelta_t without softplus),
+ *     dz_t = go_t y_t (the gate's derivative),   dw = -sum_t delta_t q_t,
+ *     db_t = sum over the group's channels of delta_t x_t g_t,   dc_t = that of gy_t h_t,
+ *     dd = sum gy_t x_t,   ddt_bias = sum ddt_t,   ds_in = a_1 g_1.
+ * Sums are float32 in a fixed order (bitwise reproducible).
+ *
+ * go        [B, T, C] in_dtype.  Rows behind a row's length are not read.
+ * dx, ddt, dz [B, T, C], db, dc [B, T, G N] in_dtype, zeros behind a row's length; dw
+ *           [C, N], dd, ddt_bias [C] float32: fully overwritten.  dz is needed with z,
+ *           dd with d, ddt_bias with dt_bias, and they are not written without.
+ * ds_out, ds_in  [B, C, N] float32 or NULL; ds_in may be ds_out.  With T == 0 ds_in
+ *           receives ds_out (or zeros).
+ * ckpt      what wkv_select_forward wrote for these inputs, lengths and s_in, or
+ *           NULL (recomputed, from s_in).
+ * workspace wkv_select_backward_workspace_bytes(..., ws_flags) bytes, 256-byte
+ *           aligned; clobbered.  With room for it the call may split in time.
+ * Other arguments and errors as wkv_select_forward; ds_out and ds_in are 16-byte
+ * aligned too.
+ */
+wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int in_dtype, int flags,
+                                 const int32_t* lengths, const void* x, const void* dt, const float* w, const void* b,
+                                 const void* c, const float* d, const void* z, const float* dt_bias, const void* go,
+                                 const float* s_in, const float* ds_out, void* dx, void* ddt, float* dw, void* db,
+                                 void* dc, float* dd, void* dz, float* ddt_bias, float* ds_in, const void* ckpt,
+                                 void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/*
+ * wkv_grad_norm / wkv_clip_gradients - between the backward calls and the
+ * optimizer: the norm of all gradients together, and the gradients scaled so that
+ * it is at most max_norm.
+ *
+ * Defines, over `count` tensors of any sizes:
+ *     norm = sqrt(sum of all squares),   out = grad * min(1, max_norm / (norm + eps))
+ * Squares are added up in float64 in a fixed order, so nothing over- or underflows
+ * that float32 holds; each element is rounded once.  With a norm that is
+ * infinite or not a number the factor is 0 or not a number, and so are the outputs.
+ *
+ * grads, outs, sizes, dtypes  HOST arrays of `count` device addresses, element
+ *           counts (>= 0) and dtypes (WKV_F32 or WKV_BF16, of a tensor's gradient
+ *           and its output).  They are read before the call returns.
+ * outs      NULL: the gradients are overwritten.  An output may be its own gradient;
+ *           outputs may not overlap each other, norm or another gradient (WKV_EINVAL),
+ *           so in place no gradient may be listed twice.
+ * max_norm  0 .. 1e30, eps 0 .. 1e30 (WKV_EINVAL otherwise).  0 / 0 counts as 1.
+ * norm      [1] float32 on the device: the norm before the clipping; wkv_clip_gradients
+ *           takes NULL too.
+ * workspace wkv_clip_workspace_bytes(count) bytes, 256-byte aligned; clobbered.  Not
+ *           needed without elements.
+ */
+size_t wkv_clip_workspace_bytes(int64_t count);
+wkv_status_t wkv_grad_norm(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, float* norm,
+                           void* workspace, size_t workspace_bytes, void* hip_stream);
+wkv_status_t wkv_clip_gradients(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes,
+                                const int* dtypes, float max_norm, float eps, float* norm, void* workspace,
+                                size_t workspace_bytes, void* hip_stream);
 
 /*
  * wkv_step - one recurrent-mode (decode) token for L x B independent states.

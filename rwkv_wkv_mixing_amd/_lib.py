@@ -17,6 +17,7 @@ WKV_F32, WKV_BF16 = 0, 1
 WKV_OP_FORWARD, WKV_OP_BACKWARD = 0, 1
 WKV_CKPT_LEN = 16
 WKV_NORM_CENTER, WKV_NORM_SHARED = 1, 2
+WKV_SELECT_SOFTPLUS = 1
 WKV_ACT_NONE, WKV_ACT_SIGMOID, WKV_ACT_SILU = 0, 1, 2
 
 # every symbol include/wkv.h declares
@@ -55,6 +56,17 @@ EXPORTS = (
     "wkv_token_shift_workspace_bytes",
     "wkv_token_shift",
     "wkv_token_shift_backward",
+    "wkv_conv_backward_workspace_bytes",
+    "wkv_conv_forward",
+    "wkv_conv_backward",
+    "wkv_select_forward",
+    "wkv_select_ckpt_bytes",
+    "wkv_select_forward_workspace_bytes",
+    "wkv_select_backward_workspace_bytes",
+    "wkv_select_backward",
+    "wkv_clip_workspace_bytes",
+    "wkv_grad_norm",
+    "wkv_clip_gradients",
     "wkv_workspace_status",
     "wkv_debug_spin_limit",
     "wkv_status_str",
@@ -163,6 +175,28 @@ def declare(L):
     L.wkv_token_shift.argtypes = [i64, i64, i64, i64, i32, fp, vp, vp, vp, vp]
     L.wkv_token_shift_backward.restype = i32
     L.wkv_token_shift_backward.argtypes = [i64, i64, i64, i64, i32, fp, vp, vp, vp, fp, fp, fp, vp, sz, vp]
+    L.wkv_conv_backward_workspace_bytes.restype = sz
+    L.wkv_conv_backward_workspace_bytes.argtypes = [i64] * 4
+    L.wkv_conv_forward.restype = i32
+    L.wkv_conv_forward.argtypes = [i64] * 4 + [i32] * 2 + [vp] * 8
+    L.wkv_conv_backward.restype = i32
+    L.wkv_conv_backward.argtypes = [i64] * 4 + [i32] * 2 + [vp] * 12 + [sz, vp]
+    L.wkv_select_forward.restype = i32
+    L.wkv_select_forward.argtypes = [i64] * 5 + [i32] * 2 + [vp] * 14 + [sz, vp]
+    L.wkv_select_ckpt_bytes.restype = sz
+    L.wkv_select_ckpt_bytes.argtypes = [i64] * 4
+    L.wkv_select_forward_workspace_bytes.restype = sz
+    L.wkv_select_forward_workspace_bytes.argtypes = [i64] * 5
+    L.wkv_select_backward_workspace_bytes.restype = sz
+    L.wkv_select_backward_workspace_bytes.argtypes = [i64] * 5 + [i32]
+    L.wkv_select_backward.restype = i32
+    L.wkv_select_backward.argtypes = [i64] * 5 + [i32] * 2 + [vp] * 23 + [sz, vp]
+    L.wkv_clip_workspace_bytes.restype = sz
+    L.wkv_clip_workspace_bytes.argtypes = [i64]
+    L.wkv_grad_norm.restype = i32
+    L.wkv_grad_norm.argtypes = [i64] + [vp] * 5 + [sz, vp]
+    L.wkv_clip_gradients.restype = i32
+    L.wkv_clip_gradients.argtypes = [i64] + [vp] * 4 + [f32] * 2 + [vp] * 2 + [sz, vp]
     L.wkv_workspace_status.restype = i32
     L.wkv_workspace_status.argtypes = [vp, sz, i32, vp]
     L.wkv_debug_spin_limit.restype = ctypes.c_uint32

@@ -4,8 +4,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 
 #include "wkv.h"
 #include "wkv_launch.h"
@@ -1027,6 +1029,392 @@ wkv_status_t wkv_block_norm_backward(int64_t rows, int64_t C, int x_dtype, int d
     a.ws = static_cast<float*>(workspace);
     a.vec = C % 8 == 0 && all_aligned(16, x_out, y, gate, post_w, post_b, scale, pre_w, pre_b, gx, gh, dx, dy, dgate);
     return hip_status(wkv::launch_block_norm_bwd(a, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+struct ConvPlan {
+    wkv_status_t st;
+    int64_t n, ns;    // elements, and of the carried inputs
+    size_t ws_bytes;  // of the backward
+};
+
+ConvPlan conv_plan(int64_t B, int64_t T, int64_t C, int64_t K, int dt, int act) {
+    const auto bad = [](wkv_status_t st) { return ConvPlan{st, 0, 0, 0}; };
+    if (B < 0 || T < 0 || C < 0 || K < 2 || K > 4 || !act_ok(act)) return bad(WKV_EINVAL);
+    if (!dtype_ok(dt)) return bad(WKV_EDTYPE);
+    constexpr int64_t kMost = int64_t{1} << 31;
+    ConvPlan p{WKV_OK, 0, 0, 0};
+    if (B >= kMost || T >= kMost || C >= (int64_t{1} << 26)) return bad(WKV_ESIZE);
+    if (!mul3(B, T, C, &p.n) || p.n > (int64_t{1} << 58) || !mul3(B, K - 1, C, &p.ns)) return bad(WKV_ESIZE);
+    // grids of two dimensions of 2^20 and 2^16 workgroups at most, one for 16 tokens of 64 channels
+    int64_t blocks;
+    if (!mul3(B, (T + 15) / 16, (C + 63) / 64, &blocks) || blocks >= (int64_t{1} << 35)) return bad(WKV_ESIZE);
+    if (p.n > 0) p.ws_bytes = static_cast<size_t>(wkv::conv_slots(B, T, C)) * static_cast<size_t>((K + 1) * C) * sizeof(float);
+    return p;
+}
+
+// vectors of four elements: four floats of the weights and their gradients, which lie on the 16-byte grid
+template <class... P>
+bool conv_vec(int64_t C, int dt, const float* weight, const float* bias, P... p) {
+    return C % 4 == 0 && all_aligned(16, weight, bias) && all_aligned(4 * in_size(dt), p...);
+}
+
+struct SelectPlan {
+    wkv_status_t st;
+    int64_t ns;            // numbers of state
+    int64_t tiles, ctiles, nseg, per;
+    size_t ckpt, part, dwp, vecp, split;  // bytes
+};
+
+SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dt, bool steps, bool bwd) {
+    const auto bad = [](wkv_status_t st) { return SelectPlan{st, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0}; };
+    if (B < 0 || T < 0 || C < 0 || G < 1 || (N != 8 && N != 16 && N != 32 && N != 64) || C % G != 0) return bad(WKV_EINVAL);
+    if (!dtype_ok(dt)) return bad(WKV_EDTYPE);
+    SelectPlan p{WKV_OK, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0};
+    constexpr int64_t kMost = int64_t{1} << 31, kBig = int64_t{1} << 58;
+    int64_t n, cn, gn, bct, ck;
+    if (B >= kMost || T >= kMost) return bad(WKV_ESIZE);
+    if (!mul3(C, N, 1, &cn) || cn >= (int64_t{1} << 30) || !mul3(G, N, 1, &gn) || gn >= (int64_t{1} << 30)) return bad(WKV_ESIZE);
+    if (!mul3(B, T, C, &n) || n > kBig || !mul3(B, cn, 1, &p.ns) || p.ns > kBig || !mul3(B, T, gn, &bct) || bct > kBig)
+        return bad(WKV_ESIZE);
+    if (C == 0) return p;
+    p.tiles = (T + wkv::kSelectTile - 1) / wkv::kSelectTile;
+    const int64_t ctiles = G * ((C / G + 63) / 64);
+    // grids of fewer than 2^32 threads: up to 512 a tile of channels; a lane for four states of a few tokens
+    if (steps ? p.ns / 4 >= kMost : B * ctiles >= (int64_t{1} << 22)) return bad(WKV_ESIZE);
+    if (bwd && bct >= (int64_t{1} << 30)) return bad(WKV_ESIZE);
+    p.ctiles = ctiles;
+    const auto bytes = [](int64_t k) { return (static_cast<size_t>(k) * sizeof(float) + 255) / 256 * 256; };
+    if (!mul3(p.ns, p.tiles, 1, &ck) || ck > kBig) return bad(WKV_ESIZE);
+    p.ckpt = static_cast<size_t>(ck) * sizeof(float);
+    p.nseg = steps ? 1 : wkv::select_segments(B, T, ctiles, &p.per);
+    if (steps) p.per = T;
+    if (p.nseg > 1) p.split = bytes(p.nseg * p.ns) + bytes(p.nseg * B * C);
+    if (bwd) {
+        int64_t part, rows;
+        if (!mul3(B, T, 2 * N, &rows) || !mul3(rows, ctiles, 1, &part) || part > kBig) return bad(WKV_ESIZE);
+        p.part = bytes(part);
+        p.dwp = bytes(p.nseg * p.ns);
+        p.vecp = bytes(p.nseg * B * C * 2);
+    }
+    return p;
+}
+
+// Where a time split keeps what its segments do.
+void select_split(wkv::SelectArgs* a, const SelectPlan& p, char* scratch) {
+    a->nseg = p.nseg;
+    a->seg_len = p.per;
+    a->local = reinterpret_cast<float*>(scratch);
+    a->steps = a->local + (p.nseg * p.ns + 63) / 64 * 64;
+}
+
+bool finite_in(float v, float most) { return v >= 0.f && v <= most; }
+
+// A range of addresses; which: the tensor, out: written.
+struct Span {
+    uintptr_t first, last;
+    int64_t which;
+    bool out;
+};
+
+// The tensors' sizes and dtypes, and the tables of the launches (with == NULL: the gradients in place).
+wkv_status_t clip_check(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, int64_t* total) {
+    if (count < 0) return WKV_EINVAL;
+    if (count >= (int64_t{1} << 24)) return WKV_ESIZE;
+    *total = 0;
+    if (count > 0 && (!grads || !sizes || !dtypes)) return WKV_EINVAL;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!dtype_ok(dtypes[i])) return WKV_EDTYPE;
+        if (sizes[i] < 0) return WKV_EINVAL;
+        if (sizes[i] > (int64_t{1} << 50)) return WKV_ESIZE;
+        if (sizes[i] == 0) continue;
+        if (!grads[i]) return WKV_EINVAL;
+        if (!aligned(grads[i], in_size(dtypes[i]))) return WKV_EALIGN;
+        if (__builtin_add_overflow(*total, sizes[i], total)) return WKV_ESIZE;
+    }
+    return WKV_OK;
+}
+
+// Outputs that overlap one another, `norm` or a gradient that is not their own.
+wkv_status_t clip_overlaps(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes,
+                           const float* norm) {
+    Span* s = new (std::nothrow) Span[2 * count + 1];
+    if (s == nullptr) return WKV_EINVAL;
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * in_size(dtypes[i]);
+        const uintptr_t in = reinterpret_cast<uintptr_t>(grads[i]), out = reinterpret_cast<uintptr_t>(outs[i]);
+        s[n++] = Span{out, out + bytes, i, true};
+        if (in != out) s[n++] = Span{in, in + bytes, i, false};
+    }
+    if (norm != nullptr) s[n++] = Span{reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + sizeof(float), count, true};
+    std::sort(s, s + n, [](const Span& a, const Span& b) { return a.first < b.first; });
+    // in order of their starts: each against the farthest end so far, of an output and of anything
+    bool clash = false;
+    uintptr_t end_out = 0, end_any = 0;
+    for (int64_t i = 0; i < n && !clash; ++i) {
+        clash = s[i].out ? s[i].first < end_any : s[i].first < end_out;
+        if (s[i].out && s[i].last > end_out) end_out = s[i].last;
+        if (s[i].last > end_any) end_any = s[i].last;
+    }
+    delete[] s;
+    return clash ? WKV_EINVAL : WKV_OK;
+}
+
+// The next table: tensors from *at on.
+void clip_table(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, int64_t* at,
+                wkv::ClipTable* t) {
+    t->count = 0;
+    t->chunks = 0;
+    for (; *at < count && t->count < wkv::kClipTensors; ++*at) {
+        if (sizes[*at] == 0) continue;
+        const int k = t->count++;
+        t->in[k] = grads[*at];
+        t->out[k] = outs != nullptr ? outs[*at] : const_cast<void*>(grads[*at]);
+        t->n[k] = sizes[*at];
+        t->chunk0[k] = t->chunks;
+        t->bf16[k] = dtypes[*at] == WKV_BF16 ? 1 : 0;
+        t->chunks += (sizes[*at] + wkv::kClipChunk - 1) / wkv::kClipChunk;
+    }
+}
+
+// Partial sums that every workgroup adds up for itself; more are first added to one by a launch of their own.
+constexpr int64_t kClipParts = 4 * wkv::kClipBlocks;
+
+// The squares' sums: in part[0 .. *nparts - 1].
+hipError_t clip_sums(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, double* part, int64_t* nparts,
+                     hipStream_t stream) {
+    *nparts = 0;
+    for (int64_t at = 0; at < count;) {
+        wkv::ClipTable t;
+        clip_table(count, grads, nullptr, sizes, dtypes, &at, &t);
+        if (t.count == 0) continue;
+        const hipError_t e = wkv::launch_clip_sums(t, part + *nparts, stream);
+        if (e != hipSuccess) return e;
+        *nparts += wkv::clip_blocks(t);
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t wkv_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K) {
+    const ConvPlan p = conv_plan(B, T, C, K, WKV_F32, WKV_ACT_NONE);
+    return p.st == WKV_OK ? p.ws_bytes : 0;
+}
+
+wkv_status_t wkv_conv_forward(int64_t B, int64_t T, int64_t C, int64_t K, int in_dtype, int act, const int32_t* lengths,
+                              const void* x, const float* weight, const float* bias, const void* s_in, void* out,
+                              void* s_out, void* hip_stream) {
+    const ConvPlan p = conv_plan(B, T, C, K, in_dtype, act);
+    if (p.st != WKV_OK) return p.st;
+    const size_t es = in_size(in_dtype);
+    if (!all_aligned(es, x, s_in, out, s_out) || !all_aligned(4, weight, bias, lengths)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p.n == 0) return hip_status(wkv::launch_conv_copy(s_in, s_out, p.ns, in_dtype == WKV_BF16, stream));
+    if (!x || !weight || !out) return WKV_EINVAL;
+    wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
+    a.out = out;
+    a.s_out = s_out;
+    a.vec = conv_vec(C, in_dtype, weight, bias, x, s_in, out, s_out);
+    return hip_status(wkv::launch_conv_fwd(a, stream));
+}
+
+wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int in_dtype, int act, const int32_t* lengths,
+                               const void* x, const float* weight, const float* bias, const void* s_in,
+                               const void* gout, const void* ds_out, void* dx, float* dweight, float* dbias, void* ds_in,
+                               void* workspace, size_t workspace_bytes, void* hip_stream) {
+    const ConvPlan p = conv_plan(B, T, C, K, in_dtype, act);
+    if (p.st != WKV_OK) return p.st;
+    if (C == 0) return WKV_OK;
+    if (!dweight || (bias && !dbias)) return WKV_EINVAL;
+    const size_t es = in_size(in_dtype);
+    if (!all_aligned(es, x, s_in, gout, ds_out, dx, ds_in) || !all_aligned(4, weight, bias, dweight, dbias, lengths)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p.n == 0) {  // empty sums; the carried inputs' gradient passes back
+        hipError_t e = wkv::launch_zero(dweight, K * C, stream);
+        if (e == hipSuccess && bias) e = wkv::launch_zero(dbias, C, stream);
+        if (e == hipSuccess) e = wkv::launch_conv_copy(ds_out, ds_in, p.ns, in_dtype == WKV_BF16, stream);
+        return hip_status(e);
+    }
+    if (!x || !weight || !gout || !dx) return WKV_EINVAL;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.ws_bytes) return WKV_EWORKSPACE;
+    wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
+    a.gout = gout;
+    a.ds_out = ds_out;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = bias ? dbias : nullptr;
+    a.ds_in = ds_in;
+    a.part = static_cast<float*>(workspace);
+    a.slots = wkv::conv_slots(B, T, C);
+    a.vec = conv_vec(C, in_dtype, weight, bias, x, s_in, gout, ds_out, dx, ds_in);
+    return hip_status(wkv::launch_conv_bwd(a, stream));
+}
+
+size_t wkv_select_ckpt_bytes(int64_t B, int64_t T, int64_t C, int64_t N) {
+    const SelectPlan p = select_plan(B, T, C, 1, N, WKV_F32, false, false);
+    return p.st == WKV_OK ? p.ckpt : 0;
+}
+
+size_t wkv_select_forward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N) {
+    const SelectPlan p = select_plan(B, T, C, G, N, WKV_F32, false, false);
+    return p.st == WKV_OK && p.ns > 0 ? p.split : 0;
+}
+
+size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int ws_flags) {
+    const SelectPlan p = select_plan(B, T, C, G, N, WKV_F32, false, true);
+    if (p.st != WKV_OK || p.ns == 0 || T == 0) return 0;
+    const size_t saved = (ws_flags & WKV_WS_HAVE_CKPT) != 0 ? 0 : (p.ckpt + 255) / 256 * 256;
+    return p.part + p.dwp + p.vecp + saved + ((ws_flags & WKV_WS_NO_SPLIT) != 0 ? 0 : p.split);
+}
+
+wkv_status_t wkv_select_forward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int in_dtype, int flags,
+                                const int32_t* lengths, const void* x, const void* dt, const float* w, const void* b,
+                                const void* c, const float* d, const void* z, const float* dt_bias, void* out,
+                                const float* s_in, float* s_out, void* ckpt, void* workspace, size_t workspace_bytes,
+                                void* hip_stream) {
+    const bool steps = T <= wkv::kSelectStepMaxT && ckpt == nullptr;
+    const SelectPlan p = select_plan(B, T, C, G, N, in_dtype, steps, false);
+    if (p.st != WKV_OK) return p.st;
+    if ((flags & ~WKV_SELECT_SOFTPLUS) != 0) return WKV_EINVAL;
+    if (!all_aligned(16, s_in, s_out)) return WKV_EALIGN;
+    if (p.ns == 0) return WKV_OK;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (T == 0) return hip_status(wkv::launch_wkv5_state_copy(s_in, s_out, p.ns, stream));
+    if (!x || !dt || !w || !b || !c || !out) return WKV_EINVAL;
+    if (!all_aligned(16, w, b, c, ckpt) || !all_aligned(4, d, dt_bias, lengths) || !all_aligned(in_size(in_dtype), x, dt, z, out))
+        return WKV_EALIGN;
+    if (workspace && (!aligned(workspace, 256) || workspace_bytes < p.split)) return WKV_EWORKSPACE;
+    wkv::SelectArgs a{B, T, C, G, N, in_dtype == WKV_BF16, (flags & WKV_SELECT_SOFTPLUS) != 0, lengths, x, dt, w, b, c, d, z, dt_bias, s_in};
+    a.tiles = p.tiles;
+    a.ctiles = static_cast<int>(p.ctiles);
+    a.out = out;
+    a.s_out = s_out;
+    a.ckpt = static_cast<float*>(ckpt);
+    a.seg_len = p.tiles * wkv::kSelectTile;
+    if (steps) return hip_status(wkv::launch_select_step(a, stream));
+    if (workspace && p.nseg > 1) select_split(&a, p, static_cast<char*>(workspace));
+    return hip_status(wkv::launch_select_fwd(a, stream));
+}
+
+wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int in_dtype, int flags,
+                                 const int32_t* lengths, const void* x, const void* dt, const float* w, const void* b,
+                                 const void* c, const float* d, const void* z, const float* dt_bias, const void* go,
+                                 const float* s_in, const float* ds_out, void* dx, void* ddt, float* dw, void* db,
+                                 void* dc, float* dd, void* dz, float* ddt_bias, float* ds_in, const void* ckpt,
+                                 void* workspace, size_t workspace_bytes, void* hip_stream) {
+    const SelectPlan p = select_plan(B, T, C, G, N, in_dtype, false, true);
+    if (p.st != WKV_OK) return p.st;
+    if ((flags & ~WKV_SELECT_SOFTPLUS) != 0) return WKV_EINVAL;
+    if (C == 0) return WKV_OK;
+    if (!dw || (d && !dd) || (dt_bias && !ddt_bias)) return WKV_EINVAL;
+    if (!all_aligned(16, s_in, ds_out, ds_in, dw) || !all_aligned(4, d, dt_bias, dd, ddt_bias, lengths)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p.ns == 0 || T == 0) {  // empty sums; the state's gradient passes back
+        hipError_t e = wkv::launch_zero(dw, C * N, stream);
+        if (e == hipSuccess && d) e = wkv::launch_zero(dd, C, stream);
+        if (e == hipSuccess && dt_bias) e = wkv::launch_zero(ddt_bias, C, stream);
+        if (e == hipSuccess && p.ns > 0) e = wkv::launch_wkv5_state_copy(ds_out, ds_in, p.ns, stream);
+        return hip_status(e);
+    }
+    if (!x || !dt || !w || !b || !c || !go || !dx || !ddt || !db || !dc || (z && !dz)) return WKV_EINVAL;
+    if (!all_aligned(16, w, b, c, ckpt) || !all_aligned(in_size(in_dtype), x, dt, z, go, dx, ddt, dz, db, dc)) return WKV_EALIGN;
+    const size_t saved = ckpt ? 0 : (p.ckpt + 255) / 256 * 256, unsplit = p.part + p.dwp + p.vecp + saved;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < unsplit) return WKV_EWORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    wkv::SelectArgs a{B, T, C, G, N, in_dtype == WKV_BF16, (flags & WKV_SELECT_SOFTPLUS) != 0, lengths, x, dt, w, b, c, d, z, dt_bias, s_in};
+    a.tiles = p.tiles;
+    a.ctiles = static_cast<int>(p.ctiles);
+    a.seg_len = p.tiles * wkv::kSelectTile;
+    if (p.nseg > 1 && workspace_bytes >= unsplit + p.split) select_split(&a, p, ws + unsplit);
+    a.saved = static_cast<const float*>(ckpt);
+    if (ckpt == nullptr) {  // by a forward pass without outputs
+        wkv::SelectArgs f = a;
+        f.ckpt = reinterpret_cast<float*>(ws + p.part + p.dwp + p.vecp);
+        const hipError_t e = wkv::launch_select_fwd(f, stream);
+        if (e != hipSuccess) return hip_status(e);
+        a.saved = f.ckpt;
+    }
+    a.go = go;
+    a.ds_out = ds_out;
+    a.dx = dx;
+    a.ddt = ddt;
+    a.dw = dw;
+    a.db = db;
+    a.dc = dc;
+    a.dd = d ? dd : nullptr;
+    a.dz = dz;
+    a.ddt_bias = dt_bias ? ddt_bias : nullptr;
+    a.ds_in = ds_in;
+    a.part = reinterpret_cast<float*>(ws);
+    a.dw_part = reinterpret_cast<float*>(ws + p.part);
+    a.vec_part = reinterpret_cast<float*>(ws + p.part + p.dwp);
+    return hip_status(wkv::launch_select_bwd(a, stream));
+}
+
+size_t wkv_clip_workspace_bytes(int64_t count) {
+    if (count < 0 || count >= (int64_t{1} << 24)) return 0;
+    const int64_t launches = (count + wkv::kClipTensors - 1) / wkv::kClipTensors;
+    return launches > 0 ? static_cast<size_t>(launches * wkv::kClipBlocks + 1) * sizeof(double) : 0;
+}
+
+wkv_status_t wkv_grad_norm(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, float* norm,
+                           void* workspace, size_t workspace_bytes, void* hip_stream) {
+    int64_t total;
+    const wkv_status_t st = clip_check(count, grads, sizes, dtypes, &total);
+    if (st != WKV_OK) return st;
+    if (!norm) return WKV_EINVAL;
+    if (!aligned(norm, 4)) return WKV_EALIGN;
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (total == 0) return hip_status(wkv::launch_zero(norm, 1, stream));
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < wkv_clip_workspace_bytes(count)) return WKV_EWORKSPACE;
+    double* part = static_cast<double*>(workspace);
+    int64_t nparts;
+    hipError_t e = clip_sums(count, grads, sizes, dtypes, part, &nparts, stream);
+    if (e == hipSuccess) e = wkv::launch_clip_norm(part, nparts, norm, nullptr, stream);
+    return hip_status(e);
+}
+
+wkv_status_t wkv_clip_gradients(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes,
+                                const int* dtypes, float max_norm, float eps, float* norm, void* workspace,
+                                size_t workspace_bytes, void* hip_stream) {
+    int64_t total;
+    wkv_status_t st = clip_check(count, grads, sizes, dtypes, &total);
+    if (st != WKV_OK) return st;
+    if (!finite_in(max_norm, 1e30f) || !finite_in(eps, 1e30f)) return WKV_EINVAL;
+    if (!aligned(norm, 4)) return WKV_EALIGN;
+    for (int64_t i = 0; outs != nullptr && i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        if (!outs[i]) return WKV_EINVAL;
+        if (!aligned(outs[i], in_size(dtypes[i]))) return WKV_EALIGN;
+    }
+    hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (total == 0) return hip_status(wkv::launch_zero(norm, 1, stream));
+    void* const* to = outs != nullptr ? outs : const_cast<void* const*>(grads);
+    st = clip_overlaps(count, grads, to, sizes, dtypes, norm);
+    if (st != WKV_OK) return st;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < wkv_clip_workspace_bytes(count)) return WKV_EWORKSPACE;
+    double* part = static_cast<double*>(workspace);
+    int64_t nparts;
+    hipError_t e = clip_sums(count, grads, sizes, dtypes, part, &nparts, stream);
+    if (e == hipSuccess && nparts > kClipParts) {
+        e = wkv::launch_clip_norm(part, nparts, nullptr, part + nparts, stream);
+        part += nparts;
+        nparts = 1;
+    }
+    for (int64_t at = 0; at < count && e == hipSuccess;) {
+        wkv::ClipTable t;
+        clip_table(count, grads, to, sizes, dtypes, &at, &t);
+        if (t.count > 0) e = wkv::launch_clip_scale(t, part, nparts, max_norm, eps, norm, stream);
+    }
+    return hip_status(e);
 }
 
 size_t wkv_token_shift_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t M) {

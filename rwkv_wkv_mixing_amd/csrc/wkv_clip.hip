@@ -1,0 +1,204 @@
+// The norm of all gradients together, and the gradients scaled so that it is at most max_norm:
+//     norm = sqrt(sum over the tensors of the sums of their squares),  g' = g min(1, max_norm / (norm + eps))
+// Two passes over memory, which is what bounds them; the second one mostly reads from the last level cache where the
+// gradients fit it.  A launch takes many tensors: their addresses and sizes come as kernel arguments, their elements
+// are dealt out in chunks, and every workgroup takes every so many-th chunk of a fixed grid, so sums have a fixed order.
+//
+// Squares of eight elements are added in float32 and the eights in float64: squares cannot cancel, so the sum is good
+// to about 2^-23, and where the eight overflow or come near float32's smallest numbers they are added again in float64.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "wkv_lanes.h"
+#include "wkv_launch.h"
+
+namespace wkv {
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// The tensor that a chunk belongs to: the last one whose first chunk is not behind it.
+__device__ __forceinline__ int tensor_of(const ClipTable& t, int64_t chunk) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.chunk0[mid] <= chunk) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double squares(const float (&f)[8]) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
+    if (s > 1e-28f && s < 1e38f) return s;
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), d);
+    return d;
+}
+
+// Eight elements at e of a tensor whose address is on the 16-byte grid (kVec) or not; zeros behind its end.
+template <typename T, bool Vec>
+__device__ __forceinline__ void load8(const T* p, int64_t e, int64_t n, float (&f)[8]) {
+    if (Vec && e + 8 <= n) {
+        if constexpr (sizeof(T) == 4) {
+            const f4 a = *reinterpret_cast<const f4*>(p + e), b = *reinterpret_cast<const f4*>(p + e + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+        } else {
+            const u4 a = *reinterpret_cast<const u4*>(p + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(a[i] << 16), f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = e + i < n ? widen(p[e + i]) : 0.f;
+}
+
+template <typename T, bool Vec>
+__device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const float (&f)[8]) {
+    if (Vec && e + 8 <= n) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<f4*>(p + e) = f4{f[0], f[1], f[2], f[3]};
+            *reinterpret_cast<f4*>(p + e + 4) = f4{f[4], f[5], f[6], f[7]};
+        } else {
+            *reinterpret_cast<u4*>(p + e) = u4{pk2(f[0], f[1]), pk2(f[2], f[3]), pk2(f[4], f[5]), pk2(f[6], f[7])};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (e + i < n) {
+            if constexpr (sizeof(T) == 4) p[e + i] = f[i];
+            else p[e + i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[i]));
+        }
+    }
+}
+
+// The elements of a chunk: eight a thread, and the next eights a workgroup's width on.
+template <typename T, bool Vec>
+__device__ __forceinline__ double sum_chunk(const T* p, int64_t first, int64_t n) {
+    const int64_t end = first + kClipChunk < n ? first + kClipChunk : n;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int64_t e = first + threadIdx.x * 8; e < end; e += kThreads * 8) {
+        float f[8];
+        load8<T, Vec>(p, e, n, f);
+        sum += squares(f);
+    }
+    return sum;
+}
+
+template <typename T, bool Vec>
+__device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, int64_t n, float by) {
+    const int64_t end = first + kClipChunk < n ? first + kClipChunk : n;
+#pragma unroll 4
+    for (int64_t e = first + threadIdx.x * 8; e < end; e += kThreads * 8) {
+        float f[8];
+        load8<T, Vec>(p, e, n, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= by;
+        store8<T, Vec>(to, e, n, f);
+    }
+}
+
+__device__ __forceinline__ bool on_grid(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The sum of a workgroup's numbers, to all its threads.
+__device__ __forceinline__ double sum_block(double v) {
+    __shared__ double all[kThreads];
+    all[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll
+    for (int k = kThreads / 2; k > 0; k >>= 1) {
+        if (threadIdx.x < k) all[threadIdx.x] += all[threadIdx.x + k];
+        __syncthreads();
+    }
+    return all[0];
+}
+
+__global__ __launch_bounds__(kThreads) void clip_sums_kernel(ClipTable t, double* part) {
+    double sum = 0.0;
+    for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+        const int k = tensor_of(t, chunk);
+        const int64_t first = (chunk - t.chunk0[k]) * kClipChunk, n = t.n[k];
+        const bool vec = on_grid(t.in[k]);
+        if (t.bf16[k] != 0) {
+            const uint16_t* p = static_cast<const uint16_t*>(t.in[k]);
+            sum += vec ? sum_chunk<uint16_t, true>(p, first, n) : sum_chunk<uint16_t, false>(p, first, n);
+        } else {
+            const float* p = static_cast<const float*>(t.in[k]);
+            sum += vec ? sum_chunk<float, true>(p, first, n) : sum_chunk<float, false>(p, first, n);
+        }
+    }
+    sum = sum_block(sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+__device__ __forceinline__ double sum_parts(const double* part, int64_t n) {
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += part[i];
+    return sum_block(sum);
+}
+
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(const double* part, int64_t n, float* norm, double* total) {
+    const double sum = sum_parts(part, n);
+    if (threadIdx.x != 0) return;
+    if (norm != nullptr) *norm = static_cast<float>(sqrt(sum));
+    if (total != nullptr) *total = sum;
+}
+
+// Every workgroup adds up the partial sums for itself, so the factor needs no launch of its own.
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const double* part, int64_t nparts, float max_norm,
+                                                              float eps, float* norm) {
+    const double all = sqrt(sum_parts(part, nparts)), with = all + static_cast<double>(eps);
+    // 1 up to max_norm; a norm that is not a number is handed on to every gradient
+    const float by = with <= static_cast<double>(max_norm) ? 1.f : static_cast<float>(static_cast<double>(max_norm) / with);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(all);
+    for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+        const int k = tensor_of(t, chunk);
+        const int64_t first = (chunk - t.chunk0[k]) * kClipChunk, n = t.n[k];
+        if (by == 1.f && t.in[k] == t.out[k]) continue;
+        const bool vec = on_grid(t.in[k]) && on_grid(t.out[k]);
+        if (t.bf16[k] != 0) {
+            const uint16_t* p = static_cast<const uint16_t*>(t.in[k]);
+            uint16_t* to = static_cast<uint16_t*>(t.out[k]);
+            if (vec) scale_chunk<uint16_t, true>(p, to, first, n, by);
+            else scale_chunk<uint16_t, false>(p, to, first, n, by);
+        } else {
+            const float* p = static_cast<const float*>(t.in[k]);
+            float* to = static_cast<float*>(t.out[k]);
+            if (vec) scale_chunk<float, true>(p, to, first, n, by);
+            else scale_chunk<float, false>(p, to, first, n, by);
+        }
+    }
+}
+
+}  // namespace
+
+int64_t clip_blocks(const ClipTable& t) { return t.chunks < kClipBlocks ? t.chunks : kClipBlocks; }
+
+hipError_t launch_clip_sums(const ClipTable& t, double* part, hipStream_t stream) {
+    hipLaunchKernelGGL(clip_sums_kernel, dim3(static_cast<unsigned>(clip_blocks(t))), dim3(kThreads), 0, stream, t, part);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip_norm(const double* part, int64_t nparts, float* norm, double* total, hipStream_t stream) {
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kThreads), 0, stream, part, nparts, norm, total);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip_scale(const ClipTable& t, const double* part, int64_t nparts, float max_norm, float eps, float* norm,
+                             hipStream_t stream) {
+    const int64_t blocks = clip_blocks(t);
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, t, part, nparts, max_norm,
+                       eps, norm);
+    return hipGetLastError();
+}
+
+}  // namespace wkv

@@ -1,0 +1,369 @@
+// Short causal convolution over time, a filter of K taps a channel, with its activation: what stands before the
+// selective scan as the token shift stands before the other mixes.  With X the K - 1 carried inputs followed by the
+// row's tokens (so that X[t + K - 1] is token t):
+//     pre_t = bias + sum_j weight[j] X[t + j],   out_t = act(pre_t)
+// Streaming work: a thread owns V channels over a run of tokens, so x is read once (and K - 1 tokens a run twice) and
+// the window stays in registers; what bounds it is memory.
+//
+// Backward, with g_t = gout_t act'(pre_t) of the row's tokens (zero elsewhere):
+//     dX[e] = sum_j weight[j] g_{e - j} (+ the carried-out inputs' gradient),   dweight[j] = sum g_t X[t + j],   dbias = sum g
+// A thread walks its run and K - 1 tokens more, computing pre again from x.  The weights' sums are kept a thread, added
+// over a workgroup's runs in LDS and over workgroups by a second kernel, each in a fixed order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "wkv_lanes.h"
+#include "wkv_launch.h"
+
+namespace wkv {
+namespace {
+
+constexpr int kThreads = 256, kCols = 64, kRuns = kThreads / kCols;  // a workgroup: 64 vectors of channels, 4 runs
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+// V elements as they lie in memory, widened and narrowed.
+template <typename T, int V>
+struct Vec;
+template <>
+struct Vec<float, 4> {
+    typedef f4 Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = r[i];
+    }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[4]) { return Raw{f[0], f[1], f[2], f[3]}; }
+};
+template <>
+struct Vec<float, 1> {
+    typedef float Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[1]) { f[0] = r; }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[1]) { return f[0]; }
+};
+template <>
+struct Vec<uint16_t, 4> {
+    typedef u2 Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f[2 * i] = __uint_as_float(r[i] << 16), f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+    }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[4]) { return Raw{pk2(f[0], f[1]), pk2(f[2], f[3])}; }
+};
+template <>
+struct Vec<uint16_t, 1> {
+    typedef uint16_t Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[1]) { f[0] = wkv::widen(r); }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[1]) {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[0]));
+    }
+};
+
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * 1.44269504f)); }
+__device__ __forceinline__ float act_of(int act, float v) {
+    return act == kActNone ? v : act == kActSigmoid ? sigmoid(v) : v * sigmoid(v);
+}
+__device__ __forceinline__ float act_grad(int act, float v) {
+    if (act == kActNone) return 1.f;
+    const float p = sigmoid(v);
+    return act == kActSigmoid ? p * (1.f - p) : p * fmaf(v, 1.f - p, 1.f);
+}
+
+// A row's tokens.
+__device__ __forceinline__ int64_t row_length(const ConvArgs& P, int64_t b) {
+    const int64_t len = P.lengths != nullptr ? P.lengths[b] : P.T;
+    return len < 0 ? 0 : len > P.T ? P.T : len;
+}
+
+// V elements of channel c at row e of X (zeros where there is none: before the carried inputs when none are given,
+// and behind the row's length).
+template <typename T, int V>
+__device__ __forceinline__ typename Vec<T, V>::Raw load_ext(const ConvArgs& P, int64_t b, int64_t len, int64_t e, int64_t c, int K) {
+    typedef typename Vec<T, V>::Raw Raw;
+    const int64_t t = e - (K - 1);
+    if (t >= len) return Raw{};
+    if (t >= 0) return *reinterpret_cast<const Raw*>(static_cast<const T*>(P.x) + (b * P.T + t) * P.C + c);
+    if (P.s_in == nullptr) return Raw{};
+    return *reinterpret_cast<const Raw*>(static_cast<const T*>(P.s_in) + (b * (K - 1) + e) * P.C + c);
+}
+
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run, int64_t ncb) {
+    typedef Vec<T, V> Ops;
+    typedef typename Ops::Raw Raw;
+    constexpr int kAhead = 8;  // tokens whose loads are on their way at once
+    const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t cb = blk % ncb, rest = blk / ncb, ntb = (P.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
+    const int64_t b = rest / ntb, t0 = (rest % ntb) * kRuns * run + (threadIdx.x / kCols) * static_cast<int64_t>(run);
+    const int64_t c = (cb * kCols + threadIdx.x % kCols) * V;
+    if (b >= P.B || c >= P.C || t0 >= P.T) return;
+    const int64_t t1 = t0 + run < P.T ? t0 + run : P.T, len = row_length(P, b), te = len < t1 ? len : t1;
+    float w[K][V], bias[V], win[K][V];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = P.weight[j * P.C + c + i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = P.bias != nullptr ? P.bias[c + i] : 0.f;
+    Raw last[K - 1];  // the carried inputs of the next call: rows len .. len + K - 2 of X
+    const bool carry = t0 == 0 && P.s_out != nullptr;
+    if (carry) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) last[j] = load_ext<T, V>(P, b, len, len + j, c, K);
+    }
+    if (t0 < len) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) Ops::widen(load_ext<T, V>(P, b, len, t0 + j, c, K), win[j]);
+    }
+    const T* x = static_cast<const T*>(P.x) + (b * P.T) * P.C + c;
+    T* out = static_cast<T*>(P.out) + (b * P.T) * P.C + c;
+    for (int64_t t = t0; t < te; t += kAhead) {
+        Raw raw[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) raw[k] = t + k < te ? *reinterpret_cast<const Raw*>(x + (t + k) * P.C) : Raw{};
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (t + k < te) {
+                Ops::widen(raw[k], win[K - 1]);
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float pre = bias[i];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) pre = fmaf(w[j][i], win[j][i], pre);
+                    o[i] = act_of(P.act, pre);
+                }
+                *reinterpret_cast<Raw*>(out + (t + k) * P.C) = Ops::narrow(o);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
+            }
+        }
+    }
+    for (int64_t t = te > t0 ? te : t0; t < t1; ++t) *reinterpret_cast<Raw*>(out + t * P.C) = Raw{};
+    if (carry) {  // (s_out may be s_in: this thread alone reads and writes these rows of it)
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+            *reinterpret_cast<Raw*>(static_cast<T*>(P.s_out) + (b * (K - 1) + j) * P.C + c) = last[j];
+    }
+}
+
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run, int64_t ncb) {
+    typedef Vec<T, V> Ops;
+    typedef typename Ops::Raw Raw;
+    constexpr int kAhead = 4;
+    __shared__ float sums[kRuns][K + 1][V][kCols];
+    const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t cb = blk % ncb, slot = blk / ncb;
+    if (slot >= P.slots) return;  // (the whole workgroup)
+    const int col = threadIdx.x % kCols, r = threadIdx.x / kCols;
+    const int64_t c = (cb * kCols + col) * V;
+    const bool valid = c < P.C;
+    const int64_t ntb = (P.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
+    float w[K][V], bias[V], dw[K][V], db[V];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = valid ? P.weight[j * P.C + c + i] : 0.f, dw[j][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = valid && P.bias != nullptr ? P.bias[c + i] : 0.f, db[i] = 0.f;
+    // tiles of kRuns runs, every slots-th one
+    for (int64_t tile = slot; tile < P.B * ntb; tile += P.slots) {
+        const int64_t b = tile / ntb, t0 = (tile % ntb) * kRuns * run + r * static_cast<int64_t>(run);
+        if (!valid || t0 >= P.T) continue;
+        const int64_t t1 = t0 + run < P.T ? t0 + run : P.T, len = row_length(P, b);
+        const T* x = static_cast<const T*>(P.x) + (b * P.T) * P.C + c;
+        const T* go = static_cast<const T*>(P.gout) + (b * P.T) * P.C + c;
+        T* dx = static_cast<T*>(P.dx) + (b * P.T) * P.C + c;
+        float win[K][V], g[K][V];  // of X, and of g: the window's last row is the token at hand
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) win[j][i] = g[j][i] = 0.f;
+        if (t0 < len) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) Ops::widen(load_ext<T, V>(P, b, len, t0 + j, c, K), win[j]);
+        }
+        // row e = t of X (token t - (K - 1)) has all its g once token t is done; the run answers for the tokens
+        // t0 .. t1 - 1, and the first one for the carried inputs too
+        const int64_t end = t1 + K - 1, live = len < end ? len : end;
+        for (int64_t tt = t0; tt < end; tt += kAhead) {
+            Raw rx[kAhead], rg[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool is = tt + k < live;
+                rx[k] = is ? *reinterpret_cast<const Raw*>(x + (tt + k) * P.C) : Raw{};
+                rg[k] = is ? *reinterpret_cast<const Raw*>(go + (tt + k) * P.C) : Raw{};
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t t = tt + k;
+                if (t >= end) continue;
+                if (t < live) {
+                    float gv[V];
+                    Ops::widen(rx[k], win[K - 1]);
+                    Ops::widen(rg[k], gv);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float pre = bias[i];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) pre = fmaf(w[j][i], win[j][i], pre);
+                        g[K - 1][i] = gv[i] * act_grad(P.act, pre);
+                    }
+                    if (t < t1) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+#pragma unroll
+                            for (int j = 0; j < K; ++j) dw[j][i] = fmaf(g[K - 1][i], win[j][i], dw[j][i]);
+                            db[i] += g[K - 1][i];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[K - 1][i] = 0.f;
+                }
+                // dX[t] = sum_j weight[j] g_{t - j}
+                const int64_t to = t - (K - 1);
+                if (to >= t0 || (t0 == 0 && P.ds_in != nullptr)) {
+                    float o[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        o[i] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], g[K - 1 - j][i], o[i]);
+                    }
+                    if (P.ds_out != nullptr && t >= len && t < len + K - 1) {
+                        float e[V];
+                        Ops::widen(*reinterpret_cast<const Raw*>(static_cast<const T*>(P.ds_out) + (b * (K - 1) + t - len) * P.C + c), e);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) o[i] += e[i];
+                    }
+                    Raw ro = Ops::narrow(o);
+                    if (to < 0) {
+                        *reinterpret_cast<Raw*>(static_cast<T*>(P.ds_in) + (b * (K - 1) + t) * P.C + c) = ro;
+                    } else {
+                        if (to >= len) ro = Raw{};
+                        *reinterpret_cast<Raw*>(dx + to * P.C) = ro;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i], g[j][i] = g[j + 1][i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) sums[r][j][i][col] = dw[j][i];
+        sums[r][K][i][col] = db[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < (K + 1) * V * kCols; e += kThreads) {
+        const int q = e % kCols, i = e / kCols % V, j = e / (kCols * V);
+        const int64_t ch = (cb * kCols + q) * V + i;
+        if (ch >= P.C) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) sum += sums[k][j][i][q];
+        P.part[(slot * (K + 1) + j) * P.C + ch] = sum;
+    }
+}
+
+// dweight and dbias from the slots' sums, in order: a wave takes 64 outputs, its workgroup's four waves a quarter of
+// the slots each.
+__global__ __launch_bounds__(256) void conv_reduce_kernel(ConvArgs P) {
+    __shared__ float sums[4][64];
+    const int64_t n = (P.K + 1) * P.C, i = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    const int q = threadIdx.x >> 6;
+    const int64_t each = (P.slots + 3) / 4, first = q * each, last = first + each < P.slots ? first + each : P.slots;
+    float sum = 0.f;
+    if (i < n)
+        for (int64_t s = first; s < last; ++s) sum += P.part[s * n + i];
+    sums[q][threadIdx.x & 63] = sum;
+    __syncthreads();
+    if (q != 0 || i >= n) return;
+    const int l = threadIdx.x;
+    sum = (sums[0][l] + sums[1][l]) + (sums[2][l] + sums[3][l]);
+    if (i < P.K * P.C) P.dweight[i] = sum;
+    else if (P.dbias != nullptr) P.dbias[i - P.K * P.C] = sum;
+}
+
+// Carried inputs of a call without tokens: they pass on (or zeros do).
+template <typename T>
+__global__ __launch_bounds__(256) void conv_copy_kernel(const T* from, T* to, int64_t n) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) to[i] = from != nullptr ? from[i] : T{0};
+}
+
+// Tokens a run: long ones read less twice, but the card wants some 2048 workgroups.
+int run_of(int64_t B, int64_t T, int64_t ncb, int longest) {
+    int run = longest;
+    while (run > 4 && B * ((T + kRuns * run - 1) / (kRuns * run)) * ncb < 2048) run /= 2;
+    return run;
+}
+
+dim3 grid_of(int64_t blocks) {
+    constexpr int64_t kMost = int64_t{1} << 20;
+    if (blocks <= kMost) return dim3(static_cast<unsigned>(blocks));
+    return dim3(static_cast<unsigned>(kMost), static_cast<unsigned>((blocks + kMost - 1) / kMost));
+}
+
+template <typename T, int V, int K>
+hipError_t conv_launch(const ConvArgs& a, bool bwd, hipStream_t stream) {
+    const int64_t ncb = (a.C + kCols * V - 1) / (kCols * V);
+    if (!bwd) {
+        const int run = run_of(a.B, a.T, ncb, 16);
+        const int64_t ntb = (a.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
+        hipLaunchKernelGGL((conv_fwd_kernel<T, V, K>), grid_of(a.B * ntb * ncb), dim3(kThreads), 0, stream, a, run, ncb);
+        return hipGetLastError();
+    }
+    const int run = run_of(a.B, a.T, ncb, 32);
+    hipLaunchKernelGGL((conv_bwd_kernel<T, V, K>), grid_of(a.slots * ncb), dim3(kThreads), 0, stream, a, run, ncb);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t n = (K + 1) * a.C;
+    hipLaunchKernelGGL(conv_reduce_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t conv_k(const ConvArgs& a, bool bwd, hipStream_t stream) {
+    switch (a.K) {
+        case 2: return conv_launch<T, V, 2>(a, bwd, stream);
+        case 3: return conv_launch<T, V, 3>(a, bwd, stream);
+        default: return conv_launch<T, V, 4>(a, bwd, stream);
+    }
+}
+
+hipError_t conv_t(const ConvArgs& a, bool bwd, hipStream_t stream) {
+    if (a.bf16) return a.vec ? conv_k<uint16_t, 4>(a, bwd, stream) : conv_k<uint16_t, 1>(a, bwd, stream);
+    return a.vec ? conv_k<float, 4>(a, bwd, stream) : conv_k<float, 1>(a, bwd, stream);
+}
+
+}  // namespace
+
+// Rows of partial sums of the backward: as many workgroups as fill the card and no more than there are tiles of the
+// shortest runs.
+int64_t conv_slots(int64_t B, int64_t T, int64_t C) {
+    const int64_t ncb = (C + kCols - 1) / kCols, tiles = B * ((T + kRuns * 4 - 1) / (kRuns * 4));
+    int64_t most = 4096 / (ncb > 0 ? ncb : 1);
+    most = most < 16 ? 16 : most;
+    return tiles < most ? tiles : most;
+}
+
+hipError_t launch_conv_copy(const void* from, void* to, int64_t n, bool bf16, hipStream_t stream) {
+    if (to == nullptr || to == from || n <= 0) return hipSuccess;
+    const dim3 grid = grid_of((n + 255) / 256);
+    if (bf16) hipLaunchKernelGGL(conv_copy_kernel<uint16_t>, grid, dim3(256), 0, stream, static_cast<const uint16_t*>(from), static_cast<uint16_t*>(to), n);
+    else hipLaunchKernelGGL(conv_copy_kernel<float>, grid, dim3(256), 0, stream, static_cast<const float*>(from), static_cast<float*>(to), n);
+    return hipGetLastError();
+}
+
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) { return conv_t(a, false, stream); }
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) { return conv_t(a, true, stream); }
+
+}  // namespace wkv

@@ -375,6 +375,106 @@ hipError_t launch_zero(float* p, int64_t n, hipStream_t stream);  // p may be NU
 int64_t head_norm_chunks(int64_t rows, int64_t C);
 int64_t block_norm_slots(int64_t rows, int64_t C);
 
+struct ConvArgs {
+    int64_t B, T, C, K;       // K taps, 2 to 4
+    bool bf16, vec;           // vec: vectors of 4 elements (C a multiple of 4, pointers aligned to them)
+    int act;
+    const int32_t* lengths;   // [B] tokens of each row, or NULL (T)
+    const void* x;            // [B, T, C]
+    const float* weight;      // [K, C]
+    const float* bias;        // [C] or NULL
+    const void* s_in;         // [B, K - 1, C] the inputs before token 1, or NULL (zeros)
+    void* out = nullptr;      // [B, T, C]
+    void* s_out = nullptr;    // [B, K - 1, C] or NULL; may be s_in
+    // backward
+    const void* gout = nullptr;    // [B, T, C]
+    const void* ds_out = nullptr;  // [B, K - 1, C] or NULL
+    void* dx = nullptr;            // [B, T, C]
+    float* dweight = nullptr;      // [K, C]
+    float* dbias = nullptr;        // [C], with bias
+    void* ds_in = nullptr;         // [B, K - 1, C] or NULL
+    float* part = nullptr;         // [slots, K + 1, C]
+    int64_t slots = 0;             // = conv_slots(B, T, C)
+};
+
+// short causal convolution (wkv_conv.hip)
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv_copy(const void* from, void* to, int64_t n, bool bf16, hipStream_t stream);  // from NULL: zeros
+int64_t conv_slots(int64_t B, int64_t T, int64_t C);
+
+// Gradient norm and clipping (wkv_clip.hip): a launch takes up to kClipTensors tensors, by value.
+constexpr int kClipTensors = 96;
+struct ClipTable {
+    const void* in[kClipTensors];
+    void* out[kClipTensors];          // unused for the norm alone
+    int64_t n[kClipTensors];          // elements
+    int64_t chunk0[kClipTensors];     // number of the tensor's first chunk in this launch
+    uint8_t bf16[kClipTensors];
+    int count;
+    int64_t chunks;                   // of all the tensors
+};
+constexpr int64_t kClipBlocks = 1024;  // workgroups of a launch at most, and partial sums it writes
+constexpr int64_t kClipChunk = 16384;  // elements
+// partial sums of squares: one a workgroup, from part on; their number
+int64_t clip_blocks(const ClipTable& t);
+hipError_t launch_clip_sums(const ClipTable& t, double* part, hipStream_t stream);
+// nparts partial sums to one, behind them, when there are too many for every workgroup to add up
+hipError_t launch_clip_norm(const double* part, int64_t nparts, float* norm, double* total, hipStream_t stream);
+hipError_t launch_clip_scale(const ClipTable& t, const double* part, int64_t nparts, float max_norm, float eps, float* norm,
+                             hipStream_t stream);
+
+constexpr int kSelectTile = 16;  // tokens between saved states of the selective scan
+// Up to this many tokens without saved states it runs token by token (select_step_kernel).
+constexpr int64_t kSelectStepMaxT = 8;
+
+struct SelectArgs {
+    int64_t B, T, C, G, N;    // channels in G groups that share b and c; N states a channel
+    bool bf16, softplus;
+    const int32_t* lengths;   // [B] tokens of each row, or NULL (T)
+    const void* x;            // [B, T, C]
+    const void* dt;           // [B, T, C]
+    const float* w;           // [C, N] decay rates
+    const void* b;            // [B, T, G N]
+    const void* c;
+    const float* d;           // [C] or NULL
+    const void* z;            // [B, T, C] or NULL (no gate)
+    const float* dt_bias;     // [C] or NULL
+    const float* s_in;        // [B, C, N] or NULL (zero state)
+    int64_t tiles = 0;        // ceil(T / kSelectTile)
+    int ctiles = 0;           // tiles of 64 channels: G ceil(C / G / 64)
+    int64_t nseg = 1, seg_len = 0;  // time split: segments of seg_len tokens (a multiple of kSelectTile)
+    float* local = nullptr;   // [nseg, B, C, N] what the segments do to a state of zero, then their start states
+    float* steps = nullptr;   // [nseg, B, C] the segments' sums of delta
+    // forward
+    void* out = nullptr;      // [B, T, C]
+    float* s_out = nullptr;   // [B, C, N] or NULL
+    float* ckpt = nullptr;    // [B, tiles, N / NS, C, NS] the state before every kSelectTile tokens, or NULL
+    // backward
+    const float* saved = nullptr;  // the forward's ckpt
+    const void* go = nullptr;      // [B, T, C]
+    const float* ds_out = nullptr; // [B, C, N] or NULL
+    void* dx = nullptr;
+    void* ddt = nullptr;
+    float* dw = nullptr;           // [C, N]
+    void* db = nullptr;
+    void* dc = nullptr;
+    float* dd = nullptr;           // [C], with d
+    void* dz = nullptr;            // with z
+    float* ddt_bias = nullptr;     // [C], with dt_bias
+    float* ds_in = nullptr;        // [B, C, N] or NULL
+    float* part = nullptr;         // [ctiles, B, T, 2 N] sums over a tile's channels for db and dc
+    float* dw_part = nullptr;      // [nseg, B, C, N]
+    float* vec_part = nullptr;     // [nseg, B, C, 2] for dd and ddt_bias
+};
+
+// selective scan (wkv_select.hip)
+hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream);
+hipError_t launch_select_fwd(const SelectArgs& a, hipStream_t stream);
+hipError_t launch_select_bwd(const SelectArgs& a, hipStream_t stream);
+// segments for a time split (1: no split), *per tokens each
+int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t* per);
+
 // decode step (wkv_step.hip)
 hipError_t launch_step(const StepArgs& s, hipStream_t stream);
 

@@ -1,0 +1,673 @@
+// Selective state space scan: per channel a diagonal state of N numbers whose decay and whose writes depend on the
+// token.  With a_t = e^{-delta_t w}, delta_t = softplus(dt_t + dt_bias):
+//     h_t[n] = a_t[n] h_{t-1}[n] + delta_t x_t b_t[n],   y_t = sum_n c_t[n] h_t[n] + d x_t,   out_t = y_t silu(z_t)
+// b and c are shared by the channels of a group.  Every (channel, n) decays at a rate of its own, so nothing here is a
+// matrix product: the work is one exponential, two multiplications and two multiply-adds a (token, channel, n) on the
+// vector units, which is what bounds it (a channel-token of N = 16 moves 8 bytes in bf16 and takes some 130 lane
+// instructions, 0.1 us a million at this card's rate against 0.04 for the bytes).
+//
+// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, NS a wave: b_t and c_t are then
+// the same for a whole wave and come in through scalar loads, and only delta, the written value and the waves' parts of
+// y pass through LDS.  Tiles of 16 tokens: the threads first work out delta and what is written for (token, channel)
+// pairs, one each; then every wave walks the tile; then the threads add the waves' parts, gate and store.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "wkv_lanes.h"
+#include "wkv_launch.h"
+
+namespace wkv {
+namespace {
+
+constexpr int kTile = kSelectTile;  // tokens a tile
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ uint16_t narrow<uint16_t>(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// e^{-|x|}.  Wide: the rounding of x log2 e, up to 2^-21 of the result at |x| = 8, is put back.
+template <bool Wide>
+__device__ __forceinline__ float exp_neg_abs(float x) {
+    const float a = -__builtin_fabsf(x), t = a * kLog2e;
+    const float e = exp2_fast(t);
+    if constexpr (!Wide) return e;
+    const float lost = fmaf(a, kLog2e, -t) + a * 1.92596299e-8f;  // log2 e = kLog2e + 1.92596299e-8
+    return a < -100.f ? e : fmaf(e, 0.693147180559945f * lost, e);
+}
+
+// log(1 + e) for e in [0, 1]: e times a polynomial through the Chebyshev points of [0, 1] of log(1 + e) / e (within
+// 1.3e-7 of it), so a small e keeps its digits.
+__device__ __forceinline__ float log1p_unit(float e) {
+    float p = -0.0031760570127516985f;
+    p = fmaf(p, e, 0.019542526453733444f);
+    p = fmaf(p, e, -0.056373611092567444f);
+    p = fmaf(p, e, 0.10543623566627502f);
+    p = fmaf(p, e, -0.1526966691017151f);
+    p = fmaf(p, e, 0.1966327428817749f);
+    p = fmaf(p, e, -0.24951615929603577f);
+    p = fmaf(p, e, 0.33329710364341736f);
+    p = fmaf(p, e, -0.49999892711639404f);
+    p = fmaf(p, e, 1.0f);
+    return p * e;
+}
+
+// delta of a token, and its derivative by dt.
+template <bool Wide, bool Grad>
+__device__ __forceinline__ float step_of(float raw, bool softplus, float* grad) {
+    if (!softplus) {
+        if constexpr (Grad) *grad = 1.f;
+        return raw;
+    }
+    const float e = exp_neg_abs<Wide>(raw);
+    if constexpr (Grad) *grad = (raw >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
+    const float s = (raw > 0.f ? raw : 0.f) + log1p_unit(e);
+    return raw != raw ? raw : s;
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e)); }
+
+// NS neighbouring values of a row of b or c for a whole wave, through the scalar cache (the inputs are not written
+// while the kernel runs); zeros for a token that is none.
+template <typename T, int NS>
+struct Uniform;
+template <int NS>
+struct Uniform<float, NS> {
+    static __device__ __forceinline__ void load(const float* p, bool live, float (&f)[NS]) {
+        typedef const __attribute__((address_space(4))) uint32_t* Scalar;
+        const Scalar q = (Scalar)(p);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) f[i] = __uint_as_float(live ? q[i] : 0u);
+    }
+};
+template <int NS>
+struct Uniform<uint16_t, NS> {
+    static __device__ __forceinline__ void load(const uint16_t* p, bool live, float (&f)[NS]) {
+        typedef const __attribute__((address_space(4))) uint32_t* Scalar;
+        const Scalar q = (Scalar)(p);
+#pragma unroll
+        for (int i = 0; i < NS / 2; ++i) {
+            const uint32_t v = live ? q[i] : 0u;
+            f[2 * i] = __uint_as_float(v << 16);
+            f[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        }
+    }
+};
+
+template <int NS>
+__device__ __forceinline__ void load_states(const float* p, bool valid, float (&h)[NS]) {
+#pragma unroll
+    for (int q = 0; q < NS / 4; ++q) {
+        const f4 v = valid ? *reinterpret_cast<const f4*>(p + 4 * q) : f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[4 * q + i] = v[i];
+    }
+}
+template <int NS>
+__device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
+#pragma unroll
+    for (int q = 0; q < NS / 4; ++q) *reinterpret_cast<f4*>(p + 4 * q) = f4{h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]};
+}
+
+// Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
+struct Place {
+    int64_t b, ch;       // batch row; the lane's channel (a spare lane's: the last one of its group)
+    int ct, g, seg;
+    int t0, t1, te;      // rows t0 .. t1 - 1 of which those before te are tokens
+    bool valid;          // not a spare lane
+};
+
+__device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
+    Place p;
+    const uint32_t nct = static_cast<uint32_t>(P.ctiles);
+    uint32_t blk = blockIdx.x;
+    p.ct = blk % nct;
+    blk /= nct;
+    p.b = blk % static_cast<uint32_t>(P.B);
+    p.seg = blk / static_cast<uint32_t>(P.B);
+    const int per_group = P.ctiles / static_cast<int>(P.G);
+    p.g = p.ct / per_group;
+    const int64_t width = P.C / P.G, c = static_cast<int64_t>(p.ct % per_group) * 64 + lane;
+    p.valid = c < width;
+    p.ch = p.g * width + (p.valid ? c : width - 1);
+    const int64_t T = P.T, first = p.seg * P.seg_len, last = first + P.seg_len;
+    int64_t len = P.lengths != nullptr ? P.lengths[p.b] : T;
+    len = len < 0 ? 0 : len > T ? T : len;
+    p.t0 = static_cast<int>(first);
+    p.t1 = static_cast<int>(last < T ? last : T);
+    p.te = static_cast<int>(len < p.t0 ? p.t0 : len < p.t1 ? len : p.t1);
+    return p;
+}
+
+// What a walk does: the outputs; what each segment does to a state of zero; the same for the states' gradients, from
+// the last token to the first: g <- a (g + c gy).
+enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2 };
+
+template <typename T, int NS, int W, int Mode>
+__global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
+    constexpr int N = NS * W, kEach = kTile / W;  // (token, channel) pairs a thread works out
+    constexpr bool kWide = sizeof(T) == 4, kOut = Mode == kWalkOut, kAdj = Mode == kWalkAdjoint;
+    __shared__ float2 put[2][kTile][64];                         // delta and the written value
+    __shared__ float parts[kOut ? 2 : 1][kOut ? W : 1][kTile][64];  // the waves' parts of y
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place p = place_of(P, lane);
+    const T* __restrict__ x = static_cast<const T*>(P.x);
+    const T* __restrict__ dt = static_cast<const T*>(P.dt);
+    const T* __restrict__ z = static_cast<const T*>(P.z);
+    const T* __restrict__ go = static_cast<const T*>(P.go);
+    T* __restrict__ out = static_cast<T*>(P.out);
+    const int64_t row0 = p.b * P.T, GN = P.G * N;
+    const T* bc = static_cast<const T*>(kAdj ? P.c : P.b) + (row0 * GN + p.g * N + wave * NS);
+    const T* cc = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
+    const float bias = P.dt_bias != nullptr ? P.dt_bias[p.ch] : 0.f;
+    const float skip = P.d != nullptr ? P.d[p.ch] : 0.f;
+    const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
+
+    float w2[NS], h[NS];
+    load_states<NS>(P.w + p.ch * N + wave * NS, true, w2);
+    // (a rate of infinity is held finite, so that a step of zero keeps the state)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) w2[i] = -fminf(w2[i], 2e38f) * kLog2e, h[i] = 0.f;
+    const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
+    if constexpr (kOut) {
+        if (P.nseg > 1) load_states<NS>(P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, p.valid, h);
+        else if (P.s_in != nullptr) load_states<NS>(P.s_in + state, p.valid, h);
+    }
+
+    // inputs of the tile after the next, of the next and of this one: the raw values, then what the epilogue needs
+    T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
+    float ex[2][kEach], ez[2][kEach];
+    const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
+    const auto fetch = [&](int i) {
+        const int t = tile_at(i) + wave;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            rx[k] = rd[k] = rz[k] = rg[k] = T{0};
+            if (i < ntiles && t + W * k < p.te) {
+                const int64_t at = (row0 + t + W * k) * P.C + p.ch;
+                rd[k] = dt[at];
+                if constexpr (kAdj) rg[k] = go[at];
+                else rx[k] = x[at];
+                if ((kOut || kAdj) && z != nullptr) rz[k] = z[at];
+            }
+        }
+    };
+    float total = 0.f;  // of delta
+    const auto stage = [&](int i) {
+        if (i >= ntiles) return;
+        const int t = tile_at(i) + wave;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const bool live = t + W * k < p.te && p.valid;
+            const float raw = widen(rd[k]) + bias;
+            float delta = step_of<kWide, false>(raw, P.softplus, nullptr);
+            float v = kAdj ? widen(rg[k]) : widen(rx[k]);
+            if constexpr (kAdj) {
+                const float zz = widen(rz[k]);
+                if (z != nullptr) v *= zz * sigmoid(zz);
+            } else {
+                if constexpr (kOut) {
+                    const float zz = widen(rz[k]);
+                    ex[i & 1][k] = skip * v;
+                    ez[i & 1][k] = z != nullptr ? zz * sigmoid(zz) : 1.f;
+                }
+                v *= delta;
+            }
+            delta = live ? delta : 0.f;
+            put[i & 1][wave + W * k][lane] = make_float2(delta, live ? v : 0.f);
+            if constexpr (!kOut) total += delta;
+        }
+    };
+
+    fetch(0);
+    stage(0);
+    fetch(1);
+    __syncthreads();
+    for (int i = 0; i < ntiles; ++i) {
+        const int t = tile_at(i);
+        if constexpr (kOut) {
+            if (P.ckpt != nullptr && p.valid)
+                store_states<NS>(P.ckpt + (((p.b * P.tiles + t / kTile) * W + wave) * P.C + p.ch) * NS, h);
+        }
+        const T* bt = bc + t * GN;
+        const T* ct = cc + t * GN;
+        const int n = p.te - t;
+#pragma unroll
+        for (int jj = 0; jj < kTile; ++jj) {
+            const int j = kAdj ? kTile - 1 - jj : jj;
+            const bool live = j < n;
+            const float2 dv = put[i & 1][j][lane];
+            float b[NS], c[NS], y = 0.f;
+            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
+            if constexpr (kOut) Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const float a = exp2_fast(dv.x * w2[s]);
+                if constexpr (kAdj) {
+                    h[s] = a * fmaf(b[s], dv.y, h[s]);
+                } else {
+                    h[s] = fmaf(a, h[s], b[s] * dv.y);
+                    if constexpr (kOut) y = fmaf(c[s], h[s], y);
+                }
+            }
+            if constexpr (kOut) parts[i & 1][wave][j][lane] = y;
+        }
+        stage(i + 1);
+        __syncthreads();
+        fetch(i + 2);
+        if constexpr (kOut) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int j = wave + W * k;
+                float y = ex[i & 1][k];
+#pragma unroll
+                for (int q = 0; q < W; ++q) y += parts[i & 1][q][j][lane];
+                if (j < n && p.valid && out != nullptr) out[(row0 + t + j) * P.C + p.ch] = narrow<T>(y * ez[i & 1][k]);
+            }
+        }
+    }
+    if constexpr (kOut) {
+        if (p.valid) {
+            for (int t = p.te + wave; t < p.t1 && out != nullptr; t += W) out[(row0 + t) * P.C + p.ch] = T{0};
+            if (P.s_out != nullptr && p.seg == P.nseg - 1) store_states<NS>(P.s_out + state, h);
+        }
+    } else {
+        const int64_t at = static_cast<int64_t>(p.seg) * P.B * P.C;
+        if (p.valid) store_states<NS>(P.local + at * N + state, h);
+        __syncthreads();
+        put[0][wave][lane].x = total;
+        __syncthreads();
+        if (wave == 0 && p.valid) {
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) sum += put[0][q][lane].x;
+            P.steps[at + p.b * P.C + p.ch] = sum;
+        }
+    }
+}
+
+// The states before the segments (or their gradients behind them, from the last one), in place of what the segments do
+// to a state of zero: a state passes a segment by e^{-w (sum of its steps)}.
+__global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool reverse) {
+    const int64_t n = P.B * P.C * P.N;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t bc = i / P.N;
+    const float w2 = -fminf(P.w[bc % P.C * P.N + i % P.N], 2e38f) * kLog2e;
+    const float* first = reverse ? P.ds_out : P.s_in;
+    float h = first != nullptr ? first[i] : 0.f;
+    for (int64_t k = 0; k < P.nseg; ++k) {
+        const int64_t s = reverse ? P.nseg - 1 - k : k;
+        float* at = P.local + s * n + i;
+        const float own = *at;
+        *at = h;
+        h = fmaf(exp2_fast(P.steps[s * P.B * P.C + bc] * w2), h, own);
+    }
+}
+
+// Gradients, tile by tile from the last: the tile's states are walked again from the one that the forward kept, then its
+// tokens are taken back to front,
+//     g += c_t gy_t,   dc_t = sum gy_t h_t,   db_t = sum g u_t  (over channels),   du_t = sum_n g b_t,
+//     g *= a_t,   q = g h_{t-1},   ddelta_t = du_t x_t - sum_n w q,   dw -= delta_t q
+// The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
+// of which every exchange between lanes halves the registers, so 16 tokens end as one number a lane and register.
+template <typename T, int NS, int W>
+__global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
+    constexpr int N = NS * W, kEach = kTile / W;
+    constexpr bool kWide = sizeof(T) == 4, kKeep = NS <= 4;  // decays kept, not worked out again
+    __shared__ float4 put[kTile][64];           // delta, the written value, the gradient of y
+    __shared__ float parts[3][W][kTile][64];    // the waves' parts of y, du and -ddelta
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place p = place_of(P, lane);
+    const T* __restrict__ x = static_cast<const T*>(P.x);
+    const T* __restrict__ dt = static_cast<const T*>(P.dt);
+    const T* __restrict__ z = static_cast<const T*>(P.z);
+    const T* __restrict__ go = static_cast<const T*>(P.go);
+    T* __restrict__ dx = static_cast<T*>(P.dx);
+    T* __restrict__ ddt = static_cast<T*>(P.ddt);
+    T* __restrict__ dz = static_cast<T*>(P.dz);
+    const int64_t row0 = p.b * P.T, GN = P.G * N;
+    const T* bc = static_cast<const T*>(P.b) + (row0 * GN + p.g * N + wave * NS);
+    const T* cc = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
+    const float bias = P.dt_bias != nullptr ? P.dt_bias[p.ch] : 0.f;
+    const float skip = P.d != nullptr ? P.d[p.ch] : 0.f;
+    const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
+
+    float w1[NS], w2[NS], g[NS], dw[NS], first[NS];
+    load_states<NS>(P.w + p.ch * N + wave * NS, true, w1);
+    const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
+    const float* from = P.nseg > 1 ? P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N : P.ds_out;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) w1[i] = fminf(w1[i], 2e38f), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
+    if (from != nullptr) load_states<NS>(from + state, p.valid, g);
+
+    T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
+    const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
+    const auto fetch = [&](int i) {
+        if (i < 0) return;
+        const int t = tile_at(i) + wave;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            rx[k] = rd[k] = rz[k] = rg[k] = T{0};
+            if (t + W * k < p.te) {
+                const int64_t at = (row0 + t + W * k) * P.C + p.ch;
+                rd[k] = dt[at];
+                rx[k] = x[at];
+                rg[k] = go[at];
+                if (z != nullptr) rz[k] = z[at];
+            }
+        }
+        load_states<NS>(P.saved + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
+    };
+    float dd = 0.f, dbias = 0.f;
+    fetch(ntiles - 1);
+    for (int i = ntiles - 1; i >= 0; --i) {
+        const int t = tile_at(i), n = p.te - t;
+        float ex[kEach], egy[kEach], egs[kEach], edelta[kEach], eslope[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const bool live = wave + W * k < n && p.valid;
+            const float delta = step_of<kWide, true>(widen(rd[k]) + bias, P.softplus, &eslope[k]);
+            const float zz = widen(rz[k]), gg = widen(rg[k]), sg = sigmoid(zz);
+            ex[k] = widen(rx[k]);
+            edelta[k] = delta;
+            egy[k] = z != nullptr ? gg * (zz * sg) : gg;
+            egs[k] = gg * (sg * fmaf(zz, 1.f - sg, 1.f));
+            put[wave + W * k][lane] = live ? make_float4(delta, delta * ex[k], egy[k], 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float h[kTile + 1][NS], a[kKeep ? kTile : 1][NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) h[0][s] = first[s];
+        __syncthreads();
+        fetch(i - 1);
+        const T* bt = bc + t * GN;
+        const T* ct = cc + t * GN;
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+            const bool live = j < n;
+            const float4 v = put[j][lane];
+            float b[NS], c[NS], y = 0.f;
+            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
+            Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const float e = exp2_fast(v.x * w2[s]);
+                if constexpr (kKeep) a[j][s] = e;
+                h[j + 1][s] = fmaf(e, h[j][s], b[s] * v.y);
+                y = fmaf(c[s], h[j + 1][s], y);
+            }
+            parts[0][wave][j][lane] = y;
+        }
+        float lanes8[NS / 4][8];
+#pragma unroll
+        for (int j = kTile - 1; j >= 0; --j) {
+            const bool live = j < n;
+            const float4 v = put[j][lane];
+            float b[NS], c[NS], du = 0.f, down = 0.f;
+            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
+            Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
+#pragma unroll
+            for (int q = 0; q < NS / 4; ++q) {
+                float r[4];
+#pragma unroll
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const int s = 4 * q + i4;
+                    g[s] = fmaf(c[s], v.z, g[s]);
+                    const float pb = g[s] * v.y, pc = v.z * h[j + 1][s];
+                    du = fmaf(g[s], b[s], du);
+                    g[s] *= kKeep ? a[j][s] : exp2_fast(v.x * w2[s]);
+                    const float m = g[s] * h[j][s];
+                    down = fmaf(m, w1[s], down);
+                    dw[s] = fmaf(-m, v.x, dw[s]);
+                    // db to the lower half of the lanes, dc to the upper
+                    const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(pb), __float_as_uint(pc), false, false);
+                    r[i4] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+                }
+                // n + 0 and n + 1 to the even rows of 16 lanes, n + 2 and n + 3 to the odd ones
+                float m2[2];
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                    const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[i2]), __float_as_uint(r[i2 + 2]), false, false);
+                    m2[i2] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+                }
+                m2[0] += dpp<0x128>(m2[0]);  // row_ror:8
+                m2[1] += dpp<0x128>(m2[1]);
+                lanes8[q][j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
+                if ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
+                    float (&l)[8] = lanes8[q];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float lo = l[k] + dpp<0x141>(l[k]), hi = l[k + 4] + dpp<0x141>(l[k + 4]);  // row_half_mirror
+                        l[k] = (lane & 4) != 0 ? hi : lo;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float lo = l[k] + dpp<0x4E>(l[k]), hi = l[k + 2] + dpp<0x4E>(l[k + 2]);  // lane ^ 2
+                        l[k] = (lane & 2) != 0 ? hi : lo;
+                    }
+                    const float lo = l[0] + dpp<0xB1>(l[0]), hi = l[1] + dpp<0xB1>(l[1]);  // lane ^ 1
+                    const float sum = (lane & 1) != 0 ? hi : lo;
+                    const int tok = j + (lane & 7);
+                    if (tok < n) {
+                        const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
+                        P.part[row + (lane >> 5) * N + wave * NS + 4 * q + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = sum;
+                    }
+                }
+            }
+            parts[1][wave][j][lane] = du;
+            parts[2][wave][j][lane] = down;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int j = wave + W * k;
+            float y = skip * ex[k], du = 0.f, down = 0.f;
+#pragma unroll
+            for (int q = 0; q < W; ++q) y += parts[0][q][j][lane], du += parts[1][q][j][lane], down += parts[2][q][j][lane];
+            if (j < n && p.valid) {
+                const int64_t at = (row0 + t + j) * P.C + p.ch;
+                const float gd = fmaf(du, ex[k], -down) * eslope[k];
+                if (z != nullptr) dz[at] = narrow<T>(egs[k] * y);
+                dx[at] = narrow<T>(fmaf(du, edelta[k], skip * egy[k]));
+                ddt[at] = narrow<T>(gd);
+                dd = fmaf(egy[k], ex[k], dd);
+                dbias += gd;
+            }
+        }
+    }
+    if (p.valid) {
+        for (int t = p.te + wave; t < p.t1; t += W) {
+            const int64_t at = (row0 + t) * P.C + p.ch;
+            dx[at] = ddt[at] = T{0};
+            if (z != nullptr) dz[at] = T{0};
+        }
+        store_states<NS>(P.dw_part + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, dw);
+        if (P.ds_in != nullptr && p.seg == 0) store_states<NS>(P.ds_in + state, g);
+    }
+    __syncthreads();
+    put[wave][lane].x = dd;
+    put[wave][lane].y = dbias;
+    __syncthreads();
+    if (wave == 0 && p.valid) {
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < W; ++q) sum.x += put[q][lane].x, sum.y += put[q][lane].y;
+        const int64_t at = (static_cast<int64_t>(p.seg) * P.B + p.b) * P.C + p.ch;
+        P.vec_part[2 * at] = sum.x;
+        P.vec_part[2 * at + 1] = sum.y;
+    }
+}
+
+// db and dc from the channel tiles' sums; dw, dd and the bias's gradient from the rows' (and segments').  All in a
+// fixed order.  The first bc_blocks workgroups take b and c.
+template <typename T>
+__global__ __launch_bounds__(256) void select_reduce_kernel(SelectArgs P, int64_t bc_blocks) {
+    if (blockIdx.x < bc_blocks) {
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // (row, group, b or c, n)
+        const int64_t n2 = 2 * P.N, rows = P.B * P.T;
+        if (i >= rows * P.G * n2) return;
+        const int64_t e = i % n2, g = i / n2 % P.G, row = i / (n2 * P.G);
+        const int per_group = P.ctiles / static_cast<int>(P.G);
+        const bool live = P.lengths == nullptr || row % P.T < P.lengths[row / P.T];
+        float sum = 0.f;
+        if (live) {
+            const float* at = P.part + (g * per_group * rows + row) * n2 + e;
+            for (int k = 0; k < per_group; ++k) sum += at[k * rows * n2];
+        }
+        T* to = static_cast<T*>(e < P.N ? P.db : P.dc);
+        to[(row * P.G + g) * P.N + e % P.N] = narrow<T>(sum);
+        return;
+    }
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) - bc_blocks) * 256 + threadIdx.x;
+    const int64_t nw = P.C * P.N, rows = P.B * P.nseg;
+    if (i < nw) {
+        float sum = 0.f;
+        for (int64_t r = 0; r < rows; ++r) sum += P.dw_part[r * nw + i];
+        P.dw[i] = sum;
+    } else if (i < nw + 2 * P.C) {
+        const int64_t c = (i - nw) >> 1, k = (i - nw) & 1;
+        float* to = k == 0 ? P.dd : P.ddt_bias;
+        if (to == nullptr) return;
+        float sum = 0.f;
+        for (int64_t r = 0; r < rows; ++r) sum += P.vec_part[2 * (r * P.C + c) + k];
+        to[c] = sum;
+    }
+}
+
+// A few tokens: four states a lane, token by token in registers, the state one trip through memory.
+template <typename T>
+__global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
+    constexpr bool kWide = sizeof(T) == 4;
+    const int lanes = static_cast<int>(P.N) / 4;  // of a channel
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, n = P.B * P.C;
+    const int64_t bc = i / lanes < n ? i / lanes : n - 1;  // spare lanes take part in the sums
+    const int q = static_cast<int>(i % lanes);
+    const bool valid = i / lanes < n;
+    const int64_t b = bc / P.C, ch = bc % P.C, g = ch / (P.C / P.G), GN = P.G * P.N;
+    const T* __restrict__ x = static_cast<const T*>(P.x);
+    const T* __restrict__ dt = static_cast<const T*>(P.dt);
+    const T* __restrict__ z = static_cast<const T*>(P.z);
+    const T* __restrict__ bb = static_cast<const T*>(P.b);
+    const T* __restrict__ cc = static_cast<const T*>(P.c);
+    const int64_t state = bc * P.N + 4 * q;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, w2[4];
+    if (P.s_in != nullptr) load_states<4>(P.s_in + state, true, h);
+    load_states<4>(P.w + ch * P.N + 4 * q, true, w2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) w2[s] = -fminf(w2[s], 2e38f) * kLog2e;
+    const float bias = P.dt_bias != nullptr ? P.dt_bias[ch] : 0.f, skip = P.d != nullptr ? P.d[ch] : 0.f;
+    int64_t len = P.lengths != nullptr ? P.lengths[b] : P.T;
+    len = len < 0 ? 0 : len > P.T ? P.T : len;
+    // (all lanes walk to the longest row's end: the sums over lanes are the whole wave's)
+    for (int64_t t = 0; t < P.T; ++t) {
+        const bool live = t < len;
+        const int64_t row = b * P.T + t, at = row * P.C + ch;
+        float y = 0.f, vx = 0.f, gate = 1.f;
+        if (live) {
+            vx = widen(x[at]);
+            const float delta = step_of<kWide, false>(widen(dt[at]) + bias, P.softplus, nullptr), u = delta * vx;
+            if (z != nullptr) {
+                const float zz = widen(z[at]);
+                gate = zz * sigmoid(zz);
+            }
+            const int64_t from = row * GN + g * P.N + 4 * q;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                h[s] = fmaf(exp2_fast(delta * w2[s]), h[s], widen(bb[from + s]) * u);
+                y = fmaf(widen(cc[from + s]), h[s], y);
+            }
+        }
+        y = sum_lanes(y, lanes);
+        if (valid && q == 0) static_cast<T*>(P.out)[at] = live ? narrow<T>(fmaf(skip, vx, y) * gate) : T{0};
+    }
+    if (valid && P.s_out != nullptr) store_states<4>(P.s_out + state, h);
+}
+
+template <typename T, int NS, int W>
+hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(a.ctiles * a.B * a.nseg)), block(64 * W);
+    switch (mode) {
+        case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkOut>), grid, block, 0, stream, a); break;
+        case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkLocal>), grid, block, 0, stream, a); break;
+        case kWalkAdjoint: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkAdjoint>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((select_grad_kernel<T, NS, W>), grid, block, 0, stream, a); break;
+    }
+    return hipGetLastError();
+}
+
+constexpr int kGrad = 3;
+
+template <typename T>
+hipError_t walk_n(const SelectArgs& a, int mode, hipStream_t stream) {
+    switch (a.N) {
+        case 8: return walk_t<T, 4, 2>(a, mode, stream);
+        case 16: return walk_t<T, 4, 4>(a, mode, stream);
+        case 32: return walk_t<T, 4, 8>(a, mode, stream);
+        default: return walk_t<T, 8, 8>(a, mode, stream);
+    }
+}
+
+hipError_t walk(const SelectArgs& a, int mode, hipStream_t stream) {
+    return a.bf16 ? walk_n<uint16_t>(a, mode, stream) : walk_n<float>(a, mode, stream);
+}
+
+hipError_t chain(const SelectArgs& a, bool reverse, hipStream_t stream) {
+    const int64_t n = a.B * a.C * a.N;
+    hipLaunchKernelGGL(select_chain_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a, reverse);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t* per) {
+    const int64_t whole = (T + kTile - 1) / kTile * kTile, groups = B * ctiles;
+    *per = whole;
+    if (groups <= 0 || groups >= 256 || T < 256) return 1;
+    int64_t n = (1024 + groups - 1) / groups;
+    const int64_t most = T / 128;
+    n = n < most ? n : most;
+    if (n < 3) return 1;
+    const int64_t tiles = (T + kTile - 1) / kTile;
+    *per = (tiles + n - 1) / n * kTile;
+    return (T + *per - 1) / *per;
+}
+
+hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream) {
+    const int64_t n = a.B * a.C * (a.N / 4);
+    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+    if (a.bf16) hipLaunchKernelGGL(select_step_kernel<uint16_t>, grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(select_step_kernel<float>, grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_select_fwd(const SelectArgs& a, hipStream_t stream) {
+    if (a.nseg > 1) {
+        hipError_t e = walk(a, kWalkLocal, stream);
+        if (e == hipSuccess) e = chain(a, false, stream);
+        if (e != hipSuccess) return e;
+    }
+    return walk(a, kWalkOut, stream);
+}
+
+hipError_t launch_select_bwd(const SelectArgs& a, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    if (a.nseg > 1) {
+        e = walk(a, kWalkAdjoint, stream);
+        if (e == hipSuccess) e = chain(a, true, stream);
+        if (e != hipSuccess) return e;
+    }
+    e = walk(a, kGrad, stream);
+    if (e != hipSuccess) return e;
+    const int64_t bc = (a.B * a.T * a.G * 2 * a.N + 255) / 256, rest = (a.C * a.N + 2 * a.C + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(bc + rest));
+    if (a.bf16) hipLaunchKernelGGL(select_reduce_kernel<uint16_t>, grid, dim3(256), 0, stream, a, bc);
+    else hipLaunchKernelGGL(select_reduce_kernel<float>, grid, dim3(256), 0, stream, a, bc);
+    return hipGetLastError();
+}
+
+}  // namespace wkv

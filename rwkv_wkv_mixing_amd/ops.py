@@ -1059,3 +1059,293 @@ def block_join(x, y, pre_w, pre_b=None, *, gate=None, act="sigmoid", post_w=None
                eps=1e-5):
     """Differentiable block_norm (see BlockNormFunction): (x_out, h)."""
     return BlockNormFunction.apply(x, y, pre_w, pre_b, gate, post_w, post_b, scale, act, center, eps)
+
+
+def _conv_inputs(x, weight, bias, lengths, state_in):
+    _need(x, "x", _FLOATS)
+    if x.dim() != 3:
+        raise ValueError("x must have three dimensions [B, T, C]")
+    dev = x.device
+    B, T, C = x.shape
+    _need(weight, "weight", torch.float32, None, dev)
+    if weight.dim() != 2 or weight.shape[1] != C or not 2 <= weight.shape[0] <= 4:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected 2 to 4 taps of ({C},)")
+    K = weight.shape[0]
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (C,), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    if state_in is not None:
+        _need(state_in, "state_in", x.dtype, (B, K - 1, C), dev)
+    return dev, B, T, C, K
+
+
+def conv_forward(x, weight, bias=None, *, act="silu", lengths=None, state_in=None, state_out=None, return_state=False,
+                 out=None, bind=False):
+    """out = act(bias + sum_j weight[j] X[t + j]), a causal filter over time for every channel: x [B, T, C]
+    float32 or bfloat16 (out and the states too), weight [K, C] float32 with K = 2 to 4 taps, the last on the token
+    itself, bias [C] float32 or None; act "none", "sigmoid" or "silu".  X is state_in [B, K - 1, C], the inputs
+    before the first token (None: zeros), and then the row's tokens.
+
+    lengths: None or [B] int32, the tokens of each row (the rest are not read and give zeros).  state_out: tensor
+    to receive the last K - 1 rows of each row's X (may be state_in); with return_state and no state_out one is
+    allocated and the call returns (out, state).  One token and state_out = state_in is a decoding step."""
+    dev, B, T, C, K = _conv_inputs(x, weight, bias, lengths, state_in)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, (B, T, C), dev)
+    if state_out is not None:
+        _need(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
+    elif return_state:
+        state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
+    args = (B, T, C, K, _DT[x.dtype], _act(act), _at(lengths), _at(x), _at(weight), _at(bias), _at(state_in), _at(out),
+            _at(state_out), _stream(dev))
+    return _launch_on(dev, bind, "wkv_conv_forward", L.lib().wkv_conv_forward, args,
+                      (out, state_out) if return_state else out, locals() if bind else None)
+
+
+def conv_backward(x, gout, weight, bias=None, *, act="silu", lengths=None, state_in=None, grad_state_out=None,
+                  need_state_grad=False, workspace=None, bind=False):
+    """Gradients of sum <gout, out> + <grad_state_out, state> for (out, state) = conv_forward(x, weight, bias,
+    ..., return_state=True): (dx, dweight, dbias, dstate_in), each in its input's dtype, dbias None without a bias and
+    dstate_in without need_state_grad."""
+    dev, B, T, C, K = _conv_inputs(x, weight, bias, lengths, state_in)
+    _need(gout, "gout", x.dtype, (B, T, C), dev)
+    if grad_state_out is not None:
+        _need(grad_state_out, "grad_state_out", x.dtype, (B, K - 1, C), dev)
+    dx, dweight = torch.empty_like(x), torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    ds = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if need_state_grad else None
+    lib = L.lib()
+    workspace = _scratch(workspace, int(lib.wkv_conv_backward_workspace_bytes(B, T, C, K)), dev)
+    args = (B, T, C, K, _DT[x.dtype], _act(act), _at(lengths), _at(x), _at(weight), _at(bias), _at(state_in), _at(gout),
+            _at(grad_state_out), _at(dx), _at(dweight), _at(dbias), _at(ds), _at(workspace), _bytes_of(workspace), _stream(dev))
+    return _launch_on(dev, bind, "wkv_conv_backward", lib.wkv_conv_backward, args, (dx, dweight, dbias, ds),
+                      locals() if bind else None)
+
+
+class ConvFunction(torch.autograd.Function):
+    """Autograd wrapper: (out, state) = conv_forward(...); backward through conv_backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state_in, lengths, act):
+        out, state = conv_forward(x, weight, bias, act=act, lengths=lengths, state_in=state_in, return_state=True)
+        ctx.save_for_backward(x, weight, bias, state_in, lengths)
+        ctx.act = act
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gout, gstate):
+        x, weight, bias, state_in, lengths = ctx.saved_tensors
+        dx, dweight, dbias, ds = conv_backward(
+            x, torch.zeros_like(x) if gout is None else gout.contiguous(), weight, bias, act=ctx.act, lengths=lengths,
+            state_in=state_in, grad_state_out=None if gstate is None else gstate.contiguous(),
+            need_state_grad=state_in is not None and ctx.needs_input_grad[3])
+        return dx, dweight, dbias, ds, None, None
+
+
+def short_conv(x, weight, bias=None, state_in=None, lengths=None, act="silu"):
+    """Differentiable short causal convolution: (out, carried inputs after each row's last token) (see conv_forward).
+    Second and forward-mode derivatives are refused."""
+    return ConvFunction.apply(x, weight, bias, state_in, lengths, act)
+
+
+def _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths):
+    _need(x, "x", _FLOATS)
+    if x.dim() != 3:
+        raise ValueError("x must have three dimensions [B, T, C]")
+    dev, ty = x.device, x.dtype
+    B, T, C = shape = x.shape
+    _need(dt, "dt", ty, shape, dev)
+    _need(w, "w", torch.float32, None, dev)
+    if w.dim() != 2 or w.shape[0] != C or w.shape[1] not in (8, 16, 32, 64):
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected ({C}, N) with N 8, 16, 32 or 64")
+    N = w.shape[1]
+    _need(b, "b", ty, None, dev)
+    if b.dim() != 3 or b.shape[0] != B or b.shape[1] != T or b.shape[2] % N or not b.shape[2] or C % (b.shape[2] // N):
+        raise ValueError(f"b has shape {tuple(b.shape)}, expected ({B}, {T}, G {N}) with G a divisor of {C}")
+    _need(c, "c", ty, b.shape, dev)
+    if z is not None:
+        _need(z, "z", ty, shape, dev)
+    for t, n in ((d, "d"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _need(t, n, torch.float32, (C,), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    return dev, B, T, C, b.shape[2] // N, N
+
+
+def select_ckpt_bytes(B: int, T: int, C: int, N: int) -> int:
+    nbytes = int(L.lib().wkv_select_ckpt_bytes(B, T, C, N))
+    if nbytes == 0 and B * T * C != 0:
+        raise ValueError(f"no ckpt for B={B}, T={T}, C={C}, N={N}: these are not sizes of a selective scan")
+    return nbytes
+
+
+def new_select_ckpt(B: int, T: int, C: int, N: int, device) -> torch.Tensor:
+    """Buffer for what select_forward saves for select_backward (opaque bytes)."""
+    return torch.empty(max(select_ckpt_bytes(B, T, C, N), 1), dtype=torch.uint8, device=device)
+
+
+def _select_ckpt(ckpt, B, T, C, N, dev):
+    _need(ckpt, "ckpt", torch.uint8, None, dev)
+    if ckpt.numel() < select_ckpt_bytes(B, T, C, N):
+        raise ValueError(f"ckpt has {ckpt.numel()} bytes, needs {select_ckpt_bytes(B, T, C, N)}")
+
+
+def select_forward(x, dt, w, b, c, *, d=None, z=None, dt_bias=None, softplus=True, lengths=None, state_in=None,
+                   state_out=None, return_state=False, out=None, ckpt=None, workspace=None, split=True, bind=False):
+    """The selective state space scan: out [B, T, C] from x, dt [B, T, C], rates w [C, N] float32 (N 8, 16, 32 or
+    64; decay e^{-delta w}), b, c [B, T, G N] (channel ch reads group ch // (C // G)), d [C] float32, z [B, T, C] and
+    dt_bias [C] float32, the last three or None; x, dt, b, c, z float32 or bfloat16 alike, out too.  Per token
+    delta = softplus(dt + dt_bias) (softplus=False: dt + dt_bias), h = e^{-delta w} h + delta x b,
+    y = <c, h> + d x, out = y silu(z) (y without z).  States and sums are float32.
+
+    lengths: None or [B] int32, the tokens of each row (the rest are not read, leave the state and give zeros).
+    state_in: [B, C, N] float32 or None (zero).  state_out: tensor to receive the state after each row's last token
+    (may be state_in); with return_state and no state_out one is allocated and the call returns (out, state).  ckpt:
+    None or a new_select_ckpt() buffer for select_backward.  With few channels and many tokens the call splits the
+    sequences in time, in a workspace it allocates (or is given); split=False keeps them whole."""
+    dev, B, T, C, G, N = _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, (B, T, C), dev)
+    if state_in is not None:
+        _need(state_in, "state_in", torch.float32, (B, C, N), dev)
+    if state_out is not None:
+        _need(state_out, "state_out", torch.float32, (B, C, N), dev)
+    elif return_state:
+        state_out = torch.empty((B, C, N), dtype=torch.float32, device=dev)
+    if ckpt is not None:
+        _select_ckpt(ckpt, B, T, C, N, dev)
+    lib = L.lib()
+    # (a call of a few tiles of 16 tokens has nothing to split)
+    nws = int(lib.wkv_select_forward_workspace_bytes(B, T, C, G, N)) if split and T > 64 else 0
+    workspace = _scratch(workspace, nws, dev) if nws else None
+    args = (B, T, C, G, N, _DT[x.dtype], L.WKV_SELECT_SOFTPLUS if softplus else 0, _at(lengths), _at(x), _at(dt), _at(w),
+            _at(b), _at(c), _at(d), _at(z), _at(dt_bias), _at(out), _at(state_in), _at(state_out), _at(ckpt), _at(workspace),
+            _bytes_of(workspace) if nws else 0, _stream(dev))
+    return _launch_on(dev, bind, "wkv_select_forward", lib.wkv_select_forward, args,
+                      (out, state_out) if return_state else out, locals() if bind else None)
+
+
+def select_backward(x, dt, w, b, c, go, *, d=None, z=None, dt_bias=None, softplus=True, lengths=None, state_in=None,
+                    grad_state_out=None, need_state_grad=False, ckpt=None, workspace=None, split=True, bind=False):
+    """Gradients of sum <go, out> + <grad_state_out, h_T> for (out, h_T) = select_forward(x, dt, w, b, c, ...,
+    return_state=True): a dict of dx, ddt, dw, db, dc, dd, dz, ddt_bias, dstate_in, each in its input's dtype, None
+    for one that is None (dstate_in without need_state_grad).  go [B, T, C] in x's dtype.  ckpt: None or what the
+    forward wrote.  split as in select_forward.  Sums are float32 in a fixed order."""
+    dev, B, T, C, G, N = _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths)
+    _need(go, "go", x.dtype, (B, T, C), dev)
+    if state_in is not None:
+        _need(state_in, "state_in", torch.float32, (B, C, N), dev)
+    if grad_state_out is not None:
+        _need(grad_state_out, "grad_state_out", torch.float32, (B, C, N), dev)
+    if ckpt is not None:
+        _select_ckpt(ckpt, B, T, C, N, dev)
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    g = dict(dx=like(x), ddt=like(dt), dw=like(w), db=like(b), dc=like(c), dd=like(d), dz=like(z), ddt_bias=like(dt_bias),
+             dstate_in=torch.empty((B, C, N), dtype=torch.float32, device=dev) if need_state_grad else None)
+    lib = L.lib()
+    flags = (1 if ckpt is not None else 0) | (0 if split else 2)  # WKV_WS_HAVE_CKPT, WKV_WS_NO_SPLIT
+    nbytes = int(lib.wkv_select_backward_workspace_bytes(B, T, C, G, N, flags))
+    workspace = _scratch(workspace, nbytes, dev)
+    # without split the call is told only the unsplit size, so it never splits
+    args = (B, T, C, G, N, _DT[x.dtype], L.WKV_SELECT_SOFTPLUS if softplus else 0, _at(lengths), _at(x), _at(dt), _at(w),
+            _at(b), _at(c), _at(d), _at(z), _at(dt_bias), _at(go), _at(state_in), _at(grad_state_out), _at(g["dx"]),
+            _at(g["ddt"]), _at(g["dw"]), _at(g["db"]), _at(g["dc"]), _at(g["dd"]), _at(g["dz"]), _at(g["ddt_bias"]),
+            _at(g["dstate_in"]), _at(ckpt), _at(workspace), _bytes_of(workspace) if split else nbytes, _stream(dev))
+    keep = (x, dt, w, b, c, d, z, dt_bias, lengths, go, state_in, grad_state_out, ckpt, workspace, tuple(g.values()))
+    return _launch_on(dev, bind, "wkv_select_backward", lib.wkv_select_backward, args, g, dict(keep=keep))
+
+
+class SelectFunction(torch.autograd.Function):
+    """Autograd wrapper: (out, state) = select_forward(...); backward through select_backward."""
+
+    @staticmethod
+    def forward(ctx, x, dt, w, b, c, d, z, dt_bias, state_in, lengths, softplus):
+        ckpt = new_select_ckpt(*x.shape, w.shape[-1], x.device)
+        out, state = select_forward(x, dt, w, b, c, d=d, z=z, dt_bias=dt_bias, softplus=softplus, lengths=lengths,
+                                    state_in=state_in, return_state=True, ckpt=ckpt)
+        ctx.save_for_backward(x, dt, w, b, c, d, z, dt_bias, state_in, lengths, ckpt)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, go, gstate):
+        x, dt, w, b, c, d, z, dt_bias, state_in, lengths, ckpt = ctx.saved_tensors
+        g = select_backward(x, dt, w, b, c, torch.zeros_like(x) if go is None else go.contiguous(), d=d, z=z,
+                            dt_bias=dt_bias, softplus=ctx.softplus, lengths=lengths, state_in=state_in,
+                            grad_state_out=None if gstate is None else _on_grid(gstate),
+                            need_state_grad=state_in is not None and ctx.needs_input_grad[8], ckpt=ckpt)
+        return (g["dx"], g["ddt"], g["dw"], g["db"], g["dc"], g["dd"], g["dz"], g["ddt_bias"], g["dstate_in"], None,
+                None)
+
+
+def selective_scan(x, dt, w, b, c, d=None, z=None, dt_bias=None, state_in=None, lengths=None, softplus=True):
+    """Differentiable selective scan: (out, state after each row's last token) (see select_forward).  Without a
+    gradient to take nothing is saved for one, and a few tokens are a decoding step.  Second and forward-mode
+    derivatives are refused."""
+    inputs = (x, dt, w, b, c, d, z, dt_bias, state_in)
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)) and not _has_tangent(inputs):
+        return select_forward(x, dt, w, b, c, d=d, z=z, dt_bias=dt_bias, softplus=softplus, lengths=lengths,
+                              state_in=state_in, return_state=True)
+    return SelectFunction.apply(x, dt, w, b, c, d, z, dt_bias, state_in, lengths, softplus)
+
+
+def _clip_tables(grads, out):
+    """The tensors' device, and host arrays of their addresses, sizes and dtypes."""
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    dev = None
+    for i, g in enumerate(grads):
+        _need(g, f"grads[{i}]", _FLOATS, None, dev)
+        dev = g.device
+    n = len(grads)
+    outs = None
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != n:
+            raise ValueError(f"out has {len(out)} tensors for {n} gradients")
+        for i, (o, g) in enumerate(zip(out, grads)):
+            _need(o, f"out[{i}]", g.dtype, g.shape, dev)
+        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    return (dev, grads, out, n, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), outs,
+            (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int * n)(*[_DT[g.dtype] for g in grads]))
+
+
+def grad_norm(grads, *, norm=None, workspace=None, bind=False):
+    """The norm of all the gradients together, sqrt of the sum of all squares: a float32 tensor of no dimensions on their
+    device (norm, when given, receives it).  grads: a tensor or a list of tensors of any shapes, float32 and
+    bfloat16.  Squares are added up in float64, in a fixed order; nothing is copied to the host."""
+    dev, grads, _, n, ins, _, sizes, types = _clip_tables(grads, None)
+    if n == 0:
+        raise ValueError("grads is empty: there is no device to return a norm on")
+    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
+    _need(norm, "norm", torch.float32, (), dev)
+    lib = L.lib()
+    workspace = _scratch(workspace, int(lib.wkv_clip_workspace_bytes(n)), dev)
+    args = (n, ins, sizes, types, _at(norm), _at(workspace), _bytes_of(workspace), _stream(dev))
+    return _launch_on(dev, bind, "wkv_grad_norm", lib.wkv_grad_norm, args, norm, dict(keep=(grads, norm, workspace)))
+
+
+def clip_gradients(grads, max_norm, *, eps=1e-6, out=None, norm=None, workspace=None, bind=False):
+    """Scales the gradients by min(1, max_norm / (norm + eps)), norm that of all of them together (see grad_norm), in place
+    or into out (a tensor for each, of its shape and dtype), and returns the norm before: a float32 tensor of no
+    dimensions.  A norm that is infinite or not a number makes the gradients zeros or not numbers.  No gradient
+    may be listed twice in place."""
+    dev, grads, out, n, ins, outs, sizes, types = _clip_tables(grads, out)
+    if n == 0:
+        raise ValueError("grads is empty: there is no device to return a norm on")
+    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
+    _need(norm, "norm", torch.float32, (), dev)
+    lib = L.lib()
+    workspace = _scratch(workspace, int(lib.wkv_clip_workspace_bytes(n)), dev)
+    args = (n, ins, outs, sizes, types, max_norm, eps, _at(norm), _at(workspace), _bytes_of(workspace), _stream(dev))
+    return _launch_on(dev, bind, "wkv_clip_gradients", lib.wkv_clip_gradients, args, norm,
+                      dict(keep=(grads, out, norm, workspace)))

@@ -1,0 +1,118 @@
+"""The short causal convolution against the float64 oracle.
+
+Bounds: u = 2^-24.  pre is a sum of K + 1 terms, within (K + 2)u of their sizes P.  |act'| <= 1.1 and |act''| <= 0.5, and the
+sigmoid is good to 4u + |pre| u (the rounding of its exponent), so act(pre) is within 1.1 (K + 2)u P + 6u P + 4u and act'(pre)
+within 0.5 (K + 2)u P + 6u P + 8u: both below (2 K + 12)u (1 + P).  Gradients are sums of n terms g X or weight g: (n + 4)u of
+their sizes, plus that error of act' times the sizes of the other factors, which is the oracle on sizes with act' = 1 (act
+"none").  bf16 results 2^-8 of themselves on top."""
+import numpy as np
+import pytest
+import torch
+
+from oracle.select_ref import conv_ref
+from rwkv_wkv_mixing_amd import ops as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+DTYPES, IDS = [BF, F32], ["bf16", "f32"]
+U = 2.0 ** -24
+
+
+def draw(B, T, C, K, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed + 7 * T + 100 * C + K)
+    rn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    return dict(x=rn(B, T, C).to(dtype), weight=rn(K, C), bias=rn(C), state_in=rn(B, K - 1, C).to(dtype), go=rn(B, T, C).to(dtype),
+                gstate=rn(B, K - 1, C).to(dtype))
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def within(name, got, want, bound):
+    rel = 2.0 ** -8 if got.dtype == BF else 2.0 ** -24
+    got = host(got)
+    assert got.shape == want.shape and np.isfinite(got).all(), name
+    bound = bound * (1 + rel) + rel * np.abs(want) + 1e-37
+    worst = float((np.abs(got - want) / bound).max(initial=0.0))
+    print(f"  {name}: worst error / bound {worst:.3f}", flush=True)
+    assert worst <= 1.0, (name, worst)
+
+
+def check_all(p, act="silu", lengths=None, state=True, bias=True, clean=None):
+    """clean: the oracle's inputs, where they differ."""
+    B, T, C = p["x"].shape
+    K = p["weight"].shape[0]
+    q = {k: v.to(DEV) for k, v in p.items()}
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    bq, sq, gq = q["bias"] if bias else None, q["state_in"] if state else None, q["gstate"] if state else None
+    out, s1 = O.conv_forward(q["x"], q["weight"], bq, act=act, lengths=ln, state_in=sq, return_state=True)
+    dx, dweight, dbias, ds = O.conv_backward(q["x"], q["go"], q["weight"], bq, act=act, lengths=ln, state_in=sq, grad_state_out=gq,
+                                             need_state_grad=True)
+    torch.cuda.synchronize()
+    h = {k: host(v) for k, v in (clean or p).items()}
+    args = (h["x"], h["weight"], h["bias"] if bias else None)
+    kw = dict(lengths=lengths, state_in=h["state_in"] if state else None, gout=h["go"], gstate=h["gstate"] if state else None)
+    r, m = (conv_ref(*args, act=act, mag=k, **kw) for k in (False, True))
+    P = 1.0 + r["pre"].max()  # (one size for all the sums: the largest)
+    flat = conv_ref(*args, act="none", mag=True, **kw)  # act' = 1
+    a = (2 * K + 12) * U * P if act != "none" else 0.0
+    within("out", out, r["out"], (K + 2) * U * r["pre"] + a)
+    assert np.array_equal(host(s1), r["state"])
+    n = B * T + 8
+    for name, got in (("dx", dx), ("dweight", dweight), ("dbias", dbias), ("dstate", ds)):
+        if got is not None:
+            k = K + 8 if name in ("dx", "dstate") else n
+            within(name, got, r[name], k * U * m[name] + a * flat[name])
+    return out, s1, dx, dweight, dbias, ds
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("B,T,C", [(1, 1, 1), (3, 1, 64), (2, 2, 5), (2, 3, 260), (1, 17, 1001), (3, 130, 68), (2, 333, 64)])
+def test_conv(B, T, C, K, dtype):
+    check_all(draw(B, T, C, K, dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
+def test_options(act, dtype):
+    p = draw(2, 40, 68, 4, dtype)
+    check_all(p, act=act)
+    check_all(p, act=act, state=False, bias=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("C", [68, 63])
+@pytest.mark.parametrize("lengths", [[0, 40, 16], [1, 2, 3], [39, 33, 38]], ids=["empty", "short", "ragged"])
+def test_ragged(lengths, C, dtype):
+    """Rows behind a length are not read (they hold NaN), and give zeros; a row shorter than the filter hands on what it was given."""
+    p = draw(3, 40, C, 4, dtype)
+    clean = {k: v.clone() for k, v in p.items()}
+    for b, n in enumerate(lengths):
+        for k in ("x", "go"):
+            p[k][b, n:] = float("nan")
+            clean[k][b, n:] = 0
+    out, s1, dx, *_ = check_all(p, lengths=lengths, clean=clean)
+    for b, n in enumerate(lengths):
+        assert not bool(out[b, n:].any()) and not bool(dx[b, n:].any())
+        if n == 0:
+            assert torch.equal(s1[b].cpu(), p["state_in"][b])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("C", [64, 7])
+def test_decode_in_place_is_the_whole_sequence(C, dtype):
+    p = {k: v.to(DEV) for k, v in draw(3, 9, C, 4, dtype).items()}
+    whole, s1 = O.conv_forward(p["x"], p["weight"], p["bias"], state_in=p["state_in"], return_state=True)
+    state = p["state_in"].clone()
+    for t in range(9):
+        o = O.conv_forward(p["x"][:, t:t + 1].contiguous(), p["weight"], p["bias"], state_in=state, state_out=state)
+        assert torch.equal(o[:, 0], whole[:, t])
+    assert torch.equal(state, s1)
+    state = p["state_in"].clone()  # many workgroups, the carried inputs in place
+    long = torch.randn(3, 700, C, device=DEV).to(dtype)
+    a, sa = O.conv_forward(long, p["weight"], p["bias"], state_in=state.clone(), return_state=True)
+    b = O.conv_forward(long, p["weight"], p["bias"], state_in=state, state_out=state)
+    assert torch.equal(a, b) and torch.equal(sa, state)

@@ -1,0 +1,172 @@
+"""The selective scan against the float64 oracle: outputs, states and every gradient.
+
+Bounds, counted in the sizes of the terms (the oracle on sizes, M).  u = 2^-24 is half a step of float32.  A term that
+n tokens have carried has taken n multiply-adds (u each) and n decays e^{-delta w}: each an exponential (2u) of
+delta w log2 e, where delta, good to 8u (softplus: the exponential's, the polynomial's and the sum's), the rate and the
+products add 11u of the exponent; exponents of a term add up to at most its whole decay, and E e^{-E} < 0.4, so they
+cost it 11u at most times 0.4 of what was written.  A term's other factors (delta, x, b, c, the gate's sigmoid: 8u + 4u +
+6u), and the sums over at most 64 states, over tokens and over channels add (64 + T + C)u.  With bf16 outputs, 2^-8 of the
+result on top.  In all: (3 T + C + 128)u M (2^-8 |result| more in bf16); a gradient's chain runs through both directions, twice that."""
+import numpy as np
+import pytest
+import torch
+
+from oracle.select_ref import select_ref
+from rwkv_wkv_mixing_amd import ops as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+DTYPES, IDS = [BF, F32], ["bf16", "f32"]
+SEQ = ("x", "dt", "b", "c", "z")
+GRADS = dict(x="dx", dt="ddt", w="dw", b="db", c="dc", d="dd", z="dz", dt_bias="ddt_bias")
+
+
+def draw(B, T, C, G, N, dtype, seed=0, slow=False):
+    """Host tensors as a layer has them: rates 1 .. N, steps from 0.001 to 0.1 and beyond; slow: almost no decay."""
+    g = torch.Generator().manual_seed(seed + 7 * T + 1000 * C + N)
+    rn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    p = dict(x=rn(B, T, C), dt=rn(B, T, C), b=rn(B, T, G * N), c=rn(B, T, G * N), z=rn(B, T, C))
+    p = {k: v.to(dtype) for k, v in p.items()}
+    p["w"] = torch.arange(1, N + 1) * torch.exp(0.2 * rn(C, N)) * (1e-4 if slow else 1.0)
+    p["d"], p["dt_bias"] = rn(C), -4.0 + 1.5 * rn(C)
+    p["state_in"], p["go"], p["gstate"] = rn(B, C, N), rn(B, T, C).to(dtype), rn(B, C, N)
+    return p
+
+
+def gpu(p):
+    return {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+
+
+def host(p):
+    return {k: v.double().numpy() if isinstance(v, torch.Tensor) and v.is_floating_point() else v for k, v in p.items()}
+
+
+def check(name, got, want, mag, T, C, twice=False):
+    rel = 2.0 ** -8 if got.dtype == BF else 0.0
+    got = got.double().cpu().numpy()
+    u = (3 * T + C + 128) * 2.0 ** -24 * (2 if twice else 1)
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    assert np.isfinite(got).all(), name
+    bound = u * mag * (1 + rel) + rel * np.abs(want) + 1e-30
+    worst = float((np.abs(got - want) / bound).max(initial=0.0))
+    norm = float(np.linalg.norm(got - want) / max(np.linalg.norm(want), 1e-30))
+    print(f"  {name}: worst error / bound {worst:.3f}, error of the norm {norm:.2e}", flush=True)
+    assert worst <= 1.0, (name, worst)
+
+
+def run(p, lengths=None, softplus=True, saved=True, split=True, state=True, options=("d", "z", "dt_bias")):
+    """The calls' outputs and gradients, and the oracle's with their sizes."""
+    B, T, C = p["x"].shape
+    N = p["w"].shape[1]
+    opt = {k: p[k] if k in options else None for k in ("d", "z", "dt_bias")}
+    q = gpu({**p, **opt})
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    s_in, gs = (q["state_in"], q["gstate"]) if state else (None, None)
+    args = [q[k] for k in ("x", "dt", "w", "b", "c")]
+    kw = dict(d=q["d"], z=q["z"], dt_bias=q["dt_bias"], softplus=softplus, lengths=ln, state_in=s_in, split=split)
+    ckpt = O.new_select_ckpt(B, T, C, N, DEV) if saved else None
+    out, s1 = O.select_forward(*args, return_state=True, ckpt=ckpt, **kw)
+    g = O.select_backward(*args, q["go"], grad_state_out=gs, need_state_grad=True, ckpt=ckpt, **kw)
+    torch.cuda.synchronize()
+    h = host({**p, **opt})
+    ref = [select_ref(*(h[k] for k in ("x", "dt", "w", "b", "c")), d=h["d"], z=h["z"], dt_bias=h["dt_bias"], softplus=softplus,
+                      lengths=lengths, state_in=h["state_in"] if state else None, go=h["go"],
+                      gstate=h["gstate"] if state else None, mag=m) for m in (False, True)]
+    return out, s1, g, ref
+
+
+def check_all(p, **kw):
+    B, T, C = p["x"].shape
+    out, s1, g, (r, m) = run(p, **kw)
+    check("out", out, r["out"], m["out"], T, C)
+    check("state", s1, r["state"], m["state"], T, C)
+    for name in [*GRADS.values(), "dstate_in"]:
+        if g[name] is not None:
+            key = "dstate" if name == "dstate_in" else name
+            check(name, g[name], r[key], m[key], B * T, C, twice=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("B,T,C,G,N", [(2, 1, 5, 1, 8), (1, 15, 64, 1, 16), (2, 16, 64, 1, 16), (3, 17, 65, 1, 16), (2, 33, 130, 2, 8),
+                                       (1, 40, 66, 3, 32), (2, 50, 70, 1, 64), (1, 100, 1, 1, 16)])
+def test_select(B, T, C, G, N, dtype):
+    check_all(draw(B, T, C, G, N, dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("lengths", [[0, 40, 16], [1, 15, 33]], ids=["empty", "ragged"])
+def test_ragged(lengths, dtype):
+    """Rows behind a length are not read (they hold NaN), and give zeros."""
+    p = draw(3, 40, 70, 2, 16, dtype)
+    clean = {k: v.clone() for k, v in p.items()}
+    for b, n in enumerate(lengths):
+        for k in SEQ + ("go",):
+            p[k][b, n:] = float("nan")
+            clean[k][b, n:] = 0
+    out, s1, g, _ = run(p, lengths=lengths)
+    _, _, _, (r, m) = run(clean, lengths=lengths)
+    check("out", out, r["out"], m["out"], 40, 70)
+    check("state", s1, r["state"], m["state"], 40, 70)
+    for name in GRADS.values():
+        check(name, g[name], r[name], m[name], 120, 70, twice=True)
+    for b, n in enumerate(lengths):
+        for t in (out, g["dx"], g["ddt"], g["dz"], g["db"], g["dc"]):
+            assert not bool(t[b, n:].any())
+        if n == 0:
+            assert torch.equal(s1[b].cpu(), p["state_in"][b]) and torch.equal(g["dstate_in"][b].cpu(), p["gstate"][b])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("options", [(), ("d",), ("z",), ("dt_bias",)], ids=["none", "d", "z", "bias"])
+def test_options(options, dtype):
+    check_all(draw(2, 37, 66, 1, 16, dtype), options=options, state=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_without_softplus(dtype):
+    p = draw(2, 37, 66, 1, 16, dtype)
+    p["dt"], p["dt_bias"] = (p["dt"].abs() * 0.1).to(dtype), p["dt_bias"].abs() * 0.02
+    check_all(p, softplus=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_slow_decay(dtype):
+    check_all(draw(2, 200, 64, 1, 16, dtype, slow=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,lengths,N", [(640, None, 16), (777, [777, 300], 8), (700, [5, 0], 32), (1500, [1500, 1493], 16)])
+@pytest.mark.parametrize("saved", [True, False], ids=["ckpt", "recomputed"])
+def test_split_in_time(T, lengths, N, dtype, saved):
+    """Few channels and many tokens: segments at once, against the oracle."""
+    assert O.L.lib().wkv_select_forward_workspace_bytes(2, T, 70, 1, N) > 0
+    check_all(draw(2, T, 70, 1, N, dtype), lengths=lengths, saved=saved)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_recomputed_states_give_the_same_bits(dtype):
+    p = draw(2, 100, 70, 1, 16, dtype)
+    (*_, a, _), (*_, b, _) = (run(p, saved=saved) for saved in (True, False))
+    for name in a:
+        assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_decode(T, N, dtype):
+    """A few tokens with the state in place, ragged; then one token after the other to the same states."""
+    B, C, G = 3, 21, 3
+    p = draw(B, T, C, G, N, dtype)
+    lengths = [T, 0, T - 1]
+    q = gpu(p)
+    ln = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    state = q["state_in"].clone()
+    out = O.select_forward(*(q[k] for k in ("x", "dt", "w", "b", "c")), d=q["d"], z=q["z"], dt_bias=q["dt_bias"], lengths=ln,
+                           state_in=state, state_out=state)
+    h = host(p)
+    r, m = (select_ref(*(h[k] for k in ("x", "dt", "w", "b", "c")), d=h["d"], z=h["z"], dt_bias=h["dt_bias"], lengths=lengths,
+                       state_in=h["state_in"], mag=k) for k in (False, True))
+    check("out", out, r["out"], m["out"], T, C)
+    check("state", state, r["state"], m["state"], T, C)
