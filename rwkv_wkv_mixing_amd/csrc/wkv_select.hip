@@ -6,12 +6,14 @@
 // vector units, which is what bounds it (a channel-token of N = 16 moves 8 bytes in bf16 and takes some 130 lane
 // instructions, 0.1 us a million at this card's rate against 0.04 for the bytes).
 //
-// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, NS a wave: b_t and c_t are then
-// the same for a whole wave and come in through scalar loads, and only delta, the written value and the waves' parts of
-// y pass through LDS.  Tiles of 16 tokens: the threads first work out delta and what is written for (token, channel)
+// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, NS a wave: a wave's b_t and
+// c_t are then the same for all its lanes and reach its multiplications as lane broadcasts, and only delta, the written
+// value and the waves' parts of y pass through LDS.  Tiles of 16 tokens: the threads first work out delta and what is written for (token, channel)
 // pairs, one each; then every wave walks the tile; then the threads add the waves' parts, gate and store.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "wkv_lanes.h"
 #include "wkv_launch.h"
@@ -72,31 +74,49 @@ __device__ __forceinline__ float step_of(float raw, bool softplus, float* grad) 
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e)); }
 
-// NS neighbouring values of a row of b or c for a whole wave, through the scalar cache (the inputs are not written
-// while the kernel runs); zeros for a token that is none.
+// Calls f with std::integral_constant<int, 0> .. <int, N - 1>: the lanes of a broadcast are part of the instruction.
+template <int N, class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+// The values of lane K of every row of 16 lanes, to the row: folded into the multiplication that takes them.
+template <int K>
+__device__ __forceinline__ float row_lane(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + K, 0xf, 0xf, true));  // row_newbcast
+}
+
+// A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
+// NS registers, token by token, so that each of them is one lane of one register.
 template <typename T, int NS>
-struct Uniform;
-template <int NS>
-struct Uniform<float, NS> {
-    static __device__ __forceinline__ void load(const float* p, bool live, float (&f)[NS]) {
-        typedef const __attribute__((address_space(4))) uint32_t* Scalar;
-        const Scalar q = (Scalar)(p);
+struct Row {
+    T raw[NS];
+    float f[NS];
+    // tokens t .. t + kTile - 1 of a row with stride GN; those from te on are not read
+    __device__ __forceinline__ void fetch(const T* p, int t, int te, int64_t GN, int lane) {
+        constexpr int kPer = kTile / NS;  // tokens a register
+        const int s = lane % NS, j = (lane & 15) / NS;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) f[i] = __uint_as_float(live ? q[i] : 0u);
-    }
-};
-template <int NS>
-struct Uniform<uint16_t, NS> {
-    static __device__ __forceinline__ void load(const uint16_t* p, bool live, float (&f)[NS]) {
-        typedef const __attribute__((address_space(4))) uint32_t* Scalar;
-        const Scalar q = (Scalar)(p);
-#pragma unroll
-        for (int i = 0; i < NS / 2; ++i) {
-            const uint32_t v = live ? q[i] : 0u;
-            f[2 * i] = __uint_as_float(v << 16);
-            f[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+        for (int r = 0; r < NS; ++r) {
+            const int at = t + r * kPer + j;
+            raw[r] = at < te ? p[at * GN + s] : T{0};
         }
     }
+    __device__ __forceinline__ void ready() {
+#pragma unroll
+        for (int r = 0; r < NS; ++r) f[r] = widen(raw[r]);
+    }
+    // The compiler is to broadcast again rather than keep what it broadcast before.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int r = 0; r < NS; ++r) asm volatile("" : "+v"(f[r]));
+    }
+    template <int J, int S>
+    __device__ __forceinline__ float get() const { return row_lane<(J * NS + S) % 16>(f[(J * NS + S) / 16]); }
 };
 
 template <int NS>
@@ -116,7 +136,8 @@ __device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
 
 // Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
 struct Place {
-    int64_t b, ch;       // batch row; the lane's channel (a spare lane's: the last one of its group)
+    int64_t b;           // batch row
+    uint32_t ch;         // the lane's channel (a spare lane's: the last one of its group)
     int ct, g, seg;
     int t0, t1, te;      // rows t0 .. t1 - 1 of which those before te are tokens
     bool valid;          // not a spare lane
@@ -132,9 +153,9 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
     p.seg = blk / static_cast<uint32_t>(P.B);
     const int per_group = P.ctiles / static_cast<int>(P.G);
     p.g = p.ct / per_group;
-    const int64_t width = P.C / P.G, c = static_cast<int64_t>(p.ct % per_group) * 64 + lane;
+    const int width = static_cast<int>(P.C / P.G), c = (p.ct % per_group) * 64 + lane;
     p.valid = c < width;
-    p.ch = p.g * width + (p.valid ? c : width - 1);
+    p.ch = static_cast<uint32_t>(p.g * width + (p.valid ? c : width - 1));
     const int64_t T = P.T, first = p.seg * P.seg_len, last = first + P.seg_len;
     int64_t len = P.lengths != nullptr ? P.lengths[p.b] : T;
     len = len < 0 ? 0 : len > T ? T : len;
@@ -162,14 +183,14 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const T* __restrict__ go = static_cast<const T*>(P.go);
     T* __restrict__ out = static_cast<T*>(P.out);
     const int64_t row0 = p.b * P.T, GN = P.G * N;
-    const T* bc = static_cast<const T*>(kAdj ? P.c : P.b) + (row0 * GN + p.g * N + wave * NS);
-    const T* cc = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
+    const T* bt = static_cast<const T*>(kAdj ? P.c : P.b) + (row0 * GN + p.g * N + wave * NS);
+    const T* ct = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
     const float bias = P.dt_bias != nullptr ? P.dt_bias[p.ch] : 0.f;
     const float skip = P.d != nullptr ? P.d[p.ch] : 0.f;
     const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
 
     float w2[NS], h[NS];
-    load_states<NS>(P.w + p.ch * N + wave * NS, true, w2);
+    load_states<NS>(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w2);
     // (a rate of infinity is held finite, so that a step of zero keeps the state)
 #pragma unroll
     for (int i = 0; i < NS; ++i) w2[i] = -fminf(w2[i], 2e38f) * kLog2e, h[i] = 0.f;
@@ -179,42 +200,43 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         else if (P.s_in != nullptr) load_states<NS>(P.s_in + state, p.valid, h);
     }
 
-    // inputs of the tile after the next, of the next and of this one: the raw values, then what the epilogue needs
-    T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
-    float ex[2][kEach], ez[2][kEach];
+    // The inputs of the tile after this one on their way while this one is walked; of this one, what its outputs need.
+    T rx[kEach], rd[kEach], rz[kEach];
+    float ex[kEach], ez[kEach], nx[kEach], nz[kEach];
+    Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
-    const auto fetch = [&](int i) {
-        const int t = tile_at(i) + wave;
+    const auto fetch = [&](int i) {  // (behind the last token: that one again)
+        const int t = tile_at(i < ntiles ? i : ntiles - 1) + wave;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            rx[k] = rd[k] = rz[k] = rg[k] = T{0};
-            if (i < ntiles && t + W * k < p.te) {
-                const int64_t at = (row0 + t + W * k) * P.C + p.ch;
-                rd[k] = dt[at];
-                if constexpr (kAdj) rg[k] = go[at];
-                else rx[k] = x[at];
-                if ((kOut || kAdj) && z != nullptr) rz[k] = z[at];
-            }
+            const int at = t + W * k < p.te ? t + W * k : p.te - 1;
+            const int64_t row = (row0 + at) * P.C;
+            rd[k] = (dt + row)[p.ch];
+            rx[k] = ((kAdj ? go : x) + row)[p.ch];
+            rz[k] = T{0};
+            if ((kOut || kAdj) && z != nullptr) rz[k] = (z + row)[p.ch];
         }
+    };
+    const auto fetch_bc = [&](int i) {
+        const int t = tile_at(i < ntiles ? i : ntiles - 1);
+        b.fetch(bt, t, p.te, GN, lane);
+        if constexpr (kOut) c.fetch(ct, t, p.te, GN, lane);
     };
     float total = 0.f;  // of delta
     const auto stage = [&](int i) {
-        if (i >= ntiles) return;
         const int t = tile_at(i) + wave;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const bool live = t + W * k < p.te && p.valid;
-            const float raw = widen(rd[k]) + bias;
-            float delta = step_of<kWide, false>(raw, P.softplus, nullptr);
-            float v = kAdj ? widen(rg[k]) : widen(rx[k]);
+            const bool live = i < ntiles && t + W * k < p.te && p.valid;
+            float delta = step_of<kWide, false>(widen(rd[k]) + bias, P.softplus, nullptr), v = widen(rx[k]);
             if constexpr (kAdj) {
                 const float zz = widen(rz[k]);
                 if (z != nullptr) v *= zz * sigmoid(zz);
             } else {
                 if constexpr (kOut) {
                     const float zz = widen(rz[k]);
-                    ex[i & 1][k] = skip * v;
-                    ez[i & 1][k] = z != nullptr ? zz * sigmoid(zz) : 1.f;
+                    nx[k] = skip * v;
+                    nz[k] = z != nullptr ? zz * sigmoid(zz) : 1.f;
                 }
                 v *= delta;
             }
@@ -224,39 +246,41 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         }
     };
 
-    fetch(0);
-    stage(0);
-    fetch(1);
-    __syncthreads();
+    if (ntiles > 0) {
+        fetch(0);
+        fetch_bc(0);
+        stage(0);
+        fetch(1);
+        __syncthreads();
+    }
     for (int i = 0; i < ntiles; ++i) {
-        const int t = tile_at(i);
+        const int t = tile_at(i), n = p.te - t;
         if constexpr (kOut) {
             if (P.ckpt != nullptr && p.valid)
                 store_states<NS>(P.ckpt + (((p.b * P.tiles + t / kTile) * W + wave) * P.C + p.ch) * NS, h);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) ex[k] = nx[k], ez[k] = nz[k];
         }
-        const T* bt = bc + t * GN;
-        const T* ct = cc + t * GN;
-        const int n = p.te - t;
-#pragma unroll
-        for (int jj = 0; jj < kTile; ++jj) {
-            const int j = kAdj ? kTile - 1 - jj : jj;
-            const bool live = j < n;
-            const float2 dv = put[i & 1][j][lane];
-            float b[NS], c[NS], y = 0.f;
-            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
-            if constexpr (kOut) Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
+        b.ready();
+        if constexpr (kOut) c.ready();
+        fetch_bc(i + 1);
+        const float2(&now)[kTile][64] = put[i & 1];
+        each<kTile>([&](auto jj) {
+            constexpr int j = kAdj ? kTile - 1 - decltype(jj)::value : decltype(jj)::value;
+            const float2 dv = now[j][lane];
+            float y = 0.f;
+            each<NS>([&](auto ss) {
+                constexpr int s = decltype(ss)::value;
                 const float a = exp2_fast(dv.x * w2[s]);
                 if constexpr (kAdj) {
-                    h[s] = a * fmaf(b[s], dv.y, h[s]);
+                    h[s] = a * fmaf(b.template get<j, s>(), dv.y, h[s]);
                 } else {
-                    h[s] = fmaf(a, h[s], b[s] * dv.y);
-                    if constexpr (kOut) y = fmaf(c[s], h[s], y);
+                    h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
+                    if constexpr (kOut) y = fmaf(c.template get<j, s>(), h[s], y);
                 }
-            }
+            });
             if constexpr (kOut) parts[i & 1][wave][j][lane] = y;
-        }
+        });
         stage(i + 1);
         __syncthreads();
         fetch(i + 2);
@@ -264,10 +288,10 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
 #pragma unroll
             for (int k = 0; k < kEach; ++k) {
                 const int j = wave + W * k;
-                float y = ex[i & 1][k];
+                float y = ex[k];
 #pragma unroll
                 for (int q = 0; q < W; ++q) y += parts[i & 1][q][j][lane];
-                if (j < n && p.valid && out != nullptr) out[(row0 + t + j) * P.C + p.ch] = narrow<T>(y * ez[i & 1][k]);
+                if (j < n && p.valid && out != nullptr) (out + (row0 + t + j) * P.C)[p.ch] = narrow<T>(y * ez[k]);
             }
         }
     }
@@ -319,8 +343,8 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;
-    constexpr bool kWide = sizeof(T) == 4, kKeep = NS <= 4;  // decays kept, not worked out again
-    __shared__ float4 put[kTile][64];           // delta, the written value, the gradient of y
+    constexpr bool kWide = sizeof(T) == 4;
+    __shared__ float4 put[kTile][64];           // delta, the written value, the gradient of y, x
     __shared__ float parts[3][W][kTile][64];    // the waves' parts of y, du and -ddelta
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Place p = place_of(P, lane);
@@ -332,14 +356,14 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     T* __restrict__ ddt = static_cast<T*>(P.ddt);
     T* __restrict__ dz = static_cast<T*>(P.dz);
     const int64_t row0 = p.b * P.T, GN = P.G * N;
-    const T* bc = static_cast<const T*>(P.b) + (row0 * GN + p.g * N + wave * NS);
-    const T* cc = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
+    const T* bt = static_cast<const T*>(P.b) + (row0 * GN + p.g * N + wave * NS);
+    const T* ct = static_cast<const T*>(P.c) + (row0 * GN + p.g * N + wave * NS);
     const float bias = P.dt_bias != nullptr ? P.dt_bias[p.ch] : 0.f;
     const float skip = P.d != nullptr ? P.d[p.ch] : 0.f;
     const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
 
     float w1[NS], w2[NS], g[NS], dw[NS], first[NS];
-    load_states<NS>(P.w + p.ch * N + wave * NS, true, w1);
+    load_states<NS>(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w1);
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     const float* from = P.nseg > 1 ? P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N : P.ds_out;
 #pragma unroll
@@ -347,135 +371,129 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     if (from != nullptr) load_states<NS>(from + state, p.valid, g);
 
     T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
+    Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
-    const auto fetch = [&](int i) {
-        if (i < 0) return;
-        const int t = tile_at(i) + wave;
+    const auto fetch = [&](int i) {  // (behind the last token: that one again; before the first tile: nothing new)
+        const int tile = tile_at(i > 0 ? i : 0), t = tile + wave;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            rx[k] = rd[k] = rz[k] = rg[k] = T{0};
-            if (t + W * k < p.te) {
-                const int64_t at = (row0 + t + W * k) * P.C + p.ch;
-                rd[k] = dt[at];
-                rx[k] = x[at];
-                rg[k] = go[at];
-                if (z != nullptr) rz[k] = z[at];
-            }
+            const int at = t + W * k < p.te ? t + W * k : p.te - 1;
+            const int64_t row = (row0 + at) * P.C;
+            rd[k] = (dt + row)[p.ch];
+            rx[k] = (x + row)[p.ch];
+            rg[k] = (go + row)[p.ch];
+            rz[k] = T{0};
+            if (z != nullptr) rz[k] = (z + row)[p.ch];
         }
-        load_states<NS>(P.saved + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
+        load_states<NS>(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
+        b.fetch(bt, tile, p.te, GN, lane);
+        c.fetch(ct, tile, p.te, GN, lane);
     };
     float dd = 0.f, dbias = 0.f;
-    fetch(ntiles - 1);
+    if (ntiles > 0) fetch(ntiles - 1);
     for (int i = ntiles - 1; i >= 0; --i) {
         const int t = tile_at(i), n = p.te - t;
-        float ex[kEach], egy[kEach], egs[kEach], edelta[kEach], eslope[kEach];
+        float egs[kEach], eslope[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const bool live = wave + W * k < n && p.valid;
             const float delta = step_of<kWide, true>(widen(rd[k]) + bias, P.softplus, &eslope[k]);
             const float zz = widen(rz[k]), gg = widen(rg[k]), sg = sigmoid(zz);
-            ex[k] = widen(rx[k]);
-            edelta[k] = delta;
-            egy[k] = z != nullptr ? gg * (zz * sg) : gg;
+            const float xx = widen(rx[k]), gy = z != nullptr ? gg * (zz * sg) : gg;
             egs[k] = gg * (sg * fmaf(zz, 1.f - sg, 1.f));
-            put[wave + W * k][lane] = live ? make_float4(delta, delta * ex[k], egy[k], 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            put[wave + W * k][lane] = live ? make_float4(delta, delta * xx, gy, xx) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float h[kTile + 1][NS], a[kKeep ? kTile : 1][NS];
+        float before[NS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) h[0][s] = first[s];
+        for (int s = 0; s < NS; ++s) before[s] = first[s];
+        b.ready();
+        c.ready();
         __syncthreads();
         fetch(i - 1);
-        const T* bt = bc + t * GN;
-        const T* ct = cc + t * GN;
+        each<NS / 4>([&](auto qq) {  // four states at a time
+            constexpr int q = decltype(qq)::value;
+            float h[kTile + 1][4], a[kTile][4];
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) {
-            const bool live = j < n;
-            const float4 v = put[j][lane];
-            float b[NS], c[NS], y = 0.f;
-            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
-            Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const float e = exp2_fast(v.x * w2[s]);
-                if constexpr (kKeep) a[j][s] = e;
-                h[j + 1][s] = fmaf(e, h[j][s], b[s] * v.y);
-                y = fmaf(c[s], h[j + 1][s], y);
-            }
-            parts[0][wave][j][lane] = y;
-        }
-        float lanes8[NS / 4][8];
-#pragma unroll
-        for (int j = kTile - 1; j >= 0; --j) {
-            const bool live = j < n;
-            const float4 v = put[j][lane];
-            float b[NS], c[NS], du = 0.f, down = 0.f;
-            Uniform<T, NS>::load(bt + (live ? j * GN : 0), live, b);
-            Uniform<T, NS>::load(ct + (live ? j * GN : 0), live, c);
-#pragma unroll
-            for (int q = 0; q < NS / 4; ++q) {
-                float r[4];
-#pragma unroll
-                for (int i4 = 0; i4 < 4; ++i4) {
-                    const int s = 4 * q + i4;
-                    g[s] = fmaf(c[s], v.z, g[s]);
-                    const float pb = g[s] * v.y, pc = v.z * h[j + 1][s];
-                    du = fmaf(g[s], b[s], du);
-                    g[s] *= kKeep ? a[j][s] : exp2_fast(v.x * w2[s]);
-                    const float m = g[s] * h[j][s];
-                    down = fmaf(m, w1[s], down);
-                    dw[s] = fmaf(-m, v.x, dw[s]);
+            for (int s = 0; s < 4; ++s) h[0][s] = before[4 * q + s];
+            each<kTile>([&](auto jj) {
+                constexpr int j = decltype(jj)::value;
+                const float4 v = put[j][lane];
+                float y = q > 0 ? parts[0][wave][j][lane] : 0.f;
+                each<4>([&](auto ss) {
+                    constexpr int s = decltype(ss)::value;
+                    a[j][s] = exp2_fast(v.x * w2[4 * q + s]);
+                    h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, 4 * q + s>() * v.y);
+                    y = fmaf(c.template get<j, 4 * q + s>(), h[j + 1][s], y);
+                });
+                parts[0][wave][j][lane] = y;
+            });
+            b.forget();
+            c.forget();
+            float tokens[8];
+            each<kTile>([&](auto jj) {
+                constexpr int j = kTile - 1 - decltype(jj)::value;
+                const float4 v = put[j][lane];
+                float du = q > 0 ? parts[1][wave][j][lane] : 0.f, down = q > 0 ? parts[2][wave][j][lane] : 0.f, r[4];
+                each<4>([&](auto ss) {
+                    constexpr int s = decltype(ss)::value, s4 = 4 * q + s;
+                    g[s4] = fmaf(c.template get<j, s4>(), v.z, g[s4]);
+                    const float pb = g[s4] * v.y, pc = v.z * h[j + 1][s];
+                    du = fmaf(b.template get<j, s4>(), g[s4], du);
+                    g[s4] *= a[j][s];
+                    const float m = g[s4] * h[j][s];
+                    down = fmaf(m, w1[s4], down);
+                    dw[s4] = fmaf(-m, v.x, dw[s4]);
                     // db to the lower half of the lanes, dc to the upper
                     const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(pb), __float_as_uint(pc), false, false);
-                    r[i4] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
-                }
-                // n + 0 and n + 1 to the even rows of 16 lanes, n + 2 and n + 3 to the odd ones
+                    r[s] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+                });
+                parts[1][wave][j][lane] = du;
+                parts[2][wave][j][lane] = down;
+                // states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones
                 float m2[2];
 #pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2) {
-                    const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[i2]), __float_as_uint(r[i2 + 2]), false, false);
-                    m2[i2] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+                for (int s = 0; s < 2; ++s) {
+                    const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[s]), __float_as_uint(r[s + 2]), false, false);
+                    m2[s] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
                 }
                 m2[0] += dpp<0x128>(m2[0]);  // row_ror:8
                 m2[1] += dpp<0x128>(m2[1]);
-                lanes8[q][j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
-                if ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
-                    float (&l)[8] = lanes8[q];
+                tokens[j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
+                if constexpr ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float lo = l[k] + dpp<0x141>(l[k]), hi = l[k + 4] + dpp<0x141>(l[k + 4]);  // row_half_mirror
-                        l[k] = (lane & 4) != 0 ? hi : lo;
+                        const float lo = tokens[k] + dpp<0x141>(tokens[k]), hi = tokens[k + 4] + dpp<0x141>(tokens[k + 4]);  // row_half_mirror
+                        tokens[k] = (lane & 4) != 0 ? hi : lo;
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float lo = l[k] + dpp<0x4E>(l[k]), hi = l[k + 2] + dpp<0x4E>(l[k + 2]);  // lane ^ 2
-                        l[k] = (lane & 2) != 0 ? hi : lo;
+                        const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 2] + dpp<0x4E>(tokens[k + 2]);  // lane ^ 2
+                        tokens[k] = (lane & 2) != 0 ? hi : lo;
                     }
-                    const float lo = l[0] + dpp<0xB1>(l[0]), hi = l[1] + dpp<0xB1>(l[1]);  // lane ^ 1
-                    const float sum = (lane & 1) != 0 ? hi : lo;
+                    const float lo = tokens[0] + dpp<0xB1>(tokens[0]), hi = tokens[1] + dpp<0xB1>(tokens[1]);  // lane ^ 1
                     const int tok = j + (lane & 7);
                     if (tok < n) {
                         const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
-                        P.part[row + (lane >> 5) * N + wave * NS + 4 * q + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = sum;
+                        P.part[row + (lane >> 5) * N + wave * NS + 4 * q + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = (lane & 1) != 0 ? hi : lo;
                     }
                 }
-            }
-            parts[1][wave][j][lane] = du;
-            parts[2][wave][j][lane] = down;
-        }
+            });
+        });
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int j = wave + W * k;
-            float y = skip * ex[k], du = 0.f, down = 0.f;
+            const float4 v = put[j][lane];
+            float y = skip * v.w, du = 0.f, down = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) y += parts[0][q][j][lane], du += parts[1][q][j][lane], down += parts[2][q][j][lane];
             if (j < n && p.valid) {
-                const int64_t at = (row0 + t + j) * P.C + p.ch;
-                const float gd = fmaf(du, ex[k], -down) * eslope[k];
-                if (z != nullptr) dz[at] = narrow<T>(egs[k] * y);
-                dx[at] = narrow<T>(fmaf(du, edelta[k], skip * egy[k]));
-                ddt[at] = narrow<T>(gd);
-                dd = fmaf(egy[k], ex[k], dd);
+                const int64_t row = (row0 + t + j) * P.C;
+                const float gd = fmaf(du, v.w, -down) * eslope[k];
+                if (z != nullptr) (dz + row)[p.ch] = narrow<T>(egs[k] * y);
+                (dx + row)[p.ch] = narrow<T>(fmaf(du, v.x, skip * v.z));
+                (ddt + row)[p.ch] = narrow<T>(gd);
+                dd = fmaf(v.z, v.w, dd);
                 dbias += gd;
             }
         }
