@@ -59,17 +59,22 @@ __device__ __forceinline__ float log1p_unit(float e) {
     return p * e;
 }
 
-// delta of a token, and its derivative by dt.
-template <bool Wide, bool Grad>
-__device__ __forceinline__ float step_of(float raw, bool softplus, float* grad) {
+// delta of some tokens from dt + dt_bias, and its derivative by dt.
+template <bool Wide, bool Grad, int E>
+__device__ __forceinline__ void steps_of(float (&raw)[E], bool softplus, float (&grad)[E]) {
     if (!softplus) {
-        if constexpr (Grad) *grad = 1.f;
-        return raw;
+        if constexpr (Grad) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) grad[k] = 1.f;
+        }
+        return;
     }
-    const float e = exp_neg_abs<Wide>(raw);
-    if constexpr (Grad) *grad = (raw >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
-    const float s = (raw > 0.f ? raw : 0.f) + log1p_unit(e);
-    return raw != raw ? raw : s;
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+        const float e = exp_neg_abs<Wide>(raw[k]);
+        if constexpr (Grad) grad[k] = (raw[k] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
+        raw[k] = fmaxf(raw[k], 0.f) + log1p_unit(e);  // (of NaN: 0 + NaN)
+    }
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e)); }
@@ -88,6 +93,34 @@ __device__ __forceinline__ void each(F&& f) {
 template <int K>
 __device__ __forceinline__ float row_lane(float x) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + K, 0xf, 0xf, true));  // row_newbcast
+}
+
+// y += sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
+// instructions of a write to that register, which the compiler does not look for inside here: hence the wait, which
+// costs this wave a moment and the others of its SIMD nothing.
+template <int K>
+__device__ __forceinline__ void dot_row(float& y, float c, float h0, float h1, float h2, float h3) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+}
+// g[s] += (lane K + s of its row of c) v, then du += sum of (lane K + s of b) g[s].
+template <int K>
+__device__ __forceinline__ void add_dot_row(float& g0, float& g1, float& g2, float& g3, float& du, float c, float v, float b) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %5, %6 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %5, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %5, %6 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %5, %6 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %7, %0 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %7, %1 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %7, %2 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %4, %7, %3 row_newbcast:%11 row_mask:0xf bank_mask:0xf"
+        : "+v"(g0), "+v"(g1), "+v"(g2), "+v"(g3), "+v"(du)
+        : "v"(c), "v"(v), "v"(b), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
 }
 
 // A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
@@ -115,6 +148,11 @@ struct Row {
 #pragma unroll
         for (int r = 0; r < NS; ++r) asm volatile("" : "+v"(f[r]));
     }
+    // the lane and the register of state S of token J
+    template <int J, int S>
+    static constexpr int lane_of() { return (J * NS + S) % 16; }
+    template <int J, int S>
+    __device__ __forceinline__ float reg() const { return f[(J * NS + S) / 16]; }
     template <int J, int S>
     __device__ __forceinline__ float get() const { return row_lane<(J * NS + S) % 16>(f[(J * NS + S) / 16]); }
 };
@@ -132,6 +170,12 @@ template <int NS>
 __device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
 #pragma unroll
     for (int q = 0; q < NS / 4; ++q) *reinterpret_cast<f4*>(p + 4 * q) = f4{h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]};
+}
+
+// The element `bytes` behind a wave's common address.
+template <typename T>
+__device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
+    return *reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
 }
 
 // Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
@@ -200,21 +244,25 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         else if (P.s_in != nullptr) load_states<NS>(P.s_in + state, p.valid, h);
     }
 
-    // The inputs of the tile after this one on their way while this one is walked; of this one, what its outputs need.
+    // Inputs come in two tiles ahead, in the raw, and are worked out one tile ahead; a tile's outputs leave while the
+    // next one is walked.  ex, ez: what the outputs need of x and z, of the tiles i + 1, i and i - 1.
+    const bool has_z = z != nullptr, spare = !__all(p.valid);
+    const T* const first_in = kAdj ? go : x;
+    const T* const gate_in = has_z ? z : dt;
+    const uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
     T rx[kEach], rd[kEach], rz[kEach];
-    float ex[kEach], ez[kEach], nx[kEach], nz[kEach];
+    float ex[3][kEach], ez[3][kEach];
     Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
-    const auto fetch = [&](int i) {  // (behind the last token: that one again)
+    const auto fetch = [&](int i) {
         const int t = tile_at(i < ntiles ? i : ntiles - 1) + wave;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int at = t + W * k < p.te ? t + W * k : p.te - 1;
+            const int at = t + W * k < p.te ? t + W * k : p.te - 1;  // (behind the last token: that one again)
             const int64_t row = (row0 + at) * P.C;
-            rd[k] = (dt + row)[p.ch];
-            rx[k] = ((kAdj ? go : x) + row)[p.ch];
-            rz[k] = T{0};
-            if ((kOut || kAdj) && z != nullptr) rz[k] = (z + row)[p.ch];
+            rd[k] = at_bytes(dt + row, chb);
+            rx[k] = at_bytes(first_in + row, chb);
+            if constexpr (kOut || kAdj) rz[k] = at_bytes(gate_in + row, chb);
         }
     };
     const auto fetch_bc = [&](int i) {
@@ -224,42 +272,83 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     };
     float total = 0.f;  // of delta
     const auto stage = [&](int i) {
-        const int t = tile_at(i) + wave;
+        float delta[kEach], v[kEach], unused[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) delta[k] = widen(rd[k]) + bias, v[k] = widen(rx[k]);
+        steps_of<kWide, false>(delta, P.softplus, unused);
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const bool live = i < ntiles && t + W * k < p.te && p.valid;
-            float delta = step_of<kWide, false>(widen(rd[k]) + bias, P.softplus, nullptr), v = widen(rx[k]);
-            if constexpr (kAdj) {
-                const float zz = widen(rz[k]);
-                if (z != nullptr) v *= zz * sigmoid(zz);
-            } else {
-                if constexpr (kOut) {
-                    const float zz = widen(rz[k]);
-                    nx[k] = skip * v;
-                    nz[k] = z != nullptr ? zz * sigmoid(zz) : 1.f;
-                }
-                v *= delta;
+            if constexpr (kOut || kAdj) {
+                const float zz = widen(rz[k]), gate = has_z ? zz * sigmoid(zz) : 1.f;
+                if constexpr (kAdj) v[k] *= gate;
+                else ex[0][k] = skip * v[k], ez[0][k] = gate;
             }
-            delta = live ? delta : 0.f;
-            put[i & 1][wave + W * k][lane] = make_float2(delta, live ? v : 0.f);
-            if constexpr (!kOut) total += delta;
+            if constexpr (!kAdj) v[k] *= delta[k];
+        }
+        const int left = i < ntiles ? p.te - tile_at(i) - wave : 0;
+        if (spare || left < kTile) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const bool live = W * k < left && p.valid;
+                delta[k] = live ? delta[k] : 0.f;
+                v[k] = live ? v[k] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            put[i & 1][wave + W * k][lane] = make_float2(delta[k], v[k]);
+            if constexpr (!kOut) total += delta[k];
+        }
+    };
+    const auto pass = [&] {  // on to the next tile
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+#pragma unroll
+            for (int q = 2; q > 0; --q) ex[q][k] = ex[q - 1][k], ez[q][k] = ez[q - 1][k];
+        }
+    };
+    // the outputs of tile i, from the waves' parts
+    T o[kEach];
+    const auto add_up = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            float y = ex[2][k];
+#pragma unroll
+            for (int q = 0; q < W; ++q) y += parts[i & 1][q][wave + W * k][lane];
+            o[k] = narrow<T>(y * ez[2][k]);
+        }
+    };
+    const auto write = [&](int i) {
+        const int t = tile_at(i) + wave, left = p.te - t;
+        T* const row = out + (row0 + t) * P.C;
+        if (out == nullptr || i < 0) return;
+        if (spare || left < kTile) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                if (W * k < left && p.valid) at_bytes(row + W * k * P.C, chb) = o[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) at_bytes(row + W * k * P.C, chb) = o[k];
         }
     };
 
     if (ntiles > 0) {
         fetch(0);
         fetch_bc(0);
+        if constexpr (kOut) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) ex[1][k] = ez[1][k] = 0.f;
+        }
         stage(0);
+        if constexpr (kOut) pass();
         fetch(1);
         __syncthreads();
     }
     for (int i = 0; i < ntiles; ++i) {
-        const int t = tile_at(i), n = p.te - t;
         if constexpr (kOut) {
             if (P.ckpt != nullptr && p.valid)
-                store_states<NS>(P.ckpt + (((p.b * P.tiles + t / kTile) * W + wave) * P.C + p.ch) * NS, h);
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) ex[k] = nx[k], ez[k] = nz[k];
+                store_states<NS>(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
+            if (i > 0) add_up(i - 1);
         }
         b.ready();
         if constexpr (kOut) c.ready();
@@ -268,31 +357,33 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         each<kTile>([&](auto jj) {
             constexpr int j = kAdj ? kTile - 1 - decltype(jj)::value : decltype(jj)::value;
             const float2 dv = now[j][lane];
-            float y = 0.f;
             each<NS>([&](auto ss) {
                 constexpr int s = decltype(ss)::value;
                 const float a = exp2_fast(dv.x * w2[s]);
-                if constexpr (kAdj) {
-                    h[s] = a * fmaf(b.template get<j, s>(), dv.y, h[s]);
-                } else {
-                    h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
-                    if constexpr (kOut) y = fmaf(c.template get<j, s>(), h[s], y);
-                }
+                if constexpr (kAdj) h[s] = a * fmaf(b.template get<j, s>(), dv.y, h[s]);
+                else h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
             });
-            if constexpr (kOut) parts[i & 1][wave][j][lane] = y;
+            if constexpr (kOut) {
+                float y = 0.f;
+                each<NS / 4>([&](auto qq) {
+                    constexpr int s = 4 * decltype(qq)::value;
+                    dot_row<c.template lane_of<j, s>()>(y, c.template reg<j, s>(), h[s], h[s + 1], h[s + 2], h[s + 3]);
+                });
+                parts[i & 1][wave][j][lane] = y;
+            }
         });
         stage(i + 1);
+        if constexpr (kOut) {
+            write(i - 1);
+            pass();
+        }
         __syncthreads();
         fetch(i + 2);
-        if constexpr (kOut) {
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                const int j = wave + W * k;
-                float y = ex[k];
-#pragma unroll
-                for (int q = 0; q < W; ++q) y += parts[i & 1][q][j][lane];
-                if (j < n && p.valid && out != nullptr) (out + (row0 + t + j) * P.C)[p.ch] = narrow<T>(y * ez[k]);
-            }
+    }
+    if constexpr (kOut) {
+        if (ntiles > 0) {
+            add_up(ntiles - 1);
+            write(ntiles - 1);
         }
     }
     if constexpr (kOut) {
@@ -370,6 +461,9 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     for (int i = 0; i < NS; ++i) w1[i] = fminf(w1[i], 2e38f), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
     if (from != nullptr) load_states<NS>(from + state, p.valid, g);
 
+    const bool has_z = z != nullptr, spare = !__all(p.valid);
+    const T* const gate_in = has_z ? z : dt;
+    const uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
     T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
     Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
@@ -379,11 +473,10 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
         for (int k = 0; k < kEach; ++k) {
             const int at = t + W * k < p.te ? t + W * k : p.te - 1;
             const int64_t row = (row0 + at) * P.C;
-            rd[k] = (dt + row)[p.ch];
-            rx[k] = (x + row)[p.ch];
-            rg[k] = (go + row)[p.ch];
-            rz[k] = T{0};
-            if (z != nullptr) rz[k] = (z + row)[p.ch];
+            rd[k] = at_bytes(dt + row, chb);
+            rx[k] = at_bytes(x + row, chb);
+            rg[k] = at_bytes(go + row, chb);
+            rz[k] = at_bytes(gate_in + row, chb);
         }
         load_states<NS>(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
         b.fetch(bt, tile, p.te, GN, lane);
@@ -393,15 +486,19 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     if (ntiles > 0) fetch(ntiles - 1);
     for (int i = ntiles - 1; i >= 0; --i) {
         const int t = tile_at(i), n = p.te - t;
-        float egs[kEach], eslope[kEach];
+        float egs[kEach], eslope[kEach], delta[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) delta[k] = widen(rd[k]) + bias;
+        steps_of<kWide, true>(delta, P.softplus, eslope);
+        const bool edge = spare || n < kTile;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const bool live = wave + W * k < n && p.valid;
-            const float delta = step_of<kWide, true>(widen(rd[k]) + bias, P.softplus, &eslope[k]);
-            const float zz = widen(rz[k]), gg = widen(rg[k]), sg = sigmoid(zz);
-            const float xx = widen(rx[k]), gy = z != nullptr ? gg * (zz * sg) : gg;
-            egs[k] = gg * (sg * fmaf(zz, 1.f - sg, 1.f));
-            put[wave + W * k][lane] = live ? make_float4(delta, delta * xx, gy, xx) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float zz = widen(rz[k]), gg = widen(rg[k]), sg = sigmoid(zz), xx = widen(rx[k]);
+            const float gate = has_z ? zz * sg : 1.f;
+            egs[k] = gg * fmaf(gate, 1.f - sg, sg);  // times the gate's derivative, sg (1 + z (1 - sg))
+            float4 v = make_float4(delta[k], delta[k] * xx, gg * gate, xx);
+            if (edge && !(wave + W * k < n && p.valid)) v = make_float4(0.f, 0.f, 0.f, 0.f);
+            put[wave + W * k][lane] = v;
         }
         float before[NS];
 #pragma unroll
@@ -423,8 +520,8 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
                     constexpr int s = decltype(ss)::value;
                     a[j][s] = exp2_fast(v.x * w2[4 * q + s]);
                     h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, 4 * q + s>() * v.y);
-                    y = fmaf(c.template get<j, 4 * q + s>(), h[j + 1][s], y);
                 });
+                dot_row<c.template lane_of<j, 4 * q>()>(y, c.template reg<j, 4 * q>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
                 parts[0][wave][j][lane] = y;
             });
             b.forget();
@@ -434,11 +531,11 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
                 constexpr int j = kTile - 1 - decltype(jj)::value;
                 const float4 v = put[j][lane];
                 float du = q > 0 ? parts[1][wave][j][lane] : 0.f, down = q > 0 ? parts[2][wave][j][lane] : 0.f, r[4];
+                add_dot_row<c.template lane_of<j, 4 * q>()>(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3], du,
+                                                            c.template reg<j, 4 * q>(), v.z, b.template reg<j, 4 * q>());
                 each<4>([&](auto ss) {
                     constexpr int s = decltype(ss)::value, s4 = 4 * q + s;
-                    g[s4] = fmaf(c.template get<j, s4>(), v.z, g[s4]);
                     const float pb = g[s4] * v.y, pc = v.z * h[j + 1][s];
-                    du = fmaf(b.template get<j, s4>(), g[s4], du);
                     g[s4] *= a[j][s];
                     const float m = g[s4] * h[j][s];
                     down = fmaf(m, w1[s4], down);
@@ -480,6 +577,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             });
         });
         __syncthreads();
+        T oz[kEach], ox[kEach], od[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int j = wave + W * k;
@@ -487,15 +585,22 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             float y = skip * v.w, du = 0.f, down = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) y += parts[0][q][j][lane], du += parts[1][q][j][lane], down += parts[2][q][j][lane];
-            if (j < n && p.valid) {
-                const int64_t row = (row0 + t + j) * P.C;
-                const float gd = fmaf(du, v.w, -down) * eslope[k];
-                if (z != nullptr) (dz + row)[p.ch] = narrow<T>(egs[k] * y);
-                (dx + row)[p.ch] = narrow<T>(fmaf(du, v.x, skip * v.z));
-                (ddt + row)[p.ch] = narrow<T>(gd);
-                dd = fmaf(v.z, v.w, dd);
-                dbias += gd;
-            }
+            float gd = fmaf(du, v.w, -down) * eslope[k];
+            if (edge) gd = j < n && p.valid ? gd : 0.f;
+            oz[k] = narrow<T>(egs[k] * y);
+            ox[k] = narrow<T>(fmaf(du, v.x, skip * v.z));
+            od[k] = narrow<T>(gd);
+            dd = fmaf(v.z, v.w, dd);
+            dbias += gd;
+        }
+        const int64_t row = (row0 + t + wave) * P.C;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (edge && !(wave + W * k < n && p.valid)) continue;
+            const int64_t at = row + W * k * P.C;
+            at_bytes(dx + at, chb) = ox[k];
+            at_bytes(ddt + at, chb) = od[k];
+            if (has_z) at_bytes(dz + at, chb) = oz[k];
         }
     }
     if (p.valid) {
@@ -588,7 +693,9 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
         float y = 0.f, vx = 0.f, gate = 1.f;
         if (live) {
             vx = widen(x[at]);
-            const float delta = step_of<kWide, false>(widen(dt[at]) + bias, P.softplus, nullptr), u = delta * vx;
+            float d1[1] = {widen(dt[at]) + bias}, unused[1];
+            steps_of<kWide, false>(d1, P.softplus, unused);
+            const float delta = d1[0], u = delta * vx;
             if (z != nullptr) {
                 const float zz = widen(z[at]);
                 gate = zz * sigmoid(zz);
