@@ -1077,7 +1077,7 @@ SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, in
     constexpr int64_t kMost = int64_t{1} << 31, kBig = int64_t{1} << 58;
     int64_t n, cn, gn, bct, ck;
     if (B >= kMost || T >= kMost) return bad(WKV_ESIZE);
-    if (!mul3(C, N, 1, &cn) || cn >= (int64_t{1} << 30) || !mul3(G, N, 1, &gn) || gn >= (int64_t{1} << 30)) return bad(WKV_ESIZE);
+    if (!mul3(C, N, 1, &cn) || cn >= (int64_t{1} << 30) || !mul3(G, N, 1, &gn) || gn >= (int64_t{1} << 25)) return bad(WKV_ESIZE);
     if (!mul3(B, T, C, &n) || n > kBig || !mul3(B, cn, 1, &p.ns) || p.ns > kBig || !mul3(B, T, gn, &bct) || bct > kBig)
         return bad(WKV_ESIZE);
     if (C == 0) return p;

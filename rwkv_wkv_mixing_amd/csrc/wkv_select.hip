@@ -73,11 +73,24 @@ __device__ __forceinline__ void steps_of(float (&raw)[E], bool softplus, float (
     for (int k = 0; k < E; ++k) {
         const float e = exp_neg_abs<Wide>(raw[k]);
         if constexpr (Grad) grad[k] = (raw[k] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
-        raw[k] = fmaxf(raw[k], 0.f) + log1p_unit(e);  // (of NaN: 0 + NaN)
+        raw[k] = __builtin_amdgcn_fmed3f(raw[k], 0.f, __builtin_inff()) + log1p_unit(e);  // (of NaN: 0 + NaN)
     }
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e)); }
+
+// The element `bytes` behind a wave's common address.
+template <typename T>
+__device__ __forceinline__ const T& at_bytes(const T* p, uint32_t bytes) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes);
+}
+template <typename T>
+__device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
+    return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + bytes);
+}
+
+// Keeps an offset one of 32 bits in a loop, so that an address is a wave's own and this offset, not a sum of 64 bits.
+__device__ __forceinline__ void keep32(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // Calls f with std::integral_constant<int, 0> .. <int, N - 1>: the lanes of a broadcast are part of the instruction.
 template <int N, class F, int... I>
@@ -95,53 +108,81 @@ __device__ __forceinline__ float row_lane(float x) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + K, 0xf, 0xf, true));  // row_newbcast
 }
 
-// y += sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
+// y = (Add: y +) sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
 // instructions of a write to that register, which the compiler does not look for inside here: hence the wait, which
 // costs this wave a moment and the others of its SIMD nothing.
-template <int K>
+template <int K, bool Add>
 __device__ __forceinline__ void dot_row(float& y, float c, float h0, float h1, float h2, float h3) {
-    asm("s_nop 1\n\t"
-        "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-        : "+v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    if constexpr (Add) {
+        asm("s_nop 1\n\t"
+            "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "+v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    } else {
+        asm("s_nop 1\n\t"
+            "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+            : "=&v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    }
 }
-// g[s] += (lane K + s of its row of c) v, then du += sum of (lane K + s of b) g[s].
-template <int K>
+// g[s] += (lane K + s of its row of c) v, then du = (Add: du +) the sum of (lane K + s of b) g[s].
+template <int K, bool Add>
 __device__ __forceinline__ void add_dot_row(float& g0, float& g1, float& g2, float& g3, float& du, float c, float v, float b) {
     asm("s_nop 1\n\t"
-        "v_fmac_f32_dpp %0, %5, %6 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %1, %5, %6 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %2, %5, %6 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %3, %5, %6 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %7, %0 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %7, %1 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %7, %2 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n\t"
-        "v_fmac_f32_dpp %4, %7, %3 row_newbcast:%11 row_mask:0xf bank_mask:0xf"
-        : "+v"(g0), "+v"(g1), "+v"(g2), "+v"(g3), "+v"(du)
-        : "v"(c), "v"(v), "v"(b), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %5 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %5 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(g0), "+v"(g1), "+v"(g2), "+v"(g3)
+        : "v"(c), "v"(v), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    dot_row<K, Add>(du, b, g0, g1, g2, g3);
 }
 
 // A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
 // NS registers, token by token, so that each of them is one lane of one register.
 template <typename T, int NS>
 struct Row {
+    static constexpr int kPer = kTile / NS;  // tokens a register
     T raw[NS];
     float f[NS];
-    // tokens t .. t + kTile - 1 of a row with stride GN; those from te on are not read
-    __device__ __forceinline__ void fetch(const T* p, int t, int te, int64_t GN, int lane) {
-        constexpr int kPer = kTile / NS;  // tokens a register
-        const int s = lane % NS, j = (lane & 15) / NS;
+    // where a lane reads: its state, its token of the first register's, the bytes from token to token
+    struct Where {
+        uint32_t stride, s, first;
+        int j;
+    };
+    static __device__ __forceinline__ Where where(int64_t GN, int lane) {
+        Where w;
+        w.stride = static_cast<uint32_t>(GN) * sizeof(T);
+        w.s = (lane % NS) * sizeof(T);
+        w.j = (lane & 15) / NS;
+        w.first = w.j * w.stride + w.s;
+        return w;
+    }
+    // the tile's tokens from p on, `left` of them there (at least one): the others are zeros
+    __device__ __forceinline__ void fetch(const T* p, Where& w, int left) {
+        keep32(w.first);
+        if (left >= kTile) {
 #pragma unroll
-        for (int r = 0; r < NS; ++r) {
-            const int at = t + r * kPer + j;
-            raw[r] = at < te ? p[at * GN + s] : T{0};
+            for (int r = 0; r < NS; ++r) raw[r] = at_bytes(p + static_cast<int64_t>(r * kPer) * (w.stride / sizeof(T)), w.first);
+        } else {
+#pragma unroll
+            for (int r = 0; r < NS; ++r) {
+                const int j = r * kPer + w.j;
+                const T v = at_bytes(p, (j < left ? j : left - 1) * w.stride + w.s);
+                raw[r] = j < left ? v : T{0};
+            }
         }
     }
     __device__ __forceinline__ void ready() {
 #pragma unroll
-        for (int r = 0; r < NS; ++r) f[r] = widen(raw[r]);
+        for (int r = 0; r < NS; ++r) {
+            f[r] = widen(raw[r]);
+            asm volatile("" : "+v"(f[r]));  // (here and now, not where it is used)
+        }
     }
     // The compiler is to broadcast again rather than keep what it broadcast before.
     __device__ __forceinline__ void forget() {
@@ -170,12 +211,6 @@ template <int NS>
 __device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
 #pragma unroll
     for (int q = 0; q < NS / 4; ++q) *reinterpret_cast<f4*>(p + 4 * q) = f4{h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]};
-}
-
-// The element `bytes` behind a wave's common address.
-template <typename T>
-__device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
-    return *reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + bytes);
 }
 
 // Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
@@ -249,12 +284,13 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const bool has_z = z != nullptr, spare = !__all(p.valid);
     const T* const first_in = kAdj ? go : x;
     const T* const gate_in = has_z ? z : dt;
-    const uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
+    uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
     T rx[kEach], rd[kEach], rz[kEach];
     float ex[3][kEach], ez[3][kEach];
     Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
     const auto fetch = [&](int i) {
+        keep32(chb);
         const int t = tile_at(i < ntiles ? i : ntiles - 1) + wave;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
@@ -265,10 +301,11 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
             if constexpr (kOut || kAdj) rz[k] = at_bytes(gate_in + row, chb);
         }
     };
+    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
     const auto fetch_bc = [&](int i) {
         const int t = tile_at(i < ntiles ? i : ntiles - 1);
-        b.fetch(bt, t, p.te, GN, lane);
-        if constexpr (kOut) c.fetch(ct, t, p.te, GN, lane);
+        b.fetch(bt + t * GN, where, p.te - t);
+        if constexpr (kOut) c.fetch(ct + t * GN, where, p.te - t);
     };
     float total = 0.f;  // of delta
     const auto stage = [&](int i) {
@@ -321,6 +358,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const auto write = [&](int i) {
         const int t = tile_at(i) + wave, left = p.te - t;
         T* const row = out + (row0 + t) * P.C;
+        keep32(chb);
         if (out == nullptr || i < 0) return;
         if (spare || left < kTile) {
 #pragma unroll
@@ -340,7 +378,11 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
             for (int k = 0; k < kEach; ++k) ex[1][k] = ez[1][k] = 0.f;
         }
         stage(0);
-        if constexpr (kOut) pass();
+        b.ready();
+        if constexpr (kOut) {
+            c.ready();
+            pass();
+        }
         fetch(1);
         __syncthreads();
     }
@@ -350,8 +392,6 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
                 store_states<NS>(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
             if (i > 0) add_up(i - 1);
         }
-        b.ready();
-        if constexpr (kOut) c.ready();
         fetch_bc(i + 1);
         const float2(&now)[kTile][64] = put[i & 1];
         each<kTile>([&](auto jj) {
@@ -364,16 +404,21 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
                 else h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
             });
             if constexpr (kOut) {
-                float y = 0.f;
+                float y;
                 each<NS / 4>([&](auto qq) {
                     constexpr int s = 4 * decltype(qq)::value;
-                    dot_row<c.template lane_of<j, s>()>(y, c.template reg<j, s>(), h[s], h[s + 1], h[s + 2], h[s + 3]);
+                    dot_row<c.template lane_of<j, s>(), (s > 0)>(y, c.template reg<j, s>(), h[s], h[s + 1], h[s + 2], h[s + 3]);
                 });
                 parts[i & 1][wave][j][lane] = y;
             }
         });
         stage(i + 1);
+        b.ready();
         if constexpr (kOut) {
+            c.ready();
+            // (worked out here, before the stores: a load waited for behind them would wait for them too)
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) asm volatile("" : "+v"(ex[0][k]), "+v"(ez[0][k]));
             write(i - 1);
             pass();
         }
@@ -463,12 +508,14 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
 
     const bool has_z = z != nullptr, spare = !__all(p.valid);
     const T* const gate_in = has_z ? z : dt;
-    const uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
+    uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
     T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
     Row<T, NS> b, c;
+    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
     const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
     const auto fetch = [&](int i) {  // (behind the last token: that one again; before the first tile: nothing new)
-        const int tile = tile_at(i > 0 ? i : 0), t = tile + wave;
+        keep32(chb);
+        const int tile = tile_at(i > 0 ? i : 0), t = tile + wave, left = p.te - tile;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int at = t + W * k < p.te ? t + W * k : p.te - 1;
@@ -479,8 +526,8 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             rz[k] = at_bytes(gate_in + row, chb);
         }
         load_states<NS>(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
-        b.fetch(bt, tile, p.te, GN, lane);
-        c.fetch(ct, tile, p.te, GN, lane);
+        b.fetch(bt + tile * GN, where, left);
+        c.fetch(ct + tile * GN, where, left);
     };
     float dd = 0.f, dbias = 0.f;
     if (ntiles > 0) fetch(ntiles - 1);
@@ -496,9 +543,12 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             const float zz = widen(rz[k]), gg = widen(rg[k]), sg = sigmoid(zz), xx = widen(rx[k]);
             const float gate = has_z ? zz * sg : 1.f;
             egs[k] = gg * fmaf(gate, 1.f - sg, sg);  // times the gate's derivative, sg (1 + z (1 - sg))
-            float4 v = make_float4(delta[k], delta[k] * xx, gg * gate, xx);
-            if (edge && !(wave + W * k < n && p.valid)) v = make_float4(0.f, 0.f, 0.f, 0.f);
-            put[wave + W * k][lane] = v;
+            put[wave + W * k][lane] = make_float4(delta[k], delta[k] * xx, gg * gate, xx);
+        }
+        if (edge) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                if (!(wave + W * k < n && p.valid)) put[wave + W * k][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float before[NS];
 #pragma unroll
@@ -515,13 +565,14 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             each<kTile>([&](auto jj) {
                 constexpr int j = decltype(jj)::value;
                 const float4 v = put[j][lane];
-                float y = q > 0 ? parts[0][wave][j][lane] : 0.f;
+                float y;
+                if constexpr (q > 0) y = parts[0][wave][j][lane];
                 each<4>([&](auto ss) {
                     constexpr int s = decltype(ss)::value;
                     a[j][s] = exp2_fast(v.x * w2[4 * q + s]);
                     h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, 4 * q + s>() * v.y);
                 });
-                dot_row<c.template lane_of<j, 4 * q>()>(y, c.template reg<j, 4 * q>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
+                dot_row<c.template lane_of<j, 4 * q>(), (q > 0)>(y, c.template reg<j, 4 * q>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
                 parts[0][wave][j][lane] = y;
             });
             b.forget();
@@ -530,8 +581,9 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             each<kTile>([&](auto jj) {
                 constexpr int j = kTile - 1 - decltype(jj)::value;
                 const float4 v = put[j][lane];
-                float du = q > 0 ? parts[1][wave][j][lane] : 0.f, down = q > 0 ? parts[2][wave][j][lane] : 0.f, r[4];
-                add_dot_row<c.template lane_of<j, 4 * q>()>(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3], du,
+                float du, down = q > 0 ? parts[2][wave][j][lane] : 0.f, r[4];
+                if constexpr (q > 0) du = parts[1][wave][j][lane];
+                add_dot_row<c.template lane_of<j, 4 * q>(), (q > 0)>(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3], du,
                                                             c.template reg<j, 4 * q>(), v.z, b.template reg<j, 4 * q>());
                 each<4>([&](auto ss) {
                     constexpr int s = decltype(ss)::value, s4 = 4 * q + s;
@@ -594,6 +646,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             dbias += gd;
         }
         const int64_t row = (row0 + t + wave) * P.C;
+        keep32(chb);
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             if (edge && !(wave + W * k < n && p.valid)) continue;
