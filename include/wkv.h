@@ -777,7 +777,7 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
  * States and sums are float32 whatever the inputs' dtype; outputs are rounded once.
  *
  * B, T, C   batch rows, tokens, channels (>= 0).  G  groups of channels that share
- *           b and c: a divisor of C (1 with C = 0).  N  8, 16, 32 or 64.
+ *           b and c: a divisor of C (1 with C = 0).  N  8, 16 or 32.
  * in_dtype  dtype of x, dt, b, c, z and out.
  * lengths   [B] int32 or NULL: tokens of each row (clamped to 0 .. T).  Tokens
  *           behind it are not read, leave the state as it is, and their rows of

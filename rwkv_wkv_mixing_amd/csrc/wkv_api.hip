@@ -1071,7 +1071,7 @@ struct SelectPlan {
 
 SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dt, bool steps, bool bwd) {
     const auto bad = [](wkv_status_t st) { return SelectPlan{st, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0}; };
-    if (B < 0 || T < 0 || C < 0 || G < 1 || (N != 8 && N != 16 && N != 32 && N != 64) || C % G != 0) return bad(WKV_EINVAL);
+    if (B < 0 || T < 0 || C < 0 || G < 1 || (N != 8 && N != 16 && N != 32) || C % G != 0) return bad(WKV_EINVAL);
     if (!dtype_ok(dt)) return bad(WKV_EDTYPE);
     SelectPlan p{WKV_OK, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0};
     constexpr int64_t kMost = int64_t{1} << 31, kBig = int64_t{1} << 58;

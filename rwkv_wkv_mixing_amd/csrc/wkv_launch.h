@@ -449,7 +449,7 @@ struct SelectArgs {
     // forward
     void* out = nullptr;      // [B, T, C]
     float* s_out = nullptr;   // [B, C, N] or NULL
-    float* ckpt = nullptr;    // [B, tiles, N / NS, C, NS] the state before every kSelectTile tokens, or NULL
+    float* ckpt = nullptr;    // [B, tiles, N / 4, C, 4] the state before every kSelectTile tokens, or NULL
     // backward
     const float* saved = nullptr;  // the forward's ckpt
     const void* go = nullptr;      // [B, T, C]

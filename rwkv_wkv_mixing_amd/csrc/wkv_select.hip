@@ -6,7 +6,7 @@
 // vector units, which is what bounds it (a channel-token of N = 16 moves 8 bytes in bf16 and takes some 130 lane
 // instructions, 0.1 us a million at this card's rate against 0.04 for the bytes).
 //
-// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, NS a wave: a wave's b_t and
+// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, four a wave: a wave's b_t and
 // c_t are then the same for all its lanes and reach its multiplications as lane broadcasts, and only delta, the written
 // value and the waves' parts of y pass through LDS.  Tiles of 16 tokens: the threads first work out delta and what is written for (token, channel)
 // pairs, one each; then every wave walks the tile; then the threads add the waves' parts, gate and store.
@@ -22,6 +22,7 @@ namespace wkv {
 namespace {
 
 constexpr int kTile = kSelectTile;  // tokens a tile
+constexpr int NS = 4;               // states a wave
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <typename T>
@@ -79,17 +80,17 @@ __device__ __forceinline__ void steps_of(float (&raw)[E], bool softplus, float (
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e)); }
 
-// The element `bytes` behind a wave's common address.
+// The element `bytes` behind place `at` (in bytes, the whole wave's) of a tensor.  Places are counted in bytes all the way:
+// a 64-bit place shifted by the size of an element is worked out lane by lane.
 template <typename T>
-__device__ __forceinline__ const T& at_bytes(const T* p, uint32_t bytes) {
-    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + bytes);
+__device__ __forceinline__ T load_at(const T* p, int64_t at, uint32_t bytes) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + at + bytes);
 }
 template <typename T>
-__device__ __forceinline__ T& at_bytes(T* p, uint32_t bytes) {
-    return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + bytes);
+__device__ __forceinline__ void store_at(T* p, int64_t at, uint32_t bytes, T v) {
+    *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + at + bytes) = v;
 }
-
-// Keeps an offset one of 32 bits in a loop, so that an address is a wave's own and this offset, not a sum of 64 bits.
+// Keeps an offset one of 32 bits in a loop, next to a wave's address, and not part of a sum of 64 bits.
 __device__ __forceinline__ void keep32(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // Calls f with std::integral_constant<int, 0> .. <int, N - 1>: the lanes of a broadcast are part of the instruction.
@@ -108,43 +109,35 @@ __device__ __forceinline__ float row_lane(float x) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + K, 0xf, 0xf, true));  // row_newbcast
 }
 
-// y = (Add: y +) sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
+// The sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
 // instructions of a write to that register, which the compiler does not look for inside here: hence the wait, which
 // costs this wave a moment and the others of its SIMD nothing.
-template <int K, bool Add>
-__device__ __forceinline__ void dot_row(float& y, float c, float h0, float h1, float h2, float h3) {
-    if constexpr (Add) {
-        asm("s_nop 1\n\t"
-            "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-            : "+v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
-    } else {
-        asm("s_nop 1\n\t"
-            "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
-            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-            : "=&v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
-    }
+template <int K>
+__device__ __forceinline__ float dot_row(float c, float h0, float h1, float h2, float h3) {
+    float y;
+    asm("s_nop 1\n\t"
+        "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "=&v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    return y;
 }
-// g[s] += (lane K + s of its row of c) v, then du = (Add: du +) the sum of (lane K + s of b) g[s].
-template <int K, bool Add>
-__device__ __forceinline__ void add_dot_row(float& g0, float& g1, float& g2, float& g3, float& du, float c, float v, float b) {
+// g[s] += (lane K + s of its row of c) v.
+template <int K>
+__device__ __forceinline__ void add_row(float (&g)[NS], float c, float v) {
     asm("s_nop 1\n\t"
         "v_fmac_f32_dpp %0, %4, %5 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %1, %4, %5 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %2, %4, %5 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %3, %4, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-        : "+v"(g0), "+v"(g1), "+v"(g2), "+v"(g3)
+        : "+v"(g[0]), "+v"(g[1]), "+v"(g[2]), "+v"(g[3])
         : "v"(c), "v"(v), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
-    dot_row<K, Add>(du, b, g0, g1, g2, g3);
 }
 
 // A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
 // NS registers, token by token, so that each of them is one lane of one register.
-template <typename T, int NS>
+template <typename T>
 struct Row {
     static constexpr int kPer = kTile / NS;  // tokens a register
     T raw[NS];
@@ -163,16 +156,16 @@ struct Row {
         return w;
     }
     // the tile's tokens from p on, `left` of them there (at least one): the others are zeros
-    __device__ __forceinline__ void fetch(const T* p, Where& w, int left) {
+    __device__ __forceinline__ void fetch(const T* p, int64_t at, Where& w, int left) {
         keep32(w.first);
         if (left >= kTile) {
 #pragma unroll
-            for (int r = 0; r < NS; ++r) raw[r] = at_bytes(p + static_cast<int64_t>(r * kPer) * (w.stride / sizeof(T)), w.first);
+            for (int r = 0; r < NS; ++r) raw[r] = load_at(p, at + static_cast<int64_t>(r * kPer) * w.stride, w.first);
         } else {
 #pragma unroll
             for (int r = 0; r < NS; ++r) {
                 const int j = r * kPer + w.j;
-                const T v = at_bytes(p, (j < left ? j : left - 1) * w.stride + w.s);
+                const T v = load_at(p, at, (j < left ? j : left - 1) * w.stride + w.s);
                 raw[r] = j < left ? v : T{0};
             }
         }
@@ -189,28 +182,22 @@ struct Row {
 #pragma unroll
         for (int r = 0; r < NS; ++r) asm volatile("" : "+v"(f[r]));
     }
-    // the lane and the register of state S of token J
+    // the lane and the register of token J's first state
+    template <int J>
+    static constexpr int lane_of() { return J * NS % 16; }
+    template <int J>
+    __device__ __forceinline__ float reg() const { return f[J * NS / 16]; }
     template <int J, int S>
-    static constexpr int lane_of() { return (J * NS + S) % 16; }
-    template <int J, int S>
-    __device__ __forceinline__ float reg() const { return f[(J * NS + S) / 16]; }
-    template <int J, int S>
-    __device__ __forceinline__ float get() const { return row_lane<(J * NS + S) % 16>(f[(J * NS + S) / 16]); }
+    __device__ __forceinline__ float get() const { return row_lane<lane_of<J>() + S>(reg<J>()); }
 };
 
-template <int NS>
 __device__ __forceinline__ void load_states(const float* p, bool valid, float (&h)[NS]) {
+    const f4 v = valid ? *reinterpret_cast<const f4*>(p) : f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < NS / 4; ++q) {
-        const f4 v = valid ? *reinterpret_cast<const f4*>(p + 4 * q) : f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[4 * q + i] = v[i];
-    }
+    for (int i = 0; i < NS; ++i) h[i] = v[i];
 }
-template <int NS>
 __device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
-#pragma unroll
-    for (int q = 0; q < NS / 4; ++q) *reinterpret_cast<f4*>(p + 4 * q) = f4{h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]};
+    *reinterpret_cast<f4*>(p) = f4{h[0], h[1], h[2], h[3]};
 }
 
 // Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
@@ -225,22 +212,22 @@ struct Place {
 __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
     Place p;
     const uint32_t nct = static_cast<uint32_t>(P.ctiles);
-    uint32_t blk = blockIdx.x;
-    p.ct = blk % nct;
-    blk /= nct;
-    p.b = blk % static_cast<uint32_t>(P.B);
-    p.seg = blk / static_cast<uint32_t>(P.B);
-    const int per_group = P.ctiles / static_cast<int>(P.G);
-    p.g = p.ct / per_group;
-    const int width = static_cast<int>(P.C / P.G), c = (p.ct % per_group) * 64 + lane;
+    // (quotients are worked out in vector registers: readfirstlane says that they are the wave's)
+    const uint32_t blk = blockIdx.x, rest = __builtin_amdgcn_readfirstlane(blk / nct);
+    p.ct = __builtin_amdgcn_readfirstlane(blk - rest * nct);
+    p.seg = __builtin_amdgcn_readfirstlane(rest / static_cast<uint32_t>(P.B));
+    p.b = rest - static_cast<uint32_t>(p.seg) * static_cast<uint32_t>(P.B);
+    const int per_group = __builtin_amdgcn_readfirstlane(P.ctiles / static_cast<int>(P.G));
+    p.g = __builtin_amdgcn_readfirstlane(p.ct / per_group);
+    const int width = __builtin_amdgcn_readfirstlane(static_cast<int>(P.C) / static_cast<int>(P.G)), c = (p.ct - p.g * per_group) * 64 + lane;
     p.valid = c < width;
     p.ch = static_cast<uint32_t>(p.g * width + (p.valid ? c : width - 1));
-    const int64_t T = P.T, first = p.seg * P.seg_len, last = first + P.seg_len;
-    int64_t len = P.lengths != nullptr ? P.lengths[p.b] : T;
+    const int T = static_cast<int>(P.T), seg_len = static_cast<int>(P.seg_len);
+    int len = P.lengths != nullptr ? __builtin_amdgcn_readfirstlane(P.lengths[p.b]) : T;
     len = len < 0 ? 0 : len > T ? T : len;
-    p.t0 = static_cast<int>(first);
-    p.t1 = static_cast<int>(last < T ? last : T);
-    p.te = static_cast<int>(len < p.t0 ? p.t0 : len < p.t1 ? len : p.t1);
+    p.t0 = p.seg * seg_len;
+    p.t1 = T - p.t0 < seg_len ? T : p.t0 + seg_len;
+    p.te = len < p.t0 ? p.t0 : len < p.t1 ? len : p.t1;
     return p;
 }
 
@@ -248,7 +235,7 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
 // the last token to the first: g <- a (g + c gy).
 enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2 };
 
-template <typename T, int NS, int W, int Mode>
+template <typename T, int W, int Mode>
 __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;  // (token, channel) pairs a thread works out
     constexpr bool kWide = sizeof(T) == 4, kOut = Mode == kWalkOut, kAdj = Mode == kWalkAdjoint;
@@ -269,14 +256,14 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
 
     float w2[NS], h[NS];
-    load_states<NS>(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w2);
+    load_states(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w2);
     // (a rate of infinity is held finite, so that a step of zero keeps the state)
 #pragma unroll
     for (int i = 0; i < NS; ++i) w2[i] = -fminf(w2[i], 2e38f) * kLog2e, h[i] = 0.f;
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     if constexpr (kOut) {
-        if (P.nseg > 1) load_states<NS>(P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, p.valid, h);
-        else if (P.s_in != nullptr) load_states<NS>(P.s_in + state, p.valid, h);
+        if (P.nseg > 1) load_states(P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, p.valid, h);
+        else if (P.s_in != nullptr) load_states(P.s_in + state, p.valid, h);
     }
 
     // Inputs come in two tiles ahead, in the raw, and are worked out one tile ahead; a tile's outputs leave while the
@@ -285,9 +272,10 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const T* const first_in = kAdj ? go : x;
     const T* const gate_in = has_z ? z : dt;
     uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
+    const int64_t CB = P.C * static_cast<int64_t>(sizeof(T)), GNB = GN * static_cast<int64_t>(sizeof(T));  // bytes a token
     T rx[kEach], rd[kEach], rz[kEach];
     float ex[3][kEach], ez[3][kEach];
-    Row<T, NS> b, c;
+    Row<T> b, c;
     const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
     const auto fetch = [&](int i) {
         keep32(chb);
@@ -295,17 +283,17 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int at = t + W * k < p.te ? t + W * k : p.te - 1;  // (behind the last token: that one again)
-            const int64_t row = (row0 + at) * P.C;
-            rd[k] = at_bytes(dt + row, chb);
-            rx[k] = at_bytes(first_in + row, chb);
-            if constexpr (kOut || kAdj) rz[k] = at_bytes(gate_in + row, chb);
+            const int64_t row = (row0 + at) * CB;
+            rd[k] = load_at(dt, row, chb);
+            rx[k] = load_at(first_in, row, chb);
+            if constexpr (kOut || kAdj) rz[k] = load_at(gate_in, row, chb);
         }
     };
-    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
+    typename Row<T>::Where where = Row<T>::where(GN, lane);
     const auto fetch_bc = [&](int i) {
         const int t = tile_at(i < ntiles ? i : ntiles - 1);
-        b.fetch(bt + t * GN, where, p.te - t);
-        if constexpr (kOut) c.fetch(ct + t * GN, where, p.te - t);
+        b.fetch(bt, t * GNB, where, p.te - t);
+        if constexpr (kOut) c.fetch(ct, t * GNB, where, p.te - t);
     };
     float total = 0.f;  // of delta
     const auto stage = [&](int i) {
@@ -357,16 +345,16 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     };
     const auto write = [&](int i) {
         const int t = tile_at(i) + wave, left = p.te - t;
-        T* const row = out + (row0 + t) * P.C;
+        const int64_t row = (row0 + t) * CB;
         keep32(chb);
         if (out == nullptr || i < 0) return;
         if (spare || left < kTile) {
 #pragma unroll
             for (int k = 0; k < kEach; ++k)
-                if (W * k < left && p.valid) at_bytes(row + W * k * P.C, chb) = o[k];
+                if (W * k < left && p.valid) store_at(out, row + W * k * CB, chb, o[k]);
         } else {
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) at_bytes(row + W * k * P.C, chb) = o[k];
+            for (int k = 0; k < kEach; ++k) store_at(out, row + W * k * CB, chb, o[k]);
         }
     };
 
@@ -389,7 +377,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     for (int i = 0; i < ntiles; ++i) {
         if constexpr (kOut) {
             if (P.ckpt != nullptr && p.valid)
-                store_states<NS>(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
+                store_states(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
             if (i > 0) add_up(i - 1);
         }
         fetch_bc(i + 1);
@@ -404,12 +392,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
                 else h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
             });
             if constexpr (kOut) {
-                float y;
-                each<NS / 4>([&](auto qq) {
-                    constexpr int s = 4 * decltype(qq)::value;
-                    dot_row<c.template lane_of<j, s>(), (s > 0)>(y, c.template reg<j, s>(), h[s], h[s + 1], h[s + 2], h[s + 3]);
-                });
-                parts[i & 1][wave][j][lane] = y;
+                parts[i & 1][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[0], h[1], h[2], h[3]);
             }
         });
         stage(i + 1);
@@ -434,11 +417,11 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     if constexpr (kOut) {
         if (p.valid) {
             for (int t = p.te + wave; t < p.t1 && out != nullptr; t += W) out[(row0 + t) * P.C + p.ch] = T{0};
-            if (P.s_out != nullptr && p.seg == P.nseg - 1) store_states<NS>(P.s_out + state, h);
+            if (P.s_out != nullptr && p.seg == P.nseg - 1) store_states(P.s_out + state, h);
         }
     } else {
         const int64_t at = static_cast<int64_t>(p.seg) * P.B * P.C;
-        if (p.valid) store_states<NS>(P.local + at * N + state, h);
+        if (p.valid) store_states(P.local + at * N + state, h);
         __syncthreads();
         put[0][wave][lane].x = total;
         __syncthreads();
@@ -476,7 +459,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
 //     g *= a_t,   q = g h_{t-1},   ddelta_t = du_t x_t - sum_n w q,   dw -= delta_t q
 // The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
 // of which every exchange between lanes halves the registers, so 16 tokens end as one number a lane and register.
-template <typename T, int NS, int W>
+template <typename T, int W>
 __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;
     constexpr bool kWide = sizeof(T) == 4;
@@ -499,19 +482,20 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     const int ntiles = (p.te - p.t0 + kTile - 1) / kTile;
 
     float w1[NS], w2[NS], g[NS], dw[NS], first[NS];
-    load_states<NS>(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w1);
+    load_states(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w1);
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     const float* from = P.nseg > 1 ? P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N : P.ds_out;
 #pragma unroll
     for (int i = 0; i < NS; ++i) w1[i] = fminf(w1[i], 2e38f), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
-    if (from != nullptr) load_states<NS>(from + state, p.valid, g);
+    if (from != nullptr) load_states(from + state, p.valid, g);
 
     const bool has_z = z != nullptr, spare = !__all(p.valid);
     const T* const gate_in = has_z ? z : dt;
     uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
+    const int64_t CB = P.C * static_cast<int64_t>(sizeof(T)), GNB = GN * static_cast<int64_t>(sizeof(T));  // bytes a token
     T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
-    Row<T, NS> b, c;
-    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
+    Row<T> b, c;
+    typename Row<T>::Where where = Row<T>::where(GN, lane);
     const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
     const auto fetch = [&](int i) {  // (behind the last token: that one again; before the first tile: nothing new)
         keep32(chb);
@@ -519,15 +503,15 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int at = t + W * k < p.te ? t + W * k : p.te - 1;
-            const int64_t row = (row0 + at) * P.C;
-            rd[k] = at_bytes(dt + row, chb);
-            rx[k] = at_bytes(x + row, chb);
-            rg[k] = at_bytes(go + row, chb);
-            rz[k] = at_bytes(gate_in + row, chb);
+            const int64_t row = (row0 + at) * CB;
+            rd[k] = load_at(dt, row, chb);
+            rx[k] = load_at(x, row, chb);
+            rg[k] = load_at(go, row, chb);
+            rz[k] = load_at(gate_in, row, chb);
         }
-        load_states<NS>(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
-        b.fetch(bt + tile * GN, where, left);
-        c.fetch(ct + tile * GN, where, left);
+        load_states(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
+        b.fetch(bt, tile * GNB, where, left);
+        c.fetch(ct, tile * GNB, where, left);
     };
     float dd = 0.f, dbias = 0.f;
     if (ntiles > 0) fetch(ntiles - 1);
@@ -550,83 +534,72 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             for (int k = 0; k < kEach; ++k)
                 if (!(wave + W * k < n && p.valid)) put[wave + W * k][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float before[NS];
+        float h[kTile + 1][NS], a[kTile][NS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) before[s] = first[s];
+        for (int s = 0; s < NS; ++s) h[0][s] = first[s];
         b.ready();
         c.ready();
         __syncthreads();
         fetch(i - 1);
-        each<NS / 4>([&](auto qq) {  // four states at a time
-            constexpr int q = decltype(qq)::value;
-            float h[kTile + 1][4], a[kTile][4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) h[0][s] = before[4 * q + s];
-            each<kTile>([&](auto jj) {
-                constexpr int j = decltype(jj)::value;
-                const float4 v = put[j][lane];
-                float y;
-                if constexpr (q > 0) y = parts[0][wave][j][lane];
-                each<4>([&](auto ss) {
-                    constexpr int s = decltype(ss)::value;
-                    a[j][s] = exp2_fast(v.x * w2[4 * q + s]);
-                    h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, 4 * q + s>() * v.y);
-                });
-                dot_row<c.template lane_of<j, 4 * q>(), (q > 0)>(y, c.template reg<j, 4 * q>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
-                parts[0][wave][j][lane] = y;
+        each<kTile>([&](auto jj) {
+            constexpr int j = decltype(jj)::value;
+            const float4 v = put[j][lane];
+            each<NS>([&](auto ss) {
+                constexpr int s = decltype(ss)::value;
+                a[j][s] = exp2_fast(v.x * w2[s]);
+                h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, s>() * v.y);
             });
-            b.forget();
-            c.forget();
-            float tokens[8];
-            each<kTile>([&](auto jj) {
-                constexpr int j = kTile - 1 - decltype(jj)::value;
-                const float4 v = put[j][lane];
-                float du, down = q > 0 ? parts[2][wave][j][lane] : 0.f, r[4];
-                if constexpr (q > 0) du = parts[1][wave][j][lane];
-                add_dot_row<c.template lane_of<j, 4 * q>(), (q > 0)>(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3], du,
-                                                            c.template reg<j, 4 * q>(), v.z, b.template reg<j, 4 * q>());
-                each<4>([&](auto ss) {
-                    constexpr int s = decltype(ss)::value, s4 = 4 * q + s;
-                    const float pb = g[s4] * v.y, pc = v.z * h[j + 1][s];
-                    g[s4] *= a[j][s];
-                    const float m = g[s4] * h[j][s];
-                    down = fmaf(m, w1[s4], down);
-                    dw[s4] = fmaf(-m, v.x, dw[s4]);
-                    // db to the lower half of the lanes, dc to the upper
-                    const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(pb), __float_as_uint(pc), false, false);
-                    r[s] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
-                });
-                parts[1][wave][j][lane] = du;
-                parts[2][wave][j][lane] = down;
-                // states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones
-                float m2[2];
+            parts[0][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
+        });
+        b.forget();
+        c.forget();
+        float tokens[8];
+        each<kTile>([&](auto jj) {
+            constexpr int j = kTile - 1 - decltype(jj)::value;
+            const float4 v = put[j][lane];
+            float down = 0.f, r[NS];
+            add_row<c.template lane_of<j>()>(g, c.template reg<j>(), v.z);
+            parts[1][wave][j][lane] = dot_row<b.template lane_of<j>()>(b.template reg<j>(), g[0], g[1], g[2], g[3]);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[s]), __float_as_uint(r[s + 2]), false, false);
-                    m2[s] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+            for (int s = 0; s < NS; ++s) {
+                const float pb = g[s] * v.y, pc = v.z * h[j + 1][s];
+                g[s] *= a[j][s];
+                const float m = g[s] * h[j][s];
+                down = fmaf(m, w1[s], down);
+                dw[s] = fmaf(-m, v.x, dw[s]);
+                // db to the lower half of the lanes, dc to the upper
+                const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(pb), __float_as_uint(pc), false, false);
+                r[s] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+            }
+            parts[2][wave][j][lane] = down;
+            // states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones
+            float m2[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[s]), __float_as_uint(r[s + 2]), false, false);
+                m2[s] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+            }
+            m2[0] += dpp<0x128>(m2[0]);  // row_ror:8
+            m2[1] += dpp<0x128>(m2[1]);
+            tokens[j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
+            if constexpr ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float lo = tokens[k] + dpp<0x141>(tokens[k]), hi = tokens[k + 4] + dpp<0x141>(tokens[k + 4]);  // row_half_mirror
+                    tokens[k] = (lane & 4) != 0 ? hi : lo;
                 }
-                m2[0] += dpp<0x128>(m2[0]);  // row_ror:8
-                m2[1] += dpp<0x128>(m2[1]);
-                tokens[j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
-                if constexpr ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float lo = tokens[k] + dpp<0x141>(tokens[k]), hi = tokens[k + 4] + dpp<0x141>(tokens[k + 4]);  // row_half_mirror
-                        tokens[k] = (lane & 4) != 0 ? hi : lo;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 2] + dpp<0x4E>(tokens[k + 2]);  // lane ^ 2
-                        tokens[k] = (lane & 2) != 0 ? hi : lo;
-                    }
-                    const float lo = tokens[0] + dpp<0xB1>(tokens[0]), hi = tokens[1] + dpp<0xB1>(tokens[1]);  // lane ^ 1
-                    const int tok = j + (lane & 7);
-                    if (tok < n) {
-                        const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
-                        P.part[row + (lane >> 5) * N + wave * NS + 4 * q + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = (lane & 1) != 0 ? hi : lo;
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 2] + dpp<0x4E>(tokens[k + 2]);  // lane ^ 2
+                    tokens[k] = (lane & 2) != 0 ? hi : lo;
                 }
-            });
+                const float lo = tokens[0] + dpp<0xB1>(tokens[0]), hi = tokens[1] + dpp<0xB1>(tokens[1]);  // lane ^ 1
+                const int tok = j + (lane & 7);
+                if (tok < n) {
+                    const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
+                    P.part[row + (lane >> 5) * N + wave * NS + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = (lane & 1) != 0 ? hi : lo;
+                }
+            }
         });
         __syncthreads();
         T oz[kEach], ox[kEach], od[kEach];
@@ -645,15 +618,23 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             dd = fmaf(v.z, v.w, dd);
             dbias += gd;
         }
-        const int64_t row = (row0 + t + wave) * P.C;
+        const int64_t row = (row0 + t + wave) * CB;
         keep32(chb);
+        if (!edge) {
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            if (edge && !(wave + W * k < n && p.valid)) continue;
-            const int64_t at = row + W * k * P.C;
-            at_bytes(dx + at, chb) = ox[k];
-            at_bytes(ddt + at, chb) = od[k];
-            if (has_z) at_bytes(dz + at, chb) = oz[k];
+            for (int k = 0; k < kEach; ++k) {
+                store_at(dx, row + W * k * CB, chb, ox[k]);
+                store_at(ddt, row + W * k * CB, chb, od[k]);
+                if (has_z) store_at(dz, row + W * k * CB, chb, oz[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                if (!(wave + W * k < n && p.valid)) continue;
+                store_at(dx, row + W * k * CB, chb, ox[k]);
+                store_at(ddt, row + W * k * CB, chb, od[k]);
+                if (has_z) store_at(dz, row + W * k * CB, chb, oz[k]);
+            }
         }
     }
     if (p.valid) {
@@ -662,8 +643,8 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             dx[at] = ddt[at] = T{0};
             if (z != nullptr) dz[at] = T{0};
         }
-        store_states<NS>(P.dw_part + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, dw);
-        if (P.ds_in != nullptr && p.seg == 0) store_states<NS>(P.ds_in + state, g);
+        store_states(P.dw_part + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, dw);
+        if (P.ds_in != nullptr && p.seg == 0) store_states(P.ds_in + state, g);
     }
     __syncthreads();
     put[wave][lane].x = dd;
@@ -732,8 +713,8 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     const T* __restrict__ cc = static_cast<const T*>(P.c);
     const int64_t state = bc * P.N + 4 * q;
     float h[4] = {0.f, 0.f, 0.f, 0.f}, w2[4];
-    if (P.s_in != nullptr) load_states<4>(P.s_in + state, true, h);
-    load_states<4>(P.w + ch * P.N + 4 * q, true, w2);
+    if (P.s_in != nullptr) load_states(P.s_in + state, true, h);
+    load_states(P.w + ch * P.N + 4 * q, true, w2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) w2[s] = -fminf(w2[s], 2e38f) * kLog2e;
     const float bias = P.dt_bias != nullptr ? P.dt_bias[ch] : 0.f, skip = P.d != nullptr ? P.d[ch] : 0.f;
@@ -763,17 +744,17 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
         y = sum_lanes(y, lanes);
         if (valid && q == 0) static_cast<T*>(P.out)[at] = live ? narrow<T>(fmaf(skip, vx, y) * gate) : T{0};
     }
-    if (valid && P.s_out != nullptr) store_states<4>(P.s_out + state, h);
+    if (valid && P.s_out != nullptr) store_states(P.s_out + state, h);
 }
 
-template <typename T, int NS, int W>
+template <typename T, int W>
 hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(a.ctiles * a.B * a.nseg)), block(64 * W);
     switch (mode) {
-        case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkOut>), grid, block, 0, stream, a); break;
-        case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkLocal>), grid, block, 0, stream, a); break;
-        case kWalkAdjoint: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkAdjoint>), grid, block, 0, stream, a); break;
-        default: hipLaunchKernelGGL((select_grad_kernel<T, NS, W>), grid, block, 0, stream, a); break;
+        case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkOut>), grid, block, 0, stream, a); break;
+        case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkLocal>), grid, block, 0, stream, a); break;
+        case kWalkAdjoint: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkAdjoint>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((select_grad_kernel<T, W>), grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
 }
@@ -783,10 +764,9 @@ constexpr int kGrad = 3;
 template <typename T>
 hipError_t walk_n(const SelectArgs& a, int mode, hipStream_t stream) {
     switch (a.N) {
-        case 8: return walk_t<T, 4, 2>(a, mode, stream);
-        case 16: return walk_t<T, 4, 4>(a, mode, stream);
-        case 32: return walk_t<T, 4, 8>(a, mode, stream);
-        default: return walk_t<T, 8, 8>(a, mode, stream);
+        case 8: return walk_t<T, 2>(a, mode, stream);
+        case 16: return walk_t<T, 4>(a, mode, stream);
+        default: return walk_t<T, 8>(a, mode, stream);
     }
 }
 

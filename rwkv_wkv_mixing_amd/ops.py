@@ -1161,8 +1161,8 @@ def _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths):
     B, T, C = shape = x.shape
     _need(dt, "dt", ty, shape, dev)
     _need(w, "w", torch.float32, None, dev)
-    if w.dim() != 2 or w.shape[0] != C or w.shape[1] not in (8, 16, 32, 64):
-        raise ValueError(f"w has shape {tuple(w.shape)}, expected ({C}, N) with N 8, 16, 32 or 64")
+    if w.dim() != 2 or w.shape[0] != C or w.shape[1] not in (8, 16, 32):
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected ({C}, N) with N 8, 16 or 32")
     N = w.shape[1]
     _need(b, "b", ty, None, dev)
     if b.dim() != 3 or b.shape[0] != B or b.shape[1] != T or b.shape[2] % N or not b.shape[2] or C % (b.shape[2] // N):
@@ -1198,8 +1198,8 @@ def _select_ckpt(ckpt, B, T, C, N, dev):
 
 def select_forward(x, dt, w, b, c, *, d=None, z=None, dt_bias=None, softplus=True, lengths=None, state_in=None,
                    state_out=None, return_state=False, out=None, ckpt=None, workspace=None, split=True, bind=False):
-    """The selective state space scan: out [B, T, C] from x, dt [B, T, C], rates w [C, N] float32 (N 8, 16, 32 or
-    64; decay e^{-delta w}), b, c [B, T, G N] (channel ch reads group ch // (C // G)), d [C] float32, z [B, T, C] and
+    """The selective state space scan: out [B, T, C] from x, dt [B, T, C], rates w [C, N] float32 (N 8, 16 or 32;
+    decay e^{-delta w}), b, c [B, T, G N] (channel ch reads group ch // (C // G)), d [C] float32, z [B, T, C] and
     dt_bias [C] float32, the last three or None; x, dt, b, c, z float32 or bfloat16 alike, out too.  Per token
     delta = softplus(dt + dt_bias) (softplus=False: dt + dt_bias), h = e^{-delta w} h + delta x b,
     y = <c, h> + d x, out = y silu(z) (y without z).  States and sums are float32.

@@ -5,7 +5,7 @@ n tokens have carried has taken n multiply-adds (u each) and n decays e^{-delta 
 delta w log2 e, where delta, good to 8u (softplus: the exponential's, the polynomial's and the sum's), the rate and the
 products add 11u of the exponent; exponents of a term add up to at most its whole decay, and E e^{-E} < 0.4, so they
 cost it 11u at most times 0.4 of what was written.  A term's other factors (delta, x, b, c, the gate's sigmoid: 8u + 4u +
-6u), and the sums over at most 64 states, over tokens and over channels add (64 + T + C)u.  With bf16 outputs, 2^-8 of the
+6u), and the sums over at most 32 states, over tokens and over channels add (64 + T + C)u.  With bf16 outputs, 2^-8 of the
 result on top.  In all: (3 T + C + 128)u M (2^-8 |result| more in bf16); a gradient's chain runs through both directions, twice that."""
 import numpy as np
 import pytest
@@ -89,7 +89,7 @@ def check_all(p, **kw):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("B,T,C,G,N", [(2, 1, 5, 1, 8), (1, 15, 64, 1, 16), (2, 16, 64, 1, 16), (3, 17, 65, 1, 16), (2, 33, 130, 2, 8),
-                                       (1, 40, 66, 3, 32), (2, 50, 70, 1, 64), (1, 100, 1, 1, 16)])
+                                       (1, 40, 66, 3, 32), (2, 50, 70, 1, 32), (1, 100, 1, 1, 16)])
 def test_select(B, T, C, G, N, dtype):
     check_all(draw(B, T, C, G, N, dtype))
 
@@ -154,7 +154,7 @@ def test_recomputed_states_give_the_same_bits(dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("T", [1, 2, 7, 8, 9])
-@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("N", [8, 16, 32])
 def test_decode(T, N, dtype):
     """A few tokens with the state in place, ragged; then one token after the other to the same states."""
     B, C, G = 3, 21, 3
