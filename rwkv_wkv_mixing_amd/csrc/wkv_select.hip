@@ -84,6 +84,7 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 // a 64-bit place shifted by the size of an element is worked out lane by lane.
 template <typename T>
 __device__ __forceinline__ T load_at(const T* p, int64_t at, uint32_t bytes) {
+    asm("" : "+s"(at));
     return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + at + bytes);
 }
 template <typename T>
