@@ -795,7 +795,7 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
  *           256-byte aligned (WKV_EWORKSPACE otherwise); clobbered.
  * w, b, c, s_in, s_out, ckpt are 16-byte aligned, the other tensors to their
  * elements (WKV_EALIGN otherwise).
- * WKV_ESIZE from T = 2^31, B = 2^31, C N = 2^30, G N = 2^25, B G ceil(C / G / 64) = 2^22
+ * WKV_ESIZE from T = 2^31 - 64, B = 2^31, C N = 2^30, G N = 2^25, B G ceil(C / G / 64) = 2^22
  * (for up to 8 tokens without a ckpt instead from B C N = 2^33); in the backward also
  * from B T G N = 2^30.
  */

@@ -1065,18 +1065,20 @@ bool conv_vec(int64_t C, int dt, const float* weight, const float* bias, P... p)
 struct SelectPlan {
     wkv_status_t st;
     int64_t ns;            // numbers of state
-    int64_t tiles, ctiles, nseg, per;
+    int64_t tiles, ctiles;
+    int64_t nseg, per;     // of a time split
+    int64_t fwd_nseg, fwd_per;  // of the forward's, by which a backward recomputes the states to the same bits
     size_t ckpt, part, dwp, vecp, split;  // bytes
 };
 
 SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dt, bool steps, bool bwd) {
-    const auto bad = [](wkv_status_t st) { return SelectPlan{st, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0}; };
+    const auto bad = [](wkv_status_t st) { return SelectPlan{st, 0, 0, 0, 1, 0, 1, 0, 0, 0, 0, 0, 0}; };
     if (B < 0 || T < 0 || C < 0 || G < 1 || (N != 8 && N != 16 && N != 32) || C % G != 0) return bad(WKV_EINVAL);
     if (!dtype_ok(dt)) return bad(WKV_EDTYPE);
-    SelectPlan p{WKV_OK, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0};
+    SelectPlan p{WKV_OK, 0, 0, 0, 1, 0, 1, 0, 0, 0, 0, 0, 0};
     constexpr int64_t kMost = int64_t{1} << 31, kBig = int64_t{1} << 58;
     int64_t n, cn, gn, bct, ck;
-    if (B >= kMost || T >= kMost) return bad(WKV_ESIZE);
+    if (B >= kMost || T >= kMost - 64) return bad(WKV_ESIZE);
     if (!mul3(C, N, 1, &cn) || cn >= (int64_t{1} << 30) || !mul3(G, N, 1, &gn) || gn >= (int64_t{1} << 25)) return bad(WKV_ESIZE);
     if (!mul3(B, T, C, &n) || n > kBig || !mul3(B, cn, 1, &p.ns) || p.ns > kBig || !mul3(B, T, gn, &bct) || bct > kBig)
         return bad(WKV_ESIZE);
@@ -1090,9 +1092,12 @@ SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, in
     const auto bytes = [](int64_t k) { return (static_cast<size_t>(k) * sizeof(float) + 255) / 256 * 256; };
     if (!mul3(p.ns, p.tiles, 1, &ck) || ck > kBig) return bad(WKV_ESIZE);
     p.ckpt = static_cast<size_t>(ck) * sizeof(float);
-    p.nseg = steps ? 1 : wkv::select_segments(B, T, ctiles, &p.per);
-    if (steps) p.per = T;
-    if (p.nseg > 1) p.split = bytes(p.nseg * p.ns) + bytes(p.nseg * B * C);
+    if (steps) return p;
+    p.fwd_nseg = wkv::select_segments(B, T, ctiles, N, false, &p.fwd_per);
+    p.nseg = bwd ? wkv::select_segments(B, T, ctiles, N, true, &p.per) : p.fwd_nseg;
+    if (!bwd) p.per = p.fwd_per;
+    const int64_t most = p.nseg > p.fwd_nseg ? p.nseg : p.fwd_nseg;
+    if (most > 1) p.split = bytes(most * p.ns) + bytes(most * B * C);
     if (bwd) {
         int64_t part, rows;
         if (!mul3(B, T, 2 * N, &rows) || !mul3(rows, ctiles, 1, &part) || part > kBig) return bad(WKV_ESIZE);
@@ -1104,11 +1109,11 @@ SelectPlan select_plan(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, in
 }
 
 // Where a time split keeps what its segments do.
-void select_split(wkv::SelectArgs* a, const SelectPlan& p, char* scratch) {
-    a->nseg = p.nseg;
-    a->seg_len = p.per;
+void select_split(wkv::SelectArgs* a, int64_t nseg, int64_t per, int64_t ns, char* scratch) {
+    a->nseg = nseg;
+    a->seg_len = per;
     a->local = reinterpret_cast<float*>(scratch);
-    a->steps = a->local + (p.nseg * p.ns + 63) / 64 * 64;
+    a->steps = a->local + (nseg * ns + 63) / 64 * 64;
 }
 
 bool finite_in(float v, float most) { return v >= 0.f && v <= most; }
@@ -1300,7 +1305,7 @@ wkv_status_t wkv_select_forward(int64_t B, int64_t T, int64_t C, int64_t G, int6
     a.ckpt = static_cast<float*>(ckpt);
     a.seg_len = p.tiles * wkv::kSelectTile;
     if (steps) return hip_status(wkv::launch_select_step(a, stream));
-    if (workspace && p.nseg > 1) select_split(&a, p, static_cast<char*>(workspace));
+    if (workspace && p.nseg > 1) select_split(&a, p.nseg, p.per, p.ns, static_cast<char*>(workspace));
     return hip_status(wkv::launch_select_fwd(a, stream));
 }
 
@@ -1333,15 +1338,17 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
     a.tiles = p.tiles;
     a.ctiles = static_cast<int>(p.ctiles);
     a.seg_len = p.tiles * wkv::kSelectTile;
-    if (p.nseg > 1 && workspace_bytes >= unsplit + p.split) select_split(&a, p, ws + unsplit);
+    const bool room = p.split > 0 && workspace_bytes >= unsplit + p.split;
     a.saved = static_cast<const float*>(ckpt);
     if (ckpt == nullptr) {  // by a forward pass without outputs
         wkv::SelectArgs f = a;
+        if (room && p.fwd_nseg > 1) select_split(&f, p.fwd_nseg, p.fwd_per, p.ns, ws + unsplit);
         f.ckpt = reinterpret_cast<float*>(ws + p.part + p.dwp + p.vecp);
         const hipError_t e = wkv::launch_select_fwd(f, stream);
         if (e != hipSuccess) return hip_status(e);
         a.saved = f.ckpt;
     }
+    if (room && p.nseg > 1) select_split(&a, p.nseg, p.per, p.ns, ws + unsplit);
     a.go = go;
     a.ds_out = ds_out;
     a.dx = dx;

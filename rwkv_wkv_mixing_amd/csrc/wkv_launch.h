@@ -473,7 +473,7 @@ hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream);
 hipError_t launch_select_fwd(const SelectArgs& a, hipStream_t stream);
 hipError_t launch_select_bwd(const SelectArgs& a, hipStream_t stream);
 // segments for a time split (1: no split), *per tokens each
-int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t* per);
+int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bwd, int64_t* per);
 
 // decode step (wkv_step.hip)
 hipError_t launch_step(const StepArgs& s, hipStream_t stream);

@@ -232,6 +232,17 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
     return p;
 }
 
+// Two workgroups on a compute unit do not share it evenly: the waves that came first go first, so one workgroup is done
+// early and the other one walks its rest alone, which leaves the vector units waiting (132 and 182 us at B = 8, T = 1024,
+// C = 4096).  A wave's priority falls with every quarter of its tiles, so that who is behind goes first.
+__device__ __forceinline__ void yield_to_later(int done, int all) {
+    const int quarter = (all + 3) / 4;
+    if (done == 0) __builtin_amdgcn_s_setprio(3);
+    else if (done == quarter) __builtin_amdgcn_s_setprio(2);
+    else if (done == 2 * quarter) __builtin_amdgcn_s_setprio(1);
+    else if (done == 3 * quarter) __builtin_amdgcn_s_setprio(0);
+}
+
 // What a walk does: the outputs; what each segment does to a state of zero; the same for the states' gradients, from
 // the last token to the first: g <- a (g + c gy).
 enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2 };
@@ -376,6 +387,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         __syncthreads();
     }
     for (int i = 0; i < ntiles; ++i) {
+        yield_to_later(i, ntiles);
         if constexpr (kOut) {
             if (P.ckpt != nullptr && p.valid)
                 store_states(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
@@ -517,6 +529,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     float dd = 0.f, dbias = 0.f;
     if (ntiles > 0) fetch(ntiles - 1);
     for (int i = ntiles - 1; i >= 0; --i) {
+        yield_to_later(ntiles - 1 - i, ntiles);
         const int t = tile_at(i), n = p.te - t;
         float egs[kEach], eslope[kEach], delta[kEach];
 #pragma unroll
@@ -783,17 +796,29 @@ hipError_t chain(const SelectArgs& a, bool reverse, hipStream_t stream) {
 
 }  // namespace
 
-int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t* per) {
-    const int64_t whole = (T + kTile - 1) / kTile * kTile, groups = B * ctiles;
-    *per = whole;
-    if (groups <= 0 || groups >= 256 || T < 256) return 1;
-    int64_t n = (1024 + groups - 1) / groups;
-    const int64_t most = T / 128;
-    n = n < most ? n : most;
-    if (n < 3) return 1;
-    const int64_t tiles = (T + kTile - 1) / kTile;
-    *per = (tiles + n - 1) / n * kTile;
-    return (T + *per - 1) / *per;
+// A time split walks everything twice (once for what the segments do to a state of zero, then from their start states), and
+// pays where the channel tiles alone leave most of the card idle or there are tokens without end.  The model, in us: a
+// tile of 16 tokens takes a workgroup on a compute unit of its own about `alone`, and the unit's workgroups together at
+// least 0.35 a wave; the backward 2.6 times that; the second walk 0.8 of the first; its launches 8.
+int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bwd, int64_t* per) {
+    const int64_t tiles = (T + kTile - 1) / kTile, groups = B * ctiles;
+    *per = tiles * kTile;
+    if (groups <= 0 || groups >= 512 || tiles < 4) return 1;
+    const double alone = N == 8 ? 2.4 : 1.7, shared = 0.35 * (N / 4), scale = bwd ? 2.6 : 1.0;
+    const auto tile_us = [&](int64_t workgroups) {
+        const double busy = shared * static_cast<double>((workgroups + 255) / 256);
+        return scale * (busy > alone ? busy : alone);
+    };
+    double best = static_cast<double>(tiles) * tile_us(groups);
+    int64_t n = 1;
+    for (int64_t each = 2; each < tiles; each = each < 16 ? each + 1 : each + each / 8) {
+        const int64_t k = (tiles + each - 1) / each;
+        if (groups * k > (int64_t{1} << 20)) continue;
+        const double second = bwd ? 1.0 + 0.8 / 2.6 : 1.8;
+        const double us = second * static_cast<double>(each) * tile_us(groups * k) + 8.0 + 0.1 * static_cast<double>(k);
+        if (us < best) best = us, n = k, *per = each * kTile;
+    }
+    return n;
 }
 
 hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream) {
