@@ -749,7 +749,7 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
  * tokens in a fixed order; all outputs are overwritten.
  * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
  *           clobbered.  Not needed without tokens.
- * WKV_ESIZE from T = 2^31, B = 2^31 or C = 2^26.
+ * WKV_ESIZE from T = 2^31 - 64, B = 2^31 or C = 2^26.
  */
 size_t wkv_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K);
 wkv_status_t wkv_conv_forward(int64_t B, int64_t T, int64_t C, int64_t K, int in_dtype, int act, const int32_t* lengths,

@@ -1047,7 +1047,7 @@ ConvPlan conv_plan(int64_t B, int64_t T, int64_t C, int64_t K, int dt, int act) 
     if (!dtype_ok(dt)) return bad(WKV_EDTYPE);
     constexpr int64_t kMost = int64_t{1} << 31;
     ConvPlan p{WKV_OK, 0, 0, 0};
-    if (B >= kMost || T >= kMost || C >= (int64_t{1} << 26)) return bad(WKV_ESIZE);
+    if (B >= kMost || T >= kMost - 64 || C >= (int64_t{1} << 26)) return bad(WKV_ESIZE);
     if (!mul3(B, T, C, &p.n) || p.n > (int64_t{1} << 58) || !mul3(B, K - 1, C, &p.ns)) return bad(WKV_ESIZE);
     // grids of two dimensions of 2^20 and 2^16 workgroups at most, one for 16 tokens of 64 channels
     int64_t blocks;

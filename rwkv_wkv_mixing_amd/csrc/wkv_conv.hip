@@ -17,7 +17,6 @@
 
 namespace wkv {
 namespace {
-
 constexpr int kThreads = 256, kCols = 64, kRuns = kThreads / kCols;  // a workgroup: 64 vectors of channels, 4 runs
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
@@ -42,6 +41,20 @@ struct Vec<float, 1> {
     static __device__ __forceinline__ Raw narrow(const float (&f)[1]) { return f[0]; }
 };
 template <>
+struct Vec<float, 2> {
+    typedef f2 Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[2]) { f[0] = r.x, f[1] = r.y; }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[2]) { return Raw{f[0], f[1]}; }
+};
+template <>
+struct Vec<uint16_t, 2> {
+    typedef uint32_t Raw;
+    static __device__ __forceinline__ void widen(Raw r, float (&f)[2]) {
+        f[0] = __uint_as_float(r << 16), f[1] = __uint_as_float(r & 0xffff0000u);
+    }
+    static __device__ __forceinline__ Raw narrow(const float (&f)[2]) { return pk2(f[0], f[1]); }
+};
+template <>
 struct Vec<uint16_t, 4> {
     typedef u2 Raw;
     static __device__ __forceinline__ void widen(Raw r, float (&f)[4]) {
@@ -60,27 +73,46 @@ struct Vec<uint16_t, 1> {
 };
 
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * 1.44269504f)); }
-__device__ __forceinline__ float act_of(int act, float v) {
-    return act == kActNone ? v : act == kActSigmoid ? sigmoid(v) : v * sigmoid(v);
+// act(v), and g act'(v): the activation is looked up once for all of them.
+template <int V>
+__device__ __forceinline__ void act_of(int act, float (&v)[V]) {
+    if (act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
+    } else if (act == kActSigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = sigmoid(v[i]);
+    }
 }
-__device__ __forceinline__ float act_grad(int act, float v) {
-    if (act == kActNone) return 1.f;
-    const float p = sigmoid(v);
-    return act == kActSigmoid ? p * (1.f - p) : p * fmaf(v, 1.f - p, 1.f);
+template <int V>
+__device__ __forceinline__ void act_grad(int act, const float (&v)[V], float (&g)[V]) {
+    if (act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = sigmoid(v[i]);
+            g[i] *= p * fmaf(v[i], 1.f - p, 1.f);
+        }
+    } else if (act == kActSigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = sigmoid(v[i]);
+            g[i] *= p * (1.f - p);
+        }
+    }
 }
 
 // A row's tokens.
-__device__ __forceinline__ int64_t row_length(const ConvArgs& P, int64_t b) {
-    const int64_t len = P.lengths != nullptr ? P.lengths[b] : P.T;
-    return len < 0 ? 0 : len > P.T ? P.T : len;
+__device__ __forceinline__ int row_length(const ConvArgs& P, int64_t b) {
+    const int all = static_cast<int>(P.T), len = P.lengths != nullptr ? __builtin_amdgcn_readfirstlane(P.lengths[b]) : all;
+    return len < 0 ? 0 : len > all ? all : len;
 }
 
 // V elements of channel c at row e of X (zeros where there is none: before the carried inputs when none are given,
 // and behind the row's length).
 template <typename T, int V>
-__device__ __forceinline__ typename Vec<T, V>::Raw load_ext(const ConvArgs& P, int64_t b, int64_t len, int64_t e, int64_t c, int K) {
+__device__ __forceinline__ typename Vec<T, V>::Raw load_ext(const ConvArgs& P, int64_t b, int len, int e, int64_t c, int K) {
     typedef typename Vec<T, V>::Raw Raw;
-    const int64_t t = e - (K - 1);
+    const int t = e - (K - 1);
     if (t >= len) return Raw{};
     if (t >= 0) return *reinterpret_cast<const Raw*>(static_cast<const T*>(P.x) + (b * P.T + t) * P.C + c);
     if (P.s_in == nullptr) return Raw{};
@@ -93,11 +125,12 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
     typedef typename Ops::Raw Raw;
     constexpr int kAhead = 8;  // tokens whose loads are on their way at once
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-    const int64_t cb = blk % ncb, rest = blk / ncb, ntb = (P.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
-    const int64_t b = rest / ntb, t0 = (rest % ntb) * kRuns * run + (threadIdx.x / kCols) * static_cast<int64_t>(run);
-    const int64_t c = (cb * kCols + threadIdx.x % kCols) * V;
-    if (b >= P.B || c >= P.C || t0 >= P.T) return;
-    const int64_t t1 = t0 + run < P.T ? t0 + run : P.T, len = row_length(P, b), te = len < t1 ? len : t1;
+    const int64_t cb = blk % ncb, rest = blk / ncb, ntb = (P.T + kRuns * run - 1) / (kRuns * run);
+    const int64_t b = rest / ntb, c = (cb * kCols + threadIdx.x % kCols) * V;
+    const int64_t first = (rest % ntb) * kRuns * run + __builtin_amdgcn_readfirstlane(threadIdx.x / kCols) * run;
+    if (b >= P.B || c >= P.C || first >= P.T) return;
+    const int all = static_cast<int>(P.T), t0 = static_cast<int>(first), t1 = all - t0 < run ? all : t0 + run, len = row_length(P, b),
+              te = len < t1 ? len : t1;
     float w[K][V], bias[V], win[K][V];
 #pragma unroll
     for (int j = 0; j < K; ++j)
@@ -117,10 +150,11 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
     }
     const T* x = static_cast<const T*>(P.x) + (b * P.T) * P.C + c;
     T* out = static_cast<T*>(P.out) + (b * P.T) * P.C + c;
-    for (int64_t t = t0; t < te; t += kAhead) {
+    for (int t = t0; t < te; t += kAhead) {
         Raw raw[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) raw[k] = t + k < te ? *reinterpret_cast<const Raw*>(x + (t + k) * P.C) : Raw{};
+        for (int k = 0; k < kAhead; ++k)  // (behind the last token: that one again)
+            raw[k] = *reinterpret_cast<const Raw*>(x + static_cast<int64_t>(t + k < te ? t + k : te - 1) * P.C);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (t + k < te) {
@@ -128,12 +162,12 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float pre = bias[i];
+                    o[i] = bias[i];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) pre = fmaf(w[j][i], win[j][i], pre);
-                    o[i] = act_of(P.act, pre);
+                    for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], win[j][i], o[i]);
                 }
-                *reinterpret_cast<Raw*>(out + (t + k) * P.C) = Ops::narrow(o);
+                act_of(P.act, o);
+                *reinterpret_cast<Raw*>(out + static_cast<int64_t>(t + k) * P.C) = Ops::narrow(o);
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
 #pragma unroll
@@ -141,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
             }
         }
     }
-    for (int64_t t = te > t0 ? te : t0; t < t1; ++t) *reinterpret_cast<Raw*>(out + t * P.C) = Raw{};
+    for (int t = te > t0 ? te : t0; t < t1; ++t) *reinterpret_cast<Raw*>(out + static_cast<int64_t>(t) * P.C) = Raw{};
     if (carry) {  // (s_out may be s_in: this thread alone reads and writes these rows of it)
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
@@ -158,10 +192,10 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t cb = blk % ncb, slot = blk / ncb;
     if (slot >= P.slots) return;  // (the whole workgroup)
-    const int col = threadIdx.x % kCols, r = threadIdx.x / kCols;
+    const int col = threadIdx.x % kCols, r = __builtin_amdgcn_readfirstlane(threadIdx.x / kCols);
     const int64_t c = (cb * kCols + col) * V;
     const bool valid = c < P.C;
-    const int64_t ntb = (P.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
+    const int64_t ntb = (P.T + kRuns * run - 1) / (kRuns * run);
     float w[K][V], bias[V], dw[K][V], db[V];
 #pragma unroll
     for (int j = 0; j < K; ++j)
@@ -171,9 +205,9 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
     for (int i = 0; i < V; ++i) bias[i] = valid && P.bias != nullptr ? P.bias[c + i] : 0.f, db[i] = 0.f;
     // tiles of kRuns runs, every slots-th one
     for (int64_t tile = slot; tile < P.B * ntb; tile += P.slots) {
-        const int64_t b = tile / ntb, t0 = (tile % ntb) * kRuns * run + r * static_cast<int64_t>(run);
-        if (!valid || t0 >= P.T) continue;
-        const int64_t t1 = t0 + run < P.T ? t0 + run : P.T, len = row_length(P, b);
+        const int64_t b = tile / ntb, first = (tile % ntb) * kRuns * run + r * run;
+        if (!valid || first >= P.T) continue;
+        const int all = static_cast<int>(P.T), t0 = static_cast<int>(first), t1 = all - t0 < run ? all : t0 + run, len = row_length(P, b);
         const T* x = static_cast<const T*>(P.x) + (b * P.T) * P.C + c;
         const T* go = static_cast<const T*>(P.gout) + (b * P.T) * P.C + c;
         T* dx = static_cast<T*>(P.dx) + (b * P.T) * P.C + c;
@@ -188,52 +222,89 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
         }
         // row e = t of X (token t - (K - 1)) has all its g once token t is done; the run answers for the tokens
         // t0 .. t1 - 1, and the first one for the carried inputs too
-        const int64_t end = t1 + K - 1, live = len < end ? len : end;
-        for (int64_t tt = t0; tt < end; tt += kAhead) {
-            Raw rx[kAhead], rg[kAhead];
+        const int end = t1 + K - 1, live = len < end ? len : end;
+        // one token: its g into the window's last row, and (own) its part of the weights' sums
+        const auto take = [&](Raw rx, Raw rg, bool own) {
+            float pre[V];
+            Ops::widen(rx, win[K - 1]);
+            Ops::widen(rg, g[K - 1]);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const bool is = tt + k < live;
-                rx[k] = is ? *reinterpret_cast<const Raw*>(x + (tt + k) * P.C) : Raw{};
-                rg[k] = is ? *reinterpret_cast<const Raw*>(go + (tt + k) * P.C) : Raw{};
+            for (int i = 0; i < V; ++i) {
+                pre[i] = bias[i];
+#pragma unroll
+                for (int j = 0; j < K; ++j) pre[i] = fmaf(w[j][i], win[j][i], pre[i]);
             }
+            act_grad(P.act, pre, g[K - 1]);
+            if (own) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+#pragma unroll
+                    for (int j = 0; j < K; ++j) dw[j][i] = fmaf(g[K - 1][i], win[j][i], dw[j][i]);
+                    db[i] += g[K - 1][i];
+                }
+            }
+        };
+        // dX at the window's first row: sum_j weight[j] g_{t - j}
+        const auto give = [&](float (&o)[V]) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                o[i] = w[0][i] * g[K - 1][i];
+#pragma unroll
+                for (int j = 1; j < K; ++j) o[i] = fmaf(w[j][i], g[K - 1 - j][i], o[i]);
+            }
+        };
+        const auto shift = [&] {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i], g[j][i] = g[j + 1][i];
+        };
+        Raw rx[kAhead], rg[kAhead];
+        const auto fetch = [&](int tt) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int64_t t = tt + k;
-                if (t >= end) continue;
+                rx[k] = rg[k] = Raw{};
+                if (tt + k < live) {
+                    rx[k] = *reinterpret_cast<const Raw*>(x + static_cast<int64_t>(tt + k) * P.C);
+                    rg[k] = *reinterpret_cast<const Raw*>(go + static_cast<int64_t>(tt + k) * P.C);
+                }
+            }
+        };
+        fetch(t0);
+        for (int tt = t0; tt < end; tt += kAhead) {
+            Raw cx[kAhead], cg[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) cx[k] = rx[k], cg[k] = rg[k];
+            fetch(tt + kAhead);
+            if (tt >= t0 + K - 1 && tt + kAhead <= (live < t1 ? live : t1) && (P.ds_out == nullptr || tt + kAhead <= len)) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {  // within the run: every token its own, every row of X inside
+                    take(cx[k], cg[k], true);
+                    float o[V];
+                    give(o);
+                    *reinterpret_cast<Raw*>(dx + static_cast<int64_t>(tt + k - (K - 1)) * P.C) = Ops::narrow(o);
+                    shift();
+                }
+                continue;
+            }
+#pragma unroll 1
+            for (int k = 0; k < kAhead; ++k) {
+                const int t = tt + k;
+                if (t >= end) break;
+                Raw vx = cx[0], vg = cg[0];
+#pragma unroll
+                for (int q = 1; q < kAhead; ++q)
+                    if (k == q) vx = cx[q], vg = cg[q];
                 if (t < live) {
-                    float gv[V];
-                    Ops::widen(rx[k], win[K - 1]);
-                    Ops::widen(rg[k], gv);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        float pre = bias[i];
-#pragma unroll
-                        for (int j = 0; j < K; ++j) pre = fmaf(w[j][i], win[j][i], pre);
-                        g[K - 1][i] = gv[i] * act_grad(P.act, pre);
-                    }
-                    if (t < t1) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-#pragma unroll
-                            for (int j = 0; j < K; ++j) dw[j][i] = fmaf(g[K - 1][i], win[j][i], dw[j][i]);
-                            db[i] += g[K - 1][i];
-                        }
-                    }
+                    take(vx, vg, t < t1);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[K - 1][i] = 0.f;
                 }
-                // dX[t] = sum_j weight[j] g_{t - j}
-                const int64_t to = t - (K - 1);
+                const int to = t - (K - 1);
                 if (to >= t0 || (t0 == 0 && P.ds_in != nullptr)) {
                     float o[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        o[i] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], g[K - 1 - j][i], o[i]);
-                    }
+                    give(o);
                     if (P.ds_out != nullptr && t >= len && t < len + K - 1) {
                         float e[V];
                         Ops::widen(*reinterpret_cast<const Raw*>(static_cast<const T*>(P.ds_out) + (b * (K - 1) + t - len) * P.C + c), e);
@@ -245,13 +316,10 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
                         *reinterpret_cast<Raw*>(static_cast<T*>(P.ds_in) + (b * (K - 1) + t) * P.C + c) = ro;
                     } else {
                         if (to >= len) ro = Raw{};
-                        *reinterpret_cast<Raw*>(dx + to * P.C) = ro;
+                        *reinterpret_cast<Raw*>(dx + static_cast<int64_t>(to) * P.C) = ro;
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i], g[j][i] = g[j + 1][i];
+                shift();
             }
         }
     }
@@ -340,8 +408,9 @@ hipError_t conv_k(const ConvArgs& a, bool bwd, hipStream_t stream) {
 }
 
 hipError_t conv_t(const ConvArgs& a, bool bwd, hipStream_t stream) {
-    if (a.bf16) return a.vec ? conv_k<uint16_t, 4>(a, bwd, stream) : conv_k<uint16_t, 1>(a, bwd, stream);
-    return a.vec ? conv_k<float, 4>(a, bwd, stream) : conv_k<float, 1>(a, bwd, stream);
+    if (!a.vec) return a.bf16 ? conv_k<uint16_t, 1>(a, bwd, stream) : conv_k<float, 1>(a, bwd, stream);
+    if (bwd) return a.bf16 ? conv_k<uint16_t, 2>(a, bwd, stream) : conv_k<float, 2>(a, bwd, stream);
+    return a.bf16 ? conv_k<uint16_t, 4>(a, bwd, stream) : conv_k<float, 4>(a, bwd, stream);
 }
 
 }  // namespace
