@@ -123,7 +123,8 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run, int64_t ncb) {
     typedef Vec<T, V> Ops;
     typedef typename Ops::Raw Raw;
-    constexpr int kAhead = 8;  // tokens whose loads are on their way at once
+    // tokens whose loads are on their way at once: a multiple of K, so that the window, a ring of K rows, is back where it was
+    constexpr int kAhead = K == 3 ? 6 : 8;
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t cb = blk % ncb, rest = blk / ncb, ntb = (P.T + kRuns * run - 1) / (kRuns * run);
     const int64_t b = rest / ntb, c = (cb * kCols + threadIdx.x % kCols) * V;
@@ -158,20 +159,16 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (t + k < te) {
-                Ops::widen(raw[k], win[K - 1]);
+                Ops::widen(raw[k], win[(k + K - 1) % K]);
                 float o[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     o[i] = bias[i];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], win[j][i], o[i]);
+                    for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], win[(k + j) % K][i], o[i]);
                 }
                 act_of(P.act, o);
                 *reinterpret_cast<Raw*>(out + static_cast<int64_t>(t + k) * P.C) = Ops::narrow(o);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
             }
         }
     }
@@ -187,7 +184,7 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run, int64_t ncb) {
     typedef Vec<T, V> Ops;
     typedef typename Ops::Raw Raw;
-    constexpr int kAhead = 4;
+    constexpr int kAhead = K == 3 ? 3 : 4;  // a multiple of K: the windows are rings
     __shared__ float sums[kRuns][K + 1][V][kCols];
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t cb = blk % ncb, slot = blk / ncb;
@@ -223,34 +220,37 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
         // row e = t of X (token t - (K - 1)) has all its g once token t is done; the run answers for the tokens
         // t0 .. t1 - 1, and the first one for the carried inputs too
         const int end = t1 + K - 1, live = len < end ? len : end;
-        // one token: its g into the window's last row, and (own) its part of the weights' sums
-        const auto take = [&](Raw rx, Raw rg, bool own) {
+        // one token: its g, and (own) its part of the weights' sums.  The windows start at row `at` of their rings.
+        const auto take = [&](auto at, Raw rx, Raw rg, bool own) {
+            constexpr int a0 = decltype(at)::value;
+            float (&gt)[V] = g[(a0 + K - 1) % K];
             float pre[V];
-            Ops::widen(rx, win[K - 1]);
-            Ops::widen(rg, g[K - 1]);
+            Ops::widen(rx, win[(a0 + K - 1) % K]);
+            Ops::widen(rg, gt);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 pre[i] = bias[i];
 #pragma unroll
-                for (int j = 0; j < K; ++j) pre[i] = fmaf(w[j][i], win[j][i], pre[i]);
+                for (int j = 0; j < K; ++j) pre[i] = fmaf(w[j][i], win[(a0 + j) % K][i], pre[i]);
             }
-            act_grad(P.act, pre, g[K - 1]);
+            act_grad(P.act, pre, gt);
             if (own) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
 #pragma unroll
-                    for (int j = 0; j < K; ++j) dw[j][i] = fmaf(g[K - 1][i], win[j][i], dw[j][i]);
-                    db[i] += g[K - 1][i];
+                    for (int j = 0; j < K; ++j) dw[j][i] = fmaf(gt[i], win[(a0 + j) % K][i], dw[j][i]);
+                    db[i] += gt[i];
                 }
             }
         };
         // dX at the window's first row: sum_j weight[j] g_{t - j}
-        const auto give = [&](float (&o)[V]) {
+        const auto give = [&](auto at, float (&o)[V]) {
+            constexpr int a0 = decltype(at)::value;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                o[i] = w[0][i] * g[K - 1][i];
+                o[i] = w[0][i] * g[(a0 + K - 1) % K][i];
 #pragma unroll
-                for (int j = 1; j < K; ++j) o[i] = fmaf(w[j][i], g[K - 1 - j][i], o[i]);
+                for (int j = 1; j < K; ++j) o[i] = fmaf(w[j][i], g[(a0 + K - 1 - j) % K][i], o[i]);
             }
         };
         const auto shift = [&] {
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 rx[k] = rg[k] = Raw{};
-                if (tt + k < live) {
+                if (tt + k < len && tt < end) {
                     rx[k] = *reinterpret_cast<const Raw*>(x + static_cast<int64_t>(tt + k) * P.C);
                     rg[k] = *reinterpret_cast<const Raw*>(go + static_cast<int64_t>(tt + k) * P.C);
                 }
@@ -276,15 +276,14 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) cx[k] = rx[k], cg[k] = rg[k];
             fetch(tt + kAhead);
-            if (tt >= t0 + K - 1 && tt + kAhead <= (live < t1 ? live : t1) && (P.ds_out == nullptr || tt + kAhead <= len)) {
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {  // within the run: every token its own, every row of X inside
-                    take(cx[k], cg[k], true);
+            if (tt + kAhead <= len && !(tt == 0 && P.ds_in != nullptr)) {  // all of them tokens, no carried input's gradient
+                each<kAhead>([&](auto k) {
+                    const int to = tt + k - (K - 1);
+                    take(k, cx[k], cg[k], tt + k < t1);
                     float o[V];
-                    give(o);
-                    *reinterpret_cast<Raw*>(dx + static_cast<int64_t>(tt + k - (K - 1)) * P.C) = Ops::narrow(o);
-                    shift();
-                }
+                    give(k, o);
+                    if (to >= t0 && to < t1) *reinterpret_cast<Raw*>(dx + static_cast<int64_t>(to) * P.C) = Ops::narrow(o);
+                });
                 continue;
             }
 #pragma unroll 1
@@ -296,7 +295,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
                 for (int q = 1; q < kAhead; ++q)
                     if (k == q) vx = cx[q], vg = cg[q];
                 if (t < live) {
-                    take(vx, vg, t < t1);
+                    take(std::integral_constant<int, 0>{}, vx, vg, t < t1);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[K - 1][i] = 0.f;
@@ -304,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
                 const int to = t - (K - 1);
                 if (to >= t0 || (t0 == 0 && P.ds_in != nullptr)) {
                     float o[V];
-                    give(o);
+                    give(std::integral_constant<int, 0>{}, o);
                     if (P.ds_out != nullptr && t >= len && t < len + K - 1) {
                         float e[V];
                         Ops::widen(*reinterpret_cast<const Raw*>(static_cast<const T*>(P.ds_out) + (b * (K - 1) + t - len) * P.C + c), e);

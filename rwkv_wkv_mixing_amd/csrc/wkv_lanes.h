@@ -1,9 +1,11 @@
-// What the delta-rule and norm kernels share: float32 and bf16 values, and sums over the lanes of a wave without a
+// What the delta-rule, norm, convolution and scan kernels share: float32 and bf16 values, and sums over the lanes of a wave without a
 // trip through LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 namespace wkv {
 
@@ -17,6 +19,16 @@ __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ uint32_t pk2(float a, float b) {
     const f2 p = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf2));
+}
+
+// Calls f with std::integral_constant<int, 0> .. <int, N - 1>: for what has to be known when the code is made.
+template <int N, class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
 template <int Ctrl>

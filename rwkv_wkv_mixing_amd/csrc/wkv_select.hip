@@ -13,8 +13,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <utility>
-
 #include "wkv_lanes.h"
 #include "wkv_launch.h"
 
@@ -93,16 +91,6 @@ __device__ __forceinline__ void store_at(T* p, int64_t at, uint32_t bytes, T v) 
 }
 // Keeps an offset one of 32 bits in a loop, next to a wave's address, and not part of a sum of 64 bits.
 __device__ __forceinline__ void keep32(uint32_t& v) { asm volatile("" : "+v"(v)); }
-
-// Calls f with std::integral_constant<int, 0> .. <int, N - 1>: the lanes of a broadcast are part of the instruction.
-template <int N, class F, int... I>
-__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
-    (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void each(F&& f) {
-    each_of<N>(f, std::make_integer_sequence<int, N>{});
-}
 
 // The values of lane K of every row of 16 lanes, to the row: folded into the multiplication that takes them.
 template <int K>
