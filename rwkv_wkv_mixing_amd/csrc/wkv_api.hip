@@ -1138,7 +1138,7 @@ wkv_status_t clip_check(int64_t count, const void* const* grads, const int64_t* 
         if (sizes[i] == 0) continue;
         if (!grads[i]) return WKV_EINVAL;
         if (!aligned(grads[i], in_size(dtypes[i]))) return WKV_EALIGN;
-        if (__builtin_add_overflow(*total, sizes[i], total)) return WKV_ESIZE;
+        if (__builtin_add_overflow(*total, sizes[i], total) || *total > (int64_t{1} << 58)) return WKV_ESIZE;
     }
     return WKV_OK;
 }
@@ -1170,22 +1170,26 @@ wkv_status_t clip_overlaps(int64_t count, const void* const* grads, void* const*
     return clash ? WKV_EINVAL : WKV_OK;
 }
 
-// The next table: tensors from *at on.
-void clip_table(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, int64_t* at,
+// The table of the launch'th group of tensors (those without elements left out).
+void clip_table(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, int64_t launch,
                 wkv::ClipTable* t) {
     t->count = 0;
+    t->past_cache = false;
     t->chunks = 0;
-    for (; *at < count && t->count < wkv::kClipTensors; ++*at) {
-        if (sizes[*at] == 0) continue;
+    const int64_t first = launch * wkv::kClipTensors, last = first + wkv::kClipTensors;
+    for (int64_t i = first; i < last && i < count; ++i) {
+        if (sizes[i] == 0) continue;
         const int k = t->count++;
-        t->in[k] = grads[*at];
-        t->out[k] = outs != nullptr ? outs[*at] : const_cast<void*>(grads[*at]);
-        t->n[k] = sizes[*at];
+        t->in[k] = grads[i];
+        t->out[k] = outs != nullptr ? outs[i] : const_cast<void*>(grads[i]);
+        t->n[k] = sizes[i];
         t->chunk0[k] = t->chunks;
-        t->bf16[k] = dtypes[*at] == WKV_BF16 ? 1 : 0;
-        t->chunks += (sizes[*at] + wkv::kClipChunk - 1) / wkv::kClipChunk;
+        t->bf16[k] = dtypes[i] == WKV_BF16 ? 1 : 0;
+        t->chunks += (sizes[i] + wkv::kClipChunk - 1) / wkv::kClipChunk;
     }
 }
+
+int64_t clip_launches(int64_t count) { return (count + wkv::kClipTensors - 1) / wkv::kClipTensors; }
 
 // Partial sums that every workgroup adds up for itself; more are first added to one by a launch of their own.
 constexpr int64_t kClipParts = 4 * wkv::kClipBlocks;
@@ -1194,9 +1198,9 @@ constexpr int64_t kClipParts = 4 * wkv::kClipBlocks;
 hipError_t clip_sums(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, double* part, int64_t* nparts,
                      hipStream_t stream) {
     *nparts = 0;
-    for (int64_t at = 0; at < count;) {
+    for (int64_t l = 0; l < clip_launches(count); ++l) {
         wkv::ClipTable t;
-        clip_table(count, grads, nullptr, sizes, dtypes, &at, &t);
+        clip_table(count, grads, nullptr, sizes, dtypes, l, &t);
         if (t.count == 0) continue;
         const hipError_t e = wkv::launch_clip_sums(t, part + *nparts, stream);
         if (e != hipSuccess) return e;
@@ -1368,7 +1372,7 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
 
 size_t wkv_clip_workspace_bytes(int64_t count) {
     if (count < 0 || count >= (int64_t{1} << 24)) return 0;
-    const int64_t launches = (count + wkv::kClipTensors - 1) / wkv::kClipTensors;
+    const int64_t launches = clip_launches(count);
     return launches > 0 ? static_cast<size_t>(launches * wkv::kClipBlocks + 1) * sizeof(double) : 0;
 }
 
@@ -1408,6 +1412,8 @@ wkv_status_t wkv_clip_gradients(int64_t count, const void* const* grads, void* c
     st = clip_overlaps(count, grads, to, sizes, dtypes, norm);
     if (st != WKV_OK) return st;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < wkv_clip_workspace_bytes(count)) return WKV_EWORKSPACE;
+    int64_t bytes = 0;
+    for (int64_t i = 0; i < count; ++i) bytes += sizes[i] * static_cast<int64_t>(in_size(dtypes[i]));
     double* part = static_cast<double*>(workspace);
     int64_t nparts;
     hipError_t e = clip_sums(count, grads, sizes, dtypes, part, &nparts, stream);
@@ -1416,9 +1422,10 @@ wkv_status_t wkv_clip_gradients(int64_t count, const void* const* grads, void* c
         part += nparts;
         nparts = 1;
     }
-    for (int64_t at = 0; at < count && e == hipSuccess;) {
+    for (int64_t l = clip_launches(count) - 1; l >= 0 && e == hipSuccess; --l) {  // from the last: see clip_scale_kernel
         wkv::ClipTable t;
-        clip_table(count, grads, to, sizes, dtypes, &at, &t);
+        clip_table(count, grads, to, sizes, dtypes, l, &t);
+        t.past_cache = bytes > wkv::kClipCached;
         if (t.count > 0) e = wkv::launch_clip_scale(t, part, nparts, max_norm, eps, norm, stream);
     }
     return hip_status(e);

@@ -60,14 +60,20 @@ __device__ __forceinline__ void load8(const T* p, int64_t e, int64_t n, float (&
     for (int i = 0; i < 8; ++i) f[i] = e + i < n ? widen(p[e + i]) : 0.f;
 }
 
+template <typename V>
+__device__ __forceinline__ void store_vec(V* p, V v, bool past_cache) {
+    if (past_cache) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 template <typename T, bool Vec>
-__device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const float (&f)[8], bool past_cache) {
     if (Vec && e + 8 <= n) {
         if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<f4*>(p + e) = f4{f[0], f[1], f[2], f[3]};
-            *reinterpret_cast<f4*>(p + e + 4) = f4{f[4], f[5], f[6], f[7]};
+            store_vec(reinterpret_cast<f4*>(p + e), f4{f[0], f[1], f[2], f[3]}, past_cache);
+            store_vec(reinterpret_cast<f4*>(p + e + 4), f4{f[4], f[5], f[6], f[7]}, past_cache);
         } else {
-            *reinterpret_cast<u4*>(p + e) = u4{pk2(f[0], f[1]), pk2(f[2], f[3]), pk2(f[4], f[5]), pk2(f[6], f[7])};
+            store_vec(reinterpret_cast<u4*>(p + e), u4{pk2(f[0], f[1]), pk2(f[2], f[3]), pk2(f[4], f[5]), pk2(f[6], f[7])}, past_cache);
         }
         return;
     }
@@ -80,14 +86,50 @@ __device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const float (
     }
 }
 
-// The elements of a chunk: eight a thread, and the next eights a workgroup's width on.
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+    u4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const u4*>(p)[i];
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i / 4][i % 4]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(v[0][i] << 16), f[2 * i + 1] = __uint_as_float(v[0][i] & 0xffff0000u);
+        }
+    }
+};
+
+// The elements of a chunk: eight a thread, and the next eights a workgroup's width on.  A whole chunk of a tensor on the
+// 16-byte grid has kBatch eights of a thread on their way at once.
+constexpr int kStep = kThreads * 8, kBatch = 4;
+static_assert(kClipChunk % (kStep * kBatch) == 0, "whole batches a chunk");
+
 template <typename T, bool Vec>
 __device__ __forceinline__ double sum_chunk(const T* p, int64_t first, int64_t n) {
-    const int64_t end = first + kClipChunk < n ? first + kClipChunk : n;
     double sum = 0.0;
-#pragma unroll 4
-    for (int64_t e = first + threadIdx.x * 8; e < end; e += kThreads * 8) {
-        float f[8];
+    float f[8];
+    if (Vec && first + kClipChunk <= n) {
+        const T* at = p + first + threadIdx.x * 8;
+        for (int k = 0; k < kClipChunk / kStep; k += kBatch) {
+            Raw8<T> raw[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) raw[q].load(at + (k + q) * kStep);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                raw[q].widen(f);
+                sum += squares(f);
+            }
+        }
+        return sum;
+    }
+    const int64_t end = first + kClipChunk < n ? first + kClipChunk : n;
+    for (int64_t e = first + threadIdx.x * 8; e < end; e += kStep) {
         load8<T, Vec>(p, e, n, f);
         sum += squares(f);
     }
@@ -95,15 +137,30 @@ __device__ __forceinline__ double sum_chunk(const T* p, int64_t first, int64_t n
 }
 
 template <typename T, bool Vec>
-__device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, int64_t n, float by) {
+__device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, int64_t n, float by, bool past_cache) {
+    float f[8];
+    if (Vec && first + kClipChunk <= n) {
+        const int64_t at = first + threadIdx.x * 8;
+        for (int k = 0; k < kClipChunk / kStep; k += kBatch) {
+            Raw8<T> raw[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) raw[q].load(p + at + (k + q) * kStep);
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                raw[q].widen(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= by;
+                store8<T, true>(to, at + (k + q) * kStep, n, f, past_cache);
+            }
+        }
+        return;
+    }
     const int64_t end = first + kClipChunk < n ? first + kClipChunk : n;
-#pragma unroll 4
-    for (int64_t e = first + threadIdx.x * 8; e < end; e += kThreads * 8) {
-        float f[8];
+    for (int64_t e = first + threadIdx.x * 8; e < end; e += kStep) {
         load8<T, Vec>(p, e, n, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= by;
-        store8<T, Vec>(to, e, n, f);
+        store8<T, Vec>(to, e, n, f, past_cache);
     }
 }
 
@@ -160,7 +217,8 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
     // 1 up to max_norm; a norm that is not a number is handed on to every gradient
     const float by = with <= static_cast<double>(max_norm) ? 1.f : static_cast<float>(static_cast<double>(max_norm) / with);
     if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(all);
-    for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+    // from the last chunk to the first, as the launches go: what the sums read last is still in the last level cache
+    for (int64_t chunk = t.chunks - 1 - blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
         const int k = tensor_of(t, chunk);
         const int64_t first = (chunk - t.chunk0[k]) * kClipChunk, n = t.n[k];
         if (by == 1.f && t.in[k] == t.out[k]) continue;
@@ -168,13 +226,13 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
         if (t.bf16[k] != 0) {
             const uint16_t* p = static_cast<const uint16_t*>(t.in[k]);
             uint16_t* to = static_cast<uint16_t*>(t.out[k]);
-            if (vec) scale_chunk<uint16_t, true>(p, to, first, n, by);
-            else scale_chunk<uint16_t, false>(p, to, first, n, by);
+            if (vec) scale_chunk<uint16_t, true>(p, to, first, n, by, t.past_cache);
+            else scale_chunk<uint16_t, false>(p, to, first, n, by, t.past_cache);
         } else {
             const float* p = static_cast<const float*>(t.in[k]);
             float* to = static_cast<float*>(t.out[k]);
-            if (vec) scale_chunk<float, true>(p, to, first, n, by);
-            else scale_chunk<float, false>(p, to, first, n, by);
+            if (vec) scale_chunk<float, true>(p, to, first, n, by, t.past_cache);
+            else scale_chunk<float, false>(p, to, first, n, by, t.past_cache);
         }
     }
 }

@@ -412,10 +412,12 @@ struct ClipTable {
     int64_t chunk0[kClipTensors];     // number of the tensor's first chunk in this launch
     uint8_t bf16[kClipTensors];
     int count;
+    bool past_cache;                  // outputs are written past the caches: the call's gradients do not fit them
     int64_t chunks;                   // of all the tensors
 };
 constexpr int64_t kClipBlocks = 1024;  // workgroups of a launch at most, and partial sums it writes
 constexpr int64_t kClipChunk = 16384;  // elements
+constexpr int64_t kClipCached = int64_t{200} << 20;  // bytes that stay in the last level cache (256 MB) with something to spare
 // partial sums of squares: one a workgroup, from part on; their number
 int64_t clip_blocks(const ClipTable& t);
 hipError_t launch_clip_sums(const ClipTable& t, double* part, hipStream_t stream);

@@ -698,55 +698,57 @@ __global__ __launch_bounds__(256) void select_reduce_kernel(SelectArgs P, int64_
     }
 }
 
-// A few tokens: four states a lane, token by token in registers, the state one trip through memory.
-template <typename T>
+// A few tokens: four states a lane, token by token in registers, the state one trip through memory, which is what bounds
+// it.  A workgroup takes 256 / Lanes channels of a batch row (and of every gridDim.y-th row after it).
+template <typename T, int Lanes>
 __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     constexpr bool kWide = sizeof(T) == 4;
-    const int lanes = static_cast<int>(P.N) / 4;  // of a channel
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, n = P.B * P.C;
-    const int64_t bc = i / lanes < n ? i / lanes : n - 1;  // spare lanes take part in the sums
-    const int q = static_cast<int>(i % lanes);
-    const bool valid = i / lanes < n;
-    const int64_t b = bc / P.C, ch = bc % P.C, g = ch / (P.C / P.G), GN = P.G * P.N;
-    const T* __restrict__ x = static_cast<const T*>(P.x);
-    const T* __restrict__ dt = static_cast<const T*>(P.dt);
-    const T* __restrict__ z = static_cast<const T*>(P.z);
-    const T* __restrict__ bb = static_cast<const T*>(P.b);
-    const T* __restrict__ cc = static_cast<const T*>(P.c);
-    const int64_t state = bc * P.N + 4 * q;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, w2[4];
-    if (P.s_in != nullptr) load_states(P.s_in + state, true, h);
-    load_states(P.w + ch * P.N + 4 * q, true, w2);
+    constexpr int N = 4 * Lanes;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (256 / Lanes) + threadIdx.x / Lanes;
+    const bool valid = at < P.C;
+    const int ch = static_cast<int>(valid ? at : P.C - 1), q = threadIdx.x % Lanes;  // spare lanes take part in the sums
+    const int g = P.G > 1 ? ch / (static_cast<int>(P.C) / static_cast<int>(P.G)) : 0;
+    const int64_t GN = P.G * N;
+    float w2[NS];
+    load_states(P.w + static_cast<int64_t>(ch) * N + 4 * q, true, w2);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) w2[s] = -fminf(w2[s], 2e38f) * kLog2e;
+    for (int s = 0; s < NS; ++s) w2[s] = -fminf(w2[s], 2e38f) * kLog2e;
     const float bias = P.dt_bias != nullptr ? P.dt_bias[ch] : 0.f, skip = P.d != nullptr ? P.d[ch] : 0.f;
-    int64_t len = P.lengths != nullptr ? P.lengths[b] : P.T;
-    len = len < 0 ? 0 : len > P.T ? P.T : len;
-    // (all lanes walk to the longest row's end: the sums over lanes are the whole wave's)
-    for (int64_t t = 0; t < P.T; ++t) {
-        const bool live = t < len;
-        const int64_t row = b * P.T + t, at = row * P.C + ch;
-        float y = 0.f, vx = 0.f, gate = 1.f;
-        if (live) {
-            vx = widen(x[at]);
-            float d1[1] = {widen(dt[at]) + bias}, unused[1];
-            steps_of<kWide, false>(d1, P.softplus, unused);
-            const float delta = d1[0], u = delta * vx;
-            if (z != nullptr) {
-                const float zz = widen(z[at]);
+    const int tokens = static_cast<int>(P.T);
+    for (int64_t b = blockIdx.y; b < P.B; b += gridDim.y) {
+        const int64_t state = (b * P.C + ch) * N + 4 * q;
+        float h[NS] = {0.f, 0.f, 0.f, 0.f};
+        if (P.s_in != nullptr) load_states(P.s_in + state, true, h);
+        int len = P.lengths != nullptr ? P.lengths[b] : tokens;
+        len = len < 0 ? 0 : len > tokens ? tokens : len;
+        for (int t = 0; t < tokens; ++t) {
+            const int64_t row = b * P.T + t, to = row * P.C + ch;
+            if (t >= len) {
+                if (valid && q == 0) static_cast<T*>(P.out)[to] = T{0};
+                continue;
+            }
+            const int64_t from = row * GN + g * N + 4 * q;
+            T bb[NS], cc[NS];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) bb[s] = static_cast<const T*>(P.b)[from + s], cc[s] = static_cast<const T*>(P.c)[from + s];
+            const float vx = widen(static_cast<const T*>(P.x)[to]);
+            float gate = 1.f, y = 0.f, d1[1] = {widen(static_cast<const T*>(P.dt)[to]) + bias}, unused[1];
+            if (P.z != nullptr) {
+                const float zz = widen(static_cast<const T*>(P.z)[to]);
                 gate = zz * sigmoid(zz);
             }
-            const int64_t from = row * GN + g * P.N + 4 * q;
+            steps_of<kWide, false>(d1, P.softplus, unused);
+            const float u = d1[0] * vx;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                h[s] = fmaf(exp2_fast(delta * w2[s]), h[s], widen(bb[from + s]) * u);
-                y = fmaf(widen(cc[from + s]), h[s], y);
+            for (int s = 0; s < NS; ++s) {
+                h[s] = fmaf(exp2_fast(d1[0] * w2[s]), h[s], widen(bb[s]) * u);
+                y = fmaf(widen(cc[s]), h[s], y);
             }
+            y = sum_lanes(y, Lanes);
+            if (valid && q == 0) static_cast<T*>(P.out)[to] = narrow<T>(fmaf(skip, vx, y) * gate);
         }
-        y = sum_lanes(y, lanes);
-        if (valid && q == 0) static_cast<T*>(P.out)[at] = live ? narrow<T>(fmaf(skip, vx, y) * gate) : T{0};
+        if (valid && P.s_out != nullptr) store_states(P.s_out + state, h);
     }
-    if (valid && P.s_out != nullptr) store_states(P.s_out + state, h);
 }
 
 template <typename T, int W>
@@ -809,12 +811,22 @@ int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bw
     return n;
 }
 
-hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream) {
-    const int64_t n = a.B * a.C * (a.N / 4);
-    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
-    if (a.bf16) hipLaunchKernelGGL(select_step_kernel<uint16_t>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(select_step_kernel<float>, grid, dim3(256), 0, stream, a);
+namespace {
+
+template <typename T>
+hipError_t step_t(const SelectArgs& a, hipStream_t stream) {
+    const int64_t per = 1024 / a.N;  // channels a workgroup
+    const dim3 grid(static_cast<unsigned>((a.C + per - 1) / per), static_cast<unsigned>(a.B < 65535 ? a.B : 65535));
+    if (a.N == 8) hipLaunchKernelGGL((select_step_kernel<T, 2>), grid, dim3(256), 0, stream, a);
+    else if (a.N == 16) hipLaunchKernelGGL((select_step_kernel<T, 4>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((select_step_kernel<T, 8>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_select_step(const SelectArgs& a, hipStream_t stream) {
+    return a.bf16 ? step_t<uint16_t>(a, stream) : step_t<float>(a, stream);
 }
 
 hipError_t launch_select_fwd(const SelectArgs& a, hipStream_t stream) {

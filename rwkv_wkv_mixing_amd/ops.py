@@ -1302,18 +1302,22 @@ def selective_scan(x, dt, w, b, c, d=None, z=None, dt_bias=None, state_in=None, 
 def _clip_tables(grads, out):
     """The tensors' device, and host arrays of their addresses, sizes and dtypes."""
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
-    dev = None
-    for i, g in enumerate(grads):
-        _need(g, f"grads[{i}]", _FLOATS, None, dev)
-        dev = g.device
-    n = len(grads)
-    outs = None
+    if not grads:
+        raise ValueError("grads is empty: there is no device to return a norm on")
+    _need(grads[0], "grads[0]", _FLOATS)
+    dev, index = grads[0].device, grads[0].get_device()
+    for i, g in enumerate(grads):  # (one comparison each: there may be hundreds)
+        if not (isinstance(g, torch.Tensor) and g.get_device() == index and g.dtype in _DT and g.is_contiguous()):
+            _need(g, f"grads[{i}]", _FLOATS, None, dev)
+    n, outs = len(grads), None
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors for {n} gradients")
         for i, (o, g) in enumerate(zip(out, grads)):
-            _need(o, f"out[{i}]", g.dtype, g.shape, dev)
+            if not (isinstance(o, torch.Tensor) and o.get_device() == index and o.dtype is g.dtype and o.shape == g.shape
+                    and o.is_contiguous()):
+                _need(o, f"out[{i}]", g.dtype, g.shape, dev)
         outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
     return (dev, grads, out, n, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), outs,
             (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int * n)(*[_DT[g.dtype] for g in grads]))
@@ -1324,8 +1328,6 @@ def grad_norm(grads, *, norm=None, workspace=None, bind=False):
     device (norm, when given, receives it).  grads: a tensor or a list of tensors of any shapes, float32 and
     bfloat16.  Squares are added up in float64, in a fixed order; nothing is copied to the host."""
     dev, grads, _, n, ins, _, sizes, types = _clip_tables(grads, None)
-    if n == 0:
-        raise ValueError("grads is empty: there is no device to return a norm on")
     norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
     _need(norm, "norm", torch.float32, (), dev)
     lib = L.lib()
@@ -1340,8 +1342,6 @@ def clip_gradients(grads, max_norm, *, eps=1e-6, out=None, norm=None, workspace=
     dimensions.  A norm that is infinite or not a number makes the gradients zeros or not numbers.  No gradient
     may be listed twice in place."""
     dev, grads, out, n, ins, outs, sizes, types = _clip_tables(grads, out)
-    if n == 0:
-        raise ValueError("grads is empty: there is no device to return a norm on")
     norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
     _need(norm, "norm", torch.float32, (), dev)
     lib = L.lib()
