@@ -745,8 +745,8 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
  *           With T == 0 it receives s_in (or zeros).
  *
  * Backward, of sum <gout, out> + <ds_out, s_out>: dx, dweight, dbias (needed with
- * bias), ds_in (or NULL; may be ds_out).  dweight and dbias are sums over rows and
- * tokens in a fixed order; all outputs are overwritten.
+ * bias), ds_in (or NULL; it must not overlap ds_out: WKV_EINVAL).  dweight and dbias
+ * are sums over rows and tokens in a fixed order; all outputs are overwritten.
  * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
  *           clobbered.  Not needed without tokens.
  * WKV_ESIZE from T = 2^31 - 64, B = 2^31 or C = 2^26.

@@ -1174,7 +1174,6 @@ wkv_status_t clip_overlaps(int64_t count, const void* const* grads, void* const*
 void clip_table(int64_t count, const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes, int64_t launch,
                 wkv::ClipTable* t) {
     t->count = 0;
-    t->past_cache = false;
     t->chunks = 0;
     const int64_t first = launch * wkv::kClipTensors, last = first + wkv::kClipTensors;
     for (int64_t i = first; i < last && i < count; ++i) {
@@ -1253,6 +1252,10 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
         return hip_status(e);
     }
     if (!x || !weight || !gout || !dx) return WKV_EINVAL;
+    // a row's last tokens read ds_out when its first ones may have written ds_in
+    const uintptr_t in = reinterpret_cast<uintptr_t>(ds_in), from = reinterpret_cast<uintptr_t>(ds_out);
+    const uintptr_t span = static_cast<uintptr_t>(p.ns) * es;
+    if (ds_in && ds_out && in < from + span && from < in + span) return WKV_EINVAL;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.ws_bytes) return WKV_EWORKSPACE;
     wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
     a.gout = gout;
@@ -1425,8 +1428,7 @@ wkv_status_t wkv_clip_gradients(int64_t count, const void* const* grads, void* c
     for (int64_t l = clip_launches(count) - 1; l >= 0 && e == hipSuccess; --l) {  // from the last: see clip_scale_kernel
         wkv::ClipTable t;
         clip_table(count, grads, to, sizes, dtypes, l, &t);
-        t.past_cache = bytes > wkv::kClipCached;
-        if (t.count > 0) e = wkv::launch_clip_scale(t, part, nparts, max_norm, eps, norm, stream);
+        if (t.count > 0) e = wkv::launch_clip_scale(t, part, nparts, max_norm, eps, norm, bytes > wkv::kClipCached, stream);
     }
     return hip_status(e);
 }

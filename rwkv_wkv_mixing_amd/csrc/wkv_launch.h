@@ -412,7 +412,6 @@ struct ClipTable {
     int64_t chunk0[kClipTensors];     // number of the tensor's first chunk in this launch
     uint8_t bf16[kClipTensors];
     int count;
-    bool past_cache;                  // outputs are written past the caches: the call's gradients do not fit them
     int64_t chunks;                   // of all the tensors
 };
 constexpr int64_t kClipBlocks = 1024;  // workgroups of a launch at most, and partial sums it writes
@@ -424,7 +423,7 @@ hipError_t launch_clip_sums(const ClipTable& t, double* part, hipStream_t stream
 // nparts partial sums to one, behind them, when there are too many for every workgroup to add up
 hipError_t launch_clip_norm(const double* part, int64_t nparts, float* norm, double* total, hipStream_t stream);
 hipError_t launch_clip_scale(const ClipTable& t, const double* part, int64_t nparts, float max_norm, float eps, float* norm,
-                             hipStream_t stream);
+                             bool past_cache, hipStream_t stream);  // past_cache: the outputs are written past the caches
 
 constexpr int kSelectTile = 16;  // tokens between saved states of the selective scan
 // Up to this many tokens without saved states it runs token by token (select_step_kernel).
