@@ -198,14 +198,15 @@ struct Place {
     bool valid;          // not a spare lane
 };
 
-__device__ __forceinline__ Place place_of(const SelectArgs& P, int lane) {
+__device__ __forceinline__ Place place_of(const SelectArgs& P, int lane, int first_seg = 0) {
     Place p;
     const uint32_t nct = static_cast<uint32_t>(P.ctiles);
     // (quotients are worked out in vector registers: readfirstlane says that they are the wave's)
     const uint32_t blk = blockIdx.x, rest = __builtin_amdgcn_readfirstlane(blk / nct);
     p.ct = __builtin_amdgcn_readfirstlane(blk - rest * nct);
-    p.seg = __builtin_amdgcn_readfirstlane(rest / static_cast<uint32_t>(P.B));
-    p.b = rest - static_cast<uint32_t>(p.seg) * static_cast<uint32_t>(P.B);
+    const int seg = __builtin_amdgcn_readfirstlane(rest / static_cast<uint32_t>(P.B));
+    p.b = rest - static_cast<uint32_t>(seg) * static_cast<uint32_t>(P.B);
+    p.seg = first_seg + seg;
     const int per_group = __builtin_amdgcn_readfirstlane(P.ctiles / static_cast<int>(P.G));
     p.g = __builtin_amdgcn_readfirstlane(p.ct / per_group);
     const int width = __builtin_amdgcn_readfirstlane(static_cast<int>(P.C) / static_cast<int>(P.G)), c = (p.ct - p.g * per_group) * 64 + lane;
@@ -233,7 +234,7 @@ __device__ __forceinline__ void yield_to_later(int done, int all) {
 
 // What a walk does: the outputs; what each segment does to a state of zero; the same for the states' gradients, from
 // the last token to the first: g <- a (g + c gy).
-enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2 };
+enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2, kGrad = 3 };  // kGrad: select_grad_kernel
 
 template <typename T, int W, int Mode>
 __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     __shared__ float2 put[2][kTile][64];                         // delta and the written value
     __shared__ float parts[kOut ? 2 : 1][kOut ? W : 1][kTile][64];  // the waves' parts of y
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place p = place_of(P, lane);
+    const Place p = place_of(P, lane, kAdj ? 1 : 0);  // (what the last, or backwards the first, segment does is not asked for)
     const T* __restrict__ x = static_cast<const T*>(P.x);
     const T* __restrict__ dt = static_cast<const T*>(P.dt);
     const T* __restrict__ z = static_cast<const T*>(P.z);
@@ -448,9 +449,9 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
     for (int64_t k = 0; k < P.nseg; ++k) {
         const int64_t s = reverse ? P.nseg - 1 - k : k;
         float* at = P.local + s * n + i;
-        const float own = *at;
+        const float own = k + 1 < P.nseg ? *at : 0.f, step = k + 1 < P.nseg ? P.steps[s * P.B * P.C + bc] : 0.f;
         *at = h;
-        h = fmaf(exp2_fast(P.steps[s * P.B * P.C + bc] * w2), h, own);
+        h = fmaf(exp2_fast(step * w2), h, own);
     }
 }
 
@@ -753,7 +754,8 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
 
 template <typename T, int W>
 hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.ctiles * a.B * a.nseg)), block(64 * W);
+    const bool all = mode == kWalkOut || mode == kGrad;
+    const dim3 grid(static_cast<unsigned>(a.ctiles * a.B * (all ? a.nseg : a.nseg - 1))), block(64 * W);
     switch (mode) {
         case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkOut>), grid, block, 0, stream, a); break;
         case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkLocal>), grid, block, 0, stream, a); break;
@@ -762,8 +764,6 @@ hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
     }
     return hipGetLastError();
 }
-
-constexpr int kGrad = 3;
 
 template <typename T>
 hipError_t walk_n(const SelectArgs& a, int mode, hipStream_t stream) {
