@@ -124,6 +124,31 @@ __device__ __forceinline__ void add_row(float (&g)[NS], float c, float v) {
         : "v"(c), "v"(v), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
 }
 
+// A token's 8 numbers (b and c of the wave's states) summed over the lanes that differ in bits 2 and 3 alone: state 0 + (bit 2
+// of the lane) of b (bit 3: of c) in q0, state 2 + (bit 2) in q1.  An addition with a lane exchange writes the quarters
+// of its rows that the number belongs to, so two of them add up two numbers into one register.  The first wait is
+// for what the products before have written, the last one for the exchange that reads the results; in between nothing is
+// read through an exchange sooner than three instructions after it is written.
+__device__ __forceinline__ void fold_rows(const float (&b)[NS], const float (&c)[NS], float& q0, float& q1) {
+    float r0, r1, r2, r3;
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %2, %10, %10 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %3, %7, %7 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %3, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %4, %8, %8 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %4, %12, %12 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %5, %9, %9 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+        "v_add_f32_dpp %0, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+        "v_add_f32_dpp %1, %4, %4 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+        "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+        "s_nop 1"
+        : "=&v"(q0), "=&v"(q1), "=&v"(r0), "=&v"(r1), "=&v"(r2), "=&v"(r3)
+        : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(c[0]), "v"(c[1]), "v"(c[2]), "v"(c[3]));
+}
+
 // A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
 // NS registers, token by token, so that each of them is one lane of one register.
 template <typename T>
@@ -460,7 +485,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
 //     g += c_t gy_t,   dc_t = sum gy_t h_t,   db_t = sum g u_t  (over channels),   du_t = sum_n g b_t,
 //     g *= a_t,   q = g h_{t-1},   ddelta_t = du_t x_t - sum_n w q,   dw -= delta_t q
 // The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
-// of which every exchange between lanes halves the registers, so 16 tokens end as one number a lane and register.
+// of which every exchange between lanes halves the registers, so 16 tokens end as two registers of one number a lane.
 template <typename T, int W>
 __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;
@@ -560,50 +585,45 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
         each<kTile>([&](auto jj) {
             constexpr int j = kTile - 1 - decltype(jj)::value;
             const float4 v = put[j][lane];
-            float down = 0.f, r[NS];
+            float down = 0.f, pb[NS], pc[NS];
             add_row<c.template lane_of<j>()>(g, c.template reg<j>(), v.z);
             parts[1][wave][j][lane] = dot_row<b.template lane_of<j>()>(b.template reg<j>(), g[0], g[1], g[2], g[3]);
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const float pb = g[s] * v.y, pc = v.z * h[j + 1][s];
+                pb[s] = g[s] * v.y, pc[s] = v.z * h[j + 1][s];
                 g[s] *= a[j][s];
                 const float m = g[s] * h[j][s];
                 down = fmaf(m, w1[s], down);
                 dw[s] = fmaf(-m, v.x, dw[s]);
-                // db to the lower half of the lanes, dc to the upper
-                const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(pb), __float_as_uint(pc), false, false);
-                r[s] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
             }
             parts[2][wave][j][lane] = down;
+            float q0, q1;
+            fold_rows(pb, pc, q0, q1);
             // states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones
-            float m2[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[s]), __float_as_uint(r[s + 2]), false, false);
-                m2[s] = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
-            }
-            m2[0] += dpp<0x128>(m2[0]);  // row_ror:8
-            m2[1] += dpp<0x128>(m2[1]);
-            tokens[j & 7] = (lane & 8) != 0 ? m2[1] : m2[0];
-            if constexpr ((j & 7) == 0) {  // eight tokens: one number a lane, of token lane & 7
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float lo = tokens[k] + dpp<0x141>(tokens[k]), hi = tokens[k + 4] + dpp<0x141>(tokens[k + 4]);  // row_half_mirror
-                    tokens[k] = (lane & 4) != 0 ? hi : lo;
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 2] + dpp<0x4E>(tokens[k + 2]);  // lane ^ 2
-                    tokens[k] = (lane & 2) != 0 ? hi : lo;
-                }
-                const float lo = tokens[0] + dpp<0xB1>(tokens[0]), hi = tokens[1] + dpp<0xB1>(tokens[1]);  // lane ^ 1
-                const int tok = j + (lane & 7);
-                if (tok < n) {
-                    const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
-                    P.part[row + (lane >> 5) * N + wave * NS + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)] = (lane & 1) != 0 ? hi : lo;
-                }
+            const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(q0), __float_as_uint(q1), false, false);
+            const float one = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+            if constexpr (j >= 8) {
+                tokens[j - 8] = one;
+            } else {  // token j to the lower half of the lanes, j + 8 to the upper
+                const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(one), __float_as_uint(tokens[j]), false, false);
+                tokens[j] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
             }
         });
+        // of eight registers two: tokens j + 4 (bit 1 of the lane) and j + 2 (bit 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 4] + dpp<0x4E>(tokens[k + 4]);  // lane ^ 2
+            tokens[k] = (lane & 2) != 0 ? hi : lo;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float lo = tokens[k] + dpp<0xB1>(tokens[k]), hi = tokens[k + 2] + dpp<0xB1>(tokens[k + 2]);  // lane ^ 1
+            const int tok = k + (lane & 2) * 2 + (lane & 1) * 2 + (lane >> 5) * 8;
+            if (tok < n) {
+                const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
+                P.part[row + ((lane >> 3) & 1) * N + wave * NS + ((lane >> 4) & 1) * 2 + ((lane >> 2) & 1)] = (lane & 1) != 0 ? hi : lo;
+            }
+        }
         __syncthreads();
         T oz[kEach], ox[kEach], od[kEach];
 #pragma unroll
