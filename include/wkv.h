@@ -835,8 +835,8 @@ size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int6
  *           NULL (recomputed, from s_in).
  * workspace wkv_select_backward_workspace_bytes(..., ws_flags) bytes, 256-byte
  *           aligned; clobbered.  With room for it the call may split in time.
- * Other arguments and errors as wkv_select_forward; ds_out and ds_in are 16-byte
- * aligned too.
+ * Other arguments and errors as wkv_select_forward; db, dc, dw, ds_out and ds_in are
+ * 16-byte aligned too.
  */
 wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int in_dtype, int flags,
                                  const int32_t* lengths, const void* x, const void* dt, const float* w, const void* b,

@@ -1337,7 +1337,7 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
         return hip_status(e);
     }
     if (!x || !dt || !w || !b || !c || !go || !dx || !ddt || !db || !dc || (z && !dz)) return WKV_EINVAL;
-    if (!all_aligned(16, w, b, c, ckpt) || !all_aligned(in_size(in_dtype), x, dt, z, go, dx, ddt, dz, db, dc)) return WKV_EALIGN;
+    if (!all_aligned(16, w, b, c, ckpt, db, dc) || !all_aligned(in_size(in_dtype), x, dt, z, go, dx, ddt, dz)) return WKV_EALIGN;
     const size_t saved = ckpt ? 0 : (p.ckpt + 255) / 256 * 256, unsplit = p.part + p.dwp + p.vecp + saved;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < unsplit) return WKV_EWORKSPACE;
     char* ws = static_cast<char*>(workspace);

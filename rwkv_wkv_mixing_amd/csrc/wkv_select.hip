@@ -688,25 +688,36 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
 template <typename T>
 __global__ __launch_bounds__(256) void select_reduce_kernel(SelectArgs P, int64_t bc_blocks) {
     if (blockIdx.x < bc_blocks) {
-        const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // (row, group, b or c, n)
+        // four numbers a lane, a quarter of the channel tiles a wave
+        __shared__ f4 quarters[4][64];
+        const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+        const int64_t i = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 4;  // (row, group, b or c, n)
         const int64_t n2 = 2 * P.N, rows = P.B * P.T;
-        if (i >= rows * P.G * n2) return;
+        const bool here = i < rows * P.G * n2;
         const int64_t e = i % n2, g = i / n2 % P.G, row = i / (n2 * P.G);
-        const int per_group = P.ctiles / static_cast<int>(P.G);
-        const bool live = P.lengths == nullptr || row % P.T < P.lengths[row / P.T];
-        float sum = 0.f;
+        const int per_group = P.ctiles / static_cast<int>(P.G), each = (per_group + 3) / 4;
+        const int first = q * each, last = first + each < per_group ? first + each : per_group;
+        const bool live = here && (P.lengths == nullptr || row % P.T < P.lengths[row / P.T]);
+        f4 sum = {0.f, 0.f, 0.f, 0.f};
         if (live) {
             const float* at = P.part + (g * per_group * rows + row) * n2 + e;
-            for (int k = 0; k < per_group; ++k) sum += at[k * rows * n2];
+#pragma unroll 8
+            for (int k = first; k < last; ++k) sum += *reinterpret_cast<const f4*>(at + k * rows * n2);
         }
-        T* to = static_cast<T*>(e < P.N ? P.db : P.dc);
-        to[(row * P.G + g) * P.N + e % P.N] = narrow<T>(sum);
+        quarters[q][lane] = sum;
+        __syncthreads();
+        if (q != 0 || !here) return;
+        sum = (quarters[0][lane] + quarters[1][lane]) + (quarters[2][lane] + quarters[3][lane]);
+        T* to = static_cast<T*>(e < P.N ? P.db : P.dc) + (row * P.G + g) * P.N + e % P.N;
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<f4*>(to) = sum;
+        else *reinterpret_cast<uint2*>(to) = make_uint2(pk2(sum[0], sum[1]), pk2(sum[2], sum[3]));
         return;
     }
     const int64_t i = (static_cast<int64_t>(blockIdx.x) - bc_blocks) * 256 + threadIdx.x;
     const int64_t nw = P.C * P.N, rows = P.B * P.nseg;
     if (i < nw) {
         float sum = 0.f;
+#pragma unroll 8
         for (int64_t r = 0; r < rows; ++r) sum += P.dw_part[r * nw + i];
         P.dw[i] = sum;
     } else if (i < nw + 2 * P.C) {
@@ -714,6 +725,7 @@ __global__ __launch_bounds__(256) void select_reduce_kernel(SelectArgs P, int64_
         float* to = k == 0 ? P.dd : P.ddt_bias;
         if (to == nullptr) return;
         float sum = 0.f;
+#pragma unroll 8
         for (int64_t r = 0; r < rows; ++r) sum += P.vec_part[2 * (r * P.C + c) + k];
         to[c] = sum;
     }
@@ -867,7 +879,7 @@ hipError_t launch_select_bwd(const SelectArgs& a, hipStream_t stream) {
     }
     e = walk(a, kGrad, stream);
     if (e != hipSuccess) return e;
-    const int64_t bc = (a.B * a.T * a.G * 2 * a.N + 255) / 256, rest = (a.C * a.N + 2 * a.C + 255) / 256;
+    const int64_t bc = (a.B * a.T * a.G * 2 * a.N / 4 + 63) / 64, rest = (a.C * a.N + 2 * a.C + 255) / 256;
     const dim3 grid(static_cast<unsigned>(bc + rest));
     if (a.bf16) hipLaunchKernelGGL(select_reduce_kernel<uint16_t>, grid, dim3(256), 0, stream, a, bc);
     else hipLaunchKernelGGL(select_reduce_kernel<float>, grid, dim3(256), 0, stream, a, bc);
