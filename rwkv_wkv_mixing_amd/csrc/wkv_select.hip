@@ -6,10 +6,15 @@
 // vector units, which is what bounds it (a channel-token of N = 16 moves 8 bytes in bf16 and takes some 130 lane
 // instructions, 0.1 us a million at this card's rate against 0.04 for the bytes).
 //
-// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, four a wave: a wave's b_t and
-// c_t are then the same for all its lanes and reach its multiplications as lane broadcasts, and only delta, the written
-// value and the waves' parts of y pass through LDS.  Tiles of 16 tokens: the threads first work out delta and what is written for (token, channel)
-// pairs, one each; then every wave walks the tile; then the threads add the waves' parts, gate and store.
+// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, four a wave (two of N = 8): a
+// wave's b_t and c_t are then the same for all its lanes and reach its multiplications as lane broadcasts, and only
+// delta, the written value and the waves' parts of y pass through LDS.  Tiles of 16 tokens: the threads first work out
+// delta and what is written for (token, channel) pairs, one each; then every wave walks the tile; then the threads add
+// the waves' parts, gate and store.
+//
+// Measured at B = 8, T = 1024, C = 4096, bf16 (the data alone would take 43 us forward and 85 us back):
+//     N = 8: 142 us forward, 281 us for the gradients;  N = 16: 163 and 395 us.
+// 2048 waves are then at work, two a SIMD, and issue all but without a pause: the vector instructions are the bound.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -20,7 +25,6 @@ namespace wkv {
 namespace {
 
 constexpr int kTile = kSelectTile;  // tokens a tile
-constexpr int NS = 4;               // states a wave
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <typename T>
@@ -98,23 +102,32 @@ __device__ __forceinline__ float row_lane(float x) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + K, 0xf, 0xf, true));  // row_newbcast
 }
 
-// The sum over s < 4 of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
+// The sum over the wave's states of (lane K + s of its row of c) h[s].  A lane of another register cannot be read within two
 // instructions of a write to that register, which the compiler does not look for inside here: hence the wait, which
 // costs this wave a moment and the others of its SIMD nothing.
 template <int K>
-__device__ __forceinline__ float dot_row(float c, float h0, float h1, float h2, float h3) {
+__device__ __forceinline__ float dot_row(float c, const float (&h)[4]) {
     float y;
     asm("s_nop 1\n\t"
         "v_mul_f32_dpp %0, %1, %2 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%8 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
-        : "=&v"(y) : "v"(c), "v"(h0), "v"(h1), "v"(h2), "v"(h3), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+        : "=&v"(y) : "v"(c), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
+    return y;
+}
+template <int K>
+__device__ __forceinline__ float dot_row(float c, const float (&h)[2]) {
+    float y;
+    asm("s_nop 1\n\t"
+        "v_mul_f32_dpp %0, %1, %2 row_newbcast:%4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+        : "=&v"(y) : "v"(c), "v"(h[0]), "v"(h[1]), "n"(K), "n"(K + 1));
     return y;
 }
 // g[s] += (lane K + s of its row of c) v.
 template <int K>
-__device__ __forceinline__ void add_row(float (&g)[NS], float c, float v) {
+__device__ __forceinline__ void add_row(float (&g)[4], float c, float v) {
     asm("s_nop 1\n\t"
         "v_fmac_f32_dpp %0, %4, %5 row_newbcast:%6 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %1, %4, %5 row_newbcast:%7 row_mask:0xf bank_mask:0xf\n\t"
@@ -123,13 +136,20 @@ __device__ __forceinline__ void add_row(float (&g)[NS], float c, float v) {
         : "+v"(g[0]), "+v"(g[1]), "+v"(g[2]), "+v"(g[3])
         : "v"(c), "v"(v), "n"(K), "n"(K + 1), "n"(K + 2), "n"(K + 3));
 }
+template <int K>
+__device__ __forceinline__ void add_row(float (&g)[2], float c, float v) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %2, %3 row_newbcast:%4 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %2, %3 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+        : "+v"(g[0]), "+v"(g[1]) : "v"(c), "v"(v), "n"(K), "n"(K + 1));
+}
 
-// A token's 8 numbers (b and c of the wave's states) summed over the lanes that differ in bits 2 and 3 alone: state 0 + (bit 2
-// of the lane) of b (bit 3: of c) in q0, state 2 + (bit 2) in q1.  An addition with a lane exchange writes the quarters
+// A token's numbers (b and c of the wave's states) summed over the lanes that differ in bits 2 and 3 alone: state 0 + (bit 2
+// of the lane) of b (bit 3: of c) in q0, of four states state 2 + (bit 2) in q1.  An addition with a lane exchange writes the quarters
 // of its rows that the number belongs to, so two of them add up two numbers into one register.  The first wait is
 // for what the products before have written, the last one for the exchange that reads the results; in between nothing is
 // read through an exchange sooner than three instructions after it is written.
-__device__ __forceinline__ void fold_rows(const float (&b)[NS], const float (&c)[NS], float& q0, float& q1) {
+__device__ __forceinline__ void fold_rows(const float (&b)[4], const float (&c)[4], float& q0, float& q1) {
     float r0, r1, r2, r3;
     asm("s_nop 1\n\t"
         "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
@@ -149,13 +169,27 @@ __device__ __forceinline__ void fold_rows(const float (&b)[NS], const float (&c)
         : "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "v"(c[0]), "v"(c[1]), "v"(c[2]), "v"(c[3]));
 }
 
+__device__ __forceinline__ void fold_rows(const float (&b)[2], const float (&c)[2], float& q0) {
+    float r0, r1;
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %1, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %1, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %2, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "s_nop 1\n\t"
+        "v_add_f32_dpp %0, %1, %1 row_half_mirror row_mask:0xf bank_mask:0x5\n\t"
+        "v_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+        "s_nop 1"
+        : "=&v"(q0), "=&v"(r0), "=&v"(r1) : "v"(b[0]), "v"(b[1]), "v"(c[0]), "v"(c[1]));
+}
+
 // A wave's NS values a token of b or c for a tile: every row of 16 lanes holds the 16 NS numbers of the tile's tokens in
 // NS registers, token by token, so that each of them is one lane of one register.
-template <typename T>
+template <typename T, int NS>
 struct Row {
-    static constexpr int kPer = kTile / NS;  // tokens a register
-    T raw[NS];
-    float f[NS];
+    static constexpr int kPer = 16 / NS, kRegs = kTile / kPer;  // tokens a register, registers
+    T raw[kRegs];
+    float f[kRegs];
     // where a lane reads: its state, its token of the first register's, the bytes from token to token
     struct Where {
         uint32_t stride, s, first;
@@ -174,10 +208,10 @@ struct Row {
         keep32(w.first);
         if (left >= kTile) {
 #pragma unroll
-            for (int r = 0; r < NS; ++r) raw[r] = load_at(p, at + static_cast<int64_t>(r * kPer) * w.stride, w.first);
+            for (int r = 0; r < kRegs; ++r) raw[r] = load_at(p, at + static_cast<int64_t>(r * kPer) * w.stride, w.first);
         } else {
 #pragma unroll
-            for (int r = 0; r < NS; ++r) {
+            for (int r = 0; r < kRegs; ++r) {
                 const int j = r * kPer + w.j;
                 const T v = load_at(p, at, (j < left ? j : left - 1) * w.stride + w.s);
                 raw[r] = j < left ? v : T{0};
@@ -186,7 +220,7 @@ struct Row {
     }
     __device__ __forceinline__ void ready() {
 #pragma unroll
-        for (int r = 0; r < NS; ++r) {
+        for (int r = 0; r < kRegs; ++r) {
             f[r] = widen(raw[r]);
             asm volatile("" : "+v"(f[r]));  // (here and now, not where it is used)
         }
@@ -194,7 +228,7 @@ struct Row {
     // The compiler is to broadcast again rather than keep what it broadcast before.
     __device__ __forceinline__ void forget() {
 #pragma unroll
-        for (int r = 0; r < NS; ++r) asm volatile("" : "+v"(f[r]));
+        for (int r = 0; r < kRegs; ++r) asm volatile("" : "+v"(f[r]));
     }
     // the lane and the register of token J's first state
     template <int J>
@@ -205,13 +239,21 @@ struct Row {
     __device__ __forceinline__ float get() const { return row_lane<lane_of<J>() + S>(reg<J>()); }
 };
 
+template <int NS>
 __device__ __forceinline__ void load_states(const float* p, bool valid, float (&h)[NS]) {
-    const f4 v = valid ? *reinterpret_cast<const f4*>(p) : f4{0.f, 0.f, 0.f, 0.f};
+    typedef float Some __attribute__((ext_vector_type(NS)));
+    Some v = {};
+    if (valid) v = *reinterpret_cast<const Some*>(p);
 #pragma unroll
     for (int i = 0; i < NS; ++i) h[i] = v[i];
 }
+template <int NS>
 __device__ __forceinline__ void store_states(float* p, const float (&h)[NS]) {
-    *reinterpret_cast<f4*>(p) = f4{h[0], h[1], h[2], h[3]};
+    typedef float Some __attribute__((ext_vector_type(NS)));
+    Some v;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = h[i];
+    *reinterpret_cast<Some*>(p) = v;
 }
 
 // Where a workgroup works: tile of channels, batch row, segment; its lane's channel and its tokens.
@@ -261,7 +303,7 @@ __device__ __forceinline__ void yield_to_later(int done, int all) {
 // the last token to the first: g <- a (g + c gy).
 enum { kWalkOut = 0, kWalkLocal = 1, kWalkAdjoint = 2, kGrad = 3 };  // kGrad: select_grad_kernel
 
-template <typename T, int W, int Mode>
+template <typename T, int NS, int W, int Mode>
 __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;  // (token, channel) pairs a thread works out
     constexpr bool kWide = sizeof(T) == 4, kOut = Mode == kWalkOut, kAdj = Mode == kWalkAdjoint;
@@ -301,7 +343,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     const int64_t CB = P.C * static_cast<int64_t>(sizeof(T)), GNB = GN * static_cast<int64_t>(sizeof(T));  // bytes a token
     T rx[kEach], rd[kEach], rz[kEach];
     float ex[3][kEach], ez[3][kEach];
-    Row<T> b, c;
+    Row<T, NS> b, c;
     const auto tile_at = [&](int i) { return p.t0 + (kAdj ? ntiles - 1 - i : i) * kTile; };
     const auto fetch = [&](int i) {
         keep32(chb);
@@ -315,7 +357,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
             if constexpr (kOut || kAdj) rz[k] = load_at(gate_in, row, chb);
         }
     };
-    typename Row<T>::Where where = Row<T>::where(GN, lane);
+    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
     const auto fetch_bc = [&](int i) {
         const int t = tile_at(i < ntiles ? i : ntiles - 1);
         b.fetch(bt, t * GNB, where, p.te - t);
@@ -419,7 +461,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
                 else h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
             });
             if constexpr (kOut) {
-                parts[i & 1][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[0], h[1], h[2], h[3]);
+                parts[i & 1][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h);
             }
         });
         stage(i + 1);
@@ -486,7 +528,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
 //     g *= a_t,   q = g h_{t-1},   ddelta_t = du_t x_t - sum_n w q,   dw -= delta_t q
 // The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
 // of which every exchange between lanes halves the registers, so 16 tokens end as two registers of one number a lane.
-template <typename T, int W>
+template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     constexpr int N = NS * W, kEach = kTile / W;
     constexpr bool kWide = sizeof(T) == 4;
@@ -521,8 +563,8 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     uint32_t chb = p.ch * static_cast<uint32_t>(sizeof(T));
     const int64_t CB = P.C * static_cast<int64_t>(sizeof(T)), GNB = GN * static_cast<int64_t>(sizeof(T));  // bytes a token
     T rx[kEach], rd[kEach], rz[kEach], rg[kEach];
-    Row<T> b, c;
-    typename Row<T>::Where where = Row<T>::where(GN, lane);
+    Row<T, NS> b, c;
+    typename Row<T, NS>::Where where = Row<T, NS>::where(GN, lane);
     const auto tile_at = [&](int i) { return p.t0 + i * kTile; };
     const auto fetch = [&](int i) {  // (behind the last token: that one again; before the first tile: nothing new)
         keep32(chb);
@@ -577,7 +619,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
                 a[j][s] = exp2_fast(v.x * w2[s]);
                 h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, s>() * v.y);
             });
-            parts[0][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[j + 1][0], h[j + 1][1], h[j + 1][2], h[j + 1][3]);
+            parts[0][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[j + 1]);
         });
         b.forget();
         c.forget();
@@ -587,7 +629,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             const float4 v = put[j][lane];
             float down = 0.f, pb[NS], pc[NS];
             add_row<c.template lane_of<j>()>(g, c.template reg<j>(), v.z);
-            parts[1][wave][j][lane] = dot_row<b.template lane_of<j>()>(b.template reg<j>(), g[0], g[1], g[2], g[3]);
+            parts[1][wave][j][lane] = dot_row<b.template lane_of<j>()>(b.template reg<j>(), g);
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 pb[s] = g[s] * v.y, pc[s] = v.z * h[j + 1][s];
@@ -597,31 +639,52 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
                 dw[s] = fmaf(-m, v.x, dw[s]);
             }
             parts[2][wave][j][lane] = down;
-            float q0, q1;
-            fold_rows(pb, pc, q0, q1);
-            // states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones
-            const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(q0), __float_as_uint(q1), false, false);
-            const float one = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+            // of four states 0 and 1 to the even rows of 16 lanes, 2 and 3 to the odd ones; then token j to one half of the
+            // lanes that are left to tell apart (two states: to the even rows), j + 8 to the other
+            float one;
+            if constexpr (NS == 4) {
+                float q0, q1;
+                fold_rows(pb, pc, q0, q1);
+                const auto x1 = __builtin_amdgcn_permlane16_swap(__float_as_uint(q0), __float_as_uint(q1), false, false);
+                one = __uint_as_float(x1[0]) + __uint_as_float(x1[1]);
+            } else {
+                fold_rows(pb, pc, one);
+            }
             if constexpr (j >= 8) {
                 tokens[j - 8] = one;
-            } else {  // token j to the lower half of the lanes, j + 8 to the upper
-                const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(one), __float_as_uint(tokens[j]), false, false);
-                tokens[j] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+            } else {
+                const uint32_t lo = __float_as_uint(one), hi = __float_as_uint(tokens[j]);
+                if constexpr (NS == 4) {
+                    const auto x2 = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+                    tokens[j] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+                } else {
+                    const auto x2 = __builtin_amdgcn_permlane16_swap(lo, hi, false, false);
+                    tokens[j] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+                }
             }
         });
-        // of eight registers two: tokens j + 4 (bit 1 of the lane) and j + 2 (bit 0)
+        constexpr int kFour = NS == 4 ? 8 : 4;  // registers before the lanes of a four are told apart
+        if constexpr (NS == 2) {  // token k to the lower half of the lanes, k + 4 to the upper
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + 4] + dpp<0x4E>(tokens[k + 4]);  // lane ^ 2
+            for (int k = 0; k < 4; ++k) {
+                const auto x2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(tokens[k]), __float_as_uint(tokens[k + 4]), false, false);
+                tokens[k] = __uint_as_float(x2[0]) + __uint_as_float(x2[1]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kFour / 2; ++k) {
+            const float lo = tokens[k] + dpp<0x4E>(tokens[k]), hi = tokens[k + kFour / 2] + dpp<0x4E>(tokens[k + kFour / 2]);  // lane ^ 2
             tokens[k] = (lane & 2) != 0 ? hi : lo;
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float lo = tokens[k] + dpp<0xB1>(tokens[k]), hi = tokens[k + 2] + dpp<0xB1>(tokens[k + 2]);  // lane ^ 1
-            const int tok = k + (lane & 2) * 2 + (lane & 1) * 2 + (lane >> 5) * 8;
+        for (int k = 0; k < kFour / 4; ++k) {
+            const float lo = tokens[k] + dpp<0xB1>(tokens[k]), hi = tokens[k + kFour / 4] + dpp<0xB1>(tokens[k + kFour / 4]);  // lane ^ 1
+            const int bit0 = lane & 1, bit1 = (lane >> 1) & 1, bit4 = (lane >> 4) & 1, bit5 = lane >> 5;
+            const int tok = NS == 4 ? k + bit1 * 4 + bit0 * 2 + bit5 * 8 : bit1 * 2 + bit0 + bit5 * 4 + bit4 * 8;
+            const int state = wave * NS + (NS == 4 ? bit4 * 2 : 0) + ((lane >> 2) & 1);
             if (tok < n) {
                 const int64_t row = (static_cast<int64_t>(p.ct) * P.B * P.T + row0 + t + tok) * (2 * N);
-                P.part[row + ((lane >> 3) & 1) * N + wave * NS + ((lane >> 4) & 1) * 2 + ((lane >> 2) & 1)] = (lane & 1) != 0 ? hi : lo;
+                P.part[row + ((lane >> 3) & 1) * N + state] = bit0 != 0 ? hi : lo;
             }
         }
         __syncthreads();
@@ -736,7 +799,7 @@ __global__ __launch_bounds__(256) void select_reduce_kernel(SelectArgs P, int64_
 template <typename T, int Lanes>
 __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     constexpr bool kWide = sizeof(T) == 4;
-    constexpr int N = 4 * Lanes;
+    constexpr int NS = 4, N = NS * Lanes;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * (256 / Lanes) + threadIdx.x / Lanes;
     const bool valid = at < P.C;
     const int ch = static_cast<int>(valid ? at : P.C - 1), q = threadIdx.x % Lanes;  // spare lanes take part in the sums
@@ -784,15 +847,15 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     }
 }
 
-template <typename T, int W>
+template <typename T, int NS, int W>
 hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
     const bool all = mode == kWalkOut || mode == kGrad;
     const dim3 grid(static_cast<unsigned>(a.ctiles * a.B * (all ? a.nseg : a.nseg - 1))), block(64 * W);
     switch (mode) {
-        case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkOut>), grid, block, 0, stream, a); break;
-        case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkLocal>), grid, block, 0, stream, a); break;
-        case kWalkAdjoint: hipLaunchKernelGGL((select_walk_kernel<T, W, kWalkAdjoint>), grid, block, 0, stream, a); break;
-        default: hipLaunchKernelGGL((select_grad_kernel<T, W>), grid, block, 0, stream, a); break;
+        case kWalkOut: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkOut>), grid, block, 0, stream, a); break;
+        case kWalkLocal: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkLocal>), grid, block, 0, stream, a); break;
+        case kWalkAdjoint: hipLaunchKernelGGL((select_walk_kernel<T, NS, W, kWalkAdjoint>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((select_grad_kernel<T, NS, W>), grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
 }
@@ -800,9 +863,11 @@ hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
 template <typename T>
 hipError_t walk_n(const SelectArgs& a, int mode, hipStream_t stream) {
     switch (a.N) {
-        case 8: return walk_t<T, 2>(a, mode, stream);
-        case 16: return walk_t<T, 4>(a, mode, stream);
-        default: return walk_t<T, 8>(a, mode, stream);
+        // Two states a wave: with two waves of four the card is half empty (B = 8, T = 1024, C = 4096, bf16: forward and
+        // gradients together 833 us, of two states 422).
+        case 8: return walk_t<T, 2, 4>(a, mode, stream);
+        case 16: return walk_t<T, 4, 4>(a, mode, stream);
+        default: return walk_t<T, 4, 8>(a, mode, stream);
     }
 }
 
@@ -826,7 +891,7 @@ int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bw
     const int64_t tiles = (T + kTile - 1) / kTile, groups = B * ctiles;
     *per = tiles * kTile;
     if (groups <= 0 || groups >= 512 || tiles < 4) return 1;
-    const double alone = N == 8 ? 2.4 : 1.7, shared = 0.35 * (N / 4), scale = bwd ? 2.6 : 1.0;
+    const double alone = N == 8 ? 1.2 : 1.7, shared = N == 8 ? 0.9 : 0.35 * static_cast<double>(N / 4), scale = bwd ? 2.6 : 1.0;
     const auto tile_us = [&](int64_t workgroups) {
         const double busy = shared * static_cast<double>((workgroups + 255) / 256);
         return scale * (busy > alone ? busy : alone);
