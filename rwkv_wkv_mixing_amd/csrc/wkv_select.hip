@@ -62,6 +62,9 @@ __device__ __forceinline__ float log1p_unit(float e) {
     return p * e;
 }
 
+// A decay rate: infinity is held finite, so that a step of zero keeps the state (not a number stays what it is).
+__device__ __forceinline__ float held(float w) { return w > 2e38f ? 2e38f : w; }
+
 // delta of some tokens from dt + dt_bias, and its derivative by dt.
 template <bool Wide, bool Grad, int E>
 __device__ __forceinline__ void steps_of(float (&raw)[E], bool softplus, float (&grad)[E]) {
@@ -325,9 +328,8 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
 
     float w2[NS], h[NS];
     load_states(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w2);
-    // (a rate of infinity is held finite, so that a step of zero keeps the state)
 #pragma unroll
-    for (int i = 0; i < NS; ++i) w2[i] = -fminf(w2[i], 2e38f) * kLog2e, h[i] = 0.f;
+    for (int i = 0; i < NS; ++i) w2[i] = -held(w2[i]) * kLog2e, h[i] = 0.f;
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     if constexpr (kOut) {
         if (P.nseg > 1) load_states(P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, p.valid, h);
@@ -510,7 +512,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n) return;
     const int64_t bc = i / P.N;
-    const float w2 = -fminf(P.w[bc % P.C * P.N + i % P.N], 2e38f) * kLog2e;
+    const float w2 = -held(P.w[bc % P.C * P.N + i % P.N]) * kLog2e;
     const float* first = reverse ? P.ds_out : P.s_in;
     float h = first != nullptr ? first[i] : 0.f;
     for (int64_t k = 0; k < P.nseg; ++k) {
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     const float* from = P.nseg > 1 ? P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N : P.ds_out;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) w1[i] = fminf(w1[i], 2e38f), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
+    for (int i = 0; i < NS; ++i) w1[i] = held(w1[i]), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
     if (from != nullptr) load_states(from + state, p.valid, g);
 
     const bool has_z = z != nullptr, spare = !__all(p.valid);
@@ -808,7 +810,7 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     float w2[NS];
     load_states(P.w + static_cast<int64_t>(ch) * N + 4 * q, true, w2);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) w2[s] = -fminf(w2[s], 2e38f) * kLog2e;
+    for (int s = 0; s < NS; ++s) w2[s] = -held(w2[s]) * kLog2e;
     const float bias = P.dt_bias != nullptr ? P.dt_bias[ch] : 0.f, skip = P.d != nullptr ? P.d[ch] : 0.f;
     const int tokens = static_cast<int>(P.T);
     for (int64_t b = blockIdx.y; b < P.B; b += gridDim.y) {

@@ -176,6 +176,26 @@ def test_select_not_a_number_stays_where_it_is_read(bad, T, split, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,split", [(3, False), (40, False), (700, True)], ids=["steps", "whole", "split"])
+@pytest.mark.parametrize("N", [8, 16])
+def test_select_rates_that_are_not_a_number_show(N, T, split, dtype):
+    """A channel with one such rate has no output, state or gradient by x that is a number (the last token's gradient by x
+    needs no rate); the others are as without it."""
+    B, C = 2, 70
+    p = draw(B, T, C, 1, N, dtype)
+    args, kw = inputs(p)
+    clean, S0 = O.select_forward(*args, split=split, return_state=True, **kw)
+    ch = 66
+    p["w"][ch, N - 3] = float("nan")
+    out, S1 = O.select_forward(*args, split=split, return_state=True, **kw)
+    assert bool(torch.isnan(out[:, :, ch]).all()) and bool(torch.isnan(S1[:, ch, N - 3]).all())
+    g = O.select_backward(*args, p["go"], split=split, **kw)
+    assert bool(torch.isnan(g["dx"][:, :-1, ch]).all()) and bool(torch.isnan(g["dw"][ch, N - 3]))
+    out[:, :, ch], S1[:, ch] = clean[:, :, ch], S0[:, ch]
+    assert torch.equal(out, clean) and torch.equal(S1, S0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 def test_conv_not_a_number_stays_where_it_is_read(dtype):
     p = draw_conv(2, 70, 68, 4, dtype)
     clean = O.conv_forward(p["x"], p["weight"], p["bias"])
