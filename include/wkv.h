@@ -739,13 +739,13 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
  * in_dtype  dtype of x, s_in, s_out, out and, backward, of gout, ds_out, dx, ds_in.
  * lengths   [B] int32 or NULL: tokens of each row (clamped to 0 .. T).  Rows
  *           behind it are not read; those of out and dx are zeros.
- * x, out    [B, T, C]; out must not overlap an input.
+ * x, out    [B, T, C]; out must not overlap x, s_in or s_out, nor s_out x (WKV_EINVAL).
  * weight    [K, C] float32, the last tap on the token itself; bias [C] or NULL.
  * s_in      [B, K - 1, C] or NULL (zeros).  s_out  alike, or NULL; may be s_in.
  *           With T == 0 it receives s_in (or zeros).
  *
- * Backward, of sum <gout, out> + <ds_out, s_out>: dx, dweight, dbias (needed with
- * bias), ds_in (or NULL; it must not overlap ds_out: WKV_EINVAL).  dweight and dbias
+ * Backward, of sum <gout, out> + <ds_out, s_out>: dx (it must not overlap x or gout:
+ * WKV_EINVAL), dweight, dbias (needed with bias), ds_in (or NULL; nor may it ds_out).  dweight and dbias
  * are sums over rows and tokens in a fixed order; all outputs are overwritten.
  * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
  *           clobbered.  Not needed without tokens.

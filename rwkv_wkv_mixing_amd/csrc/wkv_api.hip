@@ -1056,6 +1056,12 @@ ConvPlan conv_plan(int64_t B, int64_t T, int64_t C, int64_t K, int dt, int act) 
     return p;
 }
 
+// Whether two tensors of so many bytes share any.
+bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a && b && p < q + static_cast<uintptr_t>(bbytes) && q < p + static_cast<uintptr_t>(abytes);
+}
+
 // vectors of four elements: four floats of the weights and their gradients, which lie on the 16-byte grid
 template <class... P>
 bool conv_vec(int64_t C, int dt, const float* weight, const float* bias, P... p) {
@@ -1227,6 +1233,11 @@ wkv_status_t wkv_conv_forward(int64_t B, int64_t T, int64_t C, int64_t K, int in
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
     if (p.n == 0) return hip_status(wkv::launch_conv_copy(s_in, s_out, p.ns, in_dtype == WKV_BF16, stream));
     if (!x || !weight || !out) return WKV_EINVAL;
+    // a token is read by the workgroups of the tokens behind it, so none of x may be overwritten
+    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
+    if (overlap(x, bytes, out, bytes) || overlap(s_in, carried, out, bytes) || overlap(x, bytes, s_out, carried) ||
+        overlap(out, bytes, s_out, carried) || (s_in != s_out && overlap(s_in, carried, s_out, carried)))
+        return WKV_EINVAL;
     wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
     a.out = out;
     a.s_out = s_out;
@@ -1252,10 +1263,9 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
         return hip_status(e);
     }
     if (!x || !weight || !gout || !dx) return WKV_EINVAL;
-    // a row's last tokens read ds_out when its first ones may have written ds_in
-    const uintptr_t in = reinterpret_cast<uintptr_t>(ds_in), from = reinterpret_cast<uintptr_t>(ds_out);
-    const uintptr_t span = static_cast<uintptr_t>(p.ns) * es;
-    if (ds_in && ds_out && in < from + span && from < in + span) return WKV_EINVAL;
+    // a row's last tokens read ds_out when its first ones may have written ds_in, and tokens are read as in the forward
+    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
+    if (overlap(ds_out, carried, ds_in, carried) || overlap(x, bytes, dx, bytes) || overlap(gout, bytes, dx, bytes)) return WKV_EINVAL;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.ws_bytes) return WKV_EWORKSPACE;
     wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
     a.gout = gout;

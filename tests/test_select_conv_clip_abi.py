@@ -29,8 +29,8 @@ def test_header_constants_match_binding():
     assert re.search(rf"#define WKV_SELECT_SOFTPLUS {L.WKV_SELECT_SOFTPLUS}\b", src)
 
 
-def conv(lib, bwd, B=2, T=20, C=8, K=4, dt=L.WKV_BF16, act=2, ln=None, x=X, weight=X, bias=X, s_in=None, out=X, s_out=None, gout=X,
-         ds_out=None, dx=X, dweight=X, dbias=X, ds_in=None, ws=X, nws=1 << 30):
+def conv(lib, bwd, B=2, T=20, C=8, K=4, dt=L.WKV_BF16, act=2, ln=None, x=X, weight=X, bias=X, s_in=None, out=X + 4096, s_out=None,
+         gout=X, ds_out=None, dx=X + 4096, dweight=X, dbias=X, ds_in=None, ws=X, nws=1 << 30):
     if not bwd:
         return lib.wkv_conv_forward(B, T, C, K, dt, act, ln, x, weight, bias, s_in, out, s_out, None)
     return lib.wkv_conv_backward(B, T, C, K, dt, act, ln, x, weight, bias, s_in, gout, ds_out, dx, dweight, dbias, ds_in, ws, nws,
@@ -51,6 +51,14 @@ def test_conv_refusals(lib, bwd):
         assert conv(lib, bwd, out=None) == L.WKV_EINVAL
         assert conv(lib, bwd, out=X + 1) == L.WKV_EALIGN and conv(lib, bwd, s_out=X + 1) == L.WKV_EALIGN
         assert conv(lib, bwd, B=0, x=None, weight=None, out=None) == L.WKV_OK
+        whole, carried = 2 * 20 * 8 * 2, 2 * 3 * 8 * 2  # bytes of x, and of the carried inputs
+        for off in (0, 2, whole - 2, -whole + 2):
+            assert conv(lib, bwd, out=X + off) == L.WKV_EINVAL, off
+        for off in (0, whole - 2, -carried + 2):
+            assert conv(lib, bwd, s_out=X + off) == L.WKV_EINVAL, off
+            assert conv(lib, bwd, s_out=X + 4096 + off) == L.WKV_EINVAL and conv(lib, bwd, s_in=X + 4096 + off) == L.WKV_EINVAL, off
+        for off in (2, carried - 2, -2):
+            assert conv(lib, bwd, s_in=X + 8192, s_out=X + 8192 + off) == L.WKV_EINVAL, off
         return
     for name in ("gout", "dx", "dweight", "dbias"):
         assert conv(lib, bwd, **{name: None}) == L.WKV_EINVAL, name
@@ -62,6 +70,10 @@ def test_conv_refusals(lib, bwd):
     for off in (0, 2, span - 2, -span + 2):
         assert conv(lib, bwd, ds_out=X, ds_in=X + off, nws=0) == L.WKV_EINVAL, off
     assert conv(lib, bwd, ds_out=X, ds_in=X + span, nws=0) == L.WKV_EWORKSPACE  # (next to each other: the next check)
+    whole = 2 * 20 * 8 * 2
+    for off in (0, 2, whole - 2, -whole + 2):
+        assert conv(lib, bwd, dx=X + off, gout=X + 8192, nws=0) == L.WKV_EINVAL, off
+        assert conv(lib, bwd, dx=X + 8192 + off, gout=X + 8192, nws=0) == L.WKV_EINVAL, off
     need = lib.wkv_conv_backward_workspace_bytes(2, 20, 8, 4)
     assert need > 0 and need % (5 * 8 * 4) == 0
     for bad in (dict(nws=need - 1), dict(ws=None), dict(ws=X + 128)):
