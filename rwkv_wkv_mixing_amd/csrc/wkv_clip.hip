@@ -1,8 +1,9 @@
 // The norm of all gradients together, and the gradients scaled so that it is at most max_norm:
 //     norm = sqrt(sum over the tensors of the sums of their squares),  g' = g min(1, max_norm / (norm + eps))
-// Two passes over memory, which is what bounds them; the second one mostly reads from the last level cache where the
-// gradients fit it.  A launch takes many tensors: their addresses and sizes come as kernel arguments, their elements
-// are dealt out in chunks, and every workgroup takes every so many-th chunk of a fixed grid, so sums have a fixed order.
+// Two passes over memory, which is what bounds them (1.4 GB in bf16 and float32: sums 228 us, 6.2 TB/s, scaling 510 us,
+// 5.5 TB/s read and written); the second one mostly reads from the last level cache where the gradients fit it.  A
+// launch takes many tensors: their addresses and sizes come as kernel arguments, their elements are dealt out in
+// chunks, and every workgroup takes every so many-th chunk of a fixed grid, so sums have a fixed order.
 //
 // Squares of eight elements are added in float32 and the eights in float64: squares cannot cancel, so the sum is good
 // to about 2^-23, and where the eight overflow or come near float32's smallest numbers they are added again in float64.
@@ -211,8 +212,8 @@ __global__ __launch_bounds__(kThreads) void clip_norm_kernel(const double* part,
 }
 
 // Every workgroup adds up the partial sums for itself, so the factor needs no launch of its own.  PastCache: outputs leave
-// past the caches, where the gradients do not fit them anyway and the stores would drive out what is read next (690 M
-// elements: 780 -> 737 us).
+// past the caches, where the gradients do not fit them anyway and the stores would drive out what is read next (282 MB
+// of gradients: 185 -> 169 us, 1.4 GB: 788 -> 746; 86 MB take 57 us either way, and are still there for the optimizer).
 template <bool PastCache>
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const double* part, int64_t nparts, float max_norm,
                                                               float eps, float* norm) {

@@ -3,12 +3,13 @@
 // row's tokens (so that X[t + K - 1] is token t):
 //     pre_t = bias + sum_j weight[j] X[t + j],   out_t = act(pre_t)
 // Streaming work: a thread owns V channels over a run of tokens, so x is read once (and K - 1 tokens a run twice) and
-// the window stays in registers; what bounds it is memory.
+// the window stays in registers; what bounds it is memory (8 x 1024 x 4096 bf16, K = 4: 23 us, 5.7 TB/s).
 //
 // Backward, with g_t = gout_t act'(pre_t) of the row's tokens (zero elsewhere):
 //     dX[e] = sum_j weight[j] g_{e - j} (+ the carried-out inputs' gradient),   dweight[j] = sum g_t X[t + j],   dbias = sum g
 // A thread walks its run and K - 1 tokens more, computing pre again from x.  The weights' sums are kept a thread, added
-// over a workgroup's runs in LDS and over workgroups by a second kernel, each in a fixed order.
+// over a workgroup's runs in LDS and over workgroups by a second kernel, each in a fixed order.  Some 40 vector
+// instructions an element next to 6 bytes: at the same size 52 us, 3.9 TB/s, with the vector units busy two thirds of them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -123,7 +124,8 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run, int64_t ncb) {
     typedef Vec<T, V> Ops;
     typedef typename Ops::Raw Raw;
-    // tokens whose loads are on their way at once: a multiple of K, so that the window, a ring of K rows, is back where it was
+    // Tokens whose loads are on their way at once (4 of them: 32.5 us for 31.1 of 8): a multiple of K, so that the window, a
+    // ring of K rows, is back where it was.
     constexpr int kAhead = K == 3 ? 6 : 8;
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t cb = blk % ncb, rest = blk / ncb, ntb = (P.T + kRuns * run - 1) / (kRuns * run);
@@ -184,7 +186,7 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run, int64_t ncb) {
     typedef Vec<T, V> Ops;
     typedef typename Ops::Raw Raw;
-    constexpr int kAhead = K == 3 ? 3 : 4;  // a multiple of K: the windows are rings
+    constexpr int kAhead = K == 3 ? 3 : 4;  // a multiple of K: the windows are rings (2: 60 us, 4: 52, 8: 58)
     __shared__ float sums[kRuns][K + 1][V][kCols];
     const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t cb = blk % ncb, slot = blk / ncb;
@@ -340,21 +342,25 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
     }
 }
 
-// dweight and dbias from the slots' sums, in order: a wave takes 64 outputs, its workgroup's four waves a quarter of
-// the slots each.
-__global__ __launch_bounds__(256) void conv_reduce_kernel(ConvArgs P) {
-    __shared__ float sums[4][64];
+// dweight and dbias from the slots' sums, in order: a lane takes an output, each of the workgroup's 16 waves a sixteenth
+// of the slots.
+constexpr int kParts = 16;
+__global__ __launch_bounds__(64 * kParts) void conv_reduce_kernel(ConvArgs P) {
+    __shared__ float sums[kParts][64];
     const int64_t n = (P.K + 1) * P.C, i = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
     const int q = threadIdx.x >> 6;
-    const int64_t each = (P.slots + 3) / 4, first = q * each, last = first + each < P.slots ? first + each : P.slots;
+    const int64_t each = (P.slots + kParts - 1) / kParts, first = q * each, last = first + each < P.slots ? first + each : P.slots;
     float sum = 0.f;
-    if (i < n)
+    if (i < n) {
+#pragma unroll 4
         for (int64_t s = first; s < last; ++s) sum += P.part[s * n + i];
+    }
     sums[q][threadIdx.x & 63] = sum;
     __syncthreads();
     if (q != 0 || i >= n) return;
-    const int l = threadIdx.x;
-    sum = (sums[0][l] + sums[1][l]) + (sums[2][l] + sums[3][l]);
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) sum += sums[k][threadIdx.x];
     if (i < P.K * P.C) P.dweight[i] = sum;
     else if (P.dbias != nullptr) P.dbias[i - P.K * P.C] = sum;
 }
@@ -366,7 +372,8 @@ __global__ __launch_bounds__(256) void conv_copy_kernel(const T* from, T* to, in
     if (i < n) to[i] = from != nullptr ? from[i] : T{0};
 }
 
-// Tokens a run: long ones read less twice, but the card wants some 2048 workgroups.
+// Tokens a run: long ones read less twice, but the card wants some 2048 workgroups (4096 of them: 32 x 1024 x 768 forward
+// 30.6 us for 22.9).
 int run_of(int64_t B, int64_t T, int64_t ncb, int longest) {
     int run = longest;
     while (run > 4 && B * ((T + kRuns * run - 1) / (kRuns * run)) * ncb < 2048) run /= 2;
@@ -383,17 +390,19 @@ template <typename T, int V, int K>
 hipError_t conv_launch(const ConvArgs& a, bool bwd, hipStream_t stream) {
     const int64_t ncb = (a.C + kCols * V - 1) / (kCols * V);
     if (!bwd) {
-        const int run = run_of(a.B, a.T, ncb, 16);
+        // (8 x 1024 x 4096: runs of 8 and 16 bf16 28.9 and 31.1 us, float32 49.8 and 54.5, 4095 channels 61.2 and 50.0)
+        const int run = run_of(a.B, a.T, ncb, V > 1 ? 8 : 16);
         const int64_t ntb = (a.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
         hipLaunchKernelGGL((conv_fwd_kernel<T, V, K>), grid_of(a.B * ntb * ncb), dim3(kThreads), 0, stream, a, run, ncb);
         return hipGetLastError();
     }
-    const int run = run_of(a.B, a.T, ncb, 32);
+    // (there too: runs of 16, 32 and 64 bf16 63.0, 60.8 and 61 us, 4095 channels 88, 83 and 94; float32 93, 104 and 106)
+    const int run = run_of(a.B, a.T, ncb, V > 1 && sizeof(T) == 4 ? 16 : 32);
     hipLaunchKernelGGL((conv_bwd_kernel<T, V, K>), grid_of(a.slots * ncb), dim3(kThreads), 0, stream, a, run, ncb);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = (K + 1) * a.C;
-    hipLaunchKernelGGL(conv_reduce_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(conv_reduce_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64 * kParts), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -407,6 +416,7 @@ hipError_t conv_k(const ConvArgs& a, bool bwd, hipStream_t stream) {
 }
 
 hipError_t conv_t(const ConvArgs& a, bool bwd, hipStream_t stream) {
+    // four channels a thread forward, two backward, where four leave room for fewer waves (bf16 52 us, 64 of four)
     if (!a.vec) return a.bf16 ? conv_k<uint16_t, 1>(a, bwd, stream) : conv_k<float, 1>(a, bwd, stream);
     if (bwd) return a.bf16 ? conv_k<uint16_t, 2>(a, bwd, stream) : conv_k<float, 2>(a, bwd, stream);
     return a.bf16 ? conv_k<uint16_t, 4>(a, bwd, stream) : conv_k<float, 4>(a, bwd, stream);
@@ -414,8 +424,8 @@ hipError_t conv_t(const ConvArgs& a, bool bwd, hipStream_t stream) {
 
 }  // namespace
 
-// Rows of partial sums of the backward: as many workgroups as fill the card and no more than there are tiles of the
-// shortest runs.
+// Rows of partial sums of the backward: as many workgroups as fill the card (4096 of one channel a thread: 4095 channels
+// 83 us; 2048: 92) and no more than there are tiles of the shortest runs.
 int64_t conv_slots(int64_t B, int64_t T, int64_t C) {
     const int64_t ncb = (C + kCols - 1) / kCols, tiles = B * ((T + kRuns * 4 - 1) / (kRuns * 4));
     int64_t most = 4096 / (ncb > 0 ? ncb : 1);

@@ -293,7 +293,8 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane, int fir
 
 // Two workgroups on a compute unit do not share it evenly: the waves that came first go first, so one workgroup is done
 // early and the other one walks its rest alone, which leaves the vector units waiting (132 and 182 us at B = 8, T = 1024,
-// C = 4096).  A wave's priority falls with every quarter of its tiles, so that who is behind goes first.
+// C = 4096, N = 16).  A wave's priority falls with every quarter of its tiles, so that who is behind goes first: the
+// forward 188 -> 180 us, the gradients 465 -> 447.
 __device__ __forceinline__ void yield_to_later(int done, int all) {
     const int quarter = (all + 3) / 4;
     if (done == 0) __builtin_amdgcn_s_setprio(3);
@@ -888,7 +889,13 @@ hipError_t chain(const SelectArgs& a, bool reverse, hipStream_t stream) {
 // A time split walks everything twice (once for what the segments do to a state of zero, then from their start states), and
 // pays where the channel tiles alone leave most of the card idle or there are tokens without end.  The model, in us: a
 // tile of 16 tokens takes a workgroup on a compute unit of its own about `alone`, and the unit's workgroups together at
-// least 0.35 a wave; the backward 2.6 times that; the second walk 0.8 of the first; its launches 8.
+// least `shared` each; the backward 2.6 times that; the second walk 0.8 of the first; its launches 8.  Split and whole, forward and
+// backward, in us:
+//     2 rows of 333 tokens, 1002 channels, N = 8, float32      22 + 33 and  37 +  81   7 segments
+//     1 row of 300 tokens, 768 channels, N = 8, bf16           17 + 24 and  31 +  70   10
+//     1 row of 2000 tokens, 4096 channels, N = 8, bf16         68 + 112 and 186 + 430  8
+//     3 rows of 929 tokens, 4008 channels, N = 8, bf16        101 + 159 and 99 + 213   none forward, 4 backward
+//     8 rows of 1024 tokens, 4096 channels, N = 8, bf16       156 + 301 and 142 + 281  none
 int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bwd, int64_t* per) {
     const int64_t tiles = (T + kTile - 1) / kTile, groups = B * ctiles;
     *per = tiles * kTile;
