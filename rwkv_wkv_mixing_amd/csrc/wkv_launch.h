@@ -453,7 +453,7 @@ struct SelectArgs {
     // forward
     void* out = nullptr;      // [B, T, C]
     float* s_out = nullptr;   // [B, C, N] or NULL
-    float* ckpt = nullptr;    // [B, tiles, N / 4, C, 4] (N = 8: [.., 4, C, 2]) the state before every kSelectTile tokens, or NULL
+    float* ckpt = nullptr;    // [B, tiles, N / 4, C, 4] the state before every kSelectTile tokens, or NULL
     // backward
     const float* saved = nullptr;  // the forward's ckpt
     const void* go = nullptr;      // [B, T, C]

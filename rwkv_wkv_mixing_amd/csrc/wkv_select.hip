@@ -6,7 +6,7 @@
 // vector units, which is what bounds it (a channel-token of N = 16 moves 8 bytes in bf16 and takes some 130 lane
 // instructions, 0.1 us a million at this card's rate against 0.04 for the bytes).
 //
-// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, four a wave (two of N = 8): a
+// A workgroup takes 64 channels, a lane each, and its W waves share out the N states, four or two a wave: a
 // wave's b_t and c_t are then the same for all its lanes and reach its multiplications as lane broadcasts, and only
 // delta, the written value and the waves' parts of y pass through LDS.  Tiles of 16 tokens: the threads first work out
 // delta and what is written for (token, channel) pairs, one each; then every wave walks the tile; then the threads add
@@ -291,6 +291,12 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane, int fir
     return p;
 }
 
+// Where a wave's states of its lane before the tile at t are kept: [B, tiles, N / 4, C, 4].
+template <int NS>
+__device__ __forceinline__ int64_t saved_at(const SelectArgs& P, const Place& p, int t, int wave, int N) {
+    return (((p.b * P.tiles + t / kTile) * (N / 4) + wave * NS / 4) * P.C + p.ch) * 4 + wave * NS % 4;
+}
+
 // Two workgroups on a compute unit do not share it evenly: the waves that came first go first, so one workgroup is done
 // early and the other one walks its rest alone, which leaves the vector units waiting (132 and 182 us at B = 8, T = 1024,
 // C = 4096, N = 16).  A wave's priority falls with every quarter of its tiles, so that who is behind goes first: the
@@ -449,7 +455,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
         yield_to_later(i, ntiles);
         if constexpr (kOut) {
             if (P.ckpt != nullptr && p.valid)
-                store_states(P.ckpt + (((p.b * P.tiles + tile_at(i) / kTile) * W + wave) * P.C + p.ch) * NS, h);
+                store_states(P.ckpt + saved_at<NS>(P, p, tile_at(i), wave, N), h);
             if (i > 0) add_up(i - 1);
         }
         fetch_bc(i + 1);
@@ -581,7 +587,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             rg[k] = load_at(go, row, chb);
             rz[k] = load_at(gate_in, row, chb);
         }
-        load_states(P.saved + (((p.b * P.tiles + tile / kTile) * W + wave) * P.C + p.ch) * NS, p.valid, first);
+        load_states(P.saved + saved_at<NS>(P, p, tile, wave, N), p.valid, first);
         b.fetch(bt, tile * GNB, where, left);
         c.fetch(ct, tile * GNB, where, left);
     };
@@ -866,10 +872,12 @@ hipError_t walk_t(const SelectArgs& a, int mode, hipStream_t stream) {
 template <typename T>
 hipError_t walk_n(const SelectArgs& a, int mode, hipStream_t stream) {
     switch (a.N) {
-        // Two states a wave: with two waves of four the card is half empty (B = 8, T = 1024, C = 4096, bf16: forward and
-        // gradients together 833 us, of two states 422).
+        // Two states a wave of N = 8, since with two waves of four the card is half empty (B = 8, T = 1024, C = 4096, bf16:
+        // forward and gradients together 833 us, of two states 422).  And of N = 16 where no compute unit has two
+        // workgroups, so that its eight waves keep each vector unit with two (4 rows of these: 125 + 303 us of four
+        // states, 110 + 256 of two; 6 rows 160 + 382 and 157 + 396, 8 rows 167 + 397 and 178 + 397).
         case 8: return walk_t<T, 2, 4>(a, mode, stream);
-        case 16: return walk_t<T, 4, 4>(a, mode, stream);
+        case 16: return a.B * a.ctiles * a.nseg <= 256 ? walk_t<T, 2, 8>(a, mode, stream) : walk_t<T, 4, 4>(a, mode, stream);
         default: return walk_t<T, 4, 8>(a, mode, stream);
     }
 }
@@ -889,13 +897,15 @@ hipError_t chain(const SelectArgs& a, bool reverse, hipStream_t stream) {
 // A time split walks everything twice (once for what the segments do to a state of zero, then from their start states), and
 // pays where the channel tiles alone leave most of the card idle or there are tokens without end.  The model, in us: a
 // tile of 16 tokens takes a workgroup on a compute unit of its own about `alone`, and the unit's workgroups together at
-// least `shared` each; the backward 2.6 times that; the second walk 0.8 of the first; its launches 8.  Split and whole, forward and
-// backward, in us:
-//     2 rows of 333 tokens, 1002 channels, N = 8, float32      22 + 33 and  37 +  81   7 segments
-//     1 row of 300 tokens, 768 channels, N = 8, bf16           17 + 24 and  31 +  70   10
-//     1 row of 2000 tokens, 4096 channels, N = 8, bf16         68 + 112 and 186 + 430  8
-//     3 rows of 929 tokens, 4008 channels, N = 8, bf16        101 + 159 and 99 + 213   none forward, 4 backward
-//     8 rows of 1024 tokens, 4096 channels, N = 8, bf16       156 + 301 and 142 + 281  none
+// least `shared` each; the backward 2.6 times that; the second walk 0.8 of the first; its launches 8.  Forward and backward
+// split, and whole, in us:
+//     2 rows of 333 tokens, 1002 channels, N = 8, float32   22 + 33 and 37 + 81          (7 segments)
+//     the same, N = 16                                      24 + 36 and 41 + 88          (7)
+//     1 row of 300 tokens, 768 channels, N = 16, bf16       19 + 27 and 35 + 78          (10)
+//     1 row of 2000 tokens, 4096 channels, N = 16, bf16     83 + 147 and 208 + 483       (8; N = 8: 68 + 112 and 186 + 430)
+//     2 rows of 1024 tokens, 4096 channels, N = 16, bf16    86 + 149 and 108 + 252       (4)
+//     3 rows of 929 tokens, 4008 channels, N = 16, bf16     not forward; 210 and 241     (4)
+//     1 row of 32768 tokens, 4096 channels, N = 16, bf16    1040 + 2030 and 3340 + 7780  (16)
 int64_t select_segments(int64_t B, int64_t T, int64_t ctiles, int64_t N, bool bwd, int64_t* per) {
     const int64_t tiles = (T + kTile - 1) / kTile, groups = B * ctiles;
     *per = tiles * kTile;
