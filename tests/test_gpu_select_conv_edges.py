@@ -269,6 +269,25 @@ def test_segments_chain_through_their_states(dtype):
         near(b0[3], gf[3])
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("N,C,B", [(16, 4096, 64), (8, 4100, 130), (32, 2052, 65)])
+def test_states_past_the_caches_are_the_same_bits(N, C, B, dtype):
+    """In place, 16 MB of states and more in one call, and row by row in calls of less; a row without tokens keeps its own."""
+    p = draw(B, 2, C, 1, N, dtype)
+    assert B * C * N >= 1 << 22 > C * N
+    lens = torch.full((B,), 2, dtype=torch.int32, device=DEV)
+    lens[3], lens[B - 1] = 0, 1
+    args, kw = inputs(p)
+    S = p["S"].clone()
+    out = O.select_forward(*args, lengths=lens, state_in=S, state_out=S, **kw)
+    for b in (0, 3, B // 2, B - 1):
+        row = [v[b:b + 1].contiguous() if v.dim() == 3 else v for v in args]
+        k1 = {k: v[b:b + 1].contiguous() if v.dim() == 3 else v for k, v in kw.items()}
+        o1, S1 = O.select_forward(*row, lengths=lens[b:b + 1].contiguous(), state_in=p["S"][b:b + 1].contiguous(), return_state=True, **k1)
+        assert torch.equal(o1[0], out[b]) and torch.equal(S1[0], S[b])
+    assert torch.equal(S[3], p["S"][3]) and not bool(out[3].any())
+
+
 def test_no_tokens_and_no_rows():
     p, q = draw(2, 0, 70, 1, 16, F32), draw_conv(2, 0, 70, 4, BF)
     args, kw = inputs(p)
