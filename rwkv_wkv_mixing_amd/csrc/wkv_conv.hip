@@ -182,6 +182,43 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
     }
 }
 
+// One token a row: everything it needs is asked for at once, where the walk waits for the carried inputs, then for the token
+// (bf16, K = 4, layers in turn: 256 rows of 4096 channels 9.3 -> 5.8 us, of 4095 29 -> 8.9, 2048 rows 53 -> 29.7, 4.6 TB/s).
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs P, int64_t ncb) {
+    typedef Vec<T, V> Ops;
+    typedef typename Ops::Raw Raw;
+    const int64_t blk = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t b = blk / ncb * kRuns + __builtin_amdgcn_readfirstlane(threadIdx.x / kCols), c = (blk % ncb * kCols + threadIdx.x % kCols) * V;
+    if (b >= P.B || c >= P.C) return;
+    const bool live = P.lengths == nullptr || P.lengths[b] > 0;
+    const T* s_in = static_cast<const T*>(P.s_in) + b * (K - 1) * P.C + c;
+    T* s_out = static_cast<T*>(P.s_out) + b * (K - 1) * P.C + c;
+    Raw raw[K];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) raw[j] = P.s_in != nullptr ? *reinterpret_cast<const Raw*>(s_in + j * P.C) : Raw{};
+    raw[K - 1] = *reinterpret_cast<const Raw*>(static_cast<const T*>(P.x) + b * P.C + c);
+    float w[K][V], o[V];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = P.weight[j * P.C + c + i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = P.bias != nullptr ? P.bias[c + i] : 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        float f[V];
+        Ops::widen(raw[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(w[j][i], f[i], o[i]);
+    }
+    act_of(P.act, o);
+    *reinterpret_cast<Raw*>(static_cast<T*>(P.out) + b * P.C + c) = live ? Ops::narrow(o) : Raw{};
+    if (P.s_out == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) *reinterpret_cast<Raw*>(s_out + j * P.C) = live ? raw[j + 1] : raw[j];
+}
+
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run, int64_t ncb) {
     typedef Vec<T, V> Ops;
@@ -389,6 +426,10 @@ dim3 grid_of(int64_t blocks) {
 template <typename T, int V, int K>
 hipError_t conv_launch(const ConvArgs& a, bool bwd, hipStream_t stream) {
     const int64_t ncb = (a.C + kCols * V - 1) / (kCols * V);
+    if (!bwd && a.T == 1) {
+        hipLaunchKernelGGL((conv_step_kernel<T, V, K>), grid_of((a.B + kRuns - 1) / kRuns * ncb), dim3(kThreads), 0, stream, a, ncb);
+        return hipGetLastError();
+    }
     if (!bwd) {
         // (8 x 1024 x 4096: runs of 8 and 16 bf16 28.9 and 31.1 us, float32 49.8 and 54.5, 4095 channels 61.2 and 50.0)
         const int run = run_of(a.B, a.T, ncb, V > 1 ? 8 : 16);

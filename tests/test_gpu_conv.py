@@ -116,3 +116,22 @@ def test_decode_in_place_is_the_whole_sequence(C, dtype):
     a, sa = O.conv_forward(long, p["weight"], p["bias"], state_in=state.clone(), return_state=True)
     b = O.conv_forward(long, p["weight"], p["bias"], state_in=state, state_out=state)
     assert torch.equal(a, b) and torch.equal(sa, state)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("K", [2, 3, 4])
+@pytest.mark.parametrize("B,C", [(1, 1), (6, 260), (9, 63), (130, 768)])
+def test_one_token_is_the_first_of_more(B, C, K, dtype):
+    """Rows with and without a token, from given carried inputs, from none, in place: the bits of a longer call's rows."""
+    p = {k: v.to(DEV) for k, v in draw(B, 3, C, K, dtype).items()}
+    lens = torch.tensor([(i + 1) % 3 % 2 for i in range(B)], dtype=torch.int32, device=DEV)
+    first = p["x"][:, :1].contiguous()
+    for state in (p["state_in"], None):
+        for bias in (p["bias"], None):
+            want, S = O.conv_forward(p["x"], p["weight"], bias, lengths=lens, state_in=state, return_state=True)
+            got, S1 = O.conv_forward(first, p["weight"], bias, lengths=lens, state_in=state, return_state=True)
+            assert torch.equal(got, want[:, :1]) and torch.equal(S1, S)
+    held = p["state_in"].clone()
+    got = O.conv_forward(first, p["weight"], p["bias"], lengths=lens, state_in=held, state_out=held)
+    want, S = O.conv_forward(p["x"], p["weight"], p["bias"], lengths=lens, state_in=p["state_in"], return_state=True)
+    assert torch.equal(got, want[:, :1]) and torch.equal(held, S)
