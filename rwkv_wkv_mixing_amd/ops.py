@@ -1153,29 +1153,38 @@ def short_conv(x, weight, bias=None, state_in=None, lengths=None, act="silu"):
     return ConvFunction.apply(x, weight, bias, state_in, lengths, act)
 
 
+def _fit(t, name, index, dtype, shape, device):
+    """_need for a tensor that most likely is as it should be: device objects cost more than the check's other parts, so the
+    device's number is asked for instead (a scan's decoding call of ten tensors 13.6 -> 12.8 us)."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape, device)
+
+
 def _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths):
     _need(x, "x", _FLOATS)
     if x.dim() != 3:
         raise ValueError("x must have three dimensions [B, T, C]")
-    dev, ty = x.device, x.dtype
+    dev, ty, index = x.device, x.dtype, x.get_device()
     B, T, C = shape = x.shape
-    _need(dt, "dt", ty, shape, dev)
+    _fit(dt, "dt", index, ty, shape, dev)
     _need(w, "w", torch.float32, None, dev)
-    if w.dim() != 2 or w.shape[0] != C or w.shape[1] not in (8, 16, 32):
+    N = w.shape[-1] if w.dim() else 0
+    if w.shape != (C, N) or N not in (8, 16, 32):
         raise ValueError(f"w has shape {tuple(w.shape)}, expected ({C}, N) with N 8, 16 or 32")
-    N = w.shape[1]
     _need(b, "b", ty, None, dev)
-    if b.dim() != 3 or b.shape[0] != B or b.shape[1] != T or b.shape[2] % N or not b.shape[2] or C % (b.shape[2] // N):
+    GN = b.shape[-1] if b.dim() else 0
+    if b.shape != (B, T, GN) or GN % N or not GN or C % (GN // N):
         raise ValueError(f"b has shape {tuple(b.shape)}, expected ({B}, {T}, G {N}) with G a divisor of {C}")
-    _need(c, "c", ty, b.shape, dev)
+    _fit(c, "c", index, ty, (B, T, GN), dev)
     if z is not None:
-        _need(z, "z", ty, shape, dev)
-    for t, n in ((d, "d"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _need(t, n, torch.float32, (C,), dev)
+        _fit(z, "z", index, ty, shape, dev)
+    if d is not None:
+        _fit(d, "d", index, torch.float32, (C,), dev)
+    if dt_bias is not None:
+        _fit(dt_bias, "dt_bias", index, torch.float32, (C,), dev)
     if lengths is not None:
-        _need(lengths, "lengths", torch.int32, (B,), dev)
-    return dev, B, T, C, b.shape[2] // N, N
+        _fit(lengths, "lengths", index, torch.int32, (B,), dev)
+    return dev, B, T, C, GN // N, N
 
 
 def select_ckpt_bytes(B: int, T: int, C: int, N: int) -> int:
