@@ -274,6 +274,22 @@ struct Place {
     bool valid;          // not a spare lane
 };
 
+// The batch row of the slot-th workgroups: of up to 64 ragged rows the longest first, so that the last workgroups to begin are
+// short ones.  Each workgroup ranks the rows for itself, a row a lane (4096 channels, N = 16, bf16, random lengths, in the
+// order given and so: 32 rows of up to 2048 tokens forward 740 -> 652 us, gradients 2300 -> 1900; 6 of up to 1501 189 ->
+// 179 and 469 -> 438; 3 of up to 200 tokens of 2048 channels 24.3 -> 24.7).
+__device__ __forceinline__ uint32_t row_of(const SelectArgs& P, uint32_t slot, int lane) {
+    const int B = static_cast<int>(P.B);
+    if (P.lengths == nullptr || B > 64) return slot;
+    const int len = lane < B ? P.lengths[lane] : 0;
+    int before = 0;
+    for (int k = 0; k < B; ++k) {
+        const int other = __builtin_amdgcn_readlane(len, k);
+        before += other > len || (other == len && k < lane) ? 1 : 0;
+    }
+    return static_cast<uint32_t>(__builtin_ctzll(__ballot(lane < B && before == static_cast<int>(slot))));
+}
+
 __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane, int first_seg = 0) {
     Place p;
     const uint32_t nct = static_cast<uint32_t>(P.ctiles);
@@ -281,7 +297,7 @@ __device__ __forceinline__ Place place_of(const SelectArgs& P, int lane, int fir
     const uint32_t blk = blockIdx.x, rest = __builtin_amdgcn_readfirstlane(blk / nct);
     p.ct = __builtin_amdgcn_readfirstlane(blk - rest * nct);
     const int seg = __builtin_amdgcn_readfirstlane(rest / static_cast<uint32_t>(P.B));
-    p.b = rest - static_cast<uint32_t>(seg) * static_cast<uint32_t>(P.B);
+    p.b = row_of(P, rest - static_cast<uint32_t>(seg) * static_cast<uint32_t>(P.B), lane);
     p.seg = first_seg + seg;
     const int per_group = __builtin_amdgcn_readfirstlane(P.ctiles / static_cast<int>(P.G));
     p.g = __builtin_amdgcn_readfirstlane(p.ct / per_group);

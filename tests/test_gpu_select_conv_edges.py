@@ -270,6 +270,29 @@ def test_segments_chain_through_their_states(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("B,T,C,N", [(2, 40, 66, 16), (63, 33, 5, 8), (64, 33, 70, 16), (65, 20, 66, 8), (3, 400, 64, 32)])
+def test_many_ragged_rows_are_each_their_own(B, T, C, N, dtype):
+    """Rows of all lengths, many alike, some empty, some given as negative or too long: every row as in a call by itself."""
+    p = draw(B, T, C, 1, N, dtype)
+    lens = (torch.arange(B, dtype=torch.int32) * 7 % (T + 4) - 2).to(DEV)
+    lens[0], lens[B - 1] = T, -5
+    args, kw = inputs(p)
+    split = dict(split=T > 64)
+    out, S1 = O.select_forward(*args, lengths=lens, state_in=p["S"], return_state=True, **split, **kw)
+    g = O.select_backward(*args, p["go"], lengths=lens, state_in=p["S"], grad_state_out=p["Gs"], need_state_grad=True, **split, **kw)
+    for b in sorted({0, 1, B // 3, B // 2, B - 2, B - 1}):
+        cut = lambda v: v[b:b + 1].contiguous()  # noqa: E731
+        row = [cut(v) if v.dim() == 3 else v for v in args]
+        k1 = {k: cut(v) if v.dim() == 3 else v for k, v in kw.items()}
+        one = dict(lengths=cut(lens), state_in=cut(p["S"]), split=False)
+        o1, R1 = O.select_forward(*row, return_state=True, **one, **k1)
+        g1 = O.select_backward(*row, cut(p["go"]), grad_state_out=cut(p["Gs"]), need_state_grad=True, **one, **k1)
+        for got, want in [(out[b], o1[0]), (S1[b], R1[0])] + [(g[n][b], g1[n][0]) for n in ("dx", "ddt", "dz", "db", "dc", "dstate_in")]:
+            tol = 2.0 ** -7 if got.dtype is BF else 1e-5  # (sums over states in groups of their own, a split: other roundings)
+            assert float((got.float() - want.float()).abs().max()) <= tol * float(want.float().abs().max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("N,C,B", [(16, 4096, 64), (8, 4100, 130), (32, 2052, 65)])
 def test_states_past_the_caches_are_the_same_bits(N, C, B, dtype):
     """In place, 16 MB of states and more in one call, and row by row in calls of less; a row without tokens keeps its own."""
