@@ -783,7 +783,8 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
  *           behind it are not read, leave the state as it is, and their rows of
  *           out are zeros.
  * x, dt     [B, T, C].  w  [C, N] float32 rates, >= 0; +inf keeps nothing (a step that
- *           is zero in float32 keeps everything, whatever the rate).
+ *           is zero in float32 keeps everything, whatever the rate).  Rates above 2e38 count
+ *           as infinite.
  * b, c      [B, T, G N].  d  [C] float32 or NULL (0).  z  [B, T, C] or NULL (out = y).
  * dt_bias   [C] float32 or NULL (0).
  * out       [B, T, C], fully overwritten; must not overlap an input.
@@ -823,6 +824,8 @@ size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int6
  *     dz_t = go_t y_t (the gate's derivative),   dw = -sum_t delta_t q_t,
  *     db_t = sum over the group's channels of delta_t x_t g_t,   dc_t = that of gy_t h_t,
  *     dd = sum gy_t x_t,   ddt_bias = sum ddt_t,   ds_in = a_1 g_1.
+ * Infinite rates are left out of sum_n w q_t, and where sigmoid(dt_t + dt_bias) is zero in
+ * float32 (a step of zero) the whole of it is.
  * Sums are float32 in a fixed order (bitwise reproducible).
  *
  * go        [B, T, C] in_dtype.  Rows behind a row's length are not read.

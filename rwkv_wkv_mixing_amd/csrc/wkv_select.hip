@@ -62,8 +62,14 @@ __device__ __forceinline__ float log1p_unit(float e) {
     return p * e;
 }
 
-// A decay rate: infinity is held finite, so that a step of zero keeps the state (not a number stays what it is).
-__device__ __forceinline__ float held(float w) { return w > 2e38f ? 2e38f : w; }
+// v_mul_legacy_f32, which the compiler has no builtin for (as inline assembly it would stand outside the scheduling).
+__device__ float mul_zero(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+
+// A decay e^{-delta w} from delta and w2 = -w log2 e.  The product's rule is that 0 times anything is 0, so a step of zero keeps
+// the state whatever the rate, and a rate of infinity (w2 -inf) forgets it in any other step, however small.
+__device__ __forceinline__ float decay(float delta, float w2) {
+    return exp2_fast(mul_zero(delta, w2));
+}
 
 // delta of some tokens from dt + dt_bias, and its derivative by dt.
 template <bool Wide, bool Grad, int E>
@@ -358,7 +364,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
     float w2[NS], h[NS];
     load_states(P.w + static_cast<int64_t>(p.ch) * N + wave * NS, true, w2);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) w2[i] = -held(w2[i]) * kLog2e, h[i] = 0.f;
+    for (int i = 0; i < NS; ++i) w2[i] = -w2[i] * kLog2e, h[i] = 0.f;
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     if constexpr (kOut) {
         if (P.nseg > 1) load_states(P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N + state, p.valid, h);
@@ -487,7 +493,7 @@ __global__ __launch_bounds__(64 * W) void select_walk_kernel(SelectArgs P) {
             const float2 dv = now[j][lane];
             each<NS>([&](auto ss) {
                 constexpr int s = decltype(ss)::value;
-                const float a = exp2_fast(dv.x * w2[s]);
+                const float a = decay(dv.x, w2[s]);
                 if constexpr (kAdj) h[s] = a * fmaf(b.template get<j, s>(), dv.y, h[s]);
                 else h[s] = fmaf(a, h[s], b.template get<j, s>() * dv.y);
             });
@@ -541,7 +547,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= n) return;
     const int64_t bc = i / P.N;
-    const float w2 = -held(P.w[bc % P.C * P.N + i % P.N]) * kLog2e;
+    const float w2 = -P.w[bc % P.C * P.N + i % P.N] * kLog2e;
     const float* first = reverse ? P.ds_out : P.s_in;
     float h = first != nullptr ? first[i] : 0.f;
     for (int64_t k = 0; k < P.nseg; ++k) {
@@ -549,7 +555,7 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
         float* at = P.local + s * n + i;
         const float own = k + 1 < P.nseg ? *at : 0.f, step = k + 1 < P.nseg ? P.steps[s * P.B * P.C + bc] : 0.f;
         *at = h;
-        h = fmaf(exp2_fast(step * w2), h, own);
+        h = fmaf(decay(step, w2), h, own);
     }
 }
 
@@ -557,7 +563,8 @@ __global__ __launch_bounds__(256) void select_chain_kernel(SelectArgs P, bool re
 // tokens are taken back to front,
 //     g += c_t gy_t,   dc_t = sum gy_t h_t,   db_t = sum g u_t  (over channels),   du_t = sum_n g b_t,
 //     g *= a_t,   q = g h_{t-1},   ddelta_t = du_t x_t - sum_n w q,   dw -= delta_t q
-// The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
+// An infinite rate is left out of the sum over w q (q is zero but in a step of zero, which is the end of the steps' range),
+// and where the softplus has no slope so is all of it: a large rate times q may be infinite there.  The tile's 16 states and decays stay in registers.  db and dc of a token are sums over the lanes: 8 numbers a token,
 // of which every exchange between lanes halves the registers, so 16 tokens end as two registers of one number a lane.
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
@@ -586,7 +593,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
     const int64_t state = (p.b * P.C + p.ch) * N + wave * NS;
     const float* from = P.nseg > 1 ? P.local + (static_cast<int64_t>(p.seg) * P.B * P.C) * N : P.ds_out;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) w1[i] = held(w1[i]), w2[i] = -w1[i] * kLog2e, dw[i] = g[i] = 0.f;
+    for (int i = 0; i < NS; ++i) w2[i] = -w1[i] * kLog2e, w1[i] = w2[i] == -__builtin_inff() ? 0.f : w1[i], dw[i] = g[i] = 0.f;
     if (from != nullptr) load_states(from + state, p.valid, g);
 
     const bool has_z = z != nullptr, spare = !__all(p.valid);
@@ -647,7 +654,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             const float4 v = put[j][lane];
             each<NS>([&](auto ss) {
                 constexpr int s = decltype(ss)::value;
-                a[j][s] = exp2_fast(v.x * w2[s]);
+                a[j][s] = decay(v.x, w2[s]);
                 h[j + 1][s] = fmaf(a[j][s], h[j][s], b.template get<j, s>() * v.y);
             });
             parts[0][wave][j][lane] = dot_row<c.template lane_of<j>()>(c.template reg<j>(), h[j + 1]);
@@ -727,7 +734,7 @@ __global__ __launch_bounds__(64 * W, 2) void select_grad_kernel(SelectArgs P) {
             float y = skip * v.w, du = 0.f, down = 0.f;
 #pragma unroll
             for (int q = 0; q < W; ++q) y += parts[0][q][j][lane], du += parts[1][q][j][lane], down += parts[2][q][j][lane];
-            float gd = fmaf(du, v.w, -down) * eslope[k];
+            float gd = fmaf(du, v.w, eslope[k] != 0.f ? -down : 0.f) * eslope[k];
             if (edge) gd = j < n && p.valid ? gd : 0.f;
             oz[k] = narrow<T>(egs[k] * y);
             ox[k] = narrow<T>(fmaf(du, v.x, skip * v.z));
@@ -841,7 +848,7 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
     float w2[NS];
     load_states(P.w + static_cast<int64_t>(ch) * N + 4 * q, true, w2);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) w2[s] = -held(w2[s]) * kLog2e;
+    for (int s = 0; s < NS; ++s) w2[s] = -w2[s] * kLog2e;
     const float bias = P.dt_bias != nullptr ? P.dt_bias[ch] : 0.f, skip = P.d != nullptr ? P.d[ch] : 0.f;
     const int tokens = static_cast<int>(P.T);
     for (int64_t b = blockIdx.y; b < P.B; b += gridDim.y) {
@@ -870,7 +877,7 @@ __global__ __launch_bounds__(256) void select_step_kernel(SelectArgs P) {
             const float u = d1[0] * vx;
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                h[s] = fmaf(exp2_fast(d1[0] * w2[s]), h[s], widen(bb[s]) * u);
+                h[s] = fmaf(decay(d1[0], w2[s]), h[s], widen(bb[s]) * u);
                 y = fmaf(widen(cc[s]), h[s], y);
             }
             y = sum_lanes(y, Lanes);
