@@ -744,9 +744,10 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
  * s_in      [B, K - 1, C] or NULL (zeros).  s_out  alike, or NULL; may be s_in.
  *           With T == 0 it receives s_in (or zeros).
  *
- * Backward, of sum <gout, out> + <ds_out, s_out>: dx (it must not overlap x or gout:
- * WKV_EINVAL), dweight, dbias (needed with bias), ds_in (or NULL; nor may it ds_out).  dweight and dbias
- * are sums over rows and tokens in a fixed order; all outputs are overwritten.
+ * Backward, of sum <gout, out> + <ds_out, s_out>: dx, dweight, dbias (needed with bias), ds_in
+ * (or NULL).  dx and ds_in must not overlap x, gout, s_in, ds_out or each other, but that ds_in
+ * may be s_in (WKV_EINVAL).  dweight and dbias are sums over rows and tokens in a fixed order;
+ * all outputs are overwritten.
  * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
  *           clobbered.  Not needed without tokens.
  * WKV_ESIZE from T = 2^31 - 64, B = 2^31 or C = 2^26.

@@ -1231,12 +1231,13 @@ wkv_status_t wkv_conv_forward(int64_t B, int64_t T, int64_t C, int64_t K, int in
     const size_t es = in_size(in_dtype);
     if (!all_aligned(es, x, s_in, out, s_out) || !all_aligned(4, weight, bias, lengths)) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
+    if (s_in != s_out && overlap(s_in, carried, s_out, carried)) return WKV_EINVAL;
     if (p.n == 0) return hip_status(wkv::launch_conv_copy(s_in, s_out, p.ns, in_dtype == WKV_BF16, stream));
     if (!x || !weight || !out) return WKV_EINVAL;
     // a token is read by the workgroups of the tokens behind it, so none of x may be overwritten
-    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
     if (overlap(x, bytes, out, bytes) || overlap(s_in, carried, out, bytes) || overlap(x, bytes, s_out, carried) ||
-        overlap(out, bytes, s_out, carried) || (s_in != s_out && overlap(s_in, carried, s_out, carried)))
+        overlap(out, bytes, s_out, carried))
         return WKV_EINVAL;
     wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
     a.out = out;
@@ -1256,6 +1257,9 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
     const size_t es = in_size(in_dtype);
     if (!all_aligned(es, x, s_in, gout, ds_out, dx, ds_in) || !all_aligned(4, weight, bias, dweight, dbias, lengths)) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    // a row's last tokens read ds_out when its first ones may have written ds_in, and tokens are read as in the forward
+    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
+    if (overlap(ds_out, carried, ds_in, carried)) return WKV_EINVAL;
     if (p.n == 0) {  // empty sums; the carried inputs' gradient passes back
         hipError_t e = wkv::launch_zero(dweight, K * C, stream);
         if (e == hipSuccess && bias) e = wkv::launch_zero(dbias, C, stream);
@@ -1263,10 +1267,12 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
         return hip_status(e);
     }
     if (!x || !weight || !gout || !dx) return WKV_EINVAL;
-    // a row's last tokens read ds_out when its first ones may have written ds_in, and tokens are read as in the forward
-    const int64_t bytes = p.n * static_cast<int64_t>(es), carried = p.ns * static_cast<int64_t>(es);
-    if (overlap(ds_out, carried, ds_in, carried) || overlap(x, bytes, dx, bytes) || overlap(gout, bytes, dx, bytes)) return WKV_EINVAL;
+    if (overlap(x, bytes, dx, bytes) || overlap(gout, bytes, dx, bytes)) return WKV_EINVAL;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < p.ws_bytes) return WKV_EWORKSPACE;
+    // (a row's carried inputs are read, and ds_in's of it written, by the same threads, the reads first: ds_in may be s_in)
+    if (overlap(s_in, carried, dx, bytes) || overlap(ds_out, carried, dx, bytes) || overlap(ds_in, carried, dx, bytes) ||
+        overlap(x, bytes, ds_in, carried) || overlap(gout, bytes, ds_in, carried) || (s_in != ds_in && overlap(s_in, carried, ds_in, carried)))
+        return WKV_EINVAL;
     wkv::ConvArgs a{B, T, C, K, in_dtype == WKV_BF16, false, act, lengths, x, weight, bias, s_in};
     a.gout = gout;
     a.ds_out = ds_out;
