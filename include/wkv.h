@@ -788,10 +788,11 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
  *           as infinite.
  * b, c      [B, T, G N].  d  [C] float32 or NULL (0).  z  [B, T, C] or NULL (out = y).
  * dt_bias   [C] float32 or NULL (0).
- * out       [B, T, C], fully overwritten; must not overlap an input.
+ * out       [B, T, C], fully overwritten; must not overlap an input or s_out (WKV_EINVAL).
  * s_in      [B, C, N] float32 state before token 1, or NULL (zero).
  * s_out     [B, C, N] float32 state after each row's last token, or NULL; may be
- *           s_in.  With T == 0 it receives s_in (or zeros).
+ *           s_in, and must not overlap part of it or another input (WKV_EINVAL).  With
+ *           T == 0 it receives s_in (or zeros).
  * ckpt      NULL, or wkv_select_ckpt_bytes() bytes for wkv_select_backward on the
  *           same inputs: the state before every 16 tokens (opaque).
  * workspace NULL (no time split), or wkv_select_forward_workspace_bytes() bytes,
@@ -835,6 +836,8 @@ size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int6
  *           dd with d, ddt_bias with dt_bias, and they are not written without.
  * ds_out, ds_in  [B, C, N] float32 or NULL; ds_in may be ds_out.  With T == 0 ds_in
  *           receives ds_out (or zeros).
+ * dx, ddt, dz, db, dc and ds_in must not overlap an input [B, T, ..], part of ds_out or each
+ * other (WKV_EINVAL).
  * ckpt      what wkv_select_forward wrote for these inputs, lengths and s_in, or
  *           NULL (recomputed, from s_in).
  * workspace wkv_select_backward_workspace_bytes(..., ws_flags) bytes, 256-byte

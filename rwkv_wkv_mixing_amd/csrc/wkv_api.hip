@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 
@@ -1062,6 +1063,17 @@ bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
     return a && b && p < q + static_cast<uintptr_t>(bbytes) && q < p + static_cast<uintptr_t>(abytes);
 }
 
+// A tensor's place; whether one shares bytes with any of some others.
+struct Bytes {
+    const void* p;
+    int64_t n;
+};
+bool overlaps(Bytes a, std::initializer_list<Bytes> others) {
+    for (const Bytes& b : others)
+        if (overlap(a.p, a.n, b.p, b.n)) return true;
+    return false;
+}
+
 // vectors of four elements: four floats of the weights and their gradients, which lie on the 16-byte grid
 template <class... P>
 bool conv_vec(int64_t C, int dt, const float* weight, const float* bias, P... p) {
@@ -1315,11 +1327,19 @@ wkv_status_t wkv_select_forward(int64_t B, int64_t T, int64_t C, int64_t G, int6
     if (!all_aligned(16, s_in, s_out)) return WKV_EALIGN;
     if (p.ns == 0) return WKV_OK;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-    if (T == 0) return hip_status(wkv::launch_wkv5_state_copy(s_in, s_out, p.ns, stream));
+    if (T == 0) {
+        if (s_in != s_out && overlap(s_in, p.ns * 4, s_out, p.ns * 4)) return WKV_EINVAL;
+        return hip_status(wkv::launch_wkv5_state_copy(s_in, s_out, p.ns, stream));
+    }
     if (!x || !dt || !w || !b || !c || !out) return WKV_EINVAL;
     if (!all_aligned(16, w, b, c, ckpt) || !all_aligned(4, d, dt_bias, lengths) || !all_aligned(in_size(in_dtype), x, dt, z, out))
         return WKV_EALIGN;
     if (workspace && (!aligned(workspace, 256) || workspace_bytes < p.split)) return WKV_EWORKSPACE;
+    const int64_t es = static_cast<int64_t>(in_size(in_dtype)), tokens = B * T * C * es, shared = B * T * G * N * es, states = p.ns * 4;
+    if (overlaps({out, tokens}, {{x, tokens}, {dt, tokens}, {z, tokens}, {b, shared}, {c, shared}, {s_in, states}, {s_out, states}}) ||
+        overlaps({s_out, states}, {{x, tokens}, {dt, tokens}, {z, tokens}, {b, shared}, {c, shared}}) ||
+        (s_in != s_out && overlap(s_in, states, s_out, states)))
+        return WKV_EINVAL;
     wkv::SelectArgs a{B, T, C, G, N, in_dtype == WKV_BF16, (flags & WKV_SELECT_SOFTPLUS) != 0, lengths, x, dt, w, b, c, d, z, dt_bias, s_in};
     a.tiles = p.tiles;
     a.ctiles = static_cast<int>(p.ctiles);
@@ -1345,6 +1365,8 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
     if (!dw || (d && !dd) || (dt_bias && !ddt_bias)) return WKV_EINVAL;
     if (!all_aligned(16, s_in, ds_out, ds_in, dw) || !all_aligned(4, d, dt_bias, dd, ddt_bias, lengths)) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    const int64_t states = p.ns * 4;
+    if (ds_in != ds_out && overlap(ds_in, states, ds_out, states)) return WKV_EINVAL;
     if (p.ns == 0 || T == 0) {  // empty sums; the state's gradient passes back
         hipError_t e = wkv::launch_zero(dw, C * N, stream);
         if (e == hipSuccess && d) e = wkv::launch_zero(dd, C, stream);
@@ -1356,6 +1378,14 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
     if (!all_aligned(16, w, b, c, ckpt, db, dc) || !all_aligned(in_size(in_dtype), x, dt, z, go, dx, ddt, dz)) return WKV_EALIGN;
     const size_t saved = ckpt ? 0 : (p.ckpt + 255) / 256 * 256, unsplit = p.part + p.dwp + p.vecp + saved;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < unsplit) return WKV_EWORKSPACE;
+    const int64_t es = static_cast<int64_t>(in_size(in_dtype)), tokens = B * T * C * es, shared = B * T * G * N * es;
+    const Bytes outs[] = {{dx, tokens}, {ddt, tokens}, {z ? dz : nullptr, tokens}, {db, shared}, {dc, shared}, {ds_in, states}};
+    for (size_t i = 0; i < sizeof(outs) / sizeof(outs[0]); ++i) {
+        if (overlaps(outs[i], {{x, tokens}, {dt, tokens}, {z, tokens}, {go, tokens}, {b, shared}, {c, shared}})) return WKV_EINVAL;
+        if (outs[i].p != ds_in && overlap(outs[i].p, outs[i].n, ds_out, states)) return WKV_EINVAL;
+        for (size_t k = 0; k < i; ++k)
+            if (overlap(outs[i].p, outs[i].n, outs[k].p, outs[k].n)) return WKV_EINVAL;
+    }
     char* ws = static_cast<char*>(workspace);
     wkv::SelectArgs a{B, T, C, G, N, in_dtype == WKV_BF16, (flags & WKV_SELECT_SOFTPLUS) != 0, lengths, x, dt, w, b, c, d, z, dt_bias, s_in};
     a.tiles = p.tiles;

@@ -52,3 +52,52 @@ def test_conv_carried_inputs_without_tokens(lib):
     for off in (2, CARRIED - 2, -CARRIED + 2):
         assert conv_forward(lib, T=0, s_in=X, s_out=X + off) == L.WKV_EINVAL, off
         assert conv_backward(lib, T=0, ds_out=X, ds_in=X + off) == L.WKV_EINVAL, off
+
+
+SB, ST, SC, SG, SN = 2, 20, 128, 2, 16
+TOKENS, SHARED, STATES = SB * ST * SC * 2, SB * ST * SG * SN * 2, SB * SC * SN * 4
+IN = ("x", "dt", "w", "b", "c", "d", "z", "dt_bias")
+SIZE = {**dict.fromkeys(("x", "dt", "z", "go", "out", "dx", "ddt", "dz"), TOKENS), **dict.fromkeys(("b", "c", "db", "dc"), SHARED),
+        **dict.fromkeys(("s_in", "s_out", "ds_out", "ds_in"), STATES)}
+
+
+def select_forward(lib, T=ST, **at):
+    p = {**places(IN + ("out", "s_in", "s_out")), **at}
+    return lib.wkv_select_forward(SB, T, SC, SG, SN, L.WKV_BF16, 1, None, *(p[n] for n in p), None, None, 0, None)
+
+
+def select_backward(lib, T=ST, **at):
+    p = {**places(IN + ("go", "s_in", "ds_out", "dx", "ddt", "dw", "db", "dc", "dd", "dz", "dt_bias_grad", "ds_in", "ckpt", "ws")), **at}
+    return lib.wkv_select_backward(SB, T, SC, SG, SN, L.WKV_BF16, 1, None, *(p[n] for n in p), 1 << 30, None)
+
+
+def offsets(out, of, same):
+    return (16, SIZE[of] - 16, -SIZE[out] + 16) + ((0,) if same else ())
+
+
+@pytest.mark.parametrize("T", [1, ST])
+@pytest.mark.parametrize("out,of", [(o, i) for o in ("out", "s_out") for i in ("x", "dt", "b", "c", "z", "s_in")] + [("s_out", "out")])
+def test_select_over_what_is_read(lib, out, of, T):
+    base = places(IN + ("out", "s_in", "s_out"))[of]
+    if T == 1:  # (a twentieth of the tokens' bytes)
+        offs = (0,) if (out, of) != ("s_out", "s_in") else (16,)
+    else:
+        offs = offsets(out, of, (out, of) != ("s_out", "s_in"))
+    for off in offs:
+        assert select_forward(lib, T=T, **{out: base + off}) == L.WKV_EINVAL, off
+
+
+@pytest.mark.parametrize("out", ["dx", "ddt", "dz", "db", "dc", "ds_in"])
+@pytest.mark.parametrize("of", ["x", "dt", "b", "c", "z", "go", "ds_out", "dx", "ddt", "dz", "db", "dc"])
+def test_select_gradients_over_what_is_read(lib, out, of):
+    if out == of:
+        return
+    base = places(IN + ("go", "s_in", "ds_out", "dx", "ddt", "dw", "db", "dc", "dd", "dz", "dt_bias_grad", "ds_in", "ckpt", "ws"))[of]
+    for off in offsets(out, of, (out, of) != ("ds_in", "ds_out")):
+        assert select_backward(lib, **{out: base + off}) == L.WKV_EINVAL, off
+
+
+def test_select_states_without_tokens(lib):
+    for off in (16, STATES - 16, -STATES + 16):
+        assert select_forward(lib, T=0, s_in=X, s_out=X + off) == L.WKV_EINVAL, off
+        assert select_backward(lib, T=0, ds_out=X, ds_in=X + off) == L.WKV_EINVAL, off
