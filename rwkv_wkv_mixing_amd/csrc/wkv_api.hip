@@ -1361,7 +1361,13 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
     const SelectPlan p = select_plan(B, T, C, G, N, in_dtype, false, true);
     if (p.st != WKV_OK) return p.st;
     if ((flags & ~WKV_SELECT_SOFTPLUS) != 0) return WKV_EINVAL;
-    if (C == 0) return WKV_OK;
+    if (C == 0) {  // sums over no channels (rows of N numbers are whole floats in bf16 too)
+        if (!all_aligned(16, db, dc)) return WKV_EALIGN;
+        const int64_t n = B * T * G * N * static_cast<int64_t>(in_size(in_dtype)) / 4;
+        hipError_t e = wkv::launch_zero(static_cast<float*>(db), n, static_cast<hipStream_t>(hip_stream));
+        if (e == hipSuccess) e = wkv::launch_zero(static_cast<float*>(dc), n, static_cast<hipStream_t>(hip_stream));
+        return hip_status(e);
+    }
     if (!dw || (d && !dd) || (dt_bias && !ddt_bias)) return WKV_EINVAL;
     if (!all_aligned(16, s_in, ds_out, ds_in, dw) || !all_aligned(4, d, dt_bias, dd, ddt_bias, lengths)) return WKV_EALIGN;
     hipStream_t stream = static_cast<hipStream_t>(hip_stream);
