@@ -860,8 +860,9 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
  * Defines, over `count` tensors of any sizes:
  *     norm = sqrt(sum of all squares),   out = grad * min(1, max_norm / (norm + eps))
  * Squares are added up in float64 in a fixed order, so nothing over- or underflows
- * that float32 holds; each element is rounded once.  With a norm that is
- * infinite or not a number the factor is 0 or not a number, and so are the outputs.
+ * that float32 holds.  The factor, from the norm in float64, is rounded to 24 bits, and
+ * each product with it once more.  With a gradient that is infinite or not a number the factor
+ * is 0 or not a number, and so are the outputs (0 times an infinite one is not a number).
  *
  * grads, outs, sizes, dtypes  HOST arrays of `count` device addresses, element
  *           counts (>= 0) and dtypes (WKV_F32 or WKV_BF16, of a tensor's gradient
@@ -870,8 +871,8 @@ wkv_status_t wkv_select_backward(int64_t B, int64_t T, int64_t C, int64_t G, int
  *           outputs may not overlap each other, norm or another gradient (WKV_EINVAL),
  *           so in place no gradient may be listed twice.
  * max_norm  0 .. 1e30, eps 0 .. 1e30 (WKV_EINVAL otherwise).  0 / 0 counts as 1.
- * norm      [1] float32 on the device: the norm before the clipping; wkv_clip_gradients
- *           takes NULL too.
+ * norm      [1] float32 on the device: the norm before the clipping (infinite when above
+ *           float32's range; the factor is not 0 for that); wkv_clip_gradients takes NULL too.
  * workspace wkv_clip_workspace_bytes(count) bytes, 256-byte aligned; clobbered.  Not
  *           needed without elements.
  */

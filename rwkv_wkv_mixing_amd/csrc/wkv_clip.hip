@@ -137,8 +137,21 @@ __device__ __forceinline__ double sum_chunk(const T* p, int64_t first, int64_t n
     return sum;
 }
 
+// A factor as two numbers to multiply by in turn, since one below float32's normal numbers (gradients above 1e38 to a norm
+// below 1) has lost digits where products with it are ordinary numbers.  The second one is 1, or 2^-126 and the first one then
+// up to 1, so nothing overflows on the way, and what the first product loses ends as zero.
+struct Factor {
+    float by;
+    bool tiny;  // the same for all lanes, in a scalar register: a branch that is free otherwise (a second product always: 735 -> 743 us)
+    __device__ __forceinline__ void finish(float (&f)[8]) const {
+        if (!tiny) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= 0x1p-126f;
+    }
+};
+
 template <typename T, bool Vec, bool PastCache>
-__device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, int64_t n, float by) {
+__device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, int64_t n, Factor by) {
     float f[8];
     if (Vec && first + kClipChunk <= n) {
         const int64_t at = first + threadIdx.x * 8;
@@ -150,7 +163,8 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, in
             for (int q = 0; q < kBatch; ++q) {
                 raw[q].widen(f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= by;
+                for (int i = 0; i < 8; ++i) f[i] *= by.by;
+                by.finish(f);
                 store8<T, true, PastCache>(to, at + (k + q) * kStep, n, f);
             }
         }
@@ -160,7 +174,8 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* to, int64_t first, in
     for (int64_t e = first + threadIdx.x * 8; e < end; e += kStep) {
         load8<T, Vec>(p, e, n, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= by;
+        for (int i = 0; i < 8; ++i) f[i] *= by.by;
+        by.finish(f);
         store8<T, Vec, PastCache>(to, e, n, f);
     }
 }
@@ -219,13 +234,15 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipTable t, const
                                                               float eps, float* norm) {
     const double all = sqrt(sum_parts(part, nparts)), with = all + static_cast<double>(eps);
     // 1 up to max_norm; a norm that is not a number is handed on to every gradient
-    const float by = with <= static_cast<double>(max_norm) ? 1.f : static_cast<float>(static_cast<double>(max_norm) / with);
+    const double factor = with <= static_cast<double>(max_norm) ? 1.0 : static_cast<double>(max_norm) / with;
+    const bool tiny = __builtin_amdgcn_readfirstlane(factor < 0x1p-126 ? 1 : 0) != 0;
+    const Factor by{static_cast<float>(tiny ? factor * 0x1p126 : factor), tiny};
     if (blockIdx.x == 0 && threadIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(all);
     // from the last chunk to the first, as the launches go: what the sums read last is still in the last level cache
     for (int64_t chunk = t.chunks - 1 - blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
         const int k = tensor_of(t, chunk);
         const int64_t first = (chunk - t.chunk0[k]) * kClipChunk, n = t.n[k];
-        if (by == 1.f && t.in[k] == t.out[k]) continue;
+        if (by.by == 1.f && !by.tiny && t.in[k] == t.out[k]) continue;
         const bool vec = on_grid(t.in[k]) && on_grid(t.out[k]);
         if (t.bf16[k] != 0) {
             const uint16_t* p = static_cast<const uint16_t*>(t.in[k]);

@@ -1348,7 +1348,7 @@ def grad_norm(grads, *, norm=None, workspace=None, bind=False):
 def clip_gradients(grads, max_norm, *, eps=1e-6, out=None, norm=None, workspace=None, bind=False):
     """Scales the gradients by min(1, max_norm / (norm + eps)), norm that of all of them together (see grad_norm), in place
     or into out (a tensor for each, of its shape and dtype), and returns the norm before: a float32 tensor of no
-    dimensions.  A norm that is infinite or not a number makes the gradients zeros or not numbers.  No gradient
+    dimensions.  A gradient that is infinite or not a number makes the others zeros or not numbers.  No gradient
     may be listed twice in place."""
     dev, grads, out, n, ins, outs, sizes, types = _clip_tables(grads, out)
     norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
