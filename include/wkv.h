@@ -828,7 +828,8 @@ size_t wkv_select_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int6
  *     dd = sum gy_t x_t,   ddt_bias = sum ddt_t,   ds_in = a_1 g_1.
  * Infinite rates are left out of sum_n w q_t, and where sigmoid(dt_t + dt_bias) is zero in
  * float32 (a step of zero) the whole of it is.
- * Sums are float32 in a fixed order (bitwise reproducible).
+ * Sums are float32, of dw, dd and ddt_bias float64 over rows and runs of 128 tokens, in a
+ * fixed order (bitwise reproducible).
  *
  * go        [B, T, C] in_dtype.  Rows behind a row's length are not read.
  * dx, ddt, dz [B, T, C], db, dc [B, T, G N] in_dtype, zeros behind a row's length; dw

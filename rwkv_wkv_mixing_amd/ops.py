@@ -1247,7 +1247,8 @@ def select_backward(x, dt, w, b, c, go, *, d=None, z=None, dt_bias=None, softplu
     """Gradients of sum <go, out> + <grad_state_out, h_T> for (out, h_T) = select_forward(x, dt, w, b, c, ...,
     return_state=True): a dict of dx, ddt, dw, db, dc, dd, dz, ddt_bias, dstate_in, each in its input's dtype, None
     for one that is None (dstate_in without need_state_grad).  go [B, T, C] in x's dtype.  ckpt: None or what the
-    forward wrote.  split as in select_forward.  Sums are float32 in a fixed order."""
+    forward wrote.  split as in select_forward.  Sums are float32, those
+    over rows and long runs of tokens float64, in a fixed order."""
     dev, B, T, C, G, N = _select_inputs(x, dt, w, b, c, d, z, dt_bias, lengths)
     _need(go, "go", x.dtype, (B, T, C), dev)
     if state_in is not None:
