@@ -73,30 +73,30 @@ struct Vec<uint16_t, 1> {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * 1.44269504f)); }
-// act(v), and g act'(v): the activation is looked up once for all of them.
-template <int V>
+// act(v), and g act'(v): the activation is looked up once for all of them.  Wide with float32 tensors; with bf16 ones results
+// are rounded to 2^-9, or are sums of gradients that were.
+template <bool Wide, int V>
 __device__ __forceinline__ void act_of(int act, float (&v)[V]) {
     if (act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid<Wide>(v[i]);
     } else if (act == kActSigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = sigmoid(v[i]);
+        for (int i = 0; i < V; ++i) v[i] = sigmoid<Wide>(v[i]);
     }
 }
-template <int V>
+template <bool Wide, int V>
 __device__ __forceinline__ void act_grad(int act, const float (&v)[V], float (&g)[V]) {
     if (act == kActSilu) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float p = sigmoid(v[i]);
+            const float p = sigmoid<Wide>(v[i]);
             g[i] *= p * fmaf(v[i], 1.f - p, 1.f);
         }
     } else if (act == kActSigmoid) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float p = sigmoid(v[i]);
+            const float p = sigmoid<Wide>(v[i]);
             g[i] *= p * (1.f - p);
         }
     }
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs P, int run,
 #pragma unroll
                     for (int j = 0; j < K; ++j) o[i] = fmaf(w[j][i], win[(k + j) % K][i], o[i]);
                 }
-                act_of(P.act, o);
+                act_of<sizeof(T) == 4>(P.act, o);
                 *reinterpret_cast<Raw*>(out + static_cast<int64_t>(t + k) * P.C) = Ops::narrow(o);
             }
         }
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(ConvArgs P, int64_t
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = fmaf(w[j][i], f[i], o[i]);
     }
-    act_of(P.act, o);
+    act_of<sizeof(T) == 4>(P.act, o);
     *reinterpret_cast<Raw*>(static_cast<T*>(P.out) + b * P.C + c) = live ? Ops::narrow(o) : Raw{};
     if (P.s_out == nullptr) return;
 #pragma unroll
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
 #pragma unroll
                 for (int j = 0; j < K; ++j) pre[i] = fmaf(w[j][i], win[(a0 + j) % K][i], pre[i]);
             }
-            act_grad(P.act, pre, gt);
+            act_grad<sizeof(T) == 4>(P.act, pre, gt);
             if (own) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
