@@ -20,7 +20,6 @@ namespace wkv {
 namespace {
 constexpr int kThreads = 256, kCols = 64, kRuns = kThreads / kCols;  // a workgroup: 64 vectors of channels, 4 runs
 
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 // V elements as they lie in memory, widened and narrowed.
@@ -426,20 +425,23 @@ dim3 grid_of(int64_t blocks) {
 }
 
 template <typename T, int V, int K>
-hipError_t conv_launch(const ConvArgs& a, bool bwd, hipStream_t stream) {
+hipError_t fwd_launch(const ConvArgs& a, hipStream_t stream) {
     const int64_t ncb = (a.C + kCols * V - 1) / (kCols * V);
-    if (!bwd && a.T == 1) {
+    if (a.T == 1) {
         hipLaunchKernelGGL((conv_step_kernel<T, V, K>), grid_of((a.B + kRuns - 1) / kRuns * ncb), dim3(kThreads), 0, stream, a, ncb);
         return hipGetLastError();
     }
-    if (!bwd) {
-        // (8 x 1024 x 4096: runs of 8 and 16 bf16 28.9 and 31.1 us, float32 49.8 and 54.5, 4095 channels 61.2 and 50.0)
-        const int run = run_of(a.B, a.T, ncb, V > 1 ? 8 : 16);
-        const int64_t ntb = (a.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
-        hipLaunchKernelGGL((conv_fwd_kernel<T, V, K>), grid_of(a.B * ntb * ncb), dim3(kThreads), 0, stream, a, run, ncb);
-        return hipGetLastError();
-    }
-    // (there too: runs of 16, 32 and 64 bf16 63.0, 60.8 and 61 us, 4095 channels 88, 83 and 94; float32 93, 104 and 106)
+    // (8 x 1024 x 4096: runs of 8 and 16 bf16 28.9 and 31.1 us, float32 49.8 and 54.5, 4095 channels 61.2 and 50.0)
+    const int run = run_of(a.B, a.T, ncb, V > 1 ? 8 : 16);
+    const int64_t ntb = (a.T + kRuns * static_cast<int64_t>(run) - 1) / (kRuns * static_cast<int64_t>(run));
+    hipLaunchKernelGGL((conv_fwd_kernel<T, V, K>), grid_of(a.B * ntb * ncb), dim3(kThreads), 0, stream, a, run, ncb);
+    return hipGetLastError();
+}
+
+template <typename T, int V, int K>
+hipError_t bwd_launch(const ConvArgs& a, hipStream_t stream) {
+    const int64_t ncb = (a.C + kCols * V - 1) / (kCols * V);
+    // (8 x 1024 x 4096: runs of 16, 32 and 64 bf16 63.0, 60.8 and 61 us, 4095 channels 88, 83 and 94; float32 93, 104 and 106)
     const int run = run_of(a.B, a.T, ncb, V > 1 && sizeof(T) == 4 ? 16 : 32);
     hipLaunchKernelGGL((conv_bwd_kernel<T, V, K>), grid_of(a.slots * ncb), dim3(kThreads), 0, stream, a, run, ncb);
     const hipError_t e = hipGetLastError();
@@ -450,19 +452,21 @@ hipError_t conv_launch(const ConvArgs& a, bool bwd, hipStream_t stream) {
 }
 
 template <typename T, int V>
-hipError_t conv_k(const ConvArgs& a, bool bwd, hipStream_t stream) {
+hipError_t fwd_k(const ConvArgs& a, hipStream_t stream) {
     switch (a.K) {
-        case 2: return conv_launch<T, V, 2>(a, bwd, stream);
-        case 3: return conv_launch<T, V, 3>(a, bwd, stream);
-        default: return conv_launch<T, V, 4>(a, bwd, stream);
+        case 2: return fwd_launch<T, V, 2>(a, stream);
+        case 3: return fwd_launch<T, V, 3>(a, stream);
+        default: return fwd_launch<T, V, 4>(a, stream);
     }
 }
 
-hipError_t conv_t(const ConvArgs& a, bool bwd, hipStream_t stream) {
-    // four channels a thread forward, two backward, where four leave room for fewer waves (bf16 52 us, 64 of four)
-    if (!a.vec) return a.bf16 ? conv_k<uint16_t, 1>(a, bwd, stream) : conv_k<float, 1>(a, bwd, stream);
-    if (bwd) return a.bf16 ? conv_k<uint16_t, 2>(a, bwd, stream) : conv_k<float, 2>(a, bwd, stream);
-    return a.bf16 ? conv_k<uint16_t, 4>(a, bwd, stream) : conv_k<float, 4>(a, bwd, stream);
+template <typename T, int V>
+hipError_t bwd_k(const ConvArgs& a, hipStream_t stream) {
+    switch (a.K) {
+        case 2: return bwd_launch<T, V, 2>(a, stream);
+        case 3: return bwd_launch<T, V, 3>(a, stream);
+        default: return bwd_launch<T, V, 4>(a, stream);
+    }
 }
 
 }  // namespace
@@ -484,7 +488,14 @@ hipError_t launch_conv_copy(const void* from, void* to, int64_t n, bool bf16, hi
     return hipGetLastError();
 }
 
-hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) { return conv_t(a, false, stream); }
-hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) { return conv_t(a, true, stream); }
+// Four channels a thread forward, two backward, where four leave room for fewer waves (bf16 52 us, 64 of four).
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) {
+    if (a.vec) return a.bf16 ? fwd_k<uint16_t, 4>(a, stream) : fwd_k<float, 4>(a, stream);
+    return a.bf16 ? fwd_k<uint16_t, 1>(a, stream) : fwd_k<float, 1>(a, stream);
+}
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) {
+    if (a.vec) return a.bf16 ? bwd_k<uint16_t, 2>(a, stream) : bwd_k<float, 2>(a, stream);
+    return a.bf16 ? bwd_k<uint16_t, 1>(a, stream) : bwd_k<float, 1>(a, stream);
+}
 
 }  // namespace wkv
