@@ -746,8 +746,8 @@ wkv_status_t wkv_token_shift_backward(int64_t B, int64_t T, int64_t C, int64_t M
  *
  * Backward, of sum <gout, out> + <ds_out, s_out>: dx, dweight, dbias (needed with bias), ds_in
  * (or NULL).  dx and ds_in must not overlap x, gout, s_in, ds_out or each other, but that ds_in
- * may be s_in (WKV_EINVAL).  dweight and dbias are sums over rows and tokens in a fixed order;
- * all outputs are overwritten.
+ * may be s_in (WKV_EINVAL).  dweight and dbias are sums over rows and tokens in a fixed order,
+ * float32 over 512 tokens and float64 from there; all outputs are overwritten.
  * workspace wkv_conv_backward_workspace_bytes() bytes, 256-byte aligned;
  *           clobbered.  Not needed without tokens.
  * WKV_ESIZE from T = 2^31 - 64, B = 2^31 or C = 2^26.

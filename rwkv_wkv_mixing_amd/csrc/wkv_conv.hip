@@ -8,7 +8,7 @@
 // Backward, with g_t = gout_t act'(pre_t) of the row's tokens (zero elsewhere):
 //     dX[e] = sum_j weight[j] g_{e - j} (+ the carried-out inputs' gradient),   dweight[j] = sum g_t X[t + j],   dbias = sum g
 // A thread walks its run and K - 1 tokens more, computing pre again from x.  The weights' sums are kept a thread, added
-// over a workgroup's runs in LDS and over workgroups by a second kernel, each in a fixed order.  Some 40 vector
+// over a workgroup's runs in LDS and over workgroups by a second kernel (in float64), each in a fixed order.  Some 40 vector
 // instructions an element next to 6 bytes: at the same size 52 us, 3.9 TB/s, with the vector units busy two thirds of them.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -380,15 +380,15 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs P, int run,
     }
 }
 
-// dweight and dbias from the slots' sums, in order: a lane takes an output, each of the workgroup's 16 waves a sixteenth
+// dweight and dbias from the slots' sums, in order and in float64: a lane takes an output, each of the workgroup's 16 waves a sixteenth
 // of the slots.
 constexpr int kParts = 16;
 __global__ __launch_bounds__(64 * kParts) void conv_reduce_kernel(ConvArgs P) {
-    __shared__ float sums[kParts][64];
+    __shared__ double sums[kParts][64];
     const int64_t n = (P.K + 1) * P.C, i = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
     const int q = threadIdx.x >> 6;
     const int64_t each = (P.slots + kParts - 1) / kParts, first = q * each, last = first + each < P.slots ? first + each : P.slots;
-    float sum = 0.f;
+    double sum = 0.0;
     if (i < n) {
 #pragma unroll 4
         for (int64_t s = first; s < last; ++s) sum += P.part[s * n + i];
@@ -396,11 +396,12 @@ __global__ __launch_bounds__(64 * kParts) void conv_reduce_kernel(ConvArgs P) {
     sums[q][threadIdx.x & 63] = sum;
     __syncthreads();
     if (q != 0 || i >= n) return;
-    sum = 0.f;
+    sum = 0.0;
 #pragma unroll
     for (int k = 0; k < kParts; ++k) sum += sums[k][threadIdx.x];
-    if (i < P.K * P.C) P.dweight[i] = sum;
-    else if (P.dbias != nullptr) P.dbias[i - P.K * P.C] = sum;
+    const float all = static_cast<float>(sum);
+    if (i < P.K * P.C) P.dweight[i] = all;
+    else if (P.dbias != nullptr) P.dbias[i - P.K * P.C] = all;
 }
 
 // Carried inputs of a call without tokens: they pass on (or zeros do).
@@ -472,11 +473,14 @@ hipError_t bwd_k(const ConvArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Rows of partial sums of the backward: as many workgroups as fill the card (4096 of one channel a thread: 4095 channels
-// 83 us; 2048: 92) and no more than there are tiles of the shortest runs.
+// 83 us; 2048: 92) and no more than there are tiles of the shortest runs.  But one for every 512 tokens, so that a thread adds up
+// 128 in float32: one sum over thousands of terms that are alike loses up to 2^-25 of itself with each.
 int64_t conv_slots(int64_t B, int64_t T, int64_t C) {
     const int64_t ncb = (C + kCols - 1) / kCols, tiles = B * ((T + kRuns * 4 - 1) / (kRuns * 4));
+    const int64_t longest = B * ((T + kRuns * 32 - 1) / (kRuns * 32)), fewest = (longest + 3) / 4;
     int64_t most = 4096 / (ncb > 0 ? ncb : 1);
     most = most < 16 ? 16 : most;
+    most = most < fewest ? fewest : most;
     return tiles < most ? tiles : most;
 }
 
