@@ -16,7 +16,7 @@ The compute path is the HIP library librwkv_wkv.so (C ABI in include/wkv.h);
     o = ops.head_norm_gated(o, weight, None, gate, heads=H)
     x, carried = ops.short_conv(x, filter)
     y, state = ops.selective_scan(x, dt, w, b, c, d, z)
-    norm = ops.clip_gradients([p.grad for p in parameters], 1.0)
+    norm = ops.clip_gradients([p.grad for p in parameters if p.grad is not None], 1.0)
 
 ``workloads`` draws the seeded synthetic inputs used by tests and the bench.
 """

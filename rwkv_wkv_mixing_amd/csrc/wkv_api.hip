@@ -1143,7 +1143,7 @@ struct Span {
     bool out;
 };
 
-// The tensors' sizes and dtypes, and the tables of the launches (with == NULL: the gradients in place).
+// The tensors' sizes, dtypes and addresses, and the number of their elements.
 wkv_status_t clip_check(int64_t count, const void* const* grads, const int64_t* sizes, const int* dtypes, int64_t* total) {
     if (count < 0) return WKV_EINVAL;
     if (count >= (int64_t{1} << 24)) return WKV_ESIZE;

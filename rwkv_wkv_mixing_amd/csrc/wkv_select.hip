@@ -62,7 +62,9 @@ __device__ __forceinline__ float decay(float delta, float w2) {
     return exp2_fast(mul_zero(delta, w2));
 }
 
-// delta of some tokens from dt + dt_bias, and its derivative by dt.
+// delta of some tokens from dt + dt_bias, and its derivative by dt.  Wide with float32 tensors; a bf16 dt is itself rounded by
+// 2^-9, next to which the |dt| 2^-24 of a step that is left in is nothing (put back, the bf16 forward of 8 x 1024 x 4096 takes
+// 165 us for 162, the gradients 399 for 395).
 template <bool Wide, bool Grad, int E>
 __device__ __forceinline__ void steps_of(float (&raw)[E], bool softplus, float (&grad)[E]) {
     if (!softplus) {
@@ -142,8 +144,10 @@ __device__ __forceinline__ void add_row(float (&g)[2], float c, float v) {
         : "+v"(g[0]), "+v"(g[1]) : "v"(c), "v"(v), "n"(K), "n"(K + 1));
 }
 
-// A token's numbers (b and c of the wave's states) summed over the lanes that differ in bits 2 and 3 alone: state 0 + (bit 2
-// of the lane) of b (bit 3: of c) in q0, of four states state 2 + (bit 2) in q1.  An addition with a lane exchange writes the quarters
+// A token's numbers (b and c of the wave's states) summed over pairs of lanes 8 apart, then over mirrored lanes of an eight (i
+// and 7 - i): state 0 + (bit 2 of the lane) of b (bit 3: of c) in q0, of four states state 2 + (bit 2) in q1.  The four lanes
+// that agree in bits 2 to 5 hold a sum's parts between them, whichever lane a mirror gave which, until they are added up
+// behind the tile.  An addition with a lane exchange writes the quarters
 // of its rows that the number belongs to, so two of them add up two numbers into one register.  The first wait is
 // for what the products before have written, the last one for the exchange that reads the results; in between nothing is
 // read through an exchange sooner than three instructions after it is written.
