@@ -784,8 +784,8 @@ wkv_status_t wkv_conv_backward(int64_t B, int64_t T, int64_t C, int64_t K, int i
  *           behind it are not read, leave the state as it is, and their rows of
  *           out are zeros.
  * x, dt     [B, T, C].  w  [C, N] float32 rates, >= 0; +inf keeps nothing (a step that
- *           is zero in float32 keeps everything, whatever the rate).  Rates above 2e38 count
- *           as infinite.
+ *           is zero in float32 keeps everything, whatever the rate).  Rates whose product
+ *           with log2 e is beyond float32's range (2.36e38 and more) count as infinite.
  * b, c      [B, T, G N].  d  [C] float32 or NULL (0).  z  [B, T, C] or NULL (out = y).
  * dt_bias   [C] float32 or NULL (0).
  * out       [B, T, C], fully overwritten; must not overlap an input or s_out (WKV_EINVAL).

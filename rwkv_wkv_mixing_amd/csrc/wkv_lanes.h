@@ -31,17 +31,6 @@ __device__ __forceinline__ void each(F&& f) {
     each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-// e^{-|x|} by the hardware's exp2 (within 2^-23).  Wide: the rounding of x log2 e, up to |x| 2^-24 of the result, is put back.
-template <bool Wide>
-__device__ __forceinline__ float exp_neg_abs(float x) {
-    constexpr float kLog2e = 1.44269504088896340736f;
-    const float a = -__builtin_fabsf(x), t = a * kLog2e;
-    const float e = __builtin_amdgcn_exp2f(t);
-    if constexpr (!Wide) return e;
-    const float lost = fmaf(a, kLog2e, -t) + a * 1.92596299e-8f;  // log2 e = kLog2e + 1.92596299e-8
-    return a < -100.f ? e : fmaf(e, 0.693147180559945f * lost, e);
-}
-
 // a b, but 0 where either is 0: v_mul_legacy_f32, which the compiler has no builtin for (as inline assembly it would stand
 // outside the scheduling).
 __device__ float mul_zero(float a, float b) __asm("llvm.amdgcn.fmul.legacy");

@@ -36,6 +36,16 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) { return __builtin
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// e^{-|x|} by the hardware's exp2 (within 2^-23).  Wide: the rounding of x log2 e, up to |x| 2^-24 of the result, is put back.
+template <bool Wide>
+__device__ __forceinline__ float exp_neg_abs(float x) {
+    const float a = -__builtin_fabsf(x), t = a * kLog2e;
+    const float e = exp2_fast(t);
+    if constexpr (!Wide) return e;
+    const float lost = fmaf(a, kLog2e, -t) + a * 1.92596299e-8f;  // log2 e = kLog2e + 1.92596299e-8
+    return a < -100.f ? e : fmaf(e, 0.693147180559945f * lost, e);
+}
+
 // log(1 + e) for e in [0, 1]: e times a polynomial through the Chebyshev points of [0, 1] of log(1 + e) / e (within
 // 1.3e-7 of it), so a small e keeps its digits.
 __device__ __forceinline__ float log1p_unit(float e) {

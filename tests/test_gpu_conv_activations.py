@@ -45,3 +45,22 @@ def test_conv(C, T, act):
         near(dx, p * q, p, "dx")
     else:
         near(dx, p * (1 + v * q), p * (1 + np.abs(v)), "dx")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5])
+def test_arguments_without_end(T, dtype):
+    """Of an infinite argument, or one whose product with log2 e is infinite, the sigmoid is 1 or 0; of one that is not a number
+    it is not either."""
+    v = torch.tensor([float("inf"), float("-inf"), 3e38, -3e38, 100.0, -200.0, float("nan"), 0.0], device=DEV)
+    x, weight = v.to(dtype).expand(1, T, 8).contiguous(), torch.ones(2, 8, device=DEV)
+    weight[0] = 0.0
+    s_in = torch.zeros(1, 1, 8, dtype=dtype, device=DEV)
+    out = O.conv_forward(x[:, :1].contiguous(), weight, act="sigmoid", state_in=s_in)[0, 0].float().tolist()
+    assert out[:6] == [1.0, 0.0, 1.0, 0.0, 1.0, 0.0] and out[6] != out[6] and out[7] == 0.5
+    if T > 1:  # (a tap of zero times an infinite input is not a number: finite ones only)
+        x = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+        out = O.conv_forward(x, weight, act="sigmoid")[0, -1].float().tolist()
+        assert out[2:6] == [1.0, 0.0, 1.0, 0.0]
+    dx = O.conv_backward(x[:, :1].contiguous(), torch.ones_like(x[:, :1]), weight, act="sigmoid", state_in=s_in)[0][0, 0].float().tolist()
+    assert dx[2:6] == [0.0, 0.0, 0.0, 0.0] and dx[7] == 0.25
