@@ -13,7 +13,7 @@
 // the waves' parts, gate and store.
 //
 // Measured at B = 8, T = 1024, C = 4096, bf16 (the data alone would take 43 us forward and 75 us back):
-//     N = 8: 142 us forward, 281 us for the gradients;  N = 16: 163 and 395 us.
+//     N = 8: 140 us forward, 280 us for the gradients;  N = 16: 162 and 396 us.
 // At N = 16 two waves a vector unit keep it busy 75 % of the time forward and 80 % in the gradients.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
